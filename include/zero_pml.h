@@ -582,6 +582,137 @@ int zero_onebit_update(const uint32_t *bits, const float *server_scales, int32_t
                        float *p, float *m, const float *v, void *p_lp, int32_t pdtype, void *ws, size_t ws_bytes,
                        void *stream);
 
+/* ------------------------------------------------------------------ feed-forward sub-block */
+
+/* The operators of the feed-forward half of a pre-norm transformer layer,
+ * forward and backward: the part of the model between the parameters that
+ * zero_step writes and the gradients that it reads.
+ *
+ *     t = residual + dropout(x)           zero_dropout_add, or inside the norm
+ *     y = layer_norm(t)                   zero_layer_norm
+ *     z = (act(y Wg^T) * (y Wu^T)) Wd^T   zero_gated_ffn
+ *
+ * Weights are taken in the low-precision type of p_lp and weight gradients
+ * are written in a type that zero_step takes, so both can be the tensors of
+ * a flat shard.  A loss scale on the incoming gradient passes through every
+ * backward call unchanged (all of them are linear in it).
+ *
+ * Conventions of these calls beside those at the top of this file:
+ *   - Matrices are row-major, rows x cols, with a row stride `ld` in
+ *     elements (ld >= cols).  Arrays may start at any multiple of their
+ *     element size (ZERO_EALIGN otherwise; the feed-forward asks more of its
+ *     operands, see there): a tensor of a flat shard starts wherever the one
+ *     before it ends.  Whole 16-byte rows (start and ld * element size
+ *     multiples of 16) are the fast case.
+ *   - Outputs must not overlap inputs or one another, except that
+ *     zero_dropout_add's out may be x or residual itself (same ld).
+ *   - Sums, statistics and products are binary32 or wider; each output is
+ *     rounded once (to nearest even) to its type.
+ *   - Kernels only (and fills of empty cases): every call can be captured
+ *     into a CUDA graph.
+ *   - Empty arrays (a size of zero) are accepted with NULL pointers; a
+ *     weight gradient over zero rows is written as zeros. */
+
+/* Which elements dropout keeps.  The mask is never stored: element (r, c) of
+ * a rows x cols matrix draws word c % 4 of Philox4x32-10 (Salmon, Moraes,
+ * Dror and Shaw 2011) at the counter (c / 4, r, o mod 2^32, o / 2^32), key
+ * (seed mod 2^32, seed / 2^32), o = offset + *d_offset, and is kept iff the
+ * word is at least round(p * 2^32).  Kept elements are multiplied by
+ * float(1 / (1 - p)); the others give 0 whatever their value (NaN included).
+ * p = 0 keeps and p = 1 drops everything.  The backward pass uses the same
+ * struct.  Two calls of one step must not share (seed, offset): number the
+ * calls with `offset`, and let d_offset (a device uint64, or NULL) move on
+ * between replays of a captured step. */
+typedef struct zero_dropout {
+    double p;                 /* probability of dropping an element, in [0, 1] */
+    uint64_t seed;
+    uint64_t offset;
+    const uint64_t *d_offset; /* device, read when the kernel runs; may be NULL */
+} zero_dropout_t;
+
+/* out = residual + dropout(x); residual NULL for none (the backward pass:
+ * dx = dropout of the output's gradient; the residual's gradient is the
+ * output's own).  dtype: F16, BF16 or F32, of all three.  rows < 2^32,
+ * cols <= 2^34.  Errors: ZERO_EINVAL (NULL, negative size, p outside [0, 1]),
+ * ZERO_EALIGN, ZERO_EDTYPE, ZERO_ESIZE (ld < cols, sizes past the limits),
+ * ZERO_ECUDA. */
+int zero_dropout_add(const void *x, int64_t x_ld, const void *residual, int64_t residual_ld, void *out,
+                     int64_t out_ld, int64_t rows, int64_t cols, int32_t dtype, const zero_dropout_t *drop,
+                     void *stream);
+
+/* y = (t - mean) * rstd * weight + bias over each row of t, with mean and
+ * rstd = 1 / sqrt(var + eps) of that row (var the mean squared deviation).
+ * t = residual + dropout(x) (residual NULL: none; drop NULL: all kept),
+ * stored in `sum` (required when residual or drop is given, NULL otherwise);
+ * the norm is that of t before its rounding into `sum`.  weight, bias: cols
+ * elements of wdtype, either may be NULL (1 and 0).  mean, rstd: rows fp32,
+ * for the backward pass (either may be NULL).  dtype (F16, BF16, F32) is the
+ * type of x, residual, sum and y; wdtype is dtype or F32.  eps >= 0.
+ * Limits and errors as zero_dropout_add. */
+int zero_layer_norm(const void *x, int64_t x_ld, const void *residual, int64_t residual_ld,
+                    const zero_dropout_t *drop, void *sum, int64_t sum_ld, const void *weight, const void *bias,
+                    int32_t wdtype, void *y, int64_t y_ld, float *mean, float *rstd, int64_t rows, int64_t cols,
+                    double eps, int32_t dtype, void *stream);
+
+/* The backward pass.  x is the matrix that was normalised (`sum` of a call
+ * that formed one), dy the gradient of y; with xh = (x - mean) * rstd and
+ * g = dy * weight, per row and over all rows:
+ *     dx      = dresidual + rstd * (g - avg(g) - xh * avg(g * xh))
+ *     dropped = dropout(dx)      (the gradient of the sum's dropped summand)
+ *     dweight = sum_rows dy * xh,    dbias = sum_rows dy
+ * dresidual: the gradient that reaches x by another path (the residual
+ * stream), or NULL.  dropped is written when drop is given (both or neither;
+ * from dx before its rounding).  dweight, dbias: cols elements of gdtype
+ * (dtype or F32), either may be NULL; their sums are taken in a fixed order
+ * (the same bits on every run).  ws: device, 256-byte aligned, zero-filled
+ * before its first use, ws_bytes >= zero_layer_norm_workspace_bytes(rows,
+ * cols).  Errors: as zero_dropout_add, plus ZERO_EWORKSPACE. */
+size_t zero_layer_norm_workspace_bytes(int64_t rows, int64_t cols);
+int zero_layer_norm_backward(const void *dy, int64_t dy_ld, const void *x, int64_t x_ld, const void *weight,
+                             int32_t wdtype, const float *mean, const float *rstd, const void *dresidual,
+                             int64_t dresidual_ld, void *dx, int64_t dx_ld, const zero_dropout_t *drop, void *dropped,
+                             int64_t dropped_ld, void *dweight, void *dbias, int32_t gdtype, int64_t rows,
+                             int64_t cols, int32_t dtype, void *ws, size_t ws_bytes, void *stream);
+
+/* The gate's activation (Shazeer 2020): */
+#define ZERO_ACT_SILU 0      /* g * sigmoid(g) */
+#define ZERO_ACT_GELU_TANH 1 /* g / 2 * (1 + tanh(sqrt(2/pi) * (g + 0.044715 g^3))) */
+
+/* y = (act(gate) * up) w_down^T, gate = x w_gate^T, up = x w_up^T.
+ * x: tokens x dim, y: tokens x dim; w_gate, w_up: inner x dim and w_down:
+ * dim x inner, contiguous (out features x in features).  All of `dtype`: F16
+ * or BF16, products on the tensor cores with binary32 sums; the inner product
+ * act(gate) * up is rounded to dtype once between the two products (the
+ * tensor cores' operand type).  gate, up (tokens x inner, contiguous): both
+ * given to keep them for the backward pass, or both NULL.
+ * When dim and inner are multiples of 8, x (and dy) and the weights must
+ * start on 16 bytes with x_ld (dy_ld) a multiple of 8; otherwise the call
+ * first copies the operands into rows of whole 16 bytes in the workspace, at
+ * any alignment.  ws: device, 256-byte aligned, zero-filled before its first
+ * use, of zero_gated_ffn_workspace_bytes(tokens, dim, inner, 0) bytes (1: the
+ * backward pass, which is enough for the forward as well); not shared by
+ * calls that may run at the same time.  zero_workspace_stalls takes it: a
+ * bounded wait that gave up leaves NaN in the call's outputs.
+ * Errors: ZERO_EINVAL, ZERO_EALIGN, ZERO_EDTYPE, ZERO_ESIZE (ld < cols;
+ * tokens, dim or inner past 2^31 - 512), ZERO_EWORKSPACE, ZERO_ECUDA. */
+size_t zero_gated_ffn_workspace_bytes(int64_t tokens, int64_t dim, int64_t inner, int32_t backward);
+int zero_gated_ffn(const void *x, int64_t x_ld, const void *w_gate, const void *w_up, const void *w_down, void *y,
+                   int64_t y_ld, void *gate, void *up, int64_t tokens, int64_t dim, int64_t inner, int32_t act,
+                   int32_t dtype, void *ws, size_t ws_bytes, void *stream);
+
+/* The backward pass, from x, the weights and the kept gate and up:
+ *     dh = dy w_down;  dgate = dh * up * act'(gate);  dup = dh * act(gate)
+ *     dx = dgate w_gate + dup w_up
+ *     dw_gate = dgate^T x,  dw_up = dup^T x,  dw_down = dy^T (act(gate) * up)
+ * dgate, dup and act(gate) * up are rounded to dtype once, as operands of the
+ * products that follow.  The weight gradients are of gdtype (dtype or F32).
+ * Errors as zero_gated_ffn. */
+int zero_gated_ffn_backward(const void *dy, int64_t dy_ld, const void *x, int64_t x_ld, const void *w_gate,
+                            const void *w_up, const void *w_down, const void *gate, const void *up, void *dx,
+                            int64_t dx_ld, void *dw_gate, void *dw_up, void *dw_down, int32_t gdtype, int64_t tokens,
+                            int64_t dim, int64_t inner, int32_t act, int32_t dtype, void *ws, size_t ws_bytes,
+                            void *stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -6,7 +6,10 @@ by hand-written CUDA kernels (gradient accumulation; unscale + overflow +
 global squared norm; clip + AdamW + cast to fp16/bf16).  Around the step:
 the stage-2 gradient reduction fused with the norm pass, the stage-3
 parameter gather (shards back to tensors) with its per-layer plan, the
-offload step on the host cores, and 1-bit Adam's compression stage.  The C ABI is in
+offload step on the host cores, and 1-bit Adam's compression stage.  Beside
+the step: the feed-forward half of a pre-norm transformer layer (dropout with
+the residual sum, layer norm, the gated feed-forward), forward and backward,
+which makes gradients the step reads from the parameters it writes.  The C ABI is in
 ``include/zero_pml.h``; this package is its Python binding.
 """
 from .binding import (  # noqa: F401
@@ -51,4 +54,16 @@ from .binding import (  # noqa: F401
     zero_onebit_server,
     zero_onebit_update,
     zero_onebit_worker,
+    Dropout,
+    ZERO_ACT_GELU_TANH,
+    ZERO_ACT_SILU,
+    new_gated_ffn_workspace,
+    new_layer_norm_workspace,
+    zero_dropout_add,
+    zero_gated_ffn,
+    zero_gated_ffn_backward,
+    zero_gated_ffn_workspace_bytes,
+    zero_layer_norm,
+    zero_layer_norm_backward,
+    zero_layer_norm_workspace_bytes,
 )

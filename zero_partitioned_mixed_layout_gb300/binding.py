@@ -663,6 +663,230 @@ def zero_onebit_update(bits, server_scales, S: int, numel: int, p, m, v, p_lp, w
     _check(rc, "zero_onebit_update")
 
 
+# ------------------------------------------------------------------ feed-forward sub-block
+
+ZERO_ACT_SILU, ZERO_ACT_GELU_TANH = 0, 1
+
+
+class _Dropout(ctypes.Structure):
+    _fields_ = [("p", ctypes.c_double), ("seed", ctypes.c_uint64), ("offset", ctypes.c_uint64),
+                ("d_offset", ctypes.c_void_p)]
+
+
+class Dropout:
+    """zero_dropout_t: which elements a dropout keeps.  d_offset: a device
+    int64 tensor of one element added to offset when the kernel runs (None:
+    nothing added)."""
+
+    def __init__(self, p: float, seed: int, offset: int = 0, d_offset=None):
+        import torch
+        if d_offset is not None and (not d_offset.is_cuda or d_offset.dtype != torch.int64 or d_offset.numel() != 1):
+            raise ValueError("d_offset must be a CUDA int64 tensor of one element")
+        self.p, self.seed, self.offset, self.d_offset = float(p), int(seed), int(offset), d_offset
+        mask = (1 << 64) - 1
+        self._c = _Dropout(self.p, self.seed & mask, self.offset & mask,
+                           None if d_offset is None else d_offset.data_ptr())
+
+
+def _sublayer_lib():
+    so = lib()
+    if not getattr(so, "_sublayer_ready", False):
+        vp, i64, i32, sz = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_size_t
+        dp = ctypes.POINTER(_Dropout)
+        so.zero_dropout_add.argtypes = [vp, i64, vp, i64, vp, i64, i64, i64, i32, dp, vp]
+        so.zero_layer_norm.argtypes = [vp, i64, vp, i64, dp, vp, i64, vp, vp, i32, vp, i64, vp, vp, i64, i64,
+                                       ctypes.c_double, i32, vp]
+        so.zero_layer_norm_workspace_bytes.argtypes = [i64, i64]
+        so.zero_layer_norm_backward.argtypes = [vp, i64, vp, i64, vp, i32, vp, vp, vp, i64, vp, i64, dp, vp, i64,
+                                                vp, vp, i32, i64, i64, i32, vp, sz, vp]
+        so.zero_gated_ffn_workspace_bytes.argtypes = [i64, i64, i64, i32]
+        so.zero_gated_ffn.argtypes = [vp, i64, vp, vp, vp, vp, i64, vp, vp, i64, i64, i64, i32, i32, vp, sz, vp]
+        so.zero_gated_ffn_backward.argtypes = [vp, i64, vp, i64, vp, vp, vp, vp, vp, vp, i64, vp, vp, vp, i32, i64,
+                                               i64, i64, i32, i32, vp, sz, vp]
+        for f in ("zero_dropout_add", "zero_layer_norm", "zero_layer_norm_backward", "zero_gated_ffn",
+                  "zero_gated_ffn_backward"):
+            getattr(so, f).restype = ctypes.c_int
+        for f in ("zero_layer_norm_workspace_bytes", "zero_gated_ffn_workspace_bytes"):
+            getattr(so, f).restype = sz
+        so._sublayer_ready = True
+    return so
+
+
+def _matrix(t, what: str, shape=None, dtype=None):
+    """(pointer, row stride) of a 2-D CUDA tensor whose rows are contiguous."""
+    if not t.is_cuda:
+        raise ValueError(f"{what} must be a CUDA tensor")
+    if t.dim() != 2:
+        raise ValueError(f"{what} must have two dimensions")
+    rows, cols = t.shape
+    if shape is not None and (rows, cols) != shape:
+        raise ValueError(f"{what} must be {shape[0]} x {shape[1]}")
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError(f"{what} must be {dtype}")
+    ld, inner = t.stride()
+    if cols > 1 and inner != 1:
+        raise ValueError(f"{what}: the elements of a row must be contiguous")
+    return t.data_ptr(), ld if rows > 1 and cols > 0 else max(cols, 1)
+
+
+def _vector(t, what: str, n: int, dtypes=None):
+    """The pointer of a contiguous CUDA tensor of n elements."""
+    _device_tensor(t, what)
+    if t.numel() != n:
+        raise ValueError(f"{what} must hold {n} elements")
+    if dtypes is not None and t.dtype not in dtypes:
+        raise TypeError(f"{what} must be {' or '.join(map(str, dtypes))}")
+    return t.data_ptr()
+
+
+def _f32_pointer(t, what: str, n: int):
+    import torch
+    return None if t is None else _vector(t, what, n, (torch.float32,))
+
+
+def _pair_code(a, b, what: str, default: int) -> int:
+    """The one element type of two tensors either of which may be None."""
+    codes = {_dtype_code(t) for t in (a, b) if t is not None}
+    if len(codes) > 1:
+        raise TypeError(f"{what} must share one element type")
+    return codes.pop() if codes else default
+
+
+def _drop_ref(drop):
+    return None if drop is None else ctypes.byref(drop._c)
+
+
+def zero_dropout_add(x, residual, out, drop: Dropout, stream=None) -> None:
+    """out = residual + dropout(x) (residual None: dropout alone, which is
+    also the backward pass, of the output's gradient)."""
+    shape, code = tuple(x.shape), _dtype_code(x)
+    xp, xl = _matrix(x, "x")
+    rp, rl = (None, 0) if residual is None else _matrix(residual, "residual", shape, x.dtype)
+    op, ol = _matrix(out, "out", shape, x.dtype)
+    rc = _sublayer_lib().zero_dropout_add(xp, xl, rp, rl, op, ol, shape[0], shape[1], code, _drop_ref(drop),
+                                          _stream_ptr(stream, x.device))
+    _check(rc, "zero_dropout_add")
+
+
+def zero_layer_norm(x, weight, bias, y, mean=None, rstd=None, eps: float = 1e-5, residual=None, drop=None,
+                    sum_out=None, stream=None) -> None:
+    """y = layer norm of t over each row, t = residual + dropout(x) (x itself
+    with neither); sum_out receives t when residual or drop is given, mean
+    and rstd (float32[rows]) the statistics for the backward pass."""
+    shape, code = tuple(x.shape), _dtype_code(x)
+    xp, xl = _matrix(x, "x")
+    rows, cols = shape
+    rp, rl = (None, 0) if residual is None else _matrix(residual, "residual", shape, x.dtype)
+    sp, sl = (None, 0) if sum_out is None else _matrix(sum_out, "sum_out", shape, x.dtype)
+    yp, yl = _matrix(y, "y", shape, x.dtype)
+    wp = None if weight is None else _vector(weight, "weight", cols)
+    bp = None if bias is None else _vector(bias, "bias", cols)
+    rc = _sublayer_lib().zero_layer_norm(xp, xl, rp, rl, _drop_ref(drop), sp, sl, wp, bp,
+                                         _pair_code(weight, bias, "weight and bias", code), yp, yl,
+                                         _f32_pointer(mean, "mean", rows), _f32_pointer(rstd, "rstd", rows), rows,
+                                         cols, eps, code, _stream_ptr(stream, x.device))
+    _check(rc, "zero_layer_norm")
+
+
+def zero_layer_norm_workspace_bytes(rows: int, cols: int) -> int:
+    return int(_sublayer_lib().zero_layer_norm_workspace_bytes(int(rows), int(cols)))
+
+
+def new_layer_norm_workspace(rows: int, cols: int, device="cuda"):
+    """A zero-filled workspace for zero_layer_norm_backward."""
+    import torch
+    return torch.zeros(zero_layer_norm_workspace_bytes(rows, cols), dtype=torch.uint8, device=device)
+
+
+def zero_layer_norm_backward(dy, x, weight, mean, rstd, dx, dweight, dbias, ws, dresidual=None, drop=None,
+                             dx_dropped=None, stream=None) -> None:
+    """The gradients of zero_layer_norm: dx of the normalised matrix x (the
+    sum_out of a call that formed one), dresidual added to it; dx_dropped = dx
+    through the dropout (the sublayer output's gradient); dweight and dbias
+    (either may be None)."""
+    shape, code = tuple(x.shape), _dtype_code(x)
+    xp, xl = _matrix(x, "x")
+    rows, cols = shape
+    yp, yl = _matrix(dy, "dy", shape, x.dtype)
+    rp, rl = (None, 0) if dresidual is None else _matrix(dresidual, "dresidual", shape, x.dtype)
+    dp, dl = _matrix(dx, "dx", shape, x.dtype)
+    pp, pl = (None, 0) if dx_dropped is None else _matrix(dx_dropped, "dx_dropped", shape, x.dtype)
+    wp = None if weight is None else _vector(weight, "weight", cols)
+    gw = None if dweight is None else _vector(dweight, "dweight", cols)
+    gb = None if dbias is None else _vector(dbias, "dbias", cols)
+    _device_tensor(ws, "workspace")
+    rc = _sublayer_lib().zero_layer_norm_backward(
+        yp, yl, xp, xl, wp, code if weight is None else _dtype_code(weight), _f32_pointer(mean, "mean", rows),
+        _f32_pointer(rstd, "rstd", rows), rp, rl, dp, dl, _drop_ref(drop), pp, pl, gw, gb,
+        _pair_code(dweight, dbias, "dweight and dbias", code), rows, cols, code, ws.data_ptr(), ws.numel(),
+        _stream_ptr(stream, x.device))
+    _check(rc, "zero_layer_norm_backward")
+
+
+def zero_gated_ffn_workspace_bytes(tokens: int, dim: int, inner: int, backward: bool = False) -> int:
+    return int(_sublayer_lib().zero_gated_ffn_workspace_bytes(int(tokens), int(dim), int(inner), int(bool(backward))))
+
+
+def new_gated_ffn_workspace(tokens: int, dim: int, inner: int, backward: bool = False, device="cuda"):
+    """A zero-filled workspace for zero_gated_ffn (backward=True: and for
+    zero_gated_ffn_backward)."""
+    import torch
+    return torch.zeros(zero_gated_ffn_workspace_bytes(tokens, dim, inner, backward), dtype=torch.uint8, device=device)
+
+
+def _contiguous_matrix(t, what: str, shape, dtypes):
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{what} must be {shape[0]} x {shape[1]}")
+    return _vector(t, what, shape[0] * shape[1], dtypes)
+
+
+def _ffn_weights(x, w_gate, w_up, w_down):
+    if x.dim() != 2 or w_gate.dim() != 2:
+        raise ValueError("x and w_gate must have two dimensions")
+    tokens, dim = x.shape
+    inner = w_gate.shape[0]
+    one = (x.dtype,)
+    return tokens, dim, inner, (_contiguous_matrix(w_gate, "w_gate", (inner, dim), one),
+                                _contiguous_matrix(w_up, "w_up", (inner, dim), one),
+                                _contiguous_matrix(w_down, "w_down", (dim, inner), one))
+
+
+def zero_gated_ffn(x, w_gate, w_up, w_down, y, ws, act: int = ZERO_ACT_SILU, gate=None, up=None, stream=None) -> None:
+    """y = (act(x w_gate^T) * (x w_up^T)) w_down^T; gate and up ([tokens,
+    inner], both or neither) receive the two projections for the backward."""
+    tokens, dim, inner, weights = _ffn_weights(x, w_gate, w_up, w_down)
+    xp, xl = _matrix(x, "x")
+    yp, yl = _matrix(y, "y", (tokens, dim), x.dtype)
+    gp, up_ = (None if t is None else _contiguous_matrix(t, name, (tokens, inner), (x.dtype,))
+               for t, name in ((gate, "gate"), (up, "up")))
+    _device_tensor(ws, "workspace")
+    rc = _sublayer_lib().zero_gated_ffn(xp, xl, *weights, yp, yl, gp, up_, tokens, dim, inner, int(act),
+                                        _dtype_code(x), ws.data_ptr(), ws.numel(), _stream_ptr(stream, x.device))
+    _check(rc, "zero_gated_ffn")
+
+
+def zero_gated_ffn_backward(dy, x, w_gate, w_up, w_down, gate, up, dx, dw_gate, dw_up, dw_down, ws,
+                            act: int = ZERO_ACT_SILU, stream=None) -> None:
+    """The gradients of zero_gated_ffn from the kept gate and up: dx, and the
+    three weight gradients (x's type or float32)."""
+    import torch
+    tokens, dim, inner, weights = _ffn_weights(x, w_gate, w_up, w_down)
+    xp, xl = _matrix(x, "x")
+    yp, yl = _matrix(dy, "dy", (tokens, dim), x.dtype)
+    dp, dl = _matrix(dx, "dx", (tokens, dim), x.dtype)
+    one, any_ = (x.dtype,), (x.dtype, torch.float32)
+    kept = [_contiguous_matrix(t, name, (tokens, inner), one) for t, name in ((gate, "gate"), (up, "up"))]
+    grads = [_contiguous_matrix(t, name, shape, any_) for t, name, shape in
+             ((dw_gate, "dw_gate", (inner, dim)), (dw_up, "dw_up", (inner, dim)), (dw_down, "dw_down", (dim, inner)))]
+    if len({dw_gate.dtype, dw_up.dtype, dw_down.dtype}) != 1:
+        raise TypeError("the weight gradients must share one element type")
+    _device_tensor(ws, "workspace")
+    rc = _sublayer_lib().zero_gated_ffn_backward(yp, yl, xp, xl, *weights, *kept, dp, dl, *grads, _dtype_code(dw_gate),
+                                                 tokens, dim, inner, int(act), _dtype_code(x), ws.data_ptr(),
+                                                 ws.numel(), _stream_ptr(stream, x.device))
+    _check(rc, "zero_gated_ffn_backward")
+
+
 # ------------------------------------------------------------------ offload (host)
 
 class OffloadScalars(ctypes.Structure):
