@@ -712,28 +712,54 @@ def _sublayer_lib():
     return so
 
 
-def _matrix(t, what: str, shape=None, dtype=None):
+_codes = {}
+
+
+def _type_code(t) -> int:
+    """_dtype_code with the table built once."""
+    code = _codes.get(t.dtype)
+    if code is None:
+        code = _codes[t.dtype] = _dtype_code(t)
+    return code
+
+
+def _stream_handle(stream, t):
+    """The cudaStream_t of `stream`, or of the current stream of t's device."""
+    if stream is not None:
+        return stream.cuda_stream
+    import torch
+    return torch._C._cuda_getCurrentRawStream(t.get_device())
+
+
+def _matrix(t, what: str, shape, dtype):
     """(pointer, row stride) of a 2-D CUDA tensor whose rows are contiguous."""
+    if t.shape != shape:
+        raise ValueError(f"{what} must be {' x '.join(map(str, shape))}")
+    if t.dtype != dtype:
+        raise TypeError(f"{what} must be {dtype}")
     if not t.is_cuda:
         raise ValueError(f"{what} must be a CUDA tensor")
-    if t.dim() != 2:
-        raise ValueError(f"{what} must have two dimensions")
-    rows, cols = t.shape
-    if shape is not None and (rows, cols) != shape:
-        raise ValueError(f"{what} must be {shape[0]} x {shape[1]}")
-    if dtype is not None and t.dtype != dtype:
-        raise TypeError(f"{what} must be {dtype}")
+    if t.is_contiguous():
+        return t.data_ptr(), shape[1]
     ld, inner = t.stride()
-    if cols > 1 and inner != 1:
+    if shape[1] > 1 and inner != 1:
         raise ValueError(f"{what}: the elements of a row must be contiguous")
-    return t.data_ptr(), ld if rows > 1 and cols > 0 else max(cols, 1)
+    return t.data_ptr(), ld if shape[0] > 1 else shape[1]
+
+
+def _matrix_shape(t, what: str):
+    shape = t.shape
+    if len(shape) != 2:
+        raise ValueError(f"{what} must have two dimensions")
+    return shape
 
 
 def _vector(t, what: str, n: int, dtypes=None):
     """The pointer of a contiguous CUDA tensor of n elements."""
-    _device_tensor(t, what)
-    if t.numel() != n:
-        raise ValueError(f"{what} must hold {n} elements")
+    if not t.is_cuda:
+        raise ValueError(f"{what} must be a CUDA tensor")
+    if t.numel() != n or not t.is_contiguous():
+        raise ValueError(f"{what} must hold {n} elements, contiguous")
     if dtypes is not None and t.dtype not in dtypes:
         raise TypeError(f"{what} must be {' or '.join(map(str, dtypes))}")
     return t.data_ptr()
@@ -746,10 +772,11 @@ def _f32_pointer(t, what: str, n: int):
 
 def _pair_code(a, b, what: str, default: int) -> int:
     """The one element type of two tensors either of which may be None."""
-    codes = {_dtype_code(t) for t in (a, b) if t is not None}
-    if len(codes) > 1:
+    if a is None or b is None:
+        return default if a is b else _type_code(b if a is None else a)
+    if a.dtype != b.dtype:
         raise TypeError(f"{what} must share one element type")
-    return codes.pop() if codes else default
+    return _type_code(a)
 
 
 def _drop_ref(drop):
@@ -759,12 +786,12 @@ def _drop_ref(drop):
 def zero_dropout_add(x, residual, out, drop: Dropout, stream=None) -> None:
     """out = residual + dropout(x) (residual None: dropout alone, which is
     also the backward pass, of the output's gradient)."""
-    shape, code = tuple(x.shape), _dtype_code(x)
-    xp, xl = _matrix(x, "x")
-    rp, rl = (None, 0) if residual is None else _matrix(residual, "residual", shape, x.dtype)
-    op, ol = _matrix(out, "out", shape, x.dtype)
+    shape, dtype, code = _matrix_shape(x, "x"), x.dtype, _type_code(x)
+    xp, xl = _matrix(x, "x", shape, dtype)
+    rp, rl = (None, 0) if residual is None else _matrix(residual, "residual", shape, dtype)
+    op, ol = _matrix(out, "out", shape, dtype)
     rc = _sublayer_lib().zero_dropout_add(xp, xl, rp, rl, op, ol, shape[0], shape[1], code, _drop_ref(drop),
-                                          _stream_ptr(stream, x.device))
+                                          _stream_handle(stream, x))
     _check(rc, "zero_dropout_add")
 
 
@@ -773,18 +800,18 @@ def zero_layer_norm(x, weight, bias, y, mean=None, rstd=None, eps: float = 1e-5,
     """y = layer norm of t over each row, t = residual + dropout(x) (x itself
     with neither); sum_out receives t when residual or drop is given, mean
     and rstd (float32[rows]) the statistics for the backward pass."""
-    shape, code = tuple(x.shape), _dtype_code(x)
-    xp, xl = _matrix(x, "x")
+    shape, dtype, code = _matrix_shape(x, "x"), x.dtype, _type_code(x)
+    xp, xl = _matrix(x, "x", shape, dtype)
     rows, cols = shape
-    rp, rl = (None, 0) if residual is None else _matrix(residual, "residual", shape, x.dtype)
-    sp, sl = (None, 0) if sum_out is None else _matrix(sum_out, "sum_out", shape, x.dtype)
-    yp, yl = _matrix(y, "y", shape, x.dtype)
+    rp, rl = (None, 0) if residual is None else _matrix(residual, "residual", shape, dtype)
+    sp, sl = (None, 0) if sum_out is None else _matrix(sum_out, "sum_out", shape, dtype)
+    yp, yl = _matrix(y, "y", shape, dtype)
     wp = None if weight is None else _vector(weight, "weight", cols)
     bp = None if bias is None else _vector(bias, "bias", cols)
     rc = _sublayer_lib().zero_layer_norm(xp, xl, rp, rl, _drop_ref(drop), sp, sl, wp, bp,
                                          _pair_code(weight, bias, "weight and bias", code), yp, yl,
                                          _f32_pointer(mean, "mean", rows), _f32_pointer(rstd, "rstd", rows), rows,
-                                         cols, eps, code, _stream_ptr(stream, x.device))
+                                         cols, eps, code, _stream_handle(stream, x))
     _check(rc, "zero_layer_norm")
 
 
@@ -804,22 +831,22 @@ def zero_layer_norm_backward(dy, x, weight, mean, rstd, dx, dweight, dbias, ws, 
     sum_out of a call that formed one), dresidual added to it; dx_dropped = dx
     through the dropout (the sublayer output's gradient); dweight and dbias
     (either may be None)."""
-    shape, code = tuple(x.shape), _dtype_code(x)
-    xp, xl = _matrix(x, "x")
+    shape, dtype, code = _matrix_shape(x, "x"), x.dtype, _type_code(x)
+    xp, xl = _matrix(x, "x", shape, dtype)
     rows, cols = shape
-    yp, yl = _matrix(dy, "dy", shape, x.dtype)
-    rp, rl = (None, 0) if dresidual is None else _matrix(dresidual, "dresidual", shape, x.dtype)
-    dp, dl = _matrix(dx, "dx", shape, x.dtype)
-    pp, pl = (None, 0) if dx_dropped is None else _matrix(dx_dropped, "dx_dropped", shape, x.dtype)
+    yp, yl = _matrix(dy, "dy", shape, dtype)
+    rp, rl = (None, 0) if dresidual is None else _matrix(dresidual, "dresidual", shape, dtype)
+    dp, dl = _matrix(dx, "dx", shape, dtype)
+    pp, pl = (None, 0) if dx_dropped is None else _matrix(dx_dropped, "dx_dropped", shape, dtype)
     wp = None if weight is None else _vector(weight, "weight", cols)
     gw = None if dweight is None else _vector(dweight, "dweight", cols)
     gb = None if dbias is None else _vector(dbias, "dbias", cols)
     _device_tensor(ws, "workspace")
     rc = _sublayer_lib().zero_layer_norm_backward(
-        yp, yl, xp, xl, wp, code if weight is None else _dtype_code(weight), _f32_pointer(mean, "mean", rows),
+        yp, yl, xp, xl, wp, code if weight is None else _type_code(weight), _f32_pointer(mean, "mean", rows),
         _f32_pointer(rstd, "rstd", rows), rp, rl, dp, dl, _drop_ref(drop), pp, pl, gw, gb,
         _pair_code(dweight, dbias, "dweight and dbias", code), rows, cols, code, ws.data_ptr(), ws.numel(),
-        _stream_ptr(stream, x.device))
+        _stream_handle(stream, x))
     _check(rc, "zero_layer_norm_backward")
 
 
@@ -835,16 +862,14 @@ def new_gated_ffn_workspace(tokens: int, dim: int, inner: int, backward: bool = 
 
 
 def _contiguous_matrix(t, what: str, shape, dtypes):
-    if tuple(t.shape) != shape:
+    if t.shape != shape:
         raise ValueError(f"{what} must be {shape[0]} x {shape[1]}")
     return _vector(t, what, shape[0] * shape[1], dtypes)
 
 
 def _ffn_weights(x, w_gate, w_up, w_down):
-    if x.dim() != 2 or w_gate.dim() != 2:
-        raise ValueError("x and w_gate must have two dimensions")
-    tokens, dim = x.shape
-    inner = w_gate.shape[0]
+    tokens, dim = _matrix_shape(x, "x")
+    inner = _matrix_shape(w_gate, "w_gate")[0]
     one = (x.dtype,)
     return tokens, dim, inner, (_contiguous_matrix(w_gate, "w_gate", (inner, dim), one),
                                 _contiguous_matrix(w_up, "w_up", (inner, dim), one),
@@ -855,13 +880,13 @@ def zero_gated_ffn(x, w_gate, w_up, w_down, y, ws, act: int = ZERO_ACT_SILU, gat
     """y = (act(x w_gate^T) * (x w_up^T)) w_down^T; gate and up ([tokens,
     inner], both or neither) receive the two projections for the backward."""
     tokens, dim, inner, weights = _ffn_weights(x, w_gate, w_up, w_down)
-    xp, xl = _matrix(x, "x")
-    yp, yl = _matrix(y, "y", (tokens, dim), x.dtype)
+    xp, xl = _matrix(x, "x", x.shape, x.dtype)
+    yp, yl = _matrix(y, "y", x.shape, x.dtype)
     gp, up_ = (None if t is None else _contiguous_matrix(t, name, (tokens, inner), (x.dtype,))
                for t, name in ((gate, "gate"), (up, "up")))
     _device_tensor(ws, "workspace")
     rc = _sublayer_lib().zero_gated_ffn(xp, xl, *weights, yp, yl, gp, up_, tokens, dim, inner, int(act),
-                                        _dtype_code(x), ws.data_ptr(), ws.numel(), _stream_ptr(stream, x.device))
+                                        _type_code(x), ws.data_ptr(), ws.numel(), _stream_handle(stream, x))
     _check(rc, "zero_gated_ffn")
 
 
@@ -871,9 +896,9 @@ def zero_gated_ffn_backward(dy, x, w_gate, w_up, w_down, gate, up, dx, dw_gate, 
     three weight gradients (x's type or float32)."""
     import torch
     tokens, dim, inner, weights = _ffn_weights(x, w_gate, w_up, w_down)
-    xp, xl = _matrix(x, "x")
-    yp, yl = _matrix(dy, "dy", (tokens, dim), x.dtype)
-    dp, dl = _matrix(dx, "dx", (tokens, dim), x.dtype)
+    xp, xl = _matrix(x, "x", x.shape, x.dtype)
+    yp, yl = _matrix(dy, "dy", x.shape, x.dtype)
+    dp, dl = _matrix(dx, "dx", x.shape, x.dtype)
     one, any_ = (x.dtype,), (x.dtype, torch.float32)
     kept = [_contiguous_matrix(t, name, (tokens, inner), one) for t, name in ((gate, "gate"), (up, "up"))]
     grads = [_contiguous_matrix(t, name, shape, any_) for t, name, shape in
@@ -881,9 +906,9 @@ def zero_gated_ffn_backward(dy, x, w_gate, w_up, w_down, gate, up, dx, dw_gate, 
     if len({dw_gate.dtype, dw_up.dtype, dw_down.dtype}) != 1:
         raise TypeError("the weight gradients must share one element type")
     _device_tensor(ws, "workspace")
-    rc = _sublayer_lib().zero_gated_ffn_backward(yp, yl, xp, xl, *weights, *kept, dp, dl, *grads, _dtype_code(dw_gate),
-                                                 tokens, dim, inner, int(act), _dtype_code(x), ws.data_ptr(),
-                                                 ws.numel(), _stream_ptr(stream, x.device))
+    rc = _sublayer_lib().zero_gated_ffn_backward(yp, yl, xp, xl, *weights, *kept, dp, dl, *grads, _type_code(dw_gate),
+                                                 tokens, dim, inner, int(act), _type_code(x), ws.data_ptr(),
+                                                 ws.numel(), _stream_handle(stream, x))
     _check(rc, "zero_gated_ffn_backward")
 
 

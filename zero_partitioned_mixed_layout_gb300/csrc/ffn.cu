@@ -548,6 +548,137 @@ __global__ void __launch_bounds__(S::THREADS, 1) k_ffn_product(const __grid_cons
         tmem_free<CG>(tmem, S::TMEM);
 }
 
+// ------------------------------------------------------------- a few tokens
+
+// Products for up to four tokens, where the weights' bytes are all there is:
+// a warp per row of the weight matrix (kPair: of the gate's and the up matrix
+// together), or `parts` warps of a block that each take a stretch of k and
+// add up in order through shared memory.  A lane multiplies 16-byte pieces of
+// the row with the tokens' pieces (which stay in L1) in binary32; four pieces
+// of each row are in flight per lane.
+struct TokenArgs {
+    const void *x;  // tokens x k, row stride x_ld
+    int64_t x_ld;
+    const void *w0, *w1;  // n x k, contiguous
+    void *out;            // kPair: act(C0) * C1; else C0; tokens x n, row stride out_ld
+    int64_t out_ld;
+    void *o0, *o1;        // kPair: C0 and C1, kept (or NULL), contiguous
+    int32_t tokens, n, k, parts, act;
+};
+
+// Eight elements from p[i] on (zeros from k on); kW: 16-byte pieces.
+template <bool kW>
+__device__ __forceinline__ uint4 load_piece(const uint16_t *p, int32_t i, int32_t k)
+{
+    if (kW)
+        return *reinterpret_cast<const uint4 *>(p + i);
+    uint32_t w[4] = {};
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+        if (i + e < k)
+            w[e >> 1] |= (uint32_t)p[i + e] << (16 * (e & 1));
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+template <int DT, int MT, bool kPair, bool kW>
+__global__ void __launch_bounds__(kThreads, MT == 4 ? 2 : MT == 2 ? 3 : 4)
+    k_ffn_tokens(const __grid_constant__ TokenArgs a)
+{
+    constexpr int R = kPair ? 2 : 1, U = 4;
+    __shared__ float s_part[kWarps][R * MT];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int per_block = kWarps / a.parts, unit = warp / a.parts, part = warp - unit * a.parts;
+    const int32_t pieces = (a.k + 7) >> 3;  // of a row
+    const int32_t p0 = (int32_t)((int64_t)pieces * part / a.parts), p1 = (int32_t)((int64_t)pieces * (part + 1) / a.parts);
+    const uint16_t *x = static_cast<const uint16_t *>(a.x);
+    bool waited = false;
+    pdl_launch_next();
+    for (int32_t n0 = blockIdx.x * per_block; n0 < a.n; n0 += gridDim.x * per_block) {
+        const int32_t n = n0 + unit;
+        float acc[R][MT] = {};
+        if (n < a.n) {
+            const uint16_t *w[2] = {static_cast<const uint16_t *>(a.w0) + (int64_t)n * a.k,
+                                    kPair ? static_cast<const uint16_t *>(a.w1) + (int64_t)n * a.k : nullptr};
+            for (int32_t i = p0 + lane; i < p1; i += 32 * U) {
+                uint4 wv[U][R];
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+#pragma unroll
+                    for (int q = 0; q < R; ++q)
+                        if (i + 32 * u < p1)
+                            wv[u][q] = load_piece<kW>(w[q], (i + 32 * u) * 8, a.k);
+                if (!waited) {
+                    // the weights are not written by the launch before; x is
+                    pdl_wait();
+                    waited = true;
+                }
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    if (i + 32 * u >= p1)
+                        break;
+                    float wf[R][8];
+#pragma unroll
+                    for (int q = 0; q < R; ++q)
+                        Elem<DT>::to_float(&wv[u][q], wf[q]);
+#pragma unroll
+                    for (int m = 0; m < MT; ++m) {
+                        const int64_t row = (m < a.tokens ? m : a.tokens - 1) * a.x_ld;
+                        const uint4 xv = load_piece<kW>(x + row, (i + 32 * u) * 8, a.k);
+                        float xf[8];
+                        Elem<DT>::to_float(&xv, xf);
+#pragma unroll
+                        for (int q = 0; q < R; ++q)
+#pragma unroll
+                            for (int e = 0; e < 8; ++e)
+                                acc[q][m] += wf[q][e] * xf[e];
+                    }
+                }
+            }
+        }
+#pragma unroll
+        for (int q = 0; q < R; ++q)
+#pragma unroll
+            for (int m = 0; m < MT; ++m)
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1)
+                    acc[q][m] += __shfl_xor_sync(0xffffffffu, acc[q][m], o);
+        if (a.parts > 1) {
+            __syncthreads();  // s_part was read for the rows before
+            if (lane == 0)
+#pragma unroll
+                for (int q = 0; q < R; ++q)
+#pragma unroll
+                    for (int m = 0; m < MT; ++m)
+                        s_part[warp][q * MT + m] = acc[q][m];
+            __syncthreads();
+            if (part == 0)
+#pragma unroll
+                for (int q = 0; q < R; ++q)
+#pragma unroll
+                    for (int m = 0; m < MT; ++m)
+                        for (int j = 1; j < a.parts; ++j)
+                            acc[q][m] += s_part[warp + j][q * MT + m];
+        }
+        if (part == 0 && n < a.n && lane == 0) {
+#pragma unroll
+            for (int m = 0; m < MT; ++m)
+                if (m < a.tokens) {
+                    if (kPair) {
+                        store1<DT>(a.out, m * a.out_ld + n, activate(a.act, acc[0][m]).value * acc[R - 1][m]);
+                        if (a.o0) {
+                            store1<DT>(a.o0, (int64_t)m * a.n + n, acc[0][m]);
+                            store1<DT>(a.o1, (int64_t)m * a.n + n, acc[R - 1][m]);
+                        }
+                    } else {
+                        store1<DT>(a.out, m * a.out_ld + n, acc[0][m]);
+                    }
+                }
+        }
+    }
+    if (!waited)
+        pdl_wait();
+}
+
 // Rows of 16-bit elements copied to rows of whole 16 bytes (widths that no
 // vector divides): up to five matrices in one launch.
 struct Copy {
@@ -820,6 +951,63 @@ void workspace_args(ProductArgs<NP> &g, void *ws, const FfnSpace &sp)
     g.partials = reinterpret_cast<float *>(static_cast<char *>(ws) + sp.partials);
 }
 
+// ------------------------------------------------------------- a few tokens
+
+constexpr int kFewTokens = 4;
+
+// Warps per weight row: k is shared out until a lane has about four pieces of
+// 8 elements (1024 elements per warp), as long as there are too few rows to
+// give every SM 32 warps.
+int token_parts(int64_t n, int64_t k)
+{
+    int parts = 1;
+    while (parts < kWarps && n * parts < (int64_t)kSms * 32 && k >= (int64_t)parts * 2 * 512)
+        parts *= 2;
+    return parts;
+}
+
+template <int DT, bool kPair>
+int token_product(TokenArgs &a, bool whole, bool chained, cudaStream_t st)
+{
+    a.parts = token_parts(a.n, a.k);
+    const int64_t units = cdiv(a.n, kWarps / a.parts), most = (int64_t)sm_count() * (a.tokens == 1 ? 4 : a.tokens == 2 ? 3 : 2);
+    const int grid = (int)(units < most ? units : most);
+    cudaError_t e;
+#define ZERO_MT(MT)                                                                                            \
+    (whole ? launch_k(k_ffn_tokens<DT, MT, kPair, true>, grid, kThreads, st, chained, a)                        \
+           : launch_k(k_ffn_tokens<DT, MT, kPair, false>, grid, kThreads, st, chained, a))
+    if (a.tokens == 1)
+        e = ZERO_MT(1);
+    else if (a.tokens == 2)
+        e = ZERO_MT(2);
+    else
+        e = ZERO_MT(4);
+#undef ZERO_MT
+    if (e != cudaSuccess) {
+        cudaGetLastError();
+        set_cuda_error("k_ffn_tokens", (int)e, cudaGetErrorString(e));
+        return ZERO_ECUDA;
+    }
+    return ZERO_OK;
+}
+
+// The forward pass of a few tokens.  The second launch is scheduled while the
+// first runs and has its first weights in flight when the first ends.
+template <int DT>
+int tokens_forward(const void *x, int64_t x_ld, const void *wg, const void *wu, const void *wd, void *y, int64_t y_ld,
+                   void *gate, void *up, int32_t tokens, int32_t dim, int32_t inner, int32_t act, void *h, bool whole,
+                   cudaStream_t st)
+{
+    TokenArgs a{};
+    a.x = x, a.x_ld = x_ld, a.w0 = wg, a.w1 = wu, a.out = h, a.out_ld = up8(inner), a.o0 = gate, a.o1 = up;
+    a.tokens = tokens, a.n = inner, a.k = dim, a.act = act;
+    ZERO_TRY((token_product<DT, true>(a, whole, false, st)));
+    TokenArgs b{};
+    b.x = h, b.x_ld = up8(inner), b.w0 = wd, b.out = y, b.out_ld = y_ld;
+    b.tokens = tokens, b.n = dim, b.k = inner;
+    return token_product<DT, false>(b, whole, true, st);
+}
+
 }  // namespace
 }  // namespace zpml
 
@@ -862,7 +1050,11 @@ extern "C" int zero_gated_ffn(const void *x, int64_t x_ld, const void *w_gate, c
         return zero_matrix(y, y_ld, tokens, dim, 2, st);
     }
     char *base = static_cast<char *>(ws);
-    Mat mx{x, tokens, dim, tokens > 1 ? x_ld : up8(dim)}, mg{w_gate, inner, dim, dim}, mu{w_up, inner, dim, dim};
+    if (tokens <= kFewTokens)
+        return (dtype == ZERO_F16 ? tokens_forward<ZERO_F16> : tokens_forward<ZERO_BF16>)(
+            x, x_ld, w_gate, w_up, w_down, y, y_ld, gate, up, (int32_t)tokens, (int32_t)dim, (int32_t)inner, act,
+            base + sp.mats, whole, st);
+    Mat mx{x, tokens, dim, x_ld}, mg{w_gate, inner, dim, dim}, mu{w_up, inner, dim, dim};
     Mat md{w_down, dim, inner, inner};
     if (!whole) {
         Mat *all[] = {&mx, &mg, &mu, &md};
