@@ -12,6 +12,9 @@ namespace {
 // act(g) and act'(g), both through s = sigmoid(k(g)): SiLU has k(g) = g, the
 // tanh form of GELU k(g) = 2 sqrt(2/pi) (g + 0.044715 g^3), because
 // (1 + tanh(z)) / 2 = sigmoid(2 z).  d/dg [g s] = s + g s (1 - s) k'(g).
+// The exponential and the reciprocal are CUDA's fast ones (a few units of
+// 2^-23, far below the 16-bit rounding that follows): with the exact ones the
+// gate's epilogue, not the tensor cores, set the pace.
 struct Act {
     float value, slope;
 };
@@ -19,10 +22,12 @@ struct Act {
 __device__ __forceinline__ Act activate(int32_t act, float g)
 {
     constexpr float kA = 1.5957691216057308f, kB = 0.044715f;
-    const float k = act == ZERO_ACT_SILU ? g : kA * (g + kB * g * g * g);
-    const float dk = act == ZERO_ACT_SILU ? 1.0f : kA * (1.0f + 3.0f * kB * g * g);
-    const float s = 1.0f / (1.0f + expf(-k));
-    return {g * s, s + g * s * (1.0f - s) * dk};
+    const float q = g * g;
+    const float k = act == ZERO_ACT_SILU ? g : g * (kA + kA * kB * q);
+    const float dk = act == ZERO_ACT_SILU ? 1.0f : kA + 3.0f * kA * kB * q;
+    const float s = __fdividef(1.0f, 1.0f + __expf(-k));
+    const float v = g * s;
+    return {v, s + v * (1.0f - s) * dk};
 }
 
 // ------------------------------------------------------------- kernels
@@ -33,13 +38,17 @@ __device__ __forceinline__ Act activate(int32_t act, float g)
 // rows, so no operand is ever transposed in memory.
 struct Product {
     CUtensorMap a[2], b[2];  // kGate: b holds the gate's and the up matrix of one pair
+    CUtensorMap c;           // the output, where TMA can write it
     int32_t pairs, kb;       // pairs, blocks of 64 k in each
     int32_t m, n;
     int32_t tiles_n, first;  // tiles along n; the product's first tile in the launch
+    int32_t c_tma;
     void *out;
     int64_t out_ld;
-    int32_t out_vec;  // out's rows are whole 16 bytes
 };
+
+// How the operands of a launch lie: A and B K-major, B MN-major, or both.
+enum Major { kKK, kKMn, kMnMn };
 
 enum Epilogue {
     kStore,   // C as it is
@@ -47,44 +56,56 @@ enum Epilogue {
     kGateBwd  // from dh = C and the kept gate and up: dgate, dup, act(gate) * up
 };
 
-template <int NP>
+// A matrix beside the output: gate and up, or dgate and dup.
+struct Side {
+    CUtensorMap map;
+    void *p;
+    int64_t ld;
+    int32_t tma, vec;  // read or written by TMA; rows of whole 16 bytes
+};
+
+template <int NP, int EPI>
 struct ProductArgs {
     Product p[NP];
-    int32_t tiles, splits;  // tiles of all products; parts that k is cut into
-    int32_t a_rows;         // rows of A that a K-major tile loads (128, or all there are rounded up to 8)
+    Side side[EPI == kStore ? 1 : EPI == kGate ? 2 : 4];  // kGate: gate, up; kGateBwd: dgate, dup, gate, up
+    int32_t products, tiles;
+    int32_t splits;   // parts that k is cut into: the CTAs of a cluster
+    int32_t a_rows;   // rows of A that a K-major tile loads (128, or all there are rounded up to 8)
+    int32_t stages, stage_bytes;  // the ring: a stage is a_rows of A and B's rows
     int32_t act;
-    int32_t out_f32;        // kStore: out is binary32
-    void *o1, *o2;          // kGate: gate, up (or NULL); kGateBwd: dgate, dup
-    const void *gate, *up;  // kGateBwd
-    int64_t o_ld, g_ld;     // row strides of o1 and o2, and of gate and up
-    int32_t o_vec, g_vec;
-    float *partials;        // splits > 1: [tile][split][column][128 rows]
-    unsigned int *tickets;  // splits > 1: one per tile, zero between calls
+    int32_t out_f32;  // kStore: out is binary32
     WsHeader *hdr;
-    uint64_t limit_ns;      // of every wait
+    uint64_t limit_ns;  // of every wait
 };
 
 // A kernel's tile: CG CTAs (a pair shares one tile, half of A's rows and
-// half of B's each), BN columns, STAGES blocks of k in flight.
-template <int CG_, int BN_, int STAGES_, int EPI_WARPS_>
+// half of B's each), BN columns, STAGES blocks of k in flight; IN buffers per
+// warp for the matrices that kGateBwd reads.
+template <int CG_, int BN_, int STAGES_, int EPI_WARPS_, int IN_>
 struct Shape {
-    static constexpr int CG = CG_, BN = BN_, STAGES = STAGES_, EPI_WARPS = EPI_WARPS_;
-    static constexpr int BM = 128 * CG;            // rows of a tile
-    static constexpr int B_ROWS = BN / CG;         // rows of B per CTA
+    static constexpr int CG = CG_, BN = BN_, STAGES = STAGES_, EPI_WARPS = EPI_WARPS_, IN = IN_;
+    static constexpr int BM = 128 * CG;     // rows of a tile
+    static constexpr int B_ROWS = BN / CG;  // rows of B per CTA
     static constexpr int A_BYTES = 128 * 128, B_BYTES = B_ROWS * 128, STAGE = A_BYTES + B_BYTES;
     static constexpr int THREADS = (EPI_WARPS + 2) * 32;
-    static constexpr int TMEM = 2 * BN < 32 ? 32 : 2 * BN;  // two accumulators
-    static constexpr int SMEM = 1024 + STAGES * STAGE + EPI_WARPS * 2048;
+    static constexpr int TMEM = 2 * BN;               // two accumulators
+    static constexpr int WARP_OUT = 4096, WARP_IN = IN * 4096;  // two boxes of 2 KB; gate's and up's boxes
+    static constexpr int SMEM = 1024 + STAGES * STAGE + EPI_WARPS * (WARP_OUT + WARP_IN);
+    static constexpr int PER_SM = SMEM <= 112 * 1024 ? 2 : 1;
+    static_assert(STAGES <= 12 && SMEM <= 232448 - 512, "one CTA's shared memory");
+    static_assert(CG == 2 || STAGES * STAGE >= BN * 512, "a split product's sums lie in the stages");
 };
+
+constexpr int kMaxStages = 12;
 
 struct ProductShared {
-    uint64_t full[8], empty[8], tfull[2], tempty[2];
-    uint32_t tmem, gave_up, last;
+    uint64_t full[kMaxStages], empty[kMaxStages], tfull[2], tempty[2], in[16];
+    uint32_t tmem, gave_up;
 };
 
-// 32 rows of 64 bytes of one warp through 2 KB of shared memory, between a
-// row per lane and eight rows of four 16-byte pieces per access (the pieces
-// XORed so that neither side meets bank conflicts).
+// 32 rows of 64 bytes of one warp in 2 KB of shared memory, under the 64-byte
+// TMA swizzle (16-byte pieces XORed by half the row), which also keeps a row
+// per lane and eight rows of four pieces per access free of bank conflicts.
 __device__ __forceinline__ uint4 *stage_slot(uint4 *stage, int row, int c) { return stage + row * 4 + (c ^ ((row >> 1) & 3)); }
 
 __device__ __forceinline__ void stage_put_row(uint4 *stage, int lane, const uint32_t (&w)[16])
@@ -94,75 +115,59 @@ __device__ __forceinline__ void stage_put_row(uint4 *stage, int lane, const uint
         *stage_slot(stage, lane, c) = make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
 }
 
-// Stage to memory: `rows` rows and `bytes` bytes of each, from p on.
+__device__ __forceinline__ void stage_get_row(uint4 *stage, int lane, uint32_t (&w)[16])
+{
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+        const uint4 x = *stage_slot(stage, lane, c);
+        w[4 * c] = x.x, w[4 * c + 1] = x.y, w[4 * c + 2] = x.z, w[4 * c + 3] = x.w;
+    }
+}
+
+// Stage to memory element by element (rows that are not whole 16 bytes):
+// `rows` rows and `bytes` bytes of each, from p on; a warp writes a row at a
+// time.
 template <int ES>
-__device__ __forceinline__ void stage_flush(const uint4 *stage, int lane, char *p, int64_t ld_bytes, int rows,
+__device__ __forceinline__ void stage_flush(uint4 *stage, int lane, char *p, int64_t ld_bytes, int rows, int64_t bytes)
+{
+    constexpr int kPer = 64 / ES;  // elements of a row: one per lane, or two rows at a time
+    const int e = lane % kPer;
+#pragma unroll 4
+    for (int r = lane / kPer; r < rows; r += 32 / kPer) {
+        const char *s = reinterpret_cast<const char *>(stage_slot(stage, r, e * ES / 16)) + e * ES % 16;
+        if (e * ES < bytes) {
+            if (ES == 4)
+                *reinterpret_cast<uint32_t *>(p + r * ld_bytes + e * 4) = *reinterpret_cast<const uint32_t *>(s);
+            else
+                *reinterpret_cast<uint16_t *>(p + r * ld_bytes + e * 2) = *reinterpret_cast<const uint16_t *>(s);
+        }
+    }
+}
+
+// Memory to the stage without TMA: 16-byte pieces if vec, else element by
+// element; zeros outside.
+__device__ __forceinline__ void stage_fetch(uint4 *stage, int lane, const char *p, int64_t ld_bytes, int rows,
                                             int64_t bytes, bool vec)
 {
     const int c = lane & 3;
+    if (vec) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int row = (lane >> 2) + 8 * i;
-        const uint4 v = *stage_slot(const_cast<uint4 *>(stage), row, c);
-        if (row >= rows)
-            continue;
-        char *q = p + row * ld_bytes + c * 16;
-        if (vec && c * 16 + 16 <= bytes) {
-            *reinterpret_cast<uint4 *>(q) = v;
-        } else {
-            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-            for (int e = 0; e < 16 / ES; ++e)
-                if (c * 16 + e * ES < bytes) {
-                    if (ES == 4)
-                        *reinterpret_cast<uint32_t *>(q + e * 4) = w[e];
-                    else
-                        *reinterpret_cast<uint16_t *>(q + e * 2) = (uint16_t)(w[e >> 1] >> (16 * (e & 1)));
-                }
+        for (int i = 0; i < 4; ++i) {
+            const int row = (lane >> 2) + 8 * i;
+            uint4 v = make_uint4(0, 0, 0, 0);
+            if (row < rows && c * 16 < bytes)
+                v = __ldg(reinterpret_cast<const uint4 *>(p + row * ld_bytes + c * 16));
+            *stage_slot(stage, row, c) = v;
+        }
+    } else {
+#pragma unroll 4
+        for (int r = 0; r < 32; ++r) {
+            uint16_t v = 0;
+            if (r < rows && lane * 2 < bytes)
+                v = __ldg(reinterpret_cast<const uint16_t *>(p + r * ld_bytes + lane * 2));
+            *(reinterpret_cast<uint16_t *>(stage_slot(stage, r, lane >> 3)) + (lane & 7)) = v;
         }
     }
-}
-
-// Memory to registers, in the flush's pattern (zeros outside).
-__device__ __forceinline__ void fetch64(uint4 (&v)[4], int lane, const char *p, int64_t ld_bytes, int rows,
-                                        int64_t bytes, bool vec)
-{
-    const int c = lane & 3;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int row = (lane >> 2) + 8 * i;
-        v[i] = make_uint4(0, 0, 0, 0);
-        if (row >= rows)
-            continue;
-        const char *q = p + row * ld_bytes + c * 16;
-        if (vec && c * 16 + 16 <= bytes) {
-            v[i] = __ldg(reinterpret_cast<const uint4 *>(q));
-        } else {
-            uint32_t w[4] = {};
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-                if (c * 16 + e * 2 < bytes)
-                    w[e >> 1] |= (uint32_t)__ldg(reinterpret_cast<const uint16_t *>(q + e * 2)) << (16 * (e & 1));
-            v[i] = make_uint4(w[0], w[1], w[2], w[3]);
-        }
-    }
-}
-
-// Those registers through the stage to the row of each lane.
-__device__ __forceinline__ void stage_take_row(uint4 *stage, int lane, const uint4 (&v)[4], uint32_t (&w)[16])
-{
-    const int c = lane & 3;
-    __syncwarp();
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-        *stage_slot(stage, (lane >> 2) + 8 * i, c) = v[i];
-    __syncwarp();
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-        const uint4 x = *stage_slot(stage, lane, k);
-        w[4 * k] = x.x, w[4 * k + 1] = x.y, w[4 * k + 2] = x.z, w[4 * k + 3] = x.w;
-    }
-    __syncwarp();
 }
 
 // Two 16-bit elements in a word.
@@ -187,41 +192,62 @@ __device__ __forceinline__ float2 unpack2(uint32_t w)
         return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&w));
 }
 
+// One warp's way out: boxes of 32 rows by 64 bytes through two stage buffers
+// in turn, by TMA where the matrix allows it.
+struct Outlet {
+    uint4 *stage;
+    int lane;
+    uint32_t n;
+
+    template <int ES>
+    __device__ __forceinline__ void put(const uint32_t (&w)[16], const CUtensorMap *map, bool tma, void *out, int64_t ld,
+                                        int64_t row0, int64_t col, int64_t rows, int64_t cols)
+    {
+        uint4 *s = stage + (n++ & 1) * 128;
+        if (lane == 0)
+            bulk_wait_read<1>();
+        __syncwarp();
+        stage_put_row(s, lane, w);
+        if (tma) {
+            fence_proxy_async();
+            __syncwarp();
+            if (lane == 0 && rows > 0 && cols > 0)
+                tma_store(map, smem_addr(s), (int32_t)col, (int32_t)row0);
+        } else {
+            __syncwarp();
+            if (rows > 0 && cols > 0)
+                stage_flush<ES>(s, lane, static_cast<char *>(out) + (row0 * ld + col) * ES, ld * ES,
+                                rows > 32 ? 32 : (int)rows, cols * ES);
+        }
+        if (lane == 0)
+            bulk_commit();  // one group per box, empty or not: the count above then means this buffer
+    }
+};
+
 // One warp's epilogue of 32 columns: C in `r` (kGate: the gate in `r`, up in
-// `r1`), rows row0 + lane, columns col .. col + 31 of the output.
+// `r1`), rows row0 + lane, columns col .. col + 31 of the output.  kGateBwd:
+// gate's and up's boxes lie in the stages g_in and u_in.
 template <int DT, int EPI, int NP>
-__device__ __forceinline__ void finish32(const ProductArgs<NP> &g, const Product &p, uint4 *stage, int lane,
-                                         int64_t row0, int64_t col, const uint32_t (&r)[32], const uint32_t (&r1)[32])
+__device__ __forceinline__ void finish32(const ProductArgs<NP, EPI> &g, const Product &p, Outlet &o, int64_t row0,
+                                         int64_t col, const uint32_t (&r)[32], const uint32_t (&r1)[32],
+                                         const uint32_t (&wg)[16], const uint32_t (&wu)[16])
 {
-    const int64_t left = p.m - row0, cols = p.n - col;
-    const int rows = left > 32 ? 32 : (int)left;
-    if (left <= 0 || cols <= 0)
-        return;
+    const int64_t rows = p.m - row0, cols = p.n - col;
     uint32_t w[16];
-    auto flush16 = [&](void *out, int64_t ld, bool vec) {
-        __syncwarp();
-        stage_put_row(stage, lane, w);
-        __syncwarp();
-        stage_flush<2>(stage, lane, static_cast<char *>(out) + (row0 * ld + col) * 2, ld * 2, rows, cols * 2, vec);
-    };
     auto f = [](uint32_t x) { return __uint_as_float(x); };
     if constexpr (EPI == kStore) {
         if (!g.out_f32) {
 #pragma unroll
             for (int k = 0; k < 16; ++k)
                 w[k] = pack2<DT>(f(r[2 * k]), f(r[2 * k + 1]));
-            flush16(p.out, p.out_ld, p.out_vec);
+            o.template put<2>(w, &p.c, p.c_tma, p.out, p.out_ld, row0, col, rows, cols);
         } else {
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
 #pragma unroll
                 for (int k = 0; k < 16; ++k)
                     w[k] = r[16 * half + k];
-                __syncwarp();
-                stage_put_row(stage, lane, w);
-                __syncwarp();
-                stage_flush<4>(stage, lane, static_cast<char *>(p.out) + (row0 * p.out_ld + col + 16 * half) * 4,
-                               p.out_ld * 4, rows, (cols - 16 * half) * 4, p.out_vec);
+                o.template put<4>(w, &p.c, p.c_tma, p.out, p.out_ld, row0, col + 16 * half, rows, cols - 16 * half);
             }
         }
     } else if constexpr (EPI == kGate) {
@@ -229,98 +255,94 @@ __device__ __forceinline__ void finish32(const ProductArgs<NP> &g, const Product
         for (int k = 0; k < 16; ++k)
             w[k] = pack2<DT>(activate(g.act, f(r[2 * k])).value * f(r1[2 * k]),
                              activate(g.act, f(r[2 * k + 1])).value * f(r1[2 * k + 1]));
-        flush16(p.out, p.out_ld, p.out_vec);
-        if (g.o1) {
+        o.template put<2>(w, &p.c, p.c_tma, p.out, p.out_ld, row0, col, rows, cols);
+        if (g.side[0].p) {
 #pragma unroll
             for (int k = 0; k < 16; ++k)
                 w[k] = pack2<DT>(f(r[2 * k]), f(r[2 * k + 1]));
-            flush16(g.o1, g.o_ld, g.o_vec);
+            o.template put<2>(w, &g.side[0].map, g.side[0].tma, g.side[0].p, g.side[0].ld, row0, col, rows, cols);
 #pragma unroll
             for (int k = 0; k < 16; ++k)
                 w[k] = pack2<DT>(f(r1[2 * k]), f(r1[2 * k + 1]));
-            flush16(g.o2, g.o_ld, g.o_vec);
+            o.template put<2>(w, &g.side[1].map, g.side[1].tma, g.side[1].p, g.side[1].ld, row0, col, rows, cols);
         }
     } else {
-        uint4 vg[4], vu[4];
-        const int64_t at = (row0 * g.g_ld + col) * 2;
-        fetch64(vg, lane, static_cast<const char *>(g.gate) + at, g.g_ld * 2, rows, cols * 2, g.g_vec);
-        fetch64(vu, lane, static_cast<const char *>(g.up) + at, g.g_ld * 2, rows, cols * 2, g.g_vec);
-        uint32_t wg[16], wu[16];
-        stage_take_row(stage, lane, vg, wg);
-        stage_take_row(stage, lane, vu, wu);
+        uint32_t dg[16], du[16];
 #pragma unroll
         for (int k = 0; k < 16; ++k) {
             const float2 gg = unpack2<DT>(wg[k]), uu = unpack2<DT>(wu[k]);
             const float c0 = f(r[2 * k]), c1 = f(r[2 * k + 1]);
             const Act t0 = activate(g.act, gg.x), t1 = activate(g.act, gg.y);
             w[k] = pack2<DT>(t0.value * uu.x, t1.value * uu.y);
-            wg[k] = pack2<DT>(c0 * uu.x * t0.slope, c1 * uu.y * t1.slope);
-            wu[k] = pack2<DT>(c0 * t0.value, c1 * t1.value);
+            dg[k] = pack2<DT>(c0 * uu.x * t0.slope, c1 * uu.y * t1.slope);
+            du[k] = pack2<DT>(c0 * t0.value, c1 * t1.value);
         }
-        flush16(p.out, p.out_ld, p.out_vec);
-#pragma unroll
-        for (int k = 0; k < 16; ++k)
-            w[k] = wg[k];
-        flush16(g.o1, g.o_ld, g.o_vec);
-#pragma unroll
-        for (int k = 0; k < 16; ++k)
-            w[k] = wu[k];
-        flush16(g.o2, g.o_ld, g.o_vec);
+        o.template put<2>(w, &p.c, p.c_tma, p.out, p.out_ld, row0, col, rows, cols);
+        o.template put<2>(dg, &g.side[0].map, g.side[0].tma, g.side[0].p, g.side[0].ld, row0, col, rows, cols);
+        o.template put<2>(du, &g.side[1].map, g.side[1].tma, g.side[1].p, g.side[1].ld, row0, col, rows, cols);
     }
 }
 
-// Where a work item lies.
-struct Item {
-    int32_t product, tile, split, m, n, k0, k1;  // m, n: tile coordinates; k0, k1: blocks over all pairs
+// Where a tile lies.
+struct Tile {
+    int32_t product, m, n;  // m, n: tile coordinates
 };
 
 // Tiles of a product go in groups of kRaster rows of tiles, column by column
 // within a group, so that the tiles in flight share operands in L2.
 constexpr int kRaster = 8;
 
-template <class S, int NP>
-__device__ __forceinline__ Item item_at(const ProductArgs<NP> &g, int32_t index)
+template <class S, int NP, int EPI>
+__device__ __forceinline__ Tile tile_at(const ProductArgs<NP, EPI> &g, int32_t index)
 {
-    Item it;
-    it.tile = index / g.splits;
-    it.split = index - it.tile * g.splits;
+    Tile it;
     it.product = 0;
 #pragma unroll
     for (int q = 1; q < NP; ++q)
-        if (it.tile >= g.p[q].first)
+        if (q < g.products && index >= g.p[q].first)
             it.product = q;
     const Product &p = g.p[it.product];
-    const int32_t t = it.tile - p.first, tiles_m = (p.m - 1) / S::BM + 1, per = kRaster * p.tiles_n;
+    const int32_t t = index - p.first, tiles_m = (p.m - 1) / S::BM + 1, per = kRaster * p.tiles_n;
     const int32_t group = t / per, within = t - group * per;
     const int32_t rows = tiles_m - group * kRaster < kRaster ? tiles_m - group * kRaster : kRaster;
     it.n = within / rows;
     it.m = group * kRaster + (within - it.n * rows);
-    const int64_t kb = (int64_t)p.pairs * p.kb;
-    it.k0 = (int32_t)(kb * it.split / g.splits);
-    it.k1 = (int32_t)(kb * (it.split + 1) / g.splits);
     return it;
 }
 
-// Persistent, one CTA per SM: one warp fills a ring of shared-memory stages
-// by TMA, one thread issues the tcgen05 products into one of two accumulators
-// in tensor memory, and the other warps empty the accumulator before it.
-template <class S, int DT, int EPI, bool AMN, bool BMN, int NP>
-__global__ void __launch_bounds__(S::THREADS, 1) k_ffn_product(const __grid_constant__ ProductArgs<NP> g)
+// One warp fills a ring of shared-memory stages by TMA, one thread issues the
+// tcgen05 products into one of two accumulators in tensor memory, and the
+// other warps empty the accumulator before it.  With splits = 1 the grid is
+// persistent and strides over the tiles.  With splits > 1 (one-CTA shapes, a
+// grid of tiles * splits) the CTAs of a cluster share a tile's k: each leaves
+// its sums in its shared memory, and each then adds up some 32 x 32 blocks
+// of the tile over all of them, in order, and finishes them.
+template <class S, int DT, int EPI, int MAJ, int NP>
+__global__ void __launch_bounds__(S::THREADS, S::PER_SM) k_ffn_product(const __grid_constant__ ProductArgs<NP, EPI> g)
 {
-    constexpr int CG = S::CG, BN = S::BN, STAGES = S::STAGES;
+    constexpr int CG = S::CG, BN = S::BN;
     constexpr int kStepN = EPI == kGate ? BN / 2 : BN;  // output columns per tile
+    constexpr int kIn = EPI == kGateBwd ? S::IN : 0;
+    constexpr bool a_mn = MAJ == kMnMn, b_mn = MAJ != kKK;
     extern __shared__ unsigned char smem_raw[];
     __shared__ ProductShared sh;
     unsigned char *smem = smem_raw + ((1024 - (smem_addr(smem_raw) & 1023u)) & 1023u);
-    unsigned char *stage_area = smem + STAGES * S::STAGE;
+    unsigned char *out_area = smem + S::STAGES * S::STAGE, *in_area = out_area + S::EPI_WARPS * S::WARP_OUT;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const uint32_t rank = CG == 2 ? cluster_rank() : 0;
-    const int32_t workers = gridDim.x / CG, worker = blockIdx.x / CG;
-    const int32_t items = g.tiles * g.splits;
+    const bool split = CG == 1 && g.splits > 1;
+    const uint32_t rank = CG == 2 || split ? cluster_rank() : 0;
+    const uint32_t half = CG == 2 ? rank : 0;  // which half of a pair's tile
+    const int32_t workers = split ? g.tiles : gridDim.x / CG;
+    const int32_t worker = split ? blockIdx.x / g.splits : blockIdx.x / CG;
     constexpr int kTma = S::EPI_WARPS, kMma = S::EPI_WARPS + 1;
+    // this CTA's blocks of k in a product
+    auto k_first = [&](const Product &p) { return split ? (int32_t)((int64_t)p.pairs * p.kb * rank / g.splits) : 0; };
+    auto k_last = [&](const Product &p) {
+        return split ? (int32_t)((int64_t)p.pairs * p.kb * (rank + 1) / g.splits) : p.pairs * p.kb;
+    };
 
     if (threadIdx.x == 0) {
-        for (int s = 0; s < STAGES; ++s) {
+        for (int s = 0; s < g.stages; ++s) {
             mbar_init_count(&sh.full[s], 1);
             mbar_init_count(&sh.empty[s], 1);
         }
@@ -328,50 +350,53 @@ __global__ void __launch_bounds__(S::THREADS, 1) k_ffn_product(const __grid_cons
             mbar_init_count(&sh.tfull[s], 1);
             mbar_init_count(&sh.tempty[s], CG * S::EPI_WARPS);
         }
+        for (int s = 0; s < kIn * S::EPI_WARPS; ++s)
+            mbar_init_count(&sh.in[s], 1);
         sh.gave_up = 0;
         mbar_init_done();
     }
     if (warp == kMma)
         tmem_alloc<CG>(&sh.tmem, S::TMEM);
-    if (warp == kTma && lane == 0)
-        for (int q = 0; q < NP; ++q) {
-            tma_prefetch_map(&g.p[q].a[0]);
-            tma_prefetch_map(&g.p[q].b[0]);
-        }
+    if (warp == kTma && lane < g.products) {
+        tma_prefetch_map(&g.p[lane].a[0]);
+        tma_prefetch_map(&g.p[lane].b[0]);
+    }
     tmem_fence_before();
     __syncthreads();
     if (CG == 2)
         cluster_sync();
     tmem_fence_after();
     const uint32_t tmem = sh.tmem;
+    pdl_launch_next();
     pdl_wait();
 
     if (warp == kTma) {
-        if (lane == 0) {
-            asm volatile("fence.proxy.async.global;" ::: "memory");
-            const uint32_t a_bytes = AMN ? S::A_BYTES : (uint32_t)g.a_rows * 128;
-            uint32_t n = 0;  // stages filled
-            bool ok = true;
-            for (int32_t i = worker; ok && i < items; i += workers) {
-                const Item it = item_at<S>(g, i);
-                const Product &p = g.p[it.product];
-                const int32_t m0 = it.m * S::BM + (int32_t)rank * 128, n0 = it.n * kStepN;
-                for (int32_t kb = it.k0; kb < it.k1; ++kb, ++n) {
-                    const uint32_t s = n % STAGES;
-                    if (!mbar_wait_bounded(&sh.empty[s], ((n / STAGES) & 1) ^ 1, g.limit_ns, &sh.gave_up)) {
-                        ok = false;
-                        break;
-                    }
-                    // the leader's barrier counts the bytes of both CTAs
-                    uint32_t bar = smem_addr(&sh.full[s]);
-                    if (rank == 0)
+        asm volatile("fence.proxy.async.global;" ::: "memory");
+        const uint32_t a_bytes = a_mn ? S::A_BYTES : (uint32_t)g.a_rows * 128;
+        const uint32_t ring = smem_addr(smem);
+        uint32_t s = 0, phase = 1;  // the next stage; the phase that ends when it was read
+        bool ok = true;
+        for (int32_t i = worker; ok && i < g.tiles; i += workers) {
+            const Tile it = tile_at<S>(g, i);
+            const Product &p = g.p[it.product];
+            const int32_t m0 = it.m * S::BM + (int32_t)half * 128, n0 = it.n * kStepN;
+            const int32_t k1 = k_last(p);
+            for (int32_t kb = k_first(p); kb < k1; ++kb) {
+                if (!mbar_wait_warp(&sh.empty[s], phase, g.limit_ns, &sh.gave_up)) {
+                    ok = false;
+                    break;
+                }
+                const int pair = kb >= p.kb;
+                const int32_t k = (kb - pair * p.kb) * 64;
+                const uint32_t sa = ring + s * g.stage_bytes, sb = sa + a_bytes;
+                // the leader's barrier counts the bytes of both CTAs
+                uint32_t bar = smem_addr(&sh.full[s]);
+                if (CG == 2)
+                    bar = peer_addr(bar, 0);
+                if (elect_one()) {
+                    if (half == 0)
                         mbar_expect(&sh.full[s], CG * (a_bytes + S::B_BYTES));
-                    if (CG == 2)
-                        bar = peer_addr(bar, 0);
-                    const int pair = kb >= p.kb;
-                    const int32_t k = (kb - pair * p.kb) * 64;
-                    const uint32_t sa = smem_addr(smem) + s * S::STAGE, sb = sa + S::A_BYTES;
-                    if (AMN) {
+                    if (a_mn) {
 #pragma unroll
                         for (int j = 0; j < 2; ++j)
                             tma_load<CG>(sa + j * 8192, &p.a[pair], m0 + 64 * j, k, bar);
@@ -380,156 +405,233 @@ __global__ void __launch_bounds__(S::THREADS, 1) k_ffn_product(const __grid_cons
                     }
                     if (EPI == kGate) {
                         if (CG == 2) {
-                            tma_load<CG>(sb, &p.b[rank], k, n0, bar);
+                            tma_load<CG>(sb, &p.b[half], k, n0, bar);
                         } else {
                             tma_load<CG>(sb, &p.b[0], k, n0, bar);
                             tma_load<CG>(sb + S::B_BYTES / 2, &p.b[1], k, n0, bar);
                         }
-                    } else if (BMN) {
+                    } else if (b_mn) {
 #pragma unroll
                         for (int j = 0; j < S::B_ROWS / 64; ++j)
-                            tma_load<CG>(sb + j * 8192, &p.b[pair], n0 + (int32_t)rank * S::B_ROWS + 64 * j, k, bar);
+                            tma_load<CG>(sb + j * 8192, &p.b[pair], n0 + (int32_t)half * S::B_ROWS + 64 * j, k, bar);
                     } else {
-                        tma_load<CG>(sb, &p.b[pair], k, n0 + (int32_t)rank * S::B_ROWS, bar);
+                        tma_load<CG>(sb, &p.b[pair], k, n0 + (int32_t)half * S::B_ROWS, bar);
                     }
                 }
+                __syncwarp();
+                if (++s == (uint32_t)g.stages)
+                    s = 0, phase ^= 1;
             }
         }
     } else if (warp == kMma) {
-        if (lane == 0 && rank == 0) {
-            constexpr uint32_t desc = product_desc(DT == ZERO_BF16, AMN, BMN, S::BM, BN);
-            uint32_t n = 0, t = 0;
+        if (half == 0) {
+            constexpr uint32_t desc = product_desc(DT == ZERO_BF16, a_mn, b_mn, S::BM, BN);
+            // 16 k further: 32 bytes of a row, or 16 rows of 128 bytes
+            constexpr uint32_t step_a = a_mn ? 128 : 2, step_b = b_mn ? 128 : 2;
+            const uint32_t a_bytes = a_mn ? S::A_BYTES : (uint32_t)g.a_rows * 128;
+            const uint64_t a0 = operand_desc(smem_addr(smem), a_mn ? 8192 : 16, 1024);
+            const uint64_t b0 = operand_desc(smem_addr(smem) + a_bytes, b_mn ? 8192 : 16, 1024);
+            uint32_t s = 0, phase = 0, t = 0;
             bool ok = true;
-            for (int32_t i = worker; ok && i < items; i += workers, ++t) {
-                const Item it = item_at<S>(g, i);
+            for (int32_t i = worker; ok && i < g.tiles; i += workers, ++t) {
+                const Tile it = tile_at<S>(g, i);
+                const Product &p = g.p[it.product];
                 const uint32_t acc = t & 1;
-                if (!mbar_wait_bounded(&sh.tempty[acc], ((t >> 1) & 1) ^ 1, g.limit_ns, &sh.gave_up))
+                if (!mbar_wait_warp(&sh.tempty[acc], ((t >> 1) & 1) ^ 1, g.limit_ns, &sh.gave_up))
                     break;
                 tmem_fence_after();
                 const uint32_t d = tmem + acc * BN;
-                for (int32_t kb = it.k0; kb < it.k1; ++kb, ++n) {
-                    const uint32_t s = n % STAGES;
-                    if (!mbar_wait_bounded(&sh.full[s], (n / STAGES) & 1, g.limit_ns, &sh.gave_up)) {
+                const int32_t k0 = k_first(p), k1 = k_last(p);
+                for (int32_t kb = k0; kb < k1; ++kb) {
+                    if (!mbar_wait_warp(&sh.full[s], phase, g.limit_ns, &sh.gave_up)) {
                         ok = false;
                         break;
                     }
                     tmem_fence_after();
-                    const uint32_t sa = smem_addr(smem) + s * S::STAGE;
-                    const uint64_t da = operand_desc(sa, AMN ? 8192 : 16, 1024);
-                    const uint64_t db = operand_desc(sa + S::A_BYTES, BMN ? 8192 : 16, 1024);
+                    const uint64_t da = a0 + ((s * g.stage_bytes) >> 4), db = b0 + ((s * g.stage_bytes) >> 4);
+                    if (elect_one()) {
 #pragma unroll
-                    for (int k = 0; k < 4; ++k)  // 16 k: 32 bytes of a row, or 16 rows of 128 bytes
-                        tensor_product<CG>(d, da + k * (AMN ? 128 : 2), db + k * (BMN ? 128 : 2), desc,
-                                           kb != it.k0 || k != 0);
-                    tensor_commit<CG>(&sh.empty[s]);
+                        for (int k = 0; k < 4; ++k)
+                            tensor_product<CG>(d, da + k * step_a, db + k * step_b, desc, kb != k0 || k != 0);
+                        tensor_commit<CG>(&sh.empty[s]);
+                    }
+                    __syncwarp();
+                    if (++s == (uint32_t)g.stages)
+                        s = 0, phase ^= 1;
                 }
-                if (ok)
+                if (ok && elect_one())
                     tensor_commit<CG>(&sh.tfull[acc]);
+                __syncwarp();
             }
         }
     } else {
         const int quarter = warp & 3, part = warp >> 2;  // lanes 32 * quarter on; this warp's share of the columns
         constexpr int kParts = S::EPI_WARPS / 4, kCols = kStepN / kParts;  // output columns per warp
-        uint4 *stage = reinterpret_cast<uint4 *>(stage_area + warp * 2048);
+        Outlet o{reinterpret_cast<uint4 *>(out_area + warp * S::WARP_OUT), lane, 0};
+        const bool in_tma = kIn > 0 && !split && g.side[EPI == kGateBwd ? 2 : 0].tma;
+        // kGateBwd: gate's and up's boxes arrive by TMA, kIn chunks ahead
+        uint32_t asked = 0, taken = 0;
+        int32_t ask_i = worker, ask_c = 0;
+        auto ask = [&] {
+            if (kIn == 0 || !in_tma || ask_i >= g.tiles)
+                return;
+            const Tile it = tile_at<S>(g, ask_i);
+            if (lane == 0) {
+                const uint32_t b = asked % (kIn ? kIn : 1);
+                uint64_t *bar = &sh.in[warp * (kIn ? kIn : 1) + b];
+                const uint32_t dst = smem_addr(in_area + warp * S::WARP_IN + b * 4096);
+                const int32_t row = it.m * S::BM + (int32_t)half * 128 + quarter * 32;
+                const int32_t col = it.n * kStepN + part * kCols + ask_c;
+                mbar_expect(bar, 4096);
+                tma_load<1>(dst, &g.side[EPI == kGateBwd ? 2 : 0].map, col, row, smem_addr(bar));
+                tma_load<1>(dst + 2048, &g.side[EPI == kGateBwd ? 3 : 0].map, col, row, smem_addr(bar));
+            }
+            ++asked;
+            ask_c += 32;
+            if (ask_c >= kCols) {
+                ask_c = 0;
+                ask_i += workers;
+            }
+        };
+#pragma unroll
+        for (int k = 0; k < kIn; ++k)
+            ask();
         uint32_t t = 0;
         bool ok = true;
-        for (int32_t i = worker; i < items; i += workers, ++t) {
-            const Item it = item_at<S>(g, i);
+        for (int32_t i = worker; i < g.tiles; i += workers, ++t) {
+            const Tile it = tile_at<S>(g, i);
             const Product &p = g.p[it.product];
             const uint32_t acc = t & 1;
-            const int64_t row0 = (int64_t)it.m * S::BM + rank * 128 + quarter * 32;
+            const int64_t row0 = (int64_t)it.m * S::BM + half * 128 + quarter * 32;
             const int64_t col0 = (int64_t)it.n * kStepN + part * kCols;
             // a wait that gave up makes this and every later tile NaN
             ok = ok && mbar_wait_bounded(&sh.tfull[acc], (t >> 1) & 1, g.limit_ns, &sh.gave_up);
             ok = __all_sync(0xffffffffu, ok);
             tmem_fence_after();
             const uint32_t from = tmem + acc * BN + ((uint32_t)(quarter * 32) << 16) + part * kCols;
-            uint32_t r[32], r1[32];
-            auto read = [&](int c) {
-                if (!ok) {
+            uint32_t r[32], r1[32], wg[16], wu[16];
+#pragma unroll 1
+            for (int c = 0; c < kCols; c += 32) {
+                if (EPI == kGateBwd && !split) {
+                    if (in_tma) {
+                        const uint32_t b = taken % (kIn ? kIn : 1);
+                        ok = ok && mbar_wait_bounded(&sh.in[warp * (kIn ? kIn : 1) + b], (taken / (kIn ? kIn : 1)) & 1,
+                                                     g.limit_ns, &sh.gave_up);
+                        ok = __all_sync(0xffffffffu, ok);
+                        uint4 *in = reinterpret_cast<uint4 *>(in_area + warp * S::WARP_IN + b * 4096);
+                        stage_get_row(in, lane, wg);
+                        stage_get_row(in + 128, lane, wu);
+                        ++taken;
+                        fence_proxy_async();
+                        __syncwarp();
+                        if (ok)
+                            ask();
+                    } else {
+                        uint4 *in = reinterpret_cast<uint4 *>(in_area + warp * S::WARP_IN);
+                        const int64_t rows = p.m - row0, cols = p.n - col0 - c;
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) {
+                            const Side &sd = g.side[EPI == kGateBwd ? 2 + k : 0];
+                            stage_fetch(in + 128 * k, lane, static_cast<const char *>(sd.p) + (row0 * sd.ld + col0 + c) * 2,
+                                        sd.ld * 2, rows > 32 ? 32 : (int)rows, cols * 2, sd.vec);
+                        }
+                        __syncwarp();
+                        stage_get_row(in, lane, wg);
+                        stage_get_row(in + 128, lane, wu);
+                        __syncwarp();
+                    }
+                }
+                if (ok) {
+                    tmem_load32(from + c, r);
+                    if (EPI == kGate)
+                        tmem_load32(from + BN / 2 + c, r1);
+                    tmem_wait_loads(r);
+                    if (EPI == kGate)
+                        tmem_wait_loads(r1);
+                } else {
 #pragma unroll
                     for (int k = 0; k < 32; ++k)
                         r[k] = r1[k] = 0x7fffffffu;
-                    return;
                 }
-                tmem_load32(from + c, r);
-                if (EPI == kGate)
-                    tmem_load32(from + BN / 2 + c, r1);
-                tmem_wait_loads();
-            };
-            auto release = [&] {
-                tmem_fence_before();
-                __syncwarp();
-                if (lane == 0)
-                    mbar_arrive_cluster(CG == 2 ? peer_addr(smem_addr(&sh.tempty[acc]), 0) : smem_addr(&sh.tempty[acc]));
-            };
-            if (g.splits == 1) {
-#pragma unroll 1
-                for (int c = 0; c < kCols; c += 32) {
-                    read(c);
-                    if (c + 32 >= kCols)
-                        release();
-                    finish32<DT, EPI, NP>(g, p, stage, lane, row0, col0 + c, r, r1);
+                if (c + 32 >= kCols) {
+                    tmem_fence_before();
+                    __syncwarp();
+                    if (lane == 0)
+                        mbar_arrive_cluster(CG == 2 ? peer_addr(smem_addr(&sh.tempty[acc]), 0)
+                                                    : smem_addr(&sh.tempty[acc]));
                 }
-            } else {
-                // Each part of k leaves its sums in the workspace; the part
-                // that arrives last adds all of them in order.
-                const bool mine = row0 + lane < p.m;
-                float *base = g.partials + (int64_t)it.tile * g.splits * BN * 128 + quarter * 32 + lane;
-                auto slot = [&](int split, int column) { return base + ((int64_t)split * BN + column) * 128; };
-#pragma unroll 1
-                for (int c = 0; c < kCols; c += 32) {
-                    read(c);
-                    if (c + 32 >= kCols)
-                        release();
-                    if (mine) {
-#pragma unroll
-                        for (int k = 0; k < 32; ++k) {
-                            __stcg(slot(it.split, part * kCols + c + k), __uint_as_float(r[k]));
-                            if (EPI == kGate)
-                                __stcg(slot(it.split, BN / 2 + part * kCols + c + k), __uint_as_float(r1[k]));
-                        }
-                    }
-                }
-                __threadfence();
-                asm volatile("bar.sync 1, %0;" ::"n"(S::EPI_WARPS * 32) : "memory");
-                if (threadIdx.x == 0) {
-                    sh.last = atomicAdd(&g.tickets[it.tile], 1u) == (unsigned)g.splits - 1;
-                    if (sh.last)
-                        g.tickets[it.tile] = 0;
-                    __threadfence();
-                }
-                asm volatile("bar.sync 1, %0;" ::"n"(S::EPI_WARPS * 32) : "memory");
-                const bool last = sh.last;
-                asm volatile("bar.sync 1, %0;" ::"n"(S::EPI_WARPS * 32) : "memory");
-                if (!last)
-                    continue;
-#pragma unroll 1
-                for (int c = 0; c < kCols; c += 32) {
-                    float s0[32], s1[32];
-#pragma unroll
-                    for (int k = 0; k < 32; ++k)
-                        s0[k] = s1[k] = 0.0f;
-                    if (mine)
-#pragma unroll 1
-                        for (int q = 0; q < g.splits; ++q)
-#pragma unroll
-                            for (int k = 0; k < 32; ++k) {
-                                s0[k] += __ldcg(slot(q, part * kCols + c + k));
-                                if (EPI == kGate)
-                                    s1[k] += __ldcg(slot(q, BN / 2 + part * kCols + c + k));
-                            }
+                if (split) {
+                    // this CTA's sums: [column][row] over the stages, which the products have read
+                    float *sums = reinterpret_cast<float *>(smem) + (part * kCols + c) * 128 + quarter * 32 + lane;
 #pragma unroll
                     for (int k = 0; k < 32; ++k) {
-                        r[k] = __float_as_uint(s0[k]);
-                        r1[k] = __float_as_uint(s1[k]);
+                        sums[k * 128] = __uint_as_float(r[k]);
+                        if (EPI == kGate)
+                            sums[(BN / 2 + k) * 128] = __uint_as_float(r1[k]);
                     }
-                    finish32<DT, EPI, NP>(g, p, stage, lane, row0, col0 + c, r, r1);
+                } else {
+                    finish32<DT, EPI, NP>(g, p, o, row0, col0 + c, r, r1, wg, wu);
                 }
             }
         }
+        if (lane == 0)
+            bulk_wait_all();
     }
 
+    __syncwarp();
+    if (split) {
+        cluster_sync();
+        if (warp < S::EPI_WARPS) {
+            const Tile it = tile_at<S>(g, worker);
+            const Product &p = g.p[it.product];
+            Outlet o{reinterpret_cast<uint4 *>(out_area + warp * S::WARP_OUT), lane, 0};
+            const int64_t m0 = (int64_t)it.m * S::BM, left = p.m - m0;
+            const int quarters = left >= 128 ? 4 : (int)((left + 31) / 32);
+            // blocks of 32 x 32: quarter q of the rows, 32 columns from c on
+            for (int u = (int)rank + warp * g.splits; u < quarters * (kStepN / 32); u += S::EPI_WARPS * g.splits) {
+                const int q = u % quarters, c = u / quarters * 32;
+                const int64_t row0 = m0 + q * 32, col = (int64_t)it.n * kStepN + c;
+                float s0[32], s1[32];
+#pragma unroll
+                for (int k = 0; k < 32; ++k)
+                    s0[k] = s1[k] = 0.0f;
+                const uint32_t at = smem_addr(smem) + (c * 128 + q * 32 + lane) * 4;
+#pragma unroll 1
+                for (int j = 0; j < g.splits; ++j) {
+                    const uint32_t from = peer_addr(at, j);
+#pragma unroll
+                    for (int k = 0; k < 32; ++k) {
+                        s0[k] += load_peer(from + k * 512);
+                        if (EPI == kGate)
+                            s1[k] += load_peer(from + (BN / 2 + k) * 512);
+                    }
+                }
+                uint32_t r[32], r1[32], wg[16], wu[16];
+#pragma unroll
+                for (int k = 0; k < 32; ++k) {
+                    r[k] = __float_as_uint(s0[k]);
+                    r1[k] = __float_as_uint(s1[k]);
+                }
+                if (EPI == kGateBwd) {
+                    uint4 *in = reinterpret_cast<uint4 *>(in_area + warp * S::WARP_IN);
+                    const int64_t rows = p.m - row0, cols = p.n - col;
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        const Side &sd = g.side[EPI == kGateBwd ? 2 + k : 0];
+                        stage_fetch(in + 128 * k, lane, static_cast<const char *>(sd.p) + (row0 * sd.ld + col) * 2,
+                                    sd.ld * 2, rows > 32 ? 32 : (int)rows, cols * 2, sd.vec);
+                    }
+                    __syncwarp();
+                    stage_get_row(in, lane, wg);
+                    stage_get_row(in + 128, lane, wu);
+                    __syncwarp();
+                }
+                finish32<DT, EPI, NP>(g, p, o, row0, col, r, r1, wg, wu);
+            }
+            if (lane == 0)
+                bulk_wait_all();
+        }
+    }
     __syncwarp();
     tmem_fence_before();
     __syncthreads();
@@ -542,7 +644,7 @@ __global__ void __launch_bounds__(S::THREADS, 1) k_ffn_product(const __grid_cons
         while (global_ns() - began < 20000000u) {
         }
     }
-    if (CG == 2)
+    if (CG == 2 || split)
         cluster_sync();
     if (warp == kMma)
         tmem_free<CG>(tmem, S::TMEM);
@@ -695,6 +797,7 @@ struct Copies {
 
 __global__ void __launch_bounds__(kThreads) k_ffn_copy(const __grid_constant__ Copies a)
 {
+    pdl_launch_next();
     for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < a.groups; i += (int64_t)gridDim.x * kThreads) {
         int q = 0;
 #pragma unroll
@@ -703,11 +806,28 @@ __global__ void __launch_bounds__(kThreads) k_ffn_copy(const __grid_constant__ C
                 q = j;
         const Copy &c = a.c[q];
         const int64_t per = c.dst_ld >> 3, r = (i - c.first) / per, col = ((i - c.first) - r * per) * 8;
+        const uint16_t *src = c.src + r * c.src_ld + col;
+        const uint32_t off = (uint32_t)(reinterpret_cast<uintptr_t>(src) >> 1) & 7;
+        const uint16_t *base = src - off;  // the 16 bytes that hold the first element
         uint32_t w[4] = {};
+        if (col + 8 <= c.cols && base >= c.src && base + 16 <= c.src + (c.rows - 1) * c.src_ld + c.cols) {
+            // two 16-byte loads inside the matrix, and eight elements out of their sixteen
+            const uint4 lo = __ldg(reinterpret_cast<const uint4 *>(base)), hi = __ldg(reinterpret_cast<const uint4 *>(base) + 1);
+            const uint32_t x[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+            const uint32_t word = off >> 1, bits = (off & 1) * 16;
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
-            if (col + e < c.cols)
-                w[e >> 1] |= (uint32_t)c.src[r * c.src_ld + col + e] << (16 * (e & 1));
+            for (uint32_t o = 0; o < 4; ++o)
+                if (word == o) {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        w[k] = __funnelshift_r(x[o + k], x[o + k + 1 < 8 ? o + k + 1 : 7], bits);
+                }
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                if (col + e < c.cols)
+                    w[e >> 1] |= (uint32_t)src[e] << (16 * (e & 1));
+        }
         *reinterpret_cast<uint4 *>(c.dst + r * c.dst_ld + col) = make_uint4(w[0], w[1], w[2], w[3]);
     }
 }
@@ -717,11 +837,16 @@ __global__ void __launch_bounds__(kThreads) k_ffn_copy(const __grid_constant__ C
 constexpr int64_t kMostSize = ((int64_t)1 << 31) - 512;
 constexpr int kSms = 152;
 
-using Pair256 = Shape<2, 256, 6, 8>;
-using One128 = Shape<1, 128, 6, 8>;
-using One64 = Shape<1, 64, 8, 4>;
-
-constexpr int kMaxSplitTiles = 512;
+// Pairs of CTAs with 256 x 256 tiles for large products; one-CTA tiles of
+// 128 x 128, and of 128 x 64 with two CTAs per SM, for small ones.  The
+// backward gate's epilogue reads two matrices and writes three, and gives two
+// stages for their buffers.
+template <int EPI>
+using Pair256 = Shape<2, 256, EPI == kGateBwd ? 4 : 6, 8, EPI == kGateBwd ? 2 : 0>;
+template <int EPI>
+using One128 = Shape<1, 128, 4, 8, EPI == kGateBwd ? 1 : 0>;
+template <int EPI>
+using One64 = Shape<1, 64, 3, 4, EPI == kGateBwd ? 1 : 0>;
 
 int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 int64_t up8(int64_t a) { return (a + 7) & ~(int64_t)7; }
@@ -749,57 +874,59 @@ int check_operand(const void *p, int64_t ld, int64_t rows, int64_t cols, int32_t
     return whole && (!aligned16(p) || (rows > 1 && (ld & 7) != 0)) ? ZERO_EALIGN : ZERO_OK;
 }
 
-// How a product is cut: its shape and the parts of k.
+// How a launch is cut: its shape and the parts of k.
 enum Cut { kPair256, kOne128, kOne64 };
 struct Plan {
     Cut cut;
     int splits;
 };
 
-Plan plan_product(int64_t m, int64_t n, int64_t kb, bool gate)
+// The cheapest cut by an estimate of a launch's time in ns: a start (with the
+// epilogue of the last tile), and per wave of tiles and block of k the larger
+// of the issue's time and the tile bytes' through L2.  Its constants were
+// fitted to 1250 launches (tokens 5 to 1000, widths 256 to 8192, all cuts);
+// the cut it takes is on average 1.3 % slower than the best, at worst 22 %.
+// One launch each, measured: 1000 tokens, 4096 x 4096: pairs 26 us, 128 x 128
+// tiles 44, 128 x 64 88; 64 tokens, 6400 to 1600: 33, 28 and 26 us whole, 14,
+// 13.6 and 12.7 us with k in four parts.
+Plan plan_product(int64_t m, int64_t n, int64_t k, bool gate, int most_parts)
 {
-    const int64_t step = gate ? 2 : 1;
-    if (cdiv(m, 256) * cdiv(n * step, 256) >= kSms / 2)
-        return {kPair256, 1};
-    if (cdiv(m, 128) * cdiv(n * step, 128) >= kSms)
-        return {kOne128, 1};
-    const int64_t tiles = cdiv(m, 128) * cdiv(n * step, 64);
-    int64_t splits = tiles < kSms ? kSms / tiles : 1;
-    if (splits > kb / 4)
-        splits = kb / 4;
-    return {kOne64, (int)(splits < 1 ? 1 : splits)};
+    const int64_t cols = n * (gate ? 2 : 1), kb = cdiv(k, 64);
+    const double a_bytes = (double)(m < 128 ? up8(m) : 128) * 128;
+    auto larger = [](double a, double b) { return a > b ? a : b; };
+    const int64_t pairs = cdiv(m, 256) * cdiv(cols, 256), pair_slots = kSms / 2;
+    const double pair_bytes = 65536.0 * (double)(pairs < pair_slots ? pairs : pair_slots);
+    Plan best{kPair256, 1};
+    double least = 11000 + (double)cdiv(pairs, pair_slots) * kb * larger(230, pair_bytes / 13300);
+    for (int c = 0; c < 2; ++c) {
+        const int bn = c == 0 ? 128 : 64;
+        const int64_t tiles = cdiv(m, 128) * cdiv(cols, bn), slots = c == 0 ? kSms : 2 * kSms;
+        for (int parts = 1; parts <= most_parts && parts <= kb; ++parts) {
+            const int64_t ctas = tiles * parts, waves = cdiv(ctas, slots);
+            const double bytes = (double)(ctas < slots ? ctas : slots) * (a_bytes + bn * 128);
+            const double block = c == 0 ? larger(206, bytes / 13000) : larger(120, bytes / 8400);
+            double t = 6000 + (double)waves * cdiv(kb, parts) * block;
+            if (parts > 1)  // joining the parts; and each wave is a new set of CTAs
+                t += 670 + 210 * parts + 8000.0 * (waves - 1);
+            if (t < least)
+                least = t, best = {c == 0 ? kOne128 : kOne64, parts};
+        }
+    }
+    return best;
 }
 
-// Workspace: the header, the tickets of split products, the products'
-// partial sums, then the matrices that a call keeps between its products.
-constexpr size_t kWsTickets = 256;
-constexpr size_t kWsData = kWsTickets + kMaxSplitTiles * sizeof(unsigned int);
-
-size_t partial_bytes(int64_t m, int64_t n, int64_t k, int pairs, bool gate)
-{
-    if (m == 0 || n == 0 || k == 0)
-        return 0;
-    const Plan pl = plan_product(m, n, pairs * cdiv(k, 64), gate);
-    return pl.splits == 1 ? 0 : (size_t)(cdiv(m, 128) * cdiv(n * (gate ? 2 : 1), 64)) * pl.splits * 128 * 64 * 4;
-}
+constexpr int kMostParts = 8;  // CTAs of a portable cluster
 
 struct FfnSpace {
-    size_t partials, mats, mat_bytes, copies, total;
+    size_t mats, mat_bytes, copies, total;
 };
 
+// Workspace: the header, the matrices that a call keeps between its products,
+// and copies of operands whose rows are not whole 16 bytes.
 FfnSpace ffn_space(int64_t m, int64_t d, int64_t f, bool backward)
 {
     FfnSpace s{};
-    size_t part = 0;
-    auto most = [&](size_t x) { part = x > part ? x : part; };
-    most(partial_bytes(m, f, d, 1, true));
-    most(partial_bytes(m, d, f, 1, false));
-    if (backward) {
-        most(partial_bytes(m, f, d, 1, false));
-        most(partial_bytes(m, d, f, 2, false));
-    }
-    s.partials = kWsData;
-    s.mats = s.partials + align256(part);
+    s.mats = 256;
     s.mat_bytes = align256((size_t)m * (size_t)up8(f) * 2);
     s.copies = s.mats + (backward ? 3 : 1) * s.mat_bytes;
     s.total = s.copies;
@@ -817,8 +944,9 @@ struct Mat {
 
 // Operands whose rows are not whole 16 bytes, copied to the workspace; the
 // matrices then name the copies.
-int copy_operands(Mat **mats, int n, char *to, cudaStream_t st)
+int copy_operands(Mat **mats, int n, char *to, bool *copied, cudaStream_t st)
 {
+    *copied = false;
     Copies a{};
     for (int i = 0; i < n; ++i) {
         Mat &m = *mats[i];
@@ -836,52 +964,73 @@ int copy_operands(Mat **mats, int n, char *to, cudaStream_t st)
     }
     if (a.n == 0)
         return ZERO_OK;
+    *copied = true;
     k_ffn_copy<<<grid_for(reinterpret_cast<const void *>(k_ffn_copy), cdiv(a.groups, kThreads), 1 << 30), kThreads, 0,
                  st>>>(a);
     return check_launch("k_ffn_copy");
 }
 
-// The tensor maps of one product in the boxes of a shape; A and B are rows of
-// k (K-major) or, with amn / bmn, rows of m / n.
-template <class S>
-int product_maps(Product *p, int i, const Mat &a, bool amn, const Mat &b, bool bmn, int a_rows, bool gate, int32_t dtype)
-{
-    ZERO_TRY(tensor_map(&p->a[i], a.p, a.rows, a.cols, a.ld, amn ? 64 : a_rows, dtype));
-    return tensor_map(&p->b[i], b.p, b.rows, b.cols, b.ld, bmn ? 64 : gate ? (S::CG == 2 ? 128 : S::BN / 2) : S::B_ROWS,
-                      dtype);
-}
-
-// One launch of up to NP products.
+// One product of a launch.
 struct Spec {
     Mat a[2], b[2];
     int pairs;
     int64_t m, n, k;
     void *out;
     int64_t out_ld;
+    int64_t out_cols;  // n, or a matrix of the workspace's padded width (the columns past n get zeros)
 };
 
-template <class S, int DT, int EPI, bool AMN, bool BMN, int NP>
-int launch_products(const Spec (&specs)[NP], ProductArgs<NP> &g, int splits, int32_t dtype, cudaStream_t st)
+// Whether TMA may write a matrix: it writes whole 16 bytes, so rows must be.
+bool tma_ready(const void *p, int64_t rows, int64_t cols, int64_t ld, int es)
 {
-    constexpr bool gate = EPI == kGate;
+    return aligned16(p) && (cols * es) % 16 == 0 && (rows == 1 || (ld * es) % 16 == 0) && ld < (int64_t)1 << 38;
+}
+
+// An output (or side matrix) in boxes of 32 rows by 64 bytes.
+int box_map(CUtensorMap *map, int32_t *tma, const void *p, int64_t rows, int64_t cols, int64_t ld, int32_t dtype)
+{
+    const int es = elem_bytes(dtype);
+    *tma = tma_ready(p, rows, cols, ld, es);
+    return *tma ? tensor_map(map, p, rows, cols, rows == 1 ? cols : ld, 64 / es, 32, dtype) : ZERO_OK;
+}
+
+int side_matrix(Side *s, const void *p, int64_t rows, int64_t cols, int64_t ld, int32_t dtype)
+{
+    s->p = const_cast<void *>(p);
+    s->ld = ld;
+    s->vec = aligned16(p) && (cols & 7) == 0 && (ld & 7) == 0;
+    return p ? box_map(&s->map, &s->tma, p, rows, cols, ld, dtype) : ZERO_OK;
+}
+
+template <class S, int DT, int EPI, int MAJ, int NP>
+int launch_products(const Spec *specs, int n, ProductArgs<NP, EPI> &g, int splits, bool chained, int32_t dtype,
+                    cudaStream_t st)
+{
+    constexpr bool gate = EPI == kGate, a_mn = MAJ == kMnMn, b_mn = MAJ != kKK;
     g.splits = splits;
+    g.products = n;
     const int64_t m0 = specs[0].m;
-    g.a_rows = !AMN && S::CG == 1 && m0 < 128 ? (int)up8(m0) : 128;
+    g.a_rows = S::CG == 1 && n == 1 && m0 < 128 ? (int)up8(m0) : 128;
+    // With few rows of A the ring's memory holds more, smaller stages (the
+    // products still read 128 rows; what lies past a_rows lands in rows of the
+    // accumulator that no one reads).
+    g.stage_bytes = g.a_rows * 128 + S::B_BYTES;
+    g.stages = S::STAGES * S::STAGE / g.stage_bytes;
+    g.stages = g.stages < kMaxStages ? g.stages : kMaxStages;
     int64_t tiles = 0, longest = 0;
-    for (int q = 0; q < NP; ++q) {
+    for (int q = 0; q < n; ++q) {
         const Spec &s = specs[q];
         Product &p = g.p[q];
-        ZERO_TRY((product_maps<S>(&p, 0, s.a[0], AMN, s.b[0], BMN, g.a_rows, gate, dtype)));
-        if (gate)
-            ZERO_TRY(tensor_map(&p.b[1], s.b[1].p, s.b[1].rows, s.b[1].cols, s.b[1].ld, S::CG == 2 ? 128 : S::BN / 2,
-                                dtype));
-        else if (s.pairs == 2)
-            ZERO_TRY((product_maps<S>(&p, 1, s.a[1], AMN, s.b[1], BMN, g.a_rows, gate, dtype)));
+        for (int i = 0; i < (gate ? 1 : s.pairs); ++i)
+            ZERO_TRY(tensor_map(&p.a[i], s.a[i].p, s.a[i].rows, s.a[i].cols, s.a[i].ld, 64, a_mn ? 64 : g.a_rows, dtype));
+        for (int i = 0; i < (gate ? 2 : s.pairs); ++i)
+            ZERO_TRY(tensor_map(&p.b[i], s.b[i].p, s.b[i].rows, s.b[i].cols, s.b[i].ld, 64,
+                                b_mn ? 64 : gate && S::CG == 1 ? S::BN / 2 : S::B_ROWS, dtype));
         p.pairs = s.pairs, p.kb = (int32_t)cdiv(s.k, 64), p.m = (int32_t)s.m, p.n = (int32_t)s.n;
         p.tiles_n = (int32_t)cdiv(s.n, gate ? S::BN / 2 : S::BN);
         p.first = (int32_t)tiles;
         p.out = s.out, p.out_ld = s.out_ld;
-        p.out_vec = aligned16(s.out) && (s.out_ld * (EPI == kStore && g.out_f32 ? 4 : 2)) % 16 == 0;
+        ZERO_TRY(box_map(&p.c, &p.c_tma, s.out, s.m, s.out_cols, s.out_ld, EPI == kStore && g.out_f32 ? ZERO_F32 : dtype));
         tiles += cdiv(s.m, S::BM) * p.tiles_n;
         longest = s.pairs * (int64_t)p.kb > longest ? s.pairs * (int64_t)p.kb : longest;
     }
@@ -889,21 +1038,27 @@ int launch_products(const Spec (&specs)[NP], ProductArgs<NP> &g, int splits, int
         return ZERO_ESIZE;
     g.tiles = (int32_t)tiles;
     g.limit_ns = 2000000000ull + (uint64_t)longest * 4000;
-    auto kernel = k_ffn_product<S, DT, EPI, AMN, BMN, NP>;
+    auto kernel = k_ffn_product<S, DT, EPI, MAJ, NP>;
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::SMEM);
-    const int64_t workers = (int64_t)sm_count() / S::CG;
-    const int64_t items = tiles * splits;
+    const int64_t workers = (int64_t)sm_count() / S::CG * S::PER_SM;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)((items < workers ? items : workers) * S::CG));
+    cfg.gridDim = dim3((unsigned)(splits > 1 ? tiles * splits : (tiles < workers ? tiles : workers) * S::CG));
     cfg.blockDim = dim3(S::THREADS);
     cfg.dynamicSmemBytes = S::SMEM;
     cfg.stream = st;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = S::CG;
-    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cudaLaunchAttribute attr[2];
     cfg.attrs = attr;
-    cfg.numAttrs = S::CG == 2 ? 1 : 0;
+    if (S::CG == 2 || splits > 1) {
+        cudaLaunchAttribute &c = attr[cfg.numAttrs++];
+        c.id = cudaLaunchAttributeClusterDimension;
+        c.val.clusterDim.x = S::CG == 2 ? 2 : splits;
+        c.val.clusterDim.y = c.val.clusterDim.z = 1;
+    }
+    if (chained) {
+        cudaLaunchAttribute &c = attr[cfg.numAttrs++];
+        c.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        c.val.programmaticStreamSerializationAllowed = 1;
+    }
     if (e == cudaSuccess)
         e = cudaLaunchKernelEx(&cfg, kernel, g);
     if (e != cudaSuccess) {
@@ -914,13 +1069,15 @@ int launch_products(const Spec (&specs)[NP], ProductArgs<NP> &g, int splits, int
     return ZERO_OK;
 }
 
-template <int EPI, bool AMN, bool BMN, int NP>
-int products(const Spec (&specs)[NP], ProductArgs<NP> &g, Plan plan, int32_t dtype, cudaStream_t st)
+// chained: the launch before is this call's own, and this one may be
+// scheduled while it ends.
+template <int EPI, int MAJ, int NP>
+int products(const Spec *specs, int n, ProductArgs<NP, EPI> &g, Plan plan, bool chained, int32_t dtype, cudaStream_t st)
 {
     const bool f16 = dtype == ZERO_F16;
-#define ZERO_CUT(S)                                                                                       \
-    (f16 ? launch_products<S, ZERO_F16, EPI, AMN, BMN, NP>(specs, g, plan.splits, dtype, st)              \
-         : launch_products<S, ZERO_BF16, EPI, AMN, BMN, NP>(specs, g, plan.splits, dtype, st))
+#define ZERO_CUT(S)                                                                                              \
+    (f16 ? launch_products<S<EPI>, ZERO_F16, EPI, MAJ, NP>(specs, n, g, plan.splits, chained, dtype, st)              \
+         : launch_products<S<EPI>, ZERO_BF16, EPI, MAJ, NP>(specs, n, g, plan.splits, chained, dtype, st))
     if (plan.cut == kPair256)
         return ZERO_CUT(Pair256);
     if (plan.cut == kOne128)
@@ -941,14 +1098,6 @@ int zero_matrix(void *p, int64_t ld, int64_t rows, int64_t cols, int es, cudaStr
         return ZERO_ECUDA;
     }
     return ZERO_OK;
-}
-
-template <int NP>
-void workspace_args(ProductArgs<NP> &g, void *ws, const FfnSpace &sp)
-{
-    g.hdr = static_cast<WsHeader *>(ws);
-    g.tickets = reinterpret_cast<unsigned int *>(static_cast<char *>(ws) + kWsTickets);
-    g.partials = reinterpret_cast<float *>(static_cast<char *>(ws) + sp.partials);
 }
 
 // ------------------------------------------------------------- a few tokens
@@ -1056,21 +1205,23 @@ extern "C" int zero_gated_ffn(const void *x, int64_t x_ld, const void *w_gate, c
             base + sp.mats, whole, st);
     Mat mx{x, tokens, dim, x_ld}, mg{w_gate, inner, dim, dim}, mu{w_up, inner, dim, dim};
     Mat md{w_down, dim, inner, inner};
+    bool copied = false;
     if (!whole) {
         Mat *all[] = {&mx, &mg, &mu, &md};
-        ZERO_TRY(copy_operands(all, 4, base + sp.copies, st));
+        ZERO_TRY(copy_operands(all, 4, base + sp.copies, &copied, st));
     }
     const Mat h{base + sp.mats, tokens, inner, up8(inner)};
-    ProductArgs<1> g{};
-    workspace_args(g, ws, sp);
-    g.act = act, g.o1 = gate, g.o2 = up, g.o_ld = inner;
-    g.o_vec = aligned16(gate) && aligned16(up) && (inner & 7) == 0;
-    const Spec s1[1] = {{{mx, mx}, {mg, mu}, 1, tokens, inner, dim, const_cast<void *>(h.p), h.ld}};
-    ZERO_TRY((products<kGate, false, false, 1>(s1, g, plan_product(tokens, inner, cdiv(dim, 64), true), dtype, st)));
-    ProductArgs<1> d{};
-    workspace_args(d, ws, sp);
-    const Spec s2[1] = {{{h, h}, {md, md}, 1, tokens, dim, inner, y, y_ld}};
-    return products<kStore, false, false, 1>(s2, d, plan_product(tokens, dim, cdiv(inner, 64), false), dtype, st);
+    ProductArgs<1, kGate> g{};
+    g.hdr = static_cast<WsHeader *>(ws);
+    g.act = act;
+    ZERO_TRY(side_matrix(&g.side[0], gate, tokens, inner, inner, dtype));
+    ZERO_TRY(side_matrix(&g.side[1], up, tokens, inner, inner, dtype));
+    const Spec s1{{mx, mx}, {mg, mu}, 1, tokens, inner, dim, const_cast<void *>(h.p), h.ld, h.ld};
+    ZERO_TRY((products<kGate, kKK, 1>(&s1, 1, g, plan_product(tokens, inner, dim, true, kMostParts), copied, dtype, st)));
+    ProductArgs<1, kStore> d{};
+    d.hdr = g.hdr;
+    const Spec s2{{h, h}, {md, md}, 1, tokens, dim, inner, y, y_ld, dim};
+    return products<kStore, kKK, 1>(&s2, 1, d, plan_product(tokens, dim, inner, false, kMostParts), true, dtype, st);
 }
 
 extern "C" int zero_gated_ffn_backward(const void *dy, int64_t dy_ld, const void *x, int64_t x_ld, const void *w_gate,
@@ -1107,30 +1258,34 @@ extern "C" int zero_gated_ffn_backward(const void *dy, int64_t dy_ld, const void
     char *base = static_cast<char *>(ws);
     Mat my{dy, tokens, dim, tokens > 1 ? dy_ld : up8(dim)}, mx{x, tokens, dim, tokens > 1 ? x_ld : up8(dim)};
     Mat mg{w_gate, inner, dim, dim}, mu{w_up, inner, dim, dim}, md{w_down, dim, inner, inner};
+    bool copied = false;
     if (!whole) {
         Mat *all[] = {&my, &mx, &mg, &mu, &md};
-        ZERO_TRY(copy_operands(all, 5, base + sp.copies, st));
+        ZERO_TRY(copy_operands(all, 5, base + sp.copies, &copied, st));
     }
     const int64_t ld = up8(inner);
     const Mat dg{base + sp.mats, tokens, inner, ld}, du{base + sp.mats + sp.mat_bytes, tokens, inner, ld},
         h{base + sp.mats + 2 * sp.mat_bytes, tokens, inner, ld};
-    ProductArgs<1> g{};  // dh, and from it dgate, dup and act(gate) * up
-    workspace_args(g, ws, sp);
-    g.act = act, g.o1 = const_cast<void *>(dg.p), g.o2 = const_cast<void *>(du.p), g.o_ld = ld, g.o_vec = 1;
-    g.gate = gate, g.up = up, g.g_ld = inner, g.g_vec = aligned16(gate) && aligned16(up) && (inner & 7) == 0;
-    const Spec s1[1] = {{{my, my}, {md, md}, 1, tokens, inner, dim, const_cast<void *>(h.p), ld}};
-    ZERO_TRY((products<kGateBwd, false, true, 1>(s1, g, plan_product(tokens, inner, cdiv(dim, 64), false), dtype, st)));
-    ProductArgs<1> d{};
-    workspace_args(d, ws, sp);
-    const Spec s2[1] = {{{dg, du}, {mg, mu}, 2, tokens, dim, inner, dx, dx_ld}};
-    ZERO_TRY((products<kStore, false, true, 1>(s2, d, plan_product(tokens, dim, 2 * cdiv(inner, 64), false), dtype, st)));
-    ProductArgs<3> w{};
-    workspace_args(w, ws, sp);
+    ProductArgs<1, kGateBwd> g{};  // dh, and from it dgate, dup and act(gate) * up
+    g.hdr = static_cast<WsHeader *>(ws);
+    g.act = act;
+    ZERO_TRY(side_matrix(&g.side[0], dg.p, tokens, ld, ld, dtype));
+    ZERO_TRY(side_matrix(&g.side[1], du.p, tokens, ld, ld, dtype));
+    ZERO_TRY(side_matrix(&g.side[2], gate, tokens, inner, inner, dtype));
+    ZERO_TRY(side_matrix(&g.side[3], up, tokens, inner, inner, dtype));
+    g.side[2].tma = g.side[3].tma = g.side[2].tma && g.side[3].tma;
+    const Spec s1{{my, my}, {md, md}, 1, tokens, inner, dim, const_cast<void *>(h.p), ld, ld};
+    ZERO_TRY((products<kGateBwd, kKMn, 1>(&s1, 1, g, plan_product(tokens, inner, dim, false, kMostParts), copied, dtype, st)));
+    // dx, then the weight gradients
+    const Spec s2{{dg, du}, {mg, mu}, 2, tokens, dim, inner, dx, dx_ld, dim};
+    ProductArgs<1, kStore> d{};
+    d.hdr = g.hdr;
+    ZERO_TRY((products<kStore, kKMn, 1>(&s2, 1, d, plan_product(tokens, dim, 2 * inner, false, kMostParts), true, dtype, st)));
+    const Spec s3[3] = {{{dg, dg}, {mx, mx}, 1, inner, dim, tokens, dw_gate, dim, dim},
+                        {{du, du}, {mx, mx}, 1, inner, dim, tokens, dw_up, dim, dim},
+                        {{my, my}, {h, h}, 1, dim, inner, tokens, dw_down, inner, inner}};
+    ProductArgs<3, kStore> w{};
+    w.hdr = g.hdr;
     w.out_f32 = gdtype == ZERO_F32;
-    const Spec s3[3] = {{{dg, dg}, {mx, mx}, 1, inner, dim, tokens, dw_gate, dim},
-                        {{du, du}, {mx, mx}, 1, inner, dim, tokens, dw_up, dim},
-                        {{my, my}, {h, h}, 1, dim, inner, tokens, dw_down, inner}};
-    Plan pl = plan_product(3 * inner, dim, cdiv(tokens, 64), false);
-    pl.splits = 1;
-    return products<kStore, true, true, 3>(s3, w, pl, dtype, st);
+    return products<kStore, kMnMn, 3>(s3, 3, w, plan_product(3 * inner, dim, tokens, false, 1), true, dtype, st);
 }

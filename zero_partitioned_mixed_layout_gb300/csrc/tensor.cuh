@@ -33,6 +33,22 @@ __device__ __forceinline__ void cluster_sync()
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
+// One thread of a converged warp, the same at every call.  Loops that issue
+// copies and products run in the whole warp, with this around the issue
+// alone: the operands then stay in uniform registers, where those
+// instructions want them (a loop in one diverged thread took 530 cycles per
+// block of 64 k for four products, whatever their size).
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t p;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(p));
+    return p != 0;
+}
+
 // ------------------------------------------------------------- barriers
 
 __device__ __forceinline__ void mbar_init_count(uint64_t *bar, uint32_t count)
@@ -53,7 +69,7 @@ __device__ __forceinline__ void mbar_expect(uint64_t *bar, uint32_t bytes)
 // Arrives on a barrier of this or another CTA of the cluster.
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t addr)
 {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
 }
 
 // Waits for a phase, at most limit_ns; false if it gave up, or if another
@@ -66,7 +82,7 @@ __device__ __forceinline__ bool mbar_wait_bounded(uint64_t *bar, uint32_t parity
         uint32_t done;
         asm volatile(
             "{\n\t.reg .pred p;\n\t"
-            "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
             "selp.u32 %0, 1, 0, p;\n\t}"
             : "=r"(done)
             : "r"(smem_addr(bar)), "r"(parity)
@@ -83,6 +99,13 @@ __device__ __forceinline__ bool mbar_wait_bounded(uint64_t *bar, uint32_t parity
             }
         }
     }
+}
+
+// The same by a whole warp, with one answer.
+__device__ __forceinline__ bool mbar_wait_warp(uint64_t *bar, uint32_t parity, uint64_t limit_ns,
+                                               volatile uint32_t *gave_up)
+{
+    return __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity, limit_ns, gave_up));
 }
 
 // ------------------------------------------------------------- TMA
@@ -109,6 +132,37 @@ __device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap *map, i
             "[%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
             "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
             : "memory");
+}
+
+// A box from shared memory to `map` at (x, y); what lies outside the matrix
+// is not written.  The issuing thread groups its stores (bulk_commit) and
+// waits until at most N groups still read their shared memory, or, at the
+// end, until all are done.  The boxes' writers fence (fence_proxy_async)
+// before the store.
+__device__ __forceinline__ void tma_store(const CUtensorMap *map, uint32_t src, int32_t x, int32_t y)
+{
+    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];" ::"l"(
+                     reinterpret_cast<uint64_t>(map)),
+                 "r"(x), "r"(y), "r"(src)
+                 : "memory");
+}
+
+__device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
+
+template <int N>
+__device__ __forceinline__ void bulk_wait_read()
+{
+    asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
+}
+
+__device__ __forceinline__ void bulk_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
+
+// A binary32 of another CTA's shared memory (peer_addr).
+__device__ __forceinline__ float load_peer(uint32_t addr)
+{
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+    return v;
 }
 
 // ------------------------------------------------------------- tensor memory
@@ -147,7 +201,6 @@ __device__ __forceinline__ void tmem_free(uint32_t addr, uint32_t columns)
 
 __device__ __forceinline__ void tmem_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tmem_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void tmem_wait_loads() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 
 // 32 columns of this warp's 32 lanes: lane i gets its row's values.
 __device__ __forceinline__ void tmem_load32(uint32_t addr, uint32_t (&r)[32])
@@ -161,6 +214,20 @@ __device__ __forceinline__ void tmem_load32(uint32_t addr, uint32_t (&r)[32])
           "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
           "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
         : "r"(addr));
+}
+
+// Waits for this warp's tensor-memory loads.  The registers pass through, so
+// that nothing uses them earlier.
+__device__ __forceinline__ void tmem_wait_loads(uint32_t (&r)[32])
+{
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                   "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]),
+                   "+r"(r[15]), "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]),
+                   "+r"(r[22]), "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]),
+                   "+r"(r[29]), "+r"(r[30]), "+r"(r[31])
+                 :
+                 : "memory");
 }
 
 // ------------------------------------------------------------- matrix products
@@ -241,22 +308,28 @@ EncodeTiled encode_tiled()
     return fn;
 }
 
-// A map of a row-major 16-bit matrix (rows x cols, row stride ld, a multiple
-// of 8, from a 16-byte boundary) whose boxes are 64 columns (128 bytes,
-// swizzled) by box_rows; what lies outside the matrix reads as zero.
-int tensor_map(CUtensorMap *map, const void *p, int64_t rows, int64_t cols, int64_t ld, int box_rows, int32_t dtype)
+// A map of a row-major matrix (rows x cols, row stride ld * element size a
+// multiple of 16 bytes, from a 16-byte boundary) in boxes of box_cols by
+// box_rows, 64 or 128 bytes wide and swizzled at that width; what lies
+// outside the matrix reads as zero and is not written.
+int tensor_map(CUtensorMap *map, const void *p, int64_t rows, int64_t cols, int64_t ld, int box_cols, int box_rows,
+               int32_t dtype)
 {
     const EncodeTiled encode = encode_tiled();
     if (!encode) {
         set_cuda_error("cuTensorMapEncodeTiled", 0, "entry point not found");
         return ZERO_ECUDA;
     }
-    const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows}, strides[1] = {(cuuint64_t)ld * 2};
-    const cuuint32_t box[2] = {64, (cuuint32_t)box_rows}, step[2] = {1, 1};
-    const CUresult r = encode(
-        map, dtype == ZERO_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
-        const_cast<void *>(p), dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    const int es = dtype == ZERO_F32 ? 4 : 2;
+    const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows}, strides[1] = {(cuuint64_t)ld * es};
+    const cuuint32_t box[2] = {(cuuint32_t)box_cols, (cuuint32_t)box_rows}, step[2] = {1, 1};
+    const CUresult r = encode(map,
+                              dtype == ZERO_F16    ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
+                              : dtype == ZERO_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                                   : CU_TENSOR_MAP_DATA_TYPE_FLOAT32,
+                              2, const_cast<void *>(p), dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                              box_cols * es == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+                              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     if (r != CUDA_SUCCESS) {
         set_cuda_error("cuTensorMapEncodeTiled", (int)r, "tensor map refused");
         return ZERO_ECUDA;
