@@ -652,7 +652,7 @@ __global__ void __launch_bounds__(S::THREADS, S::PER_SM) k_ffn_product(const __g
 
 // ------------------------------------------------------------- a few tokens
 
-// Products for up to four tokens, where the weights' bytes are all there is:
+// Products for one or two tokens, where the weights' bytes are all there is:
 // a warp per row of the weight matrix (kPair: of the gate's and the up matrix
 // together), or `parts` warps of a block that each take a stretch of k and
 // add up in order through shared memory.  A lane multiplies 16-byte pieces of
@@ -683,7 +683,7 @@ __device__ __forceinline__ uint4 load_piece(const uint16_t *p, int32_t i, int32_
 }
 
 template <int DT, int MT, bool kPair, bool kW>
-__global__ void __launch_bounds__(kThreads, MT == 4 ? 2 : MT == 2 ? 3 : 4)
+__global__ void __launch_bounds__(kThreads, MT == 1 ? 4 : 3)
     k_ffn_tokens(const __grid_constant__ TokenArgs a)
 {
     constexpr int R = kPair ? 2 : 1, U = 4;
@@ -787,6 +787,7 @@ struct Copy {
     const uint16_t *src;
     uint16_t *dst;
     int64_t rows, cols, src_ld, dst_ld, first;  // first: the matrix's first 8-element group in the launch
+    FastDiv per;                                // 8-element groups of a row
 };
 
 struct Copies {
@@ -805,7 +806,8 @@ __global__ void __launch_bounds__(kThreads) k_ffn_copy(const __grid_constant__ C
             if (j < a.n && i >= a.c[j].first)
                 q = j;
         const Copy &c = a.c[q];
-        const int64_t per = c.dst_ld >> 3, r = (i - c.first) / per, col = ((i - c.first) - r * per) * 8;
+        const int64_t at = i - c.first, per = c.dst_ld >> 3;
+        const int64_t r = a.groups < kFastDivMost ? fast_div((uint32_t)at, c.per) : at / per, col = (at - r * per) * 8;
         const uint16_t *src = c.src + r * c.src_ld + col;
         const uint32_t off = (uint32_t)(reinterpret_cast<uintptr_t>(src) >> 1) & 7;
         const uint16_t *base = src - off;  // the 16 bytes that hold the first element
@@ -956,7 +958,8 @@ int copy_operands(Mat **mats, int n, char *to, bool *copied, cudaStream_t st)
         if (aligned16(m.p) && (m.ld & 7) == 0)
             continue;
         Copy &c = a.c[a.n++];
-        c = {static_cast<const uint16_t *>(m.p), reinterpret_cast<uint16_t *>(to), m.rows, m.cols, m.ld, ld, a.groups};
+        c = {static_cast<const uint16_t *>(m.p), reinterpret_cast<uint16_t *>(to), m.rows, m.cols, m.ld, ld, a.groups,
+             fast_divisor((uint32_t)(ld / 8))};
         a.groups += m.rows * (ld / 8);
         m.p = to;
         m.ld = ld;
@@ -1102,15 +1105,19 @@ int zero_matrix(void *p, int64_t ld, int64_t rows, int64_t cols, int es, cudaStr
 
 // ------------------------------------------------------------- a few tokens
 
-constexpr int kFewTokens = 4;
+// Up to here a warp per weight row is faster than tensor-core tiles, which
+// hold 128 tokens or a fraction (1600 x 6400, one, two and four tokens: 18, 21
+// and 31 us here, 27 us in tiles).
+constexpr int kFewTokens = 2;
 
-// Warps per weight row: k is shared out until a lane has about four pieces of
-// 8 elements (1024 elements per warp), as long as there are too few rows to
-// give every SM 32 warps.
+// Warps per weight row: one per 2048 of k (8192 x 32768, one token: 240 us; a
+// warp for whole rows 293), and more, down to 512 of k each, while there are
+// too few rows to give every SM 32 warps.
 int token_parts(int64_t n, int64_t k)
 {
     int parts = 1;
-    while (parts < kWarps && n * parts < (int64_t)kSms * 32 && k >= (int64_t)parts * 2 * 512)
+    while (parts < kWarps && (k > (int64_t)parts * 2048 ||
+                              (n * parts < (int64_t)kSms * 32 && k >= (int64_t)parts * 2 * 512)))
         parts *= 2;
     return parts;
 }
@@ -1119,7 +1126,7 @@ template <int DT, bool kPair>
 int token_product(TokenArgs &a, bool whole, bool chained, cudaStream_t st)
 {
     a.parts = token_parts(a.n, a.k);
-    const int64_t units = cdiv(a.n, kWarps / a.parts), most = (int64_t)sm_count() * (a.tokens == 1 ? 4 : a.tokens == 2 ? 3 : 2);
+    const int64_t units = cdiv(a.n, kWarps / a.parts), most = (int64_t)sm_count() * (a.tokens == 1 ? 4 : 3);
     const int grid = (int)(units < most ? units : most);
     cudaError_t e;
 #define ZERO_MT(MT)                                                                                            \
@@ -1127,10 +1134,8 @@ int token_product(TokenArgs &a, bool whole, bool chained, cudaStream_t st)
            : launch_k(k_ffn_tokens<DT, MT, kPair, false>, grid, kThreads, st, chained, a))
     if (a.tokens == 1)
         e = ZERO_MT(1);
-    else if (a.tokens == 2)
-        e = ZERO_MT(2);
     else
-        e = ZERO_MT(4);
+        e = ZERO_MT(2);
 #undef ZERO_MT
     if (e != cudaSuccess) {
         cudaGetLastError();

@@ -12,26 +12,30 @@ namespace {
 
 // Philox4x32-10 (Salmon, Moraes, Dror and Shaw, "Parallel random numbers: as
 // easy as 1, 2, 3", 2011): ten rounds of two 32 x 32 -> 64 bit products on a
-// 128-bit counter, the key moved on by a constant per round.
-__device__ __forceinline__ uint4 philox4x32_10(uint4 c, uint32_t k0, uint32_t k1)
+// 128-bit counter, the key moved on by a constant per round.  Here word 0 of
+// the counter is the column's quad, word 1 the row and words 2 and 3 the
+// offset, so one product of each of the first two rounds is the row's alone
+// (RowMask), and the keys of all rounds come as launch constants: 38
+// instructions per four elements instead of 60, which is what bounds the
+// kernels below after memory.
+constexpr uint32_t kPhilox0 = 0xD2511F53u, kPhilox1 = 0xCD9E8D57u;
+
+// The 64-bit product as one instruction (written as a C product whose halves
+// are used apart, it became two).
+__device__ __forceinline__ uint64_t wide(uint32_t a, uint32_t b)
 {
-#pragma unroll
-    for (int r = 0; r < 10; ++r) {
-        const uint64_t a = (uint64_t)0xD2511F53u * c.x, b = (uint64_t)0xCD9E8D57u * c.z;
-        c = make_uint4((uint32_t)(b >> 32) ^ c.y ^ k0, (uint32_t)b, (uint32_t)(a >> 32) ^ c.w ^ k1, (uint32_t)a);
-        k0 += 0x9E3779B9u;
-        k1 += 0xBB67AE85u;
-    }
-    return c;
+    uint64_t r;
+    asm("mul.wide.u32 %0, %1, %2;" : "=l"(r) : "r"(a), "r"(b));
+    return r;
 }
 
 // A dropout as the kernels take it.
 struct Drop {
     const uint64_t *d_offset;
     uint64_t offset;
-    uint32_t k0, k1;
-    uint32_t threshold;  // kept iff the word is at least this ...
-    uint32_t all;        // ... and not everything is dropped (p = 1)
+    uint32_t key[10][2];  // of each round
+    uint32_t threshold;   // kept iff the word is at least this ...
+    uint32_t all;         // ... and not everything is dropped (p = 1)
     float scale;
 };
 
@@ -40,13 +44,31 @@ __device__ __forceinline__ uint64_t drop_offset(const Drop &d)
     return d.d_offset ? d.offset + *d.d_offset : d.offset;
 }
 
-// Whether word w of a counter keeps its element.
-__device__ __forceinline__ bool kept(const Drop &d, uint32_t w) { return w >= d.threshold && !d.all; }
+struct RowMask {
+    uint32_t w0, w2, w3;  // what a row and an offset put into the state after two rounds
+    uint32_t first;       // and into word 2 after the first
+};
 
-__device__ __forceinline__ uint4 drop_words(const Drop &d, uint64_t off, int64_t row, int64_t col)
+__device__ __forceinline__ RowMask row_mask(const Drop &d, uint64_t off, int64_t row)
 {
-    return philox4x32_10(make_uint4((uint32_t)(col >> 2), (uint32_t)row, (uint32_t)off, (uint32_t)(off >> 32)), d.k0,
-                         d.k1);
+    const uint64_t b = wide(kPhilox1, (uint32_t)off);
+    const uint64_t a = wide(kPhilox0, (uint32_t)(b >> 32) ^ (uint32_t)row ^ d.key[0][0]);
+    return {(uint32_t)b ^ d.key[1][0], (uint32_t)(a >> 32) ^ d.key[1][1], (uint32_t)a, (uint32_t)(off >> 32) ^ d.key[0][1]};
+}
+
+// The four words of the columns 4 quad .. 4 quad + 3.
+__device__ __forceinline__ uint4 mask_words(const Drop &d, const RowMask &m, uint32_t quad)
+{
+    const uint64_t a1 = wide(kPhilox0, quad);
+    const uint64_t b2 = wide(kPhilox1, (uint32_t)(a1 >> 32) ^ m.first);
+    uint4 c = make_uint4((uint32_t)(b2 >> 32) ^ m.w0, (uint32_t)b2, m.w2 ^ (uint32_t)a1, m.w3);
+#pragma unroll
+    for (int r = 2; r < 10; ++r) {
+        const uint64_t a = wide(kPhilox0, c.x), b = wide(kPhilox1, c.z);
+        c = make_uint4((uint32_t)(b >> 32) ^ c.y ^ d.key[r][0], (uint32_t)b, (uint32_t)(a >> 32) ^ c.w ^ d.key[r][1],
+                       (uint32_t)a);
+    }
+    return c;
 }
 
 // ------------------------------------------------------------- groups of eight columns
@@ -80,6 +102,7 @@ __device__ __forceinline__ int row_shift(const Rows &a, int64_t r)
     return kW ? 0 : (int)((a.s0 + (uint32_t)r * a.s_step) & a.s_mask);
 }
 
+// (rows are fewer than 2^32)
 template <int DT>
 __device__ __forceinline__ char *row_ptr(const Matrix &m, int64_t r)
 {
@@ -99,7 +122,19 @@ struct Group {
     uint4 w[Elem<DT>::kWords];
 
     __device__ __forceinline__ void to_float(float (&f)[8]) const { Elem<DT>::to_float(w, f); }
+
+    // as pairs, for the two-element binary32 instructions
+    __device__ __forceinline__ void to_pairs(float2 (&f)[4]) const
+    {
+        float t[8];
+        Elem<DT>::to_float(w, t);
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            f[k] = make_float2(t[2 * k], t[2 * k + 1]);
+    }
 };
+
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
 
 // The group at column c0 (< cols) of a row; zeros outside the row.  kRead:
 // the matrix is not written by this kernel.
@@ -148,45 +183,84 @@ __device__ __forceinline__ void store_group(char *row, I c0, I cols, bool vec, c
             store1<DT>(q, e, f[e]);
 }
 
-// The mask words of the eight columns from c0 on.  c0 is 0 mod 4 unless the
-// rows are shifted: then a group spans three counters.
+// Zeros the dropped ones of the eight columns from c0 on (the scale is left to
+// the caller).  c0 is 0 mod 4 unless the rows are shifted: then a group spans
+// three counters, and the third is the first of the next lane's group.  So
+// the kernels give a warp 31 groups of a row that is not whole (lane_group),
+// its last lane works out masks for its neighbour alone, and all lanes of a
+// warp come here together.
 template <bool kW>
-__device__ __forceinline__ void group_words(const Drop &d, uint64_t off, int64_t row, int64_t c0, uint32_t (&w)[8])
+__device__ __forceinline__ void keep_group(const Drop &d, const RowMask &m, int64_t c0, float (&f)[8])
 {
-    const int64_t base = kW ? c0 : c0 & ~(int64_t)3;
-    const uint4 a = drop_words(d, off, row, base), b = drop_words(d, off, row, base + 4);
+    uint32_t w[8];
+    const uint32_t quad = (uint32_t)(c0 >> 2);
+    const uint4 a = mask_words(d, m, quad), b = mask_words(d, m, quad + 1);
     w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w;
     w[4] = b.x, w[5] = b.y, w[6] = b.z, w[7] = b.w;
-    const int o = kW ? 0 : (int)(c0 & 3);
-    if (o != 0) {
-        const uint4 e = drop_words(d, off, row, base + 8);
-        if (o == 1) {
+    if (!kW) {
+        const int o = (int)(c0 & 3);
+        const uint32_t n0 = __shfl_down_sync(0xffffffffu, a.x, 1), n1 = __shfl_down_sync(0xffffffffu, a.y, 1),
+                       n2 = __shfl_down_sync(0xffffffffu, a.z, 1);
+        if (o & 1) {
 #pragma unroll
             for (int k = 0; k < 7; ++k)
                 w[k] = w[k + 1];
-            w[7] = e.x;
-        } else if (o == 2) {
+            w[7] = n0;
+        }
+        if (o & 2) {
 #pragma unroll
             for (int k = 0; k < 6; ++k)
                 w[k] = w[k + 2];
-            w[6] = e.x, w[7] = e.y;
-        } else {
-#pragma unroll
-            for (int k = 0; k < 5; ++k)
-                w[k] = w[k + 3];
-            w[5] = e.x, w[6] = e.y, w[7] = e.z;
+            w[6] = o & 1 ? n1 : n0;
+            w[7] = o & 1 ? n2 : n1;
         }
+    }
+    if (d.all) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            f[e] = 0.0f;
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            f[e] = w[e] >= d.threshold ? f[e] : 0.0f;
     }
 }
 
+// The group of thread t of a row's threads, and whether it is the thread's
+// own (see keep_group).
 template <bool kW>
-__device__ __forceinline__ void drop_group(const Drop &d, uint64_t off, int64_t row, int64_t c0, float (&f)[8])
+__device__ __forceinline__ int lane_group(int t)
 {
-    uint32_t w[8];
-    group_words<kW>(d, off, row, c0, w);
+    return kW ? t : (t >> 5) * 31 + (t & 31);
+}
+
+template <bool kW>
+__device__ __forceinline__ bool owns_group()
+{
+    return kW || (threadIdx.x & 31) != 31;
+}
+
+template <bool kW>
+__device__ __forceinline__ void keep_pairs(const Drop &d, const RowMask &m, int64_t c0, float2 (&f)[4])
+{
+    float t[8];
 #pragma unroll
-    for (int e = 0; e < 8; ++e)
-        f[e] = kept(d, w[e]) ? f[e] * d.scale : 0.0f;
+    for (int k = 0; k < 4; ++k)
+        t[2 * k] = f[k].x, t[2 * k + 1] = f[k].y;
+    keep_group<kW>(d, m, c0, t);
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+        f[k] = make_float2(t[2 * k], t[2 * k + 1]);
+}
+
+template <int DT, bool kW, class I>
+__device__ __forceinline__ void store_pairs(char *row, I c0, I cols, bool vec, const float2 (&f)[4])
+{
+    float t[8];
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+        t[2 * k] = f[k].x, t[2 * k + 1] = f[k].y;
+    store_group<DT, kW>(row, c0, cols, vec, t);
 }
 
 // A weight or bias vector's eight columns, as binary32 (`none` without one).
@@ -211,42 +285,63 @@ __device__ __forceinline__ void load_vector(const void *p, bool f32, I c0, I col
     }
 }
 
+template <int DT, bool kW, class I>
+__device__ __forceinline__ void load_vector(const void *p, bool f32, I c0, I cols, bool vec, float none,
+                                            float2 (&f)[4])
+{
+    float t[8];
+    load_vector<DT, kW>(p, f32, c0, cols, vec, none, t);
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+        f[k] = make_float2(t[2 * k], t[2 * k + 1]);
+}
+
 // ------------------------------------------------------------- dropout
 
 struct DropoutArgs {
     Matrix x, res, out;
     Rows rows;
-    uint32_t groups;               // per row
+    uint32_t groups;  // per row
+    FastDiv per_row;
     uint32_t step_rows, step_groups;  // what the whole grid advances by
     Drop d;
 };
 
-// One thread per group, the grid striding over all groups.
+// One thread per group, the grid striding over all groups.  32 blocks per SM
+// (four waves of them) leave no SM idle at the end: 16384 x 8192 bfloat16
+// with a residual takes 122 us (6.6 TB/s), one wave of eight blocks 130.
+// Without a residual the masks' wide multiplications, four cycles of a
+// scheduler's pipe each, are the limit (109 us).  Two groups at a time per
+// thread, for more loads in flight, took 148 us.
 template <int DT, bool kW>
 __global__ void __launch_bounds__(kThreads) k_dropout_add(const __grid_constant__ DropoutArgs a)
 {
-    const uint32_t flat = blockIdx.x * kThreads + threadIdx.x;
-    int64_t r = flat / a.groups;
-    uint32_t g = flat - (uint32_t)r * a.groups;
+    const uint32_t flat = kW ? blockIdx.x * kThreads + threadIdx.x
+                             : (blockIdx.x * kWarps + (threadIdx.x >> 5)) * 31 + (threadIdx.x & 31);
+    const uint32_t row = fast_div(flat, a.per_row);
+    int64_t r = row;
+    uint32_t g = flat - row * a.groups;
     const uint64_t off = drop_offset(a.d);
     const int64_t cols = a.rows.cols;
-    const bool vec = a.rows.kind != kLoose;
-    while (r < a.rows.rows) {
+    const bool vec = a.rows.kind != kLoose, mine = owns_group<kW>();
+    // (rows that are not whole: until the whole warp has left the matrix)
+    while (kW ? r < a.rows.rows : __any_sync(0xffffffffu, r < a.rows.rows)) {
         const int64_t c0 = (int64_t)g * 8 - row_shift<kW>(a.rows, r);
-        float f[8], t[8];
-        const Group<DT> x = load_group<DT, kW, false>(row_ptr<DT>(a.x, r), c0, cols, vec);
+        const bool in = kW || (mine && r < a.rows.rows && c0 < cols);
+        float f[8] = {}, t[8];
         Group<DT> y{};
-        if (a.res.p)
-            y = load_group<DT, kW, false>(row_ptr<DT>(a.res, r), c0, cols, vec);
-        x.to_float(f);
-        drop_group<kW>(a.d, off, r, c0, f);
-        if (a.res.p) {
-            y.to_float(t);
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-                f[e] += t[e];
+        if (in) {
+            load_group<DT, kW, false>(row_ptr<DT>(a.x, r), c0, cols, vec).to_float(f);
+            if (a.res.p)
+                y = load_group<DT, kW, false>(row_ptr<DT>(a.res, r), c0, cols, vec);
         }
-        store_group<DT, kW>(row_ptr<DT>(a.out, r), c0, cols, vec, f);
+        keep_group<kW>(a.d, row_mask(a.d, off, r), c0, f);
+        y.to_float(t);  // zeros without a residual
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            f[e] = f[e] * a.d.scale + t[e];
+        if (in)
+            store_group<DT, kW>(row_ptr<DT>(a.out, r), c0, cols, vec, f);
         r += a.step_rows;
         g += a.step_groups;
         if (g >= a.groups) {
@@ -266,19 +361,20 @@ __device__ __forceinline__ float warp_sum_f(float v)
     return v;
 }
 
-// Sum over the threads of a row: one warp, or a whole block of `warps` warps
-// (s: 33 floats; one barrier before s is used again).
-template <bool kWarp>
-__device__ __forceinline__ float row_sum(float v, float *s)
+// Sum over the threads of a row: a team of `tpr` threads (whole warps) with
+// its own named barrier; s: a slot per warp of the team.
+__device__ __forceinline__ float team_sum(float v, float *s, int tpr, int team, int t)
 {
     v = warp_sum_f(v);
-    if (kWarp)
+    if (tpr == 32)
         return v;
-    const int lane = threadIdx.x & 31, warps = blockDim.x >> 5;
-    if (lane == 0)
-        s[threadIdx.x >> 5] = v;
-    __syncthreads();
-    return warp_sum_f(lane < warps ? s[lane] : 0.0f);
+    if ((t & 31) == 0)
+        s[t >> 5] = v;
+    asm volatile("bar.sync %0, %1;" ::"r"(team + 1), "r"(tpr) : "memory");
+    v = (t & 31) < (tpr >> 5) ? s[t & 31] : 0.0f;
+    for (int o = 1; o < (tpr >> 5); o <<= 1)
+        v += __shfl_xor_sync(0xffffffffu, v, o);
+    return __shfl_sync(0xffffffffu, v, 0);
 }
 
 struct NormArgs {
@@ -289,92 +385,130 @@ struct NormArgs {
     Rows rows;
     float eps, inv_cols;
     int32_t dropping;
+    int32_t tpr;  // threads per row
     Drop d;
 };
 
-// Forward: a row in registers, NV groups per thread, read once; mean, then
-// the squared deviations from it, then the output.  kWarp: a warp per row
-// (no barriers), else a block per row.
-template <int DT, int NV, bool kWarp, bool kFused, bool kW>
-__global__ void __launch_bounds__(kWarp ? 256 : 512, !kWarp ? 1 : NV <= 2 ? 4 : NV <= 4 ? 3 : 2)
-    k_norm_fwd(const __grid_constant__ NormArgs a)
+// Forward: a row in the registers of a team of tpr threads, NV groups of
+// columns each, read once; mean, then the squared deviations from it, then
+// the output.  A thread keeps its columns (the rows of a team are a multiple
+// of 8 apart, so their shift is the same), and with up to two groups also
+// their weight and bias, and has the next row on its way while it works on
+// this one.
+template <int DT, int NV, bool kFused, bool kW>
+__global__ void __launch_bounds__(NV == 1 ? 768 : NV == 2 ? 640 : 512) k_norm_fwd(const __grid_constant__ NormArgs a)
 {
+    constexpr bool kAhead = NV <= 2;
     __shared__ float s_red[2][32];
-    const int lane = kWarp ? (int)(threadIdx.x & 31) : (int)threadIdx.x;
-    const int tpr = kWarp ? 32 : (int)blockDim.x;
-    const int64_t first = kWarp ? (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5) : (int64_t)blockIdx.x;
-    const int64_t step = kWarp ? (int64_t)gridDim.x * 8 : (int64_t)gridDim.x;
+    const int tpr = a.tpr, team = threadIdx.x / tpr, t0 = threadIdx.x - team * tpr, teams = blockDim.x / tpr;
+    float *const red0 = s_red[0] + team * (tpr >> 5), *const red1 = s_red[1] + team * (tpr >> 5);
     const uint64_t off = kFused && a.dropping ? drop_offset(a.d) : 0;
     const int cols = (int)a.rows.cols;
     const bool vec = a.rows.kind != kLoose;
-    for (int64_t r = first; r < a.rows.rows; r += step) {
-        const int at = lane * 8 - row_shift<kW>(a.rows, r);
-        Group<DT> raw[NV], add[kFused ? NV : 1];
+    const int64_t step = (int64_t)gridDim.x * teams;
+    int64_t r = (int64_t)blockIdx.x * teams + team;
+    const int at = lane_group<kW>(t0) * 8 - row_shift<kW>(a.rows, r);
+    const int wide = kW ? tpr * 8 : (tpr >> 5) * 31 * 8;  // columns from one of a thread's groups to the next
+    const bool mine = owns_group<kW>();
+    float2 w[kAhead ? NV : 1][4], b[kAhead ? NV : 1][4];
+    const float2 scale = both(kFused && a.dropping ? a.d.scale : 1.0f);
+    if (kAhead) {
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
-            const int c0 = at + v * tpr * 8;
-            if (c0 < cols)
-                raw[v] = load_group<DT, kW>(row_ptr<DT>(a.x, r), c0, cols, vec);
-            else
-                raw[v] = Group<DT>{};
-        }
-        if (kFused && a.res.p) {
+            const int c0 = at + v * wide;
 #pragma unroll
-            for (int v = 0; v < NV; ++v) {
-                const int c0 = at + v * tpr * 8;
-                if (c0 < cols)
-                    add[kFused ? v : 0] = load_group<DT, kW>(row_ptr<DT>(a.res, r), c0, cols, vec);
-                else
-                    add[kFused ? v : 0] = Group<DT>{};
+            for (int k = 0; k < 4; ++k)
+                w[kAhead ? v : 0][k] = b[kAhead ? v : 0][k] = both(0.0f);
+            if (mine && c0 < cols) {
+                load_vector<DT, kW>(a.weight, a.w_f32, c0, cols, a.w_vec, 1.0f, w[kAhead ? v : 0]);
+                load_vector<DT, kW>(a.bias, a.w_f32, c0, cols, a.w_vec, 0.0f, b[kAhead ? v : 0]);
             }
         }
-        float t[NV][8], s = 0.0f;
+    }
+    Group<DT> raw[NV], add[kFused ? NV : 1];
+    auto fetch = [&](int64_t row) {
+        if (row >= a.rows.rows)
+            return;
+        const char *px = row_ptr<DT>(a.x, row), *pr = row_ptr<DT>(a.res, row);
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
-            const int c0 = at + v * tpr * 8;
-            raw[v].to_float(t[v]);
-            if (kFused && c0 < cols) {
-                if (a.dropping)
-                    drop_group<kW>(a.d, off, r, c0, t[v]);
-                if (a.res.p) {
-                    float x[8];
-                    add[kFused ? v : 0].to_float(x);
+            const int c0 = at + v * wide;
+            if (mine && c0 < cols) {
+                raw[v] = load_group<DT, kW>(px, c0, cols, vec);
+                if (kFused && a.res.p)
+                    add[kFused ? v : 0] = load_group<DT, kW>(pr, c0, cols, vec);
+            }
+        }
+    };
 #pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        t[v][e] += x[e];
+    for (int v = 0; v < NV; ++v)
+        raw[v] = add[kFused ? v : 0] = Group<DT>{};
+    if (kAhead)
+        fetch(r);
+    for (; r < a.rows.rows; r += step) {
+        if (!kAhead)
+            fetch(r);
+        RowMask mask{};
+        if (kFused && a.dropping)
+            mask = row_mask(a.d, off, r);
+        char *const ps = row_ptr<DT>(a.sum, r), *const py = row_ptr<DT>(a.y, r);
+        float2 t[NV][4], s = both(0.0f);
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+            const int c0 = at + v * wide;
+            raw[v].to_pairs(t[v]);
+            // (a warp stays together unless its rows are whole)
+            if (kFused && a.dropping && (kW ? c0 : c0 - (int)(threadIdx.x & 31) * 8) < cols)
+                keep_pairs<kW>(a.d, mask, c0, t[v]);
+            if (kFused && mine && c0 < cols) {
+                float2 x[4];
+                add[kFused ? v : 0].to_pairs(x);  // zeros without a residual
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    t[v][k] = __ffma2_rn(t[v][k], scale, x[k]);
+                store_pairs<DT, kW>(ps, c0, cols, vec, t[v]);
+            }
+            // elements outside the row are 0 here
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                s = __fadd2_rn(s, t[v][k]);
+        }
+        if (kAhead)
+            fetch(r + step);
+        const float mean = team_sum(s.x + s.y, red0, tpr, team, t0) * a.inv_cols;
+        s = both(0.0f);
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+            const int c0 = at + v * wide;
+            if (mine && c0 < cols) {
+                const bool full = kW || (c0 >= 0 && c0 + 8 <= cols);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    t[v][k] = __fadd2_rn(t[v][k], both(-mean));
+                    if (!full) {
+                        t[v][k].x = inside<kW>(c0, 2 * k, cols) ? t[v][k].x : 0.0f;
+                        t[v][k].y = inside<kW>(c0, 2 * k + 1, cols) ? t[v][k].y : 0.0f;
+                    }
+                    s = __ffma2_rn(t[v][k], t[v][k], s);
                 }
-                store_group<DT, kW>(row_ptr<DT>(a.sum, r), c0, cols, vec, t[v]);
             }
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-                s += t[v][e];
         }
-        const float mean = row_sum<kWarp>(s, s_red[0]) * a.inv_cols;
-        s = 0.0f;
+        const float rstd = __frsqrt_rn(team_sum(s.x + s.y, red1, tpr, team, t0) * a.inv_cols + a.eps);
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
-            const int c0 = at + v * tpr * 8;
+            const int c0 = at + v * wide;
+            if (mine && c0 < cols) {
+                if (!kAhead) {
+                    load_vector<DT, kW>(a.weight, a.w_f32, c0, cols, a.w_vec, 1.0f, w[0]);
+                    load_vector<DT, kW>(a.bias, a.w_f32, c0, cols, a.w_vec, 0.0f, b[0]);
+                }
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                t[v][e] = inside<kW>(c0, e, cols) ? t[v][e] - mean : 0.0f;
-                s += t[v][e] * t[v][e];
+                for (int k = 0; k < 4; ++k)
+                    t[v][k] = __ffma2_rn(__fmul2_rn(t[v][k], both(rstd)), w[kAhead ? v : 0][k], b[kAhead ? v : 0][k]);
+                store_pairs<DT, kW>(py, c0, cols, vec, t[v]);
             }
         }
-        const float rstd = 1.0f / sqrtf(row_sum<kWarp>(s, s_red[1]) * a.inv_cols + a.eps);
-#pragma unroll
-        for (int v = 0; v < NV; ++v) {
-            const int c0 = at + v * tpr * 8;
-            if (c0 < cols) {
-                float w[8], b[8];
-                load_vector<DT, kW>(a.weight, a.w_f32, c0, cols, a.w_vec, 1.0f, w);
-                load_vector<DT, kW>(a.bias, a.w_f32, c0, cols, a.w_vec, 0.0f, b);
-#pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    t[v][e] = t[v][e] * rstd * w[e] + b[e];
-                store_group<DT, kW>(row_ptr<DT>(a.y, r), c0, cols, vec, t[v]);
-            }
-        }
-        if (lane == 0) {
+        if (t0 == 0) {
             if (a.mean)
                 a.mean[r] = mean;
             if (a.rstd)
@@ -390,42 +524,59 @@ __global__ void __launch_bounds__(512) k_norm_fwd_wide(const __grid_constant__ N
 {
     __shared__ float s_red[2][32];
     const uint64_t off = a.dropping ? drop_offset(a.d) : 0;
-    const int64_t cols = a.rows.cols, step = (int64_t)blockDim.x * 8;
+    const int64_t cols = a.rows.cols, step = (int64_t)(blockDim.x >> 5) * 31 * 8;
+    const bool mine = owns_group<false>();
     const bool vec = a.rows.kind != kLoose;
     for (int64_t r = blockIdx.x; r < a.rows.rows; r += gridDim.x) {
-        const int64_t at = (int64_t)threadIdx.x * 8 - row_shift<false>(a.rows, r);
+        const int64_t first = -(int64_t)row_shift<false>(a.rows, r), at = lane_group<false>(threadIdx.x) * 8;
+        const RowMask mask = row_mask(a.d, off, r);
+        // the whole warp together, for keep_group
         auto value = [&](int64_t c0, float(&t)[8]) {
-            load_group<DT, false>(row_ptr<DT>(a.x, r), c0, cols, vec).to_float(t);
-            if (a.dropping)
-                drop_group<false>(a.d, off, r, c0, t);
-            if (a.res.p) {
-                float x[8];
-                load_group<DT, false>(row_ptr<DT>(a.res, r), c0, cols, vec).to_float(x);
+            const bool in = mine && c0 < cols;
+            Group<DT> x{}, y{};
+            if (in) {
+                x = load_group<DT, false>(row_ptr<DT>(a.x, r), c0, cols, vec);
+                if (a.res.p)
+                    y = load_group<DT, false>(row_ptr<DT>(a.res, r), c0, cols, vec);
+            }
+            x.to_float(t);
+            if (a.dropping) {
+                keep_group<false>(a.d, mask, c0, t);
 #pragma unroll
                 for (int e = 0; e < 8; ++e)
-                    t[e] += x[e];
+                    t[e] *= a.d.scale;
             }
+            float z[8];
+            y.to_float(z);
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                t[e] += z[e];
         };
         float s = 0.0f, t[8];
-        for (int64_t c0 = at; c0 < cols; c0 += step) {
+        for (int64_t pass = first; pass < cols; pass += step) {
+            const int64_t c0 = pass + at;
             value(c0, t);
 #pragma unroll
             for (int e = 0; e < 8; ++e)
                 s += t[e];
         }
-        const float mean = row_sum<false>(s, s_red[0]) * a.inv_cols;
+        const float mean = team_sum(s, s_red[0], 512, 0, threadIdx.x) * a.inv_cols;
         s = 0.0f;
-        for (int64_t c0 = at; c0 < cols; c0 += step) {
+        for (int64_t pass = first; pass < cols; pass += step) {
+            const int64_t c0 = pass + at;
             value(c0, t);
 #pragma unroll
             for (int e = 0; e < 8; ++e)
-                if (c0 + e >= 0 && c0 + e < cols)
+                if (mine && c0 + e >= 0 && c0 + e < cols)
                     s += (t[e] - mean) * (t[e] - mean);
         }
-        const float rstd = 1.0f / sqrtf(row_sum<false>(s, s_red[1]) * a.inv_cols + a.eps);
-        for (int64_t c0 = at; c0 < cols; c0 += step) {
+        const float rstd = __frsqrt_rn(team_sum(s, s_red[1], 512, 0, threadIdx.x) * a.inv_cols + a.eps);
+        for (int64_t pass = first; pass < cols; pass += step) {
+            const int64_t c0 = pass + at;
             float w[8], b[8];
             value(c0, t);
+            if (!mine || c0 >= cols)
+                continue;
             if (a.sum.p)
                 store_group<DT, false>(row_ptr<DT>(a.sum, r), c0, cols, vec, t);
             load_vector<DT, false>(a.weight, a.w_f32, c0, cols, a.w_vec, 1.0f, w);
@@ -458,21 +609,37 @@ struct NormBwdArgs {
     Drop d;
 };
 
+// Two sums over a warp: the halves exchange one of the two, then each half
+// adds up its own (five shuffles, one more to share the results).  Lanes below
+// 16 end with the sum of x, the others with that of y.
+__device__ __forceinline__ float half_sums(float2 v)
+{
+    const bool hi = (threadIdx.x & 16) != 0;
+    float k = hi ? v.y : v.x;
+    k += __shfl_xor_sync(0xffffffffu, hi ? v.x : v.y, 16);
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1)
+        k += __shfl_xor_sync(0xffffffffu, k, o);
+    return k;
+}
+
+__device__ __forceinline__ float2 both_sums(float k)
+{
+    const float other = __shfl_xor_sync(0xffffffffu, k, 16);
+    return (threadIdx.x & 16) != 0 ? make_float2(other, k) : make_float2(k, other);
+}
+
 // Two sums over the threads of a row group (tpr threads of the block, its
 // own named barrier), in a buffer that alternates from row to row.
 __device__ __forceinline__ float2 group_sum2(float2 v, float2 *s, int tpr, int group, int t)
 {
-    v.x = warp_sum_f(v.x);
-    v.y = warp_sum_f(v.y);
+    const float k = half_sums(v);
     if (tpr == 32)
-        return v;
-    if ((t & 31) == 0)
-        s[t >> 5] = v;
+        return both_sums(k);
+    if ((t & 15) == 0)
+        (t & 16 ? s[t >> 5].y : s[t >> 5].x) = k;
     asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(tpr) : "memory");
-    v = (t & 31) < (tpr >> 5) ? s[t & 31] : make_float2(0.0f, 0.0f);
-    v.x = warp_sum_f(v.x);
-    v.y = warp_sum_f(v.y);
-    return v;
+    return both_sums(half_sums((t & 31) < (tpr >> 5) ? s[t & 31] : make_float2(0.0f, 0.0f)));
 }
 
 // Backward: a block of several row groups of tpr threads, each thread with NV
@@ -492,8 +659,11 @@ __global__ void __launch_bounds__(NV == 1 ? 768 : 512) k_norm_bwd(const __grid_c
     const int64_t step = (int64_t)gridDim.x * groups;
     const uint64_t off = a.dropping ? drop_offset(a.d) : 0;
     const bool vec = a.rows.kind != kLoose;
+    pdl_launch_next();
     int64_t r = (int64_t)blockIdx.x * groups + group;
-    const int at = t * 8 - row_shift<kW>(a.rows, r);
+    const int at = lane_group<kW>(t) * 8 - row_shift<kW>(a.rows, r);
+    const int wide = kW ? tpr * 8 : (tpr >> 5) * 31 * 8;  // columns from one of a thread's groups to the next
+    const bool mine = owns_group<kW>();
     float dw[NV][8], db[NV][8], w[NV][8];
     Group<DT> ndy[NV], nx[NV], nres[NV];
     float nmean = 0.0f, nrstd = 0.0f;
@@ -502,8 +672,8 @@ __global__ void __launch_bounds__(NV == 1 ? 768 : 512) k_norm_bwd(const __grid_c
             return;
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
-            const int c0 = at + v * tpr * 8;
-            if (c0 < cols) {
+            const int c0 = at + v * wide;
+            if (mine && c0 < cols) {
                 ndy[v] = load_group<DT, kW>(row_ptr<DT>(a.dy, row), c0, cols, vec);
                 nx[v] = load_group<DT, kW>(row_ptr<DT>(a.x, row), c0, cols, vec);
                 if (a.dres.p)
@@ -515,12 +685,12 @@ __global__ void __launch_bounds__(NV == 1 ? 768 : 512) k_norm_bwd(const __grid_c
     };
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
-        const int c0 = at + v * tpr * 8;
+        const int c0 = at + v * wide;
         ndy[v] = nx[v] = nres[v] = Group<DT>{};
 #pragma unroll
         for (int e = 0; e < 8; ++e)
             dw[v][e] = db[v][e] = w[v][e] = 0.0f;
-        if (c0 < cols)
+        if (mine && c0 < cols)
             load_vector<DT, kW>(a.weight, a.w_f32, c0, cols, a.w_vec, 1.0f, w[v]);
     }
     fetch(r);
@@ -530,15 +700,14 @@ __global__ void __launch_bounds__(NV == 1 ? 768 : 512) k_norm_bwd(const __grid_c
         float2 s = make_float2(0.0f, 0.0f);
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
-            const int c0 = at + v * tpr * 8;
             float dy[8], x[8];
             cdy[v] = ndy[v], cx[v] = nx[v], cres[v] = nres[v];
             cdy[v].to_float(dy);
             cx[v].to_float(x);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                // outside the row dy is 0, and 0 - mean must not be seen
-                const float xh = inside<kW>(c0, e, cols) ? (x[e] - mean) * rstd : 0.0f, g = dy[e] * w[v][e];
+                // outside the row dy and w are 0: its terms vanish
+                const float xh = (x[e] - mean) * rstd, g = dy[e] * w[v][e];
                 dw[v][e] += dy[e] * xh;
                 db[v][e] += dy[e];
                 s.x += g;
@@ -551,9 +720,10 @@ __global__ void __launch_bounds__(NV == 1 ? 768 : 512) k_norm_bwd(const __grid_c
         s.y *= a.inv_cols;
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
-            const int c0 = at + v * tpr * 8;
-            if (c0 >= cols)
+            const int c0 = at + v * wide;
+            if (kW && c0 >= cols)
                 continue;
+            const bool in = kW || (mine && c0 < cols);
             float dy[8], x[8];
             cdy[v].to_float(dy);
             cx[v].to_float(x);
@@ -566,25 +736,33 @@ __global__ void __launch_bounds__(NV == 1 ? 768 : 512) k_norm_bwd(const __grid_c
                 for (int e = 0; e < 8; ++e)
                     dy[e] += x[e];
             }
-            store_group<DT, kW>(row_ptr<DT>(a.dx, r), c0, cols, vec, dy);
-            if (a.dropping) {
-                drop_group<kW>(a.d, off, r, c0, dy);
-                store_group<DT, kW>(row_ptr<DT>(a.dropped, r), c0, cols, vec, dy);
+            if (in)
+                store_group<DT, kW>(row_ptr<DT>(a.dx, r), c0, cols, vec, dy);
+            // (a warp stays together unless its rows are whole)
+            if (a.dropping && (kW || c0 - (int)(threadIdx.x & 31) * 8 < cols)) {
+                keep_group<kW>(a.d, row_mask(a.d, off, r), c0, dy);
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    dy[e] *= a.d.scale;
+                if (in)
+                    store_group<DT, kW>(row_ptr<DT>(a.dropped, r), c0, cols, vec, dy);
             }
         }
     }
     if (!a.partials)
         return;
     // the block's row groups, in order, column by column
-    const int width = tpr * NV * 8;
+    const int width = wide * NV;
 #pragma unroll 1
     for (int which = 0; which < 2; ++which) {
         __syncthreads();
+        if (mine) {
 #pragma unroll
-        for (int v = 0; v < NV; ++v)
+            for (int v = 0; v < NV; ++v)
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-                s_cols[group * width + (v * tpr + t) * 8 + e] = which ? db[v][e] : dw[v][e];
+                for (int e = 0; e < 8; ++e)
+                    s_cols[group * width + v * wide + lane_group<kW>(t) * 8 + e] = which ? db[v][e] : dw[v][e];
+        }
         __syncthreads();
         for (int c = threadIdx.x; c < cols; c += blockDim.x) {
             float sum = 0.0f;
@@ -604,12 +782,14 @@ __global__ void __launch_bounds__(512) k_norm_bwd_wide(const __grid_constant__ N
 {
     __shared__ float2 s_red[2][32];
     const uint64_t off = a.dropping ? drop_offset(a.d) : 0;
-    const int64_t cols = a.rows.cols, step = (int64_t)blockDim.x * 8;
+    const int64_t cols = a.rows.cols, step = (int64_t)(blockDim.x >> 5) * 31 * 8;
+    const bool mine = owns_group<false>();
     const bool vec = a.rows.kind != kLoose;
     int buf = 0;
     for (int64_t r = blockIdx.x; r < a.rows.rows; r += gridDim.x, buf ^= 1) {
-        const int64_t at = (int64_t)threadIdx.x * 8 - row_shift<false>(a.rows, r);
+        const int64_t first = -(int64_t)row_shift<false>(a.rows, r), at = lane_group<false>(threadIdx.x) * 8;
         const float mean = a.mean[r], rstd = a.rstd[r];
+        const RowMask mask = row_mask(a.d, off, r);
         auto value = [&](int64_t c0, float(&g)[8], float(&xh)[8]) {
             float w[8];
             load_group<DT, false>(row_ptr<DT>(a.dy, r), c0, cols, vec).to_float(g);
@@ -622,7 +802,11 @@ __global__ void __launch_bounds__(512) k_norm_bwd_wide(const __grid_constant__ N
             }
         };
         float2 s = make_float2(0.0f, 0.0f);
-        for (int64_t c0 = at; c0 < cols; c0 += step) {
+        for (int64_t pass = first; pass < cols; pass += step) {
+            const int64_t c0 = pass + at;
+            const bool in = mine && c0 < cols;
+            if (!in)
+                continue;
             float g[8], xh[8];
             value(c0, g, xh);
 #pragma unroll
@@ -635,23 +819,31 @@ __global__ void __launch_bounds__(512) k_norm_bwd_wide(const __grid_constant__ N
         s = group_sum2(s, s_red[buf], blockDim.x, 0, threadIdx.x);
         s.x *= a.inv_cols;
         s.y *= a.inv_cols;
-        for (int64_t c0 = at; c0 < cols; c0 += step) {
-            float g[8], xh[8];
-            value(c0, g, xh);
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-                g[e] = rstd * (g[e] - s.x - xh[e] * s.y);
-            if (a.dres.p) {
-                float x[8];
-                load_group<DT, false>(row_ptr<DT>(a.dres, r), c0, cols, vec).to_float(x);
+        for (int64_t pass = first; pass < cols; pass += step) {
+            const int64_t c0 = pass + at;
+            const bool in = mine && c0 < cols;
+            float g[8] = {}, xh[8];
+            if (in) {
+                value(c0, g, xh);
 #pragma unroll
                 for (int e = 0; e < 8; ++e)
-                    g[e] += x[e];
+                    g[e] = rstd * (g[e] - s.x - xh[e] * s.y);
+                if (a.dres.p) {
+                    float x[8];
+                    load_group<DT, false>(row_ptr<DT>(a.dres, r), c0, cols, vec).to_float(x);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        g[e] += x[e];
+                }
+                store_group<DT, false>(row_ptr<DT>(a.dx, r), c0, cols, vec, g);
             }
-            store_group<DT, false>(row_ptr<DT>(a.dx, r), c0, cols, vec, g);
             if (a.dropping) {
-                drop_group<false>(a.d, off, r, c0, g);
-                store_group<DT, false>(row_ptr<DT>(a.dropped, r), c0, cols, vec, g);
+                keep_group<false>(a.d, mask, c0, g);  // the whole warp together
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    g[e] *= a.d.scale;
+                if (in)
+                    store_group<DT, false>(row_ptr<DT>(a.dropped, r), c0, cols, vec, g);
             }
         }
     }
@@ -697,11 +889,11 @@ __global__ void __launch_bounds__(kThreads) k_norm_bwd_wide_cols(const __grid_co
 }
 
 // dweight (blockIdx.y 0) and dbias (1): `n` partials of each column added in
-// a fixed order, a block per 32 columns, eight warps taking every eighth.
-__global__ void __launch_bounds__(kThreads) k_norm_bwd_sum(const float *partials, int n, int64_t cols, void *dweight,
-                                                           void *dbias, int32_t gdtype)
+// a fixed order, a block per 32 columns, 32 warps taking every 32nd.
+__global__ void __launch_bounds__(1024) k_norm_bwd_sum(const float *partials, int n, int64_t cols, void *dweight,
+                                                       void *dbias, int32_t gdtype)
 {
-    __shared__ float s[kWarps][32];
+    __shared__ float s[32][33];
     void *out = blockIdx.y ? dbias : dweight;
     if (!out)
         return;
@@ -710,17 +902,15 @@ __global__ void __launch_bounds__(kThreads) k_norm_bwd_sum(const float *partials
     pdl_wait();
     float sum = 0.0f;
     if (c < cols)
-#pragma unroll 8
-        for (int q = warp; q < n; q += kWarps)
+#pragma unroll 5
+        for (int q = warp; q < n; q += 32)
             sum += __ldcg(partials + ((int64_t)q * 2 + blockIdx.y) * cols + c);
     s[warp][lane] = sum;
     __syncthreads();
-    if (warp == 0 && c < cols) {
-#pragma unroll
-        for (int k = 1; k < kWarps; ++k)
-            sum += s[k][lane];
-        store1_as(gdtype, out, c, sum);
-    }
+    sum = warp_sum_f(s[lane][warp]);  // column `warp` of the block's
+    const int64_t mine = (int64_t)blockIdx.x * 32 + warp;
+    if (lane == 0 && mine < cols)
+        store1_as(gdtype, out, mine, sum);
 }
 
 // ------------------------------------------------------------- host side
@@ -742,8 +932,10 @@ int drop_args(const zero_dropout_t *drop, Drop *d)
     const uint64_t t = (uint64_t)std::floor(drop->p * 4294967296.0 + 0.5);
     d->d_offset = drop->d_offset;
     d->offset = drop->offset;
-    d->k0 = (uint32_t)drop->seed;
-    d->k1 = (uint32_t)(drop->seed >> 32);
+    for (uint32_t r = 0; r < 10; ++r) {
+        d->key[r][0] = (uint32_t)drop->seed + r * 0x9E3779B9u;
+        d->key[r][1] = (uint32_t)(drop->seed >> 32) + r * 0xBB67AE85u;
+    }
     d->all = t > 0xffffffffu;
     d->threshold = (uint32_t)t;
     d->scale = drop->p < 1.0 ? (float)(1.0 / (1.0 - drop->p)) : 0.0f;
@@ -791,53 +983,61 @@ Rows row_groups(int64_t rows, int64_t cols, int32_t dtype, std::initializer_list
 // Groups that cover a row at any of its shifts.
 int64_t groups_per_row(const Rows &g) { return (g.cols + g.s_mask + 7) / 8; }
 
+// Whole warps for a row's groups, per_thread of them each (see keep_group).
+int row_threads(int64_t groups, int per_thread, bool whole)
+{
+    const int64_t lanes = (groups + per_thread - 1) / per_thread;
+    return (int)((whole ? (lanes + 31) / 32 : (lanes + 30) / 31) * 32);
+}
+
 int vector_groups(const Rows &g, const void *a, const void *b) { return g.s_mask == 0 && aligned16(a) && aligned16(b); }
 
-// Rows wider than this go through the three-pass kernels (registers hold NV
-// <= 8 groups for each of at most 512 threads).
-constexpr int64_t kMostGroups = 512 * 8;
+// Threads of a row with four groups each; wider rows go through the
+// three-pass kernels.
+constexpr int kMostThreads = 512;
 
-template <int DT, int NV, bool kFused, bool kW>
-int norm_fwd_nv(const NormArgs &a, bool warp, int block, cudaStream_t st)
+// Blocks of the kernels that go from row to row: one per SM, and a multiple
+// of 8, so that a thread's rows all have the same shift.
+constexpr int kRowBlocks = 152;
+
+template <int DT, bool kFused, bool kW>
+int norm_fwd(NormArgs &a, cudaStream_t st)
 {
-    const int64_t most = (int64_t)sm_count() * 32;
-    if (warp) {
-        const int64_t g = (a.rows.rows + 7) / 8;
-        k_norm_fwd<DT, NV, true, kFused, kW><<<(unsigned)(g < most ? g : most), 256, 0, st>>>(a);
-    } else {
-        k_norm_fwd<DT, NV, false, kFused, kW><<<(unsigned)(a.rows.rows < most ? a.rows.rows : most), block, 0, st>>>(a);
+    const int64_t groups = groups_per_row(a.rows), rows = a.rows.rows;
+    if (row_threads(groups, 4, kW) > kMostThreads) {
+        const int64_t most = (int64_t)sm_count() * 4;
+        k_norm_fwd_wide<DT><<<(unsigned)(rows < most ? rows : most), 512, 0, st>>>(a);
+        return check_launch("k_norm_fwd_wide");
     }
+    // Two groups per thread, one while rows are few (latency); teams fill a
+    // block (what the registers of one block per SM allow), few rows are
+    // spread over all SMs first.
+    const bool few = rows <= 4 * kRowBlocks;
+    int nv = 4;
+    if (groups <= 32 || (few && row_threads(groups, 1, kW) <= 768))
+        nv = 1;
+    else if (row_threads(groups, 2, kW) <= 640)
+        nv = 2;
+    const int tpr = row_threads(groups, nv, kW), most = nv == 1 ? 768 : nv == 2 ? 640 : 512;
+    int64_t teams = most / tpr;
+    if (tpr > 32 && teams > 15)
+        teams = 15;  // named barriers
+    if (rows < teams * kRowBlocks)
+        teams = rows < kRowBlocks ? 1 : (rows + kRowBlocks - 1) / kRowBlocks;
+    a.tpr = tpr;
+    const int64_t need = (rows + teams - 1) / teams;
+    const unsigned grid = (unsigned)(need < kRowBlocks ? need : kRowBlocks), block = (unsigned)(teams * tpr);
+    if (nv == 1)
+        k_norm_fwd<DT, 1, kFused, kW><<<grid, block, 0, st>>>(a);
+    else if (nv == 2)
+        k_norm_fwd<DT, 2, kFused, kW><<<grid, block, 0, st>>>(a);
+    else
+        k_norm_fwd<DT, 4, kFused, kW><<<grid, block, 0, st>>>(a);
     return check_launch("k_norm_fwd");
 }
 
-template <int DT, bool kFused, bool kW>
-int norm_fwd(const NormArgs &a, cudaStream_t st)
-{
-    const int64_t groups = groups_per_row(a.rows);
-    if (groups > kMostGroups) {
-        const int64_t most = (int64_t)sm_count() * 4;
-        k_norm_fwd_wide<DT><<<(unsigned)(a.rows.rows < most ? a.rows.rows : most), 512, 0, st>>>(a);
-        return check_launch("k_norm_fwd_wide");
-    }
-    // A warp per row where that fills the GPU (16 warps per SM) and a lane's
-    // share fits its registers; else a block per row, one or two groups per
-    // thread while rows are few (latency), up to eight for wide rows.
-    const bool warp = groups <= 32 || (groups <= 32 * 8 && a.rows.rows >= 16 * (int64_t)sm_count());
-    int block = 32;
-    if (!warp)
-        block = groups >= 512 ? 512 : (int)((groups + 31) / 32 * 32);
-    const int64_t nv = (groups + block - 1) / block;
-    if (nv <= 1)
-        return norm_fwd_nv<DT, 1, kFused, kW>(a, warp, block, st);
-    if (nv <= 2)
-        return norm_fwd_nv<DT, 2, kFused, kW>(a, warp, block, st);
-    if (nv <= 4)
-        return norm_fwd_nv<DT, 4, kFused, kW>(a, warp, block, st);
-    return norm_fwd_nv<DT, 8, kFused, kW>(a, warp, block, st);
-}
-
 template <int DT>
-int norm_fwd_of(const NormArgs &a, cudaStream_t st)
+int norm_fwd_of(NormArgs &a, cudaStream_t st)
 {
     const bool whole = a.rows.kind == kWhole;
     if (a.sum.p)
@@ -853,29 +1053,27 @@ struct BwdPlan {
     int64_t blocks, partials;
 };
 
-constexpr int kBwdBlocks = 152;  // a multiple of 8 (see k_norm_bwd); one block per SM
-
-BwdPlan bwd_plan(int64_t rows, int64_t groups_row)
+BwdPlan bwd_plan(int64_t rows, int64_t groups_row, bool whole)
 {
     BwdPlan p{};
-    p.wide = groups_row > 1024;
+    p.nv = row_threads(groups_row, 1, whole) <= 768 ? 1 : 2;
+    p.tpr = row_threads(groups_row, p.nv, whole);
+    p.wide = p.tpr > 512 && p.nv == 2;
     if (p.wide) {
         p.partials = rows < kWarps * 64 ? (rows + kWarps - 1) / kWarps : 64;
         return p;
     }
-    p.nv = groups_row <= 768 ? 1 : 2;
-    p.tpr = (int)(((groups_row + p.nv - 1) / p.nv + 31) / 32 * 32);
     p.groups = (p.nv == 1 ? 768 : 512) / p.tpr;
     if (p.tpr > 32 && p.groups > 15)
         p.groups = 15;  // named barriers
     const int64_t need = (rows + p.groups - 1) / p.groups;
-    if (need < kBwdBlocks) {  // few rows: spread them over the SMs
-        const int64_t per = (rows + kBwdBlocks - 1) / kBwdBlocks;
+    if (need < kRowBlocks) {  // few rows: spread them over the SMs
+        const int64_t per = (rows + kRowBlocks - 1) / kRowBlocks;
         if (per < p.groups)
             p.groups = (int)(per < 1 ? 1 : per);
     }
     const int64_t n = (rows + p.groups - 1) / p.groups;
-    p.blocks = n < kBwdBlocks ? n : kBwdBlocks;
+    p.blocks = n < kRowBlocks ? n : kRowBlocks;
     p.partials = p.blocks;
     return p;
 }
@@ -934,12 +1132,15 @@ extern "C" int zero_dropout_add(const void *x, int64_t x_ld, const void *residua
     DropoutArgs a{};
     a.x = matrix(x, x_ld), a.res = matrix(residual, residual_ld), a.out = matrix(out, out_ld);
     a.rows = row_groups(rows, cols, dtype, {a.x, a.res, a.out});
-    a.groups = (uint32_t)groups_per_row(a.rows);
-    a.d = d;
-    const int64_t blocks = (rows * (int64_t)a.groups + kThreads - 1) / kThreads, most = (int64_t)sm_count() * 8;
-    const unsigned grid = (unsigned)(blocks < most ? blocks : most);
-    a.step_rows = grid * kThreads / a.groups, a.step_groups = grid * kThreads % a.groups;
     const bool whole = a.rows.kind == kWhole;
+    // (one more group in rows that are not whole: each then has a neighbour)
+    a.groups = (uint32_t)groups_per_row(a.rows) + (whole ? 0 : 1);
+    a.d = d;
+    a.per_row = fast_divisor(a.groups);
+    const int64_t per_block = whole ? kThreads : kWarps * 31;
+    const int64_t blocks = (rows * (int64_t)a.groups + per_block - 1) / per_block, most = (int64_t)sm_count() * 32;
+    const unsigned grid = (unsigned)(blocks < most ? blocks : most);
+    a.step_rows = (uint32_t)(grid * per_block / a.groups), a.step_groups = (uint32_t)(grid * per_block % a.groups);
     if (dtype == ZERO_F16)
         (whole ? k_dropout_add<ZERO_F16, true> : k_dropout_add<ZERO_F16, false>)<<<grid, kThreads, 0, st>>>(a);
     else if (dtype == ZERO_BF16)
@@ -994,8 +1195,10 @@ extern "C" size_t zero_layer_norm_workspace_bytes(int64_t rows, int64_t cols)
     if (rows < 0 || cols < 0 || check_sizes(rows, cols) != ZERO_OK)
         return 0;
     // rows may start off 16 bytes: up to a group more
-    const BwdPlan a = bwd_plan(rows, (cols + 7) / 8), b = bwd_plan(rows, (cols + 7) / 8 + 1);
-    const int64_t n = a.partials > b.partials ? a.partials : b.partials;
+    const BwdPlan a = bwd_plan(rows, (cols + 7) / 8, true), b = bwd_plan(rows, (cols + 7) / 8, false),
+                  c = bwd_plan(rows, (cols + 7) / 8 + 1, false);
+    int64_t n = a.partials > b.partials ? a.partials : b.partials;
+    n = n > c.partials ? n : c.partials;
     return 256 + align256((size_t)n * 2 * (size_t)cols * 4);
 }
 
@@ -1048,7 +1251,7 @@ extern "C" int zero_layer_norm_backward(const void *dy, int64_t dy_ld, const voi
     }
     if (dweight || dbias)
         a.partials = reinterpret_cast<float *>(static_cast<char *>(ws) + 256);
-    const BwdPlan plan = bwd_plan(rows, groups_per_row(a.rows));
+    const BwdPlan plan = bwd_plan(rows, groups_per_row(a.rows), a.rows.kind == kWhole);
     if (dtype == ZERO_F16)
         ZERO_TRY(norm_bwd<ZERO_F16>(a, plan, st));
     else if (dtype == ZERO_BF16)
@@ -1059,7 +1262,7 @@ extern "C" int zero_layer_norm_backward(const void *dy, int64_t dy_ld, const voi
         return ZERO_OK;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)((cols + 31) / 32), 2);
-    cfg.blockDim = dim3(kThreads);
+    cfg.blockDim = dim3(1024);
     cfg.stream = st;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

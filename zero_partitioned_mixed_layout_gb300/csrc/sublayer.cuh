@@ -49,6 +49,28 @@ __device__ __forceinline__ void store1_as(int32_t dt, void *p, int64_t i, float 
         store1<ZERO_BF16>(p, i, v);
 }
 
+// Division of n < 2^31 by a divisor known at launch: a product and a shift
+// (Granlund and Montgomery 1994).
+struct FastDiv {
+    uint32_t magic, shift;
+};
+
+constexpr int64_t kFastDivMost = (int64_t)1 << 31;
+
+inline FastDiv fast_divisor(uint32_t d)
+{
+    FastDiv f{0, 0};
+    while (((uint64_t)1 << f.shift) < d)
+        ++f.shift;
+    f.magic = (uint32_t)((((uint64_t)1 << 32) * (((uint64_t)1 << f.shift) - d)) / d + 1);
+    return f;
+}
+
+__device__ __forceinline__ uint32_t fast_div(uint32_t n, FastDiv f)
+{
+    return (uint32_t)(((uint64_t)__umulhi(n, f.magic) + n) >> f.shift);
+}
+
 inline int elem_bytes(int32_t dt) { return dt == ZERO_F32 ? 4 : 2; }
 
 // Checks of one array that a call reads or writes: n elements from p on
