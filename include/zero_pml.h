@@ -681,9 +681,9 @@ int zero_layer_norm_backward(const void *dy, int64_t dy_ld, const void *x, int64
 /* y = (act(gate) * up) w_down^T, gate = x w_gate^T, up = x w_up^T.
  * x: tokens x dim, y: tokens x dim; w_gate, w_up: inner x dim and w_down:
  * dim x inner, contiguous (out features x in features).  All of `dtype`: F16
- * or BF16, products on the tensor cores with binary32 sums; the inner product
- * act(gate) * up is rounded to dtype once between the two products (the
- * tensor cores' operand type).  gate, up (tokens x inner, contiguous): both
+ * or BF16, with binary32 sums; act(gate) * up is rounded to dtype once between
+ * the two products (the tensor cores' operand type), but for one or two
+ * tokens, whose products run without them.  gate, up (tokens x inner, contiguous): both
  * given to keep them for the backward pass, or both NULL.
  * When dim and inner are multiples of 8, x (and dy) and the weights must
  * start on 16 bytes with x_ld (dy_ld) a multiple of 8; otherwise the call

@@ -688,9 +688,13 @@ class Dropout:
                            None if d_offset is None else d_offset.data_ptr())
 
 
+_sublayer = None
+
+
 def _sublayer_lib():
-    so = lib()
-    if not getattr(so, "_sublayer_ready", False):
+    global _sublayer
+    if _sublayer is None:
+        so = lib()
         vp, i64, i32, sz = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_size_t
         dp = ctypes.POINTER(_Dropout)
         so.zero_dropout_add.argtypes = [vp, i64, vp, i64, vp, i64, i64, i64, i32, dp, vp]
@@ -708,8 +712,8 @@ def _sublayer_lib():
             getattr(so, f).restype = ctypes.c_int
         for f in ("zero_layer_norm_workspace_bytes", "zero_gated_ffn_workspace_bytes"):
             getattr(so, f).restype = sz
-        so._sublayer_ready = True
-    return so
+        _sublayer = so
+    return _sublayer
 
 
 _codes = {}
@@ -862,9 +866,13 @@ def new_gated_ffn_workspace(tokens: int, dim: int, inner: int, backward: bool = 
 
 
 def _contiguous_matrix(t, what: str, shape, dtypes):
-    if t.shape != shape:
-        raise ValueError(f"{what} must be {shape[0]} x {shape[1]}")
-    return _vector(t, what, shape[0] * shape[1], dtypes)
+    if t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{what} must be {shape[0]} x {shape[1]}, contiguous")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{what} must be {' or '.join(map(str, dtypes))}")
+    if not t.is_cuda:
+        raise ValueError(f"{what} must be a CUDA tensor")
+    return t.data_ptr()
 
 
 def _ffn_weights(x, w_gate, w_up, w_down):

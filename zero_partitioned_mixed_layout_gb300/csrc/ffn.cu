@@ -79,18 +79,18 @@ struct ProductArgs {
 };
 
 // A kernel's tile: CG CTAs (a pair shares one tile, half of A's rows and
-// half of B's each), BN columns, STAGES blocks of k in flight; IN buffers per
-// warp for the matrices that kGateBwd reads.
-template <int CG_, int BN_, int STAGES_, int EPI_WARPS_, int IN_>
+// half of B's each), BN columns, STAGES blocks of k in flight; SETS sets of
+// BOXES boxes (32 rows by 64 bytes) per epilogue warp, one set per 32 columns.
+template <int CG_, int BN_, int STAGES_, int EPI_WARPS_, int BOXES_, int SETS_>
 struct Shape {
-    static constexpr int CG = CG_, BN = BN_, STAGES = STAGES_, EPI_WARPS = EPI_WARPS_, IN = IN_;
+    static constexpr int CG = CG_, BN = BN_, STAGES = STAGES_, EPI_WARPS = EPI_WARPS_, BOXES = BOXES_, SETS = SETS_;
     static constexpr int BM = 128 * CG;     // rows of a tile
     static constexpr int B_ROWS = BN / CG;  // rows of B per CTA
     static constexpr int A_BYTES = 128 * 128, B_BYTES = B_ROWS * 128, STAGE = A_BYTES + B_BYTES;
     static constexpr int THREADS = (EPI_WARPS + 2) * 32;
-    static constexpr int TMEM = 2 * BN;               // two accumulators
-    static constexpr int WARP_OUT = 4096, WARP_IN = IN * 4096;  // two boxes of 2 KB; gate's and up's boxes
-    static constexpr int SMEM = 1024 + STAGES * STAGE + EPI_WARPS * (WARP_OUT + WARP_IN);
+    static constexpr int TMEM = 2 * BN;                // two accumulators
+    static constexpr int WARP_OUT = SETS * BOXES * 2048;
+    static constexpr int SMEM = 1024 + STAGES * STAGE + EPI_WARPS * WARP_OUT;
     static constexpr int PER_SM = SMEM <= 112 * 1024 ? 2 : 1;
     static_assert(STAGES <= 12 && SMEM <= 232448 - 512, "one CTA's shared memory");
     static_assert(CG == 2 || STAGES * STAGE >= BN * 512, "a split product's sums lie in the stages");
@@ -192,45 +192,63 @@ __device__ __forceinline__ float2 unpack2(uint32_t w)
         return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&w));
 }
 
-// One warp's way out: boxes of 32 rows by 64 bytes through two stage buffers
-// in turn, by TMA where the matrix allows it.
+// One warp's way out: the boxes of 32 columns make a set; a set's TMA stores
+// are one group, and sets are used in turn.
+template <class S>
 struct Outlet {
     uint4 *stage;
     int lane;
-    uint32_t n;
+    uint32_t n;  // sets used before
+
+    __device__ __forceinline__ uint4 *box(int k) const { return stage + ((n % S::SETS) * S::BOXES + k) * 128; }
+
+    // The set is free once its last stores have read it.
+    __device__ __forceinline__ void begin() const
+    {
+        if (lane == 0)
+            bulk_wait_read<S::SETS - 1>();
+        __syncwarp();
+    }
+
+    __device__ __forceinline__ void put(int k, const uint32_t (&w)[16]) const { stage_put_row(box(k), lane, w); }
+
+    // Between the last put() and the first store().
+    __device__ __forceinline__ void filled() const
+    {
+        fence_proxy_async();
+        __syncwarp();
+    }
 
     template <int ES>
-    __device__ __forceinline__ void put(const uint32_t (&w)[16], const CUtensorMap *map, bool tma, void *out, int64_t ld,
-                                        int64_t row0, int64_t col, int64_t rows, int64_t cols)
+    __device__ __forceinline__ void store(int k, const CUtensorMap *map, bool tma, void *out, int64_t ld, int64_t row0,
+                                          int64_t col, int64_t rows, int64_t cols) const
     {
-        uint4 *s = stage + (n++ & 1) * 128;
+        if (rows <= 0 || cols <= 0)
+            return;
+        if (!tma)
+            stage_flush<ES>(box(k), lane, static_cast<char *>(out) + (row0 * ld + col) * ES, ld * ES,
+                            rows > 32 ? 32 : (int)rows, cols * ES);
+        else if (lane == 0)
+            tma_store(map, smem_addr(box(k)), (int32_t)col, (int32_t)row0);
+    }
+
+    // One group per set, empty or not, so that begin() can count.
+    __device__ __forceinline__ void end()
+    {
         if (lane == 0)
-            bulk_wait_read<1>();
-        __syncwarp();
-        stage_put_row(s, lane, w);
-        if (tma) {
-            fence_proxy_async();
-            __syncwarp();
-            if (lane == 0 && rows > 0 && cols > 0)
-                tma_store(map, smem_addr(s), (int32_t)col, (int32_t)row0);
-        } else {
-            __syncwarp();
-            if (rows > 0 && cols > 0)
-                stage_flush<ES>(s, lane, static_cast<char *>(out) + (row0 * ld + col) * ES, ld * ES,
-                                rows > 32 ? 32 : (int)rows, cols * ES);
-        }
-        if (lane == 0)
-            bulk_commit();  // one group per box, empty or not: the count above then means this buffer
+            bulk_commit();
+        ++n;
     }
 };
 
 // One warp's epilogue of 32 columns: C in `r` (kGate: the gate in `r`, up in
-// `r1`), rows row0 + lane, columns col .. col + 31 of the output.  kGateBwd:
-// gate's and up's boxes lie in the stages g_in and u_in.
-template <int DT, int EPI, int NP>
-__device__ __forceinline__ void finish32(const ProductArgs<NP, EPI> &g, const Product &p, Outlet &o, int64_t row0,
+// `r1`; kGateBwd: the kept gate and up in `wg` and `wu`, the set begun),
+// rows row0 + lane, columns col .. col + 31 of the output.  `ready` runs when
+// the results are in registers.
+template <class S, int DT, int EPI, int NP, class Ready>
+__device__ __forceinline__ void finish32(const ProductArgs<NP, EPI> &g, const Product &p, Outlet<S> &o, int64_t row0,
                                          int64_t col, const uint32_t (&r)[32], const uint32_t (&r1)[32],
-                                         const uint32_t (&wg)[16], const uint32_t (&wu)[16])
+                                         uint32_t (&wg)[16], uint32_t (&wu)[16], Ready ready)
 {
     const int64_t rows = p.m - row0, cols = p.n - col;
     uint32_t w[16];
@@ -240,47 +258,83 @@ __device__ __forceinline__ void finish32(const ProductArgs<NP, EPI> &g, const Pr
 #pragma unroll
             for (int k = 0; k < 16; ++k)
                 w[k] = pack2<DT>(f(r[2 * k]), f(r[2 * k + 1]));
-            o.template put<2>(w, &p.c, p.c_tma, p.out, p.out_ld, row0, col, rows, cols);
+            o.begin();
+            o.put(0, w);
+            o.filled();
+            o.template store<2>(0, &p.c, p.c_tma, p.out, p.out_ld, row0, col, rows, cols);
+            o.end();
         } else {
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
 #pragma unroll
                 for (int k = 0; k < 16; ++k)
                     w[k] = r[16 * half + k];
-                o.template put<4>(w, &p.c, p.c_tma, p.out, p.out_ld, row0, col + 16 * half, rows, cols - 16 * half);
+                o.begin();
+                o.put(0, w);
+                o.filled();
+                o.template store<4>(0, &p.c, p.c_tma, p.out, p.out_ld, row0, col + 16 * half, rows, cols - 16 * half);
+                o.end();
             }
         }
-    } else if constexpr (EPI == kGate) {
-#pragma unroll
-        for (int k = 0; k < 16; ++k)
-            w[k] = pack2<DT>(activate(g.act, f(r[2 * k])).value * f(r1[2 * k]),
-                             activate(g.act, f(r[2 * k + 1])).value * f(r1[2 * k + 1]));
-        o.template put<2>(w, &p.c, p.c_tma, p.out, p.out_ld, row0, col, rows, cols);
-        if (g.side[0].p) {
-#pragma unroll
-            for (int k = 0; k < 16; ++k)
-                w[k] = pack2<DT>(f(r[2 * k]), f(r[2 * k + 1]));
-            o.template put<2>(w, &g.side[0].map, g.side[0].tma, g.side[0].p, g.side[0].ld, row0, col, rows, cols);
-#pragma unroll
-            for (int k = 0; k < 16; ++k)
-                w[k] = pack2<DT>(f(r1[2 * k]), f(r1[2 * k + 1]));
-            o.template put<2>(w, &g.side[1].map, g.side[1].tma, g.side[1].p, g.side[1].ld, row0, col, rows, cols);
-        }
     } else {
-        uint32_t dg[16], du[16];
+        if constexpr (EPI == kGate) {
 #pragma unroll
-        for (int k = 0; k < 16; ++k) {
-            const float2 gg = unpack2<DT>(wg[k]), uu = unpack2<DT>(wu[k]);
-            const float c0 = f(r[2 * k]), c1 = f(r[2 * k + 1]);
-            const Act t0 = activate(g.act, gg.x), t1 = activate(g.act, gg.y);
-            w[k] = pack2<DT>(t0.value * uu.x, t1.value * uu.y);
-            dg[k] = pack2<DT>(c0 * uu.x * t0.slope, c1 * uu.y * t1.slope);
-            du[k] = pack2<DT>(c0 * t0.value, c1 * t1.value);
+            for (int k = 0; k < 16; ++k) {
+                const float g0 = f(r[2 * k]), g1 = f(r[2 * k + 1]), u0 = f(r1[2 * k]), u1 = f(r1[2 * k + 1]);
+                w[k] = pack2<DT>(activate(g.act, g0).value * u0, activate(g.act, g1).value * u1);
+                wg[k] = pack2<DT>(g0, g1);
+                wu[k] = pack2<DT>(u0, u1);
+            }
+            o.begin();
+        } else {
+#pragma unroll
+            for (int k = 0; k < 16; ++k) {
+                const float2 gg = unpack2<DT>(wg[k]), uu = unpack2<DT>(wu[k]);
+                const float c0 = f(r[2 * k]), c1 = f(r[2 * k + 1]);
+                const Act t0 = activate(g.act, gg.x), t1 = activate(g.act, gg.y);
+                w[k] = pack2<DT>(t0.value * uu.x, t1.value * uu.y);
+                wg[k] = pack2<DT>(c0 * uu.x * t0.slope, c1 * uu.y * t1.slope);
+                wu[k] = pack2<DT>(c0 * t0.value, c1 * t1.value);
+            }
+            ready();
         }
-        o.template put<2>(w, &p.c, p.c_tma, p.out, p.out_ld, row0, col, rows, cols);
-        o.template put<2>(dg, &g.side[0].map, g.side[0].tma, g.side[0].p, g.side[0].ld, row0, col, rows, cols);
-        o.template put<2>(du, &g.side[1].map, g.side[1].tma, g.side[1].p, g.side[1].ld, row0, col, rows, cols);
+        const bool sides = EPI == kGateBwd || g.side[0].p;
+        o.put(2, w);
+        if (sides) {
+            o.put(0, wg);
+            o.put(1, wu);
+        }
+        o.filled();
+        o.template store<2>(2, &p.c, p.c_tma, p.out, p.out_ld, row0, col, rows, cols);
+        if (sides) {
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+                o.template store<2>(k, &g.side[EPI == kStore ? 0 : k].map, g.side[EPI == kStore ? 0 : k].tma,
+                                    g.side[EPI == kStore ? 0 : k].p, g.side[EPI == kStore ? 0 : k].ld, row0, col, rows,
+                                    cols);
+        }
+        o.end();
     }
+}
+
+// gate's and up's boxes of 32 columns without TMA: into the set and to the
+// row of each lane.
+template <class S, int NP>
+__device__ __forceinline__ void fetch_sides(const ProductArgs<NP, kGateBwd> &g, const Product &p, const Outlet<S> &o,
+                                            int64_t row0, int64_t col, uint32_t (&wg)[16], uint32_t (&wu)[16])
+{
+    const int64_t rows = p.m - row0, cols = p.n - col;
+    o.begin();
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        const Side &sd = g.side[2 + k];
+        stage_fetch(o.box(k), o.lane, static_cast<const char *>(sd.p) + (row0 * sd.ld + col) * 2, sd.ld * 2,
+                    rows > 32 ? 32 : (int)rows, cols * 2, sd.vec);
+    }
+    __syncwarp();
+    stage_get_row(o.box(0), o.lane, wg);
+    stage_get_row(o.box(1), o.lane, wu);
+    __syncwarp();
 }
 
 // Where a tile lies.
@@ -292,15 +346,22 @@ struct Tile {
 // within a group, so that the tiles in flight share operands in L2.
 constexpr int kRaster = 8;
 
+template <int NP, int EPI>
+__device__ __forceinline__ int32_t product_at(const ProductArgs<NP, EPI> &g, int32_t index)
+{
+    int32_t product = 0;
+#pragma unroll
+    for (int q = 1; q < NP; ++q)
+        if (q < g.products && index >= g.p[q].first)
+            product = q;
+    return product;
+}
+
 template <class S, int NP, int EPI>
 __device__ __forceinline__ Tile tile_at(const ProductArgs<NP, EPI> &g, int32_t index)
 {
     Tile it;
-    it.product = 0;
-#pragma unroll
-    for (int q = 1; q < NP; ++q)
-        if (q < g.products && index >= g.p[q].first)
-            it.product = q;
+    it.product = product_at(g, index);
     const Product &p = g.p[it.product];
     const int32_t t = index - p.first, tiles_m = (p.m - 1) / S::BM + 1, per = kRaster * p.tiles_n;
     const int32_t group = t / per, within = t - group * per;
@@ -322,12 +383,11 @@ __global__ void __launch_bounds__(S::THREADS, S::PER_SM) k_ffn_product(const __g
 {
     constexpr int CG = S::CG, BN = S::BN;
     constexpr int kStepN = EPI == kGate ? BN / 2 : BN;  // output columns per tile
-    constexpr int kIn = EPI == kGateBwd ? S::IN : 0;
     constexpr bool a_mn = MAJ == kMnMn, b_mn = MAJ != kKK;
     extern __shared__ unsigned char smem_raw[];
     __shared__ ProductShared sh;
     unsigned char *smem = smem_raw + ((1024 - (smem_addr(smem_raw) & 1023u)) & 1023u);
-    unsigned char *out_area = smem + S::STAGES * S::STAGE, *in_area = out_area + S::EPI_WARPS * S::WARP_OUT;
+    unsigned char *out_area = smem + S::STAGES * S::STAGE;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const bool split = CG == 1 && g.splits > 1;
     const uint32_t rank = CG == 2 || split ? cluster_rank() : 0;
@@ -350,7 +410,7 @@ __global__ void __launch_bounds__(S::THREADS, S::PER_SM) k_ffn_product(const __g
             mbar_init_count(&sh.tfull[s], 1);
             mbar_init_count(&sh.tempty[s], CG * S::EPI_WARPS);
         }
-        for (int s = 0; s < kIn * S::EPI_WARPS; ++s)
+        for (int s = 0; EPI == kGateBwd && s < S::SETS * S::EPI_WARPS; ++s)
             mbar_init_count(&sh.in[s], 1);
         sh.gave_up = 0;
         mbar_init_done();
@@ -434,8 +494,7 @@ __global__ void __launch_bounds__(S::THREADS, S::PER_SM) k_ffn_product(const __g
             uint32_t s = 0, phase = 0, t = 0;
             bool ok = true;
             for (int32_t i = worker; ok && i < g.tiles; i += workers, ++t) {
-                const Tile it = tile_at<S>(g, i);
-                const Product &p = g.p[it.product];
+                const Product &p = g.p[product_at(g, i)];
                 const uint32_t acc = t & 1;
                 if (!mbar_wait_warp(&sh.tempty[acc], ((t >> 1) & 1) ^ 1, g.limit_ns, &sh.gave_up))
                     break;
@@ -467,21 +526,23 @@ __global__ void __launch_bounds__(S::THREADS, S::PER_SM) k_ffn_product(const __g
     } else {
         const int quarter = warp & 3, part = warp >> 2;  // lanes 32 * quarter on; this warp's share of the columns
         constexpr int kParts = S::EPI_WARPS / 4, kCols = kStepN / kParts;  // output columns per warp
-        Outlet o{reinterpret_cast<uint4 *>(out_area + warp * S::WARP_OUT), lane, 0};
-        const bool in_tma = kIn > 0 && !split && g.side[EPI == kGateBwd ? 2 : 0].tma;
-        // kGateBwd: gate's and up's boxes arrive by TMA, kIn chunks ahead
-        uint32_t asked = 0, taken = 0;
+        Outlet<S> o{reinterpret_cast<uint4 *>(out_area + warp * S::WARP_OUT), lane, 0};
+        // kGateBwd: gate's and up's boxes arrive by TMA in the set that their
+        // results leave from, asked for one set ahead
+        const bool in_tma = EPI == kGateBwd && !split && g.side[EPI == kGateBwd ? 2 : 0].tma;
         int32_t ask_i = worker, ask_c = 0;
+        uint32_t asked = 0;
         auto ask = [&] {
-            if (kIn == 0 || !in_tma || ask_i >= g.tiles)
+            if (EPI != kGateBwd || !in_tma || ask_i >= g.tiles)
                 return;
             const Tile it = tile_at<S>(g, ask_i);
             if (lane == 0) {
-                const uint32_t b = asked % (kIn ? kIn : 1);
-                uint64_t *bar = &sh.in[warp * (kIn ? kIn : 1) + b];
-                const uint32_t dst = smem_addr(in_area + warp * S::WARP_IN + b * 4096);
+                const uint32_t b = asked % S::SETS;
+                uint64_t *bar = &sh.in[warp * S::SETS + b];
+                const uint32_t dst = smem_addr(o.stage + b * S::BOXES * 128);
                 const int32_t row = it.m * S::BM + (int32_t)half * 128 + quarter * 32;
                 const int32_t col = it.n * kStepN + part * kCols + ask_c;
+                bulk_wait_read<0>();  // the set's last stores have read it
                 mbar_expect(bar, 4096);
                 tma_load<1>(dst, &g.side[EPI == kGateBwd ? 2 : 0].map, col, row, smem_addr(bar));
                 tma_load<1>(dst + 2048, &g.side[EPI == kGateBwd ? 3 : 0].map, col, row, smem_addr(bar));
@@ -493,9 +554,7 @@ __global__ void __launch_bounds__(S::THREADS, S::PER_SM) k_ffn_product(const __g
                 ask_i += workers;
             }
         };
-#pragma unroll
-        for (int k = 0; k < kIn; ++k)
-            ask();
+        ask();
         uint32_t t = 0;
         bool ok = true;
         for (int32_t i = worker; i < g.tiles; i += workers, ++t) {
@@ -512,33 +571,17 @@ __global__ void __launch_bounds__(S::THREADS, S::PER_SM) k_ffn_product(const __g
             uint32_t r[32], r1[32], wg[16], wu[16];
 #pragma unroll 1
             for (int c = 0; c < kCols; c += 32) {
-                if (EPI == kGateBwd && !split) {
+                if constexpr (EPI == kGateBwd) {
                     if (in_tma) {
-                        const uint32_t b = taken % (kIn ? kIn : 1);
-                        ok = ok && mbar_wait_bounded(&sh.in[warp * (kIn ? kIn : 1) + b], (taken / (kIn ? kIn : 1)) & 1,
+                        ok = ok && mbar_wait_bounded(&sh.in[warp * S::SETS + o.n % S::SETS], (o.n / S::SETS) & 1,
                                                      g.limit_ns, &sh.gave_up);
                         ok = __all_sync(0xffffffffu, ok);
-                        uint4 *in = reinterpret_cast<uint4 *>(in_area + warp * S::WARP_IN + b * 4096);
-                        stage_get_row(in, lane, wg);
-                        stage_get_row(in + 128, lane, wu);
-                        ++taken;
-                        fence_proxy_async();
-                        __syncwarp();
-                        if (ok)
-                            ask();
-                    } else {
-                        uint4 *in = reinterpret_cast<uint4 *>(in_area + warp * S::WARP_IN);
-                        const int64_t rows = p.m - row0, cols = p.n - col0 - c;
-#pragma unroll
-                        for (int k = 0; k < 2; ++k) {
-                            const Side &sd = g.side[EPI == kGateBwd ? 2 + k : 0];
-                            stage_fetch(in + 128 * k, lane, static_cast<const char *>(sd.p) + (row0 * sd.ld + col0 + c) * 2,
-                                        sd.ld * 2, rows > 32 ? 32 : (int)rows, cols * 2, sd.vec);
-                        }
-                        __syncwarp();
-                        stage_get_row(in, lane, wg);
-                        stage_get_row(in + 128, lane, wu);
-                        __syncwarp();
+                        stage_get_row(o.box(0), lane, wg);
+                        stage_get_row(o.box(1), lane, wu);
+                        if (S::SETS == 1)
+                            __syncwarp();
+                    } else if (!split) {
+                        fetch_sides<S, NP>(g, p, o, row0, col0 + c, wg, wu);
                     }
                 }
                 if (ok) {
@@ -570,12 +613,18 @@ __global__ void __launch_bounds__(S::THREADS, S::PER_SM) k_ffn_product(const __g
                             sums[(BN / 2 + k) * 128] = __uint_as_float(r1[k]);
                     }
                 } else {
-                    finish32<DT, EPI, NP>(g, p, o, row0, col0 + c, r, r1, wg, wu);
+                    // (with one set the next is asked for when this one has left it)
+                    finish32<S, DT, EPI, NP>(g, p, o, row0, col0 + c, r, r1, wg, wu, [&] {
+                        if (ok && S::SETS > 1)
+                            ask();
+                    });
+                    if (ok && S::SETS == 1)
+                        ask();
                 }
             }
         }
         if (lane == 0)
-            bulk_wait_all();
+            bulk_wait_read<0>();
     }
 
     __syncwarp();
@@ -584,7 +633,7 @@ __global__ void __launch_bounds__(S::THREADS, S::PER_SM) k_ffn_product(const __g
         if (warp < S::EPI_WARPS) {
             const Tile it = tile_at<S>(g, worker);
             const Product &p = g.p[it.product];
-            Outlet o{reinterpret_cast<uint4 *>(out_area + warp * S::WARP_OUT), lane, 0};
+            Outlet<S> o{reinterpret_cast<uint4 *>(out_area + warp * S::WARP_OUT), lane, 0};
             const int64_t m0 = (int64_t)it.m * S::BM, left = p.m - m0;
             const int quarters = left >= 128 ? 4 : (int)((left + 31) / 32);
             // blocks of 32 x 32: quarter q of the rows, 32 columns from c on
@@ -612,24 +661,12 @@ __global__ void __launch_bounds__(S::THREADS, S::PER_SM) k_ffn_product(const __g
                     r[k] = __float_as_uint(s0[k]);
                     r1[k] = __float_as_uint(s1[k]);
                 }
-                if (EPI == kGateBwd) {
-                    uint4 *in = reinterpret_cast<uint4 *>(in_area + warp * S::WARP_IN);
-                    const int64_t rows = p.m - row0, cols = p.n - col;
-#pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                        const Side &sd = g.side[EPI == kGateBwd ? 2 + k : 0];
-                        stage_fetch(in + 128 * k, lane, static_cast<const char *>(sd.p) + (row0 * sd.ld + col) * 2,
-                                    sd.ld * 2, rows > 32 ? 32 : (int)rows, cols * 2, sd.vec);
-                    }
-                    __syncwarp();
-                    stage_get_row(in, lane, wg);
-                    stage_get_row(in + 128, lane, wu);
-                    __syncwarp();
-                }
-                finish32<DT, EPI, NP>(g, p, o, row0, col, r, r1, wg, wu);
+                if constexpr (EPI == kGateBwd)
+                    fetch_sides<S, NP>(g, p, o, row0, col, wg, wu);
+                finish32<S, DT, EPI, NP>(g, p, o, row0, col, r, r1, wg, wu, [] {});
             }
             if (lane == 0)
-                bulk_wait_all();
+                bulk_wait_read<0>();
         }
     }
     __syncwarp();
@@ -659,10 +696,10 @@ __global__ void __launch_bounds__(S::THREADS, S::PER_SM) k_ffn_product(const __g
 // the row with the tokens' pieces (which stay in L1) in binary32; four pieces
 // of each row are in flight per lane.
 struct TokenArgs {
-    const void *x;  // tokens x k, row stride x_ld
+    const void *x;  // tokens x k, row stride x_ld (kPair: of the weights' type; else binary32)
     int64_t x_ld;
     const void *w0, *w1;  // n x k, contiguous
-    void *out;            // kPair: act(C0) * C1; else C0; tokens x n, row stride out_ld
+    void *out;            // kPair: act(C0) * C1 in binary32; else C0; tokens x n, row stride out_ld
     int64_t out_ld;
     void *o0, *o1;        // kPair: C0 and C1, kept (or NULL), contiguous
     int32_t tokens, n, k, parts, act;
@@ -692,7 +729,6 @@ __global__ void __launch_bounds__(kThreads, MT == 1 ? 4 : 3)
     const int per_block = kWarps / a.parts, unit = warp / a.parts, part = warp - unit * a.parts;
     const int32_t pieces = (a.k + 7) >> 3;  // of a row
     const int32_t p0 = (int32_t)((int64_t)pieces * part / a.parts), p1 = (int32_t)((int64_t)pieces * (part + 1) / a.parts);
-    const uint16_t *x = static_cast<const uint16_t *>(a.x);
     bool waited = false;
     pdl_launch_next();
     for (int32_t n0 = blockIdx.x * per_block; n0 < a.n; n0 += gridDim.x * per_block) {
@@ -725,9 +761,21 @@ __global__ void __launch_bounds__(kThreads, MT == 1 ? 4 : 3)
 #pragma unroll
                     for (int m = 0; m < MT; ++m) {
                         const int64_t row = (m < a.tokens ? m : a.tokens - 1) * a.x_ld;
-                        const uint4 xv = load_piece<kW>(x + row, (i + 32 * u) * 8, a.k);
                         float xf[8];
-                        Elem<DT>::to_float(&xv, xf);
+                        if (kPair) {
+                            const uint4 xv = load_piece<kW>(static_cast<const uint16_t *>(a.x) + row, (i + 32 * u) * 8, a.k);
+                            Elem<DT>::to_float(&xv, xf);
+                        } else {  // rows of whole 32 bytes; past k they meet zeros
+                            const float4 *xv = reinterpret_cast<const float4 *>(static_cast<const float *>(a.x) + row) +
+                                               (i + 32 * u) * 2;
+                            const float4 lo = xv[0], hi = xv[1];
+                            xf[0] = lo.x, xf[1] = lo.y, xf[2] = lo.z, xf[3] = lo.w;
+                            xf[4] = hi.x, xf[5] = hi.y, xf[6] = hi.z, xf[7] = hi.w;
+                            if (!kW)
+#pragma unroll
+                                for (int e = 0; e < 8; ++e)
+                                    xf[e] = (i + 32 * u) * 8 + e < a.k ? xf[e] : 0.0f;
+                        }
 #pragma unroll
                         for (int q = 0; q < R; ++q)
 #pragma unroll
@@ -766,7 +814,7 @@ __global__ void __launch_bounds__(kThreads, MT == 1 ? 4 : 3)
             for (int m = 0; m < MT; ++m)
                 if (m < a.tokens) {
                     if (kPair) {
-                        store1<DT>(a.out, m * a.out_ld + n, activate(a.act, acc[0][m]).value * acc[R - 1][m]);
+                        static_cast<float *>(a.out)[m * a.out_ld + n] = activate(a.act, acc[0][m]).value * acc[R - 1][m];
                         if (a.o0) {
                             store1<DT>(a.o0, (int64_t)m * a.n + n, acc[0][m]);
                             store1<DT>(a.o1, (int64_t)m * a.n + n, acc[R - 1][m]);
@@ -840,15 +888,19 @@ constexpr int64_t kMostSize = ((int64_t)1 << 31) - 512;
 constexpr int kSms = 152;
 
 // Pairs of CTAs with 256 x 256 tiles for large products; one-CTA tiles of
-// 128 x 128, and of 128 x 64 with two CTAs per SM, for small ones.  The
-// backward gate's epilogue reads two matrices and writes three, and gives two
-// stages for their buffers.
+// 128 x 128, and of 128 x 64 with two CTAs per SM, for small ones.  The gate's
+// epilogues fill three boxes per set, at the cost of stages.
 template <int EPI>
-using Pair256 = Shape<2, 256, EPI == kGateBwd ? 4 : 6, 8, EPI == kGateBwd ? 2 : 0>;
+using Pair256 = Shape<2, 256, EPI == kStore ? 6 : 4, 8, EPI == kStore ? 1 : 3, 2>;
 template <int EPI>
-using One128 = Shape<1, 128, 4, 8, EPI == kGateBwd ? 1 : 0>;
+using One128 = Shape<1, 128, 4, 8, EPI == kStore ? 1 : 3, 2>;
 template <int EPI>
-using One64 = Shape<1, 64, 3, 4, EPI == kGateBwd ? 1 : 0>;
+using One64 = Shape<1, 64, 3, 4, EPI == kStore ? 1 : 3, EPI == kStore ? 2 : 1>;
+
+// Up to here a warp per weight row is faster than tensor-core tiles, which
+// hold 128 tokens or a fraction (1600 x 6400, one, two and four tokens: 18, 21
+// and 31 us here, 27 us in tiles).
+constexpr int kFewTokens = 2;
 
 int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 int64_t up8(int64_t a) { return (a + 7) & ~(int64_t)7; }
@@ -929,7 +981,8 @@ FfnSpace ffn_space(int64_t m, int64_t d, int64_t f, bool backward)
 {
     FfnSpace s{};
     s.mats = 256;
-    s.mat_bytes = align256((size_t)m * (size_t)up8(f) * 2);
+    // (a few tokens' act(gate) * up stays in binary32)
+    s.mat_bytes = align256((size_t)m * (size_t)up8(f) * (!backward && m <= kFewTokens ? 4 : 2));
     s.copies = s.mats + (backward ? 3 : 1) * s.mat_bytes;
     s.total = s.copies;
     if (((d | f) & 7) != 0)
@@ -1104,11 +1157,6 @@ int zero_matrix(void *p, int64_t ld, int64_t rows, int64_t cols, int es, cudaStr
 }
 
 // ------------------------------------------------------------- a few tokens
-
-// Up to here a warp per weight row is faster than tensor-core tiles, which
-// hold 128 tokens or a fraction (1600 x 6400, one, two and four tokens: 18, 21
-// and 31 us here, 27 us in tiles).
-constexpr int kFewTokens = 2;
 
 // Warps per weight row: one per 2048 of k (8192 x 32768, one token: 240 us; a
 // warp for whole rows 293), and more, down to 512 of k each, while there are

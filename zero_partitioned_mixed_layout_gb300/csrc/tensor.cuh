@@ -136,9 +136,9 @@ __device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap *map, i
 
 // A box from shared memory to `map` at (x, y); what lies outside the matrix
 // is not written.  The issuing thread groups its stores (bulk_commit) and
-// waits until at most N groups still read their shared memory, or, at the
-// end, until all are done.  The boxes' writers fence (fence_proxy_async)
-// before the store.
+// waits until at most N groups still read their shared memory (the writes
+// themselves are complete when the grid is).  The boxes' writers fence
+// (fence_proxy_async) before the store.
 __device__ __forceinline__ void tma_store(const CUtensorMap *map, uint32_t src, int32_t x, int32_t y)
 {
     asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];" ::"l"(
@@ -154,8 +154,6 @@ __device__ __forceinline__ void bulk_wait_read()
 {
     asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
 }
-
-__device__ __forceinline__ void bulk_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 
 // A binary32 of another CTA's shared memory (peer_addr).
 __device__ __forceinline__ float load_peer(uint32_t addr)
