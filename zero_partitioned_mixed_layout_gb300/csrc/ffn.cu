@@ -97,6 +97,7 @@ struct Shape {
 };
 
 constexpr int kMaxStages = 12;
+constexpr int kMostParts = 8;  // of k: CTAs of a portable cluster
 
 struct ProductShared {
     uint64_t full[kMaxStages], empty[kMaxStages], tfull[2], tempty[2], in[16];
@@ -377,7 +378,9 @@ __device__ __forceinline__ Tile tile_at(const ProductArgs<NP, EPI> &g, int32_t i
 // persistent and strides over the tiles.  With splits > 1 (one-CTA shapes, a
 // grid of tiles * splits) the CTAs of a cluster share a tile's k: each leaves
 // its sums in its shared memory, and each then adds up some 32 x 32 blocks
-// of the tile over all of them, in order, and finishes them.
+// of the tile over all of them, in order, and finishes them (all threads add,
+// 16 bytes at a time, and then a warp finishes a block; a warp that also added
+// up its block took 1 us longer).
 template <class S, int DT, int EPI, int MAJ, int NP>
 __global__ void __launch_bounds__(S::THREADS, S::PER_SM) k_ffn_product(const __grid_constant__ ProductArgs<NP, EPI> g)
 {
@@ -630,36 +633,43 @@ __global__ void __launch_bounds__(S::THREADS, S::PER_SM) k_ffn_product(const __g
     __syncwarp();
     if (split) {
         cluster_sync();
+        const Tile it = tile_at<S>(g, worker);
+        const Product &p = g.p[it.product];
+        const int64_t m0 = (int64_t)it.m * S::BM, left = p.m - m0;
+        // blocks of 32 x 32: quarter q of the rows, 32 columns from c on; every
+        // splits-th of them is this CTA's, and all of its threads add it up
+        // over the cluster, four rows at a time, in order, in its own memory
+        const int quarters = left >= 128 ? 4 : (int)((left + 31) / 32), blocks = quarters * (kStepN / 32);
+        constexpr int kPieces = EPI == kGate ? 512 : 256;
+        const int pieces = (blocks - (int)rank + g.splits - 1) / g.splits * kPieces;
+#pragma unroll 2
+        for (int v = threadIdx.x; v < pieces; v += S::THREADS) {
+            const int u = (int)rank + v / kPieces * g.splits, e = v % kPieces;
+            const int column = u / quarters * 32 + (e >> 3 & 31) + (e >> 8) * (BN / 2);
+            float4 *sums = reinterpret_cast<float4 *>(smem) + column * 32 + u % quarters * 8 + (e & 7);
+            const uint32_t at = smem_addr(sums);
+            float4 sum = load_peer4(peer_addr(at, 0));
+#pragma unroll
+            for (int j = 1; j < kMostParts; ++j)
+                if (j < g.splits) {
+                    const float4 x = load_peer4(peer_addr(at, j));
+                    sum.x += x.x, sum.y += x.y, sum.z += x.z, sum.w += x.w;
+                }
+            *sums = sum;
+        }
+        __syncthreads();
         if (warp < S::EPI_WARPS) {
-            const Tile it = tile_at<S>(g, worker);
-            const Product &p = g.p[it.product];
             Outlet<S> o{reinterpret_cast<uint4 *>(out_area + warp * S::WARP_OUT), lane, 0};
-            const int64_t m0 = (int64_t)it.m * S::BM, left = p.m - m0;
-            const int quarters = left >= 128 ? 4 : (int)((left + 31) / 32);
-            // blocks of 32 x 32: quarter q of the rows, 32 columns from c on
-            for (int u = (int)rank + warp * g.splits; u < quarters * (kStepN / 32); u += S::EPI_WARPS * g.splits) {
+            for (int u = (int)rank + warp * g.splits; u < blocks; u += S::EPI_WARPS * g.splits) {
                 const int q = u % quarters, c = u / quarters * 32;
                 const int64_t row0 = m0 + q * 32, col = (int64_t)it.n * kStepN + c;
-                float s0[32], s1[32];
-#pragma unroll
-                for (int k = 0; k < 32; ++k)
-                    s0[k] = s1[k] = 0.0f;
-                const uint32_t at = smem_addr(smem) + (c * 128 + q * 32 + lane) * 4;
-#pragma unroll 1
-                for (int j = 0; j < g.splits; ++j) {
-                    const uint32_t from = peer_addr(at, j);
-#pragma unroll
-                    for (int k = 0; k < 32; ++k) {
-                        s0[k] += load_peer(from + k * 512);
-                        if (EPI == kGate)
-                            s1[k] += load_peer(from + (BN / 2 + k) * 512);
-                    }
-                }
+                const uint32_t *sums = reinterpret_cast<const uint32_t *>(smem) + c * 128 + q * 32 + lane;
                 uint32_t r[32], r1[32], wg[16], wu[16];
 #pragma unroll
                 for (int k = 0; k < 32; ++k) {
-                    r[k] = __float_as_uint(s0[k]);
-                    r1[k] = __float_as_uint(s1[k]);
+                    r[k] = sums[k * 128];
+                    if (EPI == kGate)
+                        r1[k] = sums[(BN / 2 + k) * 128];
                 }
                 if constexpr (EPI == kGateBwd)
                     fetch_sides<S, NP>(g, p, o, row0, col, wg, wu);
@@ -939,10 +949,10 @@ struct Plan {
 // epilogue of the last tile), and per wave of tiles and block of k the larger
 // of the issue's time and the tile bytes' through L2.  Its constants were
 // fitted to 1250 launches (tokens 5 to 1000, widths 256 to 8192, all cuts);
-// the cut it takes is on average 1.3 % slower than the best, at worst 22 %.
+// the cut it takes is on average 1.9 % slower than the best, at worst 23 %.
 // One launch each, measured: 1000 tokens, 4096 x 4096: pairs 26 us, 128 x 128
-// tiles 44, 128 x 64 88; 64 tokens, 6400 to 1600: 33, 28 and 26 us whole, 14,
-// 13.6 and 12.7 us with k in four parts.
+// tiles 44, 128 x 64 88; 64 tokens, 6400 to 1600: 33, 28 and 26 us whole, 13.0
+// and 12.3 us with k in four parts, 10.8 us for 128 x 128 tiles in eight.
 Plan plan_product(int64_t m, int64_t n, int64_t k, bool gate, int most_parts)
 {
     const int64_t cols = n * (gate ? 2 : 1), kb = cdiv(k, 64);
@@ -958,18 +968,16 @@ Plan plan_product(int64_t m, int64_t n, int64_t k, bool gate, int most_parts)
         for (int parts = 1; parts <= most_parts && parts <= kb; ++parts) {
             const int64_t ctas = tiles * parts, waves = cdiv(ctas, slots);
             const double bytes = (double)(ctas < slots ? ctas : slots) * (a_bytes + bn * 128);
-            const double block = c == 0 ? larger(206, bytes / 13000) : larger(120, bytes / 8400);
+            const double block = c == 0 ? larger(206, bytes / 13000) : larger(133, bytes / 8400);
             double t = 6000 + (double)waves * cdiv(kb, parts) * block;
             if (parts > 1)  // joining the parts; and each wave is a new set of CTAs
-                t += 670 + 210 * parts + 8000.0 * (waves - 1);
+                t += 900 + 130 * parts + 8000.0 * (waves - 1);
             if (t < least)
                 least = t, best = {c == 0 ? kOne128 : kOne64, parts};
         }
     }
     return best;
 }
-
-constexpr int kMostParts = 8;  // CTAs of a portable cluster
 
 struct FfnSpace {
     size_t mats, mat_bytes, copies, total;
