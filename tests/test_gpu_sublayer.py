@@ -235,6 +235,46 @@ def test_layer_norm_backward(zp, shape, dtype):
         assert torch.equal(dx, dx2), "the same dx whether or not the weight's gradient is taken"
 
 
+# rows, cols where a block stages its rows: every number of column groups per
+# lane, one to sixteen warps per row, last groups that are partly and wholly
+# outside the row, rows that do not divide among the blocks
+MANY = [(1216, 520), (1300, 1000), (1217, 1280), (1700, 1288), (2501, 1600), (1219, 2048), (1300, 2056), (2433, 2568),
+        (2433, 4096), (2440, 4104), (2440, 6400), (2450, 8192), (310, 8200), (400, 16384)]
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("shape", MANY, ids=str)
+def test_layer_norm_of_many_rows(zp, shape, dtype):
+    test_layer_norm(zp, shape, dtype)
+    test_layer_norm_backward(zp, shape, dtype)
+
+
+@pytest.mark.parametrize("cols", [1600, 4096])
+def test_layer_norm_of_many_rows_keeps_rows_apart(zp, cols):
+    """A row that is not finite changes no other row; a rate of one drops everything."""
+    rows, dt = 2600, torch.float16
+    x, res, w, b = randn((rows, cols), dt, 45), randn((rows, cols), dt, 46), randn((cols,), dt, 47), randn((cols,), dt, 48)
+    mean, rstd = (torch.empty(rows, device="cuda") for _ in range(2))
+    bad = x.clone()
+    bad[7, 3], bad[1999, cols - 1] = float("nan"), float("inf")
+    others = torch.ones(rows, dtype=torch.bool, device="cuda")
+    others[[7, 1999]] = False
+    out = []
+    for t in (x, bad):
+        y, s, dx, dd = (torch.empty_like(x) for _ in range(4))
+        zp.zero_layer_norm(t, w, b, y, mean, rstd, residual=res, sum_out=s, drop=zp.Dropout(2.0 ** -40, 1))
+        dw, ws = torch.empty_like(w), zp.new_layer_norm_workspace(rows, cols)
+        zp.zero_layer_norm_backward(res, s, w, mean, rstd, dx, dw, None, ws, dresidual=res, dx_dropped=dd,
+                                    drop=zp.Dropout(0.3, 2))
+        out.append((y[others], s[others], dx[others], dd[others]))
+        assert torch.isfinite(y).all(1).eq(others if t is bad else torch.ones_like(others)).all()
+    assert all(torch.equal(p, q) for p, q in zip(*out))
+    zp.zero_layer_norm(bad, w, b, y, mean, rstd, residual=res, sum_out=s, drop=zp.Dropout(1.0, 1))
+    assert torch.equal(s, res)
+    zp.zero_layer_norm_backward(bad, s, w, mean, rstd, dx, dw, None, ws, dx_dropped=dd, drop=zp.Dropout(1.0, 1))
+    assert torch.equal(dd[others], torch.zeros_like(dd[others]))
+
+
 def test_layer_norm_gradient_against_differences(zp):
     """Central differences of the binary32 kernel itself.  Step 2^-6 in a unit
     direction of 40 x 96 elements: truncation below step^2 times third

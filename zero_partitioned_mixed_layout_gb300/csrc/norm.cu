@@ -2,6 +2,7 @@
 // front of it), forward and backward.
 #include <cmath>
 #include <initializer_list>
+#include <type_traits>
 
 #include "sublayer.cuh"
 
@@ -183,13 +184,28 @@ __device__ __forceinline__ void store_group(char *row, I c0, I cols, bool vec, c
             store1<DT>(q, e, f[e]);
 }
 
+// Zeros what the words drop (kAll: everything may be).
+template <bool kAll>
+__device__ __forceinline__ void drop_words(const Drop &d, const uint32_t (&w)[8], float (&f)[8])
+{
+    if (kAll && d.all) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            f[e] = 0.0f;
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            f[e] = w[e] >= d.threshold ? f[e] : 0.0f;
+    }
+}
+
 // Zeros the dropped ones of the eight columns from c0 on (the scale is left to
 // the caller).  c0 is 0 mod 4 unless the rows are shifted: then a group spans
 // three counters, and the third is the first of the next lane's group.  So
 // the kernels give a warp 31 groups of a row that is not whole (lane_group),
 // its last lane works out masks for its neighbour alone, and all lanes of a
 // warp come here together.
-template <bool kW>
+template <bool kW, bool kAll = true>
 __device__ __forceinline__ void keep_group(const Drop &d, const RowMask &m, int64_t c0, float (&f)[8])
 {
     uint32_t w[8];
@@ -215,15 +231,7 @@ __device__ __forceinline__ void keep_group(const Drop &d, const RowMask &m, int6
             w[7] = o & 1 ? n2 : n1;
         }
     }
-    if (d.all) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-            f[e] = 0.0f;
-    } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-            f[e] = w[e] >= d.threshold ? f[e] : 0.0f;
-    }
+    drop_words<kAll>(d, w, f);
 }
 
 // The group of thread t of a row's threads, and whether it is the thread's
@@ -240,14 +248,14 @@ __device__ __forceinline__ bool owns_group()
     return kW || (threadIdx.x & 31) != 31;
 }
 
-template <bool kW>
+template <bool kW, bool kAll = true>
 __device__ __forceinline__ void keep_pairs(const Drop &d, const RowMask &m, int64_t c0, float2 (&f)[4])
 {
     float t[8];
 #pragma unroll
     for (int k = 0; k < 4; ++k)
         t[2 * k] = f[k].x, t[2 * k + 1] = f[k].y;
-    keep_group<kW>(d, m, c0, t);
+    keep_group<kW, kAll>(d, m, c0, t);
 #pragma unroll
     for (int k = 0; k < 4; ++k)
         f[k] = make_float2(t[2 * k], t[2 * k + 1]);
@@ -394,11 +402,14 @@ struct NormArgs {
 // the output.  A thread keeps its columns (the rows of a team are a multiple
 // of 8 apart, so their shift is the same), and with up to two groups also
 // their weight and bias, and has the next row on its way while it works on
-// this one.
+// this one (four groups of binary32 leave no registers for that; of 16 bits,
+// 4096 x 16384: 73 us with it, 98 without).  One row of 1600 takes 2.3 us,
+// which is a launch and two trips to memory; 8192 x 1600 binary32 21.6
+// (4.9 TB/s), bounded by the instructions of a row's two sums and its ends.
 template <int DT, int NV, bool kFused, bool kW>
 __global__ void __launch_bounds__(NV == 1 ? 768 : NV == 2 ? 640 : 512) k_norm_fwd(const __grid_constant__ NormArgs a)
 {
-    constexpr bool kAhead = NV <= 2;
+    constexpr bool kKeep = NV <= 2, kAhead = NV <= 2 || DT != ZERO_F32;
     __shared__ float s_red[2][32];
     const int tpr = a.tpr, team = threadIdx.x / tpr, t0 = threadIdx.x - team * tpr, teams = blockDim.x / tpr;
     float *const red0 = s_red[0] + team * (tpr >> 5), *const red1 = s_red[1] + team * (tpr >> 5);
@@ -410,18 +421,18 @@ __global__ void __launch_bounds__(NV == 1 ? 768 : NV == 2 ? 640 : 512) k_norm_fw
     const int at = lane_group<kW>(t0) * 8 - row_shift<kW>(a.rows, r);
     const int wide = kW ? tpr * 8 : (tpr >> 5) * 31 * 8;  // columns from one of a thread's groups to the next
     const bool mine = owns_group<kW>();
-    float2 w[kAhead ? NV : 1][4], b[kAhead ? NV : 1][4];
+    float2 w[kKeep ? NV : 1][4], b[kKeep ? NV : 1][4];
     const float2 scale = both(kFused && a.dropping ? a.d.scale : 1.0f);
-    if (kAhead) {
+    if (kKeep) {
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
             const int c0 = at + v * wide;
 #pragma unroll
             for (int k = 0; k < 4; ++k)
-                w[kAhead ? v : 0][k] = b[kAhead ? v : 0][k] = both(0.0f);
+                w[kKeep ? v : 0][k] = b[kKeep ? v : 0][k] = both(0.0f);
             if (mine && c0 < cols) {
-                load_vector<DT, kW>(a.weight, a.w_f32, c0, cols, a.w_vec, 1.0f, w[kAhead ? v : 0]);
-                load_vector<DT, kW>(a.bias, a.w_f32, c0, cols, a.w_vec, 0.0f, b[kAhead ? v : 0]);
+                load_vector<DT, kW>(a.weight, a.w_f32, c0, cols, a.w_vec, 1.0f, w[kKeep ? v : 0]);
+                load_vector<DT, kW>(a.bias, a.w_f32, c0, cols, a.w_vec, 0.0f, b[kKeep ? v : 0]);
             }
         }
     }
@@ -498,13 +509,13 @@ __global__ void __launch_bounds__(NV == 1 ? 768 : NV == 2 ? 640 : 512) k_norm_fw
         for (int v = 0; v < NV; ++v) {
             const int c0 = at + v * wide;
             if (mine && c0 < cols) {
-                if (!kAhead) {
+                if (!kKeep) {
                     load_vector<DT, kW>(a.weight, a.w_f32, c0, cols, a.w_vec, 1.0f, w[0]);
                     load_vector<DT, kW>(a.bias, a.w_f32, c0, cols, a.w_vec, 0.0f, b[0]);
                 }
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
-                    t[v][k] = __ffma2_rn(__fmul2_rn(t[v][k], both(rstd)), w[kAhead ? v : 0][k], b[kAhead ? v : 0][k]);
+                    t[v][k] = __ffma2_rn(__fmul2_rn(t[v][k], both(rstd)), w[kKeep ? v : 0][k], b[kKeep ? v : 0][k]);
                 store_pairs<DT, kW>(py, c0, cols, vec, t[v]);
             }
         }
@@ -517,8 +528,158 @@ __global__ void __launch_bounds__(NV == 1 ? 768 : NV == 2 ? 640 : 512) k_norm_fw
     }
 }
 
+// Sixteen bytes of memory to shared memory without registers between, or as
+// many zeros if not `there` (memory is then not read); each thread waits for
+// its own copies alone and reads them alone.
+__device__ __forceinline__ void copy16(void *to, const void *from, bool there)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"((uint32_t)__cvta_generic_to_shared(to)), "l"(from),
+                 "r"(there ? 16 : 0)
+                 : "memory");
+}
+
+__device__ __forceinline__ void copies_done() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
+// Threads of a block of the kernel below: the registers of NV groups decide.
+constexpr int norm_rows_threads(int nv) { return nv <= 3 ? 1024 : nv <= 4 ? 896 : nv <= 6 ? 768 : nv == 7 ? 640 : 512; }
+
+// Forward of whole rows of 16-bit elements, for many rows: teams of T warps
+// that take a row each, one warp where the row fits its registers (no barrier
+// then, and no idle lanes but in the last group).  A lane keeps its NV groups
+// in binary32, weight and bias lie in shared memory in binary32, and a group's
+// copy of the next row is under way as soon as this row's has been read, so
+// registers hold no row ahead and an SM more rows at once.  Straight-line code
+// over the groups: 208 instructions per group with sum and mask, where
+// k_norm_fwd takes 290 and a barrier.  8192 x 1600 float16: 11.8 us (4.4 TB/s)
+// where k_norm_fwd takes 15.5; with sum and mask 23.1 (4.5 TB/s) and 31.9;
+// 16384 x 8192: 100 (5.4 TB/s) and 122.  The issue of the mask's multiplications
+// and the start and end of the launch are what is left over the copy's time.
+// Rows of binary32 stay with k_norm_fwd: staged they are twice as long, so half
+// the warps fit (8192 x 1600: 28.7 us staged, 21.6 there).
+template <int DT, int NV, int T, bool kFused>
+__global__ void __launch_bounds__(norm_rows_threads(NV)) k_norm_fwd_rows(const __grid_constant__ NormArgs a)
+{
+    constexpr int kNext = T * 32;  // groups from one of a lane's to the next
+    extern __shared__ float4 s_rows[];
+    __shared__ float s_red[2][32];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, team = warp / T, teams = blockDim.x / kNext;
+    const int cols = (int)a.rows.cols, groups = cols >> 3, g0 = warp % T * 32 + lane;
+    // weight, then bias: the first and the last four columns of each group apart
+    float4 *const vec = s_rows;
+    uint4 *const in = reinterpret_cast<uint4 *>(s_rows + 4 * groups) + warp * (kFused ? 2 : 1) * NV * 32 + lane;
+    const int64_t step = (int64_t)gridDim.x * teams;
+    int64_t r = (int64_t)blockIdx.x * teams + team;
+    // (T = 1: only the last group may be outside the row; else the last two)
+    auto has = [&](int v) { return v < NV - (T == 1 ? 1 : 2) || g0 + v * kNext < groups; };
+    auto fetch = [&](int64_t row, int v) {
+        const bool there = row < a.rows.rows;
+        copy16(in + v * 32, row_ptr<DT>(a.x, row) + (g0 + v * kNext) * 16, there);
+        if (kFused)
+            copy16(in + (NV + v) * 32, row_ptr<DT>(a.res, row) + (g0 + v * kNext) * 16, there && a.res.p);
+    };
+    auto sum_of = [&](float2 s, int which) {
+        const float v = warp_sum_f(s.x + s.y);
+        if (T == 1)
+            return v;
+        float *const red = s_red[which] + team * T;
+        if (lane == 0)
+            red[warp % T] = v;
+        asm volatile("bar.sync %0, %1;" ::"r"(team + 1), "n"(kNext) : "memory");
+        float sum = red[0];
+#pragma unroll
+        for (int q = 1; q < T; ++q)
+            sum += red[q];
+        return sum;
+    };
+#pragma unroll
+    for (int v = 0; v < NV; ++v)
+        if (has(v))
+            fetch(r, v);
+    for (int i = threadIdx.x; i < cols; i += blockDim.x) {
+        float *const to = reinterpret_cast<float *>(vec + (i >> 2 & 1) * groups + (i >> 3)) + (i & 3);
+        to[0] = !a.weight ? 1.0f : a.w_f32 ? load1<ZERO_F32>(a.weight, i) : load1<DT>(a.weight, i);
+        to[8 * groups] = !a.bias ? 0.0f : a.w_f32 ? load1<ZERO_F32>(a.bias, i) : load1<DT>(a.bias, i);
+    }
+    __syncthreads();
+    const uint64_t off = kFused && a.dropping ? drop_offset(a.d) : 0;
+    const float2 scale = both(kFused && a.dropping ? a.d.scale : 1.0f);
+    for (; r < a.rows.rows; r += step) {
+        RowMask mask{};
+        if (kFused && a.dropping)
+            mask = row_mask(a.d, off, r);
+        char *const ps = row_ptr<DT>(a.sum, r) + g0 * 16, *const py = row_ptr<DT>(a.y, r) + g0 * 16;
+        float2 t[NV][4], s = both(0.0f);
+        copies_done();
+        auto first = [&](auto dropping) {
+#pragma unroll
+            for (int v = 0; v < NV; ++v) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    t[v][k] = both(0.0f);
+                if (has(v)) {
+                    Group<DT> g;
+                    g.w[0] = in[v * 32];
+                    g.to_pairs(t[v]);
+                    if (kFused) {
+                        if (dropping)
+                            keep_pairs<true, false>(a.d, mask, (g0 + kNext * v) * 8, t[v]);
+                        float2 x[4];
+                        g.w[0] = in[(NV + v) * 32];
+                        g.to_pairs(x);
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            t[v][k] = __ffma2_rn(t[v][k], scale, x[k]);
+                        store_pairs<DT, true>(ps, v * kNext * 8, cols, true, t[v]);
+                    }
+                    fetch(r + step, v);
+                }
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    s = __fadd2_rn(s, t[v][k]);
+            }
+        };
+        if (kFused && a.dropping)
+            first(std::true_type{});
+        else
+            first(std::false_type{});
+        const float mean = sum_of(s, 0) * a.inv_cols;
+        s = both(0.0f);
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+            float2 q = both(0.0f);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                t[v][k] = __fadd2_rn(t[v][k], both(-mean));
+                q = __ffma2_rn(t[v][k], t[v][k], q);
+            }
+            if (has(v))
+                s = __fadd2_rn(s, q);
+        }
+        const float rstd = __frsqrt_rn(sum_of(s, 1) * a.inv_cols + a.eps);
+#pragma unroll
+        for (int v = 0; v < NV; ++v)
+            if (has(v)) {
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const float4 w = vec[h * groups + g0 + kNext * v], b = vec[(2 + h) * groups + g0 + kNext * v];
+                    float2 &t0 = t[v][2 * h], &t1 = t[v][2 * h + 1];
+                    t0 = __ffma2_rn(__fmul2_rn(t0, both(rstd)), make_float2(w.x, w.y), make_float2(b.x, b.y));
+                    t1 = __ffma2_rn(__fmul2_rn(t1, both(rstd)), make_float2(w.z, w.w), make_float2(b.z, b.w));
+                }
+                store_pairs<DT, true>(py, v * kNext * 8, cols, true, t[v]);
+            }
+        if (g0 == 0) {
+            if (a.mean)
+                a.mean[r] = mean;
+            if (a.rstd)
+                a.rstd[r] = rstd;
+        }
+    }
+}
+
 // Forward of rows too wide for the registers of a block: three passes over
-// the row (the later two from L2).
+// the row (the later two from L2), bounded by their latency, one after the
+// other.
 template <int DT>
 __global__ void __launch_bounds__(512) k_norm_fwd_wide(const __grid_constant__ NormArgs a)
 {
@@ -648,7 +809,10 @@ __device__ __forceinline__ float2 group_sum2(float2 v, float2 *s, int tpr, int g
 // block) apart; NG is a multiple of 8 when a group takes more than one row,
 // so that its rows all have the same shift.  The next row is loaded before
 // the sums of this one are exchanged; a row is held as it came (16-bit) and
-// converted again after the exchange.
+// converted again after the exchange.  3001 x 2049 binary32: 27.5 us
+// (2.7 TB/s); 8192 x 1600 binary32 with sum and mask 54 (4.9 TB/s): bounded by
+// instructions (a row's address, ends and two sums are each warp's own) and by
+// the barrier that the sums cross.
 template <int DT, int NV, bool kW>
 __global__ void __launch_bounds__(NV == 1 ? 768 : 512) k_norm_bwd(const __grid_constant__ NormBwdArgs a)
 {
@@ -776,6 +940,178 @@ __global__ void __launch_bounds__(NV == 1 ? 768 : 512) k_norm_bwd(const __grid_c
     }
 }
 
+constexpr int kBwdRowsThreads = 512;
+
+// Backward of whole rows of 16-bit elements, for many rows: teams of T warps
+// that take a row each, NV groups per lane, whose dweight and dbias build up
+// in registers; the row stays in shared memory between the sums over it and
+// dx, and a group's copy of the next row is under way as soon as this row's
+// has been read for dx.  T is the least that leaves four groups to a lane: with
+// one warp for seven groups the sums' registers left 11 warps to an SM (36.4 us
+// for 8192 x 1600 with sum and mask; two warps of four groups 35.4, 3.7 TB/s;
+// k_norm_bwd 39.6).  16384 x 1600: 61 us where k_norm_bwd takes 71; 8192 x 16384
+// 294 (5.4 TB/s) where the two passes take 580.  9 us of each call are its start,
+// its partials and their sum; the rest runs at 5.2 TB/s.
+template <int DT, int NV, int T>
+__global__ void __launch_bounds__(kBwdRowsThreads) k_norm_bwd_rows(const __grid_constant__ NormBwdArgs a)
+{
+    constexpr int kPieces = NV * 32;  // of a warp's part of a row, in shared memory
+    constexpr int kNext = T * 32;  // groups from one of a lane's to the next
+    extern __shared__ float4 s_rows[];
+    __shared__ float2 s_red[2][32];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, teams = blockDim.x / (T * 32), team = warp / T;
+    const int cols = (int)a.rows.cols, groups = cols >> 3, g0 = warp % T * 32 + lane;
+    const int64_t step = (int64_t)gridDim.x * teams;
+    const uint64_t off = a.dropping ? drop_offset(a.d) : 0;
+    float4 *const vec = s_rows;  // weight: the first and the last four columns of each group apart
+    uint4 *const in = reinterpret_cast<uint4 *>(s_rows + 2 * groups) + warp * 3 * kPieces + lane;
+    pdl_launch_next();
+    int64_t r = (int64_t)blockIdx.x * teams + team;
+    // (T = 16: only the last two groups may be outside the row; else the last)
+    auto has = [&](int v) { return v < NV - (T == 16 ? 2 : 1) || g0 + v * kNext < groups; };
+    auto fetch = [&](int64_t row, int v) {
+        const int at = (g0 + v * kNext) * 16;
+        const bool there = row < a.rows.rows;
+        copy16(in + v * 32, row_ptr<DT>(a.dy, row) + at, there);
+        copy16(in + kPieces + v * 32, row_ptr<DT>(a.x, row) + at, there);
+        copy16(in + 2 * kPieces + v * 32, row_ptr<DT>(a.dres, row) + at, there && a.dres.p);
+    };
+    auto take = [&](int which, int v, float2 (&f)[4]) {
+        Group<DT> g;
+        g.w[0] = in[which * kPieces + v * 32];
+        g.to_pairs(f);
+    };
+#pragma unroll
+    for (int v = 0; v < NV; ++v)
+        if (has(v))
+            fetch(r, v);
+    float nmean = 0.0f, nrstd = 0.0f;  // of the next row
+    auto statistics = [&](int64_t row) {
+        if (row < a.rows.rows)
+            nmean = __ldg(a.mean + row), nrstd = __ldg(a.rstd + row);
+    };
+    statistics(r);
+    for (int i = threadIdx.x; i < cols; i += blockDim.x) {
+        float *const to = reinterpret_cast<float *>(vec + (i >> 2 & 1) * groups + (i >> 3)) + (i & 3);
+        *to = !a.weight ? 1.0f : a.w_f32 ? load1<ZERO_F32>(a.weight, i) : load1<DT>(a.weight, i);
+    }
+    float2 dw[NV][4], db[NV][4];
+#pragma unroll
+    for (int v = 0; v < NV; ++v)
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            dw[v][k] = db[v][k] = both(0.0f);
+    __syncthreads();
+    auto weights = [&](int v, float2 (&w)[4]) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const float4 q = vec[h * groups + g0 + kNext * v];
+            w[2 * h] = make_float2(q.x, q.y), w[2 * h + 1] = make_float2(q.z, q.w);
+        }
+    };
+    for (int buf = 0; r < a.rows.rows; r += step, buf ^= 1) {
+        const float mean = nmean, rstd = nrstd;
+        statistics(r + step);
+        float2 sx = both(0.0f), sy = both(0.0f);
+        copies_done();
+#pragma unroll
+        for (int v = 0; v < NV; ++v)
+            if (has(v)) {
+                float2 g[4], xh[4], w[4];
+                take(0, v, g);
+                take(1, v, xh);
+                weights(v, w);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    xh[k] = __fmul2_rn(__fadd2_rn(xh[k], both(-mean)), both(rstd));
+                    dw[v][k] = __ffma2_rn(g[k], xh[k], dw[v][k]);
+                    db[v][k] = __fadd2_rn(db[v][k], g[k]);
+                    g[k] = __fmul2_rn(g[k], w[k]);
+                    sx = __fadd2_rn(sx, g[k]);
+                    sy = __ffma2_rn(g[k], xh[k], sy);
+                }
+            }
+        const float half = half_sums(make_float2(sx.x + sx.y, sy.x + sy.y));
+        float2 s;
+        if (T == 1) {
+            s = both_sums(half);
+        } else {
+            float2 *const red = s_red[buf] + team * T;
+            if ((lane & 15) == 0)
+                (lane ? red[warp % T].y : red[warp % T].x) = half;
+            asm volatile("bar.sync %0, %1;" ::"r"(team + 1), "n"(T * 32) : "memory");
+            s = red[0];
+#pragma unroll
+            for (int q = 1; q < T; ++q)
+                s = __fadd2_rn(s, red[q]);
+        }
+        // rstd (g - mean(g) - xh mean(g xh))
+        const float2 c1 = both(-s.x * a.inv_cols * rstd), c2 = both(-s.y * a.inv_cols * rstd);
+        RowMask mask{};
+        if (a.dropping)
+            mask = row_mask(a.d, off, r);
+        char *const px = row_ptr<DT>(a.dx, r) + g0 * 16, *const pd = row_ptr<DT>(a.dropped, r) + g0 * 16;
+        auto second = [&](auto dropping) {
+#pragma unroll
+            for (int v = 0; v < NV; ++v)
+                if (has(v)) {
+                    float2 g[4], xh[4], w[4], add[4];
+                    take(0, v, g);
+                    take(1, v, xh);
+                    take(2, v, add);
+                    weights(v, w);
+                    fetch(r + step, v);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        xh[k] = __fmul2_rn(__fadd2_rn(xh[k], both(-mean)), both(rstd));
+                        g[k] = __fmul2_rn(g[k], w[k]);
+                        g[k] = __ffma2_rn(xh[k], c2, __ffma2_rn(g[k], both(rstd), __fadd2_rn(add[k], c1)));
+                    }
+                    store_pairs<DT, true>(px, v * kNext * 8, cols, true, g);
+                    if (dropping) {
+                        keep_pairs<true, false>(a.d, mask, (g0 + kNext * v) * 8, g);
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            g[k] = __fmul2_rn(g[k], both(a.d.scale));
+                        store_pairs<DT, true>(pd, v * kNext * 8, cols, true, g);
+                    }
+                }
+        };
+        if (a.dropping)
+            second(std::true_type{});
+        else
+            second(std::false_type{});
+    }
+    if (!a.partials)
+        return;
+    // the block's teams, in order, column by column (the first and the last
+    // four of each group apart again)
+    __syncthreads();
+    constexpr int width = NV * kNext;  // groups
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+        float4 *const to = s_rows + team * 4 * width + g0 + kNext * v;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            to[h * width] = make_float4(dw[v][2 * h].x, dw[v][2 * h].y, dw[v][2 * h + 1].x, dw[v][2 * h + 1].y);
+            to[(2 + h) * width] = make_float4(db[v][2 * h].x, db[v][2 * h].y, db[v][2 * h + 1].x, db[v][2 * h + 1].y);
+        }
+    }
+    __syncthreads();
+    float4 *const out = reinterpret_cast<float4 *>(a.partials + (int64_t)blockIdx.x * 2 * cols);
+    for (int i = threadIdx.x; i < 4 * groups; i += blockDim.x) {
+        const int which = i >= 2 * groups, q = i - which * 2 * groups;
+        const float4 *from = s_rows + (2 * which + (q & 1)) * width + (q >> 1);
+        float4 sum = from[0];
+#pragma unroll 4
+        for (int k = 1; k < teams; ++k) {
+            const float4 x = from[k * 4 * width];
+            sum.x += x.x, sum.y += x.y, sum.z += x.z, sum.w += x.w;
+        }
+        out[i] = sum;
+    }
+}
+
 // dx of rows too wide for k_norm_bwd: a block per row, two passes.
 template <int DT>
 __global__ void __launch_bounds__(512) k_norm_bwd_wide(const __grid_constant__ NormBwdArgs a)
@@ -889,28 +1225,36 @@ __global__ void __launch_bounds__(kThreads) k_norm_bwd_wide_cols(const __grid_co
 }
 
 // dweight (blockIdx.y 0) and dbias (1): `n` partials of each column added in
-// a fixed order, a block per 32 columns, 32 warps taking every 32nd.
-__global__ void __launch_bounds__(1024) k_norm_bwd_sum(const float *partials, int n, int64_t cols, void *dweight,
+// a fixed order, a block per 16 columns, 32 threads of a column taking every
+// 32nd.  It is launched ahead and waits; what it adds to a call is 2 to 3 us of
+// start and of two trips to L2 (8 columns per block were 0.1 us faster for 1600
+// columns and 2 us slower for 8192).
+constexpr int kSumThreads = 512, kSumCols = 16;
+
+__global__ void __launch_bounds__(kSumThreads) k_norm_bwd_sum(const float *partials, int n, int64_t cols, void *dweight,
                                                        void *dbias, int32_t gdtype)
 {
-    __shared__ float s[32][33];
+    constexpr int kSlots = kSumThreads / kSumCols;
+    __shared__ float s[kSlots][kSumCols];
     void *out = blockIdx.y ? dbias : dweight;
     if (!out)
         return;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int64_t c = (int64_t)blockIdx.x * 32 + lane;
+    const int at = threadIdx.x % kSumCols, slot = threadIdx.x / kSumCols;
+    const int64_t c = (int64_t)blockIdx.x * kSumCols + at;
     pdl_wait();
     float sum = 0.0f;
     if (c < cols)
 #pragma unroll 5
-        for (int q = warp; q < n; q += 32)
+        for (int q = slot; q < n; q += kSlots)
             sum += __ldcg(partials + ((int64_t)q * 2 + blockIdx.y) * cols + c);
-    s[warp][lane] = sum;
+    s[slot][at] = sum;
     __syncthreads();
-    sum = warp_sum_f(s[lane][warp]);  // column `warp` of the block's
-    const int64_t mine = (int64_t)blockIdx.x * 32 + warp;
-    if (lane == 0 && mine < cols)
-        store1_as(gdtype, out, mine, sum);
+    if (slot == 0 && c < cols) {
+#pragma unroll
+        for (int q = 1; q < kSlots; ++q)
+            sum += s[q][at];
+        store1_as(gdtype, out, c, sum);
+    }
 }
 
 // ------------------------------------------------------------- host side
@@ -1000,6 +1344,35 @@ constexpr int kMostThreads = 512;
 // of 8, so that a thread's rows all have the same shift.
 constexpr int kRowBlocks = 152;
 
+// From how many rows on the kernels that stage their rows are taken, for a
+// team of so many warps: a start and an end of theirs cost one to two us more
+// than the others', a row less (forward of 1600 columns: 4.2 us against 3.9
+// for 700 rows, 4.1 against 4.9 for 1500).  Sixteen warps stand against the
+// kernels of two passes (backward of 16384 columns: 31 us against 20 for 160
+// rows, 42 against 51 for 700).
+constexpr int64_t many_rows(int team) { return (team == 16 ? 2 : team > 2 ? 16 : 8) * kRowBlocks; }
+constexpr int kMostShared = 232448 - 1024;  // of a block, less what the row kernels have besides
+
+// Teams of `size` warps for a block's share of the rows: as few rows after one
+// another as `most` warps allow, and as few teams as do that.
+int64_t row_teams(int64_t rows, int most, int size)
+{
+    const int64_t all = (int64_t)kRowBlocks * (most / size), waves = (rows + all - 1) / all;
+    return (rows + waves * kRowBlocks - 1) / (waves * kRowBlocks);
+}
+
+template <int DT, int NV, int T, bool kFused>
+int norm_fwd_rows(NormArgs &a, cudaStream_t st)
+{
+    const int64_t warps = row_teams(a.rows.rows, norm_rows_threads(NV) / 32, T) * T;
+    const int smem = (int)(a.rows.cols * 8 + warps * (kFused ? 2 : 1) * NV * 512);
+    auto kernel = k_norm_fwd_rows<DT, NV, T, kFused>;
+    // (the most there is, whatever this call needs: other threads' calls set it too)
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostShared) == cudaSuccess)
+        kernel<<<kRowBlocks, (unsigned)warps * 32, smem, st>>>(a);
+    return check_launch("k_norm_fwd_rows");
+}
+
 template <int DT, bool kFused, bool kW>
 int norm_fwd(NormArgs &a, cudaStream_t st)
 {
@@ -1014,6 +1387,26 @@ int norm_fwd(NormArgs &a, cudaStream_t st)
     // spread over all SMs first.
     const bool few = rows <= 4 * kRowBlocks;
     int nv = 4;
+    if constexpr (kW && DT != ZERO_F32) {
+        // (p = 1 drops what no word says)
+        if (rows >= many_rows(groups <= 512 ? 1 : 4) && groups > 64 && groups <= 1024 && !a.d.all) {
+            switch ((groups + 31) / 32) {
+            case 3: return norm_fwd_rows<DT, 3, 1, kFused>(a, st);
+            case 4: return norm_fwd_rows<DT, 4, 1, kFused>(a, st);
+            case 5: return norm_fwd_rows<DT, 5, 1, kFused>(a, st);
+            case 6: return norm_fwd_rows<DT, 6, 1, kFused>(a, st);
+            case 7: return norm_fwd_rows<DT, 7, 1, kFused>(a, st);
+            case 8: return norm_fwd_rows<DT, 8, 1, kFused>(a, st);
+            }
+            if (groups <= 6 * 64)
+                return norm_fwd_rows<DT, 6, 2, kFused>(a, st);
+            if (groups <= 8 * 64)
+                return norm_fwd_rows<DT, 8, 2, kFused>(a, st);
+            if (groups <= 6 * 128)
+                return norm_fwd_rows<DT, 6, 4, kFused>(a, st);
+            return norm_fwd_rows<DT, 8, 4, kFused>(a, st);
+        }
+    }
     if (groups <= 32 || (few && row_threads(groups, 1, kW) <= 768))
         nv = 1;
     else if (row_threads(groups, 2, kW) <= 640)
@@ -1049,13 +1442,25 @@ int norm_fwd_of(NormArgs &a, cudaStream_t st)
 // and partials of dweight and dbias that they leave.
 struct BwdPlan {
     bool wide;
+    int rows_team;  // k_norm_bwd_rows' warps per row, or 0
     int nv, tpr, groups;
     int64_t blocks, partials;
 };
 
-BwdPlan bwd_plan(int64_t rows, int64_t groups_row, bool whole)
+// `staged`: rows that k_norm_bwd_rows may take.
+BwdPlan bwd_plan(int64_t rows, int64_t groups_row, bool whole, bool staged)
 {
     BwdPlan p{};
+    int team = 1;
+    while (team < 16 && groups_row > 128 * team)
+        team *= 2;
+    if (staged && rows >= many_rows(team) && groups_row > (team == 1 || team == 16 ? 64 : 96) * team &&
+        groups_row <= 128 * team) {
+        p.rows_team = team;
+        p.nv = groups_row <= 96 ? 3 : 4;
+        p.blocks = p.partials = kRowBlocks;
+        return p;
+    }
     p.nv = row_threads(groups_row, 1, whole) <= 768 ? 1 : 2;
     p.tpr = row_threads(groups_row, p.nv, whole);
     p.wide = p.tpr > 512 && p.nv == 2;
@@ -1078,6 +1483,17 @@ BwdPlan bwd_plan(int64_t rows, int64_t groups_row, bool whole)
     return p;
 }
 
+template <int DT, int NV, int T>
+int norm_bwd_rows(NormBwdArgs &a, cudaStream_t st)
+{
+    const int64_t warps = row_teams(a.rows.rows, kBwdRowsThreads / 32, T) * T;
+    const int64_t rows = a.rows.cols * 4 + warps * 3 * NV * 512, sums = warps * NV * 2048;
+    auto kernel = k_norm_bwd_rows<DT, NV, T>;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostShared) == cudaSuccess)
+        kernel<<<kRowBlocks, (unsigned)warps * 32, rows > sums ? rows : sums, st>>>(a);
+    return check_launch("k_norm_bwd_rows");
+}
+
 template <int DT>
 int norm_bwd(NormBwdArgs &a, const BwdPlan &p, cudaStream_t st)
 {
@@ -1095,6 +1511,15 @@ int norm_bwd(NormBwdArgs &a, const BwdPlan &p, cudaStream_t st)
     const int smem = p.groups * p.tpr * p.nv * 8 * 4;
     const unsigned grid = (unsigned)p.blocks, block = (unsigned)(p.groups * p.tpr);
     const bool whole = a.rows.kind == kWhole;
+    if (p.rows_team) {
+        if constexpr (DT != ZERO_F32) {
+            if (p.rows_team == 1)
+                return p.nv == 3 ? norm_bwd_rows<DT, 3, 1>(a, st) : norm_bwd_rows<DT, 4, 1>(a, st);
+            if (p.rows_team <= 4)
+                return p.rows_team == 2 ? norm_bwd_rows<DT, 4, 2>(a, st) : norm_bwd_rows<DT, 4, 4>(a, st);
+            return p.rows_team == 8 ? norm_bwd_rows<DT, 4, 8>(a, st) : norm_bwd_rows<DT, 4, 16>(a, st);
+        }
+    }
     if (p.nv == 1 && whole)
         k_norm_bwd<DT, 1, true><<<grid, block, smem, st>>>(a);
     else if (p.nv == 1)
@@ -1195,10 +1620,11 @@ extern "C" size_t zero_layer_norm_workspace_bytes(int64_t rows, int64_t cols)
     if (rows < 0 || cols < 0 || check_sizes(rows, cols) != ZERO_OK)
         return 0;
     // rows may start off 16 bytes: up to a group more
-    const BwdPlan a = bwd_plan(rows, (cols + 7) / 8, true), b = bwd_plan(rows, (cols + 7) / 8, false),
-                  c = bwd_plan(rows, (cols + 7) / 8 + 1, false);
-    int64_t n = a.partials > b.partials ? a.partials : b.partials;
-    n = n > c.partials ? n : c.partials;
+    const BwdPlan all[] = {bwd_plan(rows, (cols + 7) / 8, true, true), bwd_plan(rows, (cols + 7) / 8, true, false),
+                           bwd_plan(rows, (cols + 7) / 8, false, false), bwd_plan(rows, (cols + 7) / 8 + 1, false, false)};
+    int64_t n = 0;
+    for (const BwdPlan &p : all)
+        n = n > p.partials ? n : p.partials;
     return 256 + align256((size_t)n * 2 * (size_t)cols * 4);
 }
 
@@ -1251,7 +1677,8 @@ extern "C" int zero_layer_norm_backward(const void *dy, int64_t dy_ld, const voi
     }
     if (dweight || dbias)
         a.partials = reinterpret_cast<float *>(static_cast<char *>(ws) + 256);
-    const BwdPlan plan = bwd_plan(rows, groups_per_row(a.rows), a.rows.kind == kWhole);
+    const bool whole = a.rows.kind == kWhole;
+    const BwdPlan plan = bwd_plan(rows, groups_per_row(a.rows), whole, whole && dtype != ZERO_F32 && !a.d.all);
     if (dtype == ZERO_F16)
         ZERO_TRY(norm_bwd<ZERO_F16>(a, plan, st));
     else if (dtype == ZERO_BF16)
@@ -1261,8 +1688,8 @@ extern "C" int zero_layer_norm_backward(const void *dy, int64_t dy_ld, const voi
     if (!a.partials)
         return ZERO_OK;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)((cols + 31) / 32), 2);
-    cfg.blockDim = dim3(1024);
+    cfg.gridDim = dim3((unsigned)((cols + kSumCols - 1) / kSumCols), 2);
+    cfg.blockDim = dim3(kSumThreads);
     cfg.stream = st;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
