@@ -362,7 +362,8 @@ def test_empty_sizes(zp):
 FFN = [(1, 1, 1), (1, 8, 8), (1, 64, 256), (1, 1600, 640), (2, 257, 96), (3, 24, 40), (4, 512, 1024), (5, 8, 300),
        (8, 1024, 512), (9, 96, 520), (16, 200, 400), (17, 33, 65), (31, 136, 72), (64, 64, 64), (65, 320, 192),
        (127, 128, 256), (128, 256, 128), (129, 264, 136), (200, 101, 203), (256, 512, 768), (300, 72, 1000),
-       (513, 640, 264), (700, 1001, 513), (1030, 512, 520), (2049, 1608, 2056), (1999, 1501, 2011)]
+       (513, 640, 264), (700, 1001, 513), (1030, 512, 520), (2049, 1608, 2056), (1999, 1501, 2011),
+       (3, 101, 203), (3, 104, 203), (4, 257, 1001), (4, 1001, 264), (2500, 72, 200), (4001, 147, 333)]
 
 
 def ffn_inputs(m, d, f, dt, seed):

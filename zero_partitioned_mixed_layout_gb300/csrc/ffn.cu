@@ -161,13 +161,16 @@ __device__ __forceinline__ void stage_fetch(uint4 *stage, int lane, const char *
             *stage_slot(stage, row, c) = v;
         }
     } else {
-#pragma unroll 4
+        uint16_t v[32];  // all on their way at once
+#pragma unroll
         for (int r = 0; r < 32; ++r) {
-            uint16_t v = 0;
+            v[r] = 0;
             if (r < rows && lane * 2 < bytes)
-                v = __ldg(reinterpret_cast<const uint16_t *>(p + r * ld_bytes + lane * 2));
-            *(reinterpret_cast<uint16_t *>(stage_slot(stage, r, lane >> 3)) + (lane & 7)) = v;
+                v[r] = __ldg(reinterpret_cast<const uint16_t *>(p + r * ld_bytes + lane * 2));
         }
+#pragma unroll
+        for (int r = 0; r < 32; ++r)
+            *(reinterpret_cast<uint16_t *>(stage_slot(stage, r, lane >> 3)) + (lane & 7)) = v[r];
     }
 }
 
@@ -699,12 +702,18 @@ __global__ void __launch_bounds__(S::THREADS, S::PER_SM) k_ffn_product(const __g
 
 // ------------------------------------------------------------- a few tokens
 
-// Products for one or two tokens, where the weights' bytes are all there is:
-// a warp per row of the weight matrix (kPair: of the gate's and the up matrix
-// together), or `parts` warps of a block that each take a stretch of k and
-// add up in order through shared memory.  A lane multiplies 16-byte pieces of
-// the row with the tokens' pieces (which stay in L1) in binary32; four pieces
-// of each row are in flight per lane.
+// Products for one or two tokens (up to four where the widths are no multiples
+// of 8 and the tensor cores would need copies), where the weights' bytes are
+// all there is: a warp per row of the weight matrix (kPair: of the gate's and
+// the up matrix together), or `parts` warps of a block that each take a
+// stretch of k and add up in order through shared memory.  A lane multiplies
+// 16-byte pieces of the row with the tokens' pieces (which stay in L1) in
+// binary32; four pieces of each row are in flight per lane.  1600 x 6400, one
+// token: 17.3 us for both products, 3.6 TB/s of weights: each is a launch and
+// a few trips to memory long, so the time is latency as much as bytes.  Rows
+// that start anywhere cost two loads and a shift per piece, registers and
+// blocks with them: 1001 x 2731, one token: 9.9 us, four: 15.6 (21.7 by copies
+// and tiles; eight tokens this way 25.0, so tiles take over).
 struct TokenArgs {
     const void *x;  // tokens x k, row stride x_ld (kPair: of the weights' type; else binary32)
     int64_t x_ld;
@@ -715,25 +724,58 @@ struct TokenArgs {
     int32_t tokens, n, k, parts, act;
 };
 
-// Eight elements from p[i] on (zeros from k on); kW: 16-byte pieces.
-template <bool kW>
-__device__ __forceinline__ uint4 load_piece(const uint16_t *p, int32_t i, int32_t k)
+// Eight elements of a row that may start anywhere come out of the two aligned
+// 16 bytes that hold them, where those lie in the matrix (lo to hi).  The
+// loads stand apart from the shifts, so that several are on their way at once.
+struct Window {
+    uint4 a, b;
+    bool in;
+};
+
+__device__ __forceinline__ Window load_window(const uint16_t *src, const uint16_t *lo, const uint16_t *hi)
 {
-    if (kW)
-        return *reinterpret_cast<const uint4 *>(p + i);
+    const uint16_t *base = src - ((uint32_t)(reinterpret_cast<uintptr_t>(src) >> 1) & 7);
+    Window x{{}, {}, base >= lo && base + 16 <= hi};
+    if (x.in) {
+        x.a = __ldg(reinterpret_cast<const uint4 *>(base));
+        x.b = __ldg(reinterpret_cast<const uint4 *>(base) + 1);
+    }
+    return x;
+}
+
+// p[i] to p[i + 7], zeros from k on.
+__device__ __forceinline__ uint4 shifted_piece(const Window &x, const uint16_t *p, int64_t i, int64_t k)
+{
+    const uint32_t v[8] = {x.a.x, x.a.y, x.a.z, x.a.w, x.b.x, x.b.y, x.b.z, x.b.w};
+    const uint32_t off = (uint32_t)(reinterpret_cast<uintptr_t>(p + i) >> 1) & 7, bits = (off & 1) * 16;
     uint32_t w[4] = {};
 #pragma unroll
-    for (int e = 0; e < 8; ++e)
-        if (i + e < k)
-            w[e >> 1] |= (uint32_t)p[i + e] << (16 * (e & 1));
+    for (uint32_t o = 0; o < 4; ++o)  // (most often the same for a whole warp)
+        if (off >> 1 == o) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                w[e] = __funnelshift_r(v[o + e], v[o + e + 1 < 8 ? o + e + 1 : 7], bits);
+        }
+    if (!x.in) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            w[e] = (i + 2 * e < k ? p[i + 2 * e] : 0u) | (i + 2 * e + 1 < k ? (uint32_t)p[i + 2 * e + 1] << 16 : 0u);
+    } else if (i + 8 > k) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            w[e] = i + 2 * e + 1 < k ? w[e] : i + 2 * e < k ? w[e] & 0xffffu : 0u;
+    }
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
+constexpr int token_blocks(int tokens, bool whole) { return tokens == 1 ? 4 : whole ? 3 : 2; }
+
 template <int DT, int MT, bool kPair, bool kW>
-__global__ void __launch_bounds__(kThreads, MT == 1 ? 4 : 3)
+__global__ void __launch_bounds__(kThreads, token_blocks(MT, kW))
     k_ffn_tokens(const __grid_constant__ TokenArgs a)
 {
-    constexpr int R = kPair ? 2 : 1, U = 4;
+    constexpr int R = kPair ? 2 : 1, U = kW ? 4 : MT == 1 ? 1 : 2;
+    constexpr bool kX = kW || MT > 2;  // x's rows are whole 16 bytes too (zeros past k)
     __shared__ float s_part[kWarps][R * MT];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int per_block = kWarps / a.parts, unit = warp / a.parts, part = warp - unit * a.parts;
@@ -745,16 +787,20 @@ __global__ void __launch_bounds__(kThreads, MT == 1 ? 4 : 3)
         const int32_t n = n0 + unit;
         float acc[R][MT] = {};
         if (n < a.n) {
-            const uint16_t *w[2] = {static_cast<const uint16_t *>(a.w0) + (int64_t)n * a.k,
-                                    kPair ? static_cast<const uint16_t *>(a.w1) + (int64_t)n * a.k : nullptr};
+            const uint16_t *const first[2] = {static_cast<const uint16_t *>(a.w0), static_cast<const uint16_t *>(kPair ? a.w1 : a.w0)};
+            const uint16_t *const w[2] = {first[0] + (int64_t)n * a.k, first[1] + (int64_t)n * a.k};
             for (int32_t i = p0 + lane; i < p1; i += 32 * U) {
-                uint4 wv[U][R];
+                uint4 wv[kW ? U : 1][R];
+                Window win[kW ? 1 : U][R];
 #pragma unroll
                 for (int u = 0; u < U; ++u)
 #pragma unroll
                     for (int q = 0; q < R; ++q)
                         if (i + 32 * u < p1)
-                            wv[u][q] = load_piece<kW>(w[q], (i + 32 * u) * 8, a.k);
+                            if constexpr (kW)
+                                wv[u][q] = __ldg(reinterpret_cast<const uint4 *>(w[q]) + i + 32 * u);
+                            else
+                                win[u][q] = load_window(w[q] + (i + 32 * u) * 8, first[q], first[q] + (int64_t)a.n * a.k);
                 if (!waited) {
                     // the weights are not written by the launch before; x is
                     pdl_wait();
@@ -766,14 +812,23 @@ __global__ void __launch_bounds__(kThreads, MT == 1 ? 4 : 3)
                         break;
                     float wf[R][8];
 #pragma unroll
-                    for (int q = 0; q < R; ++q)
-                        Elem<DT>::to_float(&wv[u][q], wf[q]);
+                    for (int q = 0; q < R; ++q) {
+                        if constexpr (!kW)
+                            wv[0][q] = shifted_piece(win[u][q], w[q], (i + 32 * u) * 8, a.k);
+                        Elem<DT>::to_float(&wv[kW ? u : 0][q], wf[q]);
+                    }
 #pragma unroll
                     for (int m = 0; m < MT; ++m) {
                         const int64_t row = (m < a.tokens ? m : a.tokens - 1) * a.x_ld;
                         float xf[8];
                         if (kPair) {
-                            const uint4 xv = load_piece<kW>(static_cast<const uint16_t *>(a.x) + row, (i + 32 * u) * 8, a.k);
+                            const uint16_t *px = static_cast<const uint16_t *>(a.x);
+                            const int32_t c = (i + 32 * u) * 8;
+                            uint4 xv;
+                            if constexpr (kX)
+                                xv = reinterpret_cast<const uint4 *>(px + row)[i + 32 * u];
+                            else
+                                xv = shifted_piece(load_window(px + row + c, px, px + (a.tokens - 1) * a.x_ld + a.k), px + row, c, a.k);
                             Elem<DT>::to_float(&xv, xf);
                         } else {  // rows of whole 32 bytes; past k they meet zeros
                             const float4 *xv = reinterpret_cast<const float4 *>(static_cast<const float *>(a.x) + row) +
@@ -839,8 +894,10 @@ __global__ void __launch_bounds__(kThreads, MT == 1 ? 4 : 3)
         pdl_wait();
 }
 
-// Rows of 16-bit elements copied to rows of whole 16 bytes (widths that no
-// vector divides): up to five matrices in one launch.
+// Rows of 16-bit elements copied to rows of whole 16 bytes, which TMA asks
+// for (widths that no vector divides): up to five matrices in one launch,
+// bounded by memory (75 MB of weights: 32 us, 4.7 TB/s read and written).  It
+// is most of a call on few tokens and little of one on thousands.
 struct Copy {
     const uint16_t *src;
     uint16_t *dst;
@@ -866,29 +923,9 @@ __global__ void __launch_bounds__(kThreads) k_ffn_copy(const __grid_constant__ C
         const Copy &c = a.c[q];
         const int64_t at = i - c.first, per = c.dst_ld >> 3;
         const int64_t r = a.groups < kFastDivMost ? fast_div((uint32_t)at, c.per) : at / per, col = (at - r * per) * 8;
-        const uint16_t *src = c.src + r * c.src_ld + col;
-        const uint32_t off = (uint32_t)(reinterpret_cast<uintptr_t>(src) >> 1) & 7;
-        const uint16_t *base = src - off;  // the 16 bytes that hold the first element
-        uint32_t w[4] = {};
-        if (col + 8 <= c.cols && base >= c.src && base + 16 <= c.src + (c.rows - 1) * c.src_ld + c.cols) {
-            // two 16-byte loads inside the matrix, and eight elements out of their sixteen
-            const uint4 lo = __ldg(reinterpret_cast<const uint4 *>(base)), hi = __ldg(reinterpret_cast<const uint4 *>(base) + 1);
-            const uint32_t x[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
-            const uint32_t word = off >> 1, bits = (off & 1) * 16;
-#pragma unroll
-            for (uint32_t o = 0; o < 4; ++o)
-                if (word == o) {
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        w[k] = __funnelshift_r(x[o + k], x[o + k + 1 < 8 ? o + k + 1 : 7], bits);
-                }
-        } else {
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-                if (col + e < c.cols)
-                    w[e >> 1] |= (uint32_t)src[e] << (16 * (e & 1));
-        }
-        *reinterpret_cast<uint4 *>(c.dst + r * c.dst_ld + col) = make_uint4(w[0], w[1], w[2], w[3]);
+        const uint16_t *row = c.src + r * c.src_ld;
+        *reinterpret_cast<uint4 *>(c.dst + r * c.dst_ld + col) =
+            shifted_piece(load_window(row + col, c.src, c.src + (c.rows - 1) * c.src_ld + c.cols), row, col, c.cols);
     }
 }
 
@@ -909,8 +946,9 @@ using One64 = Shape<1, 64, 3, 4, EPI == kStore ? 1 : 3, EPI == kStore ? 2 : 1>;
 
 // Up to here a warp per weight row is faster than tensor-core tiles, which
 // hold 128 tokens or a fraction (1600 x 6400, one, two and four tokens: 18, 21
-// and 31 us here, 27 us in tiles).
-constexpr int kFewTokens = 2;
+// and 31 us here, 27 us in tiles; widths that need copies for tiles, 3423 x
+// 1147, four tokens: 20.7 here, 28.5 in tiles).
+constexpr int few_tokens(bool whole) { return whole ? 2 : 4; }
 
 int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 int64_t up8(int64_t a) { return (a + 7) & ~(int64_t)7; }
@@ -945,14 +983,21 @@ struct Plan {
     int splits;
 };
 
+// Clusters of one to eight CTAs that the GPU holds at once, one and two CTAs to
+// an SM (as cudaOccupancyMaxActiveClusters tells): its SMs come in groups that
+// a cluster does not cross.
+constexpr int kClusters[2][kMostParts] = {{152, 76, 46, 36, 28, 23, 15, 15}, {304, 152, 97, 74, 58, 46, 38, 36}};
+
 // The cheapest cut by an estimate of a launch's time in ns: a start (with the
 // epilogue of the last tile), and per wave of tiles and block of k the larger
 // of the issue's time and the tile bytes' through L2.  Its constants were
-// fitted to 1250 launches (tokens 5 to 1000, widths 256 to 8192, all cuts);
-// the cut it takes is on average 1.9 % slower than the best, at worst 23 %.
+// fitted to 1344 launches (tokens 5 to 1000, widths 256 to 8192, all cuts);
+// the cut it takes is on average 1.7 % slower than the best, at worst 23 %.
 // One launch each, measured: 1000 tokens, 4096 x 4096: pairs 26 us, 128 x 128
 // tiles 44, 128 x 64 88; 64 tokens, 6400 to 1600: 33, 28 and 26 us whole, 13.0
-// and 12.3 us with k in four parts, 10.8 us for 128 x 128 tiles in eight.
+// and 12.3 us with k in four parts, 10.8 us for 128 x 128 tiles in eight;
+// the backward pass of 3125 tokens, 704 x 256: 32.6 us with the three weight
+// gradients whole, 28.3 with their k in parts.
 Plan plan_product(int64_t m, int64_t n, int64_t k, bool gate, int most_parts)
 {
     const int64_t cols = n * (gate ? 2 : 1), kb = cdiv(k, 64);
@@ -961,17 +1006,19 @@ Plan plan_product(int64_t m, int64_t n, int64_t k, bool gate, int most_parts)
     const int64_t pairs = cdiv(m, 256) * cdiv(cols, 256), pair_slots = kSms / 2;
     const double pair_bytes = 65536.0 * (double)(pairs < pair_slots ? pairs : pair_slots);
     Plan best{kPair256, 1};
-    double least = 11000 + (double)cdiv(pairs, pair_slots) * kb * larger(230, pair_bytes / 13300);
+    double least = 9500 + (double)cdiv(pairs, pair_slots) * kb * larger(285, pair_bytes / 12600);
     for (int c = 0; c < 2; ++c) {
         const int bn = c == 0 ? 128 : 64;
-        const int64_t tiles = cdiv(m, 128) * cdiv(cols, bn), slots = c == 0 ? kSms : 2 * kSms;
+        const int64_t tiles = cdiv(m, 128) * cdiv(cols, bn);
         for (int parts = 1; parts <= most_parts && parts <= kb; ++parts) {
-            const int64_t ctas = tiles * parts, waves = cdiv(ctas, slots);
+            if (parts == 7)  // clusters of seven started late: 9 tokens, 2731 to 1001: 16 us, five parts 9
+                continue;
+            const int64_t ctas = tiles * parts, slots = parts * kClusters[c][parts - 1], waves = cdiv(ctas, slots);
             const double bytes = (double)(ctas < slots ? ctas : slots) * (a_bytes + bn * 128);
-            const double block = c == 0 ? larger(206, bytes / 13000) : larger(133, bytes / 8400);
-            double t = 6000 + (double)waves * cdiv(kb, parts) * block;
+            const double block = c == 0 ? larger(207, bytes / 14000) : larger(137, bytes / 8400);
+            double t = 6400 + (double)waves * cdiv(kb, parts) * block;
             if (parts > 1)  // joining the parts; and each wave is a new set of CTAs
-                t += 900 + 130 * parts + 8000.0 * (waves - 1);
+                t += 1100 + 130 * parts + 7700.0 * (waves - 1);
             if (t < least)
                 least = t, best = {c == 0 ? kOne128 : kOne64, parts};
         }
@@ -990,7 +1037,7 @@ FfnSpace ffn_space(int64_t m, int64_t d, int64_t f, bool backward)
     FfnSpace s{};
     s.mats = 256;
     // (a few tokens' act(gate) * up stays in binary32)
-    s.mat_bytes = align256((size_t)m * (size_t)up8(f) * (!backward && m <= kFewTokens ? 4 : 2));
+    s.mat_bytes = align256((size_t)m * (size_t)up8(f) * (!backward && m <= few_tokens(((d | f) & 7) == 0) ? 4 : 2));
     s.copies = s.mats + (backward ? 3 : 1) * s.mat_bytes;
     s.total = s.copies;
     if (((d | f) & 7) != 0)
@@ -1005,9 +1052,10 @@ struct Mat {
     int64_t rows, cols, ld;
 };
 
-// Operands whose rows are not whole 16 bytes, copied to the workspace; the
-// matrices then name the copies.
-int copy_operands(Mat **mats, int n, char *to, bool *copied, cudaStream_t st)
+// Operands whose rows are not whole 16 bytes (`zeros`: nor followed by zeros
+// up to the next 16), copied to the workspace; the matrices then name the
+// copies.
+int copy_operands(Mat **mats, int n, char *to, bool *copied, bool zeros, cudaStream_t st)
 {
     *copied = false;
     Copies a{};
@@ -1016,7 +1064,7 @@ int copy_operands(Mat **mats, int n, char *to, bool *copied, cudaStream_t st)
         const int64_t ld = up8(m.cols);
         if (m.rows == 0 || m.cols == 0)
             continue;
-        if (aligned16(m.p) && (m.ld & 7) == 0)
+        if (aligned16(m.p) && (m.ld & 7) == 0 && !(zeros && (m.cols & 7) != 0))
             continue;
         Copy &c = a.c[a.n++];
         c = {static_cast<const uint16_t *>(m.p), reinterpret_cast<uint16_t *>(to), m.rows, m.cols, m.ld, ld, a.groups,
@@ -1182,7 +1230,7 @@ template <int DT, bool kPair>
 int token_product(TokenArgs &a, bool whole, bool chained, cudaStream_t st)
 {
     a.parts = token_parts(a.n, a.k);
-    const int64_t units = cdiv(a.n, kWarps / a.parts), most = (int64_t)sm_count() * (a.tokens == 1 ? 4 : 3);
+    const int64_t units = cdiv(a.n, kWarps / a.parts), most = (int64_t)sm_count() * token_blocks(a.tokens, whole);
     const int grid = (int)(units < most ? units : most);
     cudaError_t e;
 #define ZERO_MT(MT)                                                                                            \
@@ -1190,8 +1238,10 @@ int token_product(TokenArgs &a, bool whole, bool chained, cudaStream_t st)
            : launch_k(k_ffn_tokens<DT, MT, kPair, false>, grid, kThreads, st, chained, a))
     if (a.tokens == 1)
         e = ZERO_MT(1);
-    else
+    else if (a.tokens == 2)
         e = ZERO_MT(2);
+    else  // (widths that no 16 bytes divide)
+        e = launch_k(k_ffn_tokens<DT, 4, kPair, false>, grid, kThreads, st, chained, a);
 #undef ZERO_MT
     if (e != cudaSuccess) {
         cudaGetLastError();
@@ -1206,12 +1256,12 @@ int token_product(TokenArgs &a, bool whole, bool chained, cudaStream_t st)
 template <int DT>
 int tokens_forward(const void *x, int64_t x_ld, const void *wg, const void *wu, const void *wd, void *y, int64_t y_ld,
                    void *gate, void *up, int32_t tokens, int32_t dim, int32_t inner, int32_t act, void *h, bool whole,
-                   cudaStream_t st)
+                   bool copied, cudaStream_t st)
 {
     TokenArgs a{};
     a.x = x, a.x_ld = x_ld, a.w0 = wg, a.w1 = wu, a.out = h, a.out_ld = up8(inner), a.o0 = gate, a.o1 = up;
     a.tokens = tokens, a.n = inner, a.k = dim, a.act = act;
-    ZERO_TRY((token_product<DT, true>(a, whole, false, st)));
+    ZERO_TRY((token_product<DT, true>(a, whole, copied, st)));
     TokenArgs b{};
     b.x = h, b.x_ld = up8(inner), b.w0 = wd, b.out = y, b.out_ld = y_ld;
     b.tokens = tokens, b.n = dim, b.k = inner;
@@ -1260,16 +1310,21 @@ extern "C" int zero_gated_ffn(const void *x, int64_t x_ld, const void *w_gate, c
         return zero_matrix(y, y_ld, tokens, dim, 2, st);
     }
     char *base = static_cast<char *>(ws);
-    if (tokens <= kFewTokens)
+    if (tokens <= few_tokens(whole)) {
+        Mat mx{x, tokens, dim, x_ld}, *only[] = {&mx};
+        bool copied = false;
+        if (tokens > 2 && !whole)
+            ZERO_TRY(copy_operands(only, 1, base + sp.copies, &copied, true, st));
         return (dtype == ZERO_F16 ? tokens_forward<ZERO_F16> : tokens_forward<ZERO_BF16>)(
-            x, x_ld, w_gate, w_up, w_down, y, y_ld, gate, up, (int32_t)tokens, (int32_t)dim, (int32_t)inner, act,
-            base + sp.mats, whole, st);
+            mx.p, mx.ld, w_gate, w_up, w_down, y, y_ld, gate, up, (int32_t)tokens, (int32_t)dim, (int32_t)inner, act,
+            base + sp.mats, whole, copied, st);
+    }
     Mat mx{x, tokens, dim, x_ld}, mg{w_gate, inner, dim, dim}, mu{w_up, inner, dim, dim};
     Mat md{w_down, dim, inner, inner};
     bool copied = false;
     if (!whole) {
         Mat *all[] = {&mx, &mg, &mu, &md};
-        ZERO_TRY(copy_operands(all, 4, base + sp.copies, &copied, st));
+        ZERO_TRY(copy_operands(all, 4, base + sp.copies, &copied, false, st));
     }
     const Mat h{base + sp.mats, tokens, inner, up8(inner)};
     ProductArgs<1, kGate> g{};
@@ -1322,7 +1377,7 @@ extern "C" int zero_gated_ffn_backward(const void *dy, int64_t dy_ld, const void
     bool copied = false;
     if (!whole) {
         Mat *all[] = {&my, &mx, &mg, &mu, &md};
-        ZERO_TRY(copy_operands(all, 5, base + sp.copies, &copied, st));
+        ZERO_TRY(copy_operands(all, 5, base + sp.copies, &copied, false, st));
     }
     const int64_t ld = up8(inner);
     const Mat dg{base + sp.mats, tokens, inner, ld}, du{base + sp.mats + sp.mat_bytes, tokens, inner, ld},
@@ -1348,5 +1403,5 @@ extern "C" int zero_gated_ffn_backward(const void *dy, int64_t dy_ld, const void
     ProductArgs<3, kStore> w{};
     w.hdr = g.hdr;
     w.out_f32 = gdtype == ZERO_F32;
-    return products<kStore, kMnMn, 3>(s3, 3, w, plan_product(3 * inner, dim, tokens, false, 1), true, dtype, st);
+    return products<kStore, kMnMn, 3>(s3, 3, w, plan_product(3 * inner, dim, tokens, false, kMostParts), true, dtype, st);
 }
