@@ -131,16 +131,30 @@ __device__ __forceinline__ void stage_get_row(uint4 *stage, int lane, uint32_t (
 template <int ES>
 __device__ __forceinline__ void stage_flush(uint4 *stage, int lane, char *p, int64_t ld_bytes, int rows, int64_t bytes)
 {
-    constexpr int kPer = 64 / ES;  // elements of a row: one per lane, or two rows at a time
-    const int e = lane % kPer;
-#pragma unroll 4
-    for (int r = lane / kPer; r < rows; r += 32 / kPer) {
-        const char *s = reinterpret_cast<const char *>(stage_slot(stage, r, e * ES / 16)) + e * ES % 16;
-        if (e * ES < bytes) {
-            if (ES == 4)
-                *reinterpret_cast<uint32_t *>(p + r * ld_bytes + e * 4) = *reinterpret_cast<const uint32_t *>(s);
-            else
-                *reinterpret_cast<uint16_t *>(p + r * ld_bytes + e * 2) = *reinterpret_cast<const uint16_t *>(s);
+    constexpr int kPer = 64 / ES, kAtOnce = 32 / kPer;  // elements of a row: one per lane, or two rows at a time
+    const int e = lane % kPer, r0 = lane / kPer;
+    if (e * ES >= bytes)
+        return;
+    p += r0 * ld_bytes + e * ES;
+    // sixteen rows read before the first is written: the compiler cannot know
+    // that the writes leave the stage alone
+#pragma unroll 1
+    for (int first = 0; first < rows; first += 16 * kAtOnce) {
+        uint32_t v[16];
+#pragma unroll
+        for (int k = 0; k < 16; ++k) {
+            const char *s = reinterpret_cast<const char *>(stage_slot(stage, first + k * kAtOnce + r0, e * ES / 16)) + e * ES % 16;
+            v[k] = ES == 4 ? *reinterpret_cast<const uint32_t *>(s) : *reinterpret_cast<const uint16_t *>(s);
+        }
+#pragma unroll
+        for (int k = 0; k < 16; ++k) {
+            if (first + k * kAtOnce + r0 < rows) {
+                if (ES == 4)
+                    *reinterpret_cast<uint32_t *>(p) = v[k];
+                else
+                    *reinterpret_cast<uint16_t *>(p) = (uint16_t)v[k];
+            }
+            p += kAtOnce * ld_bytes;
         }
     }
 }
