@@ -727,24 +727,30 @@ def _type_code(t) -> int:
     return code
 
 
+_raw_stream = None
+
+
 def _stream_handle(stream, t):
     """The cudaStream_t of `stream`, or of the current stream of t's device."""
+    global _raw_stream
     if stream is not None:
         return stream.cuda_stream
-    import torch
-    return torch._C._cuda_getCurrentRawStream(t.get_device())
+    if _raw_stream is None:
+        import torch
+        _raw_stream = torch._C._cuda_getCurrentRawStream
+    return _raw_stream(t.get_device())
 
 
 def _matrix(t, what: str, shape, dtype):
     """(pointer, row stride) of a 2-D CUDA tensor whose rows are contiguous."""
+    if t.shape == shape and t.dtype == dtype and t.is_cuda and t.is_contiguous():
+        return t.data_ptr(), shape[1]
     if t.shape != shape:
         raise ValueError(f"{what} must be {' x '.join(map(str, shape))}")
     if t.dtype != dtype:
         raise TypeError(f"{what} must be {dtype}")
     if not t.is_cuda:
         raise ValueError(f"{what} must be a CUDA tensor")
-    if t.is_contiguous():
-        return t.data_ptr(), shape[1]
     ld, inner = t.stride()
     if shape[1] > 1 and inner != 1:
         raise ValueError(f"{what}: the elements of a row must be contiguous")
@@ -758,20 +764,21 @@ def _matrix_shape(t, what: str):
     return shape
 
 
-def _vector(t, what: str, n: int, dtypes=None):
+def _vector(t, what: str, n: int):
     """The pointer of a contiguous CUDA tensor of n elements."""
     if not t.is_cuda:
         raise ValueError(f"{what} must be a CUDA tensor")
     if t.numel() != n or not t.is_contiguous():
         raise ValueError(f"{what} must hold {n} elements, contiguous")
-    if dtypes is not None and t.dtype not in dtypes:
-        raise TypeError(f"{what} must be {' or '.join(map(str, dtypes))}")
     return t.data_ptr()
 
 
 def _f32_pointer(t, what: str, n: int):
-    import torch
-    return None if t is None else _vector(t, what, n, (torch.float32,))
+    if t is None:
+        return None
+    if _type_code(t) != ZERO_F32:
+        raise TypeError(f"{what} must be float32")
+    return _vector(t, what, n)
 
 
 def _pair_code(a, b, what: str, default: int) -> int:
@@ -890,8 +897,9 @@ def zero_gated_ffn(x, w_gate, w_up, w_down, y, ws, act: int = ZERO_ACT_SILU, gat
     tokens, dim, inner, weights = _ffn_weights(x, w_gate, w_up, w_down)
     xp, xl = _matrix(x, "x", x.shape, x.dtype)
     yp, yl = _matrix(y, "y", x.shape, x.dtype)
-    gp, up_ = (None if t is None else _contiguous_matrix(t, name, (tokens, inner), (x.dtype,))
-               for t, name in ((gate, "gate"), (up, "up")))
+    one = (x.dtype,)
+    gp = None if gate is None else _contiguous_matrix(gate, "gate", (tokens, inner), one)
+    up_ = None if up is None else _contiguous_matrix(up, "up", (tokens, inner), one)
     _device_tensor(ws, "workspace")
     rc = _sublayer_lib().zero_gated_ffn(xp, xl, *weights, yp, yl, gp, up_, tokens, dim, inner, int(act),
                                         _type_code(x), ws.data_ptr(), ws.numel(), _stream_handle(stream, x))
@@ -902,20 +910,22 @@ def zero_gated_ffn_backward(dy, x, w_gate, w_up, w_down, gate, up, dx, dw_gate, 
                             act: int = ZERO_ACT_SILU, stream=None) -> None:
     """The gradients of zero_gated_ffn from the kept gate and up: dx, and the
     three weight gradients (x's type or float32)."""
-    import torch
     tokens, dim, inner, weights = _ffn_weights(x, w_gate, w_up, w_down)
     xp, xl = _matrix(x, "x", x.shape, x.dtype)
     yp, yl = _matrix(dy, "dy", x.shape, x.dtype)
     dp, dl = _matrix(dx, "dx", x.shape, x.dtype)
-    one, any_ = (x.dtype,), (x.dtype, torch.float32)
-    kept = [_contiguous_matrix(t, name, (tokens, inner), one) for t, name in ((gate, "gate"), (up, "up"))]
-    grads = [_contiguous_matrix(t, name, shape, any_) for t, name, shape in
-             ((dw_gate, "dw_gate", (inner, dim)), (dw_up, "dw_up", (inner, dim)), (dw_down, "dw_down", (dim, inner)))]
-    if len({dw_gate.dtype, dw_up.dtype, dw_down.dtype}) != 1:
+    one, code, gcode = (x.dtype,), _type_code(x), _type_code(dw_gate)
+    if gcode != code and gcode != ZERO_F32:
+        raise TypeError(f"dw_gate must be {x.dtype} or float32")
+    if dw_gate.dtype != dw_up.dtype or dw_gate.dtype != dw_down.dtype:
         raise TypeError("the weight gradients must share one element type")
+    kept = [_contiguous_matrix(gate, "gate", (tokens, inner), one), _contiguous_matrix(up, "up", (tokens, inner), one)]
+    one = (dw_gate.dtype,)
+    grads = [_contiguous_matrix(dw_gate, "dw_gate", (inner, dim), one), _contiguous_matrix(dw_up, "dw_up", (inner, dim), one),
+             _contiguous_matrix(dw_down, "dw_down", (dim, inner), one)]
     _device_tensor(ws, "workspace")
-    rc = _sublayer_lib().zero_gated_ffn_backward(yp, yl, xp, xl, *weights, *kept, dp, dl, *grads, _type_code(dw_gate),
-                                                 tokens, dim, inner, int(act), _type_code(x), ws.data_ptr(),
+    rc = _sublayer_lib().zero_gated_ffn_backward(yp, yl, xp, xl, *weights, *kept, dp, dl, *grads, gcode,
+                                                 tokens, dim, inner, int(act), code, ws.data_ptr(),
                                                  ws.numel(), _stream_handle(stream, x))
     _check(rc, "zero_gated_ffn_backward")
 

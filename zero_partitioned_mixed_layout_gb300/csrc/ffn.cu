@@ -1023,14 +1023,17 @@ Plan plan_product(int64_t m, int64_t n, int64_t k, bool gate, int most_parts)
     double least = 9500 + (double)cdiv(pairs, pair_slots) * kb * larger(285, pair_bytes / 12600);
     for (int c = 0; c < 2; ++c) {
         const int bn = c == 0 ? 128 : 64;
-        const int64_t tiles = cdiv(m, 128) * cdiv(cols, bn);
-        for (int parts = 1; parts <= most_parts && parts <= kb; ++parts) {
+        const int64_t all = cdiv(m, 128) * cdiv(cols, bn);
+        if (all > 1 << 24)  // (pairs, by far; and what follows fits 32 bits)
+            continue;
+        const int tiles = (int)all, blocks = (int)kb, most = blocks < most_parts ? blocks : most_parts;
+        for (int parts = 1; parts <= most; ++parts) {
             if (parts == 7)  // clusters of seven started late: 9 tokens, 2731 to 1001: 16 us, five parts 9
                 continue;
-            const int64_t ctas = tiles * parts, slots = parts * kClusters[c][parts - 1], waves = cdiv(ctas, slots);
+            const int ctas = tiles * parts, slots = parts * kClusters[c][parts - 1], waves = (ctas - 1) / slots + 1;
             const double bytes = (double)(ctas < slots ? ctas : slots) * (a_bytes + bn * 128);
             const double block = c == 0 ? larger(207, bytes / 14000) : larger(137, bytes / 8400);
-            double t = 6400 + (double)waves * cdiv(kb, parts) * block;
+            double t = 6400 + (double)waves * ((blocks - 1) / parts + 1) * block;
             if (parts > 1)  // joining the parts; and each wave is a new set of CTAs
                 t += 1100 + 130 * parts + 7700.0 * (waves - 1);
             if (t < least)
