@@ -406,8 +406,8 @@ struct NormArgs {
 // 4096 x 16384: 73 us with it, 98 without).  One row of 1600 takes 2.3 us,
 // which is a launch and two trips to memory; 8192 x 1600 binary32 21.6
 // (4.9 TB/s), bounded by the instructions of a row's two sums and its ends.
-template <int DT, int NV, bool kFused, bool kW>
-__global__ void __launch_bounds__(NV == 1 ? 768 : NV == 2 ? 640 : 512) k_norm_fwd(const __grid_constant__ NormArgs a)
+template <int DT, int NV, bool kFused, bool kW, int THREADS>
+__global__ void __launch_bounds__(THREADS) k_norm_fwd(const __grid_constant__ NormArgs a)
 {
     constexpr bool kKeep = NV <= 2, kAhead = NV <= 2 || DT != ZERO_F32;
     __shared__ float s_red[2][32];
@@ -809,12 +809,12 @@ __device__ __forceinline__ float2 group_sum2(float2 v, float2 *s, int tpr, int g
 // block) apart; NG is a multiple of 8 when a group takes more than one row,
 // so that its rows all have the same shift.  The next row is loaded before
 // the sums of this one are exchanged; a row is held as it came (16-bit) and
-// converted again after the exchange.  3001 x 2049 binary32: 27.5 us
-// (2.7 TB/s); 8192 x 1600 binary32 with sum and mask 54 (4.9 TB/s): bounded by
+// converted again after the exchange.  3001 x 2049 binary32: 23.1 us
+// (3.2 TB/s); 8192 x 1600 binary32 with sum and mask 50 (5.2 TB/s): bounded by
 // instructions (a row's address, ends and two sums are each warp's own) and by
 // the barrier that the sums cross.
-template <int DT, int NV, bool kW>
-__global__ void __launch_bounds__(NV == 1 ? 768 : 512) k_norm_bwd(const __grid_constant__ NormBwdArgs a)
+template <int DT, int NV, bool kW, int THREADS>
+__global__ void __launch_bounds__(THREADS) k_norm_bwd(const __grid_constant__ NormBwdArgs a)
 {
     extern __shared__ float s_cols[];
     __shared__ float2 s_red[2][32];
@@ -1386,6 +1386,11 @@ int norm_fwd(NormArgs &a, cudaStream_t st)
     // block (what the registers of one block per SM allow), few rows are
     // spread over all SMs first.
     const bool few = rows <= 4 * kRowBlocks;
+    // Binary32 with the sum spills in the registers of 640 threads: 512 there
+    // (8192 x 1600 37.7 us to 34.0, 8192 x 1601 52 to 37), and 384 where four
+    // groups leave them.
+    constexpr bool kSpills = DT == ZERO_F32 && kFused;
+    constexpr int kTwo = kSpills ? 512 : 640, kFour = kSpills ? 384 : 512;
     int nv = 4;
     if constexpr (kW && DT != ZERO_F32) {
         // (p = 1 drops what no word says)
@@ -1409,9 +1414,9 @@ int norm_fwd(NormArgs &a, cudaStream_t st)
     }
     if (groups <= 32 || (few && row_threads(groups, 1, kW) <= 768))
         nv = 1;
-    else if (row_threads(groups, 2, kW) <= 640)
+    else if (row_threads(groups, 2, kW) <= kTwo)
         nv = 2;
-    const int tpr = row_threads(groups, nv, kW), most = nv == 1 ? 768 : nv == 2 ? 640 : 512;
+    const int tpr = row_threads(groups, nv, kW), most = nv == 1 ? 768 : nv == 2 ? kTwo : 512;
     int64_t teams = most / tpr;
     if (tpr > 32 && teams > 15)
         teams = 15;  // named barriers
@@ -1421,11 +1426,13 @@ int norm_fwd(NormArgs &a, cudaStream_t st)
     const int64_t need = (rows + teams - 1) / teams;
     const unsigned grid = (unsigned)(need < kRowBlocks ? need : kRowBlocks), block = (unsigned)(teams * tpr);
     if (nv == 1)
-        k_norm_fwd<DT, 1, kFused, kW><<<grid, block, 0, st>>>(a);
+        k_norm_fwd<DT, 1, kFused, kW, 768><<<grid, block, 0, st>>>(a);
     else if (nv == 2)
-        k_norm_fwd<DT, 2, kFused, kW><<<grid, block, 0, st>>>(a);
+        k_norm_fwd<DT, 2, kFused, kW, kTwo><<<grid, block, 0, st>>>(a);
+    else if (block <= kFour)
+        k_norm_fwd<DT, 4, kFused, kW, kFour><<<grid, block, 0, st>>>(a);
     else
-        k_norm_fwd<DT, 4, kFused, kW><<<grid, block, 0, st>>>(a);
+        k_norm_fwd<DT, 4, kFused, kW, 512><<<grid, block, 0, st>>>(a);
     return check_launch("k_norm_fwd");
 }
 
@@ -1448,7 +1455,7 @@ struct BwdPlan {
 };
 
 // `staged`: rows that k_norm_bwd_rows may take.
-BwdPlan bwd_plan(int64_t rows, int64_t groups_row, bool whole, bool staged)
+BwdPlan bwd_plan(int64_t rows, int64_t groups_row, bool whole, bool staged, bool f32)
 {
     BwdPlan p{};
     int team = 1;
@@ -1468,7 +1475,7 @@ BwdPlan bwd_plan(int64_t rows, int64_t groups_row, bool whole, bool staged)
         p.partials = rows < kWarps * 64 ? (rows + kWarps - 1) / kWarps : 64;
         return p;
     }
-    p.groups = (p.nv == 1 ? 768 : 512) / p.tpr;
+    p.groups = (p.nv == 2 ? 512 : f32 && p.tpr <= 640 ? 640 : 768) / p.tpr;
     if (p.tpr > 32 && p.groups > 15)
         p.groups = 15;  // named barriers
     const int64_t need = (rows + p.groups - 1) / p.groups;
@@ -1520,14 +1527,14 @@ int norm_bwd(NormBwdArgs &a, const BwdPlan &p, cudaStream_t st)
             return p.rows_team == 8 ? norm_bwd_rows<DT, 4, 8>(a, st) : norm_bwd_rows<DT, 4, 16>(a, st);
         }
     }
-    if (p.nv == 1 && whole)
-        k_norm_bwd<DT, 1, true><<<grid, block, smem, st>>>(a);
-    else if (p.nv == 1)
-        k_norm_bwd<DT, 1, false><<<grid, block, smem, st>>>(a);
-    else if (whole)
-        k_norm_bwd<DT, 2, true><<<grid, block, smem, st>>>(a);
+    // (binary32 spills in the registers of 768 threads: 3001 x 2049 27.9 us to 23.1, 8192 x 1601 45 to 40)
+    constexpr int kMost = DT == ZERO_F32 ? 640 : 768;
+    if (p.nv == 2)
+        (whole ? k_norm_bwd<DT, 2, true, 512> : k_norm_bwd<DT, 2, false, 512>)<<<grid, block, smem, st>>>(a);
+    else if (block <= kMost)
+        (whole ? k_norm_bwd<DT, 1, true, kMost> : k_norm_bwd<DT, 1, false, kMost>)<<<grid, block, smem, st>>>(a);
     else
-        k_norm_bwd<DT, 2, false><<<grid, block, smem, st>>>(a);
+        (whole ? k_norm_bwd<DT, 1, true, 768> : k_norm_bwd<DT, 1, false, 768>)<<<grid, block, smem, st>>>(a);
     return check_launch("k_norm_bwd");
 }
 
@@ -1620,11 +1627,11 @@ extern "C" size_t zero_layer_norm_workspace_bytes(int64_t rows, int64_t cols)
     if (rows < 0 || cols < 0 || check_sizes(rows, cols) != ZERO_OK)
         return 0;
     // rows may start off 16 bytes: up to a group more
-    const BwdPlan all[] = {bwd_plan(rows, (cols + 7) / 8, true, true), bwd_plan(rows, (cols + 7) / 8, true, false),
-                           bwd_plan(rows, (cols + 7) / 8, false, false), bwd_plan(rows, (cols + 7) / 8 + 1, false, false)};
-    int64_t n = 0;
-    for (const BwdPlan &p : all)
-        n = n > p.partials ? n : p.partials;
+    int64_t n = bwd_plan(rows, (cols + 7) / 8, true, true, false).partials;
+    for (bool f32 : {false, true})
+        for (const BwdPlan &p : {bwd_plan(rows, (cols + 7) / 8, true, false, f32), bwd_plan(rows, (cols + 7) / 8, false, false, f32),
+                                 bwd_plan(rows, (cols + 7) / 8 + 1, false, false, f32)})
+            n = n > p.partials ? n : p.partials;
     return 256 + align256((size_t)n * 2 * (size_t)cols * 4);
 }
 
@@ -1678,7 +1685,7 @@ extern "C" int zero_layer_norm_backward(const void *dy, int64_t dy_ld, const voi
     if (dweight || dbias)
         a.partials = reinterpret_cast<float *>(static_cast<char *>(ws) + 256);
     const bool whole = a.rows.kind == kWhole;
-    const BwdPlan plan = bwd_plan(rows, groups_per_row(a.rows), whole, whole && dtype != ZERO_F32 && !a.d.all);
+    const BwdPlan plan = bwd_plan(rows, groups_per_row(a.rows), whole, whole && dtype != ZERO_F32 && !a.d.all, dtype == ZERO_F32);
     if (dtype == ZERO_F16)
         ZERO_TRY(norm_bwd<ZERO_F16>(a, plan, st));
     else if (dtype == ZERO_BF16)
