@@ -1,0 +1,41 @@
+"""The feed-forward sub-block on the GPU at the edges of its sizes, values and
+waits, against its formulas in binary64 (sublayer_ref.py)."""
+import pytest
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+import sublayer_ref as ref  # noqa: E402
+
+TYPES = {"f16": torch.float16, "bf16": torch.bfloat16, "f32": torch.float32}
+
+
+@pytest.fixture(scope="module")
+def zp():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from zero_partitioned_mixed_layout_gb300 import _build
+    _build.build()
+    import zero_partitioned_mixed_layout_gb300 as zp
+    zp.lib()
+    return zp
+
+
+def randn(shape, dtype, seed, std=1.0, mean=0.0):
+    gen = torch.Generator(device="cuda").manual_seed(seed)
+    return torch.empty(shape, device="cuda").normal_(mean, std, generator=gen).to(dtype)
+
+
+def close(got, want, dtype, what):
+    value, err = want
+    ref.check(got, value, ref.rounded(value, err, dtype), what)
+
+
+@pytest.mark.parametrize("rows", [0, 1, 700, 5000])
+def test_layer_norm_of_no_columns(zp, rows):
+    z = torch.empty((rows, 0), dtype=torch.float16, device="cuda")
+    stats = torch.empty(rows, device="cuda")
+    none = torch.empty(0, device="cuda")
+    zp.zero_layer_norm(z, None, None, z)
+    zp.zero_layer_norm_backward(z, z, None, stats, stats, z, none, none, zp.new_layer_norm_workspace(rows, 0))
+    torch.cuda.synchronize()

@@ -1626,6 +1626,8 @@ extern "C" size_t zero_layer_norm_workspace_bytes(int64_t rows, int64_t cols)
 {
     if (rows < 0 || cols < 0 || check_sizes(rows, cols) != ZERO_OK)
         return 0;
+    if (rows == 0 || cols == 0)
+        return 256;  // (no plan is made for nothing)
     // rows may start off 16 bytes: up to a group more
     int64_t n = bwd_plan(rows, (cols + 7) / 8, true, true, false).partials;
     for (bool f32 : {false, true})
