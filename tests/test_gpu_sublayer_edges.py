@@ -39,3 +39,28 @@ def test_layer_norm_of_no_columns(zp, rows):
     zp.zero_layer_norm(z, None, None, z)
     zp.zero_layer_norm_backward(z, z, None, stats, stats, z, none, none, zp.new_layer_norm_workspace(rows, 0))
     torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("shape", [(1217, 1600), (1216, 2048), (2433, 4096), (305, 16384)], ids=str)
+def test_layer_norm_backward_repeats_its_weight_gradients(zp, shape):
+    """Rows that leave some teams without one, and the last copies of all teams
+    just behind their last row: the sums over the block, which take the place
+    of the staged rows, are right and the same bits on every run."""
+    rows, cols = shape
+    dt = torch.bfloat16
+    x, dy, w = randn(shape, dt, 1, 1.5, 0.5), randn(shape, dt, 2), randn((cols,), dt, 3, 0.2, 1.0)
+    r = ref.layer_norm(x, None, None, 1e-5)
+    mean, rstd = r["mean"][0].float(), r["rstd"][0].float()
+    ws, dx = zp.new_layer_norm_workspace(rows, cols), torch.empty_like(x)
+    dw, db = (torch.empty(cols, device="cuda") for _ in range(2))
+    b = ref.layer_norm_backward(dy, x, w, mean, rstd)
+    first = None
+    for _ in range(50):
+        dw.fill_(float("nan"))
+        db.fill_(float("nan"))
+        zp.zero_layer_norm_backward(dy, x, w, mean, rstd, dx, dw, db, ws)
+        if first is None:
+            first = dw.clone(), db.clone()
+            close(dw, b["dweight"], torch.float32, "dweight")
+            close(db, b["dbias"], torch.float32, "dbias")
+        assert torch.equal(dw, first[0]) and torch.equal(db, first[1])

@@ -39,3 +39,27 @@ def test_layer_norm_backward_of_no_columns(zp):
         "print(bwd(4, 256, 16), bwd(4, 128, 256), bwd(4, None, 256), bwd(0, 256, 16))\n")
     assert out[:4] == ["256"] * 4
     assert out[4:] == ["-5", "-2", "-5", "-5"]  # ZERO_EWORKSPACE, ZERO_EALIGN
+
+
+def kernel_source(name):
+    """The text of a kernel's body in norm.cu."""
+    text = open(os.path.join(ROOT, "zero_partitioned_mixed_layout_gb300", "csrc", "norm.cu")).read()
+    at = text.index("{", text.index(f" {name}(const __grid_constant__"))
+    depth = 0
+    for end in range(at, len(text)):
+        depth += {"{": 1, "}": -1}.get(text[end], 0)
+        if depth == 0:
+            return text[at:end]
+    raise AssertionError(name)
+
+
+def test_norm_backward_waits_for_its_copies_before_their_memory_is_used_again():
+    """A team's last turn, and a team without rows, issue copies that write
+    zeros to shared memory; a barrier does not order them, only their thread's
+    own wait does, so it comes between the rows and the sums over the block."""
+    body = kernel_source("k_norm_bwd_rows")
+    last_issue = body.rindex("second(std::false_type{})")
+    join = body.index("float4 *const to = s_rows + team", last_issue)
+    between = body[last_issue:join]
+    assert "copies_done();" in between
+    assert between.index("copies_done();") < between.rindex("__syncthreads();")

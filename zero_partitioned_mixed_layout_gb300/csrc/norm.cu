@@ -1082,6 +1082,9 @@ __global__ void __launch_bounds__(kBwdRowsThreads) k_norm_bwd_rows(const __grid_
         else
             second(std::false_type{});
     }
+    // the last turn's copies, of rows that are not there, write zeros where the
+    // rows lay at any time until their thread has waited for them
+    copies_done();
     if (!a.partials)
         return;
     // the block's teams, in order, column by column (the first and the last
