@@ -63,3 +63,19 @@ def test_norm_backward_waits_for_its_copies_before_their_memory_is_used_again():
     between = body[last_issue:join]
     assert "copies_done();" in between
     assert between.index("copies_done();") < between.rindex("__syncthreads();")
+
+
+@pytest.mark.parametrize("name", ["k_norm_fwd_rows", "k_norm_bwd_rows"])
+def test_a_staging_kernel_ends_without_copies_under_way(name):
+    """After the loop over rows, before the first return: the copies that the
+    last turn (or a team without rows) has issued."""
+    body = kernel_source(name)
+    loop = body.index("{", body.rindex("r < a.rows.rows; r += step"))
+    depth = 0
+    for end in range(loop, len(body)):
+        depth += {"{": 1, "}": -1}.get(body[end], 0)
+        if depth == 0:
+            break
+    after = body[end:]
+    assert "copies_done();" in after
+    assert "return" not in after[:after.index("copies_done();")]

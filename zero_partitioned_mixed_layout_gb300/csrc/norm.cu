@@ -675,6 +675,7 @@ __global__ void __launch_bounds__(norm_rows_threads(NV)) k_norm_fwd_rows(const _
                 a.rstd[r] = rstd;
         }
     }
+    copies_done();  // (the last turn's, before the block gives its memory back)
 }
 
 // Forward of rows too wide for the registers of a block: three passes over
