@@ -64,3 +64,37 @@ def test_layer_norm_backward_repeats_its_weight_gradients(zp, shape):
             close(dw, b["dweight"], torch.float32, "dweight")
             close(db, b["dbias"], torch.float32, "dbias")
         assert torch.equal(dw, first[0]) and torch.equal(db, first[1])
+
+
+@pytest.mark.parametrize("tokens", [1, 3])
+def test_gated_ffn_with_rows_up_to_the_limit(zp, tokens):
+    """An inner width of 2^31 - 512, the largest: the rows of the gate's and
+    the up matrix (one element each) end within a grid's step of 2^31.  x is
+    one or a power of two, so gate and up are the weights, exactly; w_down is
+    zero but for some columns, so y is their sum."""
+    inner, dt = 2 ** 31 - 512, torch.float16
+    x = torch.tensor([[1.0], [2.0], [0.5]], dtype=dt, device="cuda")[:tokens]
+    wg, wu = (torch.empty((inner, 1), dtype=dt, device="cuda") for _ in range(2))
+    gen = torch.Generator(device="cuda").manual_seed(7)
+    for w in (wg, wu):
+        w.uniform_(0.5, 1.5, generator=gen)
+    wd = torch.zeros((1, inner), dtype=dt, device="cuda")
+    last = slice(inner - 6000, inner)
+    wd[:, last] = 2.0 ** -10
+    wd[:, :100] = -(2.0 ** -10)
+    y = torch.full((tokens, 1), float("nan"), dtype=dt, device="cuda")
+    gate, up = (torch.empty((tokens, inner), dtype=dt, device="cuda") for _ in range(2))
+    ws = zp.new_gated_ffn_workspace(tokens, 1, inner)
+    zp.zero_gated_ffn(x, wg, wu, wd, y, ws, gate=gate, up=up)
+    for m in range(tokens):
+        # (a product with a power of two is exact: every element normal)
+        assert torch.equal(gate[m], wg[:, 0] * x[m]) and torch.equal(up[m], wu[:, 0] * x[m])
+    for part, sign in ((slice(0, 100), -1.0), (last, 1.0)):
+        g, u = (x.double() @ w[part].double().T for w in (wg, wu))
+        v = ref.act(ref.SILU, g)
+        terms = v[0] * u * 2.0 ** -10
+        # the sum's other terms are zeros: 6100 roundings of it at most
+        err = (v[2] * u.abs() * 2.0 ** -10 + 6200 * ref.U32 * terms.abs()).sum(1, keepdim=True)
+        want = (sign * terms.sum(1, keepdim=True), err) if part.start == 0 else (
+            want[0] + terms.sum(1, keepdim=True), want[1] + err)
+    close(y, want, dt, "y")

@@ -1,6 +1,7 @@
 """The feed-forward sub-block's host side at the edges of its arguments (no
 GPU: sizes of workspaces, and calls that a check ends before any launch)."""
 import os
+import re
 import subprocess
 import sys
 
@@ -79,3 +80,17 @@ def test_a_staging_kernel_ends_without_copies_under_way(name):
     after = body[end:]
     assert "copies_done();" in after
     assert "return" not in after[:after.index("copies_done();")]
+
+
+def test_few_token_rows_are_counted_without_a_sign():
+    """Rows of a weight matrix go up to 2^31 - 512, and a block's next row is up
+    to 152 * 4 * 8 further: past 2^31, where a signed count would be negative
+    and pass for a row in front of the matrix."""
+    text = open(os.path.join(ROOT, "zero_partitioned_mixed_layout_gb300", "csrc", "ffn.cu")).read()
+    body = text[text.index("k_ffn_tokens(const __grid_constant__ TokenArgs a)"):]
+    loop = re.search(r"for \((\w+) n0 = blockIdx.x \* per_block; n0 < (\w+);", body)
+    assert loop and loop[1] == "uint32_t"
+    assert re.search(rf"const uint32_t {loop[2]} = a\.n;", body)
+    assert re.search(r"const uint32_t n = n0 \+ unit;", body)
+    most, step = 2 ** 31 - 512, 152 * 4 * 8
+    assert most + step < 2 ** 32

@@ -806,10 +806,12 @@ __global__ void __launch_bounds__(kThreads, token_blocks(MT, kW))
     const int32_t p0 = (int32_t)((int64_t)pieces * part / a.parts), p1 = (int32_t)((int64_t)pieces * (part + 1) / a.parts);
     bool waited = false;
     pdl_launch_next();
-    for (int32_t n0 = blockIdx.x * per_block; n0 < a.n; n0 += gridDim.x * per_block) {
-        const int32_t n = n0 + unit;
+    // (unsigned: a matrix may have 2^31 - 512 rows, and a step goes past them)
+    const uint32_t rows = a.n;
+    for (uint32_t n0 = blockIdx.x * per_block; n0 < rows; n0 += gridDim.x * per_block) {
+        const uint32_t n = n0 + unit;
         float acc[R][MT] = {};
-        if (n < a.n) {
+        if (n < rows) {
             const uint16_t *const first[2] = {static_cast<const uint16_t *>(a.w0), static_cast<const uint16_t *>(kPair ? a.w1 : a.w0)};
             const uint16_t *const w[2] = {first[0] + (int64_t)n * a.k, first[1] + (int64_t)n * a.k};
             for (int32_t i = p0 + lane; i < p1; i += 32 * U) {
@@ -897,7 +899,7 @@ __global__ void __launch_bounds__(kThreads, token_blocks(MT, kW))
                         for (int j = 1; j < a.parts; ++j)
                             acc[q][m] += s_part[warp + j][q * MT + m];
         }
-        if (part == 0 && n < a.n && lane == 0) {
+        if (part == 0 && n < rows && lane == 0) {
 #pragma unroll
             for (int m = 0; m < MT; ++m)
                 if (m < a.tokens) {
