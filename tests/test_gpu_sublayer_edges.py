@@ -98,3 +98,23 @@ def test_gated_ffn_with_rows_up_to_the_limit(zp, tokens):
         want = (sign * terms.sum(1, keepdim=True), err) if part.start == 0 else (
             want[0] + terms.sum(1, keepdim=True), want[1] + err)
     close(y, want, dt, "y")
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("cols", [256, 1600, 2049, 9001])
+def test_layer_norm_workspace_of_the_largest_batch_serves_all(zp, cols, dtype):
+    """One workspace, made for the longest batch, at row counts around those
+    where the blocks' plan changes."""
+    dt, most = TYPES[dtype], 1300
+    ws = zp.new_layer_norm_workspace(most, cols)
+    x, dy = randn((most, cols), dt, 4, 1.5, 0.5), randn((most, cols), dt, 5)
+    dx = torch.empty_like(x)
+    dw, db = (torch.empty(cols, device="cuda") for _ in range(2))
+    for rows in (1, 2, 7, 8, 9, 151, 152, 153, 304, 305, 456, 457, 608, 609, 760, 761, 912, 913, 1215, 1216, 1300):
+        r = ref.layer_norm(x[:rows], None, None, 1e-5)
+        mean, rstd = r["mean"][0].float(), r["rstd"][0].float()
+        zp.zero_layer_norm_backward(dy[:rows], x[:rows], None, mean, rstd, dx[:rows], dw, db, ws)
+        b = ref.layer_norm_backward(dy[:rows], x[:rows], None, mean, rstd)
+        close(dx[:rows], b["dx"], dt, f"dx of {rows}")
+        close(dw, b["dweight"], torch.float32, f"dweight of {rows}")
+        close(db, b["dbias"], torch.float32, f"dbias of {rows}")

@@ -94,3 +94,18 @@ def test_few_token_rows_are_counted_without_a_sign():
     assert re.search(r"const uint32_t n = n0 \+ unit;", body)
     most, step = 2 ** 31 - 512, 152 * 4 * 8
     assert most + step < 2 ** 32
+
+
+@pytest.mark.parametrize("cols", [1, 8, 33, 256, 1001, 1600, 2049, 8192, 8200, 16384, 20001, 40000, 1 << 20])
+def test_layer_norm_workspace_for_many_rows_serves_fewer(zp, cols):
+    sizes = [zp.zero_layer_norm_workspace_bytes(rows, cols) for rows in range(2000)]
+    assert sizes == sorted(sizes)
+    assert sizes[-1] <= zp.zero_layer_norm_workspace_bytes(1 << 20, cols)
+    # and no row's two sums are without a place while a block may take one row
+    assert all(s >= 256 + min(rows, 64) * 2 * cols * 4 for rows, s in enumerate(sizes))
+
+
+def test_layer_norm_workspace_for_wide_rows_serves_narrow_ones(zp):
+    for rows in (1, 5, 100, 153, 761, 1217, 100_000):
+        sizes = [zp.zero_layer_norm_workspace_bytes(rows, cols) for cols in range(0, 40_000, 7)]
+        assert sizes == sorted(sizes)

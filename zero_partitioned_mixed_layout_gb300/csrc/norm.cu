@@ -1630,15 +1630,11 @@ extern "C" size_t zero_layer_norm_workspace_bytes(int64_t rows, int64_t cols)
 {
     if (rows < 0 || cols < 0 || check_sizes(rows, cols) != ZERO_OK)
         return 0;
-    if (rows == 0 || cols == 0)
-        return 256;  // (no plan is made for nothing)
-    // rows may start off 16 bytes: up to a group more
-    int64_t n = bwd_plan(rows, (cols + 7) / 8, true, true, false).partials;
-    for (bool f32 : {false, true})
-        for (const BwdPlan &p : {bwd_plan(rows, (cols + 7) / 8, true, false, f32), bwd_plan(rows, (cols + 7) / 8, false, false, f32),
-                                 bwd_plan(rows, (cols + 7) / 8 + 1, false, false, f32)})
-            n = n > p.partials ? n : p.partials;
-    return 256 + align256((size_t)n * 2 * (size_t)cols * 4);
+    // No plan leaves more partials than blocks, or blocks than rows.  (Not the
+    // plan's own count: that falls as a row more gives a block another team,
+    // and a workspace for many rows is to serve fewer as well.)
+    const int64_t most = rows < kRowBlocks ? rows : kRowBlocks;
+    return 256 + align256((size_t)most * 2 * (size_t)cols * 4);
 }
 
 extern "C" int zero_layer_norm_backward(const void *dy, int64_t dy_ld, const void *x, int64_t x_ld,
