@@ -118,3 +118,16 @@ def test_layer_norm_workspace_of_the_largest_batch_serves_all(zp, cols, dtype):
         close(dx[:rows], b["dx"], dt, f"dx of {rows}")
         close(dw, b["dweight"], torch.float32, f"dweight of {rows}")
         close(db, b["dbias"], torch.float32, f"dbias of {rows}")
+
+
+@pytest.mark.parametrize("dim,inner", [(64, 256), (51, 99), (1600, 640)])
+def test_gated_ffn_workspace_of_the_largest_batch_serves_all(zp, dim, inner):
+    for most in (3, 5, 40):
+        ws = zp.new_gated_ffn_workspace(most, dim, inner)
+        for m in [k for k in (1, 2, 3, 4, 5, 9, 40) if k <= most]:
+            dt = torch.float16
+            x, wg, wu, wd = (randn(s, dt, 10 + k, std) for k, (s, std) in enumerate(
+                [((m, dim), 1.0), ((inner, dim), dim ** -0.5), ((inner, dim), dim ** -0.5), ((dim, inner), inner ** -0.5)]))
+            y = torch.empty_like(x)
+            zp.zero_gated_ffn(x, wg, wu, wd, y, ws)
+            close(y, ref.gated_ffn(x, wg, wu, wd, ref.SILU)["y"], dt, f"{m} tokens")

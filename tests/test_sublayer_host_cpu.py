@@ -109,3 +109,13 @@ def test_layer_norm_workspace_for_wide_rows_serves_narrow_ones(zp):
     for rows in (1, 5, 100, 153, 761, 1217, 100_000):
         sizes = [zp.zero_layer_norm_workspace_bytes(rows, cols) for cols in range(0, 40_000, 7)]
         assert sizes == sorted(sizes)
+
+
+@pytest.mark.parametrize("dim,inner", [(1, 1), (8, 8), (64, 256), (1600, 6400), (1001, 2731), (1600, 6401), (13, 8)])
+def test_gated_ffn_workspace_for_many_tokens_serves_fewer(zp, dim, inner):
+    for backward in (False, True):
+        sizes = [zp.zero_gated_ffn_workspace_bytes(m, dim, inner, backward) for m in range(600)]
+        assert sizes == sorted(sizes)
+    # the backward pass's is enough for the forward
+    assert all(zp.zero_gated_ffn_workspace_bytes(m, dim, inner, True) >= zp.zero_gated_ffn_workspace_bytes(m, dim, inner)
+               for m in range(600))

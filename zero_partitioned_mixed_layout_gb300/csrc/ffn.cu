@@ -1064,8 +1064,11 @@ FfnSpace ffn_space(int64_t m, int64_t d, int64_t f, bool backward)
 {
     FfnSpace s{};
     s.mats = 256;
-    // (a few tokens' act(gate) * up stays in binary32)
-    s.mat_bytes = align256((size_t)m * (size_t)up8(f) * (!backward && m <= few_tokens(((d | f) & 7) == 0) ? 4 : 2));
+    // (a few tokens' act(gate) * up stays in binary32; the matrix of more tokens
+    // has that much room too, so that a workspace for many serves fewer)
+    const int64_t few = few_tokens(((d | f) & 7) == 0), wide = m < few ? m : few;
+    const int64_t elems = !backward && m < 2 * wide ? 2 * wide : m;
+    s.mat_bytes = align256((size_t)elems * (size_t)up8(f) * 2);
     s.copies = s.mats + (backward ? 3 : 1) * s.mat_bytes;
     s.total = s.copies;
     if (((d | f) & 7) != 0)
