@@ -692,7 +692,8 @@ int zero_layer_norm_backward(const void *dy, int64_t dy_ld, const void *x, int64
  * use, of zero_gated_ffn_workspace_bytes(tokens, dim, inner, 0) bytes (1: the
  * backward pass, which is enough for the forward as well); not shared by
  * calls that may run at the same time.  zero_workspace_stalls takes it: a
- * bounded wait that gave up leaves NaN in the call's outputs.
+ * bounded wait that gave up is counted there and leaves NaN in every output
+ * that its tiles reach.
  * Errors: ZERO_EINVAL, ZERO_EALIGN, ZERO_EDTYPE, ZERO_ESIZE (ld < cols;
  * tokens, dim or inner past 2^31 - 512), ZERO_EWORKSPACE, ZERO_ECUDA. */
 size_t zero_gated_ffn_workspace_bytes(int64_t tokens, int64_t dim, int64_t inner, int32_t backward);

@@ -1,5 +1,7 @@
 """The feed-forward sub-block on the GPU at the edges of its sizes, values and
 waits, against its formulas in binary64 (sublayer_ref.py)."""
+import ctypes
+
 import pytest
 
 torch = pytest.importorskip("torch")
@@ -131,3 +133,69 @@ def test_gated_ffn_workspace_of_the_largest_batch_serves_all(zp, dim, inner):
             y = torch.empty_like(x)
             zp.zero_gated_ffn(x, wg, wu, wd, y, ws)
             close(y, ref.gated_ffn(x, wg, wu, wd, ref.SILU)["y"], dt, f"{m} tokens")
+
+
+# ------------------------------------------------------------------ waits that run out
+
+@pytest.fixture
+def short_copies(zp):
+    """Makes the waits of one kind of product run out after a fifth of a
+    second: the copies that they wait for are asked for a little too small."""
+    so = zp.lib()
+    so.zero_test_gated_ffn_waits.argtypes = [ctypes.c_int32, ctypes.c_uint64]
+    so.zero_test_gated_ffn_waits.restype = None
+    yield lambda epilogue: so.zero_test_gated_ffn_waits(epilogue, 200_000_000)
+    so.zero_test_gated_ffn_waits(-1, 0)
+
+
+STORE, GATE, GATE_BWD = 0, 1, 2
+
+# pairs of CTAs, several tiles to each; k cut among a cluster; widths whose outputs leave without TMA
+STALLED = [(1200, 512, 2048), (40, 512, 1024), (200, 101, 203), (2100, 1001, 1501)]
+
+
+@pytest.mark.parametrize("size", STALLED, ids=str)
+def test_a_wait_that_gave_up_leaves_nan_in_the_outputs(zp, short_copies, size):
+    (m, d, f), dt = size, torch.bfloat16
+    x, wg, wu, wd = (randn(s, dt, 20 + k, std) for k, (s, std) in enumerate(
+        [((m, d), 1.0), ((f, d), d ** -0.5), ((f, d), d ** -0.5), ((d, f), f ** -0.5)]))
+    dy = randn((m, d), dt, 25)
+    ws = zp.new_gated_ffn_workspace(m, d, f, True)
+
+    def forward():
+        y, gate, up = (torch.zeros(s, dtype=dt, device="cuda") for s in ((m, d), (m, f), (m, f)))
+        zp.zero_gated_ffn(x, wg, wu, wd, y, ws, gate=gate, up=up)
+        return y, gate, up
+
+    def backward(gate, up):
+        out = [torch.zeros(s, dtype=t, device="cuda") for s, t in
+               (((m, d), dt), ((f, d), torch.float32), ((f, d), torch.float32), ((d, f), torch.float32))]
+        zp.zero_gated_ffn_backward(dy, x, wg, wu, wd, gate, up, *out, ws)
+        return out
+
+    want = forward()
+    grads = backward(*want[1:])
+    torch.cuda.synchronize()
+    assert zp.zero_workspace_stalls(ws) == 0
+
+    def stalled(kind, call):
+        before = zp.zero_workspace_stalls(ws)
+        short_copies(kind)
+        out = call()
+        torch.cuda.synchronize()
+        short_copies(-1)
+        assert zp.zero_workspace_stalls(ws) > before
+        return out
+
+    # no block of any tile's k was whole: everything that the products write is NaN
+    for t in stalled(GATE, forward):
+        assert bool(torch.isnan(t).all())
+    y, gate, up = stalled(STORE, forward)
+    assert bool(torch.isnan(y).all()) and torch.equal(gate, want[1]) and torch.equal(up, want[2])
+    for t in stalled(GATE_BWD, lambda: backward(*want[1:])):
+        assert bool(torch.isnan(t).all())
+    for t in stalled(STORE, lambda: backward(*want[1:])):
+        assert bool(torch.isnan(t).all())
+    # the workspace serves the next calls as before
+    assert all(torch.equal(a, b) for a, b in zip(forward(), want))
+    assert all(torch.equal(a, b) for a, b in zip(backward(*want[1:]), grads))

@@ -1,6 +1,8 @@
 // The gated feed-forward block, forward and backward: five products on the
 // tensor cores (tcgen05, operands by TMA, sums in tensor memory) with the
 // activation and its slope in their epilogues.
+#include <atomic>
+
 #include "sublayer.cuh"
 #include "tensor.cuh"
 
@@ -355,6 +357,33 @@ __device__ __forceinline__ void fetch_sides(const ProductArgs<NP, kGateBwd> &g, 
     __syncwarp();
 }
 
+// NaN for 32 x 32 results whose sums (or gate and up) did not arrive in time:
+// rows row0 + lane, columns from col on.  Plain stores, because a copy that is
+// still on its way may yet land in the boxes.
+template <int NP, int EPI>
+__device__ __forceinline__ void give_up32(const ProductArgs<NP, EPI> &g, const Product &p, int lane, int64_t row0,
+                                          int64_t col)
+{
+    const int64_t row = row0 + lane;
+    const int cols = p.n - col < 32 ? (int)(p.n - col) : 32;
+    if (row >= p.m)
+        return;
+    auto fill = [&](void *out, int64_t ld) {
+#pragma unroll 1
+        for (int c = 0; c < cols; ++c) {
+            if (EPI == kStore && g.out_f32)
+                static_cast<uint32_t *>(out)[row * ld + col + c] = 0x7fffffffu;
+            else
+                static_cast<uint16_t *>(out)[row * ld + col + c] = 0x7fffu;
+        }
+    };
+    fill(p.out, p.out_ld);
+    if (EPI != kStore && g.side[0].p)
+#pragma unroll 1
+        for (int k = 0; k < 2; ++k)
+            fill(g.side[EPI == kStore ? 0 : k].p, g.side[EPI == kStore ? 0 : k].ld);
+}
+
 // Where a tile lies.
 struct Tile {
     int32_t product, m, n;  // m, n: tile coordinates
@@ -605,11 +634,13 @@ __global__ void __launch_bounds__(S::THREADS, S::PER_SM) k_ffn_product(const __g
                         ok = ok && mbar_wait_bounded(&sh.in[warp * S::SETS + o.n % S::SETS], (o.n / S::SETS) & 1,
                                                      g.limit_ns, &sh.gave_up);
                         ok = __all_sync(0xffffffffu, ok);
-                        stage_get_row(o.box(0), lane, wg);
-                        stage_get_row(o.box(1), lane, wu);
+                        if (ok) {
+                            stage_get_row(o.box(0), lane, wg);
+                            stage_get_row(o.box(1), lane, wu);
+                        }
                         if (S::SETS == 1)
                             __syncwarp();
-                    } else if (!split) {
+                    } else if (!split && ok) {
                         fetch_sides<S, NP>(g, p, o, row0, col0 + c, wg, wu);
                     }
                 }
@@ -620,10 +651,8 @@ __global__ void __launch_bounds__(S::THREADS, S::PER_SM) k_ffn_product(const __g
                     tmem_wait_loads(r);
                     if (EPI == kGate)
                         tmem_wait_loads(r1);
-                } else {
-#pragma unroll
-                    for (int k = 0; k < 32; ++k)
-                        r[k] = r1[k] = 0x7fffffffu;
+                } else if (!split) {
+                    give_up32(g, p, lane, row0, col0 + c);
                 }
                 if (c + 32 >= kCols) {
                     tmem_fence_before();
@@ -632,6 +661,8 @@ __global__ void __launch_bounds__(S::THREADS, S::PER_SM) k_ffn_product(const __g
                         mbar_arrive_cluster(CG == 2 ? peer_addr(smem_addr(&sh.tempty[acc]), 0)
                                                     : smem_addr(&sh.tempty[acc]));
                 }
+                if (!ok)
+                    continue;
                 if (split) {
                     // this CTA's sums: [column][row] over the stages, which the products have read
                     float *sums = reinterpret_cast<float *>(smem) + (part * kCols + c) * 128 + quarter * 32 + lane;
@@ -644,10 +675,10 @@ __global__ void __launch_bounds__(S::THREADS, S::PER_SM) k_ffn_product(const __g
                 } else {
                     // (with one set the next is asked for when this one has left it)
                     finish32<S, DT, EPI, NP>(g, p, o, row0, col0 + c, r, r1, wg, wu, [&] {
-                        if (ok && S::SETS > 1)
+                        if (S::SETS > 1)
                             ask();
                     });
-                    if (ok && S::SETS == 1)
+                    if (S::SETS == 1)
                         ask();
                 }
             }
@@ -668,6 +699,8 @@ __global__ void __launch_bounds__(S::THREADS, S::PER_SM) k_ffn_product(const __g
         const int quarters = left >= 128 ? 4 : (int)((left + 31) / 32), blocks = quarters * (kStepN / 32);
         constexpr int kPieces = EPI == kGate ? 512 : 256;
         const int pieces = (blocks - (int)rank + g.splits - 1) / g.splits * kPieces;
+        // a CTA that gave up has left no sums
+        const uint32_t late = threadIdx.x < (unsigned)g.splits ? load_peer1(peer_addr(smem_addr(&sh.gave_up), threadIdx.x)) : 0;
 #pragma unroll 2
         for (int v = threadIdx.x; v < pieces; v += S::THREADS) {
             const int u = (int)rank + v / kPieces * g.splits, e = v % kPieces;
@@ -683,12 +716,16 @@ __global__ void __launch_bounds__(S::THREADS, S::PER_SM) k_ffn_product(const __g
                 }
             *sums = sum;
         }
-        __syncthreads();
+        const bool ok = !__syncthreads_or(late);
         if (warp < S::EPI_WARPS) {
             Outlet<S> o{reinterpret_cast<uint4 *>(out_area + warp * S::WARP_OUT), lane, 0};
             for (int u = (int)rank + warp * g.splits; u < blocks; u += S::EPI_WARPS * g.splits) {
                 const int q = u % quarters, c = u / quarters * 32;
                 const int64_t row0 = m0 + q * 32, col = (int64_t)it.n * kStepN + c;
+                if (!ok) {
+                    give_up32(g, p, lane, row0, col);
+                    continue;
+                }
                 const uint32_t *sums = reinterpret_cast<const uint32_t *>(smem) + c * 128 + q * 32 + lane;
                 uint32_t r[32], r1[32], wg[16], wu[16];
 #pragma unroll
@@ -1113,6 +1150,12 @@ int copy_operands(Mat **mats, int n, char *to, bool *copied, bool zeros, cudaStr
     return check_launch("k_ffn_copy");
 }
 
+// For tests: products whose epilogue is test_short ask for boxes of A eight
+// rows too low, so that no block of k is ever whole and their waits run out
+// after test_limit_ns.
+std::atomic<int32_t> test_short{-1};
+std::atomic<uint64_t> test_limit_ns{0};
+
 // One product of a launch.
 struct Spec {
     Mat a[2], b[2];
@@ -1160,12 +1203,14 @@ int launch_products(const Spec *specs, int n, ProductArgs<NP, EPI> &g, int split
     g.stage_bytes = g.a_rows * 128 + S::B_BYTES;
     g.stages = S::STAGES * S::STAGE / g.stage_bytes;
     g.stages = g.stages < kMaxStages ? g.stages : kMaxStages;
+    const bool fails = test_short.load(std::memory_order_relaxed) == EPI;
+    const int a_box = (a_mn ? 64 : g.a_rows) - (fails ? 8 : 0);
     int64_t tiles = 0, longest = 0;
     for (int q = 0; q < n; ++q) {
         const Spec &s = specs[q];
         Product &p = g.p[q];
         for (int i = 0; i < (gate ? 1 : s.pairs); ++i)
-            ZERO_TRY(tensor_map(&p.a[i], s.a[i].p, s.a[i].rows, s.a[i].cols, s.a[i].ld, 64, a_mn ? 64 : g.a_rows, dtype));
+            ZERO_TRY(tensor_map(&p.a[i], s.a[i].p, s.a[i].rows, s.a[i].cols, s.a[i].ld, 64, a_box, dtype));
         for (int i = 0; i < (gate ? 2 : s.pairs); ++i)
             ZERO_TRY(tensor_map(&p.b[i], s.b[i].p, s.b[i].rows, s.b[i].cols, s.b[i].ld, 64,
                                 b_mn ? 64 : gate && S::CG == 1 ? S::BN / 2 : S::B_ROWS, dtype));
@@ -1180,7 +1225,7 @@ int launch_products(const Spec *specs, int n, ProductArgs<NP, EPI> &g, int split
     if (tiles * splits > 0x3fffffff)
         return ZERO_ESIZE;
     g.tiles = (int32_t)tiles;
-    g.limit_ns = 2000000000ull + (uint64_t)longest * 4000;
+    g.limit_ns = fails ? test_limit_ns.load(std::memory_order_relaxed) : 2000000000ull + (uint64_t)longest * 4000;
     auto kernel = k_ffn_product<S, DT, EPI, MAJ, NP>;
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::SMEM);
     const int64_t workers = (int64_t)sm_count() / S::CG * S::PER_SM;
@@ -1303,6 +1348,15 @@ int tokens_forward(const void *x, int64_t x_ld, const void *wg, const void *wu, 
 }  // namespace zpml
 
 using namespace zpml;
+
+// For tests, and so not in the header: see test_short.  epilogue: 0 the
+// products that store, 1 the gate's, 2 the gate's backward; -1 none (the
+// default).
+extern "C" void zero_test_gated_ffn_waits(int32_t epilogue, uint64_t limit_ns)
+{
+    test_short = epilogue;
+    test_limit_ns = limit_ns;
+}
 
 extern "C" size_t zero_gated_ffn_workspace_bytes(int64_t tokens, int64_t dim, int64_t inner, int32_t backward)
 {

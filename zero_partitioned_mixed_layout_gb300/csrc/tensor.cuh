@@ -155,7 +155,14 @@ __device__ __forceinline__ void bulk_wait_read()
     asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
 }
 
-// Four binary32 of another CTA's shared memory (peer_addr).
+// A word, and four binary32, of another CTA's shared memory (peer_addr).
+__device__ __forceinline__ uint32_t load_peer1(uint32_t addr)
+{
+    uint32_t v;
+    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+    return v;
+}
+
 __device__ __forceinline__ float4 load_peer4(uint32_t addr)
 {
     float4 v;
