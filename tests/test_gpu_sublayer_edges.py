@@ -199,3 +199,48 @@ def test_a_wait_that_gave_up_leaves_nan_in_the_outputs(zp, short_copies, size):
     # the workspace serves the next calls as before
     assert all(torch.equal(a, b) for a, b in zip(forward(), want))
     assert all(torch.equal(a, b) for a, b in zip(backward(*want[1:]), grads))
+
+
+# ------------------------------------------------------------------ the mean
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("shape", [(3, 30), (3, 1601), (700, 1600), (2, 6001), (1300, 1608), (1300, 1000), (2500, 5000),
+                                   (2500, 8008), (5, 20001), (3, 40000)], ids=str)
+def test_layer_norm_of_equal_values_is_the_bias(zp, shape, dtype):
+    """Sums of 1000 (a multiple of 8) up to 2^27 are exact in binary32 in any
+    order, so the mean, their quotient by the width, is exact too, and nothing
+    is left for rstd (316 at this eps) to magnify."""
+    (rows, cols), dt = shape, TYPES[dtype]
+    x = torch.full(shape, 1000.0, dtype=dt, device="cuda")
+    b = randn((cols,), dt, 31)
+    for weight, bias, want in ((None, None, torch.zeros_like(x)), (b, b, b.expand(rows, cols))):
+        y, mean, rstd = torch.empty_like(x), *(torch.empty(rows, device="cuda") for _ in range(2))
+        zp.zero_layer_norm(x, weight, bias, y, mean, rstd)
+        assert bool((mean == 1000.0).all()) and torch.equal(y, want)
+        s = torch.empty_like(x)
+        zp.zero_layer_norm(x, weight, bias, y, mean, rstd, residual=torch.zeros_like(x), sum_out=s)
+        assert bool((mean == 1000.0).all()) and torch.equal(y, want) and torch.equal(s, x)
+
+
+@pytest.mark.parametrize("cols", [1, 3, 7, 10, 30, 49, 100, 257, 600, 1000, 1601, 2049, 2568, 5000, 8200, 20001])
+def test_layer_norm_mean_is_the_rounded_quotient(zp, cols):
+    """Rows of small whole numbers: their sums are exact in binary32 in any
+    order, so mean is that sum divided by cols and rounded once."""
+    rows = 2500
+    gen = torch.Generator(device="cuda").manual_seed(cols)
+    x = torch.randint(-200, 256, (rows, cols), device="cuda", generator=gen)
+    for dt in (torch.float32, torch.bfloat16):
+        t, mean = x.to(dt), torch.empty(rows, device="cuda")
+        y = torch.empty_like(t)
+        zp.zero_layer_norm(t, None, None, y, mean)
+        want = x.sum(1).float() / torch.full((rows,), float(cols), device="cuda")
+        assert torch.equal(mean, want) and torch.equal(mean, (x.sum(1).double() / cols).float())
+
+
+def test_layer_norm_mean_of_an_infinite_row(zp):
+    x = randn((4, 257), torch.float32, 33)
+    x[1, 200], x[2, 0] = float("inf"), -float("inf")
+    y, mean = torch.empty_like(x), torch.empty(4, device="cuda")
+    zp.zero_layer_norm(x, None, None, y, mean)
+    assert mean[1] == float("inf") and mean[2] == -float("inf") and bool(torch.isfinite(mean[[0, 3]]).all())
+    assert bool(torch.isnan(y[1:3]).any(1).all()) and bool(torch.isfinite(y[[0, 3]]).all())
