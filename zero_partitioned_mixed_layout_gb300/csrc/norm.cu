@@ -572,6 +572,13 @@ template <int DT, int NV, int T, bool kFused>
 __global__ void __launch_bounds__(norm_rows_threads(NV)) k_norm_fwd_rows(const __grid_constant__ NormArgs a)
 {
     constexpr int kNext = T * 32;  // groups from one of a lane's to the next
+    // No copy is under way when the block gives its memory back.  Of a row that
+    // is not there, copies are either zeros, which the end waits for, or not
+    // issued: one warp per row with the sum has no registers for the branch
+    // (8192 x 1600: 24.3 us with zeros, 24.7 without), the others none for the
+    // wait (8192 x 2560 without the sum 21.7 and 17.8, 16384 x 8192 with it 191
+    // and 179).
+    constexpr bool kZeros = kFused && T == 1;
     extern __shared__ float4 s_rows[];
     __shared__ float s_red[2][32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, team = warp / T, teams = blockDim.x / kNext;
@@ -585,6 +592,8 @@ __global__ void __launch_bounds__(norm_rows_threads(NV)) k_norm_fwd_rows(const _
     auto has = [&](int v) { return v < NV - (T == 1 ? 1 : 2) || g0 + v * kNext < groups; };
     auto fetch = [&](int64_t row, int v) {
         const bool there = row < a.rows.rows;
+        if (!kZeros && !there)
+            return;
         copy16(in + v * 32, row_ptr<DT>(a.x, row) + (g0 + v * kNext) * 16, there);
         if (kFused)
             copy16(in + (NV + v) * 32, row_ptr<DT>(a.res, row) + (g0 + v * kNext) * 16, there && a.res.p);
@@ -687,7 +696,8 @@ __global__ void __launch_bounds__(norm_rows_threads(NV)) k_norm_fwd_rows(const _
                 a.rstd[r] = rstd;
         }
     }
-    copies_done();  // (the last turn's, before the block gives its memory back)
+    if (kZeros)
+        copies_done();
 }
 
 // Forward of rows too wide for the registers of a block: three passes over
