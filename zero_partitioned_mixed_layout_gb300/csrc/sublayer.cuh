@@ -32,13 +32,8 @@ __device__ __forceinline__ void store1(void *p, int64_t i, float v)
         LowP<DT>::store(p, i, v);
 }
 
-// The same with the type known at run time only (weights and weight
-// gradients, whose type may differ from the activations').
-__device__ __forceinline__ float load1_as(int32_t dt, const void *p, int64_t i)
-{
-    return dt == ZERO_F32 ? load1<ZERO_F32>(p, i) : dt == ZERO_F16 ? load1<ZERO_F16>(p, i) : load1<ZERO_BF16>(p, i);
-}
-
+// The same with the type known at run time only (weight gradients, whose type
+// may differ from the activations').
 __device__ __forceinline__ void store1_as(int32_t dt, void *p, int64_t i, float v)
 {
     if (dt == ZERO_F32)
