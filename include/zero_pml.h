@@ -681,14 +681,19 @@ int zero_layer_norm_backward(const void *dy, int64_t dy_ld, const void *x, int64
 /* y = (act(gate) * up) w_down^T, gate = x w_gate^T, up = x w_up^T.
  * x: tokens x dim, y: tokens x dim; w_gate, w_up: inner x dim and w_down:
  * dim x inner, contiguous (out features x in features).  All of `dtype`: F16
- * or BF16, with binary32 sums; act(gate) * up is rounded to dtype once between
- * the two products (the tensor cores' operand type), but for one or two
- * tokens, whose products run without them.  gate, up (tokens x inner, contiguous): both
+ * or BF16, with binary32 sums.  gate, up (tokens x inner, contiguous): both
  * given to keep them for the backward pass, or both NULL.
+ * A few tokens (one or two; up to four where dim or inner is not a multiple
+ * of 8) go without the tensor cores: act(gate) * up stays binary32 between
+ * the two products, and the weights are read where they lie.  With more it is
+ * rounded to dtype once, the tensor cores' operand type (in F16 a product
+ * past 65504 is infinite), so a token's last bits depend on which of the two
+ * its batch takes.
  * When dim and inner are multiples of 8, x (and dy) and the weights must
- * start on 16 bytes with x_ld (dy_ld) a multiple of 8; otherwise the call
- * first copies the operands into rows of whole 16 bytes in the workspace, at
- * any alignment.  ws: device, 256-byte aligned, zero-filled before its first
+ * start on 16 bytes with x_ld (dy_ld) a multiple of 8.  Otherwise they may
+ * start anywhere, and operands off 16 bytes are first copied into rows of
+ * whole 16 bytes in the workspace (of a few tokens' forward pass, x alone and
+ * from three tokens on).  ws: device, 256-byte aligned, zero-filled before its first
  * use, of zero_gated_ffn_workspace_bytes(tokens, dim, inner, 0) bytes (1: the
  * backward pass, which is enough for the forward as well); not shared by
  * calls that may run at the same time.  zero_workspace_stalls takes it: a
@@ -706,7 +711,7 @@ int zero_gated_ffn(const void *x, int64_t x_ld, const void *w_gate, const void *
  *     dx = dgate w_gate + dup w_up
  *     dw_gate = dgate^T x,  dw_up = dup^T x,  dw_down = dy^T (act(gate) * up)
  * dgate, dup and act(gate) * up are rounded to dtype once, as operands of the
- * products that follow.  The weight gradients are of gdtype (dtype or F32).
+ * products that follow (for any number of tokens).  The weight gradients are of gdtype (dtype or F32).
  * Errors as zero_gated_ffn. */
 int zero_gated_ffn_backward(const void *dy, int64_t dy_ld, const void *x, int64_t x_ld, const void *w_gate,
                             const void *w_up, const void *w_down, const void *gate, const void *up, void *dx,

@@ -261,7 +261,13 @@ struct Outlet {
     }
 };
 
-// One warp's epilogue of 32 columns: C in `r` (kGate: the gate in `r`, up in
+// One warp's epilogue of 32 columns.  All of it is binary32; what leaves it
+// is rounded to 16 bits once: C, gate and up are outputs of that type, and
+// act(gate) * up, dgate and dup are operands of the products that follow,
+// which the tensor cores take in 16 bits only.  (Against binary64 the results
+// of two products are then off by 0.00029 in float16 and 0.0023 in bfloat16,
+// relative in norm, where one rounding at the end leaves 0.00021 and 0.0017.)
+// C in `r` (kGate: the gate in `r`, up in
 // `r1`; kGateBwd: the kept gate and up in `wg` and `wu`, the set begun),
 // rows row0 + lane, columns col .. col + 31 of the output.  `ready` runs when
 // the results are in registers.
@@ -424,9 +430,11 @@ __device__ __forceinline__ Tile tile_at(const ProductArgs<NP, EPI> &g, int32_t i
 // and the other warps empty the accumulator before it.  Large products run at
 // the tensor cores' rate under the power limit, less what the last wave and
 // tiles past the edge leave idle, and a 256 x 256 pair tile already takes all
-// of the 64 bytes per clock that an SM can be fed: 8192 tokens of 1600 x 6400
-// 315 us forward (1.60 PFLOP/s), 690 us backward (1.46; the gate's backward
-// epilogue moves five matrices), 2048 of 8192 x 32768 3.85 ms backward (1.71).
+// of the 64 bytes per clock that an SM can be fed.  Back to back, with the
+// clock that the power limit leaves: 8192 tokens of 1600 x 6400 366 us forward
+// (1.37 PFLOP/s), 743 us backward (1.35; the gate's backward epilogue moves
+// five matrices), 2048 of 8192 x 32768 4.09 ms backward (1.61); in the first
+// milliseconds, before that, 329 us, 703 us and 4.01 ms.
 // Small ones are bounded by latency: a launch of one tile per SM takes 5 us
 // beside its blocks of k (1000 clocks to start, 1500 to the first operands,
 // 2000 for an epilogue, 500 to end).  With splits = 1 the grid is
@@ -769,7 +777,7 @@ __global__ void __launch_bounds__(S::THREADS, S::PER_SM) k_ffn_product(const __g
 // stretch of k and add up in order through shared memory.  A lane multiplies
 // 16-byte pieces of the row with the tokens' pieces (which stay in L1) in
 // binary32; four pieces of each row are in flight per lane.  1600 x 6400, one
-// token: 17.3 us for both products, 3.6 TB/s of weights: each is a launch and
+// token: 17.6 us for both products, 3.5 TB/s of weights: each is a launch and
 // a few trips to memory long, so the time is latency as much as bytes.  Rows
 // that start anywhere cost two loads and a shift per piece, registers and
 // blocks with them: 1001 x 2731, one token: 9.9 us, four: 15.6 (21.7 by copies

@@ -416,8 +416,8 @@ __device__ __forceinline__ float row_mean(float sum, const NormArgs &a)
 // their weight and bias, and has the next row on its way while it works on
 // this one (four groups of binary32 leave no registers for that; of 16 bits,
 // 4096 x 16384: 73 us with it, 98 without).  One row of 1600 takes 2.3 us,
-// which is a launch and two trips to memory; 8192 x 1600 binary32 21.6
-// (4.9 TB/s), bounded by the instructions of a row's two sums and its ends.
+// which is a launch and two trips to memory; 8192 x 1600 binary32 23.0
+// (4.6 TB/s), bounded by the instructions of a row's two sums and its ends.
 template <int DT, int NV, bool kFused, bool kW, int THREADS>
 __global__ void __launch_bounds__(THREADS) k_norm_fwd(const __grid_constant__ NormArgs a)
 {
@@ -562,12 +562,12 @@ constexpr int norm_rows_threads(int nv) { return nv <= 3 ? 1024 : nv <= 4 ? 896 
 // copy of the next row is under way as soon as this row's has been read, so
 // registers hold no row ahead and an SM more rows at once.  Straight-line code
 // over the groups: 208 instructions per group with sum and mask, where
-// k_norm_fwd takes 290 and a barrier.  8192 x 1600 float16: 11.8 us (4.4 TB/s)
-// where k_norm_fwd takes 15.5; with sum and mask 23.1 (4.5 TB/s) and 31.9;
+// k_norm_fwd takes 290 and a barrier.  8192 x 1600 float16: 12.1 us (4.3 TB/s)
+// where k_norm_fwd takes 15.5; with sum and mask 24.4 (4.3 TB/s) and 31.9;
 // 16384 x 8192: 100 (5.4 TB/s) and 122.  The issue of the mask's multiplications
 // and the start and end of the launch are what is left over the copy's time.
 // Rows of binary32 stay with k_norm_fwd: staged they are twice as long, so half
-// the warps fit (8192 x 1600: 28.7 us staged, 21.6 there).
+// the warps fit (8192 x 1600: 28.7 us staged, 23.0 there).
 template <int DT, int NV, int T, bool kFused>
 __global__ void __launch_bounds__(norm_rows_threads(NV)) k_norm_fwd_rows(const __grid_constant__ NormArgs a)
 {
@@ -832,8 +832,8 @@ __device__ __forceinline__ float2 group_sum2(float2 v, float2 *s, int tpr, int g
 // block) apart; NG is a multiple of 8 when a group takes more than one row,
 // so that its rows all have the same shift.  The next row is loaded before
 // the sums of this one are exchanged; a row is held as it came (16-bit) and
-// converted again after the exchange.  3001 x 2049 binary32: 23.1 us
-// (3.2 TB/s); 8192 x 1600 binary32 with sum and mask 50 (5.2 TB/s): bounded by
+// converted again after the exchange.  3001 x 2049 binary32: 23.4 us
+// (3.2 TB/s); 8192 x 1600 binary32 with sum and mask 51 (5.1 TB/s): bounded by
 // instructions (a row's address, ends and two sums are each warp's own) and by
 // the barrier that the sums cross.
 template <int DT, int NV, bool kW, int THREADS>
@@ -971,7 +971,7 @@ constexpr int kBwdRowsThreads = 512;
 // dx, and a group's copy of the next row is under way as soon as this row's
 // has been read for dx.  T is the least that leaves four groups to a lane: with
 // one warp for seven groups the sums' registers left 11 warps to an SM (36.4 us
-// for 8192 x 1600 with sum and mask; two warps of four groups 35.4, 3.7 TB/s;
+// for 8192 x 1600 with sum and mask; two warps of four groups 36.2, 3.6 TB/s;
 // k_norm_bwd 39.6).  16384 x 1600: 61 us where k_norm_bwd takes 71; 8192 x 16384
 // 294 (5.4 TB/s) where the two passes take 580.  9 us of each call are its start,
 // its partials and their sum; the rest runs at 5.2 TB/s.
