@@ -246,3 +246,15 @@ def test_layer_norm_mean_of_an_infinite_row(zp):
     zp.zero_layer_norm(x, None, None, y, mean)
     assert mean[1] == float("inf") and mean[2] == -float("inf") and bool(torch.isfinite(mean[[0, 3]]).all())
     assert bool(torch.isnan(y[1:3]).any(1).all()) and bool(torch.isfinite(y[[0, 3]]).all())
+
+
+def test_a_dropout_moved_on_draws_the_next_mask(zp):
+    x, out = randn((40, 100), torch.float32, 41), torch.empty((40, 100), device="cuda")
+    drop = zp.Dropout(0.5, 3, 10)
+    for offset in (10, 11):
+        zp.zero_dropout_add(x, None, out, drop)
+        close(out, ref.dropout_add(x, None, (0.5, 3, offset)), torch.float32, f"offset {offset}")
+        drop.offset += 1
+    drop.d_offset = torch.tensor([88], dtype=torch.int64, device="cuda")
+    zp.zero_dropout_add(x, None, out, drop)
+    close(out, ref.dropout_add(x, None, (0.5, 3, 100)), torch.float32, "offset 100")

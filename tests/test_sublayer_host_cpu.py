@@ -6,6 +6,7 @@ import subprocess
 import sys
 
 import pytest
+import torch
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
@@ -119,3 +120,16 @@ def test_gated_ffn_workspace_for_many_tokens_serves_fewer(zp, dim, inner):
     # the backward pass's is enough for the forward
     assert all(zp.zero_gated_ffn_workspace_bytes(m, dim, inner, True) >= zp.zero_gated_ffn_workspace_bytes(m, dim, inner)
                for m in range(600))
+
+
+def test_a_dropout_draws_from_what_its_fields_are_at_the_call(zp):
+    """The struct that a call gets follows the fields, as a new step sets them."""
+    d = zp.Dropout(0.25, 5, 7)
+    assert (d.p, d.seed, d.offset, d.d_offset) == (0.25, 5, 7, None)
+    d.offset += 1
+    d.p, d.seed = 0.5, -1
+    c = zp.binding._drop_ref(d)._obj
+    assert (c.p, c.seed, c.offset, c.d_offset) == (0.5, 2 ** 64 - 1, 8, None)
+    with pytest.raises(ValueError):
+        d.d_offset = torch.zeros(1, dtype=torch.int64)
+    assert d.d_offset is None and zp.Dropout(0.1, 2 ** 64 + 3, -2)._c.offset == 2 ** 64 - 2

@@ -676,16 +676,48 @@ class _Dropout(ctypes.Structure):
 class Dropout:
     """zero_dropout_t: which elements a dropout keeps.  d_offset: a device
     int64 tensor of one element added to offset when the kernel runs (None:
-    nothing added)."""
+    nothing added).  p, seed, offset and d_offset may be set anew between
+    calls: a call draws from what they are then."""
 
     def __init__(self, p: float, seed: int, offset: int = 0, d_offset=None):
+        self._c = _Dropout()
+        self.p, self.seed, self.offset, self.d_offset = p, seed, offset, d_offset
+
+    @property
+    def p(self) -> float:
+        return self._c.p
+
+    @p.setter
+    def p(self, p):
+        self._c.p = float(p)
+
+    @property
+    def seed(self) -> int:
+        return self._c.seed
+
+    @seed.setter
+    def seed(self, seed):
+        self._c.seed = int(seed) & (1 << 64) - 1
+
+    @property
+    def offset(self) -> int:
+        return self._c.offset
+
+    @offset.setter
+    def offset(self, offset):
+        self._c.offset = int(offset) & (1 << 64) - 1
+
+    @property
+    def d_offset(self):
+        return self._d_offset
+
+    @d_offset.setter
+    def d_offset(self, t):
         import torch
-        if d_offset is not None and (not d_offset.is_cuda or d_offset.dtype != torch.int64 or d_offset.numel() != 1):
+        if t is not None and (not t.is_cuda or t.dtype != torch.int64 or t.numel() != 1):
             raise ValueError("d_offset must be a CUDA int64 tensor of one element")
-        self.p, self.seed, self.offset, self.d_offset = float(p), int(seed), int(offset), d_offset
-        mask = (1 << 64) - 1
-        self._c = _Dropout(self.p, self.seed & mask, self.offset & mask,
-                           None if d_offset is None else d_offset.data_ptr())
+        self._d_offset = t
+        self._c.d_offset = None if t is None else t.data_ptr()
 
 
 _sublayer = None
