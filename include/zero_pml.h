@@ -719,6 +719,144 @@ int zero_gated_ffn_backward(const void *dy, int64_t dy_ld, const void *x, int64_
                             int64_t dim, int64_t inner, int32_t act, int32_t dtype, void *ws, size_t ws_bytes,
                             void *stream);
 
+/* ------------------------------------------------------------------ attention sub-block */
+
+/* The operators of the attention half of the same layer, forward and
+ * backward, between the projections that make queries, keys and values and
+ * the one that takes the output:
+ *
+ *     q, k = rotation(norm(q)), rotation(norm(k))      zero_qk_norm
+ *     o = attention(q, k, v) in a sliding window       zero_window_attention
+ *
+ * The conventions are the feed-forward sub-block's, with arrays of heads in
+ * place of matrices: tokens x heads x head_dim, the elements of a head
+ * contiguous, from one token to the next `ld` elements and from one head to
+ * the next `hd` (both at least 0, or any value where there is one token, or
+ * one head).  So q, k and v can be slices of one projection's output, in
+ * either order of its axes.  Rows of an output must not overlap. */
+
+/* The rotation of the first rot_dim elements of a head (rot_dim even, 0 for
+ * none): pair i, of elements i and i + rot_dim / 2, or 2 i and 2 i + 1 when
+ * interleaved, is turned by the angle positions[token] * inv_freq[i]:
+ *     (a, b) -> (a cos - b sin, b cos + a sin).
+ * `turns` holds the frequencies as zero_rotary_turns gives them: turns per
+ * position modulo 1, in units of 2^-64.  A position's angle is then an
+ * integer product modulo 2^64, as exact at position 10^9 as at 1. */
+typedef struct zero_rotary {
+    const uint64_t *turns; /* device, rot_dim / 2 of them */
+    int32_t rot_dim;
+    int32_t interleaved;
+} zero_rotary_t;
+
+/* Host to host: turns[i] = inv_freq[i] / (2 pi) modulo 1, times 2^64.
+ * Errors: ZERO_EINVAL (NULL, n < 0, a frequency that is NaN or past 2^20 either way). */
+int zero_rotary_turns(const double *inv_freq, int64_t n, uint64_t *turns);
+
+/* For every token and head x of q (of k):
+ *     z = x / sqrt(mean(x^2) + eps) * q_weight (k_weight);   out = rotation(z).
+ * Weights: head_dim elements of wdtype (dtype or F32) that all heads share,
+ * either may be NULL (1).  rotary NULL: no rotation.  positions: tokens
+ * int64, any sign; NULL: token i is at position i.  q_out may be q itself
+ * (same ld and hd), k_out k.  k_heads may be 0.  dtype: F16, BF16 or F32;
+ * everything between the loads and the one rounding at the end is binary32.
+ * Limits: tokens < 2^31, q_heads + k_heads <= 2^20, head_dim <= 256.
+ * Errors: ZERO_EINVAL (NULL, a negative size or stride, eps < 0), ZERO_EALIGN,
+ * ZERO_EDTYPE, ZERO_ESIZE (limits; rot_dim odd, negative or past head_dim),
+ * ZERO_ECUDA. */
+int zero_qk_norm(const void *q, int64_t q_ld, int64_t q_hd, const void *k, int64_t k_ld, int64_t k_hd,
+                 const void *q_weight, const void *k_weight, int32_t wdtype, const zero_rotary_t *rotary,
+                 const int64_t *positions, void *q_out, int64_t q_out_ld, int64_t q_out_hd, void *k_out,
+                 int64_t k_out_ld, int64_t k_out_hd, int64_t tokens, int64_t q_heads, int64_t k_heads,
+                 int64_t head_dim, double eps, int32_t dtype, void *stream);
+
+/* The backward pass, from q and k as they were before the norm and the
+ * gradients dq_out, dk_out of its outputs.  Per row, with r = 1 / sqrt(mean(x^2)
+ * + eps), xh = x r, dz = dout turned back and g = dz weight:
+ *     dx = r (g - xh mean(g xh)),     dweight = sum over tokens and heads of dz xh.
+ * dq may be dq_out or q itself (same ld and hd), dk likewise.  dq_weight,
+ * dk_weight: head_dim elements of gdtype (dtype or F32), either may be NULL;
+ * their sums are taken in a fixed order (the same bits on every run).  ws:
+ * device, 256-byte aligned, zero-filled before its first use, ws_bytes >=
+ * zero_qk_norm_workspace_bytes(tokens, q_heads, k_heads, head_dim); not shared
+ * by calls that may run at the same time.  Errors: as zero_qk_norm, plus
+ * ZERO_EWORKSPACE. */
+size_t zero_qk_norm_workspace_bytes(int64_t tokens, int64_t q_heads, int64_t k_heads, int64_t head_dim);
+int zero_qk_norm_backward(const void *dq_out, int64_t dq_out_ld, int64_t dq_out_hd, const void *dk_out,
+                          int64_t dk_out_ld, int64_t dk_out_hd, const void *q, int64_t q_ld, int64_t q_hd,
+                          const void *k, int64_t k_ld, int64_t k_hd, const void *q_weight, const void *k_weight,
+                          int32_t wdtype, const zero_rotary_t *rotary, const int64_t *positions, void *dq,
+                          int64_t dq_ld, int64_t dq_hd, void *dk, int64_t dk_ld, int64_t dk_hd, void *dq_weight,
+                          void *dk_weight, int32_t gdtype, int64_t tokens, int64_t q_heads, int64_t k_heads,
+                          int64_t head_dim, double eps, int32_t dtype, void *ws, size_t ws_bytes, void *stream);
+
+/* What an attention call works on: `sequences` sequences packed along the
+ * tokens of q and of k and v.  The queries of sequence s are the q_tokens
+ * rows from q_offsets[s] to q_offsets[s + 1]; its keys start at k_offsets[s]
+ * and are k_lengths[s] of them, at most those up to k_offsets[s + 1]
+ * (k_lengths NULL: all of those).  A padded cache of room R is k_offsets =
+ * 0, R, 2R, ... with the lengths.  The arrays are read on the device, when
+ * the kernels run (a captured call follows what they hold at each replay),
+ * and are cut to 0 .. q_tokens (k_tokens): offsets that fall give results
+ * that mean nothing, but touch no other memory.  q_offsets NULL: one sequence
+ * of all rows (sequences 1); k_offsets NULL: q_offsets (k_tokens = q_tokens).
+ *
+ * With Lq queries and Lk keys, query i stands at key p = i + Lk - Lq (the last
+ * query at the last key) and sees key j iff
+ *     0 <= j <= p  and  (j > p - window  or  j < sinks).
+ * A key that is not seen has no influence, whatever the keys and values
+ * beside the sequence's own hold (NaN included). */
+typedef struct zero_attention {
+    int64_t q_tokens, k_tokens, sequences;
+    int32_t q_heads, k_heads; /* q_heads a multiple of k_heads: query head h reads key head h / (q_heads / k_heads) */
+    int32_t head_dim;         /* a multiple of 8, at most 128 */
+    int32_t dtype;            /* ZERO_F16 or ZERO_BF16, of every array but lse */
+    int64_t window;           /* at least 1; INT64_MAX: no window */
+    int64_t sinks;            /* first keys that every later query sees; at least 0 */
+    double scale;             /* of q.k: positive, finite */
+    const int64_t *q_offsets, *k_offsets, *k_lengths;
+} zero_attention_t;
+
+/* out = softmax(scale q k^T over the keys seen) v, and lse (q_heads x
+ * q_tokens, contiguous, binary32; may be NULL) = log sum exp(scale q.k) over
+ * them, for the backward pass.  A query that sees no key gives 0, and lse
+ * -inf.  Rows of out and lse outside every sequence are left as they were.
+ * Scores, their maximum and sum, and the output's sums are binary32; the
+ * softmax's numerators are rounded to dtype once, as operands of the tensor
+ * cores.
+ * All arrays start on 16 bytes, with ld and hd multiples of 8 elements.
+ * ws: device, 256-byte aligned, zero-filled before its first use, of
+ * zero_window_attention_workspace_bytes(a, 0) bytes (1: the backward pass,
+ * which is enough for the forward as well; the arrays of `a` are not read);
+ * not shared by calls that may run at the same time.  zero_workspace_stalls
+ * takes it: a bounded wait that gave up is counted there and leaves NaN in
+ * what it would have written.
+ * Errors: ZERO_EINVAL (NULL, a negative size, window < 1, sinks < 0, scale not
+ * positive or not finite, k_lengths without k_offsets, sequences not 1
+ * without q_offsets), ZERO_EALIGN, ZERO_EDTYPE, ZERO_ESIZE (head_dim; heads
+ * that do not divide or past 2^15; q_tokens, k_tokens or sequences past 2^31 -
+ * 512; k_tokens not q_tokens without k_offsets; strides past 2^38),
+ * ZERO_EWORKSPACE, ZERO_ECUDA. */
+size_t zero_window_attention_workspace_bytes(const zero_attention_t *a, int32_t backward);
+int zero_window_attention(const zero_attention_t *a, const void *q, int64_t q_ld, int64_t q_hd, const void *k,
+                          int64_t k_ld, int64_t k_hd, const void *v, int64_t v_ld, int64_t v_hd, void *out,
+                          int64_t out_ld, int64_t out_hd, float *lse, void *ws, size_t ws_bytes, void *stream);
+
+/* The backward pass, from q, k, v and the out and lse of the forward call:
+ *     delta_i = dout_i . out_i,  P_ij = exp(scale q_i.k_j - lse_i),
+ *     dS_ij = P_ij (dout_i.v_j - delta_i),
+ *     dq_i = scale sum_j dS_ij k_j,  dk_j = scale sum_i dS_ij q_i,  dv_j = sum_i P_ij dout_i
+ * (dk and dv summed over the query heads of a key head).  P and dS are
+ * rounded to dtype once, as operands; all sums are binary32 and taken in a
+ * fixed order (the same bits on every run).  A key of a sequence that no query
+ * sees gets zeros; rows outside every sequence are left as they were.  Errors
+ * as zero_window_attention. */
+int zero_window_attention_backward(const zero_attention_t *a, const void *dout, int64_t dout_ld, int64_t dout_hd,
+                                   const void *q, int64_t q_ld, int64_t q_hd, const void *k, int64_t k_ld,
+                                   int64_t k_hd, const void *v, int64_t v_ld, int64_t v_hd, const void *out,
+                                   int64_t out_ld, int64_t out_hd, const float *lse, void *dq, int64_t dq_ld,
+                                   int64_t dq_hd, void *dk, int64_t dk_ld, int64_t dk_hd, void *dv, int64_t dv_ld,
+                                   int64_t dv_hd, void *ws, size_t ws_bytes, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -8,8 +8,10 @@ the stage-2 gradient reduction fused with the norm pass, the stage-3
 parameter gather (shards back to tensors) with its per-layer plan, the
 offload step on the host cores, and 1-bit Adam's compression stage.  Beside
 the step: the feed-forward half of a pre-norm transformer layer (dropout with
-the residual sum, layer norm, the gated feed-forward), forward and backward,
-which makes gradients the step reads from the parameters it writes.  The C ABI is in
+the residual sum, layer norm, the gated feed-forward) and the attention half
+(norms of queries and keys with the rotation, attention in a sliding window),
+forward and backward, which make gradients the step reads from the parameters
+it writes.  The C ABI is in
 ``include/zero_pml.h``; this package is its Python binding.
 """
 from .binding import (  # noqa: F401
@@ -66,4 +68,14 @@ from .binding import (  # noqa: F401
     zero_layer_norm,
     zero_layer_norm_backward,
     zero_layer_norm_workspace_bytes,
+    Rotary,
+    new_qk_norm_workspace,
+    new_window_attention_workspace,
+    zero_qk_norm,
+    zero_qk_norm_backward,
+    zero_qk_norm_workspace_bytes,
+    zero_rotary_turns,
+    zero_window_attention,
+    zero_window_attention_backward,
+    zero_window_attention_workspace_bytes,
 )

@@ -962,6 +962,284 @@ def zero_gated_ffn_backward(dy, x, w_gate, w_up, w_down, gate, up, dx, dw_gate, 
     _check(rc, "zero_gated_ffn_backward")
 
 
+# ------------------------------------------------------------------ attention sub-block
+
+class _Rotary(ctypes.Structure):
+    _fields_ = [("turns", ctypes.c_void_p), ("rot_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32)]
+
+
+class _Attention(ctypes.Structure):
+    _fields_ = [("q_tokens", ctypes.c_int64), ("k_tokens", ctypes.c_int64), ("sequences", ctypes.c_int64),
+                ("q_heads", ctypes.c_int32), ("k_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("dtype", ctypes.c_int32), ("window", ctypes.c_int64), ("sinks", ctypes.c_int64),
+                ("scale", ctypes.c_double), ("q_offsets", ctypes.c_void_p), ("k_offsets", ctypes.c_void_p),
+                ("k_lengths", ctypes.c_void_p)]
+
+
+_attention = None
+
+
+def _attention_lib():
+    global _attention
+    if _attention is None:
+        so = lib()
+        vp, i64, i32, sz, dbl = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_size_t, ctypes.c_double
+        rp, ap, heads = ctypes.POINTER(_Rotary), ctypes.POINTER(_Attention), [vp, i64, i64]
+        so.zero_rotary_turns.argtypes = [ctypes.POINTER(dbl), i64, ctypes.POINTER(ctypes.c_uint64)]
+        so.zero_qk_norm.argtypes = heads * 2 + [vp, vp, i32, rp, vp] + heads * 2 + [i64] * 4 + [dbl, i32, vp]
+        so.zero_qk_norm_workspace_bytes.argtypes = [i64] * 4
+        so.zero_qk_norm_backward.argtypes = heads * 4 + [vp, vp, i32, rp, vp] + heads * 2 + [vp, vp, i32] + [i64] * 4 + [
+            dbl, i32, vp, sz, vp]
+        so.zero_window_attention_workspace_bytes.argtypes = [ap, i32]
+        so.zero_window_attention.argtypes = [ap] + heads * 4 + [vp, vp, sz, vp]
+        so.zero_window_attention_backward.argtypes = [ap] + heads * 5 + [vp] + heads * 3 + [vp, sz, vp]
+        for f in ("zero_rotary_turns", "zero_qk_norm", "zero_qk_norm_backward", "zero_window_attention",
+                  "zero_window_attention_backward"):
+            getattr(so, f).restype = ctypes.c_int
+        for f in ("zero_qk_norm_workspace_bytes", "zero_window_attention_workspace_bytes"):
+            getattr(so, f).restype = sz
+        _attention = so
+    return _attention
+
+
+def _call_on(device: int, f, *args):
+    """f(*args) with `device` as the current one (kernels are launched there)."""
+    import torch
+    if torch.cuda.current_device() == device:
+        return f(*args)
+    with torch.cuda.device(device):
+        return f(*args)
+
+
+def _on(t, what: str, device: int):
+    if not t.is_cuda:
+        raise ValueError(f"{what} must be a CUDA tensor")
+    if t.get_device() != device:
+        raise ValueError(f"{what} must be on the device of the queries")
+    return t
+
+
+def _heads(t, what: str, shape, dtype, device: int, written: bool = False):
+    """(pointer, token stride, head stride) of a tokens x heads x head_dim
+    CUDA tensor whose heads' elements are contiguous."""
+    if t.shape != shape:
+        raise ValueError(f"{what} must be {' x '.join(map(str, shape))}")
+    if t.dtype != dtype:
+        raise TypeError(f"{what} must be {dtype}")
+    _on(t, what, device)
+    ld, hd, inner = t.stride()
+    if shape[2] > 1 and inner != 1:
+        raise ValueError(f"{what}: the elements of a head must be contiguous")
+    if written and ((ld == 0 and shape[0] > 1) or (hd == 0 and shape[1] > 1)):
+        raise ValueError(f"{what}: rows of an output must not overlap")
+    return t.data_ptr(), ld, hd
+
+
+def _heads_shape(t, what: str):
+    shape = t.shape
+    if len(shape) != 3:
+        raise ValueError(f"{what} must have three dimensions: tokens, heads, elements of a head")
+    return shape
+
+
+def zero_rotary_turns(inv_freq):
+    """The frequencies of a rotation as numpy uint64: turns per position
+    modulo 1, in units of 2^-64."""
+    f = np.ascontiguousarray(inv_freq, dtype=np.float64)
+    out = np.empty(f.size, dtype=np.uint64)
+    rc = _attention_lib().zero_rotary_turns(f.ctypes.data_as(ctypes.POINTER(ctypes.c_double)), f.size,
+                                            out.ctypes.data_as(ctypes.POINTER(ctypes.c_uint64)))
+    _check(rc, "zero_rotary_turns")
+    return out
+
+
+class Rotary:
+    """zero_rotary_t: the rotation of the first 2 * len(inv_freq) elements of
+    a head, by position * inv_freq[i] radians for pair i (elements i and
+    i + len(inv_freq), or 2 i and 2 i + 1 when interleaved)."""
+
+    def __init__(self, inv_freq, interleaved: bool = False, device="cuda"):
+        import torch
+        self.turns = torch.from_numpy(zero_rotary_turns(inv_freq).view(np.int64)).to(device)
+        self._c = _Rotary(self.turns.data_ptr(), 2 * self.turns.numel(), int(bool(interleaved)))
+
+    @property
+    def rot_dim(self) -> int:
+        return self._c.rot_dim
+
+    @property
+    def interleaved(self) -> bool:
+        return bool(self._c.interleaved)
+
+
+def _int64_pointer(t, what: str, n: int, device: int):
+    import torch
+    if t is None:
+        return None
+    if t.dtype != torch.int64:
+        raise TypeError(f"{what} must be int64")
+    _on(t, what, device)
+    return _vector(t, what, n)
+
+
+def _rotary_args(rotary, positions, tokens: int, device: int):
+    if rotary is None:
+        if positions is not None:
+            raise ValueError("positions are given without a rotary")
+        return None, None
+    _on(rotary.turns, "rotary", device)
+    return ctypes.byref(rotary._c), _int64_pointer(positions, "positions", tokens, device)
+
+
+def _head_weight(w, what: str, dim: int, device: int):
+    return None if w is None else _vector(_on(w, what, device), what, dim)
+
+
+def zero_qk_norm(q, k, q_weight, k_weight, q_out, k_out, rotary=None, positions=None, eps: float = 1e-6,
+                 stream=None) -> None:
+    """q_out = rotation(x / sqrt(mean(x^2) + eps) * q_weight) of every row x of
+    q ([tokens, q heads, head_dim]), and so for k.  rotary: a Rotary, or None;
+    positions: int64[tokens], or None for 0, 1, 2, ...; a weight may be None.
+    q_out may be q itself, k_out k."""
+    shape, dtype, code, dev = _heads_shape(q, "q"), q.dtype, _type_code(q), q.get_device()
+    kshape = _heads_shape(k, "k")
+    if kshape[0] != shape[0] or kshape[2] != shape[2]:
+        raise ValueError("k must have the tokens and the head dimension of q")
+    qs = _heads(q, "q", shape, dtype, dev)
+    ks = _heads(k, "k", kshape, dtype, dev)
+    qo = _heads(q_out, "q_out", shape, dtype, dev, True)
+    ko = _heads(k_out, "k_out", kshape, dtype, dev, True)
+    qw, kw = _head_weight(q_weight, "q_weight", shape[2], dev), _head_weight(k_weight, "k_weight", shape[2], dev)
+    ro, pos = _rotary_args(rotary, positions, shape[0], dev)
+    rc = _call_on(dev, _attention_lib().zero_qk_norm, *qs, *ks, qw, kw,
+                  _pair_code(q_weight, k_weight, "q_weight and k_weight", code), ro, pos, *qo, *ko, shape[0], shape[1],
+                  kshape[1], shape[2], eps, code, _stream_handle(stream, q))
+    _check(rc, "zero_qk_norm")
+
+
+def zero_qk_norm_workspace_bytes(tokens: int, q_heads: int, k_heads: int, head_dim: int) -> int:
+    return int(_attention_lib().zero_qk_norm_workspace_bytes(int(tokens), int(q_heads), int(k_heads), int(head_dim)))
+
+
+def new_qk_norm_workspace(tokens: int, q_heads: int, k_heads: int, head_dim: int, device="cuda"):
+    """A zero-filled workspace for zero_qk_norm_backward."""
+    import torch
+    return torch.zeros(zero_qk_norm_workspace_bytes(tokens, q_heads, k_heads, head_dim), dtype=torch.uint8,
+                       device=device)
+
+
+def zero_qk_norm_backward(dq_out, dk_out, q, k, q_weight, k_weight, dq, dk, dq_weight, dk_weight, ws, rotary=None,
+                          positions=None, eps: float = 1e-6, stream=None) -> None:
+    """The gradients of zero_qk_norm from q and k as they went in: dq, dk (each
+    may be the gradient or the input itself) and the weights' dq_weight,
+    dk_weight (q's type or float32; either may be None)."""
+    shape, dtype, code, dev = _heads_shape(q, "q"), q.dtype, _type_code(q), q.get_device()
+    kshape = _heads_shape(k, "k")
+    if kshape[0] != shape[0] or kshape[2] != shape[2]:
+        raise ValueError("k must have the tokens and the head dimension of q")
+    gq = _heads(dq_out, "dq_out", shape, dtype, dev)
+    gk = _heads(dk_out, "dk_out", kshape, dtype, dev)
+    qs = _heads(q, "q", shape, dtype, dev)
+    ks = _heads(k, "k", kshape, dtype, dev)
+    qo = _heads(dq, "dq", shape, dtype, dev, True)
+    ko = _heads(dk, "dk", kshape, dtype, dev, True)
+    qw, kw = _head_weight(q_weight, "q_weight", shape[2], dev), _head_weight(k_weight, "k_weight", shape[2], dev)
+    dqw, dkw = _head_weight(dq_weight, "dq_weight", shape[2], dev), _head_weight(dk_weight, "dk_weight", shape[2], dev)
+    ro, pos = _rotary_args(rotary, positions, shape[0], dev)
+    _device_tensor(_on(ws, "workspace", dev), "workspace")
+    rc = _call_on(dev, _attention_lib().zero_qk_norm_backward, *gq, *gk, *qs, *ks, qw, kw,
+                  _pair_code(q_weight, k_weight, "q_weight and k_weight", code), ro, pos, *qo, *ko, dqw, dkw,
+                  _pair_code(dq_weight, dk_weight, "dq_weight and dk_weight", code), shape[0], shape[1], kshape[1],
+                  shape[2], eps, code, ws.data_ptr(), ws.numel(), _stream_handle(stream, q))
+    _check(rc, "zero_qk_norm_backward")
+
+
+_NO_WINDOW = (1 << 63) - 1
+
+
+def _attention_sizes(q_tokens, k_tokens, sequences, q_heads, k_heads, head_dim, code, window, sinks, scale):
+    if window is None:
+        window = _NO_WINDOW
+    if scale is None:
+        scale = head_dim ** -0.5 if head_dim > 0 else 1.0
+    return _Attention(q_tokens, k_tokens, sequences, q_heads, k_heads, head_dim, code, min(window, _NO_WINDOW),
+                      min(sinks, _NO_WINDOW), scale)
+
+
+def _attention_struct(q, k, window, sinks, scale, q_offsets, k_offsets, k_lengths, dev):
+    tq, hq, d = _heads_shape(q, "q")
+    tk, hk, dk = _heads_shape(k, "k")
+    if dk != d:
+        raise ValueError("k must have the head dimension of q")
+    n = 1 if q_offsets is None else q_offsets.numel() - 1
+    if n < 0:
+        raise ValueError("q_offsets must hold one more than the number of sequences")
+    a = _attention_sizes(tq, tk, n, hq, hk, d, _type_code(q), window, sinks, scale)
+    a.q_offsets = _int64_pointer(q_offsets, "q_offsets", n + 1, dev)
+    a.k_offsets = _int64_pointer(k_offsets, "k_offsets", n + 1, dev)
+    a.k_lengths = _int64_pointer(k_lengths, "k_lengths", n, dev)
+    return a
+
+
+def zero_window_attention_workspace_bytes(q_tokens: int, k_tokens: int, sequences: int, q_heads: int, k_heads: int,
+                                          head_dim: int, window=None, sinks: int = 0, backward: bool = False) -> int:
+    a = _attention_sizes(int(q_tokens), int(k_tokens), int(sequences), int(q_heads), int(k_heads), int(head_dim),
+                         ZERO_F16, window, sinks, None)
+    return int(_attention_lib().zero_window_attention_workspace_bytes(ctypes.byref(a), int(bool(backward))))
+
+
+def new_window_attention_workspace(q_tokens: int, k_tokens: int, sequences: int, q_heads: int, k_heads: int,
+                                   head_dim: int, window=None, sinks: int = 0, backward: bool = False, device="cuda"):
+    """A zero-filled workspace for zero_window_attention (backward=True: and
+    for zero_window_attention_backward) at these sizes."""
+    import torch
+    return torch.zeros(zero_window_attention_workspace_bytes(q_tokens, k_tokens, sequences, q_heads, k_heads, head_dim,
+                                                             window, sinks, backward), dtype=torch.uint8, device=device)
+
+
+def zero_window_attention(q, k, v, out, ws, window=None, sinks: int = 0, scale=None, lse=None, q_offsets=None,
+                          k_offsets=None, k_lengths=None, stream=None) -> None:
+    """out = softmax(scale q k^T) v over the keys that each query sees: those
+    up to its own, within `window` of it (None: all) or among the first
+    `sinks`.  q, out: [q tokens, q heads, head_dim], k, v: [k tokens, k heads,
+    head_dim]; sequences packed along the tokens by q_offsets and k_offsets
+    (int64[sequences + 1] on the device; None: one sequence, and k's as q's),
+    with k_lengths of the keys filled (int64[sequences]; None: all); the last
+    query of a sequence stands at its last key.  lse: float32[q heads, q
+    tokens] for the backward pass.  scale None: head_dim ** -0.5."""
+    dtype, dev = q.dtype, q.get_device()
+    a = _attention_struct(q, k, window, sinks, scale, q_offsets, k_offsets, k_lengths, dev)
+    qs = _heads(q, "q", q.shape, dtype, dev)
+    ks = _heads(k, "k", k.shape, dtype, dev)
+    vs = _heads(v, "v", k.shape, dtype, dev)
+    os_ = _heads(out, "out", q.shape, dtype, dev, True)
+    lp = None if lse is None else _f32_pointer(_on(lse, "lse", dev), "lse", a.q_heads * a.q_tokens)
+    _device_tensor(_on(ws, "workspace", dev), "workspace")
+    rc = _call_on(dev, _attention_lib().zero_window_attention, ctypes.byref(a), *qs, *ks, *vs, *os_, lp, ws.data_ptr(),
+                  ws.numel(), _stream_handle(stream, q))
+    _check(rc, "zero_window_attention")
+
+
+def zero_window_attention_backward(dout, q, k, v, out, lse, dq, dk, dv, ws, window=None, sinks: int = 0, scale=None,
+                                   q_offsets=None, k_offsets=None, k_lengths=None, stream=None) -> None:
+    """The gradients of zero_window_attention from its inputs, out and lse."""
+    dtype, dev = q.dtype, q.get_device()
+    a = _attention_struct(q, k, window, sinks, scale, q_offsets, k_offsets, k_lengths, dev)
+    go = _heads(dout, "dout", q.shape, dtype, dev)
+    qs = _heads(q, "q", q.shape, dtype, dev)
+    ks = _heads(k, "k", k.shape, dtype, dev)
+    vs = _heads(v, "v", k.shape, dtype, dev)
+    os_ = _heads(out, "out", q.shape, dtype, dev)
+    lp = _f32_pointer(_on(lse, "lse", dev), "lse", a.q_heads * a.q_tokens)
+    gq = _heads(dq, "dq", q.shape, dtype, dev, True)
+    gk = _heads(dk, "dk", k.shape, dtype, dev, True)
+    gv = _heads(dv, "dv", k.shape, dtype, dev, True)
+    _device_tensor(_on(ws, "workspace", dev), "workspace")
+    rc = _call_on(dev, _attention_lib().zero_window_attention_backward, ctypes.byref(a), *go, *qs, *ks, *vs, *os_, lp,
+                  *gq, *gk, *gv, ws.data_ptr(), ws.numel(), _stream_handle(stream, q))
+    _check(rc, "zero_window_attention_backward")
+
+
 # ------------------------------------------------------------------ offload (host)
 
 class OffloadScalars(ctypes.Structure):

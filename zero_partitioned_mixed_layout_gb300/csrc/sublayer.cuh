@@ -1,6 +1,6 @@
-// Pieces shared by the feed-forward sub-block's translation units
-// (norm.cu, ffn.cu): element access at any alignment and the argument
-// checks of row-strided matrices.
+// Pieces shared by the sub-blocks' translation units (norm.cu, ffn.cu;
+// qk_norm.cu, attention.cu): element access at any alignment and the argument
+// checks of row-strided matrices and of arrays of heads.
 #pragma once
 
 #include "common.cuh"
@@ -89,6 +89,31 @@ inline int check_matrix(const void *p, int64_t ld, int64_t rows, int64_t cols, i
     if (ld < cols || ld > ((int64_t)1 << 60) / rows)
         return ZERO_ESIZE;
     return check_array(p, 1, dt);
+}
+
+// An array of heads: tokens x heads x head_dim, the elements of a head
+// contiguous.
+struct Heads {
+    const void *p;
+    int64_t ld, hd;  // elements from a token, from a head, to the next
+};
+
+// Checks of one; the strides that no two rows need become 0.
+inline int check_heads(Heads *a, int64_t tokens, int64_t heads, int64_t dim, int32_t dt)
+{
+    if (tokens == 0 || heads == 0 || dim == 0)
+        return ZERO_OK;
+    if (tokens == 1)
+        a->ld = 0;
+    if (heads == 1)
+        a->hd = 0;
+    if (a->ld < 0 || a->hd < 0)
+        return ZERO_EINVAL;
+    // offsets stay below 2^61, and a tensor map's strides below 2^40 bytes
+    const int64_t most = (int64_t)1 << 38, all = (int64_t)1 << 60;
+    if (a->ld >= most || a->hd >= most || a->ld > all / tokens || a->hd > all / heads)
+        return ZERO_ESIZE;
+    return check_array(a->p, 1, dt);
 }
 
 inline int check_workspace(const void *ws, size_t ws_bytes, size_t need)
