@@ -823,14 +823,15 @@ typedef struct zero_attention {
  * Scores, their maximum and sum, and the output's sums are binary32; the
  * softmax's numerators are rounded to dtype once, as operands of the tensor
  * cores.
- * All arrays start on 16 bytes, with ld and hd multiples of 8 elements.
+ * All arrays start on 16 bytes, with ld and hd positive multiples of 8
+ * elements (where there is more than one token, or head).
  * ws: device, 256-byte aligned, zero-filled before its first use, of
  * zero_window_attention_workspace_bytes(a, 0) bytes (1: the backward pass,
  * which is enough for the forward as well; the arrays of `a` are not read);
  * not shared by calls that may run at the same time.  zero_workspace_stalls
  * takes it: a bounded wait that gave up is counted there and leaves NaN in
  * what it would have written.
- * Errors: ZERO_EINVAL (NULL, a negative size, window < 1, sinks < 0, scale not
+ * Errors: ZERO_EINVAL (NULL, a negative size, a stride that is not positive, window < 1, sinks < 0, scale not
  * positive or not finite, k_lengths without k_offsets, sequences not 1
  * without q_offsets), ZERO_EALIGN, ZERO_EDTYPE, ZERO_ESIZE (head_dim; heads
  * that do not divide or past 2^15; q_tokens, k_tokens or sequences past 2^31 -

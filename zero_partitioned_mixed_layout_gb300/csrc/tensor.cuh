@@ -134,6 +134,17 @@ __device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap *map, i
             : "memory");
 }
 
+// The same of a map of three dimensions.
+__device__ __forceinline__ void tma_load3(uint32_t dst, const CUtensorMap *map, int32_t x, int32_t y, int32_t z,
+                                          uint32_t bar)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+        "[%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
+        : "memory");
+}
+
 // A box from shared memory to `map` at (x, y); what lies outside the matrix
 // is not written.  The issuing thread groups its stores (bulk_commit) and
 // waits until at most N groups still read their shared memory (the writes
@@ -238,6 +249,19 @@ __device__ __forceinline__ void tmem_wait_loads(uint32_t (&r)[32])
                  : "memory");
 }
 
+// Sixteen columns of this warp's 32 lanes, from its lanes' registers.
+__device__ __forceinline__ void tmem_store16(uint32_t addr, const uint32_t (&r)[16])
+{
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15};" ::"r"(r[0]),
+        "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
+        "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(addr)
+        : "memory");
+}
+
+__device__ __forceinline__ void tmem_wait_stores() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
 // ------------------------------------------------------------- matrix products
 
 // Descriptor of an operand tile in shared memory under the 128-byte swizzle
@@ -275,6 +299,17 @@ __device__ __forceinline__ void tensor_product(uint32_t d, uint64_t a, uint64_t 
             "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
             "l"(a), "l"(b), "r"(desc), "r"((uint32_t)add)
             : "memory");
+}
+
+// The same by one CTA with A in tensor memory: a row per lane, two elements
+// of k to a column (K-major).
+__device__ __forceinline__ void tensor_product_tmem(uint32_t d, uint32_t a, uint64_t b, uint32_t desc, bool add)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "r"(desc), "r"((uint32_t)add)
+        : "memory");
 }
 
 // Arrives on `bar` (in both CTAs of a pair) when the products this thread
