@@ -328,6 +328,14 @@ def test_window_attention_backward(zp, case, dtype):
     Batch(lens, h, g, d, dtype, room=3, behind=2).check_backward(zp, window, sinks)
 
 
+@pytest.mark.parametrize("case", [([(2600, 2600)], 2, 1, 64, 100, 4), ([(300, 300), (2400, 2500), (2200, 2200)], 2, 2, 128, 130, 200),
+                                  ([(4100, 4100)], 1, 1, 32, 900, 1)], ids=ids)
+def test_window_attention_backward_deals_out_the_first_keys(zp, case):
+    """Sequences long enough that the first keys' queries go in parts."""
+    lens, h, g, d, window, sinks = case
+    Batch(lens, h, g, d, "bf16", room=3, behind=2).check_backward(zp, window, sinks)
+
+
 @pytest.mark.parametrize("layout", ["slice", "heads_first"])
 @pytest.mark.parametrize("lens", [[(150, 150), (70, 300)], [(1, 400), (1, 30)]], ids=["many", "few"])
 def test_window_attention_layouts(zp, lens, layout):

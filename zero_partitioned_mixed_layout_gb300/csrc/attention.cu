@@ -146,6 +146,7 @@ __host__ __device__ inline int64_t tile_numbers(int64_t rows, int64_t sequences,
 
 struct TileAt {
     Seq s;
+    int32_t index;  // of the sequence
     int32_t first;  // row of its sequence
     bool any;
 };
@@ -171,6 +172,7 @@ __device__ __forceinline__ TileAt find_tile(const Attn &a, const int64_t *offset
         s = lo;
         first = (number - (cut(offsets[s], 0, rows) / T + s)) * T;
     }
+    t.index = s;
     t.s = sequence(a, s);
     t.any = first >= 0 && first < (keys ? t.s.lk : t.s.lq);
     t.first = t.any ? (int32_t)first : 0;
@@ -699,122 +701,953 @@ __global__ void __launch_bounds__(FwdShape<DP>::THREADS, 1) k_attn_tiles(const _
         tmem_free<1>(tmem, 512);
 }
 
-struct Bwd {
+// ------------------------------------------------------------- backward
+
+// What every pair of a query and a key takes from the query's row: lse in
+// units of log 2 (+inf where no key is seen, which makes every weight 0) and
+// delta = dout . out.  Laid out by tile of 128 queries, so that a tile's are
+// one aligned copy: [head][tile number][lse2 of 128, delta of 128].
+struct StatsArgs {
     Attn a;
-    Heads dout, q, k, v, out, dq, dk, dv;
+    Heads dout, out;
     const float *lse;
-    float *delta;  // q_heads x q_tokens
+    float *stats;
+    int64_t tiles;
 };
 
-__device__ __forceinline__ float warp_add(float t)
-{
-#pragma unroll
-    for (int x = 16; x > 0; x >>= 1)
-        t += __shfl_xor_sync(0xffffffffu, t, x);
-    return t;
-}
-
 template <int DT>
-__device__ __forceinline__ void load_row(const Heads &h, int64_t row, int64_t head, int lane, int dim, float (&f)[4])
+__global__ void __launch_bounds__(kThreads) k_attn_stats(const __grid_constant__ StatsArgs f)
 {
-#pragma unroll
-    for (int e = 0; e < 4; ++e)
-        f[e] = lane + 32 * e < dim ? load1<DT>(h.p, row * h.ld + head * h.hd + lane + 32 * e) : 0.0f;
-}
-
-template <int DT>
-__device__ __forceinline__ void store_row(const Heads &h, int64_t row, int64_t head, int lane, int dim, const float (&f)[4])
-{
-#pragma unroll
-    for (int e = 0; e < 4; ++e)
-        if (lane + 32 * e < dim)
-            store1<DT>(const_cast<void *>(h.p), row * h.ld + head * h.hd + lane + 32 * e, f[e]);
-}
-
-__device__ __forceinline__ float dot4(const float (&x)[4], const float (&y)[4])
-{
-    return warp_add(x[0] * y[0] + x[1] * y[1] + x[2] * y[2] + x[3] * y[3]);
-}
-
-// delta and dq: a warp per query and head.
-template <int DT>
-__global__ void __launch_bounds__(kThreads) k_attn_dq(const __grid_constant__ Bwd b)
-{
-    const Attn &a = b.a;
-    const int lane = threadIdx.x & 31;
-    for (int64_t u = ((int64_t)blockIdx.x * kThreads + threadIdx.x) >> 5; u < a.q_tokens * a.q_heads;
-         u += (int64_t)gridDim.x * kWarps) {
-        const int64_t row = u / a.q_heads;
-        const int32_t h = (int32_t)(u - row * a.q_heads), g = h / a.group;
-        const int32_t s = sequence_of(a.q_offsets, a.sequences, row);
-        if (s < 0)
+    const Attn &a = f.a;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    pdl_launch_next();
+    int lanes = 1;  // per row: 8 elements each
+    while (lanes * 8 < a.dim)
+        lanes *= 2;
+    const int rows = 32 / lanes, sub = lane / lanes, at = lane & (lanes - 1);
+    // a warp: 32 rows of a tile and one head
+    const int64_t all = f.tiles * a.q_heads * 4;
+    for (int64_t u = (int64_t)blockIdx.x * kWarps + warp; u < all; u += (int64_t)gridDim.x * kWarps) {
+        const int64_t number = u / 4 / a.q_heads;
+        const int32_t h = (int32_t)(u / 4 - number * a.q_heads), part = (int32_t)(u & 3);
+        const TileAt t = find_tile(a, a.q_offsets, a.q_tokens, number, 128, false, lane);
+        if (!t.any)
             continue;
-        const Seq sq = sequence(a, s);
-        if (row - sq.q0 >= sq.lq)
-            continue;
-        const int32_t p = (int32_t)(row - sq.q0) + sq.lk - sq.lq;
-        float q[4], dout[4], out[4], dq[4] = {};
-        load_row<DT>(b.q, row, h, lane, a.dim, q);
-        load_row<DT>(b.dout, row, h, lane, a.dim, dout);
-        load_row<DT>(b.out, row, h, lane, a.dim, out);
-        const float delta = dot4(dout, out), lse = b.lse[(int64_t)h * a.q_tokens + row];
-        if (lane == 0)
-            b.delta[(int64_t)h * a.q_tokens + row] = delta;
-        for (int32_t j = 0; j <= p; ++j) {
-            if (j >= a.sinks && j <= p - a.window) {
-                j = p - a.window;
-                continue;
+        float *to = f.stats + (h * f.tiles + number) * 256 + part * 32;
+#pragma unroll 4
+        for (int r0 = 0; r0 < 32; r0 += rows) {
+            const int32_t i = t.first + part * 32 + r0 + sub;
+            const int64_t row = t.s.q0 + i;
+            float sum = 0.0f;
+            if (i < t.s.lq && at * 8 < a.dim) {
+                const uint4 x = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(f.dout.p) + row * f.dout.ld + h * f.dout.hd + at * 8);
+                const uint4 y = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(f.out.p) + row * f.out.ld + h * f.out.hd + at * 8);
+                float fx[8], fy[8];
+                Elem<DT>::to_float(&x, fx);
+                Elem<DT>::to_float(&y, fy);
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    sum += fx[e] * fy[e];
             }
-            float k[4], v[4];
-            load_row<DT>(b.k, sq.k0 + j, g, lane, a.dim, k);
-            load_row<DT>(b.v, sq.k0 + j, g, lane, a.dim, v);
-            const float w = __expf(dot4(q, k) * a.scale - lse), ds = w * (dot4(dout, v) - delta) * a.scale;
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-                dq[e] += ds * k[e];
+            for (int o = 16; o > 0; o >>= 1)
+                if (o < lanes)
+                    sum += __shfl_xor_sync(0xffffffffu, sum, o);
+            if (at == 0) {
+                const bool live = i < t.s.lq;
+                const float lse = live ? f.lse[(int64_t)h * a.q_tokens + row] : -INFINITY;
+                to[r0 + sub] = lse == -INFINITY ? INFINITY : lse * 1.4426950408889634f;
+                to[128 + r0 + sub] = live ? sum : 0.0f;
+            }
         }
-        store_row<DT>(b.dq, row, h, lane, a.dim, dq);
     }
 }
 
-// dk and dv: a warp per key and key head.
-template <int DT>
-__global__ void __launch_bounds__(kThreads) k_attn_dkv(const __grid_constant__ Bwd b)
+struct BwdTiles {
+    HeadsMap q, k, v, dout;
+    Attn a;
+    Heads dq, dk, dv;
+    const float *stats;
+    int64_t q_tiles, k_tiles;  // tile numbers of 128 queries, and keys
+    // first keys seen by all queries: their tiles' queries in parts of `chunk` tiles
+    int32_t chunk, sink_tiles;
+    int64_t chunks, split_units;
+    float *partial;  // [split unit][dv, dk][128][dim]
+    float scale, scale_log2;
+    WsHeader *hdr;
+    uint64_t limit_ns;
+};
+
+// The tiles of 128 queries that see a key of the tile from key j on.
+struct QueryTiles {
+    int32_t low, high;
+};
+
+__device__ __forceinline__ QueryTiles query_tiles(const Attn &a, int32_t j, int32_t lq, int32_t lk)
 {
-    const Attn &a = b.a;
-    const int lane = threadIdx.x & 31;
-    for (int64_t u = ((int64_t)blockIdx.x * kThreads + threadIdx.x) >> 5; u < a.k_tokens * a.k_heads;
-         u += (int64_t)gridDim.x * kWarps) {
-        const int64_t key = u / a.k_heads;
-        const int32_t g = (int32_t)(u - key * a.k_heads);
-        const int32_t s = sequence_of(a.k_offsets ? a.k_offsets : a.q_offsets, a.sequences, key);
-        if (s < 0 || s >= a.sequences)
-            continue;
-        const Seq sq = sequence(a, s);
-        const int64_t j = key - sq.k0;
-        if (j >= sq.lk)
-            continue;
-        float k[4], v[4], dk[4] = {}, dv[4] = {};
-        load_row<DT>(b.k, key, g, lane, a.dim, k);
-        load_row<DT>(b.v, key, g, lane, a.dim, v);
-        const int64_t shift = sq.lk - sq.lq;
-        const int64_t first = j > shift ? j : shift;
-        const int64_t last = j < a.sinks || j + a.window > sq.lk ? sq.lk : j + a.window;
-        for (int32_t h = g * a.group; h < (g + 1) * a.group; ++h)
-            for (int64_t p = first; p < last; ++p) {
-                const int64_t row = sq.q0 + p - shift;
-                float q[4], dout[4];
-                load_row<DT>(b.q, row, h, lane, a.dim, q);
-                load_row<DT>(b.dout, row, h, lane, a.dim, dout);
-                const float w = __expf(dot4(q, k) * a.scale - b.lse[(int64_t)h * a.q_tokens + row]);
-                const float ds = w * (dot4(dout, v) - b.delta[(int64_t)h * a.q_tokens + row]) * a.scale;
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    dk[e] += ds * q[e], dv[e] += w * dout[e];
-            }
-        store_row<DT>(b.dk, key, g, lane, a.dim, dk);
-        store_row<DT>(b.dv, key, g, lane, a.dim, dv);
+    const int32_t shift = lk - lq, last = j + 127 < lk ? j + 127 : lk - 1;
+    const int32_t from = j > shift ? j - shift : 0;
+    int32_t to = lq - 1;
+    if (j >= a.sinks && last - shift + (int64_t)a.window - 1 < to)
+        to = last - shift + a.window - 1;
+    if (lq == 0 || from > to)
+        return {0, -1};
+    return {from / 128, to / 128};
+}
+
+// Whether those of a tile of first keys are dealt out.
+__device__ __forceinline__ bool is_split(const BwdTiles &f, int32_t j, const QueryTiles &t)
+{
+    return f.chunk > 0 && j < f.a.sinks && t.high - t.low + 1 > 2 * f.chunk;
+}
+
+struct KeyUnit {
+    int32_t k_row, q_row, first, lq, lk, head;  // first key of its sequence; q_row: the sequence's first query
+    int32_t low, high;                          // query tiles
+    int64_t stats;                              // tile number of query tile 0
+    int64_t slot;                               // of the partial sums, or -1
+    int32_t end;
+};
+
+template <int DP>
+struct BwdShape {
+    static constexpr int BOXES = DP / 64, TILE = BOXES * 16384;
+    static constexpr int THREADS = 320;
+    static constexpr int SMEM = 1024 + 6 * TILE + 2048;
+};
+
+struct KeyShared {
+    uint64_t kv_full, kv_empty, q_full[2], q_empty[2], o_full[2], o_empty[2], s_full, dp_full, p_full, ds_full, acc_full;
+    uint64_t unit_full[kUnitRing], unit_empty[kUnitRing];
+    KeyUnit units[kUnitRing];
+    uint32_t tmem, gave_up;
+};
+
+// The work of a unit number: false if there is none.
+__device__ __forceinline__ bool key_unit(const BwdTiles &f, int64_t i, int lane, KeyUnit &u)
+{
+    const Attn &a = f.a;
+    const int64_t *k_offsets = a.k_offsets ? a.k_offsets : a.q_offsets;
+    TileAt at;
+    u.end = 0;
+    if (i < f.split_units) {
+        const int64_t chunk = i / a.k_heads / f.sink_tiles;
+        at = find_tile(a, a.q_offsets, a.q_tokens, chunk, 128 * f.chunk, false, lane);
+        u.head = (int32_t)(i % a.k_heads);
+        u.first = (int32_t)(i / a.k_heads % f.sink_tiles) * 128;
+        if (!at.any || u.first >= at.s.lk || u.first >= a.sinks)
+            return false;
+        const QueryTiles t = query_tiles(a, u.first, at.s.lq, at.s.lk);
+        if (!is_split(f, u.first, t))
+            return false;
+        const int32_t low = at.first / 128, high = low + f.chunk - 1;
+        u.low = low > t.low ? low : t.low;
+        u.high = high < t.high ? high : t.high;
+        if (u.low > u.high)
+            return false;
+        u.slot = i;
+    } else {
+        i -= f.split_units;
+        at = find_tile(a, k_offsets, a.k_tokens, i / a.k_heads, 128, true, lane);
+        if (!at.any)
+            return false;
+        u.head = (int32_t)(i % a.k_heads);
+        u.first = at.first;
+        const QueryTiles t = query_tiles(a, u.first, at.s.lq, at.s.lk);
+        if (is_split(f, u.first, t))
+            return false;
+        u.low = t.low, u.high = t.high;
+        u.slot = -1;
     }
+    u.k_row = (int32_t)at.s.k0 + u.first;
+    u.q_row = (int32_t)at.s.q0;
+    u.lq = at.s.lq, u.lk = at.s.lk;
+    u.stats = a.q_offsets ? at.s.q0 / 128 + at.index : 0;
+    return true;
+}
+
+// dk and dv of 128 keys of one key head at a time, over the query heads of
+// its group and the tiles of queries that see them.  Everything is the
+// transpose of the forward pass's, so that the weights and their gradients,
+// which the two running products take from tensor memory, have a key per lane:
+//     S' = K Q^T, P' = exp(S' - lse), dP' = V dO^T, dS' = P' (dP' - delta),
+//     dV += P' dO, dK += dS' Q.
+template <int DT, int DP>
+__global__ void __launch_bounds__(BwdShape<DP>::THREADS, 1) k_attn_dkv(const __grid_constant__ BwdTiles f)
+{
+    using S = BwdShape<DP>;
+    extern __shared__ unsigned char smem_raw[];
+    __shared__ KeyShared sh;
+    unsigned char *smem = smem_raw + ((1024 - (smem_addr(smem_raw) & 1023u)) & 1023u);
+    unsigned char *const s_k = smem, *const s_v = smem + S::TILE, *const s_q = s_v + S::TILE, *const s_o = s_q + 2 * S::TILE;
+    float *const s_stats = reinterpret_cast<float *>(s_o + 2 * S::TILE);  // [stage][lse2, delta][128]
+    const Attn &a = f.a;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    constexpr int kTma = 8, kMma = 9;
+
+    if (threadIdx.x == 0) {
+        mbar_init_count(&sh.kv_full, 1);
+        mbar_init_count(&sh.kv_empty, 1);
+        for (int s = 0; s < 2; ++s) {
+            mbar_init_count(&sh.q_full[s], 1);
+            mbar_init_count(&sh.q_empty[s], 1);
+            mbar_init_count(&sh.o_full[s], 1);
+            mbar_init_count(&sh.o_empty[s], 1);
+        }
+        mbar_init_count(&sh.s_full, 1);
+        mbar_init_count(&sh.dp_full, 1);
+        mbar_init_count(&sh.p_full, 8);
+        mbar_init_count(&sh.ds_full, 8);
+        mbar_init_count(&sh.acc_full, 1);
+        for (int s = 0; s < kUnitRing; ++s) {
+            mbar_init_count(&sh.unit_full[s], 1);
+            mbar_init_count(&sh.unit_empty[s], 9);
+        }
+        sh.gave_up = 0;
+        mbar_init_done();
+    }
+    if (warp == kMma)
+        tmem_alloc<1>(&sh.tmem, 512);
+    if (warp == kTma && lane < 4)
+        tma_prefetch_map(lane == 0 ? &f.q.map : lane == 1 ? &f.k.map : lane == 2 ? &f.v.map : &f.dout.map);
+    tmem_fence_before();
+    __syncthreads();
+    tmem_fence_after();
+    const uint32_t tmem = sh.tmem;
+    pdl_launch_next();
+    pdl_wait();
+    auto wait = [&](uint64_t *bar, uint32_t parity) { return mbar_wait_warp(bar, parity, f.limit_ns, &sh.gave_up); };
+    uint32_t units = 0;
+    auto next = [&](KeyUnit &u) {
+        const uint32_t slot = units % kUnitRing;
+        if (!wait(&sh.unit_full[slot], (units / kUnitRing) & 1))
+            return false;
+        u = sh.units[slot];
+        __syncwarp();
+        if (lane == 0)
+            mbar_arrive_cluster(smem_addr(&sh.unit_empty[slot]));
+        ++units;
+        return u.end == 0;
+    };
+    const int64_t all = f.split_units + f.k_tiles * a.k_heads;
+
+    if (warp == kTma) {
+        asm volatile("fence.proxy.async.global;" ::: "memory");
+        uint32_t kvn = 0, qn = 0;
+        bool ok = true;
+        auto publish = [&](const KeyUnit &u) {
+            const uint32_t slot = units % kUnitRing;
+            if (!wait(&sh.unit_empty[slot], ((units / kUnitRing) & 1) ^ 1))
+                return false;
+            if (lane == 0) {
+                sh.units[slot] = u;
+                mbar_arrive_cluster(smem_addr(&sh.unit_full[slot]));
+            }
+            __syncwarp();
+            ++units;
+            return true;
+        };
+        auto load = [&](unsigned char *to, const HeadsMap &m, int32_t row, int32_t head, uint64_t *bar) {
+#pragma unroll
+            for (int x = 0; x < S::BOXES; ++x)
+                load_box(smem_addr(to) + x * 16384, m, 64 * x, row, head, smem_addr(bar));
+        };
+        for (int64_t i = blockIdx.x; ok && i < all; i += gridDim.x) {
+            KeyUnit u;
+            if (!key_unit(f, i, lane, u))
+                continue;
+            ok = publish(u);
+            if (!ok || u.low > u.high)
+                continue;
+            ok = wait(&sh.kv_empty, (kvn & 1) ^ 1);
+            if (!ok)
+                break;
+            if (elect_one()) {
+                mbar_expect(&sh.kv_full, 2 * S::TILE);
+                load(s_k, f.k, u.k_row, u.head, &sh.kv_full);
+                load(s_v, f.v, u.k_row, u.head, &sh.kv_full);
+            }
+            __syncwarp();
+            ++kvn;
+            for (int32_t h = u.head * a.group; ok && h < (u.head + 1) * a.group; ++h)
+                for (int32_t t = u.low; t <= u.high; ++t) {
+                    const uint32_t st = qn & 1, parity = ((qn >> 1) & 1) ^ 1;
+                    ok = wait(&sh.q_empty[st], parity);
+                    if (!ok)
+                        break;
+                    if (elect_one()) {
+                        mbar_expect(&sh.q_full[st], S::TILE + 1024);
+                        load(s_q + st * S::TILE, f.q, u.q_row + 128 * t, h, &sh.q_full[st]);
+                        bulk_copy(smem_addr(s_stats + st * 256), f.stats + (h * f.q_tiles + u.stats + t) * 256, 1024,
+                                  smem_addr(&sh.q_full[st]));
+                    }
+                    __syncwarp();
+                    ok = wait(&sh.o_empty[st], parity);
+                    if (!ok)
+                        break;
+                    if (elect_one()) {
+                        mbar_expect(&sh.o_full[st], S::TILE);
+                        load(s_o + st * S::TILE, f.dout, u.q_row + 128 * t, h, &sh.o_full[st]);
+                    }
+                    __syncwarp();
+                    ++qn;
+                }
+        }
+        if (ok) {
+            KeyUnit u{};
+            u.end = 1;
+            publish(u);
+        }
+    } else if (warp == kMma) {
+        constexpr bool kBf16 = DT == ZERO_BF16;
+        const uint32_t desc_s = product_desc(kBf16, false, false, 128, 128);
+        const int wide = (a.dim + 15) & ~15, steps = wide / 16;
+        const uint32_t desc_acc = product_desc(kBf16, false, true, 128, wide);
+        const uint64_t dk0 = operand_desc(smem_addr(s_k), 16, 1024), dv0 = operand_desc(smem_addr(s_v), 16, 1024);
+        const uint64_t dq0 = operand_desc(smem_addr(s_q), 16, 1024), do0 = operand_desc(smem_addr(s_o), 16, 1024);
+        const uint64_t tq0 = operand_desc(smem_addr(s_q), 16384, 1024), to0 = operand_desc(smem_addr(s_o), 16384, 1024);
+        uint32_t kvn = 0, qn = 0, n = 0;
+        bool ok = true;
+        KeyUnit u;
+        // D = A B^T over the head's elements
+        auto inner = [&](uint32_t d, uint64_t x, uint64_t y) {
+            for (int s = 0; s < steps; ++s) {
+                const uint32_t off = (s >> 2) * (16384 >> 4) + (s & 3) * 2;
+                tensor_product<1>(d, x + off, y + off, desc_s, s != 0);
+            }
+        };
+        // D += A B over 128 queries, A in tensor memory (each half where its scores were)
+        auto outer = [&](uint32_t d, uint32_t x, uint64_t y, bool add) {
+#pragma unroll
+            for (int s = 0; s < 8; ++s)
+                tensor_product_tmem(d, x + (s >> 2) * 64 + (s & 3) * 8, y + s * 128, desc_acc, add || s != 0);
+        };
+        while (ok && next(u)) {
+            const int32_t count = u.low > u.high ? 0 : (u.high - u.low + 1) * a.group;
+            if (count == 0)
+                continue;
+            ok = wait(&sh.kv_full, kvn & 1) && wait(&sh.q_full[qn & 1], (qn >> 1) & 1);
+            if (!ok)
+                break;
+            ++kvn;
+            tmem_fence_after();
+            if (elect_one()) {
+                inner(tmem, dk0, dq0 + (((qn & 1) * S::TILE) >> 4));
+                tensor_commit<1>(&sh.s_full);
+            }
+            __syncwarp();
+            for (int32_t i = 0; i < count; ++i, ++qn, ++n) {
+                const uint32_t st = qn & 1;
+                ok = wait(&sh.o_full[st], (qn >> 1) & 1);
+                if (!ok)
+                    break;
+                tmem_fence_after();
+                if (elect_one()) {
+                    inner(tmem + 128, dv0, do0 + ((st * S::TILE) >> 4));
+                    tensor_commit<1>(&sh.dp_full);
+                }
+                __syncwarp();
+                ok = wait(&sh.p_full, n & 1);
+                if (!ok)
+                    break;
+                tmem_fence_after();
+                if (elect_one()) {
+                    outer(tmem + 256, tmem, to0 + ((st * S::TILE) >> 4), i != 0);
+                    tensor_commit<1>(&sh.o_empty[st]);
+                }
+                __syncwarp();
+                if (i + 1 < count) {
+                    const uint32_t to = (qn + 1) & 1;
+                    ok = wait(&sh.q_full[to], ((qn + 1) >> 1) & 1);
+                    if (!ok)
+                        break;
+                    tmem_fence_after();
+                    if (elect_one()) {
+                        inner(tmem, dk0, dq0 + ((to * S::TILE) >> 4));
+                        tensor_commit<1>(&sh.s_full);
+                    }
+                    __syncwarp();
+                }
+                ok = wait(&sh.ds_full, n & 1);
+                if (!ok)
+                    break;
+                tmem_fence_after();
+                if (elect_one()) {
+                    outer(tmem + 384, tmem + 128, tq0 + ((st * S::TILE) >> 4), i != 0);
+                    tensor_commit<1>(&sh.q_empty[st]);
+                    if (i + 1 == count) {
+                        tensor_commit<1>(&sh.kv_empty);
+                        tensor_commit<1>(&sh.acc_full);
+                    }
+                }
+                __syncwarp();
+            }
+        }
+    } else {
+        const int half = warp >> 2, quarter = warp & 3;
+        const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
+        const uint32_t at_s = tmem + lanes + half * 64, at_p = at_s + 128;
+        uint32_t qn = 0, n = 0, accs = 0;
+        bool ok = true;
+        KeyUnit u;
+        while (ok && next(u)) {
+            const int32_t count = u.low > u.high ? 0 : (u.high - u.low + 1) * a.group;
+            const int32_t j = u.first + quarter * 32 + lane;
+            int32_t t = u.low;
+            for (int32_t i = 0; i < count; ++i, ++qn, ++n) {
+                const uint32_t st = qn & 1;
+                const int32_t p0 = 128 * t + u.lk - u.lq, nq = u.lq - 128 * t;
+                const bool whole = nq >= 128 && u.first + 127 <= p0 &&
+                                   (p0 + 127 - u.first < a.window || u.first + 127 < a.sinks);
+                ok = wait(&sh.s_full, n & 1) && wait(&sh.q_full[st], (qn >> 1) & 1);
+                if (!ok)
+                    break;
+                tmem_fence_after();
+                const float *lse2 = s_stats + st * 256 + half * 64, *delta = lse2 + 128;
+                float p[64];
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    uint32_t r[32];
+                    tmem_load32(at_s + 32 * c, r);
+                    tmem_wait_loads(r);
+#pragma unroll
+                    for (int e = 0; e < 32; e += 4) {
+                        const float4 x = *reinterpret_cast<const float4 *>(lse2 + 32 * c + e);
+                        p[32 * c + e] = exp2_fast(__uint_as_float(r[e]) * f.scale_log2 - x.x);
+                        p[32 * c + e + 1] = exp2_fast(__uint_as_float(r[e + 1]) * f.scale_log2 - x.y);
+                        p[32 * c + e + 2] = exp2_fast(__uint_as_float(r[e + 2]) * f.scale_log2 - x.z);
+                        p[32 * c + e + 3] = exp2_fast(__uint_as_float(r[e + 3]) * f.scale_log2 - x.w);
+                    }
+                }
+                uint32_t bits[2] = {~0u, ~0u};
+                if (!whole) {
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        const int32_t from = half * 64 + 32 * c;
+                        bits[c] = ~bits_up_to(j - p0 - 1 - from) & bits_up_to(nq - 1 - from);
+                        if (j >= a.sinks)
+                            bits[c] &= bits_up_to(j - p0 + a.window - 1 - from);
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)
+                            p[32 * c + e] = bits[c] & (1u << e) ? p[32 * c + e] : 0.0f;
+                    }
+                }
+                // (every lane has read its scores: stores follow loads in a warp, and a half keeps to its own columns)
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    uint32_t w[16];
+#pragma unroll
+                    for (int e = 0; e < 16; ++e)
+                        w[e] = pack2<DT>(p[32 * c + 2 * e], p[32 * c + 2 * e + 1]);
+                    tmem_store16(at_s + 16 * c, w);
+                }
+                if (nq < 128) {
+                    // rows behind the last query: zeros, since 0 times what they hold may not be 0
+                    ok = wait(&sh.o_full[st], (qn >> 1) & 1);
+                    if (!ok)
+                        break;
+                    for (int k = nq * 8 + threadIdx.x; k < 1024; k += 256)
+#pragma unroll
+                        for (int b = 0; b < S::BOXES; ++b) {
+                            *reinterpret_cast<uint4 *>(s_o + st * S::TILE + b * 16384 + k * 16) = make_uint4(0, 0, 0, 0);
+                            *reinterpret_cast<uint4 *>(s_q + st * S::TILE + b * 16384 + k * 16) = make_uint4(0, 0, 0, 0);
+                        }
+                    fence_proxy_async();
+                }
+                tmem_wait_stores();
+                tmem_fence_before();
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive_cluster(smem_addr(&sh.p_full));
+                ok = wait(&sh.dp_full, n & 1);
+                if (!ok)
+                    break;
+                tmem_fence_after();
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    uint32_t r[32], w[16];
+                    tmem_load32(at_p + 32 * c, r);
+                    tmem_wait_loads(r);
+#pragma unroll
+                    for (int e = 0; e < 32; e += 4) {
+                        const float4 x = *reinterpret_cast<const float4 *>(delta + 32 * c + e);
+                        p[32 * c + e] *= __uint_as_float(r[e]) - x.x;
+                        p[32 * c + e + 1] *= __uint_as_float(r[e + 1]) - x.y;
+                        p[32 * c + e + 2] *= __uint_as_float(r[e + 2]) - x.z;
+                        p[32 * c + e + 3] *= __uint_as_float(r[e + 3]) - x.w;
+                    }
+                    if (!whole) {
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)
+                            p[32 * c + e] = bits[c] & (1u << e) ? p[32 * c + e] : 0.0f;
+                    }
+#pragma unroll
+                    for (int e = 0; e < 16; ++e)
+                        w[e] = pack2<DT>(p[32 * c + 2 * e], p[32 * c + 2 * e + 1]);
+                    tmem_store16(at_p + 16 * c, w);
+                }
+                tmem_wait_stores();
+                tmem_fence_before();
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive_cluster(smem_addr(&sh.ds_full));
+                t = t == u.high ? u.low : t + 1;
+            }
+            if (ok && count > 0) {
+                ok = wait(&sh.acc_full, accs & 1);
+                ++accs;
+                tmem_fence_after();
+            }
+            if (!ok)
+                break;
+            // dv by the first four warps, dk by the others
+            const uint32_t from = tmem + lanes + 256 + half * 128;
+            const float by = half ? f.scale : 1.0f;
+            const Heads &to = half ? f.dk : f.dv;
+            for (int c = 0; c < a.dim; c += 32) {
+                uint32_t o[32];
+                if (count > 0) {
+                    tmem_load32(from + c, o);
+                    tmem_wait_loads(o);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 32; ++e)
+                        o[e] = 0;
+                }
+                if (u.slot >= 0) {
+                    float *out = f.partial + ((u.slot * 2 + half) * 128 + quarter * 32 + lane) * a.dim + c;
+#pragma unroll
+                    for (int e = 0; e < 32; e += 4)
+                        if (c + e < a.dim)
+                            *reinterpret_cast<uint4 *>(out + e) = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+                } else if (j < u.lk) {
+                    uint16_t *out = static_cast<uint16_t *>(const_cast<void *>(to.p)) +
+                                    ((int64_t)u.k_row + quarter * 32 + lane) * to.ld + u.head * to.hd + c;
+#pragma unroll
+                    for (int e = 0; e < 32; e += 8)
+                        if (c + e < a.dim) {
+                            uint32_t w[4];
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                w[i] = pack2<DT>(__uint_as_float(o[e + 2 * i]) * by, __uint_as_float(o[e + 2 * i + 1]) * by);
+                            *reinterpret_cast<uint4 *>(out + e) = make_uint4(w[0], w[1], w[2], w[3]);
+                        }
+                }
+                __syncwarp();
+            }
+        }
+    }
+
+    __syncwarp();
+    tmem_fence_before();
+    __syncthreads();
+    if (sh.gave_up) {
+        // copies and products may still be in flight: let them end before
+        // the memory that they use is given back
+        if (threadIdx.x == 0)
+            atomicAdd(&f.hdr->stalls, 1u);
+        const uint64_t began = global_ns();
+        while (global_ns() - began < 20000000u) {
+        }
+        // no result of this CTA is to be taken for one
+        for (int64_t i = blockIdx.x; i < all; i += gridDim.x) {
+            KeyUnit u;
+            if (!key_unit(f, i, lane, u))
+                continue;
+            for (int32_t r = warp; r < 128; r += S::THREADS / 32)
+                for (int e = lane; e < a.dim; e += 32)
+                    if (u.slot >= 0) {
+                        f.partial[((u.slot * 2) * 128 + r) * a.dim + e] = __uint_as_float(0x7fffffffu);
+                        f.partial[((u.slot * 2 + 1) * 128 + r) * a.dim + e] = __uint_as_float(0x7fffffffu);
+                    } else if (u.first + r < u.lk) {
+                        const int64_t row = (int64_t)u.k_row + r;
+                        static_cast<uint16_t *>(const_cast<void *>(f.dk.p))[row * f.dk.ld + u.head * f.dk.hd + e] = 0x7fff;
+                        static_cast<uint16_t *>(const_cast<void *>(f.dv.p))[row * f.dv.ld + u.head * f.dv.hd + e] = 0x7fff;
+                    }
+        }
+    }
+    if (warp == kMma)
+        tmem_free<1>(tmem, 512);
+}
+
+// The sums of the first keys' tiles from their parts, in order: a block takes
+// eight keys of one tile, key head and sequence.
+template <int DT>
+__global__ void __launch_bounds__(kThreads) k_attn_join(const __grid_constant__ BwdTiles f)
+{
+    const Attn &a = f.a;
+    pdl_launch_next();
+    pdl_wait();
+    for (int64_t b = blockIdx.x; b < (int64_t)a.sequences * f.sink_tiles * a.k_heads * 16; b += gridDim.x) {
+        const int rows = (int)(b & 15) * 8;
+        const int64_t i = b >> 4;
+        const int32_t g = (int32_t)(i % a.k_heads), s = (int32_t)(i / a.k_heads / f.sink_tiles);
+        const int32_t tile = (int32_t)(i / a.k_heads % f.sink_tiles), first = tile * 128;
+        const Seq sq = sequence(a, s);
+        if (first + rows >= sq.lk || first >= a.sinks)
+            continue;
+        const QueryTiles t = query_tiles(a, first, sq.lq, sq.lk);
+        if (!is_split(f, first, t))
+            continue;
+        const int64_t base = a.q_offsets ? sq.q0 / (128 * f.chunk) + s : 0;
+        for (int v = threadIdx.x; v < 2 * 8 * a.dim; v += kThreads) {
+            const int which = v / (8 * a.dim), r = rows + (v - which * 8 * a.dim) / a.dim, e = v % a.dim;
+            if (first + r >= sq.lk)
+                continue;
+            float sum = 0.0f;
+            for (int32_t c = t.low / f.chunk; c <= t.high / f.chunk; ++c) {
+                const int64_t slot = ((base + c) * f.sink_tiles + tile) * a.k_heads + g;
+                sum += f.partial[((slot * 2 + which) * 128 + r) * a.dim + e];
+            }
+            const Heads &to = which ? f.dk : f.dv;
+            store1<DT>(const_cast<void *>(to.p), (sq.k0 + first + r) * to.ld + g * to.hd + e, which ? sum * f.scale : sum);
+        }
+    }
+}
+
+struct QueryUnit {
+    int32_t q_row, k_row, first, lq, lk, head;
+    int64_t stats;  // tile number
+    int32_t end;
+};
+
+struct QueryShared {
+    uint64_t q_full, q_empty, k_full[2], k_empty[2], v_full[2], v_empty[2], sp_full, ds_full, acc_full;
+    uint64_t unit_full[kUnitRing], unit_empty[kUnitRing];
+    QueryUnit units[kUnitRing];
+    uint32_t tmem, gave_up;
+};
+
+// dq of 128 queries of one head at a time, over the tiles of keys that they
+// see: S = Q K^T, dP = dO V^T, dS = exp(S - lse) (dP - delta), dQ += dS K.
+// (S and dP are worked out here again, two products of seven, so that dq is
+// summed in one place and in one order, without atomics.)
+template <int DT, int DP>
+__global__ void __launch_bounds__(BwdShape<DP>::THREADS, 1) k_attn_dq(const __grid_constant__ BwdTiles f)
+{
+    using S = BwdShape<DP>;
+    extern __shared__ unsigned char smem_raw[];
+    __shared__ QueryShared sh;
+    unsigned char *smem = smem_raw + ((1024 - (smem_addr(smem_raw) & 1023u)) & 1023u);
+    unsigned char *const s_q = smem, *const s_o = smem + S::TILE, *const s_k = s_o + S::TILE, *const s_v = s_k + 2 * S::TILE;
+    const Attn &a = f.a;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    constexpr int kTma = 8, kMma = 9;
+
+    if (threadIdx.x == 0) {
+        mbar_init_count(&sh.q_full, 1);
+        mbar_init_count(&sh.q_empty, 1);
+        for (int s = 0; s < 2; ++s) {
+            mbar_init_count(&sh.k_full[s], 1);
+            mbar_init_count(&sh.k_empty[s], 1);
+            mbar_init_count(&sh.v_full[s], 1);
+            mbar_init_count(&sh.v_empty[s], 1);
+        }
+        mbar_init_count(&sh.sp_full, 1);
+        mbar_init_count(&sh.ds_full, 8);
+        mbar_init_count(&sh.acc_full, 1);
+        for (int s = 0; s < kUnitRing; ++s) {
+            mbar_init_count(&sh.unit_full[s], 1);
+            mbar_init_count(&sh.unit_empty[s], 9);
+        }
+        sh.gave_up = 0;
+        mbar_init_done();
+    }
+    if (warp == kMma)
+        tmem_alloc<1>(&sh.tmem, 512);
+    if (warp == kTma && lane < 4)
+        tma_prefetch_map(lane == 0 ? &f.q.map : lane == 1 ? &f.k.map : lane == 2 ? &f.v.map : &f.dout.map);
+    tmem_fence_before();
+    __syncthreads();
+    tmem_fence_after();
+    const uint32_t tmem = sh.tmem;
+    pdl_launch_next();
+    pdl_wait();
+    auto wait = [&](uint64_t *bar, uint32_t parity) { return mbar_wait_warp(bar, parity, f.limit_ns, &sh.gave_up); };
+    uint32_t units = 0;
+    auto next = [&](QueryUnit &u) {
+        const uint32_t slot = units % kUnitRing;
+        if (!wait(&sh.unit_full[slot], (units / kUnitRing) & 1))
+            return false;
+        u = sh.units[slot];
+        __syncwarp();
+        if (lane == 0)
+            mbar_arrive_cluster(smem_addr(&sh.unit_empty[slot]));
+        ++units;
+        return u.end == 0;
+    };
+    const int64_t all = f.q_tiles * a.q_heads;
+    auto unit_at = [&](int64_t i, QueryUnit &u) {
+        const int64_t number = f.q_tiles - 1 - i / a.q_heads;  // long ones first
+        const TileAt at = find_tile(a, a.q_offsets, a.q_tokens, number, 128, false, lane);
+        u = QueryUnit{(int32_t)at.s.q0 + at.first, (int32_t)at.s.k0, at.first, at.s.lq, at.s.lk, (int32_t)(i % a.q_heads), number, 0};
+        return at.any;
+    };
+
+    if (warp == kTma) {
+        asm volatile("fence.proxy.async.global;" ::: "memory");
+        uint32_t un = 0, kn = 0;
+        bool ok = true;
+        auto publish = [&](const QueryUnit &u) {
+            const uint32_t slot = units % kUnitRing;
+            if (!wait(&sh.unit_empty[slot], ((units / kUnitRing) & 1) ^ 1))
+                return false;
+            if (lane == 0) {
+                sh.units[slot] = u;
+                mbar_arrive_cluster(smem_addr(&sh.unit_full[slot]));
+            }
+            __syncwarp();
+            ++units;
+            return true;
+        };
+        auto load = [&](unsigned char *to, const HeadsMap &m, int32_t row, int32_t head, uint64_t *bar) {
+#pragma unroll
+            for (int x = 0; x < S::BOXES; ++x)
+                load_box(smem_addr(to) + x * 16384, m, 64 * x, row, head, smem_addr(bar));
+        };
+        for (int64_t i = blockIdx.x; ok && i < all; i += gridDim.x) {
+            QueryUnit u;
+            if (!unit_at(i, u))
+                continue;
+            ok = publish(u);
+            const KeyTiles kt = key_tiles(a, u.first, u.lq, u.lk);
+            const TileList list = tile_list(kt, KeyTiles{0, -1, 0, false});
+            if (!ok || list.n == 0)
+                continue;
+            ok = wait(&sh.q_empty, (un & 1) ^ 1);
+            if (!ok)
+                break;
+            if (elect_one()) {
+                mbar_expect(&sh.q_full, 2 * S::TILE);
+                load(s_q, f.q, u.q_row, u.head, &sh.q_full);
+                load(s_o, f.dout, u.q_row, u.head, &sh.q_full);
+            }
+            __syncwarp();
+            ++un;
+            const int32_t g = u.head / a.group;
+            for (int32_t n = 0; n < list.n; ++n, ++kn) {
+                const uint32_t st = kn & 1, parity = ((kn >> 1) & 1) ^ 1;
+                const int32_t row = u.k_row + 128 * list.at(n);
+                ok = wait(&sh.k_empty[st], parity);
+                if (!ok)
+                    break;
+                if (elect_one()) {
+                    mbar_expect(&sh.k_full[st], S::TILE);
+                    load(s_k + st * S::TILE, f.k, row, g, &sh.k_full[st]);
+                }
+                __syncwarp();
+                ok = wait(&sh.v_empty[st], parity);
+                if (!ok)
+                    break;
+                if (elect_one()) {
+                    mbar_expect(&sh.v_full[st], S::TILE);
+                    load(s_v + st * S::TILE, f.v, row, g, &sh.v_full[st]);
+                }
+                __syncwarp();
+            }
+        }
+        if (ok) {
+            QueryUnit u{};
+            u.end = 1;
+            publish(u);
+        }
+    } else if (warp == kMma) {
+        constexpr bool kBf16 = DT == ZERO_BF16;
+        const uint32_t desc_s = product_desc(kBf16, false, false, 128, 128);
+        const int wide = (a.dim + 15) & ~15, steps = wide / 16;
+        const uint32_t desc_acc = product_desc(kBf16, false, true, 128, wide);
+        const uint64_t dq0 = operand_desc(smem_addr(s_q), 16, 1024), do0 = operand_desc(smem_addr(s_o), 16, 1024);
+        const uint64_t dk0 = operand_desc(smem_addr(s_k), 16, 1024), dv0 = operand_desc(smem_addr(s_v), 16, 1024);
+        const uint64_t tk0 = operand_desc(smem_addr(s_k), 16384, 1024);
+        uint32_t un = 0, kn = 0, dsn = 0;
+        bool ok = true;
+        QueryUnit u;
+        auto inner = [&](uint32_t d, uint64_t x, uint64_t y) {
+            for (int s = 0; s < steps; ++s) {
+                const uint32_t off = (s >> 2) * (16384 >> 4) + (s & 3) * 2;
+                tensor_product<1>(d, x + off, y + off, desc_s, s != 0);
+            }
+        };
+        while (ok && next(u)) {
+            const KeyTiles kt = key_tiles(a, u.first, u.lq, u.lk);
+            const TileList list = tile_list(kt, KeyTiles{0, -1, 0, false});
+            if (list.n == 0)
+                continue;
+            ok = wait(&sh.q_full, un & 1);
+            ++un;
+            // scores of tile kn + m of the keys, into the one of two buffers
+            auto scores = [&](uint32_t at) {
+                const uint32_t st = at & 1;
+                ok = ok && wait(&sh.k_full[st], (at >> 1) & 1);
+                if (!ok)
+                    return;
+                tmem_fence_after();
+                if (elect_one())
+                    inner(tmem + st * 128, dq0, dk0 + ((st * S::TILE) >> 4));
+                __syncwarp();
+            };
+            auto grads = [&](uint32_t at) {
+                const uint32_t st = at & 1;
+                ok = ok && wait(&sh.v_full[st], (at >> 1) & 1);
+                if (!ok)
+                    return;
+                tmem_fence_after();
+                if (elect_one()) {
+                    inner(tmem + 256, do0, dv0 + ((st * S::TILE) >> 4));
+                    tensor_commit<1>(&sh.sp_full);
+                    tensor_commit<1>(&sh.v_empty[st]);
+                }
+                __syncwarp();
+            };
+            scores(kn);
+            grads(kn);
+            for (int32_t n = 0; ok && n < list.n; ++n, ++kn, ++dsn) {
+                const uint32_t st = kn & 1;
+                if (n + 1 < list.n)
+                    scores(kn + 1);
+                ok = ok && wait(&sh.ds_full, dsn & 1);
+                if (!ok)
+                    break;
+                tmem_fence_after();
+                if (n + 1 < list.n)
+                    grads(kn + 1);
+                if (!ok)
+                    break;
+                if (elect_one()) {
+#pragma unroll
+                    for (int s = 0; s < 8; ++s)
+                        tensor_product_tmem(tmem + 384, tmem + st * 128 + (s >> 2) * 64 + (s & 3) * 8,
+                                            tk0 + ((st * S::TILE) >> 4) + s * 128, desc_acc, n != 0 || s != 0);
+                    tensor_commit<1>(&sh.k_empty[st]);
+                    if (n + 1 == list.n) {
+                        tensor_commit<1>(&sh.q_empty);
+                        tensor_commit<1>(&sh.acc_full);
+                    }
+                }
+                __syncwarp();
+            }
+        }
+    } else {
+        const int half = warp >> 2, quarter = warp & 3;
+        const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
+        uint32_t kn = 0, accs = 0;
+        bool ok = true;
+        QueryUnit u;
+        while (ok && next(u)) {
+            const KeyTiles kt = key_tiles(a, u.first, u.lq, u.lk);
+            const TileList list = tile_list(kt, KeyTiles{0, -1, 0, false});
+            const int32_t row = u.first + quarter * 32 + lane, p = row + u.lk - u.lq;
+            const int32_t p_first = u.first + u.lk - u.lq;
+            const int32_t p_last = (u.first + 127 < u.lq ? u.first + 127 : u.lq - 1) + u.lk - u.lq;
+            const float *stats = f.stats + (u.head * f.q_tiles + u.stats) * 256 + quarter * 32 + lane;
+            const float lse2 = stats[0], delta = stats[128];
+            for (int32_t n = 0; n < list.n; ++n, ++kn) {
+                const uint32_t st = kn & 1;
+                const int32_t k_first = list.at(n) * 128;
+                const bool whole = k_first + 127 <= p_first &&
+                                   (k_first > p_last - a.window || k_first + 127 < a.sinks);
+                ok = wait(&sh.sp_full, kn & 1);
+                if (!ok)
+                    break;
+                tmem_fence_after();
+                const uint32_t at_s = tmem + lanes + st * 128 + half * 64, at_p = tmem + lanes + 256 + half * 64;
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    uint32_t r[32], g[32], w[16];
+                    tmem_load32(at_s + 32 * c, r);
+                    tmem_load32(at_p + 32 * c, g);
+                    tmem_wait_loads(r);
+                    tmem_wait_loads(g);
+                    uint32_t bits = ~0u;
+                    if (!whole)
+                        bits = seen_bits(p, a.window, a.sinks, k_first + half * 64 + 32 * c);
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) {
+                        float x = exp2_fast(__uint_as_float(r[e]) * f.scale_log2 - lse2) * (__uint_as_float(g[e]) - delta);
+                        if (!whole)
+                            x = bits & (1u << e) ? x : 0.0f;
+                        r[e] = __float_as_uint(x);
+                    }
+#pragma unroll
+                    for (int e = 0; e < 16; ++e)
+                        w[e] = pack2<DT>(__uint_as_float(r[2 * e]), __uint_as_float(r[2 * e + 1]));
+                    tmem_store16(at_s + 16 * c, w);
+                }
+                if (k_first + 128 > u.lk) {
+                    // rows behind the last key: zeros, since 0 times what they hold may not be 0
+                    for (int k = (u.lk - k_first) * 8 + threadIdx.x; k < 1024; k += 256)
+#pragma unroll
+                        for (int b = 0; b < S::BOXES; ++b)
+                            *reinterpret_cast<uint4 *>(s_k + st * S::TILE + b * 16384 + k * 16) = make_uint4(0, 0, 0, 0);
+                    fence_proxy_async();
+                }
+                tmem_wait_stores();
+                tmem_fence_before();
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive_cluster(smem_addr(&sh.ds_full));
+            }
+            if (ok && list.n > 0) {
+                ok = wait(&sh.acc_full, accs & 1);
+                ++accs;
+                tmem_fence_after();
+            }
+            if (!ok)
+                break;
+            // a half of the columns each
+            const int cols = ((a.dim + 63) / 64) * 32;
+            for (int c = half * cols; c < a.dim && c < (half + 1) * cols; c += 32) {
+                uint32_t o[32];
+                if (list.n > 0) {
+                    tmem_load32(tmem + lanes + 384 + c, o);
+                    tmem_wait_loads(o);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 32; ++e)
+                        o[e] = 0;
+                }
+                if (row < u.lq) {
+                    uint16_t *out = static_cast<uint16_t *>(const_cast<void *>(f.dq.p)) +
+                                    ((int64_t)u.q_row + quarter * 32 + lane) * f.dq.ld + u.head * f.dq.hd + c;
+#pragma unroll
+                    for (int e = 0; e < 32; e += 8)
+                        if (c + e < a.dim) {
+                            uint32_t w[4];
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                w[i] = pack2<DT>(__uint_as_float(o[e + 2 * i]) * f.scale,
+                                                 __uint_as_float(o[e + 2 * i + 1]) * f.scale);
+                            *reinterpret_cast<uint4 *>(out + e) = make_uint4(w[0], w[1], w[2], w[3]);
+                        }
+                }
+                __syncwarp();
+            }
+        }
+    }
+
+    __syncwarp();
+    tmem_fence_before();
+    __syncthreads();
+    if (sh.gave_up) {
+        // copies and products may still be in flight: let them end before
+        // the memory that they use is given back
+        if (threadIdx.x == 0)
+            atomicAdd(&f.hdr->stalls, 1u);
+        const uint64_t began = global_ns();
+        while (global_ns() - began < 20000000u) {
+        }
+        // no result of this CTA is to be taken for one
+        for (int64_t i = blockIdx.x; i < all; i += gridDim.x) {
+            QueryUnit u;
+            if (!unit_at(i, u))
+                continue;
+            for (int32_t r = warp; r < 128 && u.first + r < u.lq; r += S::THREADS / 32)
+                for (int e = lane; e < a.dim; e += 32)
+                    static_cast<uint16_t *>(const_cast<void *>(f.dq.p))[((int64_t)u.q_row + r) * f.dq.ld + u.head * f.dq.hd + e] = 0x7fff;
+        }
+    }
+    if (warp == kMma)
+        tmem_free<1>(tmem, 512);
 }
 
 // ------------------------------------------------------------- host side
@@ -873,7 +1706,9 @@ Attn attn_of(const zero_attention_t *a)
     r.q_offsets = a->q_offsets, r.k_offsets = a->k_offsets, r.k_lengths = a->k_lengths;
     r.q_tokens = a->q_tokens, r.k_tokens = a->k_tokens, r.sequences = (int32_t)a->sequences;
     r.q_heads = a->q_heads, r.k_heads = a->k_heads, r.group = a->q_heads / a->k_heads, r.dim = a->head_dim;
-    r.window = (int32_t)(a->window < most ? a->window : most);
+    // (no window of a call sees further than all of its rows)
+    const int64_t rows = 1 + (a->q_tokens > a->k_tokens ? a->q_tokens : a->k_tokens);
+    r.window = (int32_t)(a->window < rows ? a->window : rows);
     r.sinks = (int32_t)(a->sinks < most ? a->sinks : most);
     r.scale = (float)a->scale;
     return r;
@@ -947,16 +1782,88 @@ int forward_tiles(const Fwd &f, const zero_attention_t *a, void *ws, cudaStream_
     return a->dtype == ZERO_F16 ? launch_tiles<ZERO_F16, 128>(t, st) : launch_tiles<ZERO_BF16, 128>(t, st);
 }
 
+// Whether first keys' tiles are dealt out, in parts of how many query tiles:
+// about what a tile of the window's keys has to do.  (Of more than 1024 first
+// keys every tile sees so much that there is enough to go round.)
+struct SinkPlan {
+    int32_t chunk, sink_tiles;
+    int64_t chunks, units;
+};
+
+SinkPlan plan_sinks(const zero_attention_t *a, bool one)
+{
+    SinkPlan p{};
+    if (a->sinks == 0 || a->sinks > 1024 || a->k_tokens == 0)
+        return p;
+    const int64_t tiles = a->window < a->q_tokens ? (a->window + 127) / 128 + 1 : a->q_tokens;
+    const int64_t chunk = tiles > 8 ? tiles : 8;
+    if (a->q_tokens <= 2 * chunk * 128)
+        return p;
+    p.chunk = (int32_t)chunk;
+    const int64_t keys = a->sinks < a->k_tokens ? a->sinks : a->k_tokens;
+    p.sink_tiles = (int32_t)((keys + 127) / 128);
+    p.chunks = tile_numbers(a->q_tokens, a->sequences, one, 128 * p.chunk);
+    p.units = p.chunks * p.sink_tiles * a->k_heads;
+    return p;
+}
+
 struct AttnSpace {
-    size_t delta, total;
+    size_t stats, partial, total;
 };
 
 AttnSpace attn_space(const zero_attention_t *a, bool backward)
 {
     AttnSpace s{};
-    s.delta = 256;
-    s.total = s.delta + (backward ? align256((size_t)a->q_heads * (size_t)a->q_tokens * 4) : 0);
+    s.stats = 256;
+    s.partial = s.stats;
+    if (backward)
+        s.partial += (size_t)a->q_heads * (size_t)tile_numbers(a->q_tokens, a->sequences, false, 128) * 1024;
+    s.total = s.partial;
+    if (backward)
+        s.total += align256((size_t)plan_sinks(a, false).units * 256 * (size_t)a->head_dim * 4);
     return s;
+}
+
+template <int DT, int DP>
+int launch_backward(const BwdTiles &t, cudaStream_t st)
+{
+    using S = BwdShape<DP>;
+    const char *what = "k_attn_dkv";
+    cudaError_t e = cudaSuccess;
+    auto launch = [&](void (*kernel)(BwdTiles), int64_t units) {
+        if (e != cudaSuccess || units == 0)
+            return;
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::SMEM);
+        if (e != cudaSuccess)
+            return;
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3((unsigned)(units < sm_count() ? units : sm_count()));
+        cfg.blockDim = dim3(S::THREADS);
+        cfg.dynamicSmemBytes = S::SMEM;
+        cfg.stream = st;
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[0].val.programmaticStreamSerializationAllowed = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = t.q_tiles > 0;  // (a kernel of this call is before it)
+        e = cudaLaunchKernelEx(&cfg, kernel, t);
+    };
+    launch(k_attn_dkv<DT, DP>, t.split_units + t.k_tiles * t.a.k_heads);
+    if (e == cudaSuccess && t.split_units > 0) {
+        what = "k_attn_join";
+        const int64_t blocks = (int64_t)t.a.sequences * t.sink_tiles * t.a.k_heads * 16;
+        e = launch_k(k_attn_join<DT>, (int)(blocks < 152 * 8 ? blocks : 152 * 8), kThreads, st, true, t);
+    }
+    if (e == cudaSuccess) {
+        what = "k_attn_dq";
+        launch(k_attn_dq<DT, DP>, t.q_tiles * t.a.q_heads);
+    }
+    if (e != cudaSuccess) {
+        cudaGetLastError();
+        set_cuda_error(what, (int)e, cudaGetErrorString(e));
+        return ZERO_ECUDA;
+    }
+    return ZERO_OK;
 }
 
 }  // namespace
@@ -1005,29 +1912,52 @@ extern "C" int zero_window_attention_backward(const zero_attention_t *a, const v
 {
     ZERO_TRY(check_attention(a));
     ZERO_TRY(check_offsets(a));
-    Bwd b{attn_of(a), {dout, dout_ld, dout_hd}, {q, q_ld, q_hd}, {k, k_ld, k_hd}, {v, v_ld, v_hd},
-          {out, out_ld, out_hd}, {dq, dq_ld, dq_hd}, {dk, dk_ld, dk_hd}, {dv, dv_ld, dv_hd}, lse, nullptr};
-    for (Heads *h : {&b.dout, &b.q, &b.out, &b.dq})
+    Heads hdout{dout, dout_ld, dout_hd}, hq{q, q_ld, q_hd}, hk{k, k_ld, k_hd}, hv{v, v_ld, v_hd}, hout{out, out_ld, out_hd};
+    Heads hdq{dq, dq_ld, dq_hd}, hdk{dk, dk_ld, dk_hd}, hdv{dv, dv_ld, dv_hd};
+    for (Heads *h : {&hdout, &hq, &hout, &hdq})
         ZERO_TRY(check_rows(h, a->q_tokens, a->q_heads, a->head_dim, a->dtype));
-    for (Heads *h : {&b.k, &b.v, &b.dk, &b.dv})
+    for (Heads *h : {&hk, &hv, &hdk, &hdv})
         ZERO_TRY(check_rows(h, a->k_tokens, a->k_heads, a->head_dim, a->dtype));
     ZERO_TRY(check_array(lse, a->q_tokens, ZERO_F32));
-    ZERO_TRY(check_workspace(ws, ws_bytes, attn_space(a, true).total));
-    b.delta = reinterpret_cast<float *>(static_cast<char *>(ws) + attn_space(a, true).delta);
+    const AttnSpace sp = attn_space(a, true);
+    ZERO_TRY(check_workspace(ws, ws_bytes, sp.total));
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    if (a->sequences == 0)
+    if (a->sequences == 0 || (a->q_tokens == 0 && a->k_tokens == 0))
         return ZERO_OK;
+    BwdTiles t{};
+    t.a = attn_of(a);
+    t.dq = hdq, t.dk = hdk, t.dv = hdv;
+    const bool one = !a->q_offsets;
+    t.q_tiles = a->q_tokens > 0 ? tile_numbers(a->q_tokens, a->sequences, one, 128) : 0;
+    t.k_tiles = a->k_tokens > 0 ? tile_numbers(a->k_tokens, a->sequences, one && !a->k_offsets, 128) : 0;
+    t.stats = reinterpret_cast<float *>(static_cast<char *>(ws) + sp.stats);
+    t.partial = reinterpret_cast<float *>(static_cast<char *>(ws) + sp.partial);
+    t.scale = (float)a->scale;
+    t.scale_log2 = (float)(a->scale * 1.4426950408889634);
+    t.hdr = static_cast<WsHeader *>(ws);
+    t.limit_ns = kWaitLimit;
     if (a->q_tokens > 0) {
-        auto kernel = a->dtype == ZERO_F16 ? k_attn_dq<ZERO_F16> : k_attn_dq<ZERO_BF16>;
-        const int64_t blocks = (a->q_tokens * a->q_heads + kWarps - 1) / kWarps;
-        kernel<<<grid_for(reinterpret_cast<const void *>(kernel), blocks, 1 << 30), kThreads, 0, st>>>(b);
-        ZERO_TRY(check_launch("k_attn_dq"));
+        ZERO_TRY(heads_map(&t.q, hq, a->q_tokens, a->q_heads, a->head_dim, a->dtype));
+        ZERO_TRY(heads_map(&t.dout, hdout, a->q_tokens, a->q_heads, a->head_dim, a->dtype));
     }
     if (a->k_tokens > 0) {
-        auto kernel = a->dtype == ZERO_F16 ? k_attn_dkv<ZERO_F16> : k_attn_dkv<ZERO_BF16>;
-        const int64_t blocks = (a->k_tokens * a->k_heads + kWarps - 1) / kWarps;
-        kernel<<<grid_for(reinterpret_cast<const void *>(kernel), blocks, 1 << 30), kThreads, 0, st>>>(b);
-        ZERO_TRY(check_launch("k_attn_dkv"));
+        ZERO_TRY(heads_map(&t.k, hk, a->k_tokens, a->k_heads, a->head_dim, a->dtype));
+        ZERO_TRY(heads_map(&t.v, hv, a->k_tokens, a->k_heads, a->head_dim, a->dtype));
     }
-    return ZERO_OK;
+    if (a->k_tokens == 0)  // (maps that nothing is loaded by, but that kernels name)
+        t.k = t.v = t.q;
+    if (a->q_tokens == 0)
+        t.q = t.dout = t.k;
+    if (a->q_tokens > 0) {
+        const SinkPlan p = plan_sinks(a, one);
+        t.chunk = p.chunk, t.sink_tiles = p.sink_tiles, t.chunks = p.chunks, t.split_units = p.units;
+        const StatsArgs s{t.a, hdout, hout, lse, const_cast<float *>(t.stats), t.q_tiles};
+        auto kernel = a->dtype == ZERO_F16 ? k_attn_stats<ZERO_F16> : k_attn_stats<ZERO_BF16>;
+        const int64_t blocks = (t.q_tiles * a->q_heads * 4 + kWarps - 1) / kWarps;
+        kernel<<<grid_for(reinterpret_cast<const void *>(kernel), blocks, 1 << 30), kThreads, 0, st>>>(s);
+        ZERO_TRY(check_launch("k_attn_stats"));
+    }
+    if (a->head_dim <= 64)
+        return a->dtype == ZERO_F16 ? launch_backward<ZERO_F16, 64>(t, st) : launch_backward<ZERO_BF16, 64>(t, st);
+    return a->dtype == ZERO_F16 ? launch_backward<ZERO_F16, 128>(t, st) : launch_backward<ZERO_BF16, 128>(t, st);
 }

@@ -145,6 +145,15 @@ __device__ __forceinline__ void tma_load3(uint32_t dst, const CUtensorMap *map, 
         : "memory");
 }
 
+// `bytes` (a multiple of 16) from global to shared memory, both on 16 bytes.
+// Their number counts down `bar`, which whoever arms it includes (mbar_expect).
+__device__ __forceinline__ void bulk_copy(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar)
+{
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+                 "l"(src), "r"(bytes), "r"(bar)
+                 : "memory");
+}
+
 // A box from shared memory to `map` at (x, y); what lies outside the matrix
 // is not written.  The issuing thread groups its stores (bulk_commit) and
 // waits until at most N groups still read their shared memory (the writes
