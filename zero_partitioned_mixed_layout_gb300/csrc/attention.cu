@@ -43,82 +43,11 @@ __device__ __forceinline__ Seq sequence(const Attn &a, int32_t s)
     return q;
 }
 
-// The sequence that holds row `row` of `offsets`: the last that starts at or
-// before it (-1: none).
-__device__ __forceinline__ int32_t sequence_of(const int64_t *offsets, int32_t n, int64_t row)
-{
-    if (!offsets)
-        return 0;
-    int32_t lo = -1, hi = n;  // offsets[lo] <= row < offsets[hi]
-    while (hi - lo > 1) {
-        const int32_t mid = lo + (hi - lo) / 2;
-        if (offsets[mid] <= row)
-            lo = mid;
-        else
-            hi = mid;
-    }
-    return lo;
-}
-
 struct Fwd {
     Attn a;
     Heads q, k, v, out;
     float *lse;
 };
-
-// A warp per query and head, key by key.
-template <int DT>
-__global__ void __launch_bounds__(kThreads) k_attn_rows(const __grid_constant__ Fwd f)
-{
-    const Attn &a = f.a;
-    const int lane = threadIdx.x & 31;
-    for (int64_t u = ((int64_t)blockIdx.x * kThreads + threadIdx.x) >> 5; u < a.q_tokens * a.q_heads;
-         u += (int64_t)gridDim.x * kWarps) {
-        const int64_t row = u / a.q_heads;
-        const int32_t h = (int32_t)(u - row * a.q_heads), g = h / a.group;
-        const int32_t s = sequence_of(a.q_offsets, a.sequences, row);
-        if (s < 0)
-            continue;
-        const Seq sq = sequence(a, s);
-        if (row - sq.q0 >= sq.lq)
-            continue;
-        const int32_t p = (int32_t)(row - sq.q0) + sq.lk - sq.lq;
-        float q[4] = {}, o[4] = {}, m = -INFINITY, l = 0.0f;
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-            if (lane + 32 * e < a.dim)
-                q[e] = load1<DT>(f.q.p, row * f.q.ld + h * f.q.hd + lane + 32 * e) * a.scale;
-        for (int32_t j = 0; j <= p; ++j) {
-            if (j >= a.sinks && j <= p - a.window) {
-                j = p - a.window;
-                continue;
-            }
-            const int64_t key = sq.k0 + j;
-            float t = 0.0f;
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                if (lane + 32 * e < a.dim)
-                    t += q[e] * load1<DT>(f.k.p, key * f.k.ld + g * f.k.hd + lane + 32 * e);
-#pragma unroll
-            for (int x = 16; x > 0; x >>= 1)
-                t += __shfl_xor_sync(0xffffffffu, t, x);
-            const float top = fmaxf(m, t), keep = m == -INFINITY ? 0.0f : __expf(m - top), w = __expf(t - top);
-            m = top;
-            l = l * keep + w;
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                if (lane + 32 * e < a.dim)
-                    o[e] = o[e] * keep + w * load1<DT>(f.v.p, key * f.v.ld + g * f.v.hd + lane + 32 * e);
-        }
-        const float inv = p < 0 ? 0.0f : 1.0f / l;
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-            if (lane + 32 * e < a.dim)
-                store1<DT>(const_cast<void *>(f.out.p), row * f.out.ld + h * f.out.hd + lane + 32 * e, o[e] * inv);
-        if (lane == 0 && f.lse)
-            f.lse[(int64_t)h * a.q_tokens + row] = p < 0 ? -INFINITY : m + logf(l);
-    }
-}
 
 // ------------------------------------------------------------- tiles
 
@@ -699,6 +628,305 @@ __global__ void __launch_bounds__(FwdShape<DP>::THREADS, 1) k_attn_tiles(const _
     }
     if (warp == kMma)
         tmem_free<1>(tmem, 512);
+}
+
+// ------------------------------------------------------------- a few queries
+
+// Of a few queries per sequence the keys' and values' bytes are all there is,
+// so every key head's are read once for all query heads of its group: 8 or 16
+// rows (NG groups of 8) of `tokens` queries and the heads of a group meet a
+// stretch of the keys in a block, 16 keys at a time per warp.  The products
+// are mma.sync's 16 x 8 x 16, whose N of 8 fits these rows (a tcgen05 tile
+// would be 128 rows of which 120 are empty), and keys and values go from
+// memory to registers in the operands' layout, 16 bytes per lane, without
+// shared memory between: S' = K Q^T has keys for rows, O' = V^T P' elements.
+struct FewArgs {
+    Attn a;
+    Heads q, k, v, out;
+    float *lse;
+    int64_t tiles;               // tile numbers of `tokens` queries
+    int32_t tokens, parts, splits;  // parts: sets of rows of one query's heads
+    float scale_log2;
+    uint32_t *tickets;           // one per set of rows, where splits > 1
+    float *partial;              // [set of rows][split][row][dim + 2]: the sums, the reference, the weights' sum
+};
+
+constexpr int kFewWarps = 4;
+
+__device__ __forceinline__ void mma16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                      uint32_t b1, bool bf16)
+{
+    if (bf16)
+        asm volatile(
+            "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+    else
+        asm volatile(
+            "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// Lane 4 i + j's pair (row i, columns 2 j and 2 j + 1 of 8 x 8) becomes
+// (row 2 j and 2 j + 1, column i).
+__device__ __forceinline__ uint32_t transpose8(uint32_t x)
+{
+    uint32_t y;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+
+template <int DT, int DP, int NG>
+__global__ void __launch_bounds__(kFewWarps * 32) k_attn_few(const __grid_constant__ FewArgs f)
+{
+    constexpr int R = 8 * NG, KK = DP / 32, JJ = DP / 64;
+    constexpr bool kBf16 = DT == ZERO_BF16;
+    __shared__ float s_o[kFewWarps][R][DP], s_m[kFewWarps][R], s_l[kFewWarps][R];
+    __shared__ uint32_t s_last;
+    const Attn &a = f.a;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
+    const int32_t split = blockIdx.x % f.splits;
+    const int64_t set = blockIdx.x / f.splits;
+    const int32_t part = (int32_t)(set % f.parts), kh = (int32_t)(set / f.parts % a.k_heads);
+    const TileAt at = find_tile(a, a.q_offsets, a.q_tokens, set / f.parts / a.k_heads, f.tokens, false, lane);
+    if (!at.any)
+        return;
+    // rows: the group's heads of each query in turn
+    const int32_t queries = at.s.lq - at.first < f.tokens ? at.s.lq - at.first : f.tokens;
+    const int32_t row0 = part * R, rows = queries * a.group - row0 < R ? queries * a.group - row0 : R;
+    const int32_t p0 = at.first + at.s.lk - at.s.lq, p1 = p0 + queries - 1;  // where the queries stand
+    // the keys that any of them sees, in a row: first keys, then the window's
+    const int32_t low = p0 >= a.window ? p0 - a.window + 1 : 0;
+    const int32_t sinks = p1 < 0 ? 0 : a.sinks < low ? a.sinks : low;
+    const int32_t n = p1 < 0 ? 0 : sinks + p1 - low + 1;
+    const int32_t per = ((n + f.splits - 1) / f.splits + 63) / 64 * 64;
+    const int32_t x0 = split * (int64_t)per < n ? split * per : n, x1 = n - x0 < per ? n : x0 + per;
+    const int32_t used = n > 0 ? (n + per - 1) / per : 1;  // blocks with keys (the first writes where there are none)
+
+    if (split < used) {
+        uint4 q[NG][KK], k[2][KK], v[4][JJ];
+        int32_t p[NG][2];
+#pragma unroll
+        for (int i = 0; i < NG; ++i) {
+            const int32_t r = row0 + 8 * i + g;  // of queries and heads
+            const bool live = 8 * i + g < rows;
+            const uint16_t *from = static_cast<const uint16_t *>(f.q.p) + (at.s.q0 + at.first + (live ? r / a.group : 0)) * f.q.ld +
+                                   (kh * a.group + (live ? r % a.group : 0)) * f.q.hd;
+#pragma unroll
+            for (int e = 0; e < KK; ++e)
+                q[i][e] = live && (c + 4 * e) * 8 < a.dim ? __ldg(reinterpret_cast<const uint4 *>(from) + c + 4 * e) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+                p[i][e] = p0 + (row0 + 8 * i + 2 * c + e) / a.group;
+        }
+        const uint16_t *const kp = static_cast<const uint16_t *>(f.k.p) + kh * f.k.hd;
+        const uint16_t *const vp = static_cast<const uint16_t *>(f.v.p) + kh * f.v.hd;
+        auto key = [&](int32_t x) { return at.s.k0 + (x < sinks ? x : low + x - sinks); };
+        auto load_k = [&](int32_t x) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const bool in = x + 8 * h + g < x1;
+                const uint4 *from = reinterpret_cast<const uint4 *>(kp + (in ? key(x + 8 * h + g) : 0) * f.k.ld);
+#pragma unroll
+                for (int e = 0; e < KK; ++e)
+                    k[h][e] = in && (c + 4 * e) * 8 < a.dim ? __ldg(from + c + 4 * e) : make_uint4(0, 0, 0, 0);
+            }
+        };
+        auto load_v = [&](int32_t x) {
+#pragma unroll
+            for (int h = 0; h < 4; ++h) {
+                const int32_t at_x = x + 2 * c + (h & 1) + (h >> 1) * 8;
+                const bool in = at_x < x1;
+                const uint4 *from = reinterpret_cast<const uint4 *>(vp + (in ? key(at_x) : 0) * f.v.ld);
+#pragma unroll
+                for (int e = 0; e < JJ; ++e)
+                    v[h][e] = in && (g + 8 * e) * 8 < a.dim ? __ldg(from + g + 8 * e) : make_uint4(0, 0, 0, 0);
+            }
+        };
+        auto word = [](const uint4 &x, int e) { return e == 0 ? x.x : e == 1 ? x.y : e == 2 ? x.z : x.w; };
+        float o[NG][JJ * 4][4] = {}, m[NG][2], l[NG][2] = {};
+#pragma unroll
+        for (int i = 0; i < NG; ++i)
+            m[i][0] = m[i][1] = -INFINITY;
+        const bool many = queries > 1;
+        int32_t x = x0 + warp * 16;
+        if (x < x1) {
+            load_k(x);
+            load_v(x);
+        }
+        for (; x < x1; x += 16 * kFewWarps) {
+            float t[NG][4] = {};
+#pragma unroll
+            for (int e = 0; e < KK; ++e)
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int i = 0; i < NG; ++i)
+                        mma16(t[i], word(k[0][e], 2 * h), word(k[1][e], 2 * h), word(k[0][e], 2 * h + 1),
+                              word(k[1][e], 2 * h + 1), word(q[i][e], 2 * h), word(q[i][e], 2 * h + 1), kBf16);
+            const int32_t x_next = x + 16 * kFewWarps;
+            if (x_next < x1)
+                load_k(x_next);
+            bool far = false;
+            float top[NG][2];
+#pragma unroll
+            for (int i = 0; i < NG; ++i) {
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int32_t at_x = x + 8 * h + g, j = at_x < sinks ? at_x : low + at_x - sinks;
+#pragma unroll
+                    for (int e = 0; e < 2; ++e)
+                        if (at_x >= x1 || (many && (j > p[i][e] || (j <= p[i][e] - a.window && j >= a.sinks))))
+                            t[i][2 * h + e] = -INFINITY;
+                }
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    top[i][e] = fmaxf(t[i][e], t[i][2 + e]);
+                    far = far || (top[i][e] > m[i][e] && (m[i][e] == -INFINITY || (top[i][e] - m[i][e]) * f.scale_log2 > 8.0f));
+                }
+            }
+            // the reference of a row's weights follows its largest score from up to 2^8 below
+            if (__any_sync(0xffffffffu, far)) {
+#pragma unroll
+                for (int i = 0; i < NG; ++i) {
+                    float keep[2];
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        float to = fmaxf(top[i][e], m[i][e]);
+#pragma unroll
+                        for (int b = 4; b < 32; b *= 2)
+                            to = fmaxf(to, __shfl_xor_sync(0xffffffffu, to, b));
+                        keep[e] = m[i][e] == -INFINITY ? 0.0f : exp2_fast((m[i][e] - to) * f.scale_log2);
+                        m[i][e] = to;
+                        l[i][e] *= keep[e];
+                    }
+#pragma unroll
+                    for (int b = 0; b < JJ * 4; ++b)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            o[i][b][e] *= keep[e & 1];
+                }
+            }
+            uint32_t w[NG][2];
+#pragma unroll
+            for (int i = 0; i < NG; ++i)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const float m0 = m[i][0] == -INFINITY ? 0.0f : m[i][0], m1 = m[i][1] == -INFINITY ? 0.0f : m[i][1];
+                    const float w0 = exp2_fast((t[i][2 * h] - m0) * f.scale_log2);
+                    const float w1 = exp2_fast((t[i][2 * h + 1] - m1) * f.scale_log2);
+                    l[i][0] += w0;
+                    l[i][1] += w1;
+                    w[i][h] = transpose8(pack2<DT>(w0, w1));
+                }
+#pragma unroll
+            for (int e = 0; e < JJ; ++e)
+#pragma unroll
+                for (int b = 0; b < 4; ++b) {
+                    const uint32_t v0 = word(v[0][e], b), v1 = word(v[1][e], b), v2 = word(v[2][e], b), v3 = word(v[3][e], b);
+                    const uint32_t a0 = __byte_perm(v0, v1, 0x5410), a1 = __byte_perm(v0, v1, 0x7632);
+                    const uint32_t a2 = __byte_perm(v2, v3, 0x5410), a3 = __byte_perm(v2, v3, 0x7632);
+#pragma unroll
+                    for (int i = 0; i < NG; ++i)
+                        mma16(o[i][e * 4 + b], a0, a1, a2, a3, w[i][0], w[i][1], kBf16);
+                }
+            if (x_next < x1)
+                load_v(x_next);
+        }
+        // the warps' sums, each with its reference
+#pragma unroll
+        for (int i = 0; i < NG; ++i) {
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+#pragma unroll
+                for (int b = 4; b < 32; b *= 2)
+                    l[i][e] += __shfl_xor_sync(0xffffffffu, l[i][e], b);
+                if (g == 0) {
+                    s_m[warp][8 * i + 2 * c + e] = m[i][e];
+                    s_l[warp][8 * i + 2 * c + e] = l[i][e];
+                }
+            }
+#pragma unroll
+            for (int e = 0; e < JJ; ++e)
+#pragma unroll
+                for (int b = 0; b < 4; ++b)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+                        *reinterpret_cast<float2 *>(&s_o[warp][8 * i + 2 * c + h][64 * e + 8 * g + 2 * b]) =
+                            make_float2(o[i][e * 4 + b][h], o[i][e * 4 + b][2 + h]);
+        }
+    }
+    __syncthreads();
+
+    // rows of a set are finished, or joined, element by element
+    auto finish = [&](int32_t r, int32_t e, float sum, float m, float l) {
+        const int32_t rr = row0 + r;
+        const int64_t row = at.s.q0 + at.first + rr / a.group;
+        const int32_t head = kh * a.group + rr % a.group;
+        store1<DT>(const_cast<void *>(f.out.p), row * f.out.ld + head * f.out.hd + e, l == 0.0f ? 0.0f : sum / l);
+        if (e == 0 && f.lse)
+            f.lse[(int64_t)head * a.q_tokens + row] = l == 0.0f ? -INFINITY : m * a.scale + logf(l);
+    };
+    const int32_t wide = a.dim + 2;
+    float *const mine = f.partial + (set * f.splits + split) * R * wide;
+    if (split < used)
+        for (int32_t i = threadIdx.x; i < rows * a.dim; i += kFewWarps * 32) {
+            const int32_t r = i / a.dim, e = i - r * a.dim;
+            float m = s_m[0][r], sum = 0.0f, l = 0.0f;
+#pragma unroll
+            for (int w = 1; w < kFewWarps; ++w)
+                m = fmaxf(m, s_m[w][r]);
+#pragma unroll
+            for (int w = 0; w < kFewWarps; ++w) {
+                const float by = s_m[w][r] == -INFINITY ? 0.0f : exp2_fast((s_m[w][r] - m) * f.scale_log2);
+                if (s_m[w][r] != -INFINITY || s_l[w][r] != 0.0f) {
+                    sum += s_o[w][r][e] * by;
+                    l += s_l[w][r] * by;
+                }
+            }
+            if (used == 1) {
+                finish(r, e, sum, m, l);
+            } else {
+                mine[r * wide + e] = sum;
+                if (e == 0) {
+                    mine[r * wide + a.dim] = m;
+                    mine[r * wide + a.dim + 1] = l;
+                }
+            }
+        }
+    if (used == 1)
+        return;
+    // the block that comes last joins all of a set's, in order
+    __threadfence();
+    __syncthreads();
+    if (threadIdx.x == 0)
+        s_last = atomicAdd(&f.tickets[set], 1u) == (uint32_t)f.splits - 1;
+    __syncthreads();
+    if (!s_last)
+        return;
+    __threadfence();
+    const float *const all = f.partial + set * f.splits * R * wide;
+    for (int32_t i = threadIdx.x; i < rows * a.dim; i += kFewWarps * 32) {
+        const int32_t r = i / a.dim, e = i - r * a.dim;
+        float m = -INFINITY, sum = 0.0f, l = 0.0f;
+#pragma unroll 8
+        for (int32_t w = 0; w < used; ++w)
+            m = fmaxf(m, __ldcg(all + (w * R + r) * wide + a.dim));
+#pragma unroll 4
+        for (int32_t w = 0; w < used; ++w) {
+            const float *const from = all + (w * R + r) * wide;
+            const float mw = __ldcg(from + a.dim), lw = __ldcg(from + a.dim + 1), ow = __ldcg(from + e);
+            const float by = mw == -INFINITY ? 0.0f : exp2_fast((mw - m) * f.scale_log2);
+            if (lw != 0.0f) {
+                sum += ow * by;
+                l += lw * by;
+            }
+        }
+        finish(r, e, sum, m, l);
+    }
+    if (threadIdx.x == 0)
+        f.tickets[set] = 0;
 }
 
 // ------------------------------------------------------------- backward
@@ -1782,6 +2010,62 @@ int forward_tiles(const Fwd &f, const zero_attention_t *a, void *ws, cudaStream_
     return a->dtype == ZERO_F16 ? launch_tiles<ZERO_F16, 128>(t, st) : launch_tiles<ZERO_BF16, 128>(t, st);
 }
 
+// Up to here, on average over the sequences, queries go a few rows at a time
+// over their keys instead of in tiles of 128.
+constexpr int64_t kFewQueries = 4;
+constexpr int kMostTickets = 4096, kMostSplits = 64;
+
+struct FewPlan {
+    int groups;  // of 8 rows
+    int32_t tokens, parts, splits;
+    int64_t tiles, sets;
+};
+
+FewPlan plan_few(const zero_attention_t *a, int64_t q_tokens, bool one)
+{
+    FewPlan p{};
+    const int64_t group = a->q_heads / a->k_heads, n = a->sequences > 0 ? a->sequences : 1;
+    const int64_t queries = (q_tokens + n - 1) / n;
+    p.groups = group * (queries > 1 ? queries : 1) > 8 ? 2 : 1;
+    const int64_t rows = 8 * p.groups;
+    p.tokens = (int32_t)(group < rows ? rows / group : 1);
+    p.parts = (int32_t)(group > rows ? (group + rows - 1) / rows : 1);
+    p.tiles = tile_numbers(q_tokens, a->sequences, one, p.tokens);
+    p.sets = p.tiles * a->k_heads * p.parts;
+    // blocks of at least 64 keys, until there are 4096
+    const int64_t rows_k = (a->k_tokens + n - 1) / n;
+    int64_t keys = a->window < rows_k ? a->window + (a->sinks < rows_k ? a->sinks : rows_k) + p.tokens : rows_k;
+    keys = keys < rows_k ? keys : rows_k;
+    int64_t splits = p.sets > 0 ? (kMostTickets + p.sets - 1) / p.sets : 1;
+    const int64_t most = (keys + 63) / 64 < kMostSplits ? (keys + 63) / 64 : kMostSplits;
+    splits = splits < most ? splits : most;
+    p.splits = (int32_t)(splits > 1 ? splits : 1);
+    return p;
+}
+
+template <int DT, int DP, int NG>
+int launch_few(const FewArgs &t, int64_t blocks, cudaStream_t st)
+{
+    k_attn_few<DT, DP, NG><<<(unsigned)blocks, kFewWarps * 32, 0, st>>>(t);
+    return check_launch("k_attn_few");
+}
+
+int forward_few(const Fwd &f, const zero_attention_t *a, void *ws, size_t partial, cudaStream_t st)
+{
+    const FewPlan p = plan_few(a, a->q_tokens, !a->q_offsets);
+    FewArgs t{f.a, f.q, f.k, f.v, f.out, f.lse, p.tiles, p.tokens, p.parts, p.splits, (float)(a->scale * 1.4426950408889634),
+              reinterpret_cast<uint32_t *>(static_cast<char *>(ws) + 256),
+              reinterpret_cast<float *>(static_cast<char *>(ws) + partial)};
+    const int64_t blocks = p.sets * p.splits;
+    if (blocks > 0x7fffffff)
+        return ZERO_ESIZE;
+#define ZERO_FEW(DT)                                                                                             \
+    (a->head_dim <= 64 ? p.groups == 1 ? launch_few<DT, 64, 1>(t, blocks, st) : launch_few<DT, 64, 2>(t, blocks, st) \
+                       : p.groups == 1 ? launch_few<DT, 128, 1>(t, blocks, st) : launch_few<DT, 128, 2>(t, blocks, st))
+    return a->dtype == ZERO_F16 ? ZERO_FEW(ZERO_F16) : ZERO_FEW(ZERO_BF16);
+#undef ZERO_FEW
+}
+
 // Whether first keys' tiles are dealt out, in parts of how many query tiles:
 // about what a tile of the window's keys has to do.  (Of more than 1024 first
 // keys every tile sees so much that there is enough to go round.)
@@ -1807,20 +2091,41 @@ SinkPlan plan_sinks(const zero_attention_t *a, bool one)
     return p;
 }
 
+// Workspace: the header, the tickets of a few queries' blocks (which start at
+// zero and are left at zero, so nothing else may lie there), and what a call
+// keeps: a few queries' partial sums, or the backward pass's rows and sums.
 struct AttnSpace {
-    size_t stats, partial, total;
+    size_t partial;         // of a few queries
+    size_t stats, sums;     // of the backward pass
+    size_t total;
 };
 
 AttnSpace attn_space(const zero_attention_t *a, bool backward)
 {
     AttnSpace s{};
-    s.stats = 256;
-    s.partial = s.stats;
-    if (backward)
-        s.partial += (size_t)a->q_heads * (size_t)tile_numbers(a->q_tokens, a->sequences, false, 128) * 1024;
-    s.total = s.partial;
-    if (backward)
-        s.total += align256((size_t)plan_sinks(a, false).units * 256 * (size_t)a->head_dim * 4);
+    s.partial = s.stats = 256 + kMostTickets * 4;
+    // (a workspace for more queries serves fewer; sets x splits is at most
+    // 4096 more than sets, and none where there is one split)
+    const int64_t most = kFewQueries * a->sequences, q = a->q_tokens < most ? a->q_tokens : most;
+    size_t few = 0;
+    for (int groups = 1; groups <= 2; ++groups) {
+        const int64_t rows = 8 * groups, group = a->q_heads / a->k_heads;
+        const int64_t parts = group > rows ? (group + rows - 1) / rows : 1;
+        const int64_t sets = tile_numbers(q, a->sequences, false, (int32_t)(group < rows ? rows / group : 1)) * a->k_heads * parts;
+        int64_t keys = a->window < a->k_tokens ? a->window + (a->sinks < a->k_tokens ? a->sinks : a->k_tokens) + rows : a->k_tokens;
+        keys = keys < a->k_tokens ? keys : a->k_tokens;
+        int64_t blocks = 2 * kMostTickets;
+        if (sets < kMostTickets)
+            blocks = sets * ((keys + 63) / 64) < sets + kMostTickets ? sets * ((keys + 63) / 64) : sets + kMostTickets;
+        const size_t bytes = (size_t)blocks * rows * (a->head_dim + 2) * 4;
+        few = few > bytes ? few : bytes;
+    }
+    s.total = s.partial + align256(few);
+    if (backward) {
+        s.sums = s.stats + (size_t)a->q_heads * (size_t)tile_numbers(a->q_tokens, a->sequences, false, 128) * 1024;
+        const size_t end = s.sums + align256((size_t)plan_sinks(a, false).units * 256 * (size_t)a->head_dim * 4);
+        s.total = s.total > end ? s.total : end;
+    }
     return s;
 }
 
@@ -1894,12 +2199,9 @@ extern "C" int zero_window_attention(const zero_attention_t *a, const void *q, i
     if (a->q_tokens == 0 || a->sequences == 0)
         return ZERO_OK;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    if (a->k_tokens > 0 && a->q_tokens > 4 * a->sequences)
+    if (a->q_tokens > kFewQueries * a->sequences && a->k_tokens > 0)
         return forward_tiles(f, a, ws, st);
-    auto kernel = a->dtype == ZERO_F16 ? k_attn_rows<ZERO_F16> : k_attn_rows<ZERO_BF16>;
-    const int64_t blocks = (a->q_tokens * a->q_heads + kWarps - 1) / kWarps;
-    kernel<<<grid_for(reinterpret_cast<const void *>(kernel), blocks, 1 << 30), kThreads, 0, st>>>(f);
-    return check_launch("k_attn_rows");
+    return forward_few(f, a, ws, attn_space(a, false).partial, st);
 }
 
 extern "C" int zero_window_attention_backward(const zero_attention_t *a, const void *dout, int64_t dout_ld,
@@ -1931,7 +2233,7 @@ extern "C" int zero_window_attention_backward(const zero_attention_t *a, const v
     t.q_tiles = a->q_tokens > 0 ? tile_numbers(a->q_tokens, a->sequences, one, 128) : 0;
     t.k_tiles = a->k_tokens > 0 ? tile_numbers(a->k_tokens, a->sequences, one && !a->k_offsets, 128) : 0;
     t.stats = reinterpret_cast<float *>(static_cast<char *>(ws) + sp.stats);
-    t.partial = reinterpret_cast<float *>(static_cast<char *>(ws) + sp.partial);
+    t.partial = reinterpret_cast<float *>(static_cast<char *>(ws) + sp.sums);
     t.scale = (float)a->scale;
     t.scale_log2 = (float)(a->scale * 1.4426950408889634);
     t.hdr = static_cast<WsHeader *>(ws);
