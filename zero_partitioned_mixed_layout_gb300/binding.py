@@ -1002,19 +1002,27 @@ def _attention_lib():
     return _attention
 
 
+_device_now = None
+
+
 def _call_on(device: int, f, *args):
     """f(*args) with `device` as the current one (kernels are launched there)."""
-    import torch
-    if torch.cuda.current_device() == device:
+    global _device_now
+    if _device_now is None:
+        import torch
+        torch.cuda.current_device()  # (CUDA is initialised)
+        _device_now = torch._C._cuda_getDevice
+    if _device_now() == device:
         return f(*args)
+    import torch
     with torch.cuda.device(device):
         return f(*args)
 
 
 def _on(t, what: str, device: int):
-    if not t.is_cuda:
-        raise ValueError(f"{what} must be a CUDA tensor")
-    if t.get_device() != device:
+    if t.get_device() != device or device < 0:
+        if not t.is_cuda:
+            raise ValueError(f"{what} must be a CUDA tensor")
         raise ValueError(f"{what} must be on the device of the queries")
     return t
 
@@ -1026,11 +1034,12 @@ def _heads(t, what: str, shape, dtype, device: int, written: bool = False):
         raise ValueError(f"{what} must be {' x '.join(map(str, shape))}")
     if t.dtype != dtype:
         raise TypeError(f"{what} must be {dtype}")
-    _on(t, what, device)
+    if t.get_device() != device or device < 0:
+        _on(t, what, device)
     ld, hd, inner = t.stride()
-    if shape[2] > 1 and inner != 1:
+    if inner != 1 and shape[2] > 1:
         raise ValueError(f"{what}: the elements of a head must be contiguous")
-    if written and ((ld == 0 and shape[0] > 1) or (hd == 0 and shape[1] > 1)):
+    if written and (ld == 0 or hd == 0) and ((ld == 0 and shape[0] > 1) or (hd == 0 and shape[1] > 1)):
         raise ValueError(f"{what}: rows of an output must not overlap")
     return t.data_ptr(), ld, hd
 
@@ -1072,14 +1081,19 @@ class Rotary:
         return bool(self._c.interleaved)
 
 
+_int64 = None
+
+
 def _int64_pointer(t, what: str, n: int, device: int):
-    import torch
+    global _int64
     if t is None:
         return None
-    if t.dtype != torch.int64:
+    if _int64 is None:
+        import torch
+        _int64 = torch.int64
+    if t.dtype != _int64:
         raise TypeError(f"{what} must be int64")
-    _on(t, what, device)
-    return _vector(t, what, n)
+    return _vector(_on(t, what, device), what, n)
 
 
 def _rotary_args(rotary, positions, tokens: int, device: int):
