@@ -137,6 +137,11 @@ __device__ __forceinline__ uint32_t seen_bits(int32_t p, int32_t window, int32_t
     return bits_up_to(p - first) & (~bits_up_to(low - first - 1) | bits_up_to(sinks - first - 1));
 }
 
+// A value that all lanes of a warp hold, in a form that the compiler can tell:
+// loops over it are then uniform, and so are the operands of the products
+// issued in them.
+__device__ __forceinline__ int32_t uniform(int32_t x) { return __shfl_sync(0xffffffffu, x, 0); }
+
 // The key tiles of 128 queries, and of two such tiles.
 struct KeyTiles {
     int32_t low, high;  // of the window
@@ -190,6 +195,12 @@ struct Unit {
     int32_t q_row, k_row;  // of the unit's first query, and the sequence's first key
     int32_t first, lq, lk, head;
     int32_t end;
+
+    __device__ __forceinline__ void agree()
+    {
+        q_row = uniform(q_row), k_row = uniform(k_row), first = uniform(first), lq = uniform(lq), lk = uniform(lk);
+        head = uniform(head), end = uniform(end);
+    }
 };
 
 struct FwdTiles {
@@ -205,6 +216,23 @@ struct FwdTiles {
 
 constexpr int kUnitRing = 4;
 
+// D = A B^T over the elements of a head (16 to a step), in boxes of 64.
+template <int DP>
+__device__ __forceinline__ void inner_products(uint32_t d, uint64_t a, uint64_t b, uint32_t desc, int steps)
+{
+    tensor_products4<2, 2>(d, a, b, desc, false, steps);
+    if (DP == 128 && steps > 4)
+        tensor_products4<2, 2>(d, a + (16384 >> 4), b + (16384 >> 4), desc, true, steps - 4);
+}
+
+// D (+)= A B over 128 rows of B, A in tensor memory, 64 elements each from
+// a and from a + 64 on.
+__device__ __forceinline__ void outer_products(uint32_t d, uint32_t a, uint64_t b, uint32_t desc, bool add)
+{
+    tensor_products4_tmem<128>(d, a, b, desc, add);
+    tensor_products4_tmem<128>(d, a + 64, b + 512, desc, true);
+}
+
 template <int DP>
 struct FwdShape {
     static constexpr int BOXES = DP / 64, TILE = BOXES * 16384;  // bytes of 128 rows
@@ -214,7 +242,7 @@ struct FwdShape {
 };
 
 struct FwdShared {
-    uint64_t q_full[2], q_empty[2], k_full[4], k_empty[4], v_full[4], v_empty[4], s_full[2], p_full[2], o_full[2];
+    uint64_t q_full[2], q_empty[2], k_full[4], k_empty[4], v_full[4], v_empty[4], s_full[2], p_full[2][2], o_full[2];
     uint64_t unit_full[kUnitRing], unit_empty[kUnitRing];
     Unit units[kUnitRing];
     uint32_t tmem, gave_up;
@@ -230,7 +258,7 @@ __global__ void __launch_bounds__(FwdShape<DP>::THREADS, 1) k_attn_tiles(const _
     unsigned char *smem = smem_raw + ((1024 - (smem_addr(smem_raw) & 1023u)) & 1023u);
     unsigned char *const s_q = smem, *const s_k = smem + 2 * S::TILE, *const s_v = s_k + S::STAGES * S::TILE;
     const Attn &a = f.a;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
     constexpr int kTma = 8, kMma = 9;
 
     if (threadIdx.x == 0) {
@@ -238,7 +266,8 @@ __global__ void __launch_bounds__(FwdShape<DP>::THREADS, 1) k_attn_tiles(const _
             mbar_init_count(&sh.q_full[t], 1);
             mbar_init_count(&sh.q_empty[t], 1);
             mbar_init_count(&sh.s_full[t], 1);
-            mbar_init_count(&sh.p_full[t], 4);
+            mbar_init_count(&sh.p_full[t][0], 4);
+            mbar_init_count(&sh.p_full[t][1], 4);
             mbar_init_count(&sh.o_full[t], 1);
         }
         for (int s = 0; s < S::STAGES; ++s) {
@@ -261,7 +290,7 @@ __global__ void __launch_bounds__(FwdShape<DP>::THREADS, 1) k_attn_tiles(const _
     tmem_fence_before();
     __syncthreads();
     tmem_fence_after();
-    const uint32_t tmem = sh.tmem;
+    const uint32_t tmem = (uint32_t)uniform((int32_t)sh.tmem);
     auto wait = [&](uint64_t *bar, uint32_t parity) { return mbar_wait_warp(bar, parity, f.limit_ns, &sh.gave_up); };
     // the next unit, from the loading warp
     uint32_t units = 0;
@@ -270,6 +299,7 @@ __global__ void __launch_bounds__(FwdShape<DP>::THREADS, 1) k_attn_tiles(const _
         if (!wait(&sh.unit_full[slot], (units / kUnitRing) & 1))
             return false;
         u = sh.units[slot];
+        u.agree();
         __syncwarp();
         if (lane == 0)
             mbar_arrive_cluster(smem_addr(&sh.unit_empty[slot]));
@@ -358,17 +388,12 @@ __global__ void __launch_bounds__(FwdShape<DP>::THREADS, 1) k_attn_tiles(const _
             const TileList list = tile_list(kt2[0], kt2[1]);
             // S_t = Q_t K^T of the n-th tile
             auto scores = [&](int t, uint32_t stage) {
-                if (elect_one()) {
-                    const uint64_t dq = q0 + ((t * S::TILE) >> 4), dk = k0 + ((stage * S::TILE) >> 4);
-                    for (int s = 0; s < steps; ++s) {
-                        const uint32_t off = (s >> 2) * (16384 >> 4) + (s & 3) * 2;
-                        tensor_product<1>(tmem + t * 128, dq + off, dk + off, desc_s, s != 0);
-                    }
-                    tensor_commit<1>(&sh.s_full[t]);
-                }
-                __syncwarp();
+                inner_products<DP>(tmem + t * 128, q0 + ((t * S::TILE) >> 4), k0 + ((stage * S::TILE) >> 4), desc_s, steps);
+                tensor_commit_elected(&sh.s_full[t]);
             };
             bool first[2] = {true, true};
+            // (the tiles of first keys come last, down to 0; without them the window's end with its lowest)
+            const int32_t last[2] = {kt2[0].sinks && kt2[0].low ? 0 : kt2[0].low, kt2[1].sinks && kt2[1].low ? 0 : kt2[1].low};
             for (int32_t n = 0; ok && n <= list.n; ++n) {
                 const int32_t kt = n < list.n ? list.at(n) : -1, before = n > 0 ? list.at(n - 1) : -1;
                 const uint32_t ks = kn % S::STAGES, vs = vn % S::STAGES;
@@ -379,25 +404,22 @@ __global__ void __launch_bounds__(FwdShape<DP>::THREADS, 1) k_attn_tiles(const _
                         if (!v_here)
                             ok = ok && wait(&sh.v_full[vs], (vn / S::STAGES) & 1);
                         v_here = true;
-                        ok = ok && wait(&sh.p_full[t], pn[t] & 1);
+                        // the later keys' weights come first
+                        const uint64_t dv = v0 + ((vs * S::TILE) >> 4);
+#pragma unroll
+                        for (int h = 1; h >= 0; --h) {
+                            ok = ok && wait(&sh.p_full[t][h], pn[t] & 1);
+                            if (!ok)
+                                break;
+                            tmem_fence_after();
+                            tensor_products4_tmem<128>(tmem + 256 + t * 128, tmem + t * 128 + 64 + h * 32, dv + h * 512,
+                                                       desc_o, !first[t] || h == 0);
+                        }
                         ++pn[t];
                         if (!ok)
                             break;
-                        tmem_fence_after();
-                        if (elect_one()) {
-                            const uint64_t dv = v0 + ((vs * S::TILE) >> 4);
-#pragma unroll
-                            for (int s = 0; s < 8; ++s)
-                                tensor_product_tmem(tmem + 256 + t * 128, tmem + t * 128 + s * 8, dv + s * 128, desc_o,
-                                                    !first[t] || s != 0);
-                            // the last product of this tile of queries?
-                            bool more = false;
-                            for (int32_t m = n; m < list.n && !more; ++m)
-                                more = needs(kt2[t], list.at(m));
-                            if (!more)
-                                tensor_commit<1>(&sh.o_full[t]);
-                        }
-                        __syncwarp();
+                        if (before == last[t])
+                            tensor_commit_elected(&sh.o_full[t]);
                         first[t] = false;
                     }
                     if (kt >= 0 && needs(kt2[t], kt)) {
@@ -414,19 +436,16 @@ __global__ void __launch_bounds__(FwdShape<DP>::THREADS, 1) k_attn_tiles(const _
                 }
                 if (!ok)
                     break;
-                if (elect_one()) {
-                    if (n > 0)
-                        tensor_commit<1>(&sh.v_empty[vs]);
-                    if (kt >= 0)
-                        tensor_commit<1>(&sh.k_empty[ks]);
-                    if (n + 1 == list.n) {
-                        if (kt2[0].any)
-                            tensor_commit<1>(&sh.q_empty[0]);
-                        if (kt2[1].any)
-                            tensor_commit<1>(&sh.q_empty[1]);
-                    }
+                if (n > 0)
+                    tensor_commit_elected(&sh.v_empty[vs]);
+                if (kt >= 0)
+                    tensor_commit_elected(&sh.k_empty[ks]);
+                if (n + 1 == list.n) {
+                    if (kt2[0].any)
+                        tensor_commit_elected(&sh.q_empty[0]);
+                    if (kt2[1].any)
+                        tensor_commit_elected(&sh.q_empty[1]);
                 }
-                __syncwarp();
                 vn += n > 0;
                 kn += kt >= 0;
             }
@@ -461,32 +480,40 @@ __global__ void __launch_bounds__(FwdShape<DP>::THREADS, 1) k_attn_tiles(const _
                 const int32_t k_first = kt * 128;
                 const bool whole = k_first + 127 <= p_first &&
                                    (k_first > p_last - a.window || k_first + 127 < a.sinks);
-                uint32_t r[2][32];
-                auto load = [&](int c) {  // 64 scores from column 64 c on
-                    tmem_load32(at_s + 64 * c, r[0]);
-                    tmem_load32(at_s + 64 * c + 32, r[1]);
-                    tmem_wait_loads(r[0]);
-                    tmem_wait_loads(r[1]);
+                // Four pieces of 32 scores: once for the largest, the last two
+                // then stay in registers, and the first two come again.
+                uint32_t r0[32], r1[32], r2[32];
+                auto hide = [&](uint32_t (&r)[32], int c) {
                     if (!whole) {
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            const uint32_t bits = seen_bits(p, a.window, a.sinks, k_first + 64 * c + 32 * h);
-#pragma unroll
-                            for (int e = 0; e < 32; ++e)
-                                r[h][e] = bits & (1u << e) ? r[h][e] : 0xff800000u;
-                        }
-                    }
-                };
-                float top = -INFINITY;
-#pragma unroll
-                for (int c = 1; c >= 0; --c) {
-                    load(c);
-#pragma unroll
-                    for (int h = 0; h < 2; ++h)
+                        const uint32_t bits = seen_bits(p, a.window, a.sinks, k_first + 32 * c);
 #pragma unroll
                         for (int e = 0; e < 32; ++e)
-                            top = fmaxf(top, __uint_as_float(r[h][e]));
-                }
+                            r[e] = bits & (1u << e) ? r[e] : 0xff800000u;
+                    }
+                };
+                float tops[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                auto largest = [&](uint32_t (&r)[32], int c) {
+                    hide(r, c);
+#pragma unroll
+                    for (int e = 0; e < 32; e += 8)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            tops[i] = fmaxf(fmaxf(tops[i], __uint_as_float(r[e + i])), __uint_as_float(r[e + 4 + i]));
+                };
+                tmem_load32(at_s, r0);
+                tmem_wait_loads(r0);
+                tmem_load32(at_s + 32, r1);
+                largest(r0, 0);
+                tmem_wait_loads(r1);
+                tmem_load32(at_s + 64, r0);
+                largest(r1, 1);
+                tmem_wait_loads(r0);
+                tmem_load32(at_s + 96, r1);
+                largest(r0, 2);
+                tmem_wait_loads(r1);
+                tmem_load32(at_s + 32, r2);
+                largest(r1, 3);
+                const float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
                 // The weights' reference is the largest score so far, or up to
                 // 2^8 below it: the weights stay below 2^8, and sums are
                 // rarely multiplied anew.
@@ -512,27 +539,30 @@ __global__ void __launch_bounds__(FwdShape<DP>::THREADS, 1) k_attn_tiles(const _
                     l *= keep;
                     m = to;
                 }
-                const float base = m == -INFINITY ? 0.0f : m * sl;
-                float sum[4] = {};
+                const F2 scale2 = twice(sl), base2 = twice(m == -INFINITY ? 0.0f : -m * sl);
+                F2 sums[2] = {{0.0f, 0.0f}, {0.0f, 0.0f}};
+                // The weights go where scores were that are no longer needed:
+                // those of piece c into the 16 columns from 64 + 16 c on.
+                auto weigh = [&](const uint32_t (&r)[32], int c) {
+                    uint32_t w[16];
 #pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    if (c)  // the others again: all 128 do not fit the registers
-                        load(c);
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        uint32_t w[16];
-#pragma unroll
-                        for (int e = 0; e < 16; ++e) {
-                            const float w0 = exp2_fast(__uint_as_float(r[h][2 * e]) * sl - base);
-                            const float w1 = exp2_fast(__uint_as_float(r[h][2 * e + 1]) * sl - base);
-                            sum[e & 1] += w0;
-                            sum[2 + (e & 1)] += w1;
-                            w[e] = pack2<DT>(w0, w1);
-                        }
-                        tmem_store16(at_s + 32 * c + 16 * h, w);
+                    for (int e = 0; e < 16; ++e) {
+                        F2 x = fma2({__uint_as_float(r[2 * e]), __uint_as_float(r[2 * e + 1])}, scale2, base2);
+                        x = {exp2_fast(x.x), exp2_fast(x.y)};
+                        sums[e & 1] = sums[e & 1] + x;
+                        w[e] = pack2<DT>(x.x, x.y);
                     }
-                }
-                l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                    tmem_store16(at_s + 64 + 16 * c, w);
+                };
+                auto ready = [&](int h) {
+                    tmem_wait_stores();
+                    tmem_fence_before();
+                    __syncwarp();
+                    if (lane == 0)
+                        mbar_arrive_cluster(smem_addr(&sh.p_full[t][h]));
+                };
+                weigh(r1, 3);
+                weigh(r0, 2);
                 if (k_first + 128 > u.lk) {
                     // rows behind the last key: zeros, since 0 times what they hold may not be 0
                     const uint32_t now = vn + n, vs = now % S::STAGES;
@@ -547,11 +577,16 @@ __global__ void __launch_bounds__(FwdShape<DP>::THREADS, 1) k_attn_tiles(const _
                             *reinterpret_cast<uint4 *>(s_v + vs * S::TILE + b * 16384 + i * 16) = make_uint4(0, 0, 0, 0);
                     fence_proxy_async();
                 }
-                tmem_wait_stores();
-                tmem_fence_before();
-                __syncwarp();
-                if (lane == 0)
-                    mbar_arrive_cluster(smem_addr(&sh.p_full[t]));
+                tmem_wait_loads(r2);
+                ready(1);
+                tmem_load32(at_s, r0);
+                hide(r2, 1);
+                weigh(r2, 1);
+                tmem_wait_loads(r0);
+                hide(r0, 0);
+                weigh(r0, 0);
+                ready(0);
+                l += (sums[0].x + sums[0].y) + (sums[1].x + sums[1].y);
             }
             vn += list.n;
             if (!ok)
@@ -1035,6 +1070,12 @@ struct KeyUnit {
     int64_t stats;                              // tile number of query tile 0
     int64_t slot;                               // of the partial sums, or -1
     int32_t end;
+
+    __device__ __forceinline__ void agree()
+    {
+        first = uniform(first), lq = uniform(lq), lk = uniform(lk), head = uniform(head);
+        low = uniform(low), high = uniform(high), end = uniform(end);
+    }
 };
 
 template <int DP>
@@ -1110,7 +1151,7 @@ __global__ void __launch_bounds__(BwdShape<DP>::THREADS, 1) k_attn_dkv(const __g
     unsigned char *const s_k = smem, *const s_v = smem + S::TILE, *const s_q = s_v + S::TILE, *const s_o = s_q + 2 * S::TILE;
     float *const s_stats = reinterpret_cast<float *>(s_o + 2 * S::TILE);  // [stage][lse2, delta][128]
     const Attn &a = f.a;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
     constexpr int kTma = 8, kMma = 9;
 
     if (threadIdx.x == 0) {
@@ -1141,7 +1182,7 @@ __global__ void __launch_bounds__(BwdShape<DP>::THREADS, 1) k_attn_dkv(const __g
     tmem_fence_before();
     __syncthreads();
     tmem_fence_after();
-    const uint32_t tmem = sh.tmem;
+    const uint32_t tmem = (uint32_t)uniform((int32_t)sh.tmem);
     pdl_launch_next();
     pdl_wait();
     auto wait = [&](uint64_t *bar, uint32_t parity) { return mbar_wait_warp(bar, parity, f.limit_ns, &sh.gave_up); };
@@ -1151,6 +1192,7 @@ __global__ void __launch_bounds__(BwdShape<DP>::THREADS, 1) k_attn_dkv(const __g
         if (!wait(&sh.unit_full[slot], (units / kUnitRing) & 1))
             return false;
         u = sh.units[slot];
+        u.agree();
         __syncwarp();
         if (lane == 0)
             mbar_arrive_cluster(smem_addr(&sh.unit_empty[slot]));
@@ -1237,19 +1279,6 @@ __global__ void __launch_bounds__(BwdShape<DP>::THREADS, 1) k_attn_dkv(const __g
         uint32_t kvn = 0, qn = 0, n = 0;
         bool ok = true;
         KeyUnit u;
-        // D = A B^T over the head's elements
-        auto inner = [&](uint32_t d, uint64_t x, uint64_t y) {
-            for (int s = 0; s < steps; ++s) {
-                const uint32_t off = (s >> 2) * (16384 >> 4) + (s & 3) * 2;
-                tensor_product<1>(d, x + off, y + off, desc_s, s != 0);
-            }
-        };
-        // D += A B over 128 queries, A in tensor memory (each half where its scores were)
-        auto outer = [&](uint32_t d, uint32_t x, uint64_t y, bool add) {
-#pragma unroll
-            for (int s = 0; s < 8; ++s)
-                tensor_product_tmem(d, x + (s >> 2) * 64 + (s & 3) * 8, y + s * 128, desc_acc, add || s != 0);
-        };
         while (ok && next(u)) {
             const int32_t count = u.low > u.high ? 0 : (u.high - u.low + 1) * a.group;
             if (count == 0)
@@ -1259,56 +1288,41 @@ __global__ void __launch_bounds__(BwdShape<DP>::THREADS, 1) k_attn_dkv(const __g
                 break;
             ++kvn;
             tmem_fence_after();
-            if (elect_one()) {
-                inner(tmem, dk0, dq0 + (((qn & 1) * S::TILE) >> 4));
-                tensor_commit<1>(&sh.s_full);
-            }
-            __syncwarp();
+            inner_products<DP>(tmem, dk0, dq0 + (((qn & 1) * S::TILE) >> 4), desc_s, steps);
+            tensor_commit_elected(&sh.s_full);
             for (int32_t i = 0; i < count; ++i, ++qn, ++n) {
                 const uint32_t st = qn & 1;
                 ok = wait(&sh.o_full[st], (qn >> 1) & 1);
                 if (!ok)
                     break;
                 tmem_fence_after();
-                if (elect_one()) {
-                    inner(tmem + 128, dv0, do0 + ((st * S::TILE) >> 4));
-                    tensor_commit<1>(&sh.dp_full);
-                }
-                __syncwarp();
+                inner_products<DP>(tmem + 128, dv0, do0 + ((st * S::TILE) >> 4), desc_s, steps);
+                tensor_commit_elected(&sh.dp_full);
                 ok = wait(&sh.p_full, n & 1);
                 if (!ok)
                     break;
                 tmem_fence_after();
-                if (elect_one()) {
-                    outer(tmem + 256, tmem, to0 + ((st * S::TILE) >> 4), i != 0);
-                    tensor_commit<1>(&sh.o_empty[st]);
-                }
-                __syncwarp();
+                outer_products(tmem + 256, tmem, to0 + ((st * S::TILE) >> 4), desc_acc, i != 0);
+                tensor_commit_elected(&sh.o_empty[st]);
                 if (i + 1 < count) {
                     const uint32_t to = (qn + 1) & 1;
                     ok = wait(&sh.q_full[to], ((qn + 1) >> 1) & 1);
                     if (!ok)
                         break;
                     tmem_fence_after();
-                    if (elect_one()) {
-                        inner(tmem, dk0, dq0 + ((to * S::TILE) >> 4));
-                        tensor_commit<1>(&sh.s_full);
-                    }
-                    __syncwarp();
+                    inner_products<DP>(tmem, dk0, dq0 + ((to * S::TILE) >> 4), desc_s, steps);
+                    tensor_commit_elected(&sh.s_full);
                 }
                 ok = wait(&sh.ds_full, n & 1);
                 if (!ok)
                     break;
                 tmem_fence_after();
-                if (elect_one()) {
-                    outer(tmem + 384, tmem + 128, tq0 + ((st * S::TILE) >> 4), i != 0);
-                    tensor_commit<1>(&sh.q_empty[st]);
-                    if (i + 1 == count) {
-                        tensor_commit<1>(&sh.kv_empty);
-                        tensor_commit<1>(&sh.acc_full);
-                    }
+                outer_products(tmem + 384, tmem + 128, tq0 + ((st * S::TILE) >> 4), desc_acc, i != 0);
+                tensor_commit_elected(&sh.q_empty[st]);
+                if (i + 1 == count) {
+                    tensor_commit_elected(&sh.kv_empty);
+                    tensor_commit_elected(&sh.acc_full);
                 }
-                __syncwarp();
             }
         }
     } else {
@@ -1537,6 +1551,11 @@ struct QueryUnit {
     int32_t q_row, k_row, first, lq, lk, head;
     int64_t stats;  // tile number
     int32_t end;
+
+    __device__ __forceinline__ void agree()
+    {
+        first = uniform(first), lq = uniform(lq), lk = uniform(lk), head = uniform(head), end = uniform(end);
+    }
 };
 
 struct QueryShared {
@@ -1559,7 +1578,7 @@ __global__ void __launch_bounds__(BwdShape<DP>::THREADS, 1) k_attn_dq(const __gr
     unsigned char *smem = smem_raw + ((1024 - (smem_addr(smem_raw) & 1023u)) & 1023u);
     unsigned char *const s_q = smem, *const s_o = smem + S::TILE, *const s_k = s_o + S::TILE, *const s_v = s_k + 2 * S::TILE;
     const Attn &a = f.a;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
     constexpr int kTma = 8, kMma = 9;
 
     if (threadIdx.x == 0) {
@@ -1588,7 +1607,7 @@ __global__ void __launch_bounds__(BwdShape<DP>::THREADS, 1) k_attn_dq(const __gr
     tmem_fence_before();
     __syncthreads();
     tmem_fence_after();
-    const uint32_t tmem = sh.tmem;
+    const uint32_t tmem = (uint32_t)uniform((int32_t)sh.tmem);
     pdl_launch_next();
     pdl_wait();
     auto wait = [&](uint64_t *bar, uint32_t parity) { return mbar_wait_warp(bar, parity, f.limit_ns, &sh.gave_up); };
@@ -1598,6 +1617,7 @@ __global__ void __launch_bounds__(BwdShape<DP>::THREADS, 1) k_attn_dq(const __gr
         if (!wait(&sh.unit_full[slot], (units / kUnitRing) & 1))
             return false;
         u = sh.units[slot];
+        u.agree();
         __syncwarp();
         if (lane == 0)
             mbar_arrive_cluster(smem_addr(&sh.unit_empty[slot]));
@@ -1690,12 +1710,6 @@ __global__ void __launch_bounds__(BwdShape<DP>::THREADS, 1) k_attn_dq(const __gr
         uint32_t un = 0, kn = 0, dsn = 0;
         bool ok = true;
         QueryUnit u;
-        auto inner = [&](uint32_t d, uint64_t x, uint64_t y) {
-            for (int s = 0; s < steps; ++s) {
-                const uint32_t off = (s >> 2) * (16384 >> 4) + (s & 3) * 2;
-                tensor_product<1>(d, x + off, y + off, desc_s, s != 0);
-            }
-        };
         while (ok && next(u)) {
             const KeyTiles kt = key_tiles(a, u.first, u.lq, u.lk);
             const TileList list = tile_list(kt, KeyTiles{0, -1, 0, false});
@@ -1710,9 +1724,7 @@ __global__ void __launch_bounds__(BwdShape<DP>::THREADS, 1) k_attn_dq(const __gr
                 if (!ok)
                     return;
                 tmem_fence_after();
-                if (elect_one())
-                    inner(tmem + st * 128, dq0, dk0 + ((st * S::TILE) >> 4));
-                __syncwarp();
+                inner_products<DP>(tmem + st * 128, dq0, dk0 + ((st * S::TILE) >> 4), desc_s, steps);
             };
             auto grads = [&](uint32_t at) {
                 const uint32_t st = at & 1;
@@ -1720,12 +1732,9 @@ __global__ void __launch_bounds__(BwdShape<DP>::THREADS, 1) k_attn_dq(const __gr
                 if (!ok)
                     return;
                 tmem_fence_after();
-                if (elect_one()) {
-                    inner(tmem + 256, do0, dv0 + ((st * S::TILE) >> 4));
-                    tensor_commit<1>(&sh.sp_full);
-                    tensor_commit<1>(&sh.v_empty[st]);
-                }
-                __syncwarp();
+                inner_products<DP>(tmem + 256, do0, dv0 + ((st * S::TILE) >> 4), desc_s, steps);
+                tensor_commit_elected(&sh.sp_full);
+                tensor_commit_elected(&sh.v_empty[st]);
             };
             scores(kn);
             grads(kn);
@@ -1741,18 +1750,12 @@ __global__ void __launch_bounds__(BwdShape<DP>::THREADS, 1) k_attn_dq(const __gr
                     grads(kn + 1);
                 if (!ok)
                     break;
-                if (elect_one()) {
-#pragma unroll
-                    for (int s = 0; s < 8; ++s)
-                        tensor_product_tmem(tmem + 384, tmem + st * 128 + (s >> 2) * 64 + (s & 3) * 8,
-                                            tk0 + ((st * S::TILE) >> 4) + s * 128, desc_acc, n != 0 || s != 0);
-                    tensor_commit<1>(&sh.k_empty[st]);
-                    if (n + 1 == list.n) {
-                        tensor_commit<1>(&sh.q_empty);
-                        tensor_commit<1>(&sh.acc_full);
-                    }
+                outer_products(tmem + 384, tmem + st * 128, tk0 + ((st * S::TILE) >> 4), desc_acc, n != 0);
+                tensor_commit_elected(&sh.k_empty[st]);
+                if (n + 1 == list.n) {
+                    tensor_commit_elected(&sh.q_empty);
+                    tensor_commit_elected(&sh.acc_full);
                 }
-                __syncwarp();
             }
         }
     } else {

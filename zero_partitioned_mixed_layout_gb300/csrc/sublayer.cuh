@@ -44,6 +44,48 @@ __device__ __forceinline__ void store1_as(int32_t dt, void *p, int64_t i, float 
         store1<ZERO_BF16>(p, i, v);
 }
 
+// Two binary32 in one instruction.
+struct F2 {
+    float x, y;
+};
+
+__device__ __forceinline__ unsigned long long bits(F2 a)
+{
+    unsigned long long r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a.x), "f"(a.y));
+    return r;
+}
+
+__device__ __forceinline__ F2 pair(unsigned long long a)
+{
+    F2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a));
+    return r;
+}
+
+__device__ __forceinline__ F2 operator*(F2 a, F2 b)
+{
+    unsigned long long r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(bits(a)), "l"(bits(b)));
+    return pair(r);
+}
+
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c)
+{
+    unsigned long long r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(bits(a)), "l"(bits(b)), "l"(bits(c)));
+    return pair(r);
+}
+
+__device__ __forceinline__ F2 operator+(F2 a, F2 b)
+{
+    unsigned long long r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(bits(a)), "l"(bits(b)));
+    return pair(r);
+}
+
+__device__ __forceinline__ F2 twice(float a) { return {a, a}; }
+
 // Division of n < 2^31 by a divisor known at launch: a product and a shift
 // (Granlund and Montgomery 1994).
 struct FastDiv {

@@ -310,14 +310,55 @@ __device__ __forceinline__ void tensor_product(uint32_t d, uint64_t a, uint64_t 
             : "memory");
 }
 
-// The same by one CTA with A in tensor memory: a row per lane, two elements
-// of k to a column (K-major).
-__device__ __forceinline__ void tensor_product_tmem(uint32_t d, uint32_t a, uint64_t b, uint32_t desc, bool add)
+// Up to four products of one CTA in a row, D (+)= A B over 64 elements of k,
+// by the elected lane of a converged warp: the lane is a predicate of the
+// products, not a branch around them, so that their operands are worked out
+// in uniform registers between them.  (Behind a branch each product took 105
+// to 130 clocks to issue; one of 128 x 128 x 16 runs for 64.)  `n`: how many;
+// both descriptors move on by SA and SB.
+template <int SA, int SB>
+__device__ __forceinline__ void tensor_products4(uint32_t d, uint64_t a, uint64_t b, uint32_t desc, bool add, int n)
 {
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-        "r"(a), "l"(b), "r"(desc), "r"((uint32_t)add)
+        "{\n\t.reg .pred l, p, q, r1, r2, r3;\n\t.reg .b64 a1, a2, a3, b1, b2, b3;\n\t"
+        "elect.sync _|l, 0xffffffff;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\tsetp.eq.b32 q, 0, 0;\n\t"
+        "setp.gt.and.s32 r1, %5, 1, l;\n\tsetp.gt.and.s32 r2, %5, 2, l;\n\tsetp.gt.and.s32 r3, %5, 3, l;\n\t"
+        "add.s64 a1, %1, %6;\n\tadd.s64 b1, %2, %7;\n\tadd.s64 a2, a1, %6;\n\tadd.s64 b2, b1, %7;\n\t"
+        "add.s64 a3, a2, %6;\n\tadd.s64 b3, b2, %7;\n\t"
+        "@l tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t"
+        "@r1 tcgen05.mma.cta_group::1.kind::f16 [%0], a1, b1, %3, q;\n\t"
+        "@r2 tcgen05.mma.cta_group::1.kind::f16 [%0], a2, b2, %3, q;\n\t"
+        "@r3 tcgen05.mma.cta_group::1.kind::f16 [%0], a3, b3, %3, q;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(desc), "r"((uint32_t)add), "r"(n), "n"(SA), "n"(SB)
+        : "memory");
+}
+
+// The same four with A in tensor memory: a row per lane, two elements of k to
+// a column (K-major), so eight columns to a product.
+template <int SB>
+__device__ __forceinline__ void tensor_products4_tmem(uint32_t d, uint32_t a, uint64_t b, uint32_t desc, bool add)
+{
+    asm volatile(
+        "{\n\t.reg .pred l, p, q;\n\t.reg .b32 a1, a2, a3;\n\t.reg .b64 b1, b2, b3;\n\t"
+        "elect.sync _|l, 0xffffffff;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\tsetp.eq.b32 q, 0, 0;\n\t"
+        "add.s32 a1, %1, 8;\n\tadd.s64 b1, %2, %5;\n\tadd.s32 a2, %1, 16;\n\tadd.s64 b2, b1, %5;\n\t"
+        "add.s32 a3, %1, 24;\n\tadd.s64 b3, b2, %5;\n\t"
+        "@l tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t"
+        "@l tcgen05.mma.cta_group::1.kind::f16 [%0], [a1], b1, %3, q;\n\t"
+        "@l tcgen05.mma.cta_group::1.kind::f16 [%0], [a2], b2, %3, q;\n\t"
+        "@l tcgen05.mma.cta_group::1.kind::f16 [%0], [a3], b3, %3, q;\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "r"(desc), "r"((uint32_t)add), "n"(SB)
+        : "memory");
+}
+
+// Arrives on `bar` when the elected lane's products so far are done.
+__device__ __forceinline__ void tensor_commit_elected(uint64_t *bar)
+{
+    asm volatile(
+        "{\n\t.reg .pred l;\n\telect.sync _|l, 0xffffffff;\n\t"
+        "@l tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_addr(bar))
         : "memory");
 }
 
