@@ -80,7 +80,8 @@ struct TileAt {
     bool any;
 };
 
-// By a whole warp: 32 offsets at a time.
+// By a whole warp: 32 offsets at a time.  (T is a constant where it can be:
+// divisions of 64 bits are long.)
 __device__ __forceinline__ TileAt find_tile(const Attn &a, const int64_t *offsets, int64_t rows, int64_t number, int32_t T,
                                             bool keys, int lane)
 {
@@ -142,13 +143,14 @@ __device__ __forceinline__ uint32_t seen_bits(int32_t p, int32_t window, int32_t
 // issued in them.
 __device__ __forceinline__ int32_t uniform(int32_t x) { return __shfl_sync(0xffffffffu, x, 0); }
 
-// The key tiles of 128 queries, and of two such tiles.
+// The tiles of BN keys that 128 queries see, and two such tiles of queries.
 struct KeyTiles {
     int32_t low, high;  // of the window
     int32_t sinks;      // first tiles that are seen outside it
     bool any;
 };
 
+template <int BN>
 __device__ __forceinline__ KeyTiles key_tiles(const Attn &a, int32_t first, int32_t lq, int32_t lk)
 {
     KeyTiles t{0, -1, 0, false};
@@ -158,9 +160,9 @@ __device__ __forceinline__ KeyTiles key_tiles(const Attn &a, int32_t first, int3
         return t;
     const int32_t sinks = a.sinks < p1 + 1 ? a.sinks : p1 + 1;
     t.any = true;
-    t.low = p0 >= a.window ? (p0 - a.window + 1) / 128 : 0;
-    t.high = p1 / 128;
-    t.sinks = (sinks + 127) / 128;
+    t.low = p0 >= a.window ? (p0 - a.window + 1) / BN : 0;
+    t.high = p1 / BN;
+    t.sinks = (sinks + BN - 1) / BN;
     return t;
 }
 
@@ -216,53 +218,89 @@ struct FwdTiles {
 
 constexpr int kUnitRing = 4;
 
-// D = A B^T over the elements of a head (16 to a step), in boxes of 64.
-template <int DP>
+// D = A B^T over the elements of a head (16 to a step), in boxes of 64
+// elements by A_ROWS and B_ROWS rows.
+template <int DP, int A_ROWS, int B_ROWS>
 __device__ __forceinline__ void inner_products(uint32_t d, uint64_t a, uint64_t b, uint32_t desc, int steps)
 {
     tensor_products4<2, 2>(d, a, b, desc, false, steps);
     if (DP == 128 && steps > 4)
-        tensor_products4<2, 2>(d, a + (16384 >> 4), b + (16384 >> 4), desc, true, steps - 4);
+        tensor_products4<2, 2>(d, a + (A_ROWS * 128 >> 4), b + (B_ROWS * 128 >> 4), desc, true, steps - 4);
 }
 
-// D (+)= A B over 128 rows of B, A in tensor memory, 64 elements each from
-// a and from a + 64 on.
+// D (+)= A B over ROWS rows of B, A in tensor memory, 64 elements each from a
+// and from a + 64 on.
+template <int ROWS>
 __device__ __forceinline__ void outer_products(uint32_t d, uint32_t a, uint64_t b, uint32_t desc, bool add)
 {
     tensor_products4_tmem<128>(d, a, b, desc, add);
-    tensor_products4_tmem<128>(d, a + 64, b + 512, desc, true);
+    if (ROWS == 128)
+        tensor_products4_tmem<128>(d, a + 64, b + 512, desc, true);
 }
 
-template <int DP>
+// QT tiles of 128 queries against tiles of BN keys.
+template <int DP_, int QT_, int BN_, int PER_SM_>
 struct FwdShape {
-    static constexpr int BOXES = DP / 64, TILE = BOXES * 16384;  // bytes of 128 rows
-    static constexpr int STAGES = DP == 64 ? 4 : 2;
-    static constexpr int THREADS = 320;  // eight warps of rows, one that loads, one that issues
-    static constexpr int SMEM = 1024 + (2 + 2 * STAGES) * TILE;
+    static constexpr int DP = DP_, QT = QT_, BN = BN_, PER_SM = PER_SM_;
+    static constexpr int BOXES = DP / 64, Q_TILE = BOXES * 16384, K_TILE = BOXES * BN * 128;  // bytes
+    static constexpr int STAGES = 2;
+    static constexpr int ROW_WARPS = 4 * QT, THREADS = (ROW_WARPS + 2) * 32;
+    static constexpr int TMEM = QT * (BN + DP) <= 128 ? 128 : QT * (BN + DP) <= 256 ? 256 : 512;
+    static constexpr int SMEM = 1024 + QT * Q_TILE + 2 * STAGES * K_TILE + ROW_WARPS * 4096;
+    static_assert(SMEM * PER_SM <= 227 * 1024 && TMEM * PER_SM <= 512 && QT * (BN + DP) <= TMEM, "what an SM has");
 };
 
 struct FwdShared {
-    uint64_t q_full[2], q_empty[2], k_full[4], k_empty[4], v_full[4], v_empty[4], s_full[2], p_full[2][2], o_full[2];
+    uint64_t q_full[2], q_empty[2], k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2][2], o_full[2];
     uint64_t unit_full[kUnitRing], unit_empty[kUnitRing];
     Unit units[kUnitRing];
     uint32_t tmem, gave_up;
 };
 
-// Two tiles of 128 queries of one head at a time (one CTA per SM, persistent).
-template <int DT, int DP>
-__global__ void __launch_bounds__(FwdShape<DP>::THREADS, 1) k_attn_tiles(const __grid_constant__ FwdTiles f)
+// 32 rows of 32 or 64 elements of one warp, a row per lane, through 2 or 4 KB
+// of shared memory (16-byte pieces XORed by the row, so that neither way has
+// bank conflicts) to rows of memory `ld` elements apart, whole rows at a time.
+// Rows from `rows` and elements from `cols` on are not written.
+template <int WORDS>
+__device__ __forceinline__ void store_rows(uint4 *stage, int lane, const uint32_t (&w)[WORDS], uint16_t *out, int64_t ld, int rows,
+                                           int cols)
 {
-    using S = FwdShape<DP>;
+    constexpr int P = WORDS / 4, SHIFT = P == 8 ? 0 : 1;  // pieces of a row
+#pragma unroll
+    for (int k = 0; k < P; ++k)
+        stage[lane * P + (k ^ ((lane >> SHIFT) & (P - 1)))] = make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
+    __syncwarp();
+    const int k = lane & (P - 1);
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+        const int r = 32 / P * i + lane / P;
+        const uint4 v = stage[r * P + (k ^ ((r >> SHIFT) & (P - 1)))];
+        if (r < rows && k * 8 < cols)
+            *reinterpret_cast<uint4 *>(out + r * ld + k * 8) = v;
+    }
+    __syncwarp();
+}
+
+// QT tiles of 128 queries of one head at a time, by a persistent CTA: one warp
+// loads, one issues the products, and the others hold a row of the scores per
+// thread: their largest, the weights (which take the scores' place in tensor
+// memory, as the first operand of the product with the values) and their sum.
+template <int DT, class S>
+__global__ void __launch_bounds__(S::THREADS, S::PER_SM) k_attn_tiles(const __grid_constant__ FwdTiles f)
+{
+    constexpr int DP = S::DP, QT = S::QT, BN = S::BN, HALVES = BN / 64;
     extern __shared__ unsigned char smem_raw[];
     __shared__ FwdShared sh;
     unsigned char *smem = smem_raw + ((1024 - (smem_addr(smem_raw) & 1023u)) & 1023u);
-    unsigned char *const s_q = smem, *const s_k = smem + 2 * S::TILE, *const s_v = s_k + S::STAGES * S::TILE;
+    unsigned char *const s_q = smem, *const s_k = smem + QT * S::Q_TILE, *const s_v = s_k + S::STAGES * S::K_TILE;
+    unsigned char *const s_out = s_v + S::STAGES * S::K_TILE;
     const Attn &a = f.a;
     const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
-    constexpr int kTma = 8, kMma = 9;
+    constexpr int kTma = S::ROW_WARPS, kMma = S::ROW_WARPS + 1;
+    constexpr int kScores = BN, kSums = QT * BN;  // columns of tensor memory: of a tile's scores, where the sums start
 
     if (threadIdx.x == 0) {
-        for (int t = 0; t < 2; ++t) {
+        for (int t = 0; t < QT; ++t) {
             mbar_init_count(&sh.q_full[t], 1);
             mbar_init_count(&sh.q_empty[t], 1);
             mbar_init_count(&sh.s_full[t], 1);
@@ -278,13 +316,13 @@ __global__ void __launch_bounds__(FwdShape<DP>::THREADS, 1) k_attn_tiles(const _
         }
         for (int s = 0; s < kUnitRing; ++s) {
             mbar_init_count(&sh.unit_full[s], 1);
-            mbar_init_count(&sh.unit_empty[s], 9);
+            mbar_init_count(&sh.unit_empty[s], S::ROW_WARPS + 1);
         }
         sh.gave_up = 0;
         mbar_init_done();
     }
     if (warp == kMma)
-        tmem_alloc<1>(&sh.tmem, 512);
+        tmem_take(&sh.tmem, S::TMEM);
     if (warp == kTma && lane < 3)
         tma_prefetch_map(lane == 0 ? &f.q.map : lane == 1 ? &f.k.map : &f.v.map);
     tmem_fence_before();
@@ -292,6 +330,7 @@ __global__ void __launch_bounds__(FwdShape<DP>::THREADS, 1) k_attn_tiles(const _
     tmem_fence_after();
     const uint32_t tmem = (uint32_t)uniform((int32_t)sh.tmem);
     auto wait = [&](uint64_t *bar, uint32_t parity) { return mbar_wait_warp(bar, parity, f.limit_ns, &sh.gave_up); };
+    auto second = [&](const Unit &u) { return QT == 2 ? key_tiles<BN>(a, u.first + 128, u.lq, u.lk) : KeyTiles{0, -1, 0, false}; };
     // the next unit, from the loading warp
     uint32_t units = 0;
     auto next = [&](Unit &u) {
@@ -322,12 +361,12 @@ __global__ void __launch_bounds__(FwdShape<DP>::THREADS, 1) k_attn_tiles(const _
             ++units;
             return true;
         };
-        auto load = [&](unsigned char *to, const HeadsMap &m, int32_t row, int32_t head, uint64_t *bar) {
+        auto load = [&](unsigned char *to, const HeadsMap &m, int32_t row, int32_t head, int box, uint64_t *bar) {
             if (elect_one()) {
-                mbar_expect(bar, S::TILE);
+                mbar_expect(bar, S::BOXES * box);
 #pragma unroll
                 for (int x = 0; x < S::BOXES; ++x)
-                    load_box(smem_addr(to) + x * 16384, m, 64 * x, row, head, smem_addr(bar));
+                    load_box(smem_addr(to) + x * box, m, 64 * x, row, head, smem_addr(bar));
             }
             __syncwarp();
         };
@@ -335,7 +374,7 @@ __global__ void __launch_bounds__(FwdShape<DP>::THREADS, 1) k_attn_tiles(const _
         for (int64_t i = blockIdx.x; ok && i < all; i += gridDim.x) {
             // long ones first: a sequence's later queries see more keys
             const int64_t number = f.tiles - 1 - i / a.q_heads;
-            const TileAt at = find_tile(a, a.q_offsets, a.q_tokens, number, 256, false, lane);
+            const TileAt at = find_tile(a, a.q_offsets, a.q_tokens, number, 128 * QT, false, lane);
             if (!at.any)
                 continue;
             const Unit u{(int32_t)at.s.q0 + at.first, (int32_t)at.s.k0, at.first, at.s.lq, at.s.lk, (int32_t)(i % a.q_heads), 0};
@@ -343,31 +382,31 @@ __global__ void __launch_bounds__(FwdShape<DP>::THREADS, 1) k_attn_tiles(const _
                 ok = false;
                 break;
             }
-            const KeyTiles x = key_tiles(a, u.first, u.lq, u.lk), y = key_tiles(a, u.first + 128, u.lq, u.lk);
+            const KeyTiles x = key_tiles<BN>(a, u.first, u.lq, u.lk), y = second(u);
             const TileList list = tile_list(x, y);
             const int32_t g = u.head / a.group;
             for (int32_t n = 0; ok && n < list.n; ++n) {
                 const int32_t kt = list.at(n);
                 if (n == 0)
-                    for (int t = 0; ok && t < 2; ++t) {
+                    for (int t = 0; ok && t < QT; ++t) {
                         if (!(t ? y.any : x.any))
                             continue;
                         ok = wait(&sh.q_empty[t], (qn[t] & 1) ^ 1);
                         if (ok)
-                            load(s_q + t * S::TILE, f.q, u.q_row + 128 * t, u.head, &sh.q_full[t]);
+                            load(s_q + t * S::Q_TILE, f.q, u.q_row + 128 * t, u.head, 16384, &sh.q_full[t]);
                         ++qn[t];
                     }
                 const uint32_t ks = kn % S::STAGES;
                 ok = ok && wait(&sh.k_empty[ks], ((kn / S::STAGES) & 1) ^ 1);
                 if (!ok)
                     break;
-                load(s_k + ks * S::TILE, f.k, u.k_row + kt * 128, g, &sh.k_full[ks]);
+                load(s_k + ks * S::K_TILE, f.k, u.k_row + kt * BN, g, BN * 128, &sh.k_full[ks]);
                 ++kn;
                 const uint32_t vs = vn % S::STAGES;
                 ok = wait(&sh.v_empty[vs], ((vn / S::STAGES) & 1) ^ 1);
                 if (!ok)
                     break;
-                load(s_v + vs * S::TILE, f.v, u.k_row + kt * 128, g, &sh.v_full[vs]);
+                load(s_v + vs * S::K_TILE, f.v, u.k_row + kt * BN, g, BN * 128, &sh.v_full[vs]);
                 ++vn;
             }
         }
@@ -375,20 +414,20 @@ __global__ void __launch_bounds__(FwdShape<DP>::THREADS, 1) k_attn_tiles(const _
             publish(Unit{0, 0, 0, 0, 0, 0, 1});
     } else if (warp == kMma) {
         constexpr uint32_t kBf16 = DT == ZERO_BF16;
-        const uint32_t desc_s = product_desc(kBf16, false, false, 128, 128);
+        const uint32_t desc_s = product_desc(kBf16, false, false, 128, BN);
         const int wide = (a.dim + 15) & ~15, steps = wide / 16;
         const uint32_t desc_o = product_desc(kBf16, false, true, 128, wide);
         const uint64_t q0 = operand_desc(smem_addr(s_q), 16, 1024), k0 = operand_desc(smem_addr(s_k), 16, 1024);
-        const uint64_t v0 = operand_desc(smem_addr(s_v), 16384, 1024);
+        const uint64_t v0 = operand_desc(smem_addr(s_v), BN * 128, 1024);
         uint32_t kn = 0, vn = 0, qn[2] = {0, 0}, pn[2] = {0, 0};
         bool ok = true;
         Unit u;
         while (ok && next(u)) {
-            const KeyTiles kt2[2] = {key_tiles(a, u.first, u.lq, u.lk), key_tiles(a, u.first + 128, u.lq, u.lk)};
+            const KeyTiles kt2[2] = {key_tiles<BN>(a, u.first, u.lq, u.lk), second(u)};
             const TileList list = tile_list(kt2[0], kt2[1]);
             // S_t = Q_t K^T of the n-th tile
             auto scores = [&](int t, uint32_t stage) {
-                inner_products<DP>(tmem + t * 128, q0 + ((t * S::TILE) >> 4), k0 + ((stage * S::TILE) >> 4), desc_s, steps);
+                inner_products<DP, 128, BN>(tmem + t * kScores, q0 + ((t * S::Q_TILE) >> 4), k0 + ((stage * S::K_TILE) >> 4), desc_s, steps);
                 tensor_commit_elected(&sh.s_full[t]);
             };
             bool first[2] = {true, true};
@@ -399,21 +438,21 @@ __global__ void __launch_bounds__(FwdShape<DP>::THREADS, 1) k_attn_tiles(const _
                 const uint32_t ks = kn % S::STAGES, vs = vn % S::STAGES;
                 bool k_here = false, v_here = false;
 #pragma unroll
-                for (int t = 0; t < 2; ++t) {
+                for (int t = 0; t < QT; ++t) {
                     if (n > 0 && needs(kt2[t], before)) {
                         if (!v_here)
                             ok = ok && wait(&sh.v_full[vs], (vn / S::STAGES) & 1);
                         v_here = true;
                         // the later keys' weights come first
-                        const uint64_t dv = v0 + ((vs * S::TILE) >> 4);
+                        const uint64_t dv = v0 + ((vs * S::K_TILE) >> 4);
 #pragma unroll
-                        for (int h = 1; h >= 0; --h) {
+                        for (int h = HALVES - 1; h >= 0; --h) {
                             ok = ok && wait(&sh.p_full[t][h], pn[t] & 1);
                             if (!ok)
                                 break;
                             tmem_fence_after();
-                            tensor_products4_tmem<128>(tmem + 256 + t * 128, tmem + t * 128 + 64 + h * 32, dv + h * 512,
-                                                       desc_o, !first[t] || h == 0);
+                            tensor_products4_tmem<128>(tmem + kSums + t * DP, tmem + t * kScores + BN / 2 + h * 32, dv + h * 512,
+                                                       desc_o, !first[t] || h != HALVES - 1);
                         }
                         ++pn[t];
                         if (!ok)
@@ -455,13 +494,14 @@ __global__ void __launch_bounds__(FwdShape<DP>::THREADS, 1) k_attn_tiles(const _
     } else {
         const int t = warp >> 2, quarter = warp & 3;
         const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
-        const uint32_t at_s = tmem + lanes + t * 128, at_o = tmem + lanes + 256 + t * 128;
+        const uint32_t at_s = tmem + lanes + t * kScores, at_o = tmem + lanes + kSums + t * DP;
+        uint4 *const stage = reinterpret_cast<uint4 *>(s_out + warp * 4096);
         const float sl = f.scale_log2;
         uint32_t sn = 0, on = 0, vn = 0;
         bool ok = true;
         Unit u;
         while (ok && next(u)) {
-            const KeyTiles x = key_tiles(a, u.first, u.lq, u.lk), y = key_tiles(a, u.first + 128, u.lq, u.lk);
+            const KeyTiles x = key_tiles<BN>(a, u.first, u.lq, u.lk), y = second(u);
             const KeyTiles mine = t ? y : x;
             const TileList list = tile_list(x, y);
             const int32_t row = u.first + 128 * t + quarter * 32 + lane, p = row + u.lk - u.lq;
@@ -477,11 +517,12 @@ __global__ void __launch_bounds__(FwdShape<DP>::THREADS, 1) k_attn_tiles(const _
                 if (!ok)
                     break;
                 tmem_fence_after();
-                const int32_t k_first = kt * 128;
-                const bool whole = k_first + 127 <= p_first &&
-                                   (k_first > p_last - a.window || k_first + 127 < a.sinks);
-                // Four pieces of 32 scores: once for the largest, the last two
-                // then stay in registers, and the first two come again.
+                const int32_t k_first = kt * BN;
+                const bool whole = k_first + BN - 1 <= p_first &&
+                                   (k_first > p_last - a.window || k_first + BN - 1 < a.sinks);
+                // Pieces of 32 scores: once for the largest, the last two of
+                // four (the last of two) then stay in registers, and the others
+                // come again.
                 uint32_t r0[32], r1[32], r2[32];
                 auto hide = [&](uint32_t (&r)[32], int c) {
                     if (!whole) {
@@ -505,14 +546,16 @@ __global__ void __launch_bounds__(FwdShape<DP>::THREADS, 1) k_attn_tiles(const _
                 tmem_load32(at_s + 32, r1);
                 largest(r0, 0);
                 tmem_wait_loads(r1);
-                tmem_load32(at_s + 64, r0);
-                largest(r1, 1);
-                tmem_wait_loads(r0);
-                tmem_load32(at_s + 96, r1);
-                largest(r0, 2);
-                tmem_wait_loads(r1);
-                tmem_load32(at_s + 32, r2);
-                largest(r1, 3);
+                if constexpr (HALVES == 2) {
+                    tmem_load32(at_s + 64, r0);
+                    largest(r1, 1);
+                    tmem_wait_loads(r0);
+                    tmem_load32(at_s + 96, r1);
+                    largest(r0, 2);
+                    tmem_wait_loads(r1);
+                    tmem_load32(at_s + 32, r2);
+                }
+                largest(r1, BN / 32 - 1);
                 const float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
                 // The weights' reference is the largest score so far, or up to
                 // 2^8 below it: the weights stay below 2^8, and sums are
@@ -542,7 +585,7 @@ __global__ void __launch_bounds__(FwdShape<DP>::THREADS, 1) k_attn_tiles(const _
                 const F2 scale2 = twice(sl), base2 = twice(m == -INFINITY ? 0.0f : -m * sl);
                 F2 sums[2] = {{0.0f, 0.0f}, {0.0f, 0.0f}};
                 // The weights go where scores were that are no longer needed:
-                // those of piece c into the 16 columns from 64 + 16 c on.
+                // those of piece c into the 16 columns from BN / 2 + 16 c on.
                 auto weigh = [&](const uint32_t (&r)[32], int c) {
                     uint32_t w[16];
 #pragma unroll
@@ -552,7 +595,7 @@ __global__ void __launch_bounds__(FwdShape<DP>::THREADS, 1) k_attn_tiles(const _
                         sums[e & 1] = sums[e & 1] + x;
                         w[e] = pack2<DT>(x.x, x.y);
                     }
-                    tmem_store16(at_s + 64 + 16 * c, w);
+                    tmem_store16(at_s + BN / 2 + 16 * c, w);
                 };
                 auto ready = [&](int h) {
                     tmem_wait_stores();
@@ -561,9 +604,12 @@ __global__ void __launch_bounds__(FwdShape<DP>::THREADS, 1) k_attn_tiles(const _
                     if (lane == 0)
                         mbar_arrive_cluster(smem_addr(&sh.p_full[t][h]));
                 };
-                weigh(r1, 3);
-                weigh(r0, 2);
-                if (k_first + 128 > u.lk) {
+                if constexpr (HALVES == 1)
+                    tmem_load32(at_s, r2);
+                weigh(r1, BN / 32 - 1);
+                if constexpr (HALVES == 2)
+                    weigh(r0, 2);
+                if (k_first + BN > u.lk) {
                     // rows behind the last key: zeros, since 0 times what they hold may not be 0
                     const uint32_t now = vn + n, vs = now % S::STAGES;
                     ok = wait(&sh.v_full[vs], (now / S::STAGES) & 1);
@@ -571,20 +617,26 @@ __global__ void __launch_bounds__(FwdShape<DP>::THREADS, 1) k_attn_tiles(const _
                         break;
                     const int32_t from = u.lk - k_first;
                     const int id = threadIdx.x & 127;
-                    for (int i = from * 8 + id; i < 1024; i += 128)
+                    for (int i = from * 8 + id; i < BN * 8; i += 128)
 #pragma unroll
                         for (int b = 0; b < S::BOXES; ++b)
-                            *reinterpret_cast<uint4 *>(s_v + vs * S::TILE + b * 16384 + i * 16) = make_uint4(0, 0, 0, 0);
+                            *reinterpret_cast<uint4 *>(s_v + vs * S::K_TILE + b * BN * 128 + i * 16) = make_uint4(0, 0, 0, 0);
                     fence_proxy_async();
                 }
-                tmem_wait_loads(r2);
-                ready(1);
-                tmem_load32(at_s, r0);
-                hide(r2, 1);
-                weigh(r2, 1);
-                tmem_wait_loads(r0);
-                hide(r0, 0);
-                weigh(r0, 0);
+                if constexpr (HALVES == 2) {
+                    tmem_wait_loads(r2);
+                    ready(1);
+                    tmem_load32(at_s, r0);
+                    hide(r2, 1);
+                    weigh(r2, 1);
+                    tmem_wait_loads(r0);
+                    hide(r0, 0);
+                    weigh(r0, 0);
+                } else {
+                    tmem_wait_loads(r2);
+                    hide(r2, 0);
+                    weigh(r2, 0);
+                }
                 ready(0);
                 l += (sums[0].x + sums[0].y) + (sums[1].x + sums[1].y);
             }
@@ -606,33 +658,25 @@ __global__ void __launch_bounds__(FwdShape<DP>::THREADS, 1) k_attn_tiles(const _
                 f.lse[(int64_t)u.head * a.q_tokens + out_row] =
                     l == 0.0f ? -INFINITY : m * a.scale + logf(l);
             const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-            char *out = static_cast<char *>(const_cast<void *>(f.out.p)) + (out_row * f.out.ld + u.head * f.out.hd) * 2;
-            for (int c = 0; c < a.dim; c += 32) {
-                uint32_t o[32];
-                if (mine.any) {
-                    tmem_load32(at_o + c, o);
-                    tmem_wait_loads(o);
-                } else {
+            const int32_t left = u.lq - u.first - 128 * t - quarter * 32;  // rows of this warp
+            uint16_t *out = static_cast<uint16_t *>(const_cast<void *>(f.out.p)) +
+                            ((int64_t)u.q_row + 128 * t + quarter * 32) * f.out.ld + u.head * f.out.hd;
+#pragma unroll 1
+            for (int c = 0; c < a.dim; c += 64) {
+                uint32_t w[32];
 #pragma unroll
-                    for (int e = 0; e < 32; ++e)
-                        o[e] = 0;
-                }
-                if (live) {
-#pragma unroll
-                    for (int e = 0; e < 32; e += 8) {
-                        if (c + e >= a.dim)
-                            break;
-                        uint32_t w[4];
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const float f0 = l == 0.0f ? 0.0f : __uint_as_float(o[e + 2 * i]) * inv;
-                            const float f1 = l == 0.0f ? 0.0f : __uint_as_float(o[e + 2 * i + 1]) * inv;
-                            w[i] = pack2<DT>(f0, f1);
-                        }
-                        *reinterpret_cast<uint4 *>(out + (c + e) * 2) = make_uint4(w[0], w[1], w[2], w[3]);
+                for (int h = 0; h < 2; ++h) {
+                    uint32_t o[32];
+                    if (mine.any && c + 32 * h < a.dim) {
+                        tmem_load32(at_o + c + 32 * h, o);
+                        tmem_wait_loads(o);
                     }
+#pragma unroll
+                    for (int e = 0; e < 16; ++e)
+                        w[16 * h + e] = l == 0.0f ? 0u
+                                                  : pack2<DT>(__uint_as_float(o[2 * e]) * inv, __uint_as_float(o[2 * e + 1]) * inv);
                 }
-                __syncwarp();
+                store_rows(stage, lane, w, out + c, f.out.ld, left, a.dim - c);
             }
         }
     }
@@ -651,9 +695,9 @@ __global__ void __launch_bounds__(FwdShape<DP>::THREADS, 1) k_attn_tiles(const _
         // no result of this CTA is to be taken for one
         const int64_t all = f.tiles * a.q_heads;
         for (int64_t i = blockIdx.x; i < all; i += gridDim.x) {
-            const TileAt at = find_tile(a, a.q_offsets, a.q_tokens, f.tiles - 1 - i / a.q_heads, 256, false, lane);
+            const TileAt at = find_tile(a, a.q_offsets, a.q_tokens, f.tiles - 1 - i / a.q_heads, 128 * QT, false, lane);
             const int64_t head = i % a.q_heads;
-            for (int32_t r = at.first + warp; at.any && r < at.s.lq && r < at.first + 256; r += S::THREADS / 32) {
+            for (int32_t r = at.first + warp; at.any && r < at.s.lq && r < at.first + 128 * QT; r += S::THREADS / 32) {
                 for (int e = lane; e < a.dim; e += 32)
                     static_cast<uint16_t *>(const_cast<void *>(f.out.p))[(at.s.q0 + r) * f.out.ld + head * f.out.hd + e] = 0x7fff;
                 if (lane == 0 && f.lse)
@@ -662,7 +706,7 @@ __global__ void __launch_bounds__(FwdShape<DP>::THREADS, 1) k_attn_tiles(const _
         }
     }
     if (warp == kMma)
-        tmem_free<1>(tmem, 512);
+        tmem_give(tmem, S::TMEM);
 }
 
 // ------------------------------------------------------------- a few queries
@@ -1041,11 +1085,12 @@ struct BwdTiles {
     uint64_t limit_ns;
 };
 
-// The tiles of 128 queries that see a key of the tile from key j on.
+// The tiles of T queries that see a key of the tile of 128 from key j on.
 struct QueryTiles {
     int32_t low, high;
 };
 
+template <int T>
 __device__ __forceinline__ QueryTiles query_tiles(const Attn &a, int32_t j, int32_t lq, int32_t lk)
 {
     const int32_t shift = lk - lq, last = j + 127 < lk ? j + 127 : lk - 1;
@@ -1055,10 +1100,10 @@ __device__ __forceinline__ QueryTiles query_tiles(const Attn &a, int32_t j, int3
         to = last - shift + a.window - 1;
     if (lq == 0 || from > to)
         return {0, -1};
-    return {from / 128, to / 128};
+    return {from / T, to / T};
 }
 
-// Whether those of a tile of first keys are dealt out.
+// Whether those (of 128) of a tile of first keys are dealt out.
 __device__ __forceinline__ bool is_split(const BwdTiles &f, int32_t j, const QueryTiles &t)
 {
     return f.chunk > 0 && j < f.a.sinks && t.high - t.low + 1 > 2 * f.chunk;
@@ -1078,11 +1123,16 @@ struct KeyUnit {
     }
 };
 
-template <int DP>
+// Tiles of 128 keys (queries) against tiles of BN queries (keys), which a
+// group of four warps holds a row of 64 columns per thread of.
+template <int DP_, int BN_, int PER_SM_>
 struct BwdShape {
-    static constexpr int BOXES = DP / 64, TILE = BOXES * 16384;
-    static constexpr int THREADS = 320;
-    static constexpr int SMEM = 1024 + 6 * TILE + 2048;
+    static constexpr int DP = DP_, BN = BN_, PER_SM = PER_SM_;
+    static constexpr int BOXES = DP / 64, TILE = BOXES * 16384, MOVING = BOXES * BN * 128;  // bytes
+    static constexpr int ROW_WARPS = BN / 16, THREADS = (ROW_WARPS + 2) * 32;
+    static constexpr int SMEM = 1024 + 2 * TILE + 4 * MOVING + 4 * BN * 4 + ROW_WARPS * 2048;
+    static constexpr int TMEM = 2 * BN + 2 * DP;  // (dq: three of BN and one of DP)
+    static_assert(SMEM * PER_SM <= 227 * 1024 && TMEM * PER_SM <= 512 && 3 * BN + DP <= TMEM, "what an SM has");
 };
 
 struct KeyShared {
@@ -1092,7 +1142,8 @@ struct KeyShared {
     uint32_t tmem, gave_up;
 };
 
-// The work of a unit number: false if there is none.
+// The work of a unit number, its queries in tiles of T: false if there is none.
+template <int T>
 __device__ __forceinline__ bool key_unit(const BwdTiles &f, int64_t i, int lane, KeyUnit &u)
 {
     const Attn &a = f.a;
@@ -1106,10 +1157,10 @@ __device__ __forceinline__ bool key_unit(const BwdTiles &f, int64_t i, int lane,
         u.first = (int32_t)(i / a.k_heads % f.sink_tiles) * 128;
         if (!at.any || u.first >= at.s.lk || u.first >= a.sinks)
             return false;
-        const QueryTiles t = query_tiles(a, u.first, at.s.lq, at.s.lk);
-        if (!is_split(f, u.first, t))
+        if (!is_split(f, u.first, query_tiles<128>(a, u.first, at.s.lq, at.s.lk)))
             return false;
-        const int32_t low = at.first / 128, high = low + f.chunk - 1;
+        const QueryTiles t = query_tiles<T>(a, u.first, at.s.lq, at.s.lk);
+        const int32_t low = at.first / T, high = low + f.chunk * (128 / T) - 1;
         u.low = low > t.low ? low : t.low;
         u.high = high < t.high ? high : t.high;
         if (u.low > u.high)
@@ -1122,9 +1173,9 @@ __device__ __forceinline__ bool key_unit(const BwdTiles &f, int64_t i, int lane,
             return false;
         u.head = (int32_t)(i % a.k_heads);
         u.first = at.first;
-        const QueryTiles t = query_tiles(a, u.first, at.s.lq, at.s.lk);
-        if (is_split(f, u.first, t))
+        if (is_split(f, u.first, query_tiles<128>(a, u.first, at.s.lq, at.s.lk)))
             return false;
+        const QueryTiles t = query_tiles<T>(a, u.first, at.s.lq, at.s.lk);
         u.low = t.low, u.high = t.high;
         u.slot = -1;
     }
@@ -1141,18 +1192,20 @@ __device__ __forceinline__ bool key_unit(const BwdTiles &f, int64_t i, int lane,
 // which the two running products take from tensor memory, have a key per lane:
 //     S' = K Q^T, P' = exp(S' - lse), dP' = V dO^T, dS' = P' (dP' - delta),
 //     dV += P' dO, dK += dS' Q.
-template <int DT, int DP>
-__global__ void __launch_bounds__(BwdShape<DP>::THREADS, 1) k_attn_dkv(const __grid_constant__ BwdTiles f)
+template <int DT, class S>
+__global__ void __launch_bounds__(S::THREADS, S::PER_SM) k_attn_dkv(const __grid_constant__ BwdTiles f)
 {
-    using S = BwdShape<DP>;
+    constexpr int DP = S::DP, BN = S::BN;
     extern __shared__ unsigned char smem_raw[];
     __shared__ KeyShared sh;
     unsigned char *smem = smem_raw + ((1024 - (smem_addr(smem_raw) & 1023u)) & 1023u);
-    unsigned char *const s_k = smem, *const s_v = smem + S::TILE, *const s_q = s_v + S::TILE, *const s_o = s_q + 2 * S::TILE;
-    float *const s_stats = reinterpret_cast<float *>(s_o + 2 * S::TILE);  // [stage][lse2, delta][128]
+    unsigned char *const s_k = smem, *const s_v = smem + S::TILE, *const s_q = s_v + S::TILE, *const s_o = s_q + 2 * S::MOVING;
+    float *const s_stats = reinterpret_cast<float *>(s_o + 2 * S::MOVING);  // [stage][lse2, delta][BN]
+    unsigned char *const s_out = reinterpret_cast<unsigned char *>(s_stats + 4 * BN);
     const Attn &a = f.a;
     const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
-    constexpr int kTma = 8, kMma = 9;
+    constexpr int kTma = S::ROW_WARPS, kMma = S::ROW_WARPS + 1;
+    constexpr int kDp = BN, kDv = 2 * BN, kDk = 2 * BN + DP;  // columns of tensor memory
 
     if (threadIdx.x == 0) {
         mbar_init_count(&sh.kv_full, 1);
@@ -1165,18 +1218,18 @@ __global__ void __launch_bounds__(BwdShape<DP>::THREADS, 1) k_attn_dkv(const __g
         }
         mbar_init_count(&sh.s_full, 1);
         mbar_init_count(&sh.dp_full, 1);
-        mbar_init_count(&sh.p_full, 8);
-        mbar_init_count(&sh.ds_full, 8);
+        mbar_init_count(&sh.p_full, S::ROW_WARPS);
+        mbar_init_count(&sh.ds_full, S::ROW_WARPS);
         mbar_init_count(&sh.acc_full, 1);
         for (int s = 0; s < kUnitRing; ++s) {
             mbar_init_count(&sh.unit_full[s], 1);
-            mbar_init_count(&sh.unit_empty[s], 9);
+            mbar_init_count(&sh.unit_empty[s], S::ROW_WARPS + 1);
         }
         sh.gave_up = 0;
         mbar_init_done();
     }
     if (warp == kMma)
-        tmem_alloc<1>(&sh.tmem, 512);
+        tmem_take(&sh.tmem, S::TMEM);
     if (warp == kTma && lane < 4)
         tma_prefetch_map(lane == 0 ? &f.q.map : lane == 1 ? &f.k.map : lane == 2 ? &f.v.map : &f.dout.map);
     tmem_fence_before();
@@ -1217,14 +1270,14 @@ __global__ void __launch_bounds__(BwdShape<DP>::THREADS, 1) k_attn_dkv(const __g
             ++units;
             return true;
         };
-        auto load = [&](unsigned char *to, const HeadsMap &m, int32_t row, int32_t head, uint64_t *bar) {
+        auto load = [&](unsigned char *to, const HeadsMap &m, int32_t row, int32_t head, int box, uint64_t *bar) {
 #pragma unroll
             for (int x = 0; x < S::BOXES; ++x)
-                load_box(smem_addr(to) + x * 16384, m, 64 * x, row, head, smem_addr(bar));
+                load_box(smem_addr(to) + x * box, m, 64 * x, row, head, smem_addr(bar));
         };
         for (int64_t i = blockIdx.x; ok && i < all; i += gridDim.x) {
             KeyUnit u;
-            if (!key_unit(f, i, lane, u))
+            if (!key_unit<BN>(f, i, lane, u))
                 continue;
             ok = publish(u);
             if (!ok || u.low > u.high)
@@ -1234,8 +1287,8 @@ __global__ void __launch_bounds__(BwdShape<DP>::THREADS, 1) k_attn_dkv(const __g
                 break;
             if (elect_one()) {
                 mbar_expect(&sh.kv_full, 2 * S::TILE);
-                load(s_k, f.k, u.k_row, u.head, &sh.kv_full);
-                load(s_v, f.v, u.k_row, u.head, &sh.kv_full);
+                load(s_k, f.k, u.k_row, u.head, 16384, &sh.kv_full);
+                load(s_v, f.v, u.k_row, u.head, 16384, &sh.kv_full);
             }
             __syncwarp();
             ++kvn;
@@ -1246,18 +1299,19 @@ __global__ void __launch_bounds__(BwdShape<DP>::THREADS, 1) k_attn_dkv(const __g
                     if (!ok)
                         break;
                     if (elect_one()) {
-                        mbar_expect(&sh.q_full[st], S::TILE + 1024);
-                        load(s_q + st * S::TILE, f.q, u.q_row + 128 * t, h, &sh.q_full[st]);
-                        bulk_copy(smem_addr(s_stats + st * 256), f.stats + (h * f.q_tiles + u.stats + t) * 256, 1024,
-                                  smem_addr(&sh.q_full[st]));
+                        mbar_expect(&sh.q_full[st], S::MOVING + 8 * BN);
+                        load(s_q + st * S::MOVING, f.q, u.q_row + BN * t, h, BN * 128, &sh.q_full[st]);
+                        const float *const from = f.stats + (h * f.q_tiles + u.stats + BN * t / 128) * 256 + BN * t % 128;
+                        bulk_copy(smem_addr(s_stats + st * 2 * BN), from, 4 * BN, smem_addr(&sh.q_full[st]));
+                        bulk_copy(smem_addr(s_stats + st * 2 * BN + BN), from + 128, 4 * BN, smem_addr(&sh.q_full[st]));
                     }
                     __syncwarp();
                     ok = wait(&sh.o_empty[st], parity);
                     if (!ok)
                         break;
                     if (elect_one()) {
-                        mbar_expect(&sh.o_full[st], S::TILE);
-                        load(s_o + st * S::TILE, f.dout, u.q_row + 128 * t, h, &sh.o_full[st]);
+                        mbar_expect(&sh.o_full[st], S::MOVING);
+                        load(s_o + st * S::MOVING, f.dout, u.q_row + BN * t, h, BN * 128, &sh.o_full[st]);
                     }
                     __syncwarp();
                     ++qn;
@@ -1270,12 +1324,12 @@ __global__ void __launch_bounds__(BwdShape<DP>::THREADS, 1) k_attn_dkv(const __g
         }
     } else if (warp == kMma) {
         constexpr bool kBf16 = DT == ZERO_BF16;
-        const uint32_t desc_s = product_desc(kBf16, false, false, 128, 128);
+        const uint32_t desc_s = product_desc(kBf16, false, false, 128, BN);
         const int wide = (a.dim + 15) & ~15, steps = wide / 16;
         const uint32_t desc_acc = product_desc(kBf16, false, true, 128, wide);
         const uint64_t dk0 = operand_desc(smem_addr(s_k), 16, 1024), dv0 = operand_desc(smem_addr(s_v), 16, 1024);
         const uint64_t dq0 = operand_desc(smem_addr(s_q), 16, 1024), do0 = operand_desc(smem_addr(s_o), 16, 1024);
-        const uint64_t tq0 = operand_desc(smem_addr(s_q), 16384, 1024), to0 = operand_desc(smem_addr(s_o), 16384, 1024);
+        const uint64_t tq0 = operand_desc(smem_addr(s_q), BN * 128, 1024), to0 = operand_desc(smem_addr(s_o), BN * 128, 1024);
         uint32_t kvn = 0, qn = 0, n = 0;
         bool ok = true;
         KeyUnit u;
@@ -1288,7 +1342,7 @@ __global__ void __launch_bounds__(BwdShape<DP>::THREADS, 1) k_attn_dkv(const __g
                 break;
             ++kvn;
             tmem_fence_after();
-            inner_products<DP>(tmem, dk0, dq0 + (((qn & 1) * S::TILE) >> 4), desc_s, steps);
+            inner_products<DP, 128, BN>(tmem, dk0, dq0 + (((qn & 1) * S::MOVING) >> 4), desc_s, steps);
             tensor_commit_elected(&sh.s_full);
             for (int32_t i = 0; i < count; ++i, ++qn, ++n) {
                 const uint32_t st = qn & 1;
@@ -1296,13 +1350,13 @@ __global__ void __launch_bounds__(BwdShape<DP>::THREADS, 1) k_attn_dkv(const __g
                 if (!ok)
                     break;
                 tmem_fence_after();
-                inner_products<DP>(tmem + 128, dv0, do0 + ((st * S::TILE) >> 4), desc_s, steps);
+                inner_products<DP, 128, BN>(tmem + kDp, dv0, do0 + ((st * S::MOVING) >> 4), desc_s, steps);
                 tensor_commit_elected(&sh.dp_full);
                 ok = wait(&sh.p_full, n & 1);
                 if (!ok)
                     break;
                 tmem_fence_after();
-                outer_products(tmem + 256, tmem, to0 + ((st * S::TILE) >> 4), desc_acc, i != 0);
+                outer_products<BN>(tmem + kDv, tmem, to0 + ((st * S::MOVING) >> 4), desc_acc, i != 0);
                 tensor_commit_elected(&sh.o_empty[st]);
                 if (i + 1 < count) {
                     const uint32_t to = (qn + 1) & 1;
@@ -1310,14 +1364,14 @@ __global__ void __launch_bounds__(BwdShape<DP>::THREADS, 1) k_attn_dkv(const __g
                     if (!ok)
                         break;
                     tmem_fence_after();
-                    inner_products<DP>(tmem, dk0, dq0 + ((to * S::TILE) >> 4), desc_s, steps);
+                    inner_products<DP, 128, BN>(tmem, dk0, dq0 + ((to * S::MOVING) >> 4), desc_s, steps);
                     tensor_commit_elected(&sh.s_full);
                 }
                 ok = wait(&sh.ds_full, n & 1);
                 if (!ok)
                     break;
                 tmem_fence_after();
-                outer_products(tmem + 384, tmem + 128, tq0 + ((st * S::TILE) >> 4), desc_acc, i != 0);
+                outer_products<BN>(tmem + kDk, tmem + kDp, tq0 + ((st * S::MOVING) >> 4), desc_acc, i != 0);
                 tensor_commit_elected(&sh.q_empty[st]);
                 if (i + 1 == count) {
                     tensor_commit_elected(&sh.kv_empty);
@@ -1328,7 +1382,8 @@ __global__ void __launch_bounds__(BwdShape<DP>::THREADS, 1) k_attn_dkv(const __g
     } else {
         const int half = warp >> 2, quarter = warp & 3;
         const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
-        const uint32_t at_s = tmem + lanes + half * 64, at_p = at_s + 128;
+        const uint32_t at_s = tmem + lanes + half * 64, at_p = at_s + kDp;
+        uint4 *const stage = reinterpret_cast<uint4 *>(s_out + warp * 2048);
         uint32_t qn = 0, n = 0, accs = 0;
         bool ok = true;
         KeyUnit u;
@@ -1338,14 +1393,14 @@ __global__ void __launch_bounds__(BwdShape<DP>::THREADS, 1) k_attn_dkv(const __g
             int32_t t = u.low;
             for (int32_t i = 0; i < count; ++i, ++qn, ++n) {
                 const uint32_t st = qn & 1;
-                const int32_t p0 = 128 * t + u.lk - u.lq, nq = u.lq - 128 * t;
-                const bool whole = nq >= 128 && u.first + 127 <= p0 &&
-                                   (p0 + 127 - u.first < a.window || u.first + 127 < a.sinks);
+                const int32_t p0 = BN * t + u.lk - u.lq, nq = u.lq - BN * t;
+                const bool whole = nq >= BN && u.first + 127 <= p0 &&
+                                   (p0 + BN - 1 - u.first < a.window || u.first + 127 < a.sinks);
                 ok = wait(&sh.s_full, n & 1) && wait(&sh.q_full[st], (qn >> 1) & 1);
                 if (!ok)
                     break;
                 tmem_fence_after();
-                const float *lse2 = s_stats + st * 256 + half * 64, *delta = lse2 + 128;
+                const float *lse2 = s_stats + st * 2 * BN + half * 64, *delta = lse2 + BN;
                 float p[64];
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
@@ -1383,16 +1438,16 @@ __global__ void __launch_bounds__(BwdShape<DP>::THREADS, 1) k_attn_dkv(const __g
                         w[e] = pack2<DT>(p[32 * c + 2 * e], p[32 * c + 2 * e + 1]);
                     tmem_store16(at_s + 16 * c, w);
                 }
-                if (nq < 128) {
+                if (nq < BN) {
                     // rows behind the last query: zeros, since 0 times what they hold may not be 0
                     ok = wait(&sh.o_full[st], (qn >> 1) & 1);
                     if (!ok)
                         break;
-                    for (int k = nq * 8 + threadIdx.x; k < 1024; k += 256)
+                    for (int k = nq * 8 + threadIdx.x; k < BN * 8; k += S::ROW_WARPS * 32)
 #pragma unroll
                         for (int b = 0; b < S::BOXES; ++b) {
-                            *reinterpret_cast<uint4 *>(s_o + st * S::TILE + b * 16384 + k * 16) = make_uint4(0, 0, 0, 0);
-                            *reinterpret_cast<uint4 *>(s_q + st * S::TILE + b * 16384 + k * 16) = make_uint4(0, 0, 0, 0);
+                            *reinterpret_cast<uint4 *>(s_o + st * S::MOVING + b * BN * 128 + k * 16) = make_uint4(0, 0, 0, 0);
+                            *reinterpret_cast<uint4 *>(s_q + st * S::MOVING + b * BN * 128 + k * 16) = make_uint4(0, 0, 0, 0);
                         }
                     fence_proxy_async();
                 }
@@ -1442,40 +1497,39 @@ __global__ void __launch_bounds__(BwdShape<DP>::THREADS, 1) k_attn_dkv(const __g
             }
             if (!ok)
                 break;
-            // dv by the first four warps, dk by the others
-            const uint32_t from = tmem + lanes + 256 + half * 128;
-            const float by = half ? f.scale : 1.0f;
-            const Heads &to = half ? f.dk : f.dv;
-            for (int c = 0; c < a.dim; c += 32) {
-                uint32_t o[32];
-                if (count > 0) {
-                    tmem_load32(from + c, o);
-                    tmem_wait_loads(o);
-                } else {
+            // dv by the first four warps and dk by the others, or both by the four that there are
+            const int32_t left = u.lk - u.first - quarter * 32;  // rows of this warp
+#pragma unroll 1
+            for (int which = S::ROW_WARPS == 8 ? half : 0; which < (S::ROW_WARPS == 8 ? half + 1 : 2); ++which) {
+                const uint32_t from = tmem + lanes + (which ? kDk : kDv);
+                const float by = which ? f.scale : 1.0f;
+                const Heads to{which ? f.dk.p : f.dv.p, which ? f.dk.ld : f.dv.ld, which ? f.dk.hd : f.dv.hd};
+                uint16_t *out = static_cast<uint16_t *>(const_cast<void *>(to.p)) + ((int64_t)u.k_row + quarter * 32) * to.ld +
+                                u.head * to.hd;
+                float *sums = f.partial + ((u.slot * 2 + which) * 128 + quarter * 32 + lane) * a.dim;
+#pragma unroll 1
+                for (int c = 0; c < a.dim; c += 32) {
+                    uint32_t w[16], o[32];
 #pragma unroll
                     for (int e = 0; e < 32; ++e)
                         o[e] = 0;
+                    if (count > 0) {
+                        tmem_load32(from + c, o);
+                        tmem_wait_loads(o);
+                    }
+                    if (u.slot >= 0) {
+#pragma unroll
+                        for (int e = 0; e < 32; e += 4)
+                            if (c + e < a.dim)
+                                *reinterpret_cast<uint4 *>(sums + c + e) = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+                        __syncwarp();
+                        continue;
+                    }
+#pragma unroll
+                    for (int e = 0; e < 16; ++e)
+                        w[e] = pack2<DT>(__uint_as_float(o[2 * e]) * by, __uint_as_float(o[2 * e + 1]) * by);
+                    store_rows(stage, lane, w, out + c, to.ld, left, a.dim - c);
                 }
-                if (u.slot >= 0) {
-                    float *out = f.partial + ((u.slot * 2 + half) * 128 + quarter * 32 + lane) * a.dim + c;
-#pragma unroll
-                    for (int e = 0; e < 32; e += 4)
-                        if (c + e < a.dim)
-                            *reinterpret_cast<uint4 *>(out + e) = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
-                } else if (j < u.lk) {
-                    uint16_t *out = static_cast<uint16_t *>(const_cast<void *>(to.p)) +
-                                    ((int64_t)u.k_row + quarter * 32 + lane) * to.ld + u.head * to.hd + c;
-#pragma unroll
-                    for (int e = 0; e < 32; e += 8)
-                        if (c + e < a.dim) {
-                            uint32_t w[4];
-#pragma unroll
-                            for (int i = 0; i < 4; ++i)
-                                w[i] = pack2<DT>(__uint_as_float(o[e + 2 * i]) * by, __uint_as_float(o[e + 2 * i + 1]) * by);
-                            *reinterpret_cast<uint4 *>(out + e) = make_uint4(w[0], w[1], w[2], w[3]);
-                        }
-                }
-                __syncwarp();
             }
         }
     }
@@ -1494,7 +1548,7 @@ __global__ void __launch_bounds__(BwdShape<DP>::THREADS, 1) k_attn_dkv(const __g
         // no result of this CTA is to be taken for one
         for (int64_t i = blockIdx.x; i < all; i += gridDim.x) {
             KeyUnit u;
-            if (!key_unit(f, i, lane, u))
+            if (!key_unit<BN>(f, i, lane, u))
                 continue;
             for (int32_t r = warp; r < 128; r += S::THREADS / 32)
                 for (int e = lane; e < a.dim; e += 32)
@@ -1509,7 +1563,7 @@ __global__ void __launch_bounds__(BwdShape<DP>::THREADS, 1) k_attn_dkv(const __g
         }
     }
     if (warp == kMma)
-        tmem_free<1>(tmem, 512);
+        tmem_give(tmem, S::TMEM);
 }
 
 // The sums of the first keys' tiles from their parts, in order: a block takes
@@ -1528,7 +1582,7 @@ __global__ void __launch_bounds__(kThreads) k_attn_join(const __grid_constant__ 
         const Seq sq = sequence(a, s);
         if (first + rows >= sq.lk || first >= a.sinks)
             continue;
-        const QueryTiles t = query_tiles(a, first, sq.lq, sq.lk);
+        const QueryTiles t = query_tiles<128>(a, first, sq.lq, sq.lk);
         if (!is_split(f, first, t))
             continue;
         const int64_t base = a.q_offsets ? sq.q0 / (128 * f.chunk) + s : 0;
@@ -1569,17 +1623,19 @@ struct QueryShared {
 // see: S = Q K^T, dP = dO V^T, dS = exp(S - lse) (dP - delta), dQ += dS K.
 // (S and dP are worked out here again, two products of seven, so that dq is
 // summed in one place and in one order, without atomics.)
-template <int DT, int DP>
-__global__ void __launch_bounds__(BwdShape<DP>::THREADS, 1) k_attn_dq(const __grid_constant__ BwdTiles f)
+template <int DT, class S>
+__global__ void __launch_bounds__(S::THREADS, S::PER_SM) k_attn_dq(const __grid_constant__ BwdTiles f)
 {
-    using S = BwdShape<DP>;
+    constexpr int DP = S::DP, BN = S::BN;
     extern __shared__ unsigned char smem_raw[];
     __shared__ QueryShared sh;
     unsigned char *smem = smem_raw + ((1024 - (smem_addr(smem_raw) & 1023u)) & 1023u);
-    unsigned char *const s_q = smem, *const s_o = smem + S::TILE, *const s_k = s_o + S::TILE, *const s_v = s_k + 2 * S::TILE;
+    unsigned char *const s_q = smem, *const s_o = smem + S::TILE, *const s_k = s_o + S::TILE, *const s_v = s_k + 2 * S::MOVING;
+    unsigned char *const s_out = s_v + 2 * S::MOVING;
     const Attn &a = f.a;
     const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
-    constexpr int kTma = 8, kMma = 9;
+    constexpr int kTma = S::ROW_WARPS, kMma = S::ROW_WARPS + 1;
+    constexpr int kDp = 2 * BN, kDq = 3 * BN;  // columns of tensor memory
 
     if (threadIdx.x == 0) {
         mbar_init_count(&sh.q_full, 1);
@@ -1591,17 +1647,17 @@ __global__ void __launch_bounds__(BwdShape<DP>::THREADS, 1) k_attn_dq(const __gr
             mbar_init_count(&sh.v_empty[s], 1);
         }
         mbar_init_count(&sh.sp_full, 1);
-        mbar_init_count(&sh.ds_full, 8);
+        mbar_init_count(&sh.ds_full, S::ROW_WARPS);
         mbar_init_count(&sh.acc_full, 1);
         for (int s = 0; s < kUnitRing; ++s) {
             mbar_init_count(&sh.unit_full[s], 1);
-            mbar_init_count(&sh.unit_empty[s], 9);
+            mbar_init_count(&sh.unit_empty[s], S::ROW_WARPS + 1);
         }
         sh.gave_up = 0;
         mbar_init_done();
     }
     if (warp == kMma)
-        tmem_alloc<1>(&sh.tmem, 512);
+        tmem_take(&sh.tmem, S::TMEM);
     if (warp == kTma && lane < 4)
         tma_prefetch_map(lane == 0 ? &f.q.map : lane == 1 ? &f.k.map : lane == 2 ? &f.v.map : &f.dout.map);
     tmem_fence_before();
@@ -1648,17 +1704,17 @@ __global__ void __launch_bounds__(BwdShape<DP>::THREADS, 1) k_attn_dq(const __gr
             ++units;
             return true;
         };
-        auto load = [&](unsigned char *to, const HeadsMap &m, int32_t row, int32_t head, uint64_t *bar) {
+        auto load = [&](unsigned char *to, const HeadsMap &m, int32_t row, int32_t head, int box, uint64_t *bar) {
 #pragma unroll
             for (int x = 0; x < S::BOXES; ++x)
-                load_box(smem_addr(to) + x * 16384, m, 64 * x, row, head, smem_addr(bar));
+                load_box(smem_addr(to) + x * box, m, 64 * x, row, head, smem_addr(bar));
         };
         for (int64_t i = blockIdx.x; ok && i < all; i += gridDim.x) {
             QueryUnit u;
             if (!unit_at(i, u))
                 continue;
             ok = publish(u);
-            const KeyTiles kt = key_tiles(a, u.first, u.lq, u.lk);
+            const KeyTiles kt = key_tiles<BN>(a, u.first, u.lq, u.lk);
             const TileList list = tile_list(kt, KeyTiles{0, -1, 0, false});
             if (!ok || list.n == 0)
                 continue;
@@ -1667,29 +1723,29 @@ __global__ void __launch_bounds__(BwdShape<DP>::THREADS, 1) k_attn_dq(const __gr
                 break;
             if (elect_one()) {
                 mbar_expect(&sh.q_full, 2 * S::TILE);
-                load(s_q, f.q, u.q_row, u.head, &sh.q_full);
-                load(s_o, f.dout, u.q_row, u.head, &sh.q_full);
+                load(s_q, f.q, u.q_row, u.head, 16384, &sh.q_full);
+                load(s_o, f.dout, u.q_row, u.head, 16384, &sh.q_full);
             }
             __syncwarp();
             ++un;
             const int32_t g = u.head / a.group;
             for (int32_t n = 0; n < list.n; ++n, ++kn) {
                 const uint32_t st = kn & 1, parity = ((kn >> 1) & 1) ^ 1;
-                const int32_t row = u.k_row + 128 * list.at(n);
+                const int32_t row = u.k_row + BN * list.at(n);
                 ok = wait(&sh.k_empty[st], parity);
                 if (!ok)
                     break;
                 if (elect_one()) {
-                    mbar_expect(&sh.k_full[st], S::TILE);
-                    load(s_k + st * S::TILE, f.k, row, g, &sh.k_full[st]);
+                    mbar_expect(&sh.k_full[st], S::MOVING);
+                    load(s_k + st * S::MOVING, f.k, row, g, BN * 128, &sh.k_full[st]);
                 }
                 __syncwarp();
                 ok = wait(&sh.v_empty[st], parity);
                 if (!ok)
                     break;
                 if (elect_one()) {
-                    mbar_expect(&sh.v_full[st], S::TILE);
-                    load(s_v + st * S::TILE, f.v, row, g, &sh.v_full[st]);
+                    mbar_expect(&sh.v_full[st], S::MOVING);
+                    load(s_v + st * S::MOVING, f.v, row, g, BN * 128, &sh.v_full[st]);
                 }
                 __syncwarp();
             }
@@ -1701,17 +1757,17 @@ __global__ void __launch_bounds__(BwdShape<DP>::THREADS, 1) k_attn_dq(const __gr
         }
     } else if (warp == kMma) {
         constexpr bool kBf16 = DT == ZERO_BF16;
-        const uint32_t desc_s = product_desc(kBf16, false, false, 128, 128);
+        const uint32_t desc_s = product_desc(kBf16, false, false, 128, BN);
         const int wide = (a.dim + 15) & ~15, steps = wide / 16;
         const uint32_t desc_acc = product_desc(kBf16, false, true, 128, wide);
         const uint64_t dq0 = operand_desc(smem_addr(s_q), 16, 1024), do0 = operand_desc(smem_addr(s_o), 16, 1024);
         const uint64_t dk0 = operand_desc(smem_addr(s_k), 16, 1024), dv0 = operand_desc(smem_addr(s_v), 16, 1024);
-        const uint64_t tk0 = operand_desc(smem_addr(s_k), 16384, 1024);
+        const uint64_t tk0 = operand_desc(smem_addr(s_k), BN * 128, 1024);
         uint32_t un = 0, kn = 0, dsn = 0;
         bool ok = true;
         QueryUnit u;
         while (ok && next(u)) {
-            const KeyTiles kt = key_tiles(a, u.first, u.lq, u.lk);
+            const KeyTiles kt = key_tiles<BN>(a, u.first, u.lq, u.lk);
             const TileList list = tile_list(kt, KeyTiles{0, -1, 0, false});
             if (list.n == 0)
                 continue;
@@ -1724,7 +1780,7 @@ __global__ void __launch_bounds__(BwdShape<DP>::THREADS, 1) k_attn_dq(const __gr
                 if (!ok)
                     return;
                 tmem_fence_after();
-                inner_products<DP>(tmem + st * 128, dq0, dk0 + ((st * S::TILE) >> 4), desc_s, steps);
+                inner_products<DP, 128, BN>(tmem + st * BN, dq0, dk0 + ((st * S::MOVING) >> 4), desc_s, steps);
             };
             auto grads = [&](uint32_t at) {
                 const uint32_t st = at & 1;
@@ -1732,7 +1788,7 @@ __global__ void __launch_bounds__(BwdShape<DP>::THREADS, 1) k_attn_dq(const __gr
                 if (!ok)
                     return;
                 tmem_fence_after();
-                inner_products<DP>(tmem + 256, do0, dv0 + ((st * S::TILE) >> 4), desc_s, steps);
+                inner_products<DP, 128, BN>(tmem + kDp, do0, dv0 + ((st * S::MOVING) >> 4), desc_s, steps);
                 tensor_commit_elected(&sh.sp_full);
                 tensor_commit_elected(&sh.v_empty[st]);
             };
@@ -1750,7 +1806,7 @@ __global__ void __launch_bounds__(BwdShape<DP>::THREADS, 1) k_attn_dq(const __gr
                     grads(kn + 1);
                 if (!ok)
                     break;
-                outer_products(tmem + 384, tmem + st * 128, tk0 + ((st * S::TILE) >> 4), desc_acc, n != 0);
+                outer_products<BN>(tmem + kDq, tmem + st * BN, tk0 + ((st * S::MOVING) >> 4), desc_acc, n != 0);
                 tensor_commit_elected(&sh.k_empty[st]);
                 if (n + 1 == list.n) {
                     tensor_commit_elected(&sh.q_empty);
@@ -1761,11 +1817,12 @@ __global__ void __launch_bounds__(BwdShape<DP>::THREADS, 1) k_attn_dq(const __gr
     } else {
         const int half = warp >> 2, quarter = warp & 3;
         const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
+        uint4 *const stage = reinterpret_cast<uint4 *>(s_out + warp * 2048);
         uint32_t kn = 0, accs = 0;
         bool ok = true;
         QueryUnit u;
         while (ok && next(u)) {
-            const KeyTiles kt = key_tiles(a, u.first, u.lq, u.lk);
+            const KeyTiles kt = key_tiles<BN>(a, u.first, u.lq, u.lk);
             const TileList list = tile_list(kt, KeyTiles{0, -1, 0, false});
             const int32_t row = u.first + quarter * 32 + lane, p = row + u.lk - u.lq;
             const int32_t p_first = u.first + u.lk - u.lq;
@@ -1774,14 +1831,14 @@ __global__ void __launch_bounds__(BwdShape<DP>::THREADS, 1) k_attn_dq(const __gr
             const float lse2 = stats[0], delta = stats[128];
             for (int32_t n = 0; n < list.n; ++n, ++kn) {
                 const uint32_t st = kn & 1;
-                const int32_t k_first = list.at(n) * 128;
-                const bool whole = k_first + 127 <= p_first &&
-                                   (k_first > p_last - a.window || k_first + 127 < a.sinks);
+                const int32_t k_first = list.at(n) * BN;
+                const bool whole = k_first + BN - 1 <= p_first &&
+                                   (k_first > p_last - a.window || k_first + BN - 1 < a.sinks);
                 ok = wait(&sh.sp_full, kn & 1);
                 if (!ok)
                     break;
                 tmem_fence_after();
-                const uint32_t at_s = tmem + lanes + st * 128 + half * 64, at_p = tmem + lanes + 256 + half * 64;
+                const uint32_t at_s = tmem + lanes + st * BN + half * 64, at_p = tmem + lanes + kDp + half * 64;
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
                     uint32_t r[32], g[32], w[16];
@@ -1804,12 +1861,12 @@ __global__ void __launch_bounds__(BwdShape<DP>::THREADS, 1) k_attn_dq(const __gr
                         w[e] = pack2<DT>(__uint_as_float(r[2 * e]), __uint_as_float(r[2 * e + 1]));
                     tmem_store16(at_s + 16 * c, w);
                 }
-                if (k_first + 128 > u.lk) {
+                if (k_first + BN > u.lk) {
                     // rows behind the last key: zeros, since 0 times what they hold may not be 0
-                    for (int k = (u.lk - k_first) * 8 + threadIdx.x; k < 1024; k += 256)
+                    for (int k = (u.lk - k_first) * 8 + threadIdx.x; k < BN * 8; k += S::ROW_WARPS * 32)
 #pragma unroll
                         for (int b = 0; b < S::BOXES; ++b)
-                            *reinterpret_cast<uint4 *>(s_k + st * S::TILE + b * 16384 + k * 16) = make_uint4(0, 0, 0, 0);
+                            *reinterpret_cast<uint4 *>(s_k + st * S::MOVING + b * BN * 128 + k * 16) = make_uint4(0, 0, 0, 0);
                     fence_proxy_async();
                 }
                 tmem_wait_stores();
@@ -1825,33 +1882,24 @@ __global__ void __launch_bounds__(BwdShape<DP>::THREADS, 1) k_attn_dq(const __gr
             }
             if (!ok)
                 break;
-            // a half of the columns each
-            const int cols = ((a.dim + 63) / 64) * 32;
-            for (int c = half * cols; c < a.dim && c < (half + 1) * cols; c += 32) {
-                uint32_t o[32];
+            // (of eight warps four take every other 32 columns)
+            const int32_t left = u.lq - u.first - quarter * 32;  // rows of this warp
+            uint16_t *out = static_cast<uint16_t *>(const_cast<void *>(f.dq.p)) + ((int64_t)u.q_row + quarter * 32) * f.dq.ld +
+                            u.head * f.dq.hd;
+#pragma unroll 1
+            for (int c = half * 32; c < a.dim; c += S::ROW_WARPS * 8) {
+                uint32_t w[16], o[32];
+#pragma unroll
+                for (int e = 0; e < 32; ++e)
+                    o[e] = 0;
                 if (list.n > 0) {
-                    tmem_load32(tmem + lanes + 384 + c, o);
+                    tmem_load32(tmem + lanes + kDq + c, o);
                     tmem_wait_loads(o);
-                } else {
-#pragma unroll
-                    for (int e = 0; e < 32; ++e)
-                        o[e] = 0;
                 }
-                if (row < u.lq) {
-                    uint16_t *out = static_cast<uint16_t *>(const_cast<void *>(f.dq.p)) +
-                                    ((int64_t)u.q_row + quarter * 32 + lane) * f.dq.ld + u.head * f.dq.hd + c;
 #pragma unroll
-                    for (int e = 0; e < 32; e += 8)
-                        if (c + e < a.dim) {
-                            uint32_t w[4];
-#pragma unroll
-                            for (int i = 0; i < 4; ++i)
-                                w[i] = pack2<DT>(__uint_as_float(o[e + 2 * i]) * f.scale,
-                                                 __uint_as_float(o[e + 2 * i + 1]) * f.scale);
-                            *reinterpret_cast<uint4 *>(out + e) = make_uint4(w[0], w[1], w[2], w[3]);
-                        }
-                }
-                __syncwarp();
+                for (int e = 0; e < 16; ++e)
+                    w[e] = pack2<DT>(__uint_as_float(o[2 * e]) * f.scale, __uint_as_float(o[2 * e + 1]) * f.scale);
+                store_rows(stage, lane, w, out + c, f.dq.ld, left, a.dim - c);
             }
         }
     }
@@ -1878,7 +1926,7 @@ __global__ void __launch_bounds__(BwdShape<DP>::THREADS, 1) k_attn_dq(const __gr
         }
     }
     if (warp == kMma)
-        tmem_free<1>(tmem, 512);
+        tmem_give(tmem, S::TMEM);
 }
 
 // ------------------------------------------------------------- host side
@@ -1946,7 +1994,7 @@ Attn attn_of(const zero_attention_t *a)
 }
 
 // The map of an array of heads; both strides are positive or not needed.
-int heads_map(HeadsMap *m, const Heads &h, int64_t tokens, int64_t heads, int64_t dim, int32_t dtype)
+int heads_map(HeadsMap *m, const Heads &h, int64_t tokens, int64_t heads, int64_t dim, int box_rows, int32_t dtype)
 {
     const EncodeTiled encode = encode_tiled();
     if (!encode) {
@@ -1958,12 +2006,12 @@ int heads_map(HeadsMap *m, const Heads &h, int64_t tokens, int64_t heads, int64_
     m->heads_last = ld < hd;
     cuuint64_t dims[3] = {(cuuint64_t)dim, (cuuint64_t)heads, (cuuint64_t)tokens};
     cuuint64_t strides[2] = {(cuuint64_t)hd * 2, (cuuint64_t)ld * 2};
-    cuuint32_t box[3] = {64, 1, 128};
+    cuuint32_t box[3] = {64, 1, (cuuint32_t)box_rows};
     const cuuint32_t step[3] = {1, 1, 1};
     if (m->heads_last) {
         dims[1] = (cuuint64_t)tokens, dims[2] = (cuuint64_t)heads;
         strides[0] = (cuuint64_t)ld * 2, strides[1] = (cuuint64_t)hd * 2;
-        box[1] = 128, box[2] = 1;
+        box[1] = (cuuint32_t)box_rows, box[2] = 1;
     }
     const CUresult r = encode(&m->map, dtype == ZERO_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
                               3, const_cast<void *>(h.p), dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
@@ -1978,15 +2026,24 @@ int heads_map(HeadsMap *m, const Heads &h, int64_t tokens, int64_t heads, int64_
 
 constexpr uint64_t kWaitLimit = 4000000000u;
 
-template <int DT, int DP>
-int launch_tiles(const FwdTiles &t, cudaStream_t st)
+// Heads of up to 64 leave room in tensor memory for three CTAs of one tile of
+// queries each, whose turns hide one another's waits; wider ones for one CTA
+// of two tiles, whose products run while the other's weights are worked out.
+using Narrow = FwdShape<64, 1, 128, 2>;
+using Wide = FwdShape<128, 2, 128, 1>;
+
+template <int DT, class S>
+int launch_tiles(FwdTiles &t, const Fwd &f, const zero_attention_t *a, cudaStream_t st)
 {
-    using S = FwdShape<DP>;
-    auto kernel = k_attn_tiles<DT, DP>;
+    ZERO_TRY(heads_map(&t.q, f.q, a->q_tokens, a->q_heads, a->head_dim, 128, a->dtype));
+    ZERO_TRY(heads_map(&t.k, f.k, a->k_tokens, a->k_heads, a->head_dim, S::BN, a->dtype));
+    ZERO_TRY(heads_map(&t.v, f.v, a->k_tokens, a->k_heads, a->head_dim, S::BN, a->dtype));
+    t.tiles = tile_numbers(a->q_tokens, a->sequences, !a->q_offsets, 128 * S::QT);
+    auto kernel = k_attn_tiles<DT, S>;
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::SMEM);
-    const int64_t units = t.tiles * t.a.q_heads;
+    const int64_t units = t.tiles * t.a.q_heads, most = (int64_t)sm_count() * S::PER_SM;
     if (e == cudaSuccess) {
-        kernel<<<(unsigned)(units < sm_count() ? units : sm_count()), S::THREADS, S::SMEM, st>>>(t);
+        kernel<<<(unsigned)(units < most ? units : most), S::THREADS, S::SMEM, st>>>(t);
         e = cudaGetLastError();
     }
     if (e != cudaSuccess) {
@@ -2000,17 +2057,13 @@ int launch_tiles(const FwdTiles &t, cudaStream_t st)
 int forward_tiles(const Fwd &f, const zero_attention_t *a, void *ws, cudaStream_t st)
 {
     FwdTiles t{};
-    ZERO_TRY(heads_map(&t.q, f.q, a->q_tokens, a->q_heads, a->head_dim, a->dtype));
-    ZERO_TRY(heads_map(&t.k, f.k, a->k_tokens, a->k_heads, a->head_dim, a->dtype));
-    ZERO_TRY(heads_map(&t.v, f.v, a->k_tokens, a->k_heads, a->head_dim, a->dtype));
     t.a = f.a, t.out = f.out, t.lse = f.lse;
-    t.tiles = tile_numbers(a->q_tokens, a->sequences, !a->q_offsets, 256);
     t.scale_log2 = (float)(a->scale * 1.4426950408889634);
     t.hdr = static_cast<WsHeader *>(ws);
     t.limit_ns = kWaitLimit;
     if (a->head_dim <= 64)
-        return a->dtype == ZERO_F16 ? launch_tiles<ZERO_F16, 64>(t, st) : launch_tiles<ZERO_BF16, 64>(t, st);
-    return a->dtype == ZERO_F16 ? launch_tiles<ZERO_F16, 128>(t, st) : launch_tiles<ZERO_BF16, 128>(t, st);
+        return a->dtype == ZERO_F16 ? launch_tiles<ZERO_F16, Narrow>(t, f, a, st) : launch_tiles<ZERO_BF16, Narrow>(t, f, a, st);
+    return a->dtype == ZERO_F16 ? launch_tiles<ZERO_F16, Wide>(t, f, a, st) : launch_tiles<ZERO_BF16, Wide>(t, f, a, st);
 }
 
 // Up to here, on average over the sequences, queries go a few rows at a time
@@ -2132,10 +2185,17 @@ AttnSpace attn_space(const zero_attention_t *a, bool backward)
     return s;
 }
 
-template <int DT, int DP>
-int launch_backward(const BwdTiles &t, cudaStream_t st)
+// (As forward: heads of up to 64 leave room for two CTAs with smaller tiles.)
+using NarrowBwd = BwdShape<64, 64, 2>;
+using WideBwd = BwdShape<128, 128, 1>;
+
+struct BwdArrays {
+    Heads dout, q, k, v;
+};
+
+template <int DT, class S>
+int launch_backward(BwdTiles &t, const BwdArrays &h, const zero_attention_t *a, cudaStream_t st)
 {
-    using S = BwdShape<DP>;
     const char *what = "k_attn_dkv";
     cudaError_t e = cudaSuccess;
     auto launch = [&](void (*kernel)(BwdTiles), int64_t units) {
@@ -2144,8 +2204,9 @@ int launch_backward(const BwdTiles &t, cudaStream_t st)
         e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::SMEM);
         if (e != cudaSuccess)
             return;
+        const int64_t most = (int64_t)sm_count() * S::PER_SM;
         cudaLaunchConfig_t cfg = {};
-        cfg.gridDim = dim3((unsigned)(units < sm_count() ? units : sm_count()));
+        cfg.gridDim = dim3((unsigned)(units < most ? units : most));
         cfg.blockDim = dim3(S::THREADS);
         cfg.dynamicSmemBytes = S::SMEM;
         cfg.stream = st;
@@ -2156,7 +2217,24 @@ int launch_backward(const BwdTiles &t, cudaStream_t st)
         cfg.numAttrs = t.q_tiles > 0;  // (a kernel of this call is before it)
         e = cudaLaunchKernelEx(&cfg, kernel, t);
     };
-    launch(k_attn_dkv<DT, DP>, t.split_units + t.k_tiles * t.a.k_heads);
+    // the maps: what a kernel keeps in boxes of 128 rows, what moves past it in boxes of BN
+    auto maps = [&](int q_rows, int k_rows) {
+        if (a->q_tokens > 0) {
+            ZERO_TRY(heads_map(&t.q, h.q, a->q_tokens, a->q_heads, a->head_dim, q_rows, a->dtype));
+            ZERO_TRY(heads_map(&t.dout, h.dout, a->q_tokens, a->q_heads, a->head_dim, q_rows, a->dtype));
+        }
+        if (a->k_tokens > 0) {
+            ZERO_TRY(heads_map(&t.k, h.k, a->k_tokens, a->k_heads, a->head_dim, k_rows, a->dtype));
+            ZERO_TRY(heads_map(&t.v, h.v, a->k_tokens, a->k_heads, a->head_dim, k_rows, a->dtype));
+        }
+        if (a->k_tokens == 0)  // (maps that nothing is loaded by, but that kernels name)
+            t.k = t.v = t.q;
+        if (a->q_tokens == 0)
+            t.q = t.dout = t.k;
+        return ZERO_OK;
+    };
+    ZERO_TRY(maps(S::BN, 128));
+    launch(k_attn_dkv<DT, S>, t.split_units + t.k_tiles * t.a.k_heads);
     if (e == cudaSuccess && t.split_units > 0) {
         what = "k_attn_join";
         const int64_t blocks = (int64_t)t.a.sequences * t.sink_tiles * t.a.k_heads * 16;
@@ -2164,7 +2242,9 @@ int launch_backward(const BwdTiles &t, cudaStream_t st)
     }
     if (e == cudaSuccess) {
         what = "k_attn_dq";
-        launch(k_attn_dq<DT, DP>, t.q_tiles * t.a.q_heads);
+        if (S::BN != 128)
+            ZERO_TRY(maps(128, S::BN));
+        launch(k_attn_dq<DT, S>, t.q_tiles * t.a.q_heads);
     }
     if (e != cudaSuccess) {
         cudaGetLastError();
@@ -2242,18 +2322,6 @@ extern "C" int zero_window_attention_backward(const zero_attention_t *a, const v
     t.hdr = static_cast<WsHeader *>(ws);
     t.limit_ns = kWaitLimit;
     if (a->q_tokens > 0) {
-        ZERO_TRY(heads_map(&t.q, hq, a->q_tokens, a->q_heads, a->head_dim, a->dtype));
-        ZERO_TRY(heads_map(&t.dout, hdout, a->q_tokens, a->q_heads, a->head_dim, a->dtype));
-    }
-    if (a->k_tokens > 0) {
-        ZERO_TRY(heads_map(&t.k, hk, a->k_tokens, a->k_heads, a->head_dim, a->dtype));
-        ZERO_TRY(heads_map(&t.v, hv, a->k_tokens, a->k_heads, a->head_dim, a->dtype));
-    }
-    if (a->k_tokens == 0)  // (maps that nothing is loaded by, but that kernels name)
-        t.k = t.v = t.q;
-    if (a->q_tokens == 0)
-        t.q = t.dout = t.k;
-    if (a->q_tokens > 0) {
         const SinkPlan p = plan_sinks(a, one);
         t.chunk = p.chunk, t.sink_tiles = p.sink_tiles, t.chunks = p.chunks, t.split_units = p.units;
         const StatsArgs s{t.a, hdout, hout, lse, const_cast<float *>(t.stats), t.q_tiles};
@@ -2262,7 +2330,8 @@ extern "C" int zero_window_attention_backward(const zero_attention_t *a, const v
         kernel<<<grid_for(reinterpret_cast<const void *>(kernel), blocks, 1 << 30), kThreads, 0, st>>>(s);
         ZERO_TRY(check_launch("k_attn_stats"));
     }
+    const BwdArrays h{hdout, hq, hk, hv};
     if (a->head_dim <= 64)
-        return a->dtype == ZERO_F16 ? launch_backward<ZERO_F16, 64>(t, st) : launch_backward<ZERO_BF16, 64>(t, st);
-    return a->dtype == ZERO_F16 ? launch_backward<ZERO_F16, 128>(t, st) : launch_backward<ZERO_BF16, 128>(t, st);
+        return a->dtype == ZERO_F16 ? launch_backward<ZERO_F16, NarrowBwd>(t, h, a, st) : launch_backward<ZERO_BF16, NarrowBwd>(t, h, a, st);
+    return a->dtype == ZERO_F16 ? launch_backward<ZERO_F16, WideBwd>(t, h, a, st) : launch_backward<ZERO_BF16, WideBwd>(t, h, a, st);
 }

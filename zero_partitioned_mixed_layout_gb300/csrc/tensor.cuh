@@ -227,6 +227,20 @@ __device__ __forceinline__ void tmem_free(uint32_t addr, uint32_t columns)
             : "memory");
 }
 
+// The same for CTAs that share an SM: one that has what it wants gives up the
+// right to allocate at once (until then every other CTA's allocation on the SM
+// waits, whatever is free), and only the memory itself at the end.
+__device__ __forceinline__ void tmem_take(uint32_t *where, uint32_t columns)
+{
+    tmem_alloc<1>(where, columns);
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+}
+
+__device__ __forceinline__ void tmem_give(uint32_t addr, uint32_t columns)
+{
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(columns) : "memory");
+}
+
 __device__ __forceinline__ void tmem_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tmem_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 
