@@ -116,6 +116,8 @@ __device__ __forceinline__ float exp2_fast(float x)
     return y;
 }
 
+__device__ __forceinline__ F2 exp2_fast(F2 x) { return {exp2_fast(x.x), exp2_fast(x.y)}; }
+
 template <int DT>
 __device__ __forceinline__ uint32_t pack2(float lo, float hi)
 {
@@ -228,20 +230,21 @@ __device__ __forceinline__ void inner_products(uint32_t d, uint64_t a, uint64_t 
         tensor_products4<2, 2>(d, a + (A_ROWS * 128 >> 4), b + (B_ROWS * 128 >> 4), desc, true, steps - 4);
 }
 
-// D (+)= A B over ROWS rows of B, A in tensor memory, 64 elements each from a
-// and from a + 64 on.
-template <int ROWS>
-__device__ __forceinline__ void outer_products(uint32_t d, uint32_t a, uint64_t b, uint32_t desc, bool add)
+// Where a thread's 32 columns of piece c (0, 1) of BN start: a group of four
+// warps takes 64 of 128 columns, in two pieces that it shares with the other
+// group, so that the products over the first 64 can start when half of the
+// work is done; of 64 columns there is one group.  What a thread writes, two
+// elements to a column, starts where it read.
+template <int BN>
+__device__ __forceinline__ int piece_at(int group, int c)
 {
-    tensor_products4_tmem<128>(d, a, b, desc, add);
-    if (ROWS == 128)
-        tensor_products4_tmem<128>(d, a + 64, b + 512, desc, true);
+    return BN == 128 ? 64 * c + 32 * group : 32 * c;
 }
 
-// QT tiles of 128 queries against tiles of BN keys.
-template <int DP_, int QT_, int BN_, int PER_SM_>
+// QT tiles of 128 queries against tiles of 128 keys.
+template <int DP_, int QT_, int PER_SM_>
 struct FwdShape {
-    static constexpr int DP = DP_, QT = QT_, BN = BN_, PER_SM = PER_SM_;
+    static constexpr int DP = DP_, QT = QT_, BN = 128, PER_SM = PER_SM_;
     static constexpr int BOXES = DP / 64, Q_TILE = BOXES * 16384, K_TILE = BOXES * BN * 128;  // bytes
     static constexpr int STAGES = 2;
     static constexpr int ROW_WARPS = 4 * QT, THREADS = (ROW_WARPS + 2) * 32;
@@ -251,7 +254,7 @@ struct FwdShape {
 };
 
 struct FwdShared {
-    uint64_t q_full[2], q_empty[2], k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2][2], o_full[2];
+    uint64_t q_full[2], q_empty[2], k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2][2], half_done[2], o_full[2];
     uint64_t unit_full[kUnitRing], unit_empty[kUnitRing];
     Unit units[kUnitRing];
     uint32_t tmem, gave_up;
@@ -288,7 +291,7 @@ __device__ __forceinline__ void store_rows(uint4 *stage, int lane, const uint32_
 template <int DT, class S>
 __global__ void __launch_bounds__(S::THREADS, S::PER_SM) k_attn_tiles(const __grid_constant__ FwdTiles f)
 {
-    constexpr int DP = S::DP, QT = S::QT, BN = S::BN, HALVES = BN / 64;
+    constexpr int DP = S::DP, QT = S::QT, BN = S::BN;
     extern __shared__ unsigned char smem_raw[];
     __shared__ FwdShared sh;
     unsigned char *smem = smem_raw + ((1024 - (smem_addr(smem_raw) & 1023u)) & 1023u);
@@ -306,6 +309,7 @@ __global__ void __launch_bounds__(S::THREADS, S::PER_SM) k_attn_tiles(const __gr
             mbar_init_count(&sh.s_full[t], 1);
             mbar_init_count(&sh.p_full[t][0], 4);
             mbar_init_count(&sh.p_full[t][1], 4);
+            mbar_init_count(&sh.half_done[t], 1);
             mbar_init_count(&sh.o_full[t], 1);
         }
         for (int s = 0; s < S::STAGES; ++s) {
@@ -446,13 +450,15 @@ __global__ void __launch_bounds__(S::THREADS, S::PER_SM) k_attn_tiles(const __gr
                         // the later keys' weights come first
                         const uint64_t dv = v0 + ((vs * S::K_TILE) >> 4);
 #pragma unroll
-                        for (int h = HALVES - 1; h >= 0; --h) {
+                        for (int h = 1; h >= 0; --h) {
                             ok = ok && wait(&sh.p_full[t][h], pn[t] & 1);
                             if (!ok)
                                 break;
                             tmem_fence_after();
-                            tensor_products4_tmem<128>(tmem + kSums + t * DP, tmem + t * kScores + BN / 2 + h * 32, dv + h * 512,
-                                                       desc_o, !first[t] || h != HALVES - 1);
+                            tensor_products4_tmem<128, 16>(tmem + kSums + t * DP, tmem + t * kScores + h * 64, dv + h * 512, desc_o,
+                                                           !first[t] || h == 0);
+                            if (h)
+                                tensor_commit_elected(&sh.half_done[t]);
                         }
                         ++pn[t];
                         if (!ok)
@@ -520,125 +526,100 @@ __global__ void __launch_bounds__(S::THREADS, S::PER_SM) k_attn_tiles(const __gr
                 const int32_t k_first = kt * BN;
                 const bool whole = k_first + BN - 1 <= p_first &&
                                    (k_first > p_last - a.window || k_first + BN - 1 < a.sinks);
-                // Pieces of 32 scores: once for the largest, the last two of
-                // four (the last of two) then stay in registers, and the others
-                // come again.
-                uint32_t r0[32], r1[32], r2[32];
-                auto hide = [&](uint32_t (&r)[32], int c) {
-                    if (!whole) {
-                        const uint32_t bits = seen_bits(p, a.window, a.sinks, k_first + 32 * c);
+                // 64 keys at a time, the later ones first: their largest score,
+                // their weights, which go where their scores were, and on to
+                // the products while the others are worked on.
 #pragma unroll
-                        for (int e = 0; e < 32; ++e)
-                            r[e] = bits & (1u << e) ? r[e] : 0xff800000u;
-                    }
-                };
-                float tops[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-                auto largest = [&](uint32_t (&r)[32], int c) {
-                    hide(r, c);
-#pragma unroll
-                    for (int e = 0; e < 32; e += 8)
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            tops[i] = fmaxf(fmaxf(tops[i], __uint_as_float(r[e + i])), __uint_as_float(r[e + 4 + i]));
-                };
-                tmem_load32(at_s, r0);
-                tmem_wait_loads(r0);
-                tmem_load32(at_s + 32, r1);
-                largest(r0, 0);
-                tmem_wait_loads(r1);
-                if constexpr (HALVES == 2) {
-                    tmem_load32(at_s + 64, r0);
-                    largest(r1, 1);
+                for (int h = 1; h >= 0; --h) {
+                    uint32_t r0[32], r1[32];
+                    tmem_load32(at_s + 64 * h, r0);
+                    tmem_load32(at_s + 64 * h + 32, r1);
                     tmem_wait_loads(r0);
-                    tmem_load32(at_s + 96, r1);
-                    largest(r0, 2);
                     tmem_wait_loads(r1);
-                    tmem_load32(at_s + 32, r2);
-                }
-                largest(r1, BN / 32 - 1);
-                const float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
-                // The weights' reference is the largest score so far, or up to
-                // 2^8 below it: the weights stay below 2^8, and sums are
-                // rarely multiplied anew.
-                const bool far = top > m && (m == -INFINITY || (top - m) * sl > 8.0f);
-                if (__any_sync(0xffffffffu, far)) {
-                    const float to = far ? top : m;
-                    const float keep = m == -INFINITY ? 0.0f : exp2_fast((m - to) * sl);
-                    if (__any_sync(0xffffffffu, l != 0.0f)) {
-                        for (int c = 0; c < a.dim; c += 32) {
-                            uint32_t o[32];
-                            tmem_load32(at_o + c, o);
-                            tmem_wait_loads(o);
-                            uint32_t lo[16], hi[16];
+                    if (!whole) {
+                        const uint32_t b0 = seen_bits(p, a.window, a.sinks, k_first + 64 * h);
+                        const uint32_t b1 = seen_bits(p, a.window, a.sinks, k_first + 64 * h + 32);
 #pragma unroll
-                            for (int e = 0; e < 16; ++e) {
-                                lo[e] = __float_as_uint(__uint_as_float(o[e]) * keep);
-                                hi[e] = __float_as_uint(__uint_as_float(o[16 + e]) * keep);
-                            }
-                            tmem_store16(at_o + c, lo);
-                            tmem_store16(at_o + c + 16, hi);
+                        for (int e = 0; e < 32; ++e) {
+                            r0[e] = b0 & (1u << e) ? r0[e] : 0xff800000u;
+                            r1[e] = b1 & (1u << e) ? r1[e] : 0xff800000u;
                         }
                     }
-                    l *= keep;
-                    m = to;
-                }
-                const F2 scale2 = twice(sl), base2 = twice(m == -INFINITY ? 0.0f : -m * sl);
-                F2 sums[2] = {{0.0f, 0.0f}, {0.0f, 0.0f}};
-                // The weights go where scores were that are no longer needed:
-                // those of piece c into the 16 columns from BN / 2 + 16 c on.
-                auto weigh = [&](const uint32_t (&r)[32], int c) {
-                    uint32_t w[16];
+                    float tops[8];
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) {
-                        F2 x = fma2({__uint_as_float(r[2 * e]), __uint_as_float(r[2 * e + 1])}, scale2, base2);
-                        x = {exp2_fast(x.x), exp2_fast(x.y)};
-                        sums[e & 1] = sums[e & 1] + x;
-                        w[e] = pack2<DT>(x.x, x.y);
+                    for (int e = 0; e < 8; ++e)
+                        tops[e] = fmaxf(__uint_as_float(r0[e]), __uint_as_float(r1[e]));
+#pragma unroll
+                    for (int e = 8; e < 32; ++e)
+                        tops[e & 7] = fmaxf(tops[e & 7], fmaxf(__uint_as_float(r0[e]), __uint_as_float(r1[e])));
+                    const float top = fmaxf(fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3])),
+                                            fmaxf(fmaxf(tops[4], tops[5]), fmaxf(tops[6], tops[7])));
+                    // The weights' reference is the largest score so far, or up
+                    // to 2^8 below it: the weights stay below 2^8, and sums are
+                    // rarely multiplied anew.
+                    const bool far = top > m && (m == -INFINITY || (top - m) * sl > 8.0f);
+                    if (__any_sync(0xffffffffu, far)) {
+                        const float to = far ? top : m;
+                        const float keep = m == -INFINITY ? 0.0f : exp2_fast((m - to) * sl);
+                        if (__any_sync(0xffffffffu, l != 0.0f)) {
+                            // (what the products before this tile added is there; of
+                            // this tile's other half, when they say so)
+                            if (h == 0) {
+                                ok = wait(&sh.half_done[t], (sn - 1) & 1);
+                                if (!ok)
+                                    break;
+                                tmem_fence_after();
+                            }
+                            for (int c = 0; c < a.dim; c += 16) {
+                                uint32_t o[16];
+                                tmem_load16(at_o + c, o);
+                                tmem_wait_loads16(o);
+#pragma unroll
+                                for (int e = 0; e < 16; ++e)
+                                    o[e] = __float_as_uint(__uint_as_float(o[e]) * keep);
+                                tmem_store16(at_o + c, o);
+                            }
+                        }
+                        l *= keep;
+                        m = to;
                     }
-                    tmem_store16(at_s + BN / 2 + 16 * c, w);
-                };
-                auto ready = [&](int h) {
+                    const F2 scale2 = twice(sl), base2 = twice(m == -INFINITY ? 0.0f : -m * sl);
+                    F2 sums[4] = {};
+                    auto weigh = [&](const uint32_t (&r)[32], int c) {
+                        uint32_t w[16];
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) {
+                            const F2 x = exp2_fast(fma2({__uint_as_float(r[2 * e]), __uint_as_float(r[2 * e + 1])}, scale2, base2));
+                            sums[e & 3] = sums[e & 3] + x;
+                            w[e] = pack2<DT>(x.x, x.y);
+                        }
+                        tmem_store16(at_s + 64 * h + 16 * c, w);
+                    };
+                    weigh(r0, 0);
+                    weigh(r1, 1);
+                    if (k_first + BN > u.lk) {
+                        // rows behind the last key: zeros, since 0 times what they hold may not be 0
+                        const uint32_t now = vn + n, vs = now % S::STAGES;
+                        ok = wait(&sh.v_full[vs], (now / S::STAGES) & 1);
+                        if (!ok)
+                            break;
+                        const int32_t from = u.lk - k_first > 64 * h ? u.lk - k_first : 64 * h;
+                        for (int i = from * 8 + (threadIdx.x & 127); i < (h + 1) * 512; i += 128)
+#pragma unroll
+                            for (int b = 0; b < S::BOXES; ++b)
+                                *reinterpret_cast<uint4 *>(s_v + vs * S::K_TILE + b * BN * 128 + i * 16) = make_uint4(0, 0, 0, 0);
+                        fence_proxy_async();
+                    }
+                    const F2 sum = (sums[0] + sums[1]) + (sums[2] + sums[3]);
+                    l += sum.x + sum.y;
                     tmem_wait_stores();
                     tmem_fence_before();
                     __syncwarp();
                     if (lane == 0)
                         mbar_arrive_cluster(smem_addr(&sh.p_full[t][h]));
-                };
-                if constexpr (HALVES == 1)
-                    tmem_load32(at_s, r2);
-                weigh(r1, BN / 32 - 1);
-                if constexpr (HALVES == 2)
-                    weigh(r0, 2);
-                if (k_first + BN > u.lk) {
-                    // rows behind the last key: zeros, since 0 times what they hold may not be 0
-                    const uint32_t now = vn + n, vs = now % S::STAGES;
-                    ok = wait(&sh.v_full[vs], (now / S::STAGES) & 1);
-                    if (!ok)
-                        break;
-                    const int32_t from = u.lk - k_first;
-                    const int id = threadIdx.x & 127;
-                    for (int i = from * 8 + id; i < BN * 8; i += 128)
-#pragma unroll
-                        for (int b = 0; b < S::BOXES; ++b)
-                            *reinterpret_cast<uint4 *>(s_v + vs * S::K_TILE + b * BN * 128 + i * 16) = make_uint4(0, 0, 0, 0);
-                    fence_proxy_async();
                 }
-                if constexpr (HALVES == 2) {
-                    tmem_wait_loads(r2);
-                    ready(1);
-                    tmem_load32(at_s, r0);
-                    hide(r2, 1);
-                    weigh(r2, 1);
-                    tmem_wait_loads(r0);
-                    hide(r0, 0);
-                    weigh(r0, 0);
-                } else {
-                    tmem_wait_loads(r2);
-                    hide(r2, 0);
-                    weigh(r2, 0);
-                }
-                ready(0);
-                l += (sums[0].x + sums[0].y) + (sums[1].x + sums[1].y);
+                if (!ok)
+                    break;
             }
             vn += list.n;
             if (!ok)
@@ -1136,7 +1117,7 @@ struct BwdShape {
 };
 
 struct KeyShared {
-    uint64_t kv_full, kv_empty, q_full[2], q_empty[2], o_full[2], o_empty[2], s_full, dp_full, p_full, ds_full, acc_full;
+    uint64_t kv_full, kv_empty, q_full[2], q_empty[2], o_full[2], o_empty[2], s_full, dp_full, p_full[2], ds_full[2], acc_full;
     uint64_t unit_full[kUnitRing], unit_empty[kUnitRing];
     KeyUnit units[kUnitRing];
     uint32_t tmem, gave_up;
@@ -1218,8 +1199,10 @@ __global__ void __launch_bounds__(S::THREADS, S::PER_SM) k_attn_dkv(const __grid
         }
         mbar_init_count(&sh.s_full, 1);
         mbar_init_count(&sh.dp_full, 1);
-        mbar_init_count(&sh.p_full, S::ROW_WARPS);
-        mbar_init_count(&sh.ds_full, S::ROW_WARPS);
+        for (int c = 0; c < BN / 64; ++c) {
+            mbar_init_count(&sh.p_full[c], S::ROW_WARPS);
+            mbar_init_count(&sh.ds_full[c], S::ROW_WARPS);
+        }
         mbar_init_count(&sh.acc_full, 1);
         for (int s = 0; s < kUnitRing; ++s) {
             mbar_init_count(&sh.unit_full[s], 1);
@@ -1352,11 +1335,17 @@ __global__ void __launch_bounds__(S::THREADS, S::PER_SM) k_attn_dkv(const __grid
                 tmem_fence_after();
                 inner_products<DP, 128, BN>(tmem + kDp, dv0, do0 + ((st * S::MOVING) >> 4), desc_s, steps);
                 tensor_commit_elected(&sh.dp_full);
-                ok = wait(&sh.p_full, n & 1);
+#pragma unroll
+                for (int c = 0; c < BN / 64; ++c) {
+                    ok = ok && wait(&sh.p_full[c], n & 1);
+                    if (!ok)
+                        break;
+                    tmem_fence_after();
+                    tensor_products4_tmem<128, 32>(tmem + kDv, tmem + 64 * c, to0 + ((st * S::MOVING) >> 4) + 512 * c, desc_acc,
+                                                   i != 0 || c != 0);
+                }
                 if (!ok)
                     break;
-                tmem_fence_after();
-                outer_products<BN>(tmem + kDv, tmem, to0 + ((st * S::MOVING) >> 4), desc_acc, i != 0);
                 tensor_commit_elected(&sh.o_empty[st]);
                 if (i + 1 < count) {
                     const uint32_t to = (qn + 1) & 1;
@@ -1367,11 +1356,17 @@ __global__ void __launch_bounds__(S::THREADS, S::PER_SM) k_attn_dkv(const __grid
                     inner_products<DP, 128, BN>(tmem, dk0, dq0 + ((to * S::MOVING) >> 4), desc_s, steps);
                     tensor_commit_elected(&sh.s_full);
                 }
-                ok = wait(&sh.ds_full, n & 1);
+#pragma unroll
+                for (int c = 0; c < BN / 64; ++c) {
+                    ok = ok && wait(&sh.ds_full[c], n & 1);
+                    if (!ok)
+                        break;
+                    tmem_fence_after();
+                    tensor_products4_tmem<128, 32>(tmem + kDk, tmem + kDp + 64 * c, tq0 + ((st * S::MOVING) >> 4) + 512 * c,
+                                                   desc_acc, i != 0 || c != 0);
+                }
                 if (!ok)
                     break;
-                tmem_fence_after();
-                outer_products<BN>(tmem + kDk, tmem + kDp, tq0 + ((st * S::MOVING) >> 4), desc_acc, i != 0);
                 tensor_commit_elected(&sh.q_empty[st]);
                 if (i + 1 == count) {
                     tensor_commit_elected(&sh.kv_empty);
@@ -1382,7 +1377,7 @@ __global__ void __launch_bounds__(S::THREADS, S::PER_SM) k_attn_dkv(const __grid
     } else {
         const int half = warp >> 2, quarter = warp & 3;
         const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
-        const uint32_t at_s = tmem + lanes + half * 64, at_p = at_s + kDp;
+        const uint32_t at_s = tmem + lanes, at_p = at_s + kDp;
         uint4 *const stage = reinterpret_cast<uint4 *>(s_out + warp * 2048);
         uint32_t qn = 0, n = 0, accs = 0;
         bool ok = true;
@@ -1400,44 +1395,7 @@ __global__ void __launch_bounds__(S::THREADS, S::PER_SM) k_attn_dkv(const __grid
                 if (!ok)
                     break;
                 tmem_fence_after();
-                const float *lse2 = s_stats + st * 2 * BN + half * 64, *delta = lse2 + BN;
-                float p[64];
-#pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    uint32_t r[32];
-                    tmem_load32(at_s + 32 * c, r);
-                    tmem_wait_loads(r);
-#pragma unroll
-                    for (int e = 0; e < 32; e += 4) {
-                        const float4 x = *reinterpret_cast<const float4 *>(lse2 + 32 * c + e);
-                        p[32 * c + e] = exp2_fast(__uint_as_float(r[e]) * f.scale_log2 - x.x);
-                        p[32 * c + e + 1] = exp2_fast(__uint_as_float(r[e + 1]) * f.scale_log2 - x.y);
-                        p[32 * c + e + 2] = exp2_fast(__uint_as_float(r[e + 2]) * f.scale_log2 - x.z);
-                        p[32 * c + e + 3] = exp2_fast(__uint_as_float(r[e + 3]) * f.scale_log2 - x.w);
-                    }
-                }
-                uint32_t bits[2] = {~0u, ~0u};
-                if (!whole) {
-#pragma unroll
-                    for (int c = 0; c < 2; ++c) {
-                        const int32_t from = half * 64 + 32 * c;
-                        bits[c] = ~bits_up_to(j - p0 - 1 - from) & bits_up_to(nq - 1 - from);
-                        if (j >= a.sinks)
-                            bits[c] &= bits_up_to(j - p0 + a.window - 1 - from);
-#pragma unroll
-                        for (int e = 0; e < 32; ++e)
-                            p[32 * c + e] = bits[c] & (1u << e) ? p[32 * c + e] : 0.0f;
-                    }
-                }
-                // (every lane has read its scores: stores follow loads in a warp, and a half keeps to its own columns)
-#pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    uint32_t w[16];
-#pragma unroll
-                    for (int e = 0; e < 16; ++e)
-                        w[e] = pack2<DT>(p[32 * c + 2 * e], p[32 * c + 2 * e + 1]);
-                    tmem_store16(at_s + 16 * c, w);
-                }
+                const float *lse2 = s_stats + st * 2 * BN, *delta = lse2 + BN;
                 if (nq < BN) {
                     // rows behind the last query: zeros, since 0 times what they hold may not be 0
                     ok = wait(&sh.o_full[st], (qn >> 1) & 1);
@@ -1451,43 +1409,79 @@ __global__ void __launch_bounds__(S::THREADS, S::PER_SM) k_attn_dkv(const __grid
                         }
                     fence_proxy_async();
                 }
-                tmem_wait_stores();
-                tmem_fence_before();
-                __syncwarp();
-                if (lane == 0)
-                    mbar_arrive_cluster(smem_addr(&sh.p_full));
+                F2 p[2][16];
+                uint32_t bits[2] = {~0u, ~0u};
+                const F2 scale2 = twice(f.scale_log2);
+                // piece c is done (of 64 columns, both are when the second is)
+                auto ready = [&](uint64_t *bar, int c) {
+                    if (BN == 64 && c == 0)
+                        return;
+                    tmem_wait_stores();
+                    tmem_fence_before();
+                    __syncwarp();
+                    if (lane == 0)
+                        mbar_arrive_cluster(smem_addr(BN == 64 ? bar : bar + c));
+                };
+                auto weigh = [&](int c) {
+                    const int at = piece_at<BN>(half, c);
+                    uint32_t r[32], w[16];
+                    tmem_load32(at_s + at, r);
+                    tmem_wait_loads(r);
+#pragma unroll
+                    for (int e = 0; e < 16; e += 2) {
+                        const float4 x = *reinterpret_cast<const float4 *>(lse2 + at + 2 * e);
+                        p[c][e] = exp2_fast(
+                            fma2({__uint_as_float(r[2 * e]), __uint_as_float(r[2 * e + 1])}, scale2, {-x.x, -x.y}));
+                        p[c][e + 1] = exp2_fast(
+                            fma2({__uint_as_float(r[2 * e + 2]), __uint_as_float(r[2 * e + 3])}, scale2, {-x.z, -x.w}));
+                    }
+                    if (!whole) {
+                        bits[c] = ~bits_up_to(j - p0 - 1 - at) & bits_up_to(nq - 1 - at);
+                        if (j >= a.sinks)
+                            bits[c] &= bits_up_to(j - p0 + a.window - 1 - at);
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) {
+                            p[c][e].x = bits[c] & (1u << 2 * e) ? p[c][e].x : 0.0f;
+                            p[c][e].y = bits[c] & (2u << 2 * e) ? p[c][e].y : 0.0f;
+                        }
+                    }
+#pragma unroll
+                    for (int e = 0; e < 16; ++e)
+                        w[e] = pack2<DT>(p[c][e].x, p[c][e].y);
+                    tmem_store16(at_s + at, w);
+                    ready(sh.p_full, c);
+                };
+                weigh(0);
+                weigh(1);
                 ok = wait(&sh.dp_full, n & 1);
                 if (!ok)
                     break;
                 tmem_fence_after();
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
+                    const int at = piece_at<BN>(half, c);
                     uint32_t r[32], w[16];
-                    tmem_load32(at_p + 32 * c, r);
+                    tmem_load32(at_p + at, r);
                     tmem_wait_loads(r);
 #pragma unroll
-                    for (int e = 0; e < 32; e += 4) {
-                        const float4 x = *reinterpret_cast<const float4 *>(delta + 32 * c + e);
-                        p[32 * c + e] *= __uint_as_float(r[e]) - x.x;
-                        p[32 * c + e + 1] *= __uint_as_float(r[e + 1]) - x.y;
-                        p[32 * c + e + 2] *= __uint_as_float(r[e + 2]) - x.z;
-                        p[32 * c + e + 3] *= __uint_as_float(r[e + 3]) - x.w;
+                    for (int e = 0; e < 16; e += 2) {
+                        const float4 x = *reinterpret_cast<const float4 *>(delta + at + 2 * e);
+                        p[c][e] = p[c][e] * (F2{__uint_as_float(r[2 * e]), __uint_as_float(r[2 * e + 1])} + F2{-x.x, -x.y});
+                        p[c][e + 1] = p[c][e + 1] * (F2{__uint_as_float(r[2 * e + 2]), __uint_as_float(r[2 * e + 3])} + F2{-x.z, -x.w});
                     }
                     if (!whole) {
 #pragma unroll
-                        for (int e = 0; e < 32; ++e)
-                            p[32 * c + e] = bits[c] & (1u << e) ? p[32 * c + e] : 0.0f;
+                        for (int e = 0; e < 16; ++e) {
+                            p[c][e].x = bits[c] & (1u << 2 * e) ? p[c][e].x : 0.0f;
+                            p[c][e].y = bits[c] & (2u << 2 * e) ? p[c][e].y : 0.0f;
+                        }
                     }
 #pragma unroll
                     for (int e = 0; e < 16; ++e)
-                        w[e] = pack2<DT>(p[32 * c + 2 * e], p[32 * c + 2 * e + 1]);
-                    tmem_store16(at_p + 16 * c, w);
+                        w[e] = pack2<DT>(p[c][e].x, p[c][e].y);
+                    tmem_store16(at_p + at, w);
+                    ready(sh.ds_full, c);
                 }
-                tmem_wait_stores();
-                tmem_fence_before();
-                __syncwarp();
-                if (lane == 0)
-                    mbar_arrive_cluster(smem_addr(&sh.ds_full));
                 t = t == u.high ? u.low : t + 1;
             }
             if (ok && count > 0) {
@@ -1613,7 +1607,7 @@ struct QueryUnit {
 };
 
 struct QueryShared {
-    uint64_t q_full, q_empty, k_full[2], k_empty[2], v_full[2], v_empty[2], sp_full, ds_full, acc_full;
+    uint64_t q_full, q_empty, k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], dp_full, ds_full[2], acc_full;
     uint64_t unit_full[kUnitRing], unit_empty[kUnitRing];
     QueryUnit units[kUnitRing];
     uint32_t tmem, gave_up;
@@ -1645,9 +1639,11 @@ __global__ void __launch_bounds__(S::THREADS, S::PER_SM) k_attn_dq(const __grid_
             mbar_init_count(&sh.k_empty[s], 1);
             mbar_init_count(&sh.v_full[s], 1);
             mbar_init_count(&sh.v_empty[s], 1);
+            mbar_init_count(&sh.s_full[s], 1);
         }
-        mbar_init_count(&sh.sp_full, 1);
-        mbar_init_count(&sh.ds_full, S::ROW_WARPS);
+        mbar_init_count(&sh.dp_full, 1);
+        for (int c = 0; c < BN / 64; ++c)
+            mbar_init_count(&sh.ds_full[c], S::ROW_WARPS);
         mbar_init_count(&sh.acc_full, 1);
         for (int s = 0; s < kUnitRing; ++s) {
             mbar_init_count(&sh.unit_full[s], 1);
@@ -1781,6 +1777,7 @@ __global__ void __launch_bounds__(S::THREADS, S::PER_SM) k_attn_dq(const __grid_
                     return;
                 tmem_fence_after();
                 inner_products<DP, 128, BN>(tmem + st * BN, dq0, dk0 + ((st * S::MOVING) >> 4), desc_s, steps);
+                tensor_commit_elected(&sh.s_full[st]);
             };
             auto grads = [&](uint32_t at) {
                 const uint32_t st = at & 1;
@@ -1789,7 +1786,7 @@ __global__ void __launch_bounds__(S::THREADS, S::PER_SM) k_attn_dq(const __grid_
                     return;
                 tmem_fence_after();
                 inner_products<DP, 128, BN>(tmem + kDp, do0, dv0 + ((st * S::MOVING) >> 4), desc_s, steps);
-                tensor_commit_elected(&sh.sp_full);
+                tensor_commit_elected(&sh.dp_full);
                 tensor_commit_elected(&sh.v_empty[st]);
             };
             scores(kn);
@@ -1798,15 +1795,21 @@ __global__ void __launch_bounds__(S::THREADS, S::PER_SM) k_attn_dq(const __grid_
                 const uint32_t st = kn & 1;
                 if (n + 1 < list.n)
                     scores(kn + 1);
-                ok = ok && wait(&sh.ds_full, dsn & 1);
+#pragma unroll
+                for (int c = 0; c < BN / 64; ++c) {
+                    ok = ok && wait(&sh.ds_full[c], dsn & 1);
+                    if (!ok)
+                        break;
+                    tmem_fence_after();
+                    if (c == BN / 64 - 1 && n + 1 < list.n)  // all of dP is read
+                        grads(kn + 1);
+                    if (!ok)
+                        break;
+                    tensor_products4_tmem<128, 32>(tmem + kDq, tmem + st * BN + 64 * c, tk0 + ((st * S::MOVING) >> 4) + 512 * c,
+                                                   desc_acc, n != 0 || c != 0);
+                }
                 if (!ok)
                     break;
-                tmem_fence_after();
-                if (n + 1 < list.n)
-                    grads(kn + 1);
-                if (!ok)
-                    break;
-                outer_products<BN>(tmem + kDq, tmem + st * BN, tk0 + ((st * S::MOVING) >> 4), desc_acc, n != 0);
                 tensor_commit_elected(&sh.k_empty[st]);
                 if (n + 1 == list.n) {
                     tensor_commit_elected(&sh.q_empty);
@@ -1834,32 +1837,22 @@ __global__ void __launch_bounds__(S::THREADS, S::PER_SM) k_attn_dq(const __grid_
                 const int32_t k_first = list.at(n) * BN;
                 const bool whole = k_first + BN - 1 <= p_first &&
                                    (k_first > p_last - a.window || k_first + BN - 1 < a.sinks);
-                ok = wait(&sh.sp_full, kn & 1);
+                ok = wait(&sh.s_full[st], (kn >> 1) & 1);
                 if (!ok)
                     break;
                 tmem_fence_after();
-                const uint32_t at_s = tmem + lanes + st * BN + half * 64, at_p = tmem + lanes + kDp + half * 64;
+                const uint32_t at_s = tmem + lanes + st * BN, at_p = tmem + lanes + kDp;
+                F2 w2[2][16];
+                const F2 scale2 = twice(f.scale_log2), base2 = twice(-lse2), delta2 = twice(-delta);
+                // the weights, while dP is worked out
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
-                    uint32_t r[32], g[32], w[16];
-                    tmem_load32(at_s + 32 * c, r);
-                    tmem_load32(at_p + 32 * c, g);
+                    uint32_t r[32];
+                    tmem_load32(at_s + piece_at<BN>(half, c), r);
                     tmem_wait_loads(r);
-                    tmem_wait_loads(g);
-                    uint32_t bits = ~0u;
-                    if (!whole)
-                        bits = seen_bits(p, a.window, a.sinks, k_first + half * 64 + 32 * c);
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) {
-                        float x = exp2_fast(__uint_as_float(r[e]) * f.scale_log2 - lse2) * (__uint_as_float(g[e]) - delta);
-                        if (!whole)
-                            x = bits & (1u << e) ? x : 0.0f;
-                        r[e] = __float_as_uint(x);
-                    }
 #pragma unroll
                     for (int e = 0; e < 16; ++e)
-                        w[e] = pack2<DT>(__uint_as_float(r[2 * e]), __uint_as_float(r[2 * e + 1]));
-                    tmem_store16(at_s + 16 * c, w);
+                        w2[c][e] = exp2_fast(fma2({__uint_as_float(r[2 * e]), __uint_as_float(r[2 * e + 1])}, scale2, base2));
                 }
                 if (k_first + BN > u.lk) {
                     // rows behind the last key: zeros, since 0 times what they hold may not be 0
@@ -1869,11 +1862,39 @@ __global__ void __launch_bounds__(S::THREADS, S::PER_SM) k_attn_dq(const __grid_
                             *reinterpret_cast<uint4 *>(s_k + st * S::MOVING + b * BN * 128 + k * 16) = make_uint4(0, 0, 0, 0);
                     fence_proxy_async();
                 }
-                tmem_wait_stores();
-                tmem_fence_before();
-                __syncwarp();
-                if (lane == 0)
-                    mbar_arrive_cluster(smem_addr(&sh.ds_full));
+                ok = wait(&sh.dp_full, kn & 1);
+                if (!ok)
+                    break;
+                tmem_fence_after();
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    const int at = piece_at<BN>(half, c);
+                    uint32_t r[32], w[16];
+                    tmem_load32(at_p + at, r);
+                    tmem_wait_loads(r);
+#pragma unroll
+                    for (int e = 0; e < 16; ++e)
+                        w2[c][e] = w2[c][e] * (F2{__uint_as_float(r[2 * e]), __uint_as_float(r[2 * e + 1])} + delta2);
+                    if (!whole) {
+                        const uint32_t bits = seen_bits(p, a.window, a.sinks, k_first + at);
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) {
+                            w2[c][e].x = bits & (1u << 2 * e) ? w2[c][e].x : 0.0f;
+                            w2[c][e].y = bits & (2u << 2 * e) ? w2[c][e].y : 0.0f;
+                        }
+                    }
+#pragma unroll
+                    for (int e = 0; e < 16; ++e)
+                        w[e] = pack2<DT>(w2[c][e].x, w2[c][e].y);
+                    tmem_store16(at_s + at, w);
+                    if (BN == 128 || c == 1) {
+                        tmem_wait_stores();
+                        tmem_fence_before();
+                        __syncwarp();
+                        if (lane == 0)
+                            mbar_arrive_cluster(smem_addr(&sh.ds_full[BN == 128 ? c : 0]));
+                    }
+                }
             }
             if (ok && list.n > 0) {
                 ok = wait(&sh.acc_full, accs & 1);
@@ -2029,8 +2050,8 @@ constexpr uint64_t kWaitLimit = 4000000000u;
 // Heads of up to 64 leave room in tensor memory for three CTAs of one tile of
 // queries each, whose turns hide one another's waits; wider ones for one CTA
 // of two tiles, whose products run while the other's weights are worked out.
-using Narrow = FwdShape<64, 1, 128, 2>;
-using Wide = FwdShape<128, 2, 128, 1>;
+using Narrow = FwdShape<64, 1, 2>;
+using Wide = FwdShape<128, 2, 1>;
 
 template <int DT, class S>
 int launch_tiles(FwdTiles &t, const Fwd &f, const zero_attention_t *a, cudaStream_t st)

@@ -272,6 +272,26 @@ __device__ __forceinline__ void tmem_wait_loads(uint32_t (&r)[32])
                  : "memory");
 }
 
+// The same of 16 columns.
+__device__ __forceinline__ void tmem_load16(uint32_t addr, uint32_t (&r)[16])
+{
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(addr));
+}
+
+__device__ __forceinline__ void tmem_wait_loads16(uint32_t (&r)[16])
+{
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                   "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
+                 :
+                 : "memory");
+}
+
 // Sixteen columns of this warp's 32 lanes, from its lanes' registers.
 __device__ __forceinline__ void tmem_store16(uint32_t addr, const uint32_t (&r)[16])
 {
@@ -349,21 +369,22 @@ __device__ __forceinline__ void tensor_products4(uint32_t d, uint64_t a, uint64_
 }
 
 // The same four with A in tensor memory: a row per lane, two elements of k to
-// a column (K-major), so eight columns to a product.
-template <int SB>
+// a column (K-major), so eight columns to a product; the second two from X
+// columns on.
+template <int SB, int X>
 __device__ __forceinline__ void tensor_products4_tmem(uint32_t d, uint32_t a, uint64_t b, uint32_t desc, bool add)
 {
     asm volatile(
         "{\n\t.reg .pred l, p, q;\n\t.reg .b32 a1, a2, a3;\n\t.reg .b64 b1, b2, b3;\n\t"
         "elect.sync _|l, 0xffffffff;\n\t"
         "setp.ne.b32 p, %4, 0;\n\tsetp.eq.b32 q, 0, 0;\n\t"
-        "add.s32 a1, %1, 8;\n\tadd.s64 b1, %2, %5;\n\tadd.s32 a2, %1, 16;\n\tadd.s64 b2, b1, %5;\n\t"
-        "add.s32 a3, %1, 24;\n\tadd.s64 b3, b2, %5;\n\t"
+        "add.s32 a1, %1, 8;\n\tadd.s64 b1, %2, %5;\n\tadd.s32 a2, %1, %6;\n\tadd.s64 b2, b1, %5;\n\t"
+        "add.s32 a3, a2, 8;\n\tadd.s64 b3, b2, %5;\n\t"
         "@l tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t"
         "@l tcgen05.mma.cta_group::1.kind::f16 [%0], [a1], b1, %3, q;\n\t"
         "@l tcgen05.mma.cta_group::1.kind::f16 [%0], [a2], b2, %3, q;\n\t"
         "@l tcgen05.mma.cta_group::1.kind::f16 [%0], [a3], b3, %3, q;\n\t}" ::"r"(d),
-        "r"(a), "l"(b), "r"(desc), "r"((uint32_t)add), "n"(SB)
+        "r"(a), "l"(b), "r"(desc), "r"((uint32_t)add), "n"(SB), "n"(X)
         : "memory");
 }
 
