@@ -1003,50 +1003,50 @@ struct StatsArgs {
     int64_t tiles;
 };
 
-template <int DT>
-__global__ void __launch_bounds__(kThreads) k_attn_stats(const __grid_constant__ StatsArgs f)
+// A warp takes 32 queries of a tile and the heads of its block: lse by one
+// lane per query, dout and out by 2 to 16 lanes to a row.
+template <int DT, int L>
+__global__ void __launch_bounds__(128) k_attn_stats(const __grid_constant__ StatsArgs f)
 {
+    constexpr int kRows = 32 / L;
     const Attn &a = f.a;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int part = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = lane / L, at = lane & (L - 1);
     pdl_launch_next();
-    int lanes = 1;  // per row: 8 elements each
-    while (lanes * 8 < a.dim)
-        lanes *= 2;
-    const int rows = 32 / lanes, sub = lane / lanes, at = lane & (lanes - 1);
-    // a warp: 32 rows of a tile and one head
-    const int64_t all = f.tiles * a.q_heads * 4;
-    for (int64_t u = (int64_t)blockIdx.x * kWarps + warp; u < all; u += (int64_t)gridDim.x * kWarps) {
-        const int64_t number = u / 4 / a.q_heads;
-        const int32_t h = (int32_t)(u / 4 - number * a.q_heads), part = (int32_t)(u & 3);
+    for (int64_t number = blockIdx.x; number < f.tiles; number += gridDim.x) {
         const TileAt t = find_tile(a, a.q_offsets, a.q_tokens, number, 128, false, lane);
+        const int32_t first = t.first + 32 * part, left = t.s.lq - first;  // of this warp
         if (!t.any)
             continue;
-        float *to = f.stats + (h * f.tiles + number) * 256 + part * 32;
-#pragma unroll 4
-        for (int r0 = 0; r0 < 32; r0 += rows) {
-            const int32_t i = t.first + part * 32 + r0 + sub;
-            const int64_t row = t.s.q0 + i;
-            float sum = 0.0f;
-            if (i < t.s.lq && at * 8 < a.dim) {
-                const uint4 x = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(f.dout.p) + row * f.dout.ld + h * f.dout.hd + at * 8);
-                const uint4 y = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(f.out.p) + row * f.out.ld + h * f.out.hd + at * 8);
-                float fx[8], fy[8];
-                Elem<DT>::to_float(&x, fx);
-                Elem<DT>::to_float(&y, fy);
+        const bool in = at * 8 < a.dim;
+        const uint16_t *const x0 = static_cast<const uint16_t *>(f.dout.p) + (t.s.q0 + first + sub) * f.dout.ld + at * 8;
+        const uint16_t *const y0 = static_cast<const uint16_t *>(f.out.p) + (t.s.q0 + first + sub) * f.out.ld + at * 8;
+        for (int32_t h = blockIdx.y; h < a.q_heads; h += gridDim.y) {
+            const float lse = lane < left ? f.lse[(int64_t)h * a.q_tokens + t.s.q0 + first + lane] : -INFINITY;
+            const uint16_t *const xh = x0 + h * f.dout.hd, *const yh = y0 + h * f.out.hd;
+            float mine = 0.0f;
+#pragma unroll 8
+            for (int i = 0; i < L; ++i) {
+                float sum = 0.0f;
+                if (in && kRows * i + sub < left) {
+                    const uint4 x = __ldg(reinterpret_cast<const uint4 *>(xh + (int64_t)kRows * i * f.dout.ld));
+                    const uint4 y = __ldg(reinterpret_cast<const uint4 *>(yh + (int64_t)kRows * i * f.out.ld));
+                    float fx[8], fy[8];
+                    Elem<DT>::to_float(&x, fx);
+                    Elem<DT>::to_float(&y, fy);
 #pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    sum += fx[e] * fy[e];
-            }
+                    for (int e = 0; e < 8; ++e)
+                        sum += fx[e] * fy[e];
+                }
 #pragma unroll
-            for (int o = 16; o > 0; o >>= 1)
-                if (o < lanes)
+                for (int o = L / 2; o > 0; o >>= 1)
                     sum += __shfl_xor_sync(0xffffffffu, sum, o);
-            if (at == 0) {
-                const bool live = i < t.s.lq;
-                const float lse = live ? f.lse[(int64_t)h * a.q_tokens + row] : -INFINITY;
-                to[r0 + sub] = lse == -INFINITY ? INFINITY : lse * 1.4426950408889634f;
-                to[128 + r0 + sub] = live ? sum : 0.0f;
+                // row kRows i + s is the sum of lanes L s on: query `lane` gets its own
+                const float v = __shfl_sync(0xffffffffu, sum, (lane & (kRows - 1)) * L);
+                mine = lane / kRows == i ? v : mine;
             }
+            float *const to = f.stats + (h * f.tiles + number) * 256 + 32 * part + lane;
+            to[0] = lse == -INFINITY ? INFINITY : lse * 1.4426950408889634f;
+            to[128] = mine;
         }
     }
 }
@@ -1062,6 +1062,7 @@ struct BwdTiles {
     int64_t chunks, split_units;
     float *partial;  // [split unit][dv, dk][128][dim]
     float scale, scale_log2;
+    int32_t after_dkv;  // (dq: k_attn_dkv is launched before it)
     WsHeader *hdr;
     uint64_t limit_ns;
 };
@@ -1219,8 +1220,9 @@ __global__ void __launch_bounds__(S::THREADS, S::PER_SM) k_attn_dkv(const __grid
     __syncthreads();
     tmem_fence_after();
     const uint32_t tmem = (uint32_t)uniform((int32_t)sh.tmem);
-    pdl_launch_next();
+    // (dq's kernel may start when every CTA of this one has seen the rows' statistics)
     pdl_wait();
+    pdl_launch_next();
     auto wait = [&](uint64_t *bar, uint32_t parity) { return mbar_wait_warp(bar, parity, f.limit_ns, &sh.gave_up); };
     uint32_t units = 0;
     auto next = [&](KeyUnit &u) {
@@ -1561,35 +1563,33 @@ __global__ void __launch_bounds__(S::THREADS, S::PER_SM) k_attn_dkv(const __grid
 }
 
 // The sums of the first keys' tiles from their parts, in order: a block takes
-// eight keys of one tile, key head and sequence.
+// every gridDim.y-th eight keys of a tile's key heads.
 template <int DT>
 __global__ void __launch_bounds__(kThreads) k_attn_join(const __grid_constant__ BwdTiles f)
 {
     const Attn &a = f.a;
-    pdl_launch_next();
-    pdl_wait();
-    for (int64_t b = blockIdx.x; b < (int64_t)a.sequences * f.sink_tiles * a.k_heads * 16; b += gridDim.x) {
-        const int rows = (int)(b & 15) * 8;
-        const int64_t i = b >> 4;
-        const int32_t g = (int32_t)(i % a.k_heads), s = (int32_t)(i / a.k_heads / f.sink_tiles);
-        const int32_t tile = (int32_t)(i / a.k_heads % f.sink_tiles), first = tile * 128;
-        const Seq sq = sequence(a, s);
-        if (first + rows >= sq.lk || first >= a.sinks)
-            continue;
-        const QueryTiles t = query_tiles<128>(a, first, sq.lq, sq.lk);
-        if (!is_split(f, first, t))
-            continue;
-        const int64_t base = a.q_offsets ? sq.q0 / (128 * f.chunk) + s : 0;
+    const int32_t s = blockIdx.x / f.sink_tiles, tile = blockIdx.x % f.sink_tiles, first = tile * 128;
+    const Seq sq = sequence(a, s);
+    if (first >= sq.lk || first >= a.sinks)
+        return;
+    const QueryTiles t = query_tiles<128>(a, first, sq.lq, sq.lk);
+    if (!is_split(f, first, t))
+        return;
+    const int64_t base = a.q_offsets ? sq.q0 / (128 * f.chunk) + s : 0;
+    for (int32_t b = blockIdx.y; b < a.k_heads * 16; b += gridDim.y) {
+        const int rows = (b & 15) * 8;
+        const int32_t g = b >> 4;
         for (int v = threadIdx.x; v < 2 * 8 * a.dim; v += kThreads) {
             const int which = v / (8 * a.dim), r = rows + (v - which * 8 * a.dim) / a.dim, e = v % a.dim;
             if (first + r >= sq.lk)
                 continue;
             float sum = 0.0f;
+#pragma unroll 4
             for (int32_t c = t.low / f.chunk; c <= t.high / f.chunk; ++c) {
                 const int64_t slot = ((base + c) * f.sink_tiles + tile) * a.k_heads + g;
                 sum += f.partial[((slot * 2 + which) * 128 + r) * a.dim + e];
             }
-            const Heads &to = which ? f.dk : f.dv;
+            const Heads to{which ? f.dk.p : f.dv.p, which ? f.dk.ld : f.dv.ld, which ? f.dk.hd : f.dv.hd};
             store1<DT>(const_cast<void *>(to.p), (sq.k0 + first + r) * to.ld + g * to.hd + e, which ? sum * f.scale : sum);
         }
     }
@@ -1660,8 +1660,11 @@ __global__ void __launch_bounds__(S::THREADS, S::PER_SM) k_attn_dq(const __grid_
     __syncthreads();
     tmem_fence_after();
     const uint32_t tmem = (uint32_t)uniform((int32_t)sh.tmem);
-    pdl_launch_next();
-    pdl_wait();
+    // Behind k_attn_dkv this kernel starts where that one ends, SM by SM: it
+    // reads nothing that that one writes, and the statistics were complete
+    // before any CTA of that one let it start.  It ends after that one.
+    if (!f.after_dkv)
+        pdl_wait();
     auto wait = [&](uint64_t *bar, uint32_t parity) { return mbar_wait_warp(bar, parity, f.limit_ns, &sh.gave_up); };
     uint32_t units = 0;
     auto next = [&](QueryUnit &u) {
@@ -1948,6 +1951,8 @@ __global__ void __launch_bounds__(S::THREADS, S::PER_SM) k_attn_dq(const __grid_
     }
     if (warp == kMma)
         tmem_give(tmem, S::TMEM);
+    if (f.after_dkv)
+        pdl_wait();
 }
 
 // ------------------------------------------------------------- host side
@@ -2255,17 +2260,20 @@ int launch_backward(BwdTiles &t, const BwdArrays &h, const zero_attention_t *a, 
         return ZERO_OK;
     };
     ZERO_TRY(maps(S::BN, 128));
-    launch(k_attn_dkv<DT, S>, t.split_units + t.k_tiles * t.a.k_heads);
-    if (e == cudaSuccess && t.split_units > 0) {
-        what = "k_attn_join";
-        const int64_t blocks = (int64_t)t.a.sequences * t.sink_tiles * t.a.k_heads * 16;
-        e = launch_k(k_attn_join<DT>, (int)(blocks < 152 * 8 ? blocks : 152 * 8), kThreads, st, true, t);
-    }
+    const int64_t key_units = t.split_units + t.k_tiles * t.a.k_heads;
+    launch(k_attn_dkv<DT, S>, key_units);
     if (e == cudaSuccess) {
         what = "k_attn_dq";
         if (S::BN != 128)
             ZERO_TRY(maps(128, S::BN));
+        t.after_dkv = key_units > 0;
         launch(k_attn_dq<DT, S>, t.q_tiles * t.a.q_heads);
+    }
+    if (e == cudaSuccess && t.split_units > 0) {
+        what = "k_attn_join";
+        const int64_t x = (int64_t)t.a.sequences * t.sink_tiles, y = 152 * 8 / x, most = (int64_t)t.a.k_heads * 16;
+        k_attn_join<DT><<<dim3((unsigned)x, (unsigned)(y < 1 ? 1 : y < most ? y : most)), kThreads, 0, st>>>(t);
+        e = cudaGetLastError();
     }
     if (e != cudaSuccess) {
         cudaGetLastError();
@@ -2346,9 +2354,13 @@ extern "C" int zero_window_attention_backward(const zero_attention_t *a, const v
         const SinkPlan p = plan_sinks(a, one);
         t.chunk = p.chunk, t.sink_tiles = p.sink_tiles, t.chunks = p.chunks, t.split_units = p.units;
         const StatsArgs s{t.a, hdout, hout, lse, const_cast<float *>(t.stats), t.q_tiles};
-        auto kernel = a->dtype == ZERO_F16 ? k_attn_stats<ZERO_F16> : k_attn_stats<ZERO_BF16>;
-        const int64_t blocks = (t.q_tiles * a->q_heads * 4 + kWarps - 1) / kWarps;
-        kernel<<<grid_for(reinterpret_cast<const void *>(kernel), blocks, 1 << 30), kThreads, 0, st>>>(s);
+        const bool f16 = a->dtype == ZERO_F16;
+        auto kernel = a->head_dim <= 16   ? f16 ? k_attn_stats<ZERO_F16, 2> : k_attn_stats<ZERO_BF16, 2>
+                      : a->head_dim <= 64 ? f16 ? k_attn_stats<ZERO_F16, 8> : k_attn_stats<ZERO_BF16, 8>
+                                          : f16 ? k_attn_stats<ZERO_F16, 16> : k_attn_stats<ZERO_BF16, 16>;
+        // blocks for every SM to hold sixteen, or one for each tile and head
+        const int64_t x = t.q_tiles < 152 * 16 ? t.q_tiles : 152 * 16, y = (152 * 16 + x - 1) / x;
+        kernel<<<dim3((unsigned)x, (unsigned)(y < a->q_heads ? y : a->q_heads)), 128, 0, st>>>(s);
         ZERO_TRY(check_launch("k_attn_stats"));
     }
     const BwdArrays h{hdout, hq, hk, hv};
