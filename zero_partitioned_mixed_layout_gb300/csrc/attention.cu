@@ -1112,13 +1112,14 @@ struct BwdShape {
     static constexpr int DP = DP_, BN = BN_, PER_SM = PER_SM_;
     static constexpr int BOXES = DP / 64, TILE = BOXES * 16384, MOVING = BOXES * BN * 128;  // bytes
     static constexpr int ROW_WARPS = BN / 16, THREADS = (ROW_WARPS + 2) * 32;
-    static constexpr int SMEM = 1024 + 2 * TILE + 4 * MOVING + 4 * BN * 4 + ROW_WARPS * 2048;
+    static constexpr int STAGES = BN == 64 ? 4 : 2;  // of each of the two that move
+    static constexpr int SMEM = 1024 + 2 * TILE + STAGES * (2 * MOVING + 2 * BN * 4) + ROW_WARPS * 2048;
     static constexpr int TMEM = 2 * BN + 2 * DP;  // (dq: three of BN and one of DP)
     static_assert(SMEM * PER_SM <= 227 * 1024 && TMEM * PER_SM <= 512 && 3 * BN + DP <= TMEM, "what an SM has");
 };
 
 struct KeyShared {
-    uint64_t kv_full, kv_empty, q_full[2], q_empty[2], o_full[2], o_empty[2], s_full, dp_full, p_full[2], ds_full[2], acc_full;
+    uint64_t kv_full, kv_empty, q_full[4], q_empty[4], o_full[4], o_empty[4], s_full, dp_full, p_full[2], ds_full[2], acc_full;
     uint64_t unit_full[kUnitRing], unit_empty[kUnitRing];
     KeyUnit units[kUnitRing];
     uint32_t tmem, gave_up;
@@ -1181,9 +1182,9 @@ __global__ void __launch_bounds__(S::THREADS, S::PER_SM) k_attn_dkv(const __grid
     extern __shared__ unsigned char smem_raw[];
     __shared__ KeyShared sh;
     unsigned char *smem = smem_raw + ((1024 - (smem_addr(smem_raw) & 1023u)) & 1023u);
-    unsigned char *const s_k = smem, *const s_v = smem + S::TILE, *const s_q = s_v + S::TILE, *const s_o = s_q + 2 * S::MOVING;
-    float *const s_stats = reinterpret_cast<float *>(s_o + 2 * S::MOVING);  // [stage][lse2, delta][BN]
-    unsigned char *const s_out = reinterpret_cast<unsigned char *>(s_stats + 4 * BN);
+    unsigned char *const s_k = smem, *const s_v = smem + S::TILE, *const s_q = s_v + S::TILE, *const s_o = s_q + S::STAGES * S::MOVING;
+    float *const s_stats = reinterpret_cast<float *>(s_o + S::STAGES * S::MOVING);  // [stage][lse2, delta][BN]
+    unsigned char *const s_out = reinterpret_cast<unsigned char *>(s_stats + S::STAGES * 2 * BN);
     const Attn &a = f.a;
     const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
     constexpr int kTma = S::ROW_WARPS, kMma = S::ROW_WARPS + 1;
@@ -1192,7 +1193,7 @@ __global__ void __launch_bounds__(S::THREADS, S::PER_SM) k_attn_dkv(const __grid
     if (threadIdx.x == 0) {
         mbar_init_count(&sh.kv_full, 1);
         mbar_init_count(&sh.kv_empty, 1);
-        for (int s = 0; s < 2; ++s) {
+        for (int s = 0; s < S::STAGES; ++s) {
             mbar_init_count(&sh.q_full[s], 1);
             mbar_init_count(&sh.q_empty[s], 1);
             mbar_init_count(&sh.o_full[s], 1);
@@ -1279,7 +1280,7 @@ __global__ void __launch_bounds__(S::THREADS, S::PER_SM) k_attn_dkv(const __grid
             ++kvn;
             for (int32_t h = u.head * a.group; ok && h < (u.head + 1) * a.group; ++h)
                 for (int32_t t = u.low; t <= u.high; ++t) {
-                    const uint32_t st = qn & 1, parity = ((qn >> 1) & 1) ^ 1;
+                    const uint32_t st = qn % S::STAGES, parity = ((qn / S::STAGES) & 1) ^ 1;
                     ok = wait(&sh.q_empty[st], parity);
                     if (!ok)
                         break;
@@ -1322,16 +1323,16 @@ __global__ void __launch_bounds__(S::THREADS, S::PER_SM) k_attn_dkv(const __grid
             const int32_t count = u.low > u.high ? 0 : (u.high - u.low + 1) * a.group;
             if (count == 0)
                 continue;
-            ok = wait(&sh.kv_full, kvn & 1) && wait(&sh.q_full[qn & 1], (qn >> 1) & 1);
+            ok = wait(&sh.kv_full, kvn & 1) && wait(&sh.q_full[qn % S::STAGES], (qn / S::STAGES) & 1);
             if (!ok)
                 break;
             ++kvn;
             tmem_fence_after();
-            inner_products<DP, 128, BN>(tmem, dk0, dq0 + (((qn & 1) * S::MOVING) >> 4), desc_s, steps);
+            inner_products<DP, 128, BN>(tmem, dk0, dq0 + (((qn % S::STAGES) * S::MOVING) >> 4), desc_s, steps);
             tensor_commit_elected(&sh.s_full);
             for (int32_t i = 0; i < count; ++i, ++qn, ++n) {
-                const uint32_t st = qn & 1;
-                ok = wait(&sh.o_full[st], (qn >> 1) & 1);
+                const uint32_t st = qn % S::STAGES;
+                ok = wait(&sh.o_full[st], (qn / S::STAGES) & 1);
                 if (!ok)
                     break;
                 tmem_fence_after();
@@ -1350,8 +1351,8 @@ __global__ void __launch_bounds__(S::THREADS, S::PER_SM) k_attn_dkv(const __grid
                     break;
                 tensor_commit_elected(&sh.o_empty[st]);
                 if (i + 1 < count) {
-                    const uint32_t to = (qn + 1) & 1;
-                    ok = wait(&sh.q_full[to], ((qn + 1) >> 1) & 1);
+                    const uint32_t to = (qn + 1) % S::STAGES;
+                    ok = wait(&sh.q_full[to], ((qn + 1) / S::STAGES) & 1);
                     if (!ok)
                         break;
                     tmem_fence_after();
@@ -1389,18 +1390,18 @@ __global__ void __launch_bounds__(S::THREADS, S::PER_SM) k_attn_dkv(const __grid
             const int32_t j = u.first + quarter * 32 + lane;
             int32_t t = u.low;
             for (int32_t i = 0; i < count; ++i, ++qn, ++n) {
-                const uint32_t st = qn & 1;
+                const uint32_t st = qn % S::STAGES;
                 const int32_t p0 = BN * t + u.lk - u.lq, nq = u.lq - BN * t;
                 const bool whole = nq >= BN && u.first + 127 <= p0 &&
                                    (p0 + BN - 1 - u.first < a.window || u.first + 127 < a.sinks);
-                ok = wait(&sh.s_full, n & 1) && wait(&sh.q_full[st], (qn >> 1) & 1);
+                ok = wait(&sh.s_full, n & 1) && wait(&sh.q_full[st], (qn / S::STAGES) & 1);
                 if (!ok)
                     break;
                 tmem_fence_after();
                 const float *lse2 = s_stats + st * 2 * BN, *delta = lse2 + BN;
                 if (nq < BN) {
                     // rows behind the last query: zeros, since 0 times what they hold may not be 0
-                    ok = wait(&sh.o_full[st], (qn >> 1) & 1);
+                    ok = wait(&sh.o_full[st], (qn / S::STAGES) & 1);
                     if (!ok)
                         break;
                     for (int k = nq * 8 + threadIdx.x; k < BN * 8; k += S::ROW_WARPS * 32)
@@ -1607,7 +1608,7 @@ struct QueryUnit {
 };
 
 struct QueryShared {
-    uint64_t q_full, q_empty, k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], dp_full, ds_full[2], acc_full;
+    uint64_t q_full, q_empty, k_full[4], k_empty[4], v_full[4], v_empty[4], s_full[2], dp_full, ds_full[2], acc_full;
     uint64_t unit_full[kUnitRing], unit_empty[kUnitRing];
     QueryUnit units[kUnitRing];
     uint32_t tmem, gave_up;
@@ -1624,8 +1625,8 @@ __global__ void __launch_bounds__(S::THREADS, S::PER_SM) k_attn_dq(const __grid_
     extern __shared__ unsigned char smem_raw[];
     __shared__ QueryShared sh;
     unsigned char *smem = smem_raw + ((1024 - (smem_addr(smem_raw) & 1023u)) & 1023u);
-    unsigned char *const s_q = smem, *const s_o = smem + S::TILE, *const s_k = s_o + S::TILE, *const s_v = s_k + 2 * S::MOVING;
-    unsigned char *const s_out = s_v + 2 * S::MOVING;
+    unsigned char *const s_q = smem, *const s_o = smem + S::TILE, *const s_k = s_o + S::TILE, *const s_v = s_k + S::STAGES * S::MOVING;
+    unsigned char *const s_out = s_v + S::STAGES * S::MOVING;
     const Attn &a = f.a;
     const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
     constexpr int kTma = S::ROW_WARPS, kMma = S::ROW_WARPS + 1;
@@ -1634,12 +1635,13 @@ __global__ void __launch_bounds__(S::THREADS, S::PER_SM) k_attn_dq(const __grid_
     if (threadIdx.x == 0) {
         mbar_init_count(&sh.q_full, 1);
         mbar_init_count(&sh.q_empty, 1);
-        for (int s = 0; s < 2; ++s) {
+        for (int s = 0; s < S::STAGES; ++s) {
             mbar_init_count(&sh.k_full[s], 1);
             mbar_init_count(&sh.k_empty[s], 1);
             mbar_init_count(&sh.v_full[s], 1);
             mbar_init_count(&sh.v_empty[s], 1);
-            mbar_init_count(&sh.s_full[s], 1);
+            if (s < 2)
+                mbar_init_count(&sh.s_full[s], 1);
         }
         mbar_init_count(&sh.dp_full, 1);
         for (int c = 0; c < BN / 64; ++c)
@@ -1729,7 +1731,7 @@ __global__ void __launch_bounds__(S::THREADS, S::PER_SM) k_attn_dq(const __grid_
             ++un;
             const int32_t g = u.head / a.group;
             for (int32_t n = 0; n < list.n; ++n, ++kn) {
-                const uint32_t st = kn & 1, parity = ((kn >> 1) & 1) ^ 1;
+                const uint32_t st = kn % S::STAGES, parity = ((kn / S::STAGES) & 1) ^ 1;
                 const int32_t row = u.k_row + BN * list.at(n);
                 ok = wait(&sh.k_empty[st], parity);
                 if (!ok)
@@ -1774,17 +1776,17 @@ __global__ void __launch_bounds__(S::THREADS, S::PER_SM) k_attn_dq(const __grid_
             ++un;
             // scores of tile kn + m of the keys, into the one of two buffers
             auto scores = [&](uint32_t at) {
-                const uint32_t st = at & 1;
-                ok = ok && wait(&sh.k_full[st], (at >> 1) & 1);
+                const uint32_t st = at % S::STAGES, buf = at & 1;
+                ok = ok && wait(&sh.k_full[st], (at / S::STAGES) & 1);
                 if (!ok)
                     return;
                 tmem_fence_after();
-                inner_products<DP, 128, BN>(tmem + st * BN, dq0, dk0 + ((st * S::MOVING) >> 4), desc_s, steps);
-                tensor_commit_elected(&sh.s_full[st]);
+                inner_products<DP, 128, BN>(tmem + buf * BN, dq0, dk0 + ((st * S::MOVING) >> 4), desc_s, steps);
+                tensor_commit_elected(&sh.s_full[buf]);
             };
             auto grads = [&](uint32_t at) {
-                const uint32_t st = at & 1;
-                ok = ok && wait(&sh.v_full[st], (at >> 1) & 1);
+                const uint32_t st = at % S::STAGES;
+                ok = ok && wait(&sh.v_full[st], (at / S::STAGES) & 1);
                 if (!ok)
                     return;
                 tmem_fence_after();
@@ -1795,7 +1797,7 @@ __global__ void __launch_bounds__(S::THREADS, S::PER_SM) k_attn_dq(const __grid_
             scores(kn);
             grads(kn);
             for (int32_t n = 0; ok && n < list.n; ++n, ++kn, ++dsn) {
-                const uint32_t st = kn & 1;
+                const uint32_t st = kn % S::STAGES, buf = kn & 1;
                 if (n + 1 < list.n)
                     scores(kn + 1);
 #pragma unroll
@@ -1808,7 +1810,7 @@ __global__ void __launch_bounds__(S::THREADS, S::PER_SM) k_attn_dq(const __grid_
                         grads(kn + 1);
                     if (!ok)
                         break;
-                    tensor_products4_tmem<128, 32>(tmem + kDq, tmem + st * BN + 64 * c, tk0 + ((st * S::MOVING) >> 4) + 512 * c,
+                    tensor_products4_tmem<128, 32>(tmem + kDq, tmem + buf * BN + 64 * c, tk0 + ((st * S::MOVING) >> 4) + 512 * c,
                                                    desc_acc, n != 0 || c != 0);
                 }
                 if (!ok)
@@ -1836,15 +1838,15 @@ __global__ void __launch_bounds__(S::THREADS, S::PER_SM) k_attn_dq(const __grid_
             const float *stats = f.stats + (u.head * f.q_tiles + u.stats) * 256 + quarter * 32 + lane;
             const float lse2 = stats[0], delta = stats[128];
             for (int32_t n = 0; n < list.n; ++n, ++kn) {
-                const uint32_t st = kn & 1;
+                const uint32_t st = kn % S::STAGES, buf = kn & 1;
                 const int32_t k_first = list.at(n) * BN;
                 const bool whole = k_first + BN - 1 <= p_first &&
                                    (k_first > p_last - a.window || k_first + BN - 1 < a.sinks);
-                ok = wait(&sh.s_full[st], (kn >> 1) & 1);
+                ok = wait(&sh.s_full[buf], (kn >> 1) & 1);
                 if (!ok)
                     break;
                 tmem_fence_after();
-                const uint32_t at_s = tmem + lanes + st * BN, at_p = tmem + lanes + kDp;
+                const uint32_t at_s = tmem + lanes + buf * BN, at_p = tmem + lanes + kDp;
                 F2 w2[2][16];
                 const F2 scale2 = twice(f.scale_log2), base2 = twice(-lse2), delta2 = twice(-delta);
                 // the weights, while dP is worked out
