@@ -1171,13 +1171,14 @@ def zero_qk_norm_backward(dq_out, dk_out, q, k, q_weight, k_weight, dq, dk, dq_w
 _NO_WINDOW = (1 << 63) - 1
 
 
-def _attention_sizes(q_tokens, k_tokens, sequences, q_heads, k_heads, head_dim, code, window, sinks, scale):
-    if window is None:
+def _attention_sizes(q_tokens, k_tokens, sequences, q_heads, k_heads, head_dim, code, window, sinks, scale, *arrays):
+    if window is None or window > _NO_WINDOW:
         window = _NO_WINDOW
+    if sinks > _NO_WINDOW:
+        sinks = _NO_WINDOW
     if scale is None:
         scale = head_dim ** -0.5 if head_dim > 0 else 1.0
-    return _Attention(q_tokens, k_tokens, sequences, q_heads, k_heads, head_dim, code, min(window, _NO_WINDOW),
-                      min(sinks, _NO_WINDOW), scale)
+    return _Attention(q_tokens, k_tokens, sequences, q_heads, k_heads, head_dim, code, window, sinks, scale, *arrays)
 
 
 def _attention_struct(q, k, window, sinks, scale, q_offsets, k_offsets, k_lengths, dev):
@@ -1188,11 +1189,10 @@ def _attention_struct(q, k, window, sinks, scale, q_offsets, k_offsets, k_length
     n = 1 if q_offsets is None else q_offsets.numel() - 1
     if n < 0:
         raise ValueError("q_offsets must hold one more than the number of sequences")
-    a = _attention_sizes(tq, tk, n, hq, hk, d, _type_code(q), window, sinks, scale)
-    a.q_offsets = _int64_pointer(q_offsets, "q_offsets", n + 1, dev)
-    a.k_offsets = _int64_pointer(k_offsets, "k_offsets", n + 1, dev)
-    a.k_lengths = _int64_pointer(k_lengths, "k_lengths", n, dev)
-    return a
+    return _attention_sizes(tq, tk, n, hq, hk, d, _type_code(q), window, sinks, scale,
+                            _int64_pointer(q_offsets, "q_offsets", n + 1, dev),
+                            _int64_pointer(k_offsets, "k_offsets", n + 1, dev),
+                            _int64_pointer(k_lengths, "k_lengths", n, dev))
 
 
 def zero_window_attention_workspace_bytes(q_tokens: int, k_tokens: int, sequences: int, q_heads: int, k_heads: int,

@@ -27,20 +27,28 @@ struct Seq {
 
 __device__ __forceinline__ int64_t cut(int64_t x, int64_t lo, int64_t hi) { return x < lo ? lo : x > hi ? hi : x; }
 
-// Sequence s, cut to the rows that there are, whatever the arrays hold.
-__device__ __forceinline__ Seq sequence(const Attn &a, int32_t s)
+// A sequence cut to the rows that there are, whatever the arrays hold.
+__device__ __forceinline__ Seq sequence_of(const Attn &a, int64_t q_from, int64_t q_to, int64_t k_from, int64_t k_to,
+                                           int64_t k_length)
 {
     Seq q;
-    q.q0 = a.q_offsets ? cut(a.q_offsets[s], 0, a.q_tokens) : 0;
-    q.lq = (int32_t)((a.q_offsets ? cut(a.q_offsets[s + 1], q.q0, a.q_tokens) : a.q_tokens) - q.q0);
+    q.q0 = a.q_offsets ? cut(q_from, 0, a.q_tokens) : 0;
+    q.lq = (int32_t)((a.q_offsets ? cut(q_to, q.q0, a.q_tokens) : a.q_tokens) - q.q0);
     if (!a.k_offsets) {
         q.k0 = q.q0, q.lk = q.lq;
         return q;
     }
-    q.k0 = cut(a.k_offsets[s], 0, a.k_tokens);
-    const int64_t room = cut(a.k_offsets[s + 1], q.k0, a.k_tokens) - q.k0;
-    q.lk = (int32_t)(a.k_lengths ? cut(a.k_lengths[s], 0, room) : room);
+    q.k0 = cut(k_from, 0, a.k_tokens);
+    const int64_t room = cut(k_to, q.k0, a.k_tokens) - q.k0;
+    q.lk = (int32_t)(a.k_lengths ? cut(k_length, 0, room) : room);
     return q;
+}
+
+__device__ __forceinline__ Seq sequence(const Attn &a, int32_t s)
+{
+    return sequence_of(a, a.q_offsets ? a.q_offsets[s] : 0, a.q_offsets ? a.q_offsets[s + 1] : 0,
+                       a.k_offsets ? a.k_offsets[s] : 0, a.k_offsets ? a.k_offsets[s + 1] : 0,
+                       a.k_lengths ? a.k_lengths[s] : 0);
 }
 
 struct Fwd {
@@ -80,30 +88,51 @@ struct TileAt {
     bool any;
 };
 
-// By a whole warp: 32 offsets at a time.  (T is a constant where it can be:
-// divisions of 64 bits are long.)
+// The tile's number that sequence s starts at, of an offset as it is.
+__device__ __forceinline__ int64_t first_tile(int64_t offset, int64_t rows, int32_t s, int32_t T)
+{
+    return (int64_t)((uint32_t)cut(offset, 0, rows) / (uint32_t)T) + s;  // (rows fit 31 bits)
+}
+
+// By a whole warp.  Up to 31 sequences' arrays arrive in one round, an entry
+// per lane; of more, 32 offsets are looked at in each round of a search.
 __device__ __forceinline__ TileAt find_tile(const Attn &a, const int64_t *offsets, int64_t rows, int64_t number, int32_t T,
                                             bool keys, int lane)
 {
     TileAt t{};
     int32_t s = 0;
     int64_t first = number * T;
-    if (offsets) {
-        int32_t lo = -1, hi = a.sequences;
-        while (hi - lo > 1) {
-            const int32_t step = (hi - lo - 1 + 31) / 32, at = lo + (lane + 1) * step;
-            const bool before = at < hi && cut(offsets[at], 0, rows) / T + at <= number;
-            const int32_t n = __popc(__ballot_sync(0xffffffffu, before));
-            hi = hi < lo + (n + 1) * step ? hi : lo + (n + 1) * step;
-            lo += n * step;
-        }
-        if (lo < 0)
+    if (offsets && a.sequences < 32) {
+        const int32_t n = a.sequences;
+        const bool in = lane <= n;
+        const int64_t q = a.q_offsets && in ? a.q_offsets[lane] : 0, k = a.k_offsets && in ? a.k_offsets[lane] : 0;
+        const int64_t l = a.k_lengths && lane < n ? a.k_lengths[lane] : 0;
+        const int64_t at = first_tile(offsets == a.q_offsets ? q : k, rows, lane, T);
+        s = __popc(__ballot_sync(0xffffffffu, lane < n && at <= number)) - 1;
+        if (s < 0)
             return t;
-        s = lo;
-        first = (number - (cut(offsets[s], 0, rows) / T + s)) * T;
+        first = (number - __shfl_sync(0xffffffffu, at, s)) * T;
+        const int64_t q0 = __shfl_sync(0xffffffffu, q, s), q1 = __shfl_sync(0xffffffffu, q, s + 1);
+        const int64_t k0 = __shfl_sync(0xffffffffu, k, s), k1 = __shfl_sync(0xffffffffu, k, s + 1);
+        t.s = sequence_of(a, q0, q1, k0, k1, __shfl_sync(0xffffffffu, l, s));
+    } else {
+        if (offsets) {
+            int32_t lo = -1, hi = a.sequences;
+            while (hi - lo > 1) {
+                const int32_t step = (hi - lo - 1 + 31) / 32, at = lo + (lane + 1) * step;
+                const bool before = at < hi && first_tile(offsets[at], rows, at, T) <= number;
+                const int32_t n = __popc(__ballot_sync(0xffffffffu, before));
+                hi = hi < lo + (n + 1) * step ? hi : lo + (n + 1) * step;
+                lo += n * step;
+            }
+            if (lo < 0)
+                return t;
+            s = lo;
+            first = (number - first_tile(offsets[s], rows, s, T)) * T;
+        }
+        t.s = sequence(a, s);
     }
     t.index = s;
-    t.s = sequence(a, s);
     t.any = first >= 0 && first < (keys ? t.s.lk : t.s.lq);
     t.first = t.any ? (int32_t)first : 0;
     return t;
