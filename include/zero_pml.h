@@ -803,8 +803,10 @@ int zero_qk_norm_backward(const void *dq_out, int64_t dq_out_ld, int64_t dq_out_
  * With Lq queries and Lk keys, query i stands at key p = i + Lk - Lq (the last
  * query at the last key) and sees key j iff
  *     0 <= j <= p  and  (j > p - window  or  j < sinks).
- * A key that is not seen has no influence, whatever the keys and values
- * beside the sequence's own hold (NaN included). */
+ * What lies beside a sequence's own queries and keys (the rest of a padded
+ * cache, its neighbours) has no influence on it, whatever it holds, NaN
+ * included.  Its own are taken to be finite: a value that is not may also
+ * reach queries that do not see it, and keys that are not seen by it. */
 typedef struct zero_attention {
     int64_t q_tokens, k_tokens, sequences;
     int32_t q_heads, k_heads; /* q_heads a multiple of k_heads: query head h reads key head h / (q_heads / k_heads) */

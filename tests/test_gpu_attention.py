@@ -505,6 +505,132 @@ def test_bindings_refuse_on_the_gpu(zp):
             call()
 
 
+MANY = [(i * 7 % 23, 5 + i * 11 % 60) for i in range(45)]
+
+
+@pytest.mark.parametrize("lens", [MANY, [(min(q, 2), k) for q, k in MANY]], ids=["many", "few"])
+def test_window_attention_of_more_sequences_than_lanes(zp, lens):
+    b = Batch(lens, 4, 2, 64, "bf16", room=2, behind=1)
+    b.check_forward(zp, 20, 3)
+    b.check_backward(zp, 20, 3)
+
+
+@pytest.mark.parametrize("dim", range(8, 129, 8))
+def test_window_attention_head_dims(zp, dim):
+    b = Batch([(140, 200), (1, 30)], 4, 2, dim, "f16")
+    b.check_forward(zp, 90, 2)
+    b.check_backward(zp, 90, 2)
+    Batch([(1, 200), (1, 30)], 4, 2, dim, "f16").check_forward(zp, 90, 2)
+
+
+def test_window_attention_rows_before_the_first_sequence(zp):
+    """Offsets that start behind the first rows: those are left as they were."""
+    for n in (1, 200):
+        b = Batch([(40, 40), (n, 220)], 2, 2, 64, "bf16", fill=math.nan)
+        b.q[:40] = b.k[:40] = b.v[:40] = b.dout[:40] = math.nan
+        b.where = {k: v[1:].contiguous() for k, v in b.where.items()}
+        b.live[:40] = b.keyed[:40] = False
+        b.slices = lambda: [(slice(40, 40 + n), slice(40, 260))]
+        b.lens = [(n, 220)]
+        b.check_forward(zp, 50, 1)
+        b.check_backward(zp, 50, 1)
+
+
+@pytest.mark.parametrize("few", [False, True])
+def test_window_attention_offsets_that_fall_touch_nothing_else(zp, few):
+    """Results mean nothing, but no other memory is written."""
+    b = Batch([(2, 300)] * 3 if few else [(150, 150)] * 3, 2, 1, 64, "f16", fill=0.0)
+    dev = dict(dtype=torch.int64, device="cuda")
+    last = b.tq
+    where = dict(q_offsets=torch.tensor([last, 0, last // 2, 1], **dev), k_offsets=torch.tensor([400, 100, 449, 3], **dev),
+                 k_lengths=torch.tensor([500, -3, 2 ** 45], **dev))
+    guard = torch.full((64, 2, 64), 77.0, dtype=torch.float16, device="cuda")
+    out = torch.full((64 + b.tq + 64, 2, 64), 77.0, dtype=torch.float16, device="cuda")
+    lse = torch.full((2, b.tq), 0.0, device="cuda")
+    ws = b.workspace(zp, 60, 5, True)
+    zp.zero_window_attention(b.q, b.k, b.v, out[64:64 + b.tq], ws, 60, 5, None, lse, **where)
+    grads = [torch.full((64 + t.shape[0] + 64, *t.shape[1:]), 77.0, dtype=torch.float16, device="cuda") for t in (b.q, b.k, b.v)]
+    zp.zero_window_attention_backward(b.dout, b.q, b.k, b.v, out[64:64 + b.tq], lse, *(g[64:-64] for g in grads), ws, 60, 5,
+                                      **where)
+    torch.cuda.synchronize()
+    assert torch.equal(out[:64], guard) and torch.equal(out[-64:], guard)
+    assert all(bool((g[:64] == 77).all()) and bool((g[-64:] == 77).all()) for g in grads)
+    assert zp.zero_workspace_stalls(ws) == 0
+    b.check_forward(zp, 60, 5)  # (and the next call is whole)
+
+
+def test_window_attention_on_two_streams_at_once(zp):
+    jobs = []
+    for i, lens in enumerate(([(700, 700)], [(1, 3000)] * 5, [(300, 900), (20, 20)])):
+        b = Batch(lens, 4, 2, 64, "f16", seed=10 * i)
+        jobs.append((b, torch.cuda.Stream(), [b.workspace(zp, 200, 3, True) for _ in range(2)], []))
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for b, stream, ws, outs in jobs:
+            with torch.cuda.stream(stream):
+                out, lse = torch.empty_like(b.q), torch.empty((4, b.tq), device="cuda")
+                g = [torch.empty_like(x) for x in (b.q, b.k, b.v)]
+                zp.zero_window_attention(b.q, b.k, b.v, out, ws[0], 200, 3, None, lse, **b.where)
+                zp.zero_window_attention_backward(b.dout, b.q, b.k, b.v, out, lse, *g, ws[0], 200, 3, **b.where)
+                outs.append([out, lse, *g])
+    torch.cuda.synchronize()
+    for b, stream, ws, outs in jobs:
+        assert all(torch.equal(x, y) for o in outs for x, y in zip(o, outs[0]))
+        for qs, ks in b.slices():
+            r = ref.attention(b.q[qs], b.k[ks], b.v[ks], 200, 3, 0.125, b.dt)
+            close(outs[0][0][qs], r["out"], b.dt, "out")
+
+
+def test_window_attention_workspace_serves_other_calls(zp):
+    """One workspace, of the largest call, through calls of every kind."""
+    big = Batch([(300, 400)] * 3, 4, 2, 64, "bf16")
+    ws = big.workspace(zp, 100, 5, True)
+    small = [Batch([(1, 390)] * 3, 4, 2, 64, "bf16"), Batch([(2, 50)], 4, 2, 64, "bf16"), Batch([(90, 90)] * 2, 4, 2, 64, "bf16")]
+    for b in (big, *small, big, small[0]):
+        out, lse = torch.empty_like(b.q), torch.empty((4, b.tq), device="cuda")
+        zp.zero_window_attention(b.q, b.k, b.v, out, ws, 100, 5, None, lse, **b.where)
+        g = [torch.empty_like(x) for x in (b.q, b.k, b.v)]
+        zp.zero_window_attention_backward(b.dout, b.q, b.k, b.v, out, lse, *g, ws, 100, 5, **b.where)
+        for qs, ks in b.slices():
+            r = ref.attention(b.q[qs], b.k[ks], b.v[ks], 100, 5, 0.125, b.dt)
+            close(out[qs], r["out"], b.dt, "out")
+            r = ref.attention_backward(b.dout[qs], b.q[qs], b.k[ks], b.v[ks], out[qs], lse[:, qs], 100, 5, 0.125, b.dt)
+            for got, rows, name in zip(g, (qs, ks, ks), ("dq", "dk", "dv")):
+                close(got[rows], r[name], b.dt, name)
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("kernel", [0, 1, 2])
+def test_waits_that_give_up_leave_nan(zp, kernel, dim):
+    """A kernel whose tiles of queries never arrive whole: the call ends, the
+    workspace counts it, and its results are NaN; the next call is whole."""
+    import ctypes
+    hook = zp.lib().zero_test_window_attention_waits
+    hook.argtypes, hook.restype = [ctypes.c_int32, ctypes.c_uint64], None
+    b = Batch([(300, 300), (200, 400)], 4, 2, dim, "f16")
+    out, lse = b.forward(zp, 100, 2)
+    ws = b.workspace(zp, 100, 2, True)
+    o, s = torch.zeros_like(b.q), torch.zeros((4, b.tq), device="cuda")
+    g = [torch.zeros_like(x) for x in (b.q, b.k, b.v)]
+    hook(kernel, 20_000_000)
+    try:
+        if kernel == 0:
+            zp.zero_window_attention(b.q, b.k, b.v, o, ws, 100, 2, None, s, **b.where)
+        else:
+            zp.zero_window_attention_backward(b.dout, b.q, b.k, b.v, out.t, lse, *g, ws, 100, 2, **b.where)
+        stalls = zp.zero_workspace_stalls(ws)
+    finally:
+        hook(-1, 0)
+    assert stalls > 0
+    if kernel == 0:
+        assert bool(torch.isnan(o).all()) and bool(torch.isnan(s).all())
+    else:
+        assert all(bool(torch.isnan(x).all()) == (kernel == 1) for x in g[1:])
+        assert bool(torch.isnan(g[0]).all()) == (kernel == 2)
+    b.check_forward(zp, 100, 2)
+    b.check_backward(zp, 100, 2)
+
+
 # ------------------------------------------------------------------ together
 
 def test_layer_half_together(zp):

@@ -1,5 +1,6 @@
 // Attention with a sliding window and a few first keys that stay visible,
 // forward and backward, over packed sequences and caches.
+#include <atomic>
 #include <cmath>
 #include <initializer_list>
 
@@ -742,6 +743,16 @@ struct FewArgs {
 
 constexpr int kFewWarps = 4;
 
+// Read once: not kept in L1.
+__device__ __forceinline__ uint4 load_once(const uint4 *p)
+{
+    uint4 v;
+    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(p));
+    return v;
+}
+
 __device__ __forceinline__ void mma16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                       uint32_t b1, bool bf16)
 {
@@ -819,7 +830,7 @@ __global__ void __launch_bounds__(kFewWarps * 32) k_attn_few(const __grid_consta
                 const uint4 *from = reinterpret_cast<const uint4 *>(kp + (in ? key(x + 8 * h + g) : 0) * f.k.ld);
 #pragma unroll
                 for (int e = 0; e < KK; ++e)
-                    k[h][e] = in && (c + 4 * e) * 8 < a.dim ? __ldg(from + c + 4 * e) : make_uint4(0, 0, 0, 0);
+                    k[h][e] = in && (c + 4 * e) * 8 < a.dim ? load_once(from + c + 4 * e) : make_uint4(0, 0, 0, 0);
             }
         };
         auto load_v = [&](int32_t x) {
@@ -830,7 +841,7 @@ __global__ void __launch_bounds__(kFewWarps * 32) k_attn_few(const __grid_consta
                 const uint4 *from = reinterpret_cast<const uint4 *>(vp + (in ? key(at_x) : 0) * f.v.ld);
 #pragma unroll
                 for (int e = 0; e < JJ; ++e)
-                    v[h][e] = in && (g + 8 * e) * 8 < a.dim ? __ldg(from + g + 8 * e) : make_uint4(0, 0, 0, 0);
+                    v[h][e] = in && (g + 8 * e) * 8 < a.dim ? load_once(from + g + 8 * e) : make_uint4(0, 0, 0, 0);
             }
         };
         auto word = [](const uint4 &x, int e) { return e == 0 ? x.x : e == 1 ? x.y : e == 2 ? x.z : x.w; };
@@ -2083,6 +2094,20 @@ int heads_map(HeadsMap *m, const Heads &h, int64_t tokens, int64_t heads, int64_
 
 constexpr uint64_t kWaitLimit = 4000000000u;
 
+// For tests: kernel test_short (0 the forward tiles, 1 dk and dv, 2 dq) asks
+// for boxes of queries eight rows too low, so that no tile of them is ever
+// whole and its waits run out after test_limit_ns.
+std::atomic<int32_t> test_short{-1};
+std::atomic<uint64_t> test_limit_ns{0};
+
+int short_by(int kernel, uint64_t *limit_ns)
+{
+    if (test_short.load(std::memory_order_relaxed) != kernel)
+        return 0;
+    *limit_ns = test_limit_ns.load(std::memory_order_relaxed);
+    return 8;
+}
+
 // Heads of up to 64 leave room in tensor memory for three CTAs of one tile of
 // queries each, whose turns hide one another's waits; wider ones for one CTA
 // of two tiles, whose products run while the other's weights are worked out.
@@ -2092,7 +2117,7 @@ using Wide = FwdShape<128, 2, 1>;
 template <int DT, class S>
 int launch_tiles(FwdTiles &t, const Fwd &f, const zero_attention_t *a, cudaStream_t st)
 {
-    ZERO_TRY(heads_map(&t.q, f.q, a->q_tokens, a->q_heads, a->head_dim, 128, a->dtype));
+    ZERO_TRY(heads_map(&t.q, f.q, a->q_tokens, a->q_heads, a->head_dim, 128 - short_by(0, &t.limit_ns), a->dtype));
     ZERO_TRY(heads_map(&t.k, f.k, a->k_tokens, a->k_heads, a->head_dim, S::BN, a->dtype));
     ZERO_TRY(heads_map(&t.v, f.v, a->k_tokens, a->k_heads, a->head_dim, S::BN, a->dtype));
     t.tiles = tile_numbers(a->q_tokens, a->sequences, !a->q_offsets, 128 * S::QT);
@@ -2126,7 +2151,7 @@ int forward_tiles(const Fwd &f, const zero_attention_t *a, void *ws, cudaStream_
 // Up to here, on average over the sequences, queries go a few rows at a time
 // over their keys instead of in tiles of 128.
 constexpr int64_t kFewQueries = 4;
-constexpr int kMostTickets = 4096, kMostSplits = 64;
+constexpr int kMostTickets = 2048, kMostSplits = 64;
 
 struct FewPlan {
     int groups;  // of 8 rows
@@ -2145,7 +2170,7 @@ FewPlan plan_few(const zero_attention_t *a, int64_t q_tokens, bool one)
     p.parts = (int32_t)(group > rows ? (group + rows - 1) / rows : 1);
     p.tiles = tile_numbers(q_tokens, a->sequences, one, p.tokens);
     p.sets = p.tiles * a->k_heads * p.parts;
-    // blocks of at least 64 keys, until there are 4096
+    // blocks of at least 64 keys, until there are 2048
     const int64_t rows_k = (a->k_tokens + n - 1) / n;
     int64_t keys = a->window < rows_k ? a->window + (a->sinks < rows_k ? a->sinks : rows_k) + p.tokens : rows_k;
     keys = keys < rows_k ? keys : rows_k;
@@ -2217,8 +2242,9 @@ AttnSpace attn_space(const zero_attention_t *a, bool backward)
 {
     AttnSpace s{};
     s.partial = s.stats = 256 + kMostTickets * 4;
-    // (a workspace for more queries serves fewer; sets x splits is at most
-    // 4096 more than sets, and none where there is one split)
+    // (a workspace for more queries serves fewer; where there is more than one
+    // split there are fewer than 2048 sets, and sets x splits is at most 2048
+    // more than sets)
     const int64_t most = kFewQueries * a->sequences, q = a->q_tokens < most ? a->q_tokens : most;
     size_t few = 0;
     for (int groups = 1; groups <= 2; ++groups) {
@@ -2275,9 +2301,10 @@ int launch_backward(BwdTiles &t, const BwdArrays &h, const zero_attention_t *a, 
         e = cudaLaunchKernelEx(&cfg, kernel, t);
     };
     // the maps: what a kernel keeps in boxes of 128 rows, what moves past it in boxes of BN
-    auto maps = [&](int q_rows, int k_rows) {
+    auto maps = [&](int kernel, int q_rows, int k_rows) {
+        t.limit_ns = kWaitLimit;
         if (a->q_tokens > 0) {
-            ZERO_TRY(heads_map(&t.q, h.q, a->q_tokens, a->q_heads, a->head_dim, q_rows, a->dtype));
+            ZERO_TRY(heads_map(&t.q, h.q, a->q_tokens, a->q_heads, a->head_dim, q_rows - short_by(kernel, &t.limit_ns), a->dtype));
             ZERO_TRY(heads_map(&t.dout, h.dout, a->q_tokens, a->q_heads, a->head_dim, q_rows, a->dtype));
         }
         if (a->k_tokens > 0) {
@@ -2290,13 +2317,12 @@ int launch_backward(BwdTiles &t, const BwdArrays &h, const zero_attention_t *a, 
             t.q = t.dout = t.k;
         return ZERO_OK;
     };
-    ZERO_TRY(maps(S::BN, 128));
+    ZERO_TRY(maps(1, S::BN, 128));
     const int64_t key_units = t.split_units + t.k_tiles * t.a.k_heads;
     launch(k_attn_dkv<DT, S>, key_units);
     if (e == cudaSuccess) {
         what = "k_attn_dq";
-        if (S::BN != 128)
-            ZERO_TRY(maps(128, S::BN));
+        ZERO_TRY(maps(2, 128, S::BN));
         t.after_dkv = key_units > 0;
         launch(k_attn_dq<DT, S>, t.q_tiles * t.a.q_heads);
     }
@@ -2318,6 +2344,14 @@ int launch_backward(BwdTiles &t, const BwdArrays &h, const zero_attention_t *a, 
 }  // namespace zpml
 
 using namespace zpml;
+
+// For tests, and so not in the header: see test_short.  kernel -1: none (the
+// default).
+extern "C" void zero_test_window_attention_waits(int32_t kernel, uint64_t limit_ns)
+{
+    test_short = kernel;
+    test_limit_ns = limit_ns;
+}
 
 extern "C" size_t zero_window_attention_workspace_bytes(const zero_attention_t *a, int32_t backward)
 {
@@ -2380,7 +2414,6 @@ extern "C" int zero_window_attention_backward(const zero_attention_t *a, const v
     t.scale = (float)a->scale;
     t.scale_log2 = (float)(a->scale * 1.4426950408889634);
     t.hdr = static_cast<WsHeader *>(ws);
-    t.limit_ns = kWaitLimit;
     if (a->q_tokens > 0) {
         const SinkPlan p = plan_sinks(a, one);
         t.chunk = p.chunk, t.sink_tiles = p.sink_tiles, t.chunks = p.chunks, t.split_units = p.units;
