@@ -733,7 +733,8 @@ int zero_gated_ffn_backward(const void *dy, int64_t dy_ld, const void *x, int64_
  * contiguous, from one token to the next `ld` elements and from one head to
  * the next `hd` (both at least 0, or any value where there is one token, or
  * one head).  So q, k and v can be slices of one projection's output, in
- * either order of its axes.  Rows of an output must not overlap. */
+ * either order of its axes.  Rows of an output must not overlap, and outputs
+ * overlap inputs only where a call names the exception. */
 
 /* The rotation of the first rot_dim elements of a head (rot_dim even, 0 for
  * none): pair i, of elements i and i + rot_dim / 2, or 2 i and 2 i + 1 when

@@ -523,6 +523,23 @@ def test_window_attention_head_dims(zp, dim):
     Batch([(1, 200), (1, 30)], 4, 2, dim, "f16").check_forward(zp, 90, 2)
 
 
+# up to eight queries for each sequence on average: sets of 8 and of 16 rows
+# of queries and heads, windows shorter than the queries, queries without keys,
+# and so many blocks that two of them fall to a lane of the join
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("case", [
+    ([(8, 700), (5, 5), (6, 1), (7, 40)], 4, 4, 64, None, 0),
+    ([(8, 700), (8, 300)], 8, 2, 128, 3, 2),
+    ([(8, 9), (8, 3), (8, 8)], 16, 1, 64, 4, 0),
+    ([(6, 2000), (7, 65)], 24, 1, 128, 1500, 5),
+    ([(5, 30000)], 5, 1, 32, None, 0),
+    ([(16, 500), (0, 20), (8, 8)], 3, 1, 80, 100, 130),
+], ids=ids)
+def test_window_attention_of_up_to_eight_queries(zp, case, dtype):
+    lens, h, g, d, window, sinks = case
+    Batch(lens, h, g, d, dtype, room=3, behind=2).check_forward(zp, window, sinks)
+
+
 def test_window_attention_rows_before_the_first_sequence(zp):
     """Offsets that start behind the first rows: those are left as they were."""
     for n in (1, 200):

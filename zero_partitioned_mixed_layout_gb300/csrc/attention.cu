@@ -1,5 +1,20 @@
 // Attention with a sliding window and a few first keys that stay visible,
 // forward and backward, over packed sequences and caches.
+//
+// Query i of a sequence stands at key p = i + Lk - Lq and sees key j iff
+// 0 <= j <= p and (j > p - window or j < sinks).  Over the keys that it sees
+//     s_ij = scale q_i.k_j,  lse_i = log sum_j exp s_ij,  o_i = sum_j exp(s_ij - lse_i) v_j,
+// in one pass: with a reference m (about the largest score so far),
+// l = sum exp(s - m) and O = sum exp(s - m) v, and both times
+// exp(m - m') when the reference moves to m'; o = O / l, lse = m + log l.
+// Scores, l and O are binary32.  exp(s - m) is rounded to 16 bits once, as
+// the second product's operand: by at most half a step (2^-8 in bf16, 2^-11
+// in f16) of each weight, as much as the output itself is rounded by; l adds
+// up the weights as they were before.
+//
+// Three ways: tiles of 128 queries on the tensor cores (k_attn_tiles), a few
+// queries per sequence (k_attn_few), and the backward pass (k_attn_stats,
+// k_attn_dkv, k_attn_dq, k_attn_join).
 #include <atomic>
 #include <cmath>
 #include <initializer_list>
@@ -290,7 +305,7 @@ struct FwdShared {
     uint32_t tmem, gave_up;
 };
 
-// 32 rows of 32 or 64 elements of one warp, a row per lane, through 2 or 4 KB
+// 32 rows of 32 or 64 elements (16 or 32 words) of one warp, a row per lane, through 2 or 4 KB
 // of shared memory (16-byte pieces XORed by the row, so that neither way has
 // bank conflicts) to rows of memory `ld` elements apart, whole rows at a time.
 // Rows from `rows` and elements from `cols` on are not written.
@@ -318,6 +333,18 @@ __device__ __forceinline__ void store_rows(uint4 *stage, int lane, const uint32_
 // loads, one issues the products, and the others hold a row of the scores per
 // thread: their largest, the weights (which take the scores' place in tensor
 // memory, as the first operand of the product with the values) and their sum.
+//
+// What bounds it: of 128 x 128 scores the tensor pipe takes 8 clocks per
+// element of a head (1024 at 128), the exponentials 512, and the other
+// instructions of a row's thread (scores to registers, largest, sum, packing,
+// weights back) about as many issue slots again on each of the four
+// schedulers, so at 128 elements both pipes have to run without a pause.  With
+// one tile per CTA they wait for one another; two tiles take turns.  Measured:
+// 16384 tokens of 64 + 8 heads of 128, window 2048: 769 us, 1.38 PFLOP/s, 0.72
+// of cuBLAS's burst rate (the same loads and products without the softmax
+// between them: 598).  8 x 1024 tokens of 25 heads of 64, window 256: 51 us;
+// there a tile of scores is 512 clocks of the tensor pipe, and the masked
+// edges of a window of two tiles are worked out in full.
 template <int DT, class S>
 __global__ void __launch_bounds__(S::THREADS, S::PER_SM) k_attn_tiles(const __grid_constant__ FwdTiles f)
 {
@@ -730,6 +757,15 @@ __global__ void __launch_bounds__(S::THREADS, S::PER_SM) k_attn_tiles(const __gr
 // would be 128 rows of which 120 are empty), and keys and values go from
 // memory to registers in the operands' layout, 16 bytes per lane, without
 // shared memory between: S' = K Q^T has keys for rows, O' = V^T P' elements.
+// A set of rows is split over its keys among blocks; each leaves sums, a
+// reference and the weights' sum, and the last to come joins them in order.
+//
+// What bounds it: the keys' and values' bytes.  64 requests of up to 8192 keys
+// of 8 heads of 128 (0.92 GB): 165 us, 5.6 TB/s; 64 of 4096: 180, 5.9; 64 of
+// 4096 keys of 25 heads of 64 (1.68 GB): 283, 5.9.  Alone a request is a few
+// trips to memory: 7.5 us over 256 keys of 25 heads of 64, 11 over 4096.  Groups
+// of 8 heads' rows one at a time (NG = 1 throughout) read keys twice through
+// L2: 64 requests of 64 + 4 heads 167 us against 152.
 struct FewArgs {
     Attn a;
     Heads q, k, v, out;
@@ -738,10 +774,11 @@ struct FewArgs {
     int32_t tokens, parts, splits;  // parts: sets of rows of one query's heads
     float scale_log2;
     uint32_t *tickets;           // one per set of rows, where splits > 1
-    float *partial;              // [set of rows][split][row][dim + 2]: the sums, the reference, the weights' sum
+    float *partial;              // [set of rows][split]: [row][dim] sums, [row] references, [row] the weights' sums
 };
 
 constexpr int kFewWarps = 4;
+constexpr int kMostTickets = 2048, kMostSplits = 64;
 
 // Read once: not kept in L1.
 __device__ __forceinline__ uint4 load_once(const uint4 *p)
@@ -782,7 +819,9 @@ __global__ void __launch_bounds__(kFewWarps * 32) k_attn_few(const __grid_consta
 {
     constexpr int R = 8 * NG, KK = DP / 32, JJ = DP / 64;
     constexpr bool kBf16 = DT == ZERO_BF16;
-    __shared__ float s_o[kFewWarps][R][DP], s_m[kFewWarps][R], s_l[kFewWarps][R];
+    __shared__ __align__(16) float s_o[kFewWarps][R][DP];
+    __shared__ float s_m[kFewWarps][R], s_l[kFewWarps][R];
+    __shared__ uint4 s_q[NG][KK][32];  // the queries, as the lanes' operands
     __shared__ uint32_t s_last;
     const Attn &a = f.a;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
@@ -805,7 +844,7 @@ __global__ void __launch_bounds__(kFewWarps * 32) k_attn_few(const __grid_consta
     const int32_t used = n > 0 ? (n + per - 1) / per : 1;  // blocks with keys (the first writes where there are none)
 
     if (split < used) {
-        uint4 q[NG][KK], k[2][KK], v[4][JJ];
+        uint4 k[2][KK], v[4][JJ];
         int32_t p[NG][2];
 #pragma unroll
         for (int i = 0; i < NG; ++i) {
@@ -813,9 +852,8 @@ __global__ void __launch_bounds__(kFewWarps * 32) k_attn_few(const __grid_consta
             const bool live = 8 * i + g < rows;
             const uint16_t *from = static_cast<const uint16_t *>(f.q.p) + (at.s.q0 + at.first + (live ? r / a.group : 0)) * f.q.ld +
                                    (kh * a.group + (live ? r % a.group : 0)) * f.q.hd;
-#pragma unroll
-            for (int e = 0; e < KK; ++e)
-                q[i][e] = live && (c + 4 * e) * 8 < a.dim ? __ldg(reinterpret_cast<const uint4 *>(from) + c + 4 * e) : make_uint4(0, 0, 0, 0);
+            for (int e = warp; e < KK; e += kFewWarps)
+                s_q[i][e][lane] = live && (c + 4 * e) * 8 < a.dim ? __ldg(reinterpret_cast<const uint4 *>(from) + c + 4 * e) : make_uint4(0, 0, 0, 0);
 #pragma unroll
             for (int e = 0; e < 2; ++e)
                 p[i][e] = p0 + (row0 + 8 * i + 2 * c + e) / a.group;
@@ -855,16 +893,19 @@ __global__ void __launch_bounds__(kFewWarps * 32) k_attn_few(const __grid_consta
             load_k(x);
             load_v(x);
         }
+        __syncthreads();
         for (; x < x1; x += 16 * kFewWarps) {
             float t[NG][4] = {};
 #pragma unroll
             for (int e = 0; e < KK; ++e)
 #pragma unroll
-                for (int h = 0; h < 2; ++h)
+                for (int i = 0; i < NG; ++i) {
+                    const uint4 q = s_q[i][e][lane];
 #pragma unroll
-                    for (int i = 0; i < NG; ++i)
+                    for (int h = 0; h < 2; ++h)
                         mma16(t[i], word(k[0][e], 2 * h), word(k[1][e], 2 * h), word(k[0][e], 2 * h + 1),
-                              word(k[1][e], 2 * h + 1), word(q[i][e], 2 * h), word(q[i][e], 2 * h + 1), kBf16);
+                              word(k[1][e], 2 * h + 1), word(q, 2 * h), word(q, 2 * h + 1), kBf16);
+                }
             const int32_t x_next = x + 16 * kFewWarps;
             if (x_next < x1)
                 load_k(x_next);
@@ -959,21 +1000,28 @@ __global__ void __launch_bounds__(kFewWarps * 32) k_attn_few(const __grid_consta
     }
     __syncthreads();
 
-    // rows of a set are finished, or joined, element by element
-    auto finish = [&](int32_t r, int32_t e, float sum, float m, float l) {
+    // four elements of a row are finished at a time
+    auto finish = [&](int32_t r, int32_t e, float4 sum, float m, float l) {
         const int32_t rr = row0 + r;
         const int64_t row = at.s.q0 + at.first + rr / a.group;
         const int32_t head = kh * a.group + rr % a.group;
-        store1<DT>(const_cast<void *>(f.out.p), row * f.out.ld + head * f.out.hd + e, l == 0.0f ? 0.0f : sum / l);
+        uint2 w = make_uint2(0, 0);
+        if (l != 0.0f)
+            w = make_uint2(pack2<DT>(sum.x / l, sum.y / l), pack2<DT>(sum.z / l, sum.w / l));
+        *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(const_cast<void *>(f.out.p)) + row * f.out.ld + head * f.out.hd + e) = w;
         if (e == 0 && f.lse)
             f.lse[(int64_t)head * a.q_tokens + row] = l == 0.0f ? -INFINITY : m * a.scale + logf(l);
     };
-    const int32_t wide = a.dim + 2;
-    float *const mine = f.partial + (set * f.splits + split) * R * wide;
+    auto add = [](float4 &sum, float4 x, float by) {
+        sum.x += x.x * by, sum.y += x.y * by, sum.z += x.z * by, sum.w += x.w * by;
+    };
+    const int32_t fours = a.dim / 4, part_floats = R * (a.dim + 2);  // of a block: its sums, references and weights' sums
+    float *const mine = f.partial + (set * f.splits + split) * part_floats;
     if (split < used)
-        for (int32_t i = threadIdx.x; i < rows * a.dim; i += kFewWarps * 32) {
-            const int32_t r = i / a.dim, e = i - r * a.dim;
-            float m = s_m[0][r], sum = 0.0f, l = 0.0f;
+        for (int32_t i = threadIdx.x; i < rows * fours; i += kFewWarps * 32) {
+            const int32_t r = i / fours, e = 4 * (i - r * fours);
+            float m = s_m[0][r], l = 0.0f;
+            float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
             for (int w = 1; w < kFewWarps; ++w)
                 m = fmaxf(m, s_m[w][r]);
@@ -981,17 +1029,17 @@ __global__ void __launch_bounds__(kFewWarps * 32) k_attn_few(const __grid_consta
             for (int w = 0; w < kFewWarps; ++w) {
                 const float by = s_m[w][r] == -INFINITY ? 0.0f : exp2_fast((s_m[w][r] - m) * f.scale_log2);
                 if (s_m[w][r] != -INFINITY || s_l[w][r] != 0.0f) {
-                    sum += s_o[w][r][e] * by;
+                    add(sum, *reinterpret_cast<const float4 *>(&s_o[w][r][e]), by);
                     l += s_l[w][r] * by;
                 }
             }
             if (used == 1) {
                 finish(r, e, sum, m, l);
             } else {
-                mine[r * wide + e] = sum;
+                *reinterpret_cast<float4 *>(mine + r * a.dim + e) = sum;
                 if (e == 0) {
-                    mine[r * wide + a.dim] = m;
-                    mine[r * wide + a.dim + 1] = l;
+                    mine[R * a.dim + r] = m;
+                    mine[R * a.dim + R + r] = l;
                 }
             }
         }
@@ -1006,24 +1054,44 @@ __global__ void __launch_bounds__(kFewWarps * 32) k_attn_few(const __grid_consta
     if (!s_last)
         return;
     __threadfence();
-    const float *const all = f.partial + set * f.splits * R * wide;
-    for (int32_t i = threadIdx.x; i < rows * a.dim; i += kFewWarps * 32) {
-        const int32_t r = i / a.dim, e = i - r * a.dim;
-        float m = -INFINITY, sum = 0.0f, l = 0.0f;
+    const float *const all = f.partial + set * f.splits * part_floats;
+    // what each block's sums are multiplied by, a block to a lane
+    float (*const s_by)[kMostSplits] = reinterpret_cast<float (*)[kMostSplits]>(&s_o[0][0][0]);
+    static_assert(kMostSplits == 64 && sizeof(s_o) >= R * kMostSplits * 4, "two blocks to a lane, in the sums' place");
+    for (int32_t r = warp; r < rows; r += kFewWarps) {
+        float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+            if (lane + 32 * h < used) {
+                const float *const from = all + (lane + 32 * h) * part_floats + R * a.dim + r;
+                m[h] = __ldcg(from);
+                l[h] = __ldcg(from + R);
+            }
+        float top = fmaxf(m[0], m[1]), sum = 0.0f;
+#pragma unroll
+        for (int b = 16; b > 0; b >>= 1)
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, b));
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const float by = m[h] == -INFINITY ? 0.0f : exp2_fast((m[h] - top) * f.scale_log2);
+            s_by[r][lane + 32 * h] = by;
+            sum += l[h] * by;
+        }
+#pragma unroll
+        for (int b = 16; b > 0; b >>= 1)
+            sum += __shfl_xor_sync(0xffffffffu, sum, b);
+        if (lane == 0)
+            s_m[0][r] = top, s_l[0][r] = sum;
+    }
+    __syncthreads();
+    for (int32_t i = threadIdx.x; i < rows * fours; i += kFewWarps * 32) {
+        const int32_t r = i / fours, e = 4 * (i - r * fours);
+        float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        const float *const from = all + r * a.dim + e;
 #pragma unroll 8
         for (int32_t w = 0; w < used; ++w)
-            m = fmaxf(m, __ldcg(all + (w * R + r) * wide + a.dim));
-#pragma unroll 4
-        for (int32_t w = 0; w < used; ++w) {
-            const float *const from = all + (w * R + r) * wide;
-            const float mw = __ldcg(from + a.dim), lw = __ldcg(from + a.dim + 1), ow = __ldcg(from + e);
-            const float by = mw == -INFINITY ? 0.0f : exp2_fast((mw - m) * f.scale_log2);
-            if (lw != 0.0f) {
-                sum += ow * by;
-                l += lw * by;
-            }
-        }
-        finish(r, e, sum, m, l);
+            add(sum, __ldcg(reinterpret_cast<const float4 *>(from + w * part_floats)), s_by[r][w]);
+        finish(r, e, sum, s_m[0][r], s_l[0][r]);
     }
     if (threadIdx.x == 0)
         f.tickets[set] = 0;
@@ -1044,7 +1112,8 @@ struct StatsArgs {
 };
 
 // A warp takes 32 queries of a tile and the heads of its block: lse by one
-// lane per query, dout and out by 2 to 16 lanes to a row.
+// lane per query, dout and out by 2 to 16 lanes to a row.  Bound by the two
+// arrays' bytes: 5340 tokens of 25 heads of 64, 34 MB: 5 us (they are in L2).
 template <int DT, int L>
 __global__ void __launch_bounds__(128) k_attn_stats(const __grid_constant__ StatsArgs f)
 {
@@ -1099,7 +1168,7 @@ struct BwdTiles {
     int64_t q_tiles, k_tiles;  // tile numbers of 128 queries, and keys
     // first keys seen by all queries: their tiles' queries in parts of `chunk` tiles
     int32_t chunk, sink_tiles;
-    int64_t chunks, split_units;
+    int64_t split_units;
     float *partial;  // [split unit][dv, dk][128][dim]
     float scale, scale_log2;
     int32_t after_dkv;  // (dq: k_attn_dkv is launched before it)
@@ -1215,6 +1284,16 @@ __device__ __forceinline__ bool key_unit(const BwdTiles &f, int64_t i, int lane,
 // which the two running products take from tensor memory, have a key per lane:
 //     S' = K Q^T, P' = exp(S' - lse), dP' = V dO^T, dS' = P' (dP' - delta),
 //     dV += P' dO, dK += dS' Q.
+// P' and dS' are rounded to 16 bits once, as the products' operands; P' goes on
+// into dS' unrounded.  Rows of statistics come with the queries' tiles, so a
+// tile needs no reduction and no running maximum.
+//
+// What bounds it: four products, 4096 clocks of the tensor pipe for 128 x 128
+// pairs at 128 elements, and a chain of products and elementwise work that one
+// pair of buffers in tensor memory (two tiles of scores and two sums of
+// 128 x 128 are all of its 512 columns) lets overlap only by halves: 16384
+// tokens of 64 + 8 heads of 128, window 2048: about 1.28 of the pass's 2.77 ms.
+// Heads of 64: tiles of 64 queries, two CTAs per SM.
 template <int DT, class S>
 __global__ void __launch_bounds__(S::THREADS, S::PER_SM) k_attn_dkv(const __grid_constant__ BwdTiles f)
 {
@@ -1604,7 +1683,8 @@ __global__ void __launch_bounds__(S::THREADS, S::PER_SM) k_attn_dkv(const __grid
 }
 
 // The sums of the first keys' tiles from their parts, in order: a block takes
-// every gridDim.y-th eight keys of a tile's key heads.
+// every gridDim.y-th eight keys of a tile's key heads.  A few us: its bytes
+// are 1 KB for each key, element and 8 or more tiles of queries.
 template <int DT>
 __global__ void __launch_bounds__(kThreads) k_attn_join(const __grid_constant__ BwdTiles f)
 {
@@ -1658,6 +1738,12 @@ struct QueryShared {
 // see: S = Q K^T, dP = dO V^T, dS = exp(S - lse) (dP - delta), dQ += dS K.
 // (S and dP are worked out here again, two products of seven, so that dq is
 // summed in one place and in one order, without atomics.)
+//
+// What bounds it: three products, 3072 clocks of the tensor pipe at 128
+// elements, against 64 KB of keys and values, 21 B per clock and SM, which L2
+// gives at no more than 7.7 TB/s to all SMs: about 1.45 of the 2.77 ms above.
+// A window's queries of one key head's group read the same keys at about the
+// same time, so DRAM does not bound it.
 template <int DT, class S>
 __global__ void __launch_bounds__(S::THREADS, S::PER_SM) k_attn_dq(const __grid_constant__ BwdTiles f)
 {
@@ -2018,7 +2104,7 @@ int check_attention(const zero_attention_t *a)
 }
 
 // The arrays of lengths: checked by a call, not by the workspace's size.
-int check_offsets(const zero_attention_t *a)
+int check_offsets(const zero_attention_t *a, Reach *reach)
 {
     if ((a->k_lengths && !a->k_offsets) || (!a->q_offsets && a->sequences != 1))
         return ZERO_EINVAL;
@@ -2029,18 +2115,18 @@ int check_offsets(const zero_attention_t *a)
             continue;
         if ((reinterpret_cast<uintptr_t>(p) & 7u) != 0)
             return ZERO_EALIGN;
-        if (!device_ptr(p))
+        if (!reach->has(p))
             return ZERO_EINVAL;
     }
     return ZERO_OK;
 }
 
 // An array of heads whose rows are whole 16 bytes.
-int check_rows(Heads *h, int64_t tokens, int64_t heads, int64_t dim, int32_t dtype)
+int check_rows(Heads *h, int64_t tokens, int64_t heads, int64_t dim, int32_t dtype, Reach *reach)
 {
     if (tokens == 0)
         return ZERO_OK;
-    ZERO_TRY(check_heads(h, tokens, heads, dim, dtype));
+    ZERO_TRY(check_heads(h, tokens, heads, dim, dtype, reach));
     if ((tokens > 1 && h->ld == 0) || (heads > 1 && h->hd == 0))
         return ZERO_EINVAL;
     return aligned16(h->p) && ((h->ld | h->hd) & 7) == 0 ? ZERO_OK : ZERO_EALIGN;
@@ -2108,9 +2194,10 @@ int short_by(int kernel, uint64_t *limit_ns)
     return 8;
 }
 
-// Heads of up to 64 leave room in tensor memory for three CTAs of one tile of
-// queries each, whose turns hide one another's waits; wider ones for one CTA
-// of two tiles, whose products run while the other's weights are worked out.
+// Heads of up to 64 leave room for two CTAs of one tile of queries each, which
+// start and end apart from one another; wider ones for one CTA of two tiles,
+// whose products run while the other's weights are worked out.  At 16 heads of
+// 64 (narrow, wide): 8 x 1024 tokens 46, 48 us; 64 x 100 19, 36; 8192 187, 201.
 using Narrow = FwdShape<64, 1, 2>;
 using Wide = FwdShape<128, 2, 1>;
 
@@ -2149,9 +2236,11 @@ int forward_tiles(const Fwd &f, const zero_attention_t *a, void *ws, cudaStream_
 }
 
 // Up to here, on average over the sequences, queries go a few rows at a time
-// over their keys instead of in tiles of 128.
-constexpr int64_t kFewQueries = 4;
-constexpr int kMostTickets = 2048, kMostSplits = 64;
+// over their keys instead of in tiles of 128.  Both ways, 4096 keys, us (few |
+// tiles of 128) for 1, 4, 8, 16 queries: one sequence of 32 + 8 heads of 128 11,
+// 18, 21, 33 | 47; 64 of them 180, 282, 473, 816 | 605 to 613; one of 25 + 25
+// heads of 64 11, 12, 13, 17 | 41, 64 of them 283, 312, 314, 451 | 264 to 282.
+constexpr int64_t kFewQueries = 8;
 
 struct FewPlan {
     int groups;  // of 8 rows
@@ -2170,13 +2259,18 @@ FewPlan plan_few(const zero_attention_t *a, int64_t q_tokens, bool one)
     p.parts = (int32_t)(group > rows ? (group + rows - 1) / rows : 1);
     p.tiles = tile_numbers(q_tokens, a->sequences, one, p.tokens);
     p.sets = p.tiles * a->k_heads * p.parts;
-    // blocks of at least 64 keys, until there are 2048
+    // Blocks of at least 64 keys, until there are 2048 of them, and no more to
+    // a set than its join is worth: a block's keys take it longer in
+    // proportion, the last block's join in proportion to the blocks, and with
+    // sqrt(keys / 16) blocks of 4 sqrt(keys) keys the two are about equal.
     const int64_t rows_k = (a->k_tokens + n - 1) / n;
     int64_t keys = a->window < rows_k ? a->window + (a->sinks < rows_k ? a->sinks : rows_k) + p.tokens : rows_k;
     keys = keys < rows_k ? keys : rows_k;
     int64_t splits = p.sets > 0 ? (kMostTickets + p.sets - 1) / p.sets : 1;
     const int64_t most = (keys + 63) / 64 < kMostSplits ? (keys + 63) / 64 : kMostSplits;
     splits = splits < most ? splits : most;
+    const int64_t worth = (int64_t)std::sqrt((double)keys / 16);
+    splits = splits < worth ? splits : worth;
     p.splits = (int32_t)(splits > 1 ? splits : 1);
     return p;
 }
@@ -2206,10 +2300,12 @@ int forward_few(const Fwd &f, const zero_attention_t *a, void *ws, size_t partia
 
 // Whether first keys' tiles are dealt out, in parts of how many query tiles:
 // about what a tile of the window's keys has to do.  (Of more than 1024 first
-// keys every tile sees so much that there is enough to go round.)
+// keys every tile sees so much that there is enough to go round.)  Measured,
+// window 1024, 4 first keys, 32 + 8 heads of 128, dealt out or not: 16384
+// tokens 882, 1572 us; 2 x 16384 1701, 2440; 4 x 4096 794, 897.
 struct SinkPlan {
     int32_t chunk, sink_tiles;
-    int64_t chunks, units;
+    int64_t units;
 };
 
 SinkPlan plan_sinks(const zero_attention_t *a, bool one)
@@ -2224,8 +2320,7 @@ SinkPlan plan_sinks(const zero_attention_t *a, bool one)
     p.chunk = (int32_t)chunk;
     const int64_t keys = a->sinks < a->k_tokens ? a->sinks : a->k_tokens;
     p.sink_tiles = (int32_t)((keys + 127) / 128);
-    p.chunks = tile_numbers(a->q_tokens, a->sequences, one, 128 * p.chunk);
-    p.units = p.chunks * p.sink_tiles * a->k_heads;
+    p.units = tile_numbers(a->q_tokens, a->sequences, one, 128 * p.chunk) * p.sink_tiles * a->k_heads;
     return p;
 }
 
@@ -2268,7 +2363,9 @@ AttnSpace attn_space(const zero_attention_t *a, bool backward)
     return s;
 }
 
-// (As forward: heads of up to 64 leave room for two CTAs with smaller tiles.)
+// As forward: heads of up to 64 leave room for two CTAs, with smaller tiles.
+// At 16 heads of 64 (narrow, wide): 8 x 1024 tokens 111, 136 us; 64 x 100 53,
+// 69; 8192 419, 465.
 using NarrowBwd = BwdShape<64, 64, 2>;
 using WideBwd = BwdShape<128, 128, 1>;
 
@@ -2364,15 +2461,16 @@ extern "C" int zero_window_attention(const zero_attention_t *a, const void *q, i
                                      size_t ws_bytes, void *stream)
 {
     ZERO_TRY(check_attention(a));
-    ZERO_TRY(check_offsets(a));
+    Reach reach;
+    ZERO_TRY(check_offsets(a, &reach));
     Fwd f{attn_of(a), {q, q_ld, q_hd}, {k, k_ld, k_hd}, {v, v_ld, v_hd}, {out, out_ld, out_hd}, lse};
-    ZERO_TRY(check_rows(&f.q, a->q_tokens, a->q_heads, a->head_dim, a->dtype));
-    ZERO_TRY(check_rows(&f.k, a->k_tokens, a->k_heads, a->head_dim, a->dtype));
-    ZERO_TRY(check_rows(&f.v, a->k_tokens, a->k_heads, a->head_dim, a->dtype));
-    ZERO_TRY(check_rows(&f.out, a->q_tokens, a->q_heads, a->head_dim, a->dtype));
+    ZERO_TRY(check_rows(&f.q, a->q_tokens, a->q_heads, a->head_dim, a->dtype, &reach));
+    ZERO_TRY(check_rows(&f.k, a->k_tokens, a->k_heads, a->head_dim, a->dtype, &reach));
+    ZERO_TRY(check_rows(&f.v, a->k_tokens, a->k_heads, a->head_dim, a->dtype, &reach));
+    ZERO_TRY(check_rows(&f.out, a->q_tokens, a->q_heads, a->head_dim, a->dtype, &reach));
     if (lse)
-        ZERO_TRY(check_array(lse, a->q_tokens, ZERO_F32));
-    ZERO_TRY(check_workspace(ws, ws_bytes, attn_space(a, false).total));
+        ZERO_TRY(check_array(lse, a->q_tokens, ZERO_F32, &reach));
+    ZERO_TRY(check_workspace(ws, ws_bytes, attn_space(a, false).total, &reach));
     if (a->q_tokens == 0 || a->sequences == 0)
         return ZERO_OK;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
@@ -2390,16 +2488,17 @@ extern "C" int zero_window_attention_backward(const zero_attention_t *a, const v
                                               void *ws, size_t ws_bytes, void *stream)
 {
     ZERO_TRY(check_attention(a));
-    ZERO_TRY(check_offsets(a));
+    Reach reach;
+    ZERO_TRY(check_offsets(a, &reach));
     Heads hdout{dout, dout_ld, dout_hd}, hq{q, q_ld, q_hd}, hk{k, k_ld, k_hd}, hv{v, v_ld, v_hd}, hout{out, out_ld, out_hd};
     Heads hdq{dq, dq_ld, dq_hd}, hdk{dk, dk_ld, dk_hd}, hdv{dv, dv_ld, dv_hd};
     for (Heads *h : {&hdout, &hq, &hout, &hdq})
-        ZERO_TRY(check_rows(h, a->q_tokens, a->q_heads, a->head_dim, a->dtype));
+        ZERO_TRY(check_rows(h, a->q_tokens, a->q_heads, a->head_dim, a->dtype, &reach));
     for (Heads *h : {&hk, &hv, &hdk, &hdv})
-        ZERO_TRY(check_rows(h, a->k_tokens, a->k_heads, a->head_dim, a->dtype));
-    ZERO_TRY(check_array(lse, a->q_tokens, ZERO_F32));
+        ZERO_TRY(check_rows(h, a->k_tokens, a->k_heads, a->head_dim, a->dtype, &reach));
+    ZERO_TRY(check_array(lse, a->q_tokens, ZERO_F32, &reach));
     const AttnSpace sp = attn_space(a, true);
-    ZERO_TRY(check_workspace(ws, ws_bytes, sp.total));
+    ZERO_TRY(check_workspace(ws, ws_bytes, sp.total, &reach));
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     if (a->sequences == 0 || (a->q_tokens == 0 && a->k_tokens == 0))
         return ZERO_OK;
@@ -2416,7 +2515,7 @@ extern "C" int zero_window_attention_backward(const zero_attention_t *a, const v
     t.hdr = static_cast<WsHeader *>(ws);
     if (a->q_tokens > 0) {
         const SinkPlan p = plan_sinks(a, one);
-        t.chunk = p.chunk, t.sink_tiles = p.sink_tiles, t.chunks = p.chunks, t.split_units = p.units;
+        t.chunk = p.chunk, t.sink_tiles = p.sink_tiles, t.split_units = p.units;
         const StatsArgs s{t.a, hdout, hout, lse, const_cast<float *>(t.stats), t.q_tiles};
         const bool f16 = a->dtype == ZERO_F16;
         auto kernel = a->head_dim <= 16   ? f16 ? k_attn_stats<ZERO_F16, 2> : k_attn_stats<ZERO_BF16, 2>

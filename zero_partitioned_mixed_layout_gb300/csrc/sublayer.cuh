@@ -3,6 +3,8 @@
 // checks of row-strided matrices and of arrays of heads.
 #pragma once
 
+#include <cuda.h>
+
 #include "common.cuh"
 
 // Returns the code of a check or a launch that is not ZERO_OK.
@@ -110,9 +112,58 @@ __device__ __forceinline__ uint32_t fast_div(uint32_t n, FastDiv f)
 
 inline int elem_bytes(int32_t dt) { return dt == ZERO_F32 ? 4 : 2; }
 
+// The device memory that one call's pointers lie in.  The arrays of a call
+// are often slices of one allocation, and the driver takes 0.4 us to say
+// what a pointer is, so it is asked for the allocation too, and not again
+// for what lies in it.  (Of no longer life than the call.)
+class Reach {
+public:
+    bool has(const void *p)
+    {
+        const uintptr_t x = reinterpret_cast<uintptr_t>(p);
+        for (int i = 0; i < kRanges; ++i)
+            if (x - from_[i] < size_[i])
+                return true;
+        void *from = nullptr;
+        size_t size = 0;
+        unsigned type = 0;
+        CUpointer_attribute what[3] = {CU_POINTER_ATTRIBUTE_MEMORY_TYPE, CU_POINTER_ATTRIBUTE_RANGE_START_ADDR,
+                                       CU_POINTER_ATTRIBUTE_RANGE_SIZE};
+        void *to[3] = {&type, &from, &size};
+        const Query query = driver();
+        if (!query || query(3, what, to, (CUdeviceptr)x) != CUDA_SUCCESS || type != CU_MEMORYTYPE_DEVICE ||
+            x - reinterpret_cast<uintptr_t>(from) >= size)
+            return device_ptr(p);
+        from_[next_] = reinterpret_cast<uintptr_t>(from), size_[next_] = size;
+        next_ = (next_ + 1) % kRanges;
+        return true;
+    }
+
+private:
+    using Query = CUresult (*)(unsigned, CUpointer_attribute *, void **, CUdeviceptr);
+    static Query driver()
+    {
+        static Query fn = [] {
+            void *p = nullptr;
+            cudaDriverEntryPointQueryResult found = cudaDriverEntryPointSymbolNotFound;
+            if (cudaGetDriverEntryPointByVersion("cuPointerGetAttributes", &p, 12000, cudaEnableDefault, &found) !=
+                    cudaSuccess ||
+                found != cudaDriverEntryPointSuccess) {
+                cudaGetLastError();
+                p = nullptr;
+            }
+            return reinterpret_cast<Query>(p);
+        }();
+        return fn;
+    }
+    static constexpr int kRanges = 4;
+    uintptr_t from_[kRanges] = {}, size_[kRanges] = {};
+    int next_ = 0;
+};
+
 // Checks of one array that a call reads or writes: n elements from p on
 // (none if n == 0), element-aligned, in device memory.
-inline int check_array(const void *p, int64_t n, int32_t dt)
+inline int check_array(const void *p, int64_t n, int32_t dt, Reach *reach = nullptr)
 {
     if (n == 0)
         return ZERO_OK;
@@ -120,7 +171,7 @@ inline int check_array(const void *p, int64_t n, int32_t dt)
         return ZERO_EINVAL;
     if ((reinterpret_cast<uintptr_t>(p) & (uintptr_t)(elem_bytes(dt) - 1)) != 0)
         return ZERO_EALIGN;
-    return device_ptr(p) ? ZERO_OK : ZERO_EINVAL;
+    return (reach ? reach->has(p) : device_ptr(p)) ? ZERO_OK : ZERO_EINVAL;
 }
 
 // Checks of a rows x cols matrix with row stride ld.
@@ -141,7 +192,7 @@ struct Heads {
 };
 
 // Checks of one; the strides that no two rows need become 0.
-inline int check_heads(Heads *a, int64_t tokens, int64_t heads, int64_t dim, int32_t dt)
+inline int check_heads(Heads *a, int64_t tokens, int64_t heads, int64_t dim, int32_t dt, Reach *reach)
 {
     if (tokens == 0 || heads == 0 || dim == 0)
         return ZERO_OK;
@@ -155,10 +206,10 @@ inline int check_heads(Heads *a, int64_t tokens, int64_t heads, int64_t dim, int
     const int64_t most = (int64_t)1 << 38, all = (int64_t)1 << 60;
     if (a->ld >= most || a->hd >= most || a->ld > all / tokens || a->hd > all / heads)
         return ZERO_ESIZE;
-    return check_array(a->p, 1, dt);
+    return check_array(a->p, 1, dt, reach);
 }
 
-inline int check_workspace(const void *ws, size_t ws_bytes, size_t need)
+inline int check_workspace(const void *ws, size_t ws_bytes, size_t need, Reach *reach = nullptr)
 {
     if (!ws)
         return ZERO_EWORKSPACE;
@@ -166,7 +217,7 @@ inline int check_workspace(const void *ws, size_t ws_bytes, size_t need)
         return ZERO_EALIGN;
     if (ws_bytes < need)
         return ZERO_EWORKSPACE;
-    return device_ptr(ws) ? ZERO_OK : ZERO_EINVAL;
+    return (reach ? reach->has(ws) : device_ptr(ws)) ? ZERO_OK : ZERO_EINVAL;
 }
 
 }  // namespace
