@@ -232,6 +232,10 @@ def test_window_attention_workspace(zp):
                 last = now
         assert f(**{**base, "head_dim": 136}, backward=backward) == 0 and f(**{**base, "window": 0}, backward=backward) == 0
     assert f(**base, backward=True) >= f(**base)
+    # sums of first keys' parts, for no more sequences than are long enough to have parts
+    many = dict(q_tokens=65536, k_tokens=65536, q_heads=8, k_heads=8, head_dim=128, window=256, sinks=4, backward=True)
+    sizes = [f(**many, sequences=n) for n in (1, 64, 256, 257, 513, 4096)]
+    assert sizes == sorted(sizes) and sizes[-1] < 500e6
 
 
 def test_binding_refuses(zp):

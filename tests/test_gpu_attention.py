@@ -336,6 +336,13 @@ def test_window_attention_backward_deals_out_the_first_keys(zp, case):
     Batch(lens, h, g, d, "bf16", room=3, behind=2).check_backward(zp, window, sinks)
 
 
+@pytest.mark.parametrize("short", [6, 12])
+def test_window_attention_backward_of_a_long_sequence_among_short_ones(zp, short):
+    """The first keys' queries go in parts among few short sequences, and whole among many."""
+    lens = [(20, 20)] * (short // 2) + [(2400, 2400)] + [(20, 30)] * (short // 2)
+    Batch(lens, 2, 1, 64, "f16", room=3, behind=2).check_backward(zp, 100, 4)
+
+
 @pytest.mark.parametrize("layout", ["slice", "heads_first"])
 @pytest.mark.parametrize("lens", [[(150, 150), (70, 300)], [(1, 400), (1, 30)]], ids=["many", "few"])
 def test_window_attention_layouts(zp, lens, layout):

@@ -340,9 +340,9 @@ __device__ __forceinline__ void store_rows(uint4 *stage, int lane, const uint32_
 // weights back) about as many issue slots again on each of the four
 // schedulers, so at 128 elements both pipes have to run without a pause.  With
 // one tile per CTA they wait for one another; two tiles take turns.  Measured:
-// 16384 tokens of 64 + 8 heads of 128, window 2048: 769 us, 1.38 PFLOP/s, 0.72
+// 16384 tokens of 64 + 8 heads of 128, window 2048: 774 us, 1.37 PFLOP/s, 0.71
 // of cuBLAS's burst rate (the same loads and products without the softmax
-// between them: 598).  8 x 1024 tokens of 25 heads of 64, window 256: 51 us;
+// between them: 598).  8 x 1024 tokens of 25 heads of 64, window 256: 50 us;
 // there a tile of scores is 512 clocks of the tensor pipe, and the masked
 // edges of a window of two tiles are worked out in full.
 template <int DT, class S>
@@ -1689,29 +1689,31 @@ template <int DT>
 __global__ void __launch_bounds__(kThreads) k_attn_join(const __grid_constant__ BwdTiles f)
 {
     const Attn &a = f.a;
-    const int32_t s = blockIdx.x / f.sink_tiles, tile = blockIdx.x % f.sink_tiles, first = tile * 128;
-    const Seq sq = sequence(a, s);
-    if (first >= sq.lk || first >= a.sinks)
-        return;
-    const QueryTiles t = query_tiles<128>(a, first, sq.lq, sq.lk);
-    if (!is_split(f, first, t))
-        return;
-    const int64_t base = a.q_offsets ? sq.q0 / (128 * f.chunk) + s : 0;
-    for (int32_t b = blockIdx.y; b < a.k_heads * 16; b += gridDim.y) {
-        const int rows = (b & 15) * 8;
-        const int32_t g = b >> 4;
-        for (int v = threadIdx.x; v < 2 * 8 * a.dim; v += kThreads) {
-            const int which = v / (8 * a.dim), r = rows + (v - which * 8 * a.dim) / a.dim, e = v % a.dim;
-            if (first + r >= sq.lk)
-                continue;
-            float sum = 0.0f;
+    for (int64_t i = blockIdx.x; i < (int64_t)a.sequences * f.sink_tiles; i += gridDim.x) {
+        const int32_t s = (int32_t)(i / f.sink_tiles), tile = (int32_t)(i % f.sink_tiles), first = tile * 128;
+        const Seq sq = sequence(a, s);
+        if (first >= sq.lk || first >= a.sinks)
+            continue;
+        const QueryTiles t = query_tiles<128>(a, first, sq.lq, sq.lk);
+        if (!is_split(f, first, t))
+            continue;
+        const int64_t base = a.q_offsets ? sq.q0 / (128 * f.chunk) + s : 0;
+        for (int32_t b = blockIdx.y; b < a.k_heads * 16; b += gridDim.y) {
+            const int rows = (b & 15) * 8;
+            const int32_t g = b >> 4;
+            for (int v = threadIdx.x; v < 2 * 8 * a.dim; v += kThreads) {
+                const int which = v / (8 * a.dim), r = rows + (v - which * 8 * a.dim) / a.dim, e = v % a.dim;
+                if (first + r >= sq.lk)
+                    continue;
+                float sum = 0.0f;
 #pragma unroll 4
-            for (int32_t c = t.low / f.chunk; c <= t.high / f.chunk; ++c) {
-                const int64_t slot = ((base + c) * f.sink_tiles + tile) * a.k_heads + g;
-                sum += f.partial[((slot * 2 + which) * 128 + r) * a.dim + e];
+                for (int32_t c = t.low / f.chunk; c <= t.high / f.chunk; ++c) {
+                    const int64_t slot = ((base + c) * f.sink_tiles + tile) * a.k_heads + g;
+                    sum += f.partial[((slot * 2 + which) * 128 + r) * a.dim + e];
+                }
+                const Heads to{which ? f.dk.p : f.dv.p, which ? f.dk.ld : f.dv.ld, which ? f.dk.hd : f.dv.hd};
+                store1<DT>(const_cast<void *>(to.p), (sq.k0 + first + r) * to.ld + g * to.hd + e, which ? sum * f.scale : sum);
             }
-            const Heads to{which ? f.dk.p : f.dv.p, which ? f.dk.ld : f.dv.ld, which ? f.dk.hd : f.dv.hd};
-            store1<DT>(const_cast<void *>(to.p), (sq.k0 + first + r) * to.ld + g * to.hd + e, which ? sum * f.scale : sum);
         }
     }
 }
@@ -2308,7 +2310,7 @@ struct SinkPlan {
     int64_t units;
 };
 
-SinkPlan plan_sinks(const zero_attention_t *a, bool one)
+SinkPlan plan_sinks(const zero_attention_t *a, bool one, bool space)
 {
     SinkPlan p{};
     if (a->sinks == 0 || a->sinks > 1024 || a->k_tokens == 0)
@@ -2317,10 +2319,16 @@ SinkPlan plan_sinks(const zero_attention_t *a, bool one)
     const int64_t chunk = tiles > 8 ? tiles : 8;
     if (a->q_tokens <= 2 * chunk * 128)
         return p;
+    // A part's number takes in its sequence's, so of sequences that are short
+    // on average most of the room for sums would lie idle: theirs are not
+    // dealt out.  (A workspace for more sequences serves fewer.)
+    const int64_t most = 4 * (a->q_tokens / (chunk * 128)), n = a->sequences < most ? a->sequences : most;
+    if (n < a->sequences && !space)
+        return p;
     p.chunk = (int32_t)chunk;
     const int64_t keys = a->sinks < a->k_tokens ? a->sinks : a->k_tokens;
     p.sink_tiles = (int32_t)((keys + 127) / 128);
-    p.units = tile_numbers(a->q_tokens, a->sequences, one, 128 * p.chunk) * p.sink_tiles * a->k_heads;
+    p.units = tile_numbers(a->q_tokens, n, one, 128 * p.chunk) * p.sink_tiles * a->k_heads;
     return p;
 }
 
@@ -2357,7 +2365,7 @@ AttnSpace attn_space(const zero_attention_t *a, bool backward)
     s.total = s.partial + align256(few);
     if (backward) {
         s.sums = s.stats + (size_t)a->q_heads * (size_t)tile_numbers(a->q_tokens, a->sequences, false, 128) * 1024;
-        const size_t end = s.sums + align256((size_t)plan_sinks(a, false).units * 256 * (size_t)a->head_dim * 4);
+        const size_t end = s.sums + align256((size_t)plan_sinks(a, false, true).units * 256 * (size_t)a->head_dim * 4);
         s.total = s.total > end ? s.total : end;
     }
     return s;
@@ -2425,8 +2433,9 @@ int launch_backward(BwdTiles &t, const BwdArrays &h, const zero_attention_t *a, 
     }
     if (e == cudaSuccess && t.split_units > 0) {
         what = "k_attn_join";
-        const int64_t x = (int64_t)t.a.sequences * t.sink_tiles, y = 152 * 8 / x, most = (int64_t)t.a.k_heads * 16;
-        k_attn_join<DT><<<dim3((unsigned)x, (unsigned)(y < 1 ? 1 : y < most ? y : most)), kThreads, 0, st>>>(t);
+        const int64_t every = (int64_t)t.a.sequences * t.sink_tiles, x = every < 152 * 8 ? every : 152 * 8;
+        const int64_t y = 152 * 8 / x, most = (int64_t)t.a.k_heads * 16;
+        k_attn_join<DT><<<dim3((unsigned)x, (unsigned)(y < most ? y : most)), kThreads, 0, st>>>(t);
         e = cudaGetLastError();
     }
     if (e != cudaSuccess) {
@@ -2514,7 +2523,7 @@ extern "C" int zero_window_attention_backward(const zero_attention_t *a, const v
     t.scale_log2 = (float)(a->scale * 1.4426950408889634);
     t.hdr = static_cast<WsHeader *>(ws);
     if (a->q_tokens > 0) {
-        const SinkPlan p = plan_sinks(a, one);
+        const SinkPlan p = plan_sinks(a, one, false);
         t.chunk = p.chunk, t.sink_tiles = p.sink_tiles, t.split_units = p.units;
         const StatsArgs s{t.a, hdout, hout, lse, const_cast<float *>(t.stats), t.q_tiles};
         const bool f16 = a->dtype == ZERO_F16;

@@ -419,11 +419,12 @@ struct Stream {
 // With what the heads of a token share,
 //     lo' = (lo (w_lo cos) - hi (w_hi sin)) r,  hi' = (hi (w_hi cos) + lo (w_lo sin)) r,
 // r = 1 / sqrt(mean(x^2) + eps).
-// Bound by its bytes, read once and written once; a token's angles cost its
-// warps as much as a few rows, so a warp keeps to its tokens.  8192 tokens of
-// 25 + 25 heads of 64 f16 (105 MB): 23.3 us from and to L2, 29.8 (3.5 TB/s)
-// from HBM, where 8 us are ramp; 16384 of 64 + 8 heads of 128 bf16 (604 MB):
-// 102 us, 5.9 TB/s, 0.87 of the copy.  One token: 2.9 us.
+// Every byte is read once and written once; a token's angles cost its warp as
+// much as a few rows, so a warp takes rows of one token after another.  Rows of
+// 128 are bound by bytes: 16384 tokens of 64 + 8 heads bf16 (604 MB) 102 us,
+// 5.9 TB/s, 0.87 of the copy; rows of 64 by issue (72 % of the slots): 8192
+// tokens of 25 + 25 heads f16 (105 MB) 23.2 us from and to L2, 29.8 from HBM.
+// One token: 3 us.
 template <int DT, int V, int SH, int N, int L, int DEPTH>
 __global__ void __launch_bounds__(kThreads, SH == kOne ? 1 : 4) k_qk_norm(const __grid_constant__ QkArgs a)
 {
