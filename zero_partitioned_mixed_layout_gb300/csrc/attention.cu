@@ -286,20 +286,27 @@ __device__ __forceinline__ int piece_at(int group, int c)
     return BN == 128 ? 64 * c + 32 * group : 32 * c;
 }
 
-// QT tiles of 128 queries against tiles of 128 keys.
-template <int DP_, int QT_, int PER_SM_>
+// QT tiles of 128 queries against tiles of BN keys, whose scores take 128
+// columns of tensor memory for a tile of queries: one tile's of 128 keys, or
+// two's of 64.
+template <int DP_, int QT_, int BN_, int PER_SM_>
 struct FwdShape {
-    static constexpr int DP = DP_, QT = QT_, BN = 128, PER_SM = PER_SM_;
+    static constexpr int DP = DP_, QT = QT_, BN = BN_, PER_SM = PER_SM_;
+    static constexpr int HALVES = BN / 64, BUFFERS = 128 / BN;
     static constexpr int BOXES = DP / 64, Q_TILE = BOXES * 16384, K_TILE = BOXES * BN * 128;  // bytes
-    static constexpr int STAGES = 2;
+    static constexpr int STAGES = 2 * BUFFERS;
     static constexpr int ROW_WARPS = 4 * QT, THREADS = (ROW_WARPS + 2) * 32;
-    static constexpr int TMEM = QT * (BN + DP) <= 128 ? 128 : QT * (BN + DP) <= 256 ? 256 : 512;
+    static constexpr int TMEM = QT * (128 + DP) <= 256 ? 256 : 512;
     static constexpr int SMEM = 1024 + QT * Q_TILE + 2 * STAGES * K_TILE + ROW_WARPS * 4096;
-    static_assert(SMEM * PER_SM <= 227 * 1024 && TMEM * PER_SM <= 512 && QT * (BN + DP) <= TMEM, "what an SM has");
+    static_assert(SMEM * PER_SM <= 227 * 1024 && TMEM * PER_SM <= 512 && QT * (128 + DP) <= TMEM, "what an SM has");
+    static_assert(QT == 1 || BUFFERS == 1, "two barriers of scores");
 };
 
+// s_full: of each tile of queries, or of each buffer of one's scores; p_full:
+// of its halves, or buffers; sum_done: the later half's products are in the
+// sums, or a tile's.
 struct FwdShared {
-    uint64_t q_full[2], q_empty[2], k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2][2], half_done[2], o_full[2];
+    uint64_t q_full[2], q_empty[2], k_full[4], k_empty[4], v_full[4], v_empty[4], s_full[2], p_full[2][2], sum_done[2], o_full[2];
     uint64_t unit_full[kUnitRing], unit_empty[kUnitRing];
     Unit units[kUnitRing];
     uint32_t tmem, gave_up;
@@ -342,13 +349,16 @@ __device__ __forceinline__ void store_rows(uint4 *stage, int lane, const uint32_
 // one tile per CTA they wait for one another; two tiles take turns.  Measured:
 // 16384 tokens of 64 + 8 heads of 128, window 2048: 774 us, 1.37 PFLOP/s, 0.71
 // of cuBLAS's burst rate (the same loads and products without the softmax
-// between them: 598).  8 x 1024 tokens of 25 heads of 64, window 256: 50 us;
-// there a tile of scores is 512 clocks of the tensor pipe, and the masked
-// edges of a window of two tiles are worked out in full.
+// between them: 598).  Tiles of 64 keys in two buffers instead: 1039.
+// Heads of 64: 8 x 1024 tokens of 25, window 256: 44.5 us.  128 x 64 scores
+// are 256 clocks of the tensor pipe, a row's thread takes several times that,
+// and the masked edges of a short window are worked out in full.  Tiles of 64
+// keys, whose scores are ready in a second buffer when those before are
+// through, mask less and wait less than of 128 in one: 50.
 template <int DT, class S>
 __global__ void __launch_bounds__(S::THREADS, S::PER_SM) k_attn_tiles(const __grid_constant__ FwdTiles f)
 {
-    constexpr int DP = S::DP, QT = S::QT, BN = S::BN;
+    constexpr int DP = S::DP, QT = S::QT, BN = S::BN, BUFFERS = S::BUFFERS;
     extern __shared__ unsigned char smem_raw[];
     __shared__ FwdShared sh;
     unsigned char *smem = smem_raw + ((1024 - (smem_addr(smem_raw) & 1023u)) & 1023u);
@@ -357,18 +367,19 @@ __global__ void __launch_bounds__(S::THREADS, S::PER_SM) k_attn_tiles(const __gr
     const Attn &a = f.a;
     const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
     constexpr int kTma = S::ROW_WARPS, kMma = S::ROW_WARPS + 1;
-    constexpr int kScores = BN, kSums = QT * BN;  // columns of tensor memory: of a tile's scores, where the sums start
+    constexpr int kScores = 128, kSums = QT * 128;  // columns of tensor memory: of a tile's scores, where the sums start
 
     if (threadIdx.x == 0) {
         for (int t = 0; t < QT; ++t) {
             mbar_init_count(&sh.q_full[t], 1);
             mbar_init_count(&sh.q_empty[t], 1);
-            mbar_init_count(&sh.s_full[t], 1);
             mbar_init_count(&sh.p_full[t][0], 4);
             mbar_init_count(&sh.p_full[t][1], 4);
-            mbar_init_count(&sh.half_done[t], 1);
+            mbar_init_count(&sh.sum_done[t], 1);
             mbar_init_count(&sh.o_full[t], 1);
         }
+        mbar_init_count(&sh.s_full[0], 1);
+        mbar_init_count(&sh.s_full[1], 1);
         for (int s = 0; s < S::STAGES; ++s) {
             mbar_init_count(&sh.k_full[s], 1);
             mbar_init_count(&sh.k_empty[s], 1);
@@ -480,7 +491,7 @@ __global__ void __launch_bounds__(S::THREADS, S::PER_SM) k_attn_tiles(const __gr
         const uint32_t desc_o = product_desc(kBf16, false, true, 128, wide);
         const uint64_t q0 = operand_desc(smem_addr(s_q), 16, 1024), k0 = operand_desc(smem_addr(s_k), 16, 1024);
         const uint64_t v0 = operand_desc(smem_addr(s_v), BN * 128, 1024);
-        uint32_t kn = 0, vn = 0, qn[2] = {0, 0}, pn[2] = {0, 0};
+        uint32_t kn = 0, vn = 0, qn[2] = {0, 0}, sn = 0, pn[2] = {0, 0};
         bool ok = true;
         Unit u;
         while (ok && next(u)) {
@@ -488,34 +499,39 @@ __global__ void __launch_bounds__(S::THREADS, S::PER_SM) k_attn_tiles(const __gr
             const TileList list = tile_list(kt2[0], kt2[1]);
             // S_t = Q_t K^T of the n-th tile
             auto scores = [&](int t, uint32_t stage) {
-                inner_products<DP, 128, BN>(tmem + t * kScores, q0 + ((t * S::Q_TILE) >> 4), k0 + ((stage * S::K_TILE) >> 4), desc_s, steps);
-                tensor_commit_elected(&sh.s_full[t]);
+                const uint32_t buffer = BUFFERS == 2 ? sn++ & 1 : 0;
+                inner_products<DP, 128, BN>(tmem + t * kScores + buffer * 64, q0 + ((t * S::Q_TILE) >> 4),
+                                            k0 + ((stage * S::K_TILE) >> 4), desc_s, steps);
+                tensor_commit_elected(&sh.s_full[t + buffer]);
             };
             bool first[2] = {true, true};
             // (the tiles of first keys come last, down to 0; without them the window's end with its lowest)
             const int32_t last[2] = {kt2[0].sinks && kt2[0].low ? 0 : kt2[0].low, kt2[1].sinks && kt2[1].low ? 0 : kt2[1].low};
-            for (int32_t n = 0; ok && n <= list.n; ++n) {
-                const int32_t kt = n < list.n ? list.at(n) : -1, before = n > 0 ? list.at(n - 1) : -1;
+            // a tile's scores go ahead of the products of the BUFFERS-th tile before
+            for (int32_t n = 0; ok && list.n > 0 && n < list.n + BUFFERS; ++n) {
+                const bool ended = n >= BUFFERS && n - BUFFERS < list.n;
+                const int32_t kt = n < list.n ? list.at(n) : -1, before = ended ? list.at(n - BUFFERS) : -1;
                 const uint32_t ks = kn % S::STAGES, vs = vn % S::STAGES;
                 bool k_here = false, v_here = false;
 #pragma unroll
                 for (int t = 0; t < QT; ++t) {
-                    if (n > 0 && needs(kt2[t], before)) {
+                    if (ended && needs(kt2[t], before)) {
                         if (!v_here)
                             ok = ok && wait(&sh.v_full[vs], (vn / S::STAGES) & 1);
                         v_here = true;
                         // the later keys' weights come first
                         const uint64_t dv = v0 + ((vs * S::K_TILE) >> 4);
 #pragma unroll
-                        for (int h = 1; h >= 0; --h) {
-                            ok = ok && wait(&sh.p_full[t][h], pn[t] & 1);
+                        for (int h = S::HALVES - 1; h >= 0; --h) {
+                            const uint32_t piece = BUFFERS == 2 ? pn[t] & 1 : h;
+                            ok = ok && wait(&sh.p_full[t][piece], BUFFERS == 2 ? (pn[t] >> 1) & 1 : pn[t] & 1);
                             if (!ok)
                                 break;
                             tmem_fence_after();
-                            tensor_products4_tmem<128, 16>(tmem + kSums + t * DP, tmem + t * kScores + h * 64, dv + h * 512, desc_o,
-                                                           !first[t] || h == 0);
-                            if (h)
-                                tensor_commit_elected(&sh.half_done[t]);
+                            tensor_products4_tmem<128, 16>(tmem + kSums + t * DP, tmem + t * kScores + piece * 64, dv + h * 512, desc_o,
+                                                           !first[t] || h + 1 < S::HALVES);
+                            if (BUFFERS == 2 || h)
+                                tensor_commit_elected(&sh.sum_done[t]);
                         }
                         ++pn[t];
                         if (!ok)
@@ -538,7 +554,7 @@ __global__ void __launch_bounds__(S::THREADS, S::PER_SM) k_attn_tiles(const __gr
                 }
                 if (!ok)
                     break;
-                if (n > 0)
+                if (ended)
                     tensor_commit_elected(&sh.v_empty[vs]);
                 if (kt >= 0)
                     tensor_commit_elected(&sh.k_empty[ks]);
@@ -548,7 +564,7 @@ __global__ void __launch_bounds__(S::THREADS, S::PER_SM) k_attn_tiles(const __gr
                     if (kt2[1].any)
                         tensor_commit_elected(&sh.q_empty[1]);
                 }
-                vn += n > 0;
+                vn += ended;
                 kn += kt >= 0;
             }
             qn[0] += kt2[0].any;
@@ -575,7 +591,8 @@ __global__ void __launch_bounds__(S::THREADS, S::PER_SM) k_attn_tiles(const __gr
                 const int32_t kt = list.at(n);
                 if (!needs(mine, kt))
                     continue;
-                ok = ok && wait(&sh.s_full[t], sn & 1);
+                const int buffer = BUFFERS == 2 ? sn & 1 : 0;
+                ok = ok && wait(&sh.s_full[t + buffer], BUFFERS == 2 ? (sn >> 1) & 1 : sn & 1);
                 ++sn;
                 if (!ok)
                     break;
@@ -587,10 +604,11 @@ __global__ void __launch_bounds__(S::THREADS, S::PER_SM) k_attn_tiles(const __gr
                 // their weights, which go where their scores were, and on to
                 // the products while the others are worked on.
 #pragma unroll
-                for (int h = 1; h >= 0; --h) {
+                for (int h = S::HALVES - 1; h >= 0; --h) {
+                    const int piece = BUFFERS == 2 ? buffer : h;
                     uint32_t r0[32], r1[32];
-                    tmem_load32(at_s + 64 * h, r0);
-                    tmem_load32(at_s + 64 * h + 32, r1);
+                    tmem_load32(at_s + 64 * piece, r0);
+                    tmem_load32(at_s + 64 * piece + 32, r1);
                     tmem_wait_loads(r0);
                     tmem_wait_loads(r1);
                     if (!whole) {
@@ -619,10 +637,11 @@ __global__ void __launch_bounds__(S::THREADS, S::PER_SM) k_attn_tiles(const __gr
                         const float to = far ? top : m;
                         const float keep = m == -INFINITY ? 0.0f : exp2_fast((m - to) * sl);
                         if (__any_sync(0xffffffffu, l != 0.0f)) {
-                            // (what the products before this tile added is there; of
-                            // this tile's other half, when they say so)
-                            if (h == 0) {
-                                ok = wait(&sh.half_done[t], (sn - 1) & 1);
+                            // (of halves, what the products before this tile added is
+                            // there, and of its later half when they say so; of
+                            // buffers, the tile's before when they say so)
+                            if (BUFFERS == 2 || h == 0) {
+                                ok = wait(&sh.sum_done[t], BUFFERS == 2 ? sn & 1 : (sn - 1) & 1);
                                 if (!ok)
                                     break;
                                 tmem_fence_after();
@@ -650,7 +669,7 @@ __global__ void __launch_bounds__(S::THREADS, S::PER_SM) k_attn_tiles(const __gr
                             sums[e & 3] = sums[e & 3] + x;
                             w[e] = pack2<DT>(x.x, x.y);
                         }
-                        tmem_store16(at_s + 64 * h + 16 * c, w);
+                        tmem_store16(at_s + 64 * piece + 16 * c, w);
                     };
                     weigh(r0, 0);
                     weigh(r1, 1);
@@ -673,7 +692,7 @@ __global__ void __launch_bounds__(S::THREADS, S::PER_SM) k_attn_tiles(const __gr
                     tmem_fence_before();
                     __syncwarp();
                     if (lane == 0)
-                        mbar_arrive_cluster(smem_addr(&sh.p_full[t][h]));
+                        mbar_arrive_cluster(smem_addr(&sh.p_full[t][piece]));
                 }
                 if (!ok)
                     break;
@@ -2199,9 +2218,9 @@ int short_by(int kernel, uint64_t *limit_ns)
 // Heads of up to 64 leave room for two CTAs of one tile of queries each, which
 // start and end apart from one another; wider ones for one CTA of two tiles,
 // whose products run while the other's weights are worked out.  At 16 heads of
-// 64 (narrow, wide): 8 x 1024 tokens 46, 48 us; 64 x 100 19, 36; 8192 187, 201.
-using Narrow = FwdShape<64, 1, 2>;
-using Wide = FwdShape<128, 2, 1>;
+// 64 (narrow, wide): 8 x 1024 tokens 44, 48 us; 64 x 100 18, 36; 8192 178, 201.
+using Narrow = FwdShape<64, 1, 64, 2>;
+using Wide = FwdShape<128, 2, 128, 1>;
 
 template <int DT, class S>
 int launch_tiles(FwdTiles &t, const Fwd &f, const zero_attention_t *a, cudaStream_t st)
@@ -2241,7 +2260,7 @@ int forward_tiles(const Fwd &f, const zero_attention_t *a, void *ws, cudaStream_
 // over their keys instead of in tiles of 128.  Both ways, 4096 keys, us (few |
 // tiles of 128) for 1, 4, 8, 16 queries: one sequence of 32 + 8 heads of 128 11,
 // 18, 21, 33 | 47; 64 of them 180, 282, 473, 816 | 605 to 613; one of 25 + 25
-// heads of 64 11, 12, 13, 17 | 41, 64 of them 283, 312, 314, 451 | 264 to 282.
+// heads of 64 11, 12, 13, 17 | 38, 64 of them 283, 312, 314, 451 | 250 to 270.
 constexpr int64_t kFewQueries = 8;
 
 struct FewPlan {
