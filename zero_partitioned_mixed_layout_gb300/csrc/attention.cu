@@ -1307,7 +1307,7 @@ __device__ __forceinline__ bool key_unit(const BwdTiles &f, int64_t i, int lane,
 // into dS' unrounded.  Rows of statistics come with the queries' tiles, so a
 // tile needs no reduction and no running maximum.
 //
-// What bounds it: four products, 4096 clocks of the tensor pipe for 128 x 128
+// What bounds it: four products, 2048 clocks of the tensor pipe for 128 x 128
 // pairs at 128 elements, and a chain of products and elementwise work that one
 // pair of buffers in tensor memory (two tiles of scores and two sums of
 // 128 x 128 are all of its 512 columns) lets overlap only by halves: 16384
@@ -1760,9 +1760,9 @@ struct QueryShared {
 // (S and dP are worked out here again, two products of seven, so that dq is
 // summed in one place and in one order, without atomics.)
 //
-// What bounds it: three products, 3072 clocks of the tensor pipe at 128
-// elements, against 64 KB of keys and values, 21 B per clock and SM, which L2
-// gives at no more than 7.7 TB/s to all SMs: about 1.45 of the 2.77 ms above.
+// What bounds it: three products, 1536 clocks of the tensor pipe at 128
+// elements, against 64 KB of keys and values: 42 B per clock and SM, 12 TB/s,
+// where L2 gives all SMs no more than 7.7: about 1.45 of the 2.77 ms above.
 // A window's queries of one key head's group read the same keys at about the
 // same time, so DRAM does not bound it.
 template <int DT, class S>
