@@ -361,6 +361,43 @@ def test_window_attention_of_one_sequence_without_offsets(zp, lens):
     c.check_backward(zp, None, 0, q_offsets=c.where["q_offsets"])
 
 
+@pytest.mark.parametrize("lens", [(300, 700), (8, 3), (1, 5000), (200, 90)], ids=str)
+def test_window_attention_of_one_sequence_over_a_cache(zp, lens):
+    """The keys' offsets and length without offsets of the queries."""
+    b = Batch([lens], 4, 2, 64, "bf16", room=5)
+    where = {name: b.where[name] for name in ("k_offsets", "k_lengths")}
+    b.check_forward(zp, 150, 2, **where)
+    b.check_backward(zp, 150, 2, **where)
+
+
+def test_window_attention_in_three_graphs(zp):
+    """Captured calls with workspaces of their own, replayed in turn, on
+    streams of their own, and twice in a row."""
+    batches = [Batch([(1, 900)] * 3, 8, 2, 64, "f16"), Batch([(7, 4000)], 4, 4, 128, "f16"), Batch([(260, 260), (90, 140)], 4, 2, 64, "f16")]
+    want, graphs, outs = [], [], []
+    for b in batches:
+        want.append([x.t if isinstance(x, Out) else x for x in b.check_forward(zp, 300, 3)])
+        out, lse, ws = torch.zeros_like(b.q), torch.zeros((b.heads, b.tq), device="cuda"), b.workspace(zp, 300, 3)
+        run = lambda: zp.zero_window_attention(b.q, b.k, b.v, out, ws, 300, 3, None, lse, **b.where)
+        stream, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+        stream.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.graph(graph, stream=stream):
+            run()
+            run()
+        graphs.append((graph, stream, ws))
+        outs.append((out, lse))
+    torch.cuda.synchronize()
+    for _ in range(3):
+        for graph, stream, _ in graphs:
+            with torch.cuda.stream(stream):
+                graph.replay()
+                graph.replay()
+    torch.cuda.synchronize()
+    for (out, lse), (o, l) in zip(outs, want):
+        assert torch.equal(out, o) and torch.equal(lse, l)
+    assert all(zp.zero_workspace_stalls(ws) == 0 for _, _, ws in graphs)
+
+
 @pytest.mark.parametrize("lens", [[(200, 200)], [(1, 200)]], ids=["many", "one"])
 @pytest.mark.parametrize("scale,std", [(1.0, 4.0), (1e-3, 1.0), (30.0, 1.0)])
 def test_window_attention_scales(zp, lens, scale, std):
