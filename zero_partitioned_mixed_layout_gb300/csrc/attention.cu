@@ -7,6 +7,8 @@
 // in one pass: with a reference m (about the largest score so far),
 // l = sum exp(s - m) and O = sum exp(s - m) v, and both times
 // exp(m - m') when the reference moves to m'; o = O / l, lse = m + log l.
+// (lse is put together from the largest score itself, rounded as the backward
+// pass rounds it, so that of a score past 2^24 its own weight there is 1.)
 // Scores, l and O are binary32.  exp(s - m) is rounded to 16 bits once, as
 // the second product's operand: by at most half a step (2^-8 in bf16, 2^-11
 // in f16) of each weight, as much as the output itself is rounded by; l adds
@@ -162,6 +164,13 @@ __device__ __forceinline__ float exp2_fast(float x)
 }
 
 __device__ __forceinline__ F2 exp2_fast(F2 x) { return {exp2_fast(x.x), exp2_fast(x.y)}; }
+
+// log of a row's sum of weights: of the largest score `best`, the reference m
+// (up to 2^8 of a weight lower) and l.
+__device__ __forceinline__ float row_lse(float best, float m, float l, float scale)
+{
+    return __fadd_rn(__fmul_rn(best, scale), logf(l) + (m - best) * scale);
+}
 
 template <int DT>
 __device__ __forceinline__ uint32_t pack2(float lo, float hi)
@@ -586,7 +595,7 @@ __global__ void __launch_bounds__(S::THREADS, S::PER_SM) k_attn_tiles(const __gr
             const int32_t row = u.first + 128 * t + quarter * 32 + lane, p = row + u.lk - u.lq;
             const int32_t p_first = u.first + 128 * t + u.lk - u.lq;
             const int32_t p_last = (u.first + 128 * t + 127 < u.lq ? u.first + 128 * t + 127 : u.lq - 1) + u.lk - u.lq;
-            float m = -INFINITY, l = 0.0f;
+            float m = -INFINITY, best = -INFINITY, l = 0.0f;
             for (int32_t n = 0; n < list.n; ++n) {
                 const int32_t kt = list.at(n);
                 if (!needs(mine, kt))
@@ -602,8 +611,9 @@ __global__ void __launch_bounds__(S::THREADS, S::PER_SM) k_attn_tiles(const __gr
                                    (k_first > p_last - a.window || k_first + BN - 1 < a.sinks);
                 // 64 keys at a time, the later ones first: their largest score,
                 // their weights, which go where their scores were, and on to
-                // the products while the others are worked on.
-#pragma unroll
+                // the products while the others are worked on.  (Unrolled, the
+                // two halves' code took 805 us where this takes 790.)
+#pragma unroll 1
                 for (int h = S::HALVES - 1; h >= 0; --h) {
                     const int piece = BUFFERS == 2 ? buffer : h;
                     uint32_t r0[32], r1[32];
@@ -632,6 +642,7 @@ __global__ void __launch_bounds__(S::THREADS, S::PER_SM) k_attn_tiles(const __gr
                     // The weights' reference is the largest score so far, or up
                     // to 2^8 below it: the weights stay below 2^8, and sums are
                     // rarely multiplied anew.
+                    best = fmaxf(best, top);
                     const bool far = top > m && (m == -INFINITY || (top - m) * sl > 8.0f);
                     if (__any_sync(0xffffffffu, far)) {
                         const float to = far ? top : m;
@@ -659,13 +670,18 @@ __global__ void __launch_bounds__(S::THREADS, S::PER_SM) k_attn_tiles(const __gr
                         l *= keep;
                         m = to;
                     }
-                    const F2 scale2 = twice(sl), base2 = twice(m == -INFINITY ? 0.0f : -m * sl);
+                    // The difference first: s sl - m sl in one operation would be off
+                    // by the rounding of m sl, 2^4 and more from 2^28 on, which
+                    // a weight of 16 bits does not hold.  (16384 tokens of 64 + 8
+                    // heads of 128: 790 us against 774; a branch to it for
+                    // large scores alone: 825 to 860.)
+                    const F2 scale2 = twice(sl), less2 = twice(m == -INFINITY ? 0.0f : -m);
                     F2 sums[4] = {};
                     auto weigh = [&](const uint32_t (&r)[32], int c) {
                         uint32_t w[16];
 #pragma unroll
                         for (int e = 0; e < 16; ++e) {
-                            const F2 x = exp2_fast(fma2({__uint_as_float(r[2 * e]), __uint_as_float(r[2 * e + 1])}, scale2, base2));
+                            const F2 x = exp2_fast((F2{__uint_as_float(r[2 * e]), __uint_as_float(r[2 * e + 1])} + less2) * scale2);
                             sums[e & 3] = sums[e & 3] + x;
                             w[e] = pack2<DT>(x.x, x.y);
                         }
@@ -712,8 +728,7 @@ __global__ void __launch_bounds__(S::THREADS, S::PER_SM) k_attn_tiles(const __gr
             const bool live = row < u.lq;
             const int64_t out_row = (int64_t)u.q_row + 128 * t + quarter * 32 + lane;
             if (live && f.lse)
-                f.lse[(int64_t)u.head * a.q_tokens + out_row] =
-                    l == 0.0f ? -INFINITY : m * a.scale + logf(l);
+                f.lse[(int64_t)u.head * a.q_tokens + out_row] = l == 0.0f ? -INFINITY : row_lse(best, m, l, a.scale);
             const float inv = l == 0.0f ? 0.0f : 1.0f / l;
             const int32_t left = u.lq - u.first - 128 * t - quarter * 32;  // rows of this warp
             uint16_t *out = static_cast<uint16_t *>(const_cast<void *>(f.out.p)) +
@@ -902,10 +917,10 @@ __global__ void __launch_bounds__(kFewWarps * 32) k_attn_few(const __grid_consta
             }
         };
         auto word = [](const uint4 &x, int e) { return e == 0 ? x.x : e == 1 ? x.y : e == 2 ? x.z : x.w; };
-        float o[NG][JJ * 4][4] = {}, m[NG][2], l[NG][2] = {};
+        float o[NG][JJ * 4][4] = {}, m[NG][2], best[NG][2], l[NG][2] = {};
 #pragma unroll
         for (int i = 0; i < NG; ++i)
-            m[i][0] = m[i][1] = -INFINITY;
+            m[i][0] = m[i][1] = best[i][0] = best[i][1] = -INFINITY;
         const bool many = queries > 1;
         int32_t x = x0 + warp * 16;
         if (x < x1) {
@@ -943,6 +958,7 @@ __global__ void __launch_bounds__(kFewWarps * 32) k_attn_few(const __grid_consta
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     top[i][e] = fmaxf(t[i][e], t[i][2 + e]);
+                    best[i][e] = fmaxf(best[i][e], top[i][e]);
                     far = far || (top[i][e] > m[i][e] && (m[i][e] == -INFINITY || (top[i][e] - m[i][e]) * f.scale_log2 > 8.0f));
                 }
             }
@@ -994,17 +1010,21 @@ __global__ void __launch_bounds__(kFewWarps * 32) k_attn_few(const __grid_consta
             if (x_next < x1)
                 load_v(x_next);
         }
-        // the warps' sums, each with its reference
+        // the warps' sums, each with its largest score for a reference in the end
 #pragma unroll
         for (int i = 0; i < NG; ++i) {
+            float keep[2];
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
 #pragma unroll
-                for (int b = 4; b < 32; b *= 2)
+                for (int b = 4; b < 32; b *= 2) {
+                    best[i][e] = fmaxf(best[i][e], __shfl_xor_sync(0xffffffffu, best[i][e], b));
                     l[i][e] += __shfl_xor_sync(0xffffffffu, l[i][e], b);
+                }
+                keep[e] = m[i][e] == best[i][e] ? 1.0f : exp2_fast((m[i][e] - best[i][e]) * f.scale_log2);
                 if (g == 0) {
-                    s_m[warp][8 * i + 2 * c + e] = m[i][e];
-                    s_l[warp][8 * i + 2 * c + e] = l[i][e];
+                    s_m[warp][8 * i + 2 * c + e] = best[i][e];
+                    s_l[warp][8 * i + 2 * c + e] = l[i][e] * keep[e];
                 }
             }
 #pragma unroll
@@ -1014,7 +1034,7 @@ __global__ void __launch_bounds__(kFewWarps * 32) k_attn_few(const __grid_consta
 #pragma unroll
                     for (int h = 0; h < 2; ++h)
                         *reinterpret_cast<float2 *>(&s_o[warp][8 * i + 2 * c + h][64 * e + 8 * g + 2 * b]) =
-                            make_float2(o[i][e * 4 + b][h], o[i][e * 4 + b][2 + h]);
+                            make_float2(o[i][e * 4 + b][h] * keep[h], o[i][e * 4 + b][2 + h] * keep[h]);
         }
     }
     __syncthreads();
@@ -1029,7 +1049,7 @@ __global__ void __launch_bounds__(kFewWarps * 32) k_attn_few(const __grid_consta
             w = make_uint2(pack2<DT>(sum.x / l, sum.y / l), pack2<DT>(sum.z / l, sum.w / l));
         *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(const_cast<void *>(f.out.p)) + row * f.out.ld + head * f.out.hd + e) = w;
         if (e == 0 && f.lse)
-            f.lse[(int64_t)head * a.q_tokens + row] = l == 0.0f ? -INFINITY : m * a.scale + logf(l);
+            f.lse[(int64_t)head * a.q_tokens + row] = l == 0.0f ? -INFINITY : row_lse(m, m, l, a.scale);
     };
     auto add = [](float4 &sum, float4 x, float by) {
         sum.x += x.x * by, sum.y += x.y * by, sum.z += x.z * by, sum.w += x.w * by;
