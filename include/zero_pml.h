@@ -825,7 +825,11 @@ typedef struct zero_attention {
  * -inf.  Rows of out and lse outside every sequence are left as they were.
  * Scores, their maximum and sum, and the output's sums are binary32; the
  * softmax's numerators are rounded to dtype once, as operands of the tensor
- * cores.
+ * cores.  q.k is taken to fit binary32, of whose rounding lse has its share:
+ * 2^-24 of the largest score.  (The backward pass finds the scores of a
+ * forward call of more than eight queries per sequence, on average, bit for
+ * bit; those of fewer were added up in another order, so that from scores of
+ * about 10^5 on its P may be off by exp of their difference.)
  * All arrays start on 16 bytes, with ld and hd positive multiples of 8
  * elements (where there is more than one token, or head).
  * ws: device, 256-byte aligned, zero-filled before its first use, of

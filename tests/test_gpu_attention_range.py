@@ -62,3 +62,35 @@ def test_one_key_takes_all_forward(zp, size, scale, lens, dim, dtype):  # noqa: 
     # lse: the scale's, the product's and the sum's rounding, and the logarithm's of a sum that is 1
     s = b.score().T
     ref.check(lse, s, 3 * U32 * s.abs() + 32 * U32, "lse")
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("lens", [(150, 400), (4, 400)], ids=["many", "few"])
+@pytest.mark.parametrize("size,scale", DOMINATED, ids=str)
+def test_one_key_takes_all_backward(zp, size, scale, lens, dim, dtype):  # noqa: F811
+    """P is 1 whatever the score's size: lse is the rounded product that the
+    backward pass forms again."""
+    b = Dominated(lens, 4, 2, dim, dtype, size, scale)
+    out, lse = b.forward(zp, None, 0, scale)
+    b.dout.mul_(0.01)
+    out.t.mul_(0.5)  # (so that dP - delta is no difference of equal numbers)
+    ws = b.workspace(zp, None, 0, True)
+    g = [torch.empty_like(x) for x in (b.q, b.k, b.v)]
+    zp.zero_window_attention_backward(b.dout, b.q, b.k, b.v, out.t, lse, *g, ws, None, 0, scale, **b.where)
+    do, o, q, k, v = (x.double() for x in (b.dout, out.t, b.q, b.k, b.v))
+    vw, kw = v[b.key, b.key_head], k[b.key, b.key_head]
+    ds = (do * vw).sum(-1) - (do * o).sum(-1)
+    # dP and delta: binary32 sums (which may truncate) of exact products; P: 16 roundings; dS: one to 16 bits
+    eds = ((do * vw).abs().sum(-1) * 2 + (do * o).abs().sum(-1)) * (dim * U32) + ds.abs() * (UT[b.dt] + 24 * U32) + ref.TINY[b.dt]
+    ep = UT[b.dt] + 16 * U32
+    dq = (ds[..., None] * kw * scale, (eds[..., None] + ds.abs()[..., None] * 4 * U32) * kw.abs() * scale)
+
+    def by_key(x):
+        to = torch.zeros_like(k)
+        return to.index_put_((b.key, b.key_head), x, accumulate=True)
+    n = 2 * lens[0] * U32  # the sums over queries
+    dk = by_key(ds[..., None] * q) * scale, by_key((eds[..., None] + ds.abs()[..., None] * n) * q.abs()) * scale
+    dv = by_key(do), by_key(do.abs() * (ep + n))
+    for name, got, (value, err) in zip(("dq", "dk", "dv"), g, (dq, dk, dv)):
+        ref.check(got, value, ref.rounded(value, err + 4 * U32 * value.abs(), b.dt), name)

@@ -1138,10 +1138,10 @@ __global__ void __launch_bounds__(kFewWarps * 32) k_attn_few(const __grid_consta
 
 // ------------------------------------------------------------- backward
 
-// What every pair of a query and a key takes from the query's row: lse in
-// units of log 2 (+inf where no key is seen, which makes every weight 0) and
-// delta = dout . out.  Laid out by tile of 128 queries, so that a tile's are
-// one aligned copy: [head][tile number][lse2 of 128, delta of 128].
+// What every pair of a query and a key takes from the query's row: lse (+inf
+// where no key is seen, which makes every weight 0) and delta = dout . out.
+// Laid out by tile of 128 queries, so that a tile's are one aligned copy:
+// [head][tile number][lse of 128, delta of 128].
 struct StatsArgs {
     Attn a;
     Heads dout, out;
@@ -1193,10 +1193,21 @@ __global__ void __launch_bounds__(128) k_attn_stats(const __grid_constant__ Stat
                 mine = lane / kRows == i ? v : mine;
             }
             float *const to = f.stats + (h * f.tiles + number) * 256 + 32 * part + lane;
-            to[0] = lse == -INFINITY ? INFINITY : lse * 1.4426950408889634f;
+            to[0] = lse == -INFINITY ? INFINITY : lse;
             to[128] = mine;
         }
     }
+}
+
+// P of two pairs: exp(s scale - lse), with s scale rounded as the forward
+// pass rounds it for lse, so that a key that takes all has a weight of 1
+// whatever its score.  (One operation, with scale and lse in units of log 2,
+// is off by their roundings: 2^-23 of the score, so by factors from 10^7 on.
+// 16384 tokens of 64 + 8 heads of 128 took 2745 us with it and take 2777 with
+// three; 5340 of 25 heads of 64 103 and 106.7.)  zero2: see BwdTiles.
+__device__ __forceinline__ F2 weights(F2 s, F2 scale2, F2 zero2, F2 less_lse)
+{
+    return exp2_fast((fma2(s, scale2, zero2) + less_lse) * twice(1.4426950408889634f));
 }
 
 struct BwdTiles {
@@ -1209,7 +1220,8 @@ struct BwdTiles {
     int32_t chunk, sink_tiles;
     int64_t split_units;
     float *partial;  // [split unit][dv, dk][128][dim]
-    float scale, scale_log2;
+    float scale;
+    float zero;         // 0, but not so that the compiler could tell: added to a product that is to be rounded by itself
     int32_t after_dkv;  // (dq: k_attn_dkv is launched before it)
     WsHeader *hdr;
     uint64_t limit_ns;
@@ -1341,7 +1353,7 @@ __global__ void __launch_bounds__(S::THREADS, S::PER_SM) k_attn_dkv(const __grid
     __shared__ KeyShared sh;
     unsigned char *smem = smem_raw + ((1024 - (smem_addr(smem_raw) & 1023u)) & 1023u);
     unsigned char *const s_k = smem, *const s_v = smem + S::TILE, *const s_q = s_v + S::TILE, *const s_o = s_q + S::STAGES * S::MOVING;
-    float *const s_stats = reinterpret_cast<float *>(s_o + S::STAGES * S::MOVING);  // [stage][lse2, delta][BN]
+    float *const s_stats = reinterpret_cast<float *>(s_o + S::STAGES * S::MOVING);  // [stage][lse, delta][BN]
     unsigned char *const s_out = reinterpret_cast<unsigned char *>(s_stats + S::STAGES * 2 * BN);
     const Attn &a = f.a;
     const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
@@ -1556,7 +1568,7 @@ __global__ void __launch_bounds__(S::THREADS, S::PER_SM) k_attn_dkv(const __grid
                 if (!ok)
                     break;
                 tmem_fence_after();
-                const float *lse2 = s_stats + st * 2 * BN, *delta = lse2 + BN;
+                const float *lse = s_stats + st * 2 * BN, *delta = lse + BN;
                 if (nq < BN) {
                     // rows behind the last query: zeros, since 0 times what they hold may not be 0
                     ok = wait(&sh.o_full[st], (qn / S::STAGES) & 1);
@@ -1572,7 +1584,7 @@ __global__ void __launch_bounds__(S::THREADS, S::PER_SM) k_attn_dkv(const __grid
                 }
                 F2 p[2][16];
                 uint32_t bits[2] = {~0u, ~0u};
-                const F2 scale2 = twice(f.scale_log2);
+                const F2 scale2 = twice(f.scale), zero2 = twice(f.zero);
                 // piece c is done (of 64 columns, both are when the second is)
                 auto ready = [&](uint64_t *bar, int c) {
                     if (BN == 64 && c == 0)
@@ -1590,11 +1602,9 @@ __global__ void __launch_bounds__(S::THREADS, S::PER_SM) k_attn_dkv(const __grid
                     tmem_wait_loads(r);
 #pragma unroll
                     for (int e = 0; e < 16; e += 2) {
-                        const float4 x = *reinterpret_cast<const float4 *>(lse2 + at + 2 * e);
-                        p[c][e] = exp2_fast(
-                            fma2({__uint_as_float(r[2 * e]), __uint_as_float(r[2 * e + 1])}, scale2, {-x.x, -x.y}));
-                        p[c][e + 1] = exp2_fast(
-                            fma2({__uint_as_float(r[2 * e + 2]), __uint_as_float(r[2 * e + 3])}, scale2, {-x.z, -x.w}));
+                        const float4 x = *reinterpret_cast<const float4 *>(lse + at + 2 * e);
+                        p[c][e] = weights({__uint_as_float(r[2 * e]), __uint_as_float(r[2 * e + 1])}, scale2, zero2, {-x.x, -x.y});
+                        p[c][e + 1] = weights({__uint_as_float(r[2 * e + 2]), __uint_as_float(r[2 * e + 3])}, scale2, zero2, {-x.z, -x.w});
                     }
                     if (!whole) {
                         bits[c] = ~bits_up_to(j - p0 - 1 - at) & bits_up_to(nq - 1 - at);
@@ -2003,7 +2013,7 @@ __global__ void __launch_bounds__(S::THREADS, S::PER_SM) k_attn_dq(const __grid_
             const int32_t p_first = u.first + u.lk - u.lq;
             const int32_t p_last = (u.first + 127 < u.lq ? u.first + 127 : u.lq - 1) + u.lk - u.lq;
             const float *stats = f.stats + (u.head * f.q_tiles + u.stats) * 256 + quarter * 32 + lane;
-            const float lse2 = stats[0], delta = stats[128];
+            const float lse = stats[0], delta = stats[128];
             for (int32_t n = 0; n < list.n; ++n, ++kn) {
                 const uint32_t st = kn % S::STAGES, buf = kn & 1;
                 const int32_t k_first = list.at(n) * BN;
@@ -2015,7 +2025,7 @@ __global__ void __launch_bounds__(S::THREADS, S::PER_SM) k_attn_dq(const __grid_
                 tmem_fence_after();
                 const uint32_t at_s = tmem + lanes + buf * BN, at_p = tmem + lanes + kDp;
                 F2 w2[2][16];
-                const F2 scale2 = twice(f.scale_log2), base2 = twice(-lse2), delta2 = twice(-delta);
+                const F2 scale2 = twice(f.scale), zero2 = twice(f.zero), lse2 = twice(-lse), delta2 = twice(-delta);
                 // the weights, while dP is worked out
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
@@ -2024,7 +2034,7 @@ __global__ void __launch_bounds__(S::THREADS, S::PER_SM) k_attn_dq(const __grid_
                     tmem_wait_loads(r);
 #pragma unroll
                     for (int e = 0; e < 16; ++e)
-                        w2[c][e] = exp2_fast(fma2({__uint_as_float(r[2 * e]), __uint_as_float(r[2 * e + 1])}, scale2, base2));
+                        w2[c][e] = weights({__uint_as_float(r[2 * e]), __uint_as_float(r[2 * e + 1])}, scale2, zero2, lse2);
                 }
                 if (k_first + BN > u.lk) {
                     // rows behind the last key: zeros, since 0 times what they hold may not be 0
@@ -2559,7 +2569,6 @@ extern "C" int zero_window_attention_backward(const zero_attention_t *a, const v
     t.stats = reinterpret_cast<float *>(static_cast<char *>(ws) + sp.stats);
     t.partial = reinterpret_cast<float *>(static_cast<char *>(ws) + sp.sums);
     t.scale = (float)a->scale;
-    t.scale_log2 = (float)(a->scale * 1.4426950408889634);
     t.hdr = static_cast<WsHeader *>(ws);
     if (a->q_tokens > 0) {
         const SinkPlan p = plan_sinks(a, one, false);
