@@ -94,3 +94,35 @@ def test_one_key_takes_all_backward(zp, size, scale, lens, dim, dtype):  # noqa:
     dv = by_key(do), by_key(do.abs() * (ep + n))
     for name, got, (value, err) in zip(("dq", "dk", "dv"), g, (dq, dk, dv)):
         ref.check(got, value, ref.rounded(value, err + 4 * U32 * value.abs(), b.dt), name)
+
+
+# ------------------------------------------------------------------ weights far below the largest
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("few", [False, True], ids=["many", "few"])
+@pytest.mark.parametrize("below", [17.5, 16.5, 13.0])
+def test_many_keys_far_below_another(zp, below, few, dim, dtype):  # noqa: F811
+    """A key of weight 1 among others of exp(-below) each, about 2^-25 at 17.5:
+    what those add up to is in out as it is in lse.  The one key comes before
+    most of the others in either kernel's order, and in one part of them."""
+    heads, queries, n, lens = (32, 1, 1024, [(1, 1025)] * 64) if few else (2, 20, 65536, [(20, 65556)])
+    b = Batch(lens, heads, heads, dim, dtype)
+    for x in (b.q, b.k, b.v):
+        x.zero_()
+    b.q[..., 0] = 1.0
+    b.v.fill_(1.0)
+    one = torch.tensor([ks.start if few else ks.stop - queries for _, ks in b.slices()], device="cuda")
+    b.k[one, :, 0] = below
+    b.v[one] = 0.0
+    out, lse = b.forward(zp, None, 0, 1.0)
+    # queries see the one key and n others, and each one more than the query before it
+    others = (n + torch.arange(queries, dtype=torch.float64, device="cuda")).repeat(len(lens))[:, None]
+    w = others * math.exp(-below)
+    want = (w / (1 + w))[..., None].expand(-1, heads, dim)
+    # each weight: the exponent's and the exponential's own errors, and one rounding to 16 bits of 2^7 times it (half a
+    # step of f16's subnormals is 2^-32 of the weight 1); sums of at most 1024 terms' chains that may truncate
+    step = 2.0 ** -32 if dtype == "f16" else 0.0
+    err = want * (UT[b.dt] + (4 * below + 16 + 2 * 1024) * U32) + (others * step)[..., None]
+    ref.check(out.t, want, ref.rounded(want, err, b.dt), "out")
+    ref.check(lse, (below + torch.log1p(w)).T.expand(heads, -1), torch.full_like(lse, 2048 * U32 + 4 * below * U32, dtype=torch.float64), "lse")

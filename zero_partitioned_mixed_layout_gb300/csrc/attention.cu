@@ -12,7 +12,11 @@
 // Scores, l and O are binary32.  exp(s - m) is rounded to 16 bits once, as
 // the second product's operand: by at most half a step (2^-8 in bf16, 2^-11
 // in f16) of each weight, as much as the output itself is rounded by; l adds
-// up the weights as they were before.
+// up the weights as they were before.  f16 has steps of 2^-24 at its low end,
+// and so weights, l and O are all 2^7 times as large there (kShift): up to
+// 2^15 instead of 2^8, and rounded by half a step down to 2^-21 of the largest.
+// (At 1 and less, 65536 keys of a weight of 2^-25 each beside a first key of
+// 1 added up to nothing in O and to 2^-9 in l.)
 //
 // Three ways: tiles of 128 queries on the tensor cores (k_attn_tiles), a few
 // queries per sequence (k_attn_few), and the backward pass (k_attn_stats,
@@ -165,11 +169,16 @@ __device__ __forceinline__ float exp2_fast(float x)
 
 __device__ __forceinline__ F2 exp2_fast(F2 x) { return {exp2_fast(x.x), exp2_fast(x.y)}; }
 
+// The forward pass's weights are 2^kShift exp(s - m).
+template <int DT>
+constexpr float kShift = DT == ZERO_F16 ? 7.0f : 0.0f;
+
 // log of a row's sum of weights: of the largest score `best`, the reference m
 // (up to 2^8 of a weight lower) and l.
+template <int DT>
 __device__ __forceinline__ float row_lse(float best, float m, float l, float scale)
 {
-    return __fadd_rn(__fmul_rn(best, scale), logf(l) + (m - best) * scale);
+    return __fadd_rn(__fmul_rn(best, scale), logf(DT == ZERO_F16 ? l * 0x1p-7f : l) + (m - best) * scale);
 }
 
 template <int DT>
@@ -640,8 +649,8 @@ __global__ void __launch_bounds__(S::THREADS, S::PER_SM) k_attn_tiles(const __gr
                     const float top = fmaxf(fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3])),
                                             fmaxf(fmaxf(tops[4], tops[5]), fmaxf(tops[6], tops[7])));
                     // The weights' reference is the largest score so far, or up
-                    // to 2^8 below it: the weights stay below 2^8, and sums are
-                    // rarely multiplied anew.
+                    // to 2^8 below it: the weights stay below 2^(8 + kShift), and
+                    // sums are rarely multiplied anew.
                     best = fmaxf(best, top);
                     const bool far = top > m && (m == -INFINITY || (top - m) * sl > 8.0f);
                     if (__any_sync(0xffffffffu, far)) {
@@ -681,7 +690,8 @@ __global__ void __launch_bounds__(S::THREADS, S::PER_SM) k_attn_tiles(const __gr
                         uint32_t w[16];
 #pragma unroll
                         for (int e = 0; e < 16; ++e) {
-                            const F2 x = exp2_fast((F2{__uint_as_float(r[2 * e]), __uint_as_float(r[2 * e + 1])} + less2) * scale2);
+                            const F2 s = F2{__uint_as_float(r[2 * e]), __uint_as_float(r[2 * e + 1])} + less2;
+                            const F2 x = exp2_fast(kShift<DT> == 0.0f ? s * scale2 : fma2(s, scale2, twice(kShift<DT>)));
                             sums[e & 3] = sums[e & 3] + x;
                             w[e] = pack2<DT>(x.x, x.y);
                         }
@@ -728,7 +738,7 @@ __global__ void __launch_bounds__(S::THREADS, S::PER_SM) k_attn_tiles(const __gr
             const bool live = row < u.lq;
             const int64_t out_row = (int64_t)u.q_row + 128 * t + quarter * 32 + lane;
             if (live && f.lse)
-                f.lse[(int64_t)u.head * a.q_tokens + out_row] = l == 0.0f ? -INFINITY : row_lse(best, m, l, a.scale);
+                f.lse[(int64_t)u.head * a.q_tokens + out_row] = l == 0.0f ? -INFINITY : row_lse<DT>(best, m, l, a.scale);
             const float inv = l == 0.0f ? 0.0f : 1.0f / l;
             const int32_t left = u.lq - u.first - 128 * t - quarter * 32;  // rows of this warp
             uint16_t *out = static_cast<uint16_t *>(const_cast<void *>(f.out.p)) +
@@ -990,8 +1000,8 @@ __global__ void __launch_bounds__(kFewWarps * 32) k_attn_few(const __grid_consta
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     const float m0 = m[i][0] == -INFINITY ? 0.0f : m[i][0], m1 = m[i][1] == -INFINITY ? 0.0f : m[i][1];
-                    const float w0 = exp2_fast((t[i][2 * h] - m0) * f.scale_log2);
-                    const float w1 = exp2_fast((t[i][2 * h + 1] - m1) * f.scale_log2);
+                    const float w0 = exp2_fast(fmaf(t[i][2 * h] - m0, f.scale_log2, kShift<DT>));
+                    const float w1 = exp2_fast(fmaf(t[i][2 * h + 1] - m1, f.scale_log2, kShift<DT>));
                     l[i][0] += w0;
                     l[i][1] += w1;
                     w[i][h] = transpose8(pack2<DT>(w0, w1));
@@ -1049,7 +1059,7 @@ __global__ void __launch_bounds__(kFewWarps * 32) k_attn_few(const __grid_consta
             w = make_uint2(pack2<DT>(sum.x / l, sum.y / l), pack2<DT>(sum.z / l, sum.w / l));
         *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(const_cast<void *>(f.out.p)) + row * f.out.ld + head * f.out.hd + e) = w;
         if (e == 0 && f.lse)
-            f.lse[(int64_t)head * a.q_tokens + row] = l == 0.0f ? -INFINITY : row_lse(m, m, l, a.scale);
+            f.lse[(int64_t)head * a.q_tokens + row] = l == 0.0f ? -INFINITY : row_lse<DT>(m, m, l, a.scale);
     };
     auto add = [](float4 &sum, float4 x, float by) {
         sum.x += x.x * by, sum.y += x.y * by, sum.z += x.z * by, sum.w += x.w * by;
