@@ -854,7 +854,8 @@ int zero_window_attention(const zero_attention_t *a, const void *q, int64_t q_ld
  *     dS_ij = P_ij (dout_i.v_j - delta_i),
  *     dq_i = scale sum_j dS_ij k_j,  dk_j = scale sum_i dS_ij q_i,  dv_j = sum_i P_ij dout_i
  * (dk and dv summed over the query heads of a key head).  P and dS are
- * rounded to dtype once, as operands; all sums are binary32 and taken in a
+ * rounded to dtype once, as operands (in F16 times powers of two, from the
+ * sizes of dout, v and out, that keep them in its range); all sums are binary32 and taken in a
  * fixed order (the same bits on every run).  A key of a sequence that no query
  * sees gets zeros; rows outside every sequence are left as they were.  Errors
  * as zero_window_attention. */

@@ -126,3 +126,136 @@ def test_many_keys_far_below_another(zp, below, few, dim, dtype):  # noqa: F811
     err = want * (UT[b.dt] + (4 * below + 16 + 2 * 1024) * U32) + (others * step)[..., None]
     ref.check(out.t, want, ref.rounded(want, err, b.dt), "out")
     ref.check(lse, (below + torch.log1p(w)).T.expand(heads, -1), torch.full_like(lse, 2048 * U32 + 4 * below * U32, dtype=torch.float64), "lse")
+
+
+# ------------------------------------------------------------------ small and large gradients
+
+def sequence_backward(b, qs, ks, out, lse, window, sinks, scale, rows):
+    """dq, dk, dv of one sequence from the formulas in binary64, and what
+    binary32 may do to them: the errors of S, dP and delta (sums of d exact
+    products that may truncate) in each pair, independent from pair to pair.
+    rows: dq is to be compared row by row, where the roundings of dS are as few
+    as a row's keys (of the first rows' one or two to a head) and no mean:
+    each may be half a step, where the mean is 0.39 of one."""
+    group, d = b.heads // b.kv, b.dim
+    q, do, o = (x[qs].double() for x in (b.q, b.dout, out))
+    k, v = (x[ks].double() for x in (b.k, b.v))
+    mask = ref.seen(q.shape[0], k.shape[0], window, sinks, "cuda")
+    r = {n: torch.zeros_like(x) for n, x in (("dq", q), ("dk", k), ("dv", v))}
+    e = {n: torch.zeros_like(x) for n, x in r.items()}  # squares
+    for h in range(b.heads):
+        g = h // group
+        p = torch.exp((q[:, h] @ k[:, g].T) * scale - lse[h, qs].double()[:, None]).masked_fill_(~mask, 0.0)
+        delta = (do[:, h] * o[:, h]).sum(-1, keepdim=True)
+        ds = p * (do[:, h] @ v[:, g].T - delta)
+        ep = p * ((q[:, h].abs() @ k[:, g].abs().T) * scale * (2 * d * U32) + 32 * U32)
+        eds = p * (do[:, h].abs() @ v[:, g].abs().T * (2 * d * U32) + (do[:, h] * o[:, h]).abs().sum(-1, keepdim=True) * (d * U32)) + \
+            ep * (ds / p.clamp(min=1e-300)).abs()
+        r["dq"][:, h] = scale * ds @ k[:, g]
+        r["dk"][:, g] += scale * ds.T @ q[:, h]
+        r["dv"][:, g] += p.T @ do[:, h]
+        half = (UT[b.dt] * ds).square() if rows else 0.0
+        e["dq"][:, h] = scale ** 2 * (eds.square() + half) @ k[:, g].square()
+        e["dk"][:, g] += scale ** 2 * eds.square().T @ q[:, h].square()
+        e["dv"][:, g] += ep.square().T @ do[:, h].square()
+    return r, e
+
+
+def norm_wise(got, want, square, dtype, what, axes):
+    """Against the exact result rounded once.  The products' operands are
+    rounded once before (each by a relative error of the same distribution,
+    independent from term to term), and the output once: the square root of
+    two times the error of the output's rounding alone, for which 2 stands."""
+    off = (got.double() - want).square().sum(axes).sqrt()
+    # (of a value that 16 bits hold the operands were rounded all the same; 0.39 of half a step is the mean over all mantissas)
+    once = torch.maximum((want.to(dtype).double() - want).square().sum(axes).sqrt(),
+                         0.39 * UT[dtype] * want.square().sum(axes).sqrt())
+    assert bool(torch.isfinite(got).all()), what
+    assert bool((off <= 2 * once + square.sum(axes).sqrt()).all()), (what, float((off / once).max()))
+
+
+def check_norm_wise(zp, b, window, sinks, rows=False):  # noqa: F811
+    scale = b.dim ** -0.5
+    out, lse = b.forward(zp, window, sinks, scale)
+    ws = b.workspace(zp, window, sinks, True)
+    g = dict(zip(("dq", "dk", "dv"), (torch.zeros_like(x) for x in (b.q, b.k, b.v))))
+    zp.zero_window_attention_backward(b.dout, b.q, b.k, b.v, out.t, lse, *g.values(), ws, window, sinks, scale, **b.where)
+    assert zp.zero_workspace_stalls(ws) == 0
+    for qs, ks in b.slices():
+        want, square = sequence_backward(b, qs, ks, out.t, lse, window, sinks, scale, rows)
+        for name, at in (("dq", qs), ("dk", ks), ("dv", ks)):
+            norm_wise(g[name][at], want[name], square[name], b.dt, f"{name} {at}",
+                      (1, 2) if rows and name == "dq" else (0, 1, 2))
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("std", [1.0, 1e-2, 1e-3, 1e-4])
+def test_small_gradients_over_many_keys(zp, std, dim, dtype):  # noqa: F811
+    """P is about 1 / keys and dS a 4096th of the gradients, which 16 bits do
+    not hold as they are; dq, dk and dv are sums that they hold."""
+    b = Batch([(4096, 4096)], 4, 2, dim, dtype)
+    b.dout.copy_(randn(b.dout.shape, torch.float32, 9, std))
+    check_norm_wise(zp, b, None, 0)
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("dim", [64, 128])
+def test_small_gradients_of_first_keys_in_parts(zp, dim, dtype):  # noqa: F811
+    """The same where the first keys' queries are dealt out."""
+    b = Batch([(3000, 3000), (500, 700)], 4, 1, dim, dtype)
+    b.dout.copy_(randn(b.dout.shape, torch.float32, 9, 1e-3))
+    check_norm_wise(zp, b, 130, 4)
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("dim", [64, 128])
+def test_large_gradients(zp, dim, dtype):  # noqa: F811
+    """dP past 65504 (a scaled loss), over keys and queries so small that dq
+    and dk are not."""
+    b = Batch([(300, 300), (70, 200)], 4, 2, dim, dtype, std=0.05)
+    b.v.mul_(8.0)
+    b.dout.mul_(4000.0)
+    check_norm_wise(zp, b, None, 0)
+    check_norm_wise(zp, b, 40, 3)
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("dim", [64, 128])
+def test_gradients_of_many_sizes_in_one_call(zp, dim, dtype):  # noqa: F811
+    """Sequences whose gradients are 10^5 apart, and rows within one that are
+    a thousand apart: each sequence's dk and dv, and each row's dq, are as near
+    as by themselves."""
+    b = Batch([(1000, 1000), (900, 1200), (130, 130)], 4, 2, dim, dtype)
+    rows = torch.empty((b.tq, 1, 1), device="cuda").uniform_(-3, 0, generator=torch.Generator(device="cuda").manual_seed(3))
+    for (qs, _), size in zip(b.slices(), (100.0, 1e-3, 1.0)):
+        rows[qs] = 10 ** rows[qs] * size
+    b.dout.copy_(randn(b.dout.shape, torch.float32, 9) * rows)
+    b.dout[5:40] = 0.0  # (and rows without any)
+    check_norm_wise(zp, b, None, 0, rows=True)
+    check_norm_wise(zp, b, 200, 4, rows=True)
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+def test_dq_is_whole_when_the_waits_before_it_give_up(zp, dim):  # noqa: F811
+    """dk's and dv's kernel tells dq's how large the values are, also when its
+    own waits ran out (bounded, as the test of each kernel's waits has them)."""
+    import ctypes
+    hook = zp.lib().zero_test_window_attention_waits
+    hook.argtypes, hook.restype = [ctypes.c_int32, ctypes.c_uint64], None
+    b = Batch([(300, 300), (200, 400)], 4, 2, dim, "f16")
+    out, lse = b.forward(zp, 100, 2)
+    runs = []
+    for kernel in (-1, 1):
+        ws = b.workspace(zp, 100, 2, True)
+        g = [torch.zeros_like(x) for x in (b.q, b.k, b.v)]
+        hook(kernel, 20_000_000)
+        try:
+            zp.zero_window_attention_backward(b.dout, b.q, b.k, b.v, out.t, lse, *g, ws, 100, 2, **b.where)
+            stalls = zp.zero_workspace_stalls(ws)
+        finally:
+            hook(-1, 0)
+        assert (stalls > 0) == (kernel == 1)
+        runs.append(g)
+    assert bool(torch.isnan(runs[1][1]).all()) and bool(torch.isnan(runs[1][2]).all())
+    assert torch.equal(runs[0][0], runs[1][0])

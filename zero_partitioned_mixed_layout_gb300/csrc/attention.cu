@@ -1152,13 +1152,70 @@ __global__ void __launch_bounds__(kFewWarps * 32) k_attn_few(const __grid_consta
 // where no key is seen, which makes every weight 0) and delta = dout . out.
 // Laid out by tile of 128 queries, so that a tile's are one aligned copy:
 // [head][tile number][lse of 128, delta of 128].
+//
+// f16 holds neither the weights of many keys (a 16384th and less) nor dS of
+// small gradients or of a scaled loss, so there the backward pass rounds
+// powers of two times them, which leave the sums at the end.  For P it is
+// 2^kShiftP (P is at most 1); for dS the largest that keeps it below 2^15
+// whatever the products give:
+//     |dS_ij| <= |dout_i| sqrt(d) max |v_j| + |delta_i|    (P is at most 1),
+// for the dk of a key by its own value and the largest of its tile's queries,
+// for a query's dq by its own row and the values of the tiles of keys that it
+// may see.  (Unscaled, dq of normal inputs over 4096 keys and gradients of
+// 10^-4 was off by a tenth, and one of 10^5 was inf.)  5340 tokens of 25 heads
+// of 64: 117.5 us, 108.3 without: the units' largest rows and values, and
+// dS' times its power of two.
+struct Sizes {
+    float *rows;    // sqrt(d) |dout|: [head][tile number][128]
+    float2 *tops;   // of 32 rows, the largest of these and of |delta|: [head][tile number][4]
+    float *values;  // largest elements of 32 rows of v, from k_attn_dkv: [key head][tile number of the keys][4]
+};
+
 struct StatsArgs {
     Attn a;
     Heads dout, out;
     const float *lse;
     float *stats;
+    Sizes sizes;
     int64_t tiles;
 };
+
+template <int DT>
+constexpr bool kScaled = DT == ZERO_F16;
+template <int DT>
+constexpr float kShiftP = kScaled<DT> ? 15.0f : 0.0f;
+
+__device__ __forceinline__ float power_of_two(int32_t c) { return __uint_as_float((uint32_t)(c + 127) << 23); }
+
+// c with bound 2^c below 2^15 and not below 2^14 (100 of nothing; as low as
+// -100 of what is no number, which reaches what it is in all the same).
+__device__ __forceinline__ int32_t dS_exponent(float bound)
+{
+    const int32_t c = 14 + 127 - (int32_t)(__float_as_uint(bound) >> 23);
+    return c < -100 ? -100 : c > 100 ? 100 : c;
+}
+
+// Of values that are at least 0, whose bits are in their order.
+__device__ __forceinline__ float warp_max(float x)
+{
+    return __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(x)));
+}
+
+// Sums over the L lanes of a row, of L rows at once: lane i of them gets that
+// of row i, after L - 1 exchanges.
+template <int L>
+__device__ __forceinline__ float row_sums(float (&x)[L], int at)
+{
+#pragma unroll
+    for (int o = L / 2; o > 0; o >>= 1)
+#pragma unroll
+        for (int i = 0; i < o; ++i) {
+            const bool upper = at & o;
+            const float give = upper ? x[i] : x[i + o], keep = upper ? x[i + o] : x[i];
+            x[i] = keep + __shfl_xor_sync(0xffffffffu, give, o);
+        }
+    return x[0];
+}
 
 // A warp takes 32 queries of a tile and the heads of its block: lse by one
 // lane per query, dout and out by 2 to 16 lanes to a row.  Bound by the two
@@ -1169,22 +1226,22 @@ __global__ void __launch_bounds__(128) k_attn_stats(const __grid_constant__ Stat
     constexpr int kRows = 32 / L;
     const Attn &a = f.a;
     const int part = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = lane / L, at = lane & (L - 1);
+    const bool in = at * 8 < a.dim;
     pdl_launch_next();
     for (int64_t number = blockIdx.x; number < f.tiles; number += gridDim.x) {
         const TileAt t = find_tile(a, a.q_offsets, a.q_tokens, number, 128, false, lane);
         const int32_t first = t.first + 32 * part, left = t.s.lq - first;  // of this warp
         if (!t.any)
             continue;
-        const bool in = at * 8 < a.dim;
         const uint16_t *const x0 = static_cast<const uint16_t *>(f.dout.p) + (t.s.q0 + first + sub) * f.dout.ld + at * 8;
         const uint16_t *const y0 = static_cast<const uint16_t *>(f.out.p) + (t.s.q0 + first + sub) * f.out.ld + at * 8;
         for (int32_t h = blockIdx.y; h < a.q_heads; h += gridDim.y) {
             const float lse = lane < left ? f.lse[(int64_t)h * a.q_tokens + t.s.q0 + first + lane] : -INFINITY;
             const uint16_t *const xh = x0 + h * f.dout.hd, *const yh = y0 + h * f.out.hd;
-            float mine = 0.0f;
-#pragma unroll 8
+            float sums[L], squares[L];
+#pragma unroll
             for (int i = 0; i < L; ++i) {
-                float sum = 0.0f;
+                sums[i] = squares[i] = 0.0f;
                 if (in && kRows * i + sub < left) {
                     const uint4 x = __ldg(reinterpret_cast<const uint4 *>(xh + (int64_t)kRows * i * f.dout.ld));
                     const uint4 y = __ldg(reinterpret_cast<const uint4 *>(yh + (int64_t)kRows * i * f.out.ld));
@@ -1192,19 +1249,26 @@ __global__ void __launch_bounds__(128) k_attn_stats(const __grid_constant__ Stat
                     Elem<DT>::to_float(&x, fx);
                     Elem<DT>::to_float(&y, fy);
 #pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        sum += fx[e] * fy[e];
+                    for (int e = 0; e < 8; ++e) {
+                        sums[i] += fx[e] * fy[e];
+                        if (kScaled<DT>)
+                            squares[i] += fx[e] * fx[e];
+                    }
                 }
-#pragma unroll
-                for (int o = L / 2; o > 0; o >>= 1)
-                    sum += __shfl_xor_sync(0xffffffffu, sum, o);
-                // row kRows i + s is the sum of lanes L s on: query `lane` gets its own
-                const float v = __shfl_sync(0xffffffffu, sum, (lane & (kRows - 1)) * L);
-                mine = lane / kRows == i ? v : mine;
             }
+            // lane L s + i has row kRows i + s: query `lane` gets its own
+            const int from = (lane & (kRows - 1)) * L + lane / kRows;
+            const float delta = __shfl_sync(0xffffffffu, row_sums<L>(sums, at), from);
             float *const to = f.stats + (h * f.tiles + number) * 256 + 32 * part + lane;
             to[0] = lse == -INFINITY ? INFINITY : lse;
-            to[128] = mine;
+            to[128] = delta;
+            if (kScaled<DT>) {
+                const float size = sqrtf(__shfl_sync(0xffffffffu, row_sums<L>(squares, at), from) * a.dim);
+                f.sizes.rows[(h * f.tiles + number) * 128 + 32 * part + lane] = size;
+                const float2 tops = make_float2(warp_max(size), warp_max(fabsf(delta)));
+                if (lane == 0)
+                    f.sizes.tops[(h * f.tiles + number) * 4 + part] = tops;
+            }
         }
     }
 }
@@ -1214,24 +1278,26 @@ __global__ void __launch_bounds__(128) k_attn_stats(const __grid_constant__ Stat
 // whatever its score.  (One operation, with scale and lse in units of log 2,
 // is off by their roundings: 2^-23 of the score, so by factors from 10^7 on.
 // 16384 tokens of 64 + 8 heads of 128 took 2745 us with it and take 2777 with
-// three; 5340 of 25 heads of 64 103 and 106.7.)  zero2: see BwdTiles.
-__device__ __forceinline__ F2 weights(F2 s, F2 scale2, F2 zero2, F2 less_lse)
+// three; 5340 of 25 heads of 64 103 and 106.7.)  zero2: see BwdTiles.  Times
+// 2^shift.
+__device__ __forceinline__ F2 weights(F2 s, F2 scale2, F2 zero2, F2 less_lse, F2 shift2)
 {
-    return exp2_fast((fma2(s, scale2, zero2) + less_lse) * twice(1.4426950408889634f));
+    return exp2_fast(fma2(fma2(s, scale2, zero2) + less_lse, twice(1.4426950408889634f), shift2));
 }
 
 struct BwdTiles {
     HeadsMap q, k, v, dout;
     Attn a;
-    Heads dq, dk, dv;
+    Heads dq, dk, dv, v_rows;
     const float *stats;
+    Sizes sizes;
     int64_t q_tiles, k_tiles;  // tile numbers of 128 queries, and keys
     // first keys seen by all queries: their tiles' queries in parts of `chunk` tiles
     int32_t chunk, sink_tiles;
     int64_t split_units;
     float *partial;  // [split unit][dv, dk][128][dim]
     float scale;
-    float zero;         // 0, but not so that the compiler could tell: added to a product that is to be rounded by itself
+    float zero;  // 0, but not so that the compiler could tell: added to a product that is to be rounded by itself
     WsHeader *hdr;
     uint64_t limit_ns;
 };
@@ -1263,7 +1329,8 @@ __device__ __forceinline__ bool is_split(const BwdTiles &f, int32_t j, const Que
 struct KeyUnit {
     int32_t k_row, q_row, first, lq, lk, head;  // first key of its sequence; q_row: the sequence's first query
     int32_t low, high;                          // query tiles
-    int64_t stats;                              // tile number of query tile 0
+    int64_t stats, keys;                        // tile numbers of query tile 0, of key tile 0
+    float row, delta;                           // largest of the queries' (f16)
     int64_t slot;                               // of the partial sums, or -1
     int32_t end;
 
@@ -1335,7 +1402,42 @@ __device__ __forceinline__ bool key_unit(const BwdTiles &f, int64_t i, int lane,
     u.q_row = (int32_t)at.s.q0;
     u.lq = at.s.lq, u.lk = at.s.lk;
     u.stats = a.q_offsets ? at.s.q0 / 128 + at.index : 0;
+    u.keys = k_offsets ? at.s.k0 / 128 + at.index : 0;
+    u.row = u.delta = 0.0f;
     return true;
+}
+
+// The largest row and delta of a unit's queries, by a whole warp, a share to
+// each lane: an entry for every 32 queries and head (they fit 31 bits: there
+// is memory for them), 32 at a time.
+template <int T>
+__device__ __forceinline__ float2 unit_tops(const BwdTiles &f, const KeyUnit &u, int lane)
+{
+    const int32_t n = (u.high - u.low + 1) * (T / 32), all = n * f.a.group;
+    const float2 *const from = f.sizes.tops + ((int64_t)u.head * f.a.group * f.q_tiles + u.stats) * 4 + u.low * (T / 32);
+    float2 top = make_float2(0.0f, 0.0f);
+#pragma unroll 4
+    for (int32_t i = lane; i < all; i += 32) {
+        const int32_t h = i / n;
+        const float2 x = from[h * f.q_tiles * 4 + i - h * n];
+        top.x = fmaxf(top.x, x.x), top.y = fmaxf(top.y, x.y);
+    }
+    return top;
+}
+
+// The largest element of a row of f16 in shared memory: 128 bytes in each of
+// BOXES boxes, in whatever order the swizzle left them.
+template <int BOXES>
+__device__ __forceinline__ float largest_of_row(const unsigned char *tile, int row)
+{
+    __half2 top = __half2half2(__ushort_as_half(0));
+#pragma unroll
+    for (int k = 0; k < 8 * BOXES; ++k) {
+        const uint4 x = *reinterpret_cast<const uint4 *>(tile + (k >> 3) * 16384 + row * 128 + ((k ^ row) & 7) * 16);
+        const __half2 *h = reinterpret_cast<const __half2 *>(&x);
+        top = __hmax2(__hmax2(__hmax2(top, __habs2(h[0])), __habs2(h[1])), __hmax2(__habs2(h[2]), __habs2(h[3])));
+    }
+    return fmaxf(__low2float(top), __high2float(top));
 }
 
 // dk and dv of 128 keys of one key head at a time, over the query heads of
@@ -1443,10 +1545,15 @@ __global__ void __launch_bounds__(S::THREADS, S::PER_SM) k_attn_dkv(const __grid
             KeyUnit u;
             if (!key_unit<BN>(f, i, lane, u))
                 continue;
-            ok = publish(u);
-            if (!ok || u.low > u.high)
+            if (u.low > u.high) {
+                ok = publish(u);
                 continue;
-            ok = wait(&sh.kv_empty, (kvn & 1) ^ 1);
+            }
+            if (kScaled<DT>) {
+                const float2 tops = unit_tops<BN>(f, u, lane);
+                u.row = warp_max(tops.x), u.delta = warp_max(tops.y);
+            }
+            ok = publish(u) && wait(&sh.kv_empty, (kvn & 1) ^ 1);
             if (!ok)
                 break;
             if (elect_one()) {
@@ -1566,6 +1673,17 @@ __global__ void __launch_bounds__(S::THREADS, S::PER_SM) k_attn_dkv(const __grid
         while (ok && next(u)) {
             const int32_t count = u.low > u.high ? 0 : (u.high - u.low + 1) * a.group;
             const int32_t j = u.first + quarter * 32 + lane;
+            float more = 1.0f;  // from P's power of two to that of this key's dS'
+            if (kScaled<DT> && count > 0) {
+                ok = wait(&sh.kv_full, accs & 1);
+                if (!ok)
+                    break;
+                const float value = j < u.lk ? largest_of_row<S::BOXES>(s_v, quarter * 32 + lane) : 0.0f;
+                more = power_of_two(dS_exponent(u.row * value + u.delta) - (int32_t)kShiftP<DT>);
+                const float top = warp_max(value);
+                if (lane == 0 && half == 0)
+                    f.sizes.values[(u.head * f.k_tiles + u.keys + u.first / 128) * 4 + quarter] = top;
+            }
             int32_t t = u.low;
             for (int32_t i = 0; i < count; ++i, ++qn, ++n) {
                 const uint32_t st = qn % S::STAGES;
@@ -1592,7 +1710,8 @@ __global__ void __launch_bounds__(S::THREADS, S::PER_SM) k_attn_dkv(const __grid
                 }
                 F2 p[2][16];
                 uint32_t bits[2] = {~0u, ~0u};
-                const F2 scale2 = twice(f.scale), zero2 = twice(f.zero);
+                const F2 scale2 = twice(f.scale), zero2 = twice(f.zero), shift2 = twice(kShiftP<DT>);
+                const F2 more2 = twice(more);
                 // piece c is done (of 64 columns, both are when the second is)
                 auto ready = [&](uint64_t *bar, int c) {
                     if (BN == 64 && c == 0)
@@ -1611,8 +1730,8 @@ __global__ void __launch_bounds__(S::THREADS, S::PER_SM) k_attn_dkv(const __grid
 #pragma unroll
                     for (int e = 0; e < 16; e += 2) {
                         const float4 x = *reinterpret_cast<const float4 *>(lse + at + 2 * e);
-                        p[c][e] = weights({__uint_as_float(r[2 * e]), __uint_as_float(r[2 * e + 1])}, scale2, zero2, {-x.x, -x.y});
-                        p[c][e + 1] = weights({__uint_as_float(r[2 * e + 2]), __uint_as_float(r[2 * e + 3])}, scale2, zero2, {-x.z, -x.w});
+                        p[c][e] = weights({__uint_as_float(r[2 * e]), __uint_as_float(r[2 * e + 1])}, scale2, zero2, {-x.x, -x.y}, shift2);
+                        p[c][e + 1] = weights({__uint_as_float(r[2 * e + 2]), __uint_as_float(r[2 * e + 3])}, scale2, zero2, {-x.z, -x.w}, shift2);
                     }
                     if (!whole) {
                         bits[c] = ~bits_up_to(j - p0 - 1 - at) & bits_up_to(nq - 1 - at);
@@ -1647,6 +1766,8 @@ __global__ void __launch_bounds__(S::THREADS, S::PER_SM) k_attn_dkv(const __grid
                         const float4 x = *reinterpret_cast<const float4 *>(delta + at + 2 * e);
                         p[c][e] = p[c][e] * (F2{__uint_as_float(r[2 * e]), __uint_as_float(r[2 * e + 1])} + F2{-x.x, -x.y});
                         p[c][e + 1] = p[c][e + 1] * (F2{__uint_as_float(r[2 * e + 2]), __uint_as_float(r[2 * e + 3])} + F2{-x.z, -x.w});
+                        if (kScaled<DT>)
+                            p[c][e] = p[c][e] * more2, p[c][e + 1] = p[c][e + 1] * more2;
                     }
                     if (!whole) {
 #pragma unroll
@@ -1676,6 +1797,7 @@ __global__ void __launch_bounds__(S::THREADS, S::PER_SM) k_attn_dkv(const __grid
             for (int which = S::ROW_WARPS == 8 ? half : 0; which < (S::ROW_WARPS == 8 ? half + 1 : 2); ++which) {
                 const uint32_t from = tmem + lanes + (which ? kDk : kDv);
                 const float by = which ? f.scale : 1.0f;
+                const float back = kScaled<DT> ? power_of_two(-(int32_t)kShiftP<DT>) / (which ? more : 1.0f) : 1.0f;
                 const Heads to{which ? f.dk.p : f.dv.p, which ? f.dk.ld : f.dv.ld, which ? f.dk.hd : f.dv.hd};
                 uint16_t *out = static_cast<uint16_t *>(const_cast<void *>(to.p)) + ((int64_t)u.k_row + quarter * 32) * to.ld +
                                 u.head * to.hd;
@@ -1689,6 +1811,10 @@ __global__ void __launch_bounds__(S::THREADS, S::PER_SM) k_attn_dkv(const __grid
                     if (count > 0) {
                         tmem_load32(from + c, o);
                         tmem_wait_loads(o);
+                        if (kScaled<DT>)
+#pragma unroll
+                            for (int e = 0; e < 32; ++e)
+                                o[e] = __float_as_uint(__uint_as_float(o[e]) * back);
                     }
                     if (u.slot >= 0) {
 #pragma unroll
@@ -1723,6 +1849,15 @@ __global__ void __launch_bounds__(S::THREADS, S::PER_SM) k_attn_dkv(const __grid
             KeyUnit u;
             if (!key_unit<BN>(f, i, lane, u))
                 continue;
+            if (kScaled<DT> && u.low <= u.high && warp < 4) {  // (k_attn_dq's results are whole)
+                float top = 0.0f;
+                for (int32_t r = 32 * warp; r < 32 * warp + 32 && u.first + r < u.lk; ++r)
+                    for (int e = lane; e < a.dim; e += 32)
+                        top = fmaxf(top, fabsf(load1<DT>(f.v_rows.p, (u.k_row + (int64_t)r) * f.v_rows.ld + u.head * f.v_rows.hd + e)));
+                top = warp_max(top);
+                if (lane == 0)
+                    f.sizes.values[(u.head * f.k_tiles + u.keys + u.first / 128) * 4 + warp] = top;
+            }
             for (int32_t r = warp; r < 128; r += S::THREADS / 32)
                 for (int e = lane; e < a.dim; e += 32)
                     if (u.slot >= 0) {
@@ -1777,7 +1912,8 @@ __global__ void __launch_bounds__(kThreads) k_attn_join(const __grid_constant__ 
 
 struct QueryUnit {
     int32_t q_row, k_row, first, lq, lk, head;
-    int64_t stats;  // tile number
+    int64_t stats, keys;  // tile number, and that of key tile 0
+    float value;          // the largest of the keys' tiles (f16)
     int32_t end;
 
     __device__ __forceinline__ void agree()
@@ -1870,7 +2006,8 @@ __global__ void __launch_bounds__(S::THREADS, S::PER_SM) k_attn_dq(const __grid_
     auto unit_at = [&](int64_t i, QueryUnit &u) {
         const int64_t number = f.q_tiles - 1 - i / a.q_heads;  // long ones first
         const TileAt at = find_tile(a, a.q_offsets, a.q_tokens, number, 128, false, lane);
-        u = QueryUnit{(int32_t)at.s.q0 + at.first, (int32_t)at.s.k0, at.first, at.s.lq, at.s.lk, (int32_t)(i % a.q_heads), number, 0};
+        u = QueryUnit{(int32_t)at.s.q0 + at.first, (int32_t)at.s.k0, at.first, at.s.lq, at.s.lk, (int32_t)(i % a.q_heads), number,
+                      a.k_offsets || a.q_offsets ? at.s.k0 / 128 + at.index : 0, 0.0f, 0};
         return at.any;
     };
 
@@ -1899,12 +2036,24 @@ __global__ void __launch_bounds__(S::THREADS, S::PER_SM) k_attn_dq(const __grid_
             QueryUnit u;
             if (!unit_at(i, u))
                 continue;
-            ok = publish(u);
             const KeyTiles kt = key_tiles<BN>(a, u.first, u.lq, u.lk);
             const TileList list = tile_list(kt, KeyTiles{0, -1, 0, false});
-            if (!ok || list.n == 0)
+            if (list.n == 0) {
+                ok = publish(u);
                 continue;
-            ok = wait(&sh.q_empty, (un & 1) ^ 1);
+            }
+            if (kScaled<DT>) {
+                // first keys' tiles, then the window's; a share to each lane
+                const float4 *const values = reinterpret_cast<const float4 *>(f.sizes.values) + u.head / a.group * f.k_tiles + u.keys;
+                const int32_t sinks = (list.sinks * BN + 127) / 128, low = list.low * BN / 128, n = sinks + list.high * BN / 128 - low + 1;
+                for (int32_t k = lane; k < n; k += 32) {
+                    const float4 v = values[k < sinks ? k : low + k - sinks];
+                    u.value = fmaxf(u.value, fmaxf(fmaxf(v.x, v.y), fmaxf(v.z, v.w)));
+                }
+            }
+            if (kScaled<DT>)
+                u.value = warp_max(u.value);
+            ok = publish(u) && wait(&sh.q_empty, (un & 1) ^ 1);
             if (!ok)
                 break;
             if (elect_one()) {
@@ -1915,7 +2064,7 @@ __global__ void __launch_bounds__(S::THREADS, S::PER_SM) k_attn_dq(const __grid_
             __syncwarp();
             ++un;
             const int32_t g = u.head / a.group;
-            for (int32_t n = 0; n < list.n; ++n, ++kn) {
+            for (int32_t n = 0; ok && n < list.n; ++n, ++kn) {
                 const uint32_t st = kn % S::STAGES, parity = ((kn / S::STAGES) & 1) ^ 1;
                 const int32_t row = u.k_row + BN * list.at(n);
                 ok = wait(&sh.k_empty[st], parity);
@@ -2022,6 +2171,9 @@ __global__ void __launch_bounds__(S::THREADS, S::PER_SM) k_attn_dq(const __grid_
             const int32_t p_last = (u.first + 127 < u.lq ? u.first + 127 : u.lq - 1) + u.lk - u.lq;
             const float *stats = f.stats + (u.head * f.q_tiles + u.stats) * 256 + quarter * 32 + lane;
             const float lse = stats[0], delta = stats[128];
+            int32_t exponent = 0;  // of this row's dS
+            if (kScaled<DT> && list.n > 0)
+                exponent = dS_exponent(f.sizes.rows[(u.head * f.q_tiles + u.stats) * 128 + quarter * 32 + lane] * u.value + fabsf(delta));
             for (int32_t n = 0; n < list.n; ++n, ++kn) {
                 const uint32_t st = kn % S::STAGES, buf = kn & 1;
                 const int32_t k_first = list.at(n) * BN;
@@ -2033,7 +2185,7 @@ __global__ void __launch_bounds__(S::THREADS, S::PER_SM) k_attn_dq(const __grid_
                 tmem_fence_after();
                 const uint32_t at_s = tmem + lanes + buf * BN, at_p = tmem + lanes + kDp;
                 F2 w2[2][16];
-                const F2 scale2 = twice(f.scale), zero2 = twice(f.zero), lse2 = twice(-lse), delta2 = twice(-delta);
+                const F2 scale2 = twice(f.scale), zero2 = twice(f.zero), lse2 = twice(-lse), delta2 = twice(-delta), shift2 = twice((float)exponent);
                 // the weights, while dP is worked out
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
@@ -2042,7 +2194,7 @@ __global__ void __launch_bounds__(S::THREADS, S::PER_SM) k_attn_dq(const __grid_
                     tmem_wait_loads(r);
 #pragma unroll
                     for (int e = 0; e < 16; ++e)
-                        w2[c][e] = weights({__uint_as_float(r[2 * e]), __uint_as_float(r[2 * e + 1])}, scale2, zero2, lse2);
+                        w2[c][e] = weights({__uint_as_float(r[2 * e]), __uint_as_float(r[2 * e + 1])}, scale2, zero2, lse2, shift2);
                 }
                 if (k_first + BN > u.lk) {
                     // rows behind the last key: zeros, since 0 times what they hold may not be 0
@@ -2106,6 +2258,10 @@ __global__ void __launch_bounds__(S::THREADS, S::PER_SM) k_attn_dq(const __grid_
                 if (list.n > 0) {
                     tmem_load32(tmem + lanes + kDq + c, o);
                     tmem_wait_loads(o);
+                    if (kScaled<DT>)
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)
+                            o[e] = __float_as_uint(__uint_as_float(o[e]) * power_of_two(-exponent));
                 }
 #pragma unroll
                 for (int e = 0; e < 16; ++e)
@@ -2392,7 +2548,7 @@ SinkPlan plan_sinks(const zero_attention_t *a, bool one, bool space)
 // keeps: a few queries' partial sums, or the backward pass's rows and sums.
 struct AttnSpace {
     size_t partial;         // of a few queries
-    size_t stats, sums;     // of the backward pass
+    size_t stats, rows, tops, values, sums;  // of the backward pass
     size_t total;
 };
 
@@ -2419,7 +2575,12 @@ AttnSpace attn_space(const zero_attention_t *a, bool backward)
     }
     s.total = s.partial + align256(few);
     if (backward) {
-        s.sums = s.stats + (size_t)a->q_heads * (size_t)tile_numbers(a->q_tokens, a->sequences, false, 128) * 1024;
+        const size_t q_tiles = (size_t)a->q_heads * (size_t)tile_numbers(a->q_tokens, a->sequences, false, 128);
+        const size_t k_tiles = (size_t)a->k_heads * (size_t)tile_numbers(a->k_tokens, a->sequences, false, 128);
+        s.rows = s.stats + q_tiles * 1024;
+        s.tops = s.rows + q_tiles * 512;
+        s.values = s.tops + align256(q_tiles * 32);
+        s.sums = s.values + align256(k_tiles * 16);
         const size_t end = s.sums + align256((size_t)plan_sinks(a, false, true).units * 256 * (size_t)a->head_dim * 4);
         s.total = s.total > end ? s.total : end;
     }
@@ -2567,19 +2728,22 @@ extern "C" int zero_window_attention_backward(const zero_attention_t *a, const v
         return ZERO_OK;
     BwdTiles t{};
     t.a = attn_of(a);
-    t.dq = hdq, t.dk = hdk, t.dv = hdv;
+    t.dq = hdq, t.dk = hdk, t.dv = hdv, t.v_rows = hv;
     const bool one = !a->q_offsets;
     t.q_tiles = a->q_tokens > 0 ? tile_numbers(a->q_tokens, a->sequences, one, 128) : 0;
     t.k_tiles = a->k_tokens > 0 ? tile_numbers(a->k_tokens, a->sequences, one && !a->k_offsets, 128) : 0;
     t.stats = reinterpret_cast<float *>(static_cast<char *>(ws) + sp.stats);
+    t.sizes = {reinterpret_cast<float *>(static_cast<char *>(ws) + sp.rows),
+               reinterpret_cast<float2 *>(static_cast<char *>(ws) + sp.tops),
+               reinterpret_cast<float *>(static_cast<char *>(ws) + sp.values)};
     t.partial = reinterpret_cast<float *>(static_cast<char *>(ws) + sp.sums);
     t.scale = (float)a->scale;
     t.hdr = static_cast<WsHeader *>(ws);
     if (a->q_tokens > 0) {
         const SinkPlan p = plan_sinks(a, one, false);
         t.chunk = p.chunk, t.sink_tiles = p.sink_tiles, t.split_units = p.units;
-        const StatsArgs s{t.a, hdout, hout, lse, const_cast<float *>(t.stats), t.q_tiles};
         const bool f16 = a->dtype == ZERO_F16;
+        const StatsArgs s{t.a, hdout, hout, lse, const_cast<float *>(t.stats), t.sizes, t.q_tiles};
         auto kernel = a->head_dim <= 16   ? f16 ? k_attn_stats<ZERO_F16, 2> : k_attn_stats<ZERO_BF16, 2>
                       : a->head_dim <= 64 ? f16 ? k_attn_stats<ZERO_F16, 8> : k_attn_stats<ZERO_BF16, 8>
                                           : f16 ? k_attn_stats<ZERO_F16, 16> : k_attn_stats<ZERO_BF16, 16>;
