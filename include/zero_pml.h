@@ -815,7 +815,7 @@ typedef struct zero_attention {
     int32_t dtype;            /* ZERO_F16 or ZERO_BF16, of every array but lse */
     int64_t window;           /* at least 1; INT64_MAX: no window */
     int64_t sinks;            /* first keys that every later query sees; at least 0 */
-    double scale;             /* of q.k: positive, finite */
+    double scale;             /* of q.k: positive, times log2(e) within binary32 */
     const int64_t *q_offsets, *k_offsets, *k_lengths;
 } zero_attention_t;
 
@@ -839,7 +839,7 @@ typedef struct zero_attention {
  * takes it: a bounded wait that gave up is counted there and leaves NaN in
  * what it would have written.
  * Errors: ZERO_EINVAL (NULL, a negative size, a stride that is not positive, window < 1, sinks < 0, scale not
- * positive or not finite, k_lengths without k_offsets, sequences not 1
+ * positive or past binary32 times log2(e), k_lengths without k_offsets, sequences not 1
  * without q_offsets), ZERO_EALIGN, ZERO_EDTYPE, ZERO_ESIZE (head_dim; heads
  * that do not divide or past 2^15; q_tokens, k_tokens or sequences past 2^31 -
  * 512; k_tokens not q_tokens without k_offsets; strides past 2^38),

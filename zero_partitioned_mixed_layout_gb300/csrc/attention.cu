@@ -2301,6 +2301,8 @@ __global__ void __launch_bounds__(S::THREADS, S::PER_SM) k_attn_dq(const __grid_
 constexpr int64_t kMostRows = ((int64_t)1 << 31) - 512;
 constexpr int32_t kMostHeads = 1 << 15;
 
+constexpr double kLog2E = 1.4426950408889634;
+
 int check_attention(const zero_attention_t *a)
 {
     if (!a)
@@ -2308,7 +2310,7 @@ int check_attention(const zero_attention_t *a)
     if (!lp_dtype_ok(a->dtype))
         return ZERO_EDTYPE;
     if (a->q_tokens < 0 || a->k_tokens < 0 || a->sequences < 0 || a->q_heads < 1 || a->k_heads < 1 ||
-        a->head_dim < 1 || a->window < 1 || a->sinks < 0 || !(a->scale > 0) || !std::isfinite((float)a->scale))
+        a->head_dim < 1 || a->window < 1 || a->sinks < 0 || !(a->scale > 0) || !std::isfinite((float)(a->scale * kLog2E)))
         return ZERO_EINVAL;
     if (a->q_tokens > kMostRows || a->k_tokens > kMostRows || a->sequences > kMostRows || a->q_heads > kMostHeads ||
         a->q_heads % a->k_heads != 0 || a->head_dim % 8 != 0 || a->head_dim > kMostDim)
@@ -2440,7 +2442,7 @@ int forward_tiles(const Fwd &f, const zero_attention_t *a, void *ws, cudaStream_
 {
     FwdTiles t{};
     t.a = f.a, t.out = f.out, t.lse = f.lse;
-    t.scale_log2 = (float)(a->scale * 1.4426950408889634);
+    t.scale_log2 = (float)(a->scale * kLog2E);
     t.hdr = static_cast<WsHeader *>(ws);
     t.limit_ns = kWaitLimit;
     if (a->head_dim <= 64)
@@ -2498,7 +2500,7 @@ int launch_few(const FewArgs &t, int64_t blocks, cudaStream_t st)
 int forward_few(const Fwd &f, const zero_attention_t *a, void *ws, size_t partial, cudaStream_t st)
 {
     const FewPlan p = plan_few(a, a->q_tokens, !a->q_offsets);
-    FewArgs t{f.a, f.q, f.k, f.v, f.out, f.lse, p.tiles, p.tokens, p.parts, p.splits, (float)(a->scale * 1.4426950408889634),
+    FewArgs t{f.a, f.q, f.k, f.v, f.out, f.lse, p.tiles, p.tokens, p.parts, p.splits, (float)(a->scale * kLog2E),
               reinterpret_cast<uint32_t *>(static_cast<char *>(ws) + 256),
               reinterpret_cast<float *>(static_cast<char *>(ws) + partial)};
     const int64_t blocks = p.sets * p.splits;
