@@ -21,7 +21,6 @@
 // Three ways: tiles of 128 queries on the tensor cores (k_attn_tiles), a few
 // queries per sequence (k_attn_few), and the backward pass (k_attn_stats,
 // k_attn_dkv, k_attn_dq, k_attn_join).
-#include <atomic>
 #include <cmath>
 #include <initializer_list>
 
@@ -2397,15 +2396,16 @@ constexpr uint64_t kWaitLimit = 4000000000u;
 
 // For tests: kernel test_short (0 the forward tiles, 1 dk and dv, 2 dq) asks
 // for boxes of queries eight rows too low, so that no tile of them is ever
-// whole and its waits run out after test_limit_ns.
-std::atomic<int32_t> test_short{-1};
-std::atomic<uint64_t> test_limit_ns{0};
+// whole and its waits run out after test_limit_ns, in the calls of the
+// thread that set it and in no other's.
+thread_local int32_t test_short = -1;
+thread_local uint64_t test_limit_ns = 0;
 
 int short_by(int kernel, uint64_t *limit_ns)
 {
-    if (test_short.load(std::memory_order_relaxed) != kernel)
+    if (test_short != kernel)
         return 0;
-    *limit_ns = test_limit_ns.load(std::memory_order_relaxed);
+    *limit_ns = test_limit_ns;
     return 8;
 }
 

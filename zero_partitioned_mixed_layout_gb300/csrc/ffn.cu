@@ -1,7 +1,6 @@
 // The gated feed-forward block, forward and backward: five products on the
 // tensor cores (tcgen05, operands by TMA, sums in tensor memory) with the
 // activation and its slope in their epilogues.
-#include <atomic>
 
 #include "sublayer.cuh"
 #include "tensor.cuh"
@@ -1160,9 +1159,10 @@ int copy_operands(Mat **mats, int n, char *to, bool *copied, bool zeros, cudaStr
 
 // For tests: products whose epilogue is test_short ask for boxes of A eight
 // rows too low, so that no block of k is ever whole and their waits run out
-// after test_limit_ns.
-std::atomic<int32_t> test_short{-1};
-std::atomic<uint64_t> test_limit_ns{0};
+// after test_limit_ns, in the calls of the thread that set it and in no
+// other's.
+thread_local int32_t test_short = -1;
+thread_local uint64_t test_limit_ns = 0;
 
 // One product of a launch.
 struct Spec {
@@ -1211,7 +1211,7 @@ int launch_products(const Spec *specs, int n, ProductArgs<NP, EPI> &g, int split
     g.stage_bytes = g.a_rows * 128 + S::B_BYTES;
     g.stages = S::STAGES * S::STAGE / g.stage_bytes;
     g.stages = g.stages < kMaxStages ? g.stages : kMaxStages;
-    const bool fails = test_short.load(std::memory_order_relaxed) == EPI;
+    const bool fails = test_short == EPI;
     const int a_box = (a_mn ? 64 : g.a_rows) - (fails ? 8 : 0);
     int64_t tiles = 0, longest = 0;
     for (int q = 0; q < n; ++q) {
@@ -1233,7 +1233,7 @@ int launch_products(const Spec *specs, int n, ProductArgs<NP, EPI> &g, int split
     if (tiles * splits > 0x3fffffff)
         return ZERO_ESIZE;
     g.tiles = (int32_t)tiles;
-    g.limit_ns = fails ? test_limit_ns.load(std::memory_order_relaxed) : 2000000000ull + (uint64_t)longest * 4000;
+    g.limit_ns = fails ? test_limit_ns : 2000000000ull + (uint64_t)longest * 4000;
     auto kernel = k_ffn_product<S, DT, EPI, MAJ, NP>;
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::SMEM);
     const int64_t workers = (int64_t)sm_count() / S::CG * S::PER_SM;
