@@ -96,6 +96,35 @@ def test_one_key_takes_all_backward(zp, size, scale, lens, dim, dtype):  # noqa:
         ref.check(got, value, ref.rounded(value, err + 4 * U32 * value.abs(), b.dt), name)
 
 
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("dim", [64, 80, 128])
+@pytest.mark.parametrize("std", [100.0, 1000.0])
+def test_scores_that_binary32_rounds_are_the_same_in_both_passes(zp, std, dim, dtype):  # noqa: F811
+    """Sums of random products of up to 10^8, which one more or one less
+    rounding changes by up to 8: lse is of the very scores that the backward
+    pass forms, so that the P of a key that takes all is 1 all the same.  (dv
+    of a gradient of 1 in one element adds up P.)"""
+    b = Batch([(300, 300), (200, 400)], 4, 2, dim, dtype, std=std)
+    out, lse = b.forward(zp, None, 0, 1.0)
+    want = torch.zeros((b.tk, 2), dtype=torch.float64, device="cuda")
+    b.dout.zero_()
+    for qs, ks in b.slices():
+        s = torch.einsum("ihd,jhd->hij", b.q[qs].double(), b.k[ks].double().repeat_interleave(2, 1))
+        s.masked_fill_(~ref.seen(qs.stop - qs.start, ks.stop - ks.start, None, 0, "cuda"), -math.inf)
+        top, key = s.topk(min(2, s.shape[2]), -1)
+        # by so much that binary32's sums (off by 2 dim u32 of 4 std^2 sqrt(dim) at most) leave it more than 100 above the next
+        clear = ~(top[..., 0] - top[..., 1] < 100 + 2 * (2 * dim * U32) * 16 * std ** 2 * dim ** 0.5)
+        b.dout[qs, :, 0] = clear.T.to(b.dt)
+        for h in range(4):
+            want[ks, h // 2] += torch.bincount(key[h, clear[h], 0], minlength=ks.stop - ks.start).double()
+    assert float(want.sum()) > 100
+    ws = b.workspace(zp, None, 0, True)
+    g = [torch.zeros_like(x) for x in (b.q, b.k, b.v)]
+    zp.zero_window_attention_backward(b.dout, b.q, b.k, b.v, out.t, lse, *g, ws, None, 0, 1.0, **b.where)
+    # whole numbers of ones, each rounded to 16 bits as it is: one rounding of the sum
+    ref.check(g[2][..., 0], want, ref.rounded(want, want * 16 * U32, b.dt), "dv")
+
+
 # ------------------------------------------------------------------ weights far below the largest
 
 @pytest.mark.parametrize("dtype", ["f16", "bf16"])
