@@ -1325,6 +1325,16 @@ __device__ __forceinline__ bool is_split(const BwdTiles &f, int32_t j, const Que
     return f.chunk > 0 && j < f.a.sinks && t.high - t.low + 1 > 2 * f.chunk;
 }
 
+// The n-th unit of a CTA.  Of one sequence units come from the longest down,
+// and every other round of them is dealt out from the other end, so that what
+// the CTAs get adds up to about the same: 8192 tokens of 16 heads of 64,
+// without a window, bf16, 515 us from one end (dq's kernel waits for the last
+// CTA of dk's and dv's), 431 so.
+__device__ __forceinline__ int64_t nth_unit(int64_t n)
+{
+    return n * gridDim.x + (n & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+}
+
 struct KeyUnit {
     int32_t k_row, q_row, first, lq, lk, head;  // first key of its sequence; q_row: the sequence's first query
     int32_t low, high;                          // query tiles
@@ -1540,7 +1550,10 @@ __global__ void __launch_bounds__(S::THREADS, S::PER_SM) k_attn_dkv(const __grid
             for (int x = 0; x < S::BOXES; ++x)
                 load_box(smem_addr(to) + x * box, m, 64 * x, row, head, smem_addr(bar));
         };
-        for (int64_t i = blockIdx.x; ok && i < all; i += gridDim.x) {
+        for (int64_t round = 0; ok && round * gridDim.x < all; ++round) {
+            const int64_t i = nth_unit(round);
+            if (i >= all)
+                continue;
             KeyUnit u;
             if (!key_unit<BN>(f, i, lane, u))
                 continue;
@@ -1844,7 +1857,10 @@ __global__ void __launch_bounds__(S::THREADS, S::PER_SM) k_attn_dkv(const __grid
         while (global_ns() - began < 20000000u) {
         }
         // no result of this CTA is to be taken for one
-        for (int64_t i = blockIdx.x; i < all; i += gridDim.x) {
+        for (int64_t round = 0; round * gridDim.x < all; ++round) {
+            const int64_t i = nth_unit(round);
+            if (i >= all)
+                continue;
             KeyUnit u;
             if (!key_unit<BN>(f, i, lane, u))
                 continue;
@@ -2031,7 +2047,10 @@ __global__ void __launch_bounds__(S::THREADS, S::PER_SM) k_attn_dq(const __grid_
             for (int x = 0; x < S::BOXES; ++x)
                 load_box(smem_addr(to) + x * box, m, 64 * x, row, head, smem_addr(bar));
         };
-        for (int64_t i = blockIdx.x; ok && i < all; i += gridDim.x) {
+        for (int64_t round = 0; ok && round * gridDim.x < all; ++round) {
+            const int64_t i = nth_unit(round);
+            if (i >= all)
+                continue;
             QueryUnit u;
             if (!unit_at(i, u))
                 continue;
@@ -2282,7 +2301,10 @@ __global__ void __launch_bounds__(S::THREADS, S::PER_SM) k_attn_dq(const __grid_
         while (global_ns() - began < 20000000u) {
         }
         // no result of this CTA is to be taken for one
-        for (int64_t i = blockIdx.x; i < all; i += gridDim.x) {
+        for (int64_t round = 0; round * gridDim.x < all; ++round) {
+            const int64_t i = nth_unit(round);
+            if (i >= all)
+                continue;
             QueryUnit u;
             if (!unit_at(i, u))
                 continue;
