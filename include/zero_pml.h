@@ -842,7 +842,8 @@ typedef struct zero_attention {
  * positive or past binary32 times log2(e), k_lengths without k_offsets, sequences not 1
  * without q_offsets), ZERO_EALIGN, ZERO_EDTYPE, ZERO_ESIZE (head_dim; heads
  * that do not divide or past 2^15; q_tokens, k_tokens or sequences past 2^31 -
- * 512; k_tokens not q_tokens without k_offsets; strides past 2^38),
+ * 512; k_tokens not q_tokens without k_offsets; strides past 2^38; with up
+ * to eight queries per sequence more than 2^31 - 1 sets of 8 or 16 rows),
  * ZERO_EWORKSPACE, ZERO_ECUDA. */
 size_t zero_window_attention_workspace_bytes(const zero_attention_t *a, int32_t backward);
 int zero_window_attention(const zero_attention_t *a, const void *q, int64_t q_ld, int64_t q_hd, const void *k,

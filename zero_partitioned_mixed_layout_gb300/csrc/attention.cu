@@ -235,8 +235,7 @@ __device__ __forceinline__ bool needs(const KeyTiles &t, int32_t kt)
     return t.any && kt <= t.high && (kt >= t.low || kt < t.sinks);
 }
 
-// The tiles of a pair, from the last to the first: every query that sees a
-// key sees one of its first tile.
+// The tiles of a pair, from the last to the first.
 struct TileList {
     int32_t high, low, sinks, n;
     __device__ __forceinline__ int32_t at(int32_t i) const
@@ -364,14 +363,15 @@ __device__ __forceinline__ void store_rows(uint4 *stage, int lane, const uint32_
 // weights back) about as many issue slots again on each of the four
 // schedulers, so at 128 elements both pipes have to run without a pause.  With
 // one tile per CTA they wait for one another; two tiles take turns.  Measured:
-// 16384 tokens of 64 + 8 heads of 128, window 2048: 774 us, 1.37 PFLOP/s, 0.71
+// 16384 tokens of 64 + 8 heads of 128, window 2048: 792 us, 1.34 PFLOP/s, 0.69
 // of cuBLAS's burst rate (the same loads and products without the softmax
-// between them: 598).  Tiles of 64 keys in two buffers instead: 1039.
-// Heads of 64: 8 x 1024 tokens of 25, window 256: 44.5 us.  128 x 64 scores
-// are 256 clocks of the tensor pipe, a row's thread takes several times that,
+// between them: 598).  Tiles of 64 keys in two buffers instead, when it took
+// 770: 1039.  Heads of 64: 8 x 1024 tokens of 25, window 256: 44.5 us.  128 x 64
+// scores are 256 clocks of the tensor pipe, a row's thread takes several times that,
 // and the masked edges of a short window are worked out in full.  Tiles of 64
 // keys, whose scores are ready in a second buffer when those before are
-// through, mask less and wait less than of 128 in one: 50.
+// through, mask less and wait less than of 128 in one: 50 (both when one
+// operation less took 43.5).
 template <int DT, class S>
 __global__ void __launch_bounds__(S::THREADS, S::PER_SM) k_attn_tiles(const __grid_constant__ FwdTiles f)
 {
@@ -804,11 +804,11 @@ __global__ void __launch_bounds__(S::THREADS, S::PER_SM) k_attn_tiles(const __gr
 // reference and the weights' sum, and the last to come joins them in order.
 //
 // What bounds it: the keys' and values' bytes.  64 requests of up to 8192 keys
-// of 8 heads of 128 (0.92 GB): 165 us, 5.6 TB/s; 64 of 4096: 180, 5.9; 64 of
-// 4096 keys of 25 heads of 64 (1.68 GB): 283, 5.9.  Alone a request is a few
+// of 8 heads of 128 (0.92 GB): 166 us, 5.5 TB/s; 64 of 4096: 181, 5.9; 64 of
+// 4096 keys of 25 heads of 64 (1.68 GB): 281, 6.0.  Alone a request is a few
 // trips to memory: 7.5 us over 256 keys of 25 heads of 64, 11 over 4096.  Groups
 // of 8 heads' rows one at a time (NG = 1 throughout) read keys twice through
-// L2: 64 requests of 64 + 4 heads 167 us against 152.
+// L2: 64 requests of 64 + 4 heads 165 us against 154.
 struct FewArgs {
     Attn a;
     Heads q, k, v, out;
@@ -1218,7 +1218,7 @@ __device__ __forceinline__ float row_sums(float (&x)[L], int at)
 
 // A warp takes 32 queries of a tile and the heads of its block: lse by one
 // lane per query, dout and out by 2 to 16 lanes to a row.  Bound by the two
-// arrays' bytes: 5340 tokens of 25 heads of 64, 34 MB: 5 us (they are in L2).
+// arrays' bytes: 5340 tokens of 25 heads of 64, 34 MB: 11 us from HBM.
 template <int DT, int L>
 __global__ void __launch_bounds__(128) k_attn_stats(const __grid_constant__ StatsArgs f)
 {
@@ -1463,7 +1463,7 @@ __device__ __forceinline__ float largest_of_row(const unsigned char *tile, int r
 // pairs at 128 elements, and a chain of products and elementwise work that one
 // pair of buffers in tensor memory (two tiles of scores and two sums of
 // 128 x 128 are all of its 512 columns) lets overlap only by halves: 16384
-// tokens of 64 + 8 heads of 128, window 2048: about 1.28 of the pass's 2.77 ms.
+// tokens of 64 + 8 heads of 128, window 2048: about 1.27 of the pass's 2.75 ms.
 // Heads of 64: tiles of 64 queries, two CTAs per SM.
 template <int DT, class S>
 __global__ void __launch_bounds__(S::THREADS, S::PER_SM) k_attn_dkv(const __grid_constant__ BwdTiles f)
@@ -1951,7 +1951,7 @@ struct QueryShared {
 //
 // What bounds it: three products, 1536 clocks of the tensor pipe at 128
 // elements, against 64 KB of keys and values: 42 B per clock and SM, 12 TB/s,
-// where L2 gives all SMs no more than 7.7: about 1.45 of the 2.77 ms above.
+// where L2 gives all SMs no more than 7.7: about 1.25 of the 2.75 ms above.
 // A window's queries of one key head's group read the same keys at about the
 // same time, so DRAM does not bound it.
 template <int DT, class S>
@@ -2434,7 +2434,7 @@ int short_by(int kernel, uint64_t *limit_ns)
 // Heads of up to 64 leave room for two CTAs of one tile of queries each, which
 // start and end apart from one another; wider ones for one CTA of two tiles,
 // whose products run while the other's weights are worked out.  At 16 heads of
-// 64 (narrow, wide): 8 x 1024 tokens 44, 48 us; 64 x 100 18, 36; 8192 178, 201.
+// 64 (narrow, wide): 8 x 1024 tokens 45, 48 us; 64 x 100 19, 30; 8192 181, 208.
 using Narrow = FwdShape<64, 1, 64, 2>;
 using Wide = FwdShape<128, 2, 128, 1>;
 
@@ -2475,8 +2475,11 @@ int forward_tiles(const Fwd &f, const zero_attention_t *a, void *ws, cudaStream_
 // Up to here, on average over the sequences, queries go a few rows at a time
 // over their keys instead of in tiles of 128.  Both ways, 4096 keys, us (few |
 // tiles of 128) for 1, 4, 8, 16 queries: one sequence of 32 + 8 heads of 128 11,
-// 18, 21, 33 | 47; 64 of them 180, 282, 473, 816 | 605 to 613; one of 25 + 25
-// heads of 64 11, 12, 13, 17 | 38, 64 of them 283, 312, 314, 451 | 250 to 270.
+// 19, 21, 32 | 47; 64 of them 181, 285, 479, 829 | 595 to 602; one of 25 + 25
+// heads of 64 11, 12, 13, 17 | 38, 64 of them 281, 314, 317, 459 | 257 to 273.
+// (So where heads share no keys and there are enough sequences to fill every
+// SM, tiles would take up to 18 % less; and of a batch of long and short all
+// go one way, which is the wrong one for some.)
 constexpr int64_t kFewQueries = 8;
 
 struct FewPlan {
@@ -2539,7 +2542,7 @@ int forward_few(const Fwd &f, const zero_attention_t *a, void *ws, size_t partia
 // about what a tile of the window's keys has to do.  (Of more than 1024 first
 // keys every tile sees so much that there is enough to go round.)  Measured,
 // window 1024, 4 first keys, 32 + 8 heads of 128, dealt out or not: 16384
-// tokens 882, 1572 us; 2 x 16384 1701, 2440; 4 x 4096 794, 897.
+// tokens 891, 1513 us; 2 x 16384 1744, 2309; 4 x 4096 839, 917.
 struct SinkPlan {
     int32_t chunk, sink_tiles;
     int64_t units;
@@ -2612,8 +2615,8 @@ AttnSpace attn_space(const zero_attention_t *a, bool backward)
 }
 
 // As forward: heads of up to 64 leave room for two CTAs, with smaller tiles.
-// At 16 heads of 64 (narrow, wide): 8 x 1024 tokens 111, 136 us; 64 x 100 53,
-// 69; 8192 419, 465.
+// At 16 heads of 64 bf16 (narrow, wide): 8 x 1024 tokens 119, 137 us; 64 x 100
+// 52, 69; 8192 432, 478.
 using NarrowBwd = BwdShape<64, 64, 2>;
 using WideBwd = BwdShape<128, 128, 1>;
 
