@@ -825,8 +825,8 @@ typedef struct zero_attention {
  * -inf.  Rows of out and lse outside every sequence are left as they were.
  * Scores, their maximum and sum, and the output's sums are binary32; the
  * softmax's numerators are rounded to dtype once, as operands of the tensor
- * cores.  q.k is taken to fit binary32, of whose rounding lse has its share:
- * 2^-24 of the largest score.  (The backward pass finds the scores of a
+ * cores.  q.k and scale q.k are taken to fit binary32, of whose rounding
+ * lse has its share: 2^-24 of the largest score.  (The backward pass finds the scores of a
  * forward call of more than eight queries per sequence, on average, bit for
  * bit; those of fewer were added up in another order, so that from scores of
  * about 10^5 on its P may be off by exp of their difference.)

@@ -20,3 +20,15 @@ def test_a_scale_that_overflows_in_units_of_log_2_is_refused(zp, backward):  # n
         assert (f(ctypes.byref(s), int(backward)) > 0) == ok, scale
         # (an accepted scale fails at the array, which is no device memory, with the same code)
         assert attn(zp, backward, scale=scale) == EINVAL
+
+
+def test_a_rotarys_turns_are_not_set_behind_its_back(zp):  # noqa: F811
+    """A call takes the address that the object was made with, so another
+    tensor in its place would be read from memory that is gone."""
+    import torch
+    r = zp.Rotary([1.0, 0.5], interleaved=True, device="cpu")
+    before, address = r.turns, r._c.turns
+    assert (r.rot_dim, r.interleaved) == (4, True) and before.data_ptr() == address
+    with pytest.raises(AttributeError):
+        r.turns = torch.zeros_like(before)
+    assert r.turns is before and r._c.turns == address

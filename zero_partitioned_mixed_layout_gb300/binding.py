@@ -1069,8 +1069,12 @@ class Rotary:
 
     def __init__(self, inv_freq, interleaved: bool = False, device="cuda"):
         import torch
-        self.turns = torch.from_numpy(zero_rotary_turns(inv_freq).view(np.int64)).to(device)
-        self._c = _Rotary(self.turns.data_ptr(), 2 * self.turns.numel(), int(bool(interleaved)))
+        self._turns = torch.from_numpy(zero_rotary_turns(inv_freq).view(np.int64)).to(device)
+        self._c = _Rotary(self._turns.data_ptr(), 2 * self._turns.numel(), int(bool(interleaved)))
+
+    @property
+    def turns(self):
+        return self._turns
 
     @property
     def rot_dim(self) -> int:
@@ -1101,7 +1105,7 @@ def _rotary_args(rotary, positions, tokens: int, device: int):
         if positions is not None:
             raise ValueError("positions are given without a rotary")
         return None, None
-    _on(rotary.turns, "rotary", device)
+    _on(rotary._turns, "rotary", device)
     return ctypes.byref(rotary._c), _int64_pointer(positions, "positions", tokens, device)
 
 
