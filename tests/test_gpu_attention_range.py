@@ -288,3 +288,29 @@ def test_dq_is_whole_when_the_waits_before_it_give_up(zp, dim):  # noqa: F811
         runs.append(g)
     assert bool(torch.isnan(runs[1][1]).all()) and bool(torch.isnan(runs[1][2]).all())
     assert torch.equal(runs[0][0], runs[1][0])
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("what", [math.inf, -math.inf, math.nan], ids=str)
+def test_a_gradient_that_overflowed_shows(zp, what, dim, dtype):  # noqa: F811
+    """An element of dout that is no number: its query's dq, and dk and dv of
+    the keys that it sees, are none either (so that a scaled loss is found to
+    be too large), and other sequences' are what they were, to the bit."""
+    b = Batch([(200, 200), (300, 400), (70, 70)], 4, 2, dim, dtype)
+    out, lse = b.forward(zp, 90, 2)
+    ws, runs = b.workspace(zp, 90, 2, True), []
+    for value in (None, what):
+        if value is not None:
+            b.dout[300, 1, 5] = value  # (query 100 of the second sequence, at key 200)
+        g = [torch.zeros_like(x) for x in (b.q, b.k, b.v)]
+        zp.zero_window_attention_backward(b.dout, b.q, b.k, b.v, out.t, lse, *g, ws, 90, 2, **b.where)
+        runs.append(g)
+    assert zp.zero_workspace_stalls(ws) == 0
+    dq, dk, dv = runs[1]
+    assert not bool(torch.isfinite(dq[300, 1]).any())
+    seen = torch.cat([torch.arange(2), torch.arange(111, 201)]) + 200
+    assert not bool(torch.isfinite(dk[seen, 0]).any()) and not bool(torch.isfinite(dv[seen, 0, 5]).any())
+    for (before, after), parts in zip(zip(*runs), (((0, 200), (500, 570)), ((0, 200), (600, 670)), ((0, 200), (600, 670)))):
+        for a, e in parts:
+            assert torch.equal(before[a:e], after[a:e])

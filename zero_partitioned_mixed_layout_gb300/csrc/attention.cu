@@ -1160,7 +1160,8 @@ __global__ void __launch_bounds__(kFewWarps * 32) k_attn_few(const __grid_consta
 //     |dS_ij| <= |dout_i| sqrt(d) max |v_j| + |delta_i|    (P is at most 1),
 // for the dk of a key by its own value and the largest of its tile's queries,
 // for a query's dq by its own row and the values of the tiles of keys that it
-// may see.  (Unscaled, dq of normal inputs over 4096 keys and gradients of
+// may see.  (What is below 2^-29 of that bound is rounded in steps of 2^-39 of
+// it.  Unscaled, dq of normal inputs over 4096 keys and gradients of
 // 10^-4 was off by a tenth, and one of 10^5 was inf.)  5340 tokens of 25 heads
 // of 64: 117.5 us, 108.3 without: the units' largest rows and values, and
 // dS' times its power of two.
